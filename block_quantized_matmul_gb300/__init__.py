@@ -34,11 +34,16 @@ __all__ = [
     "qmm_matmul_path", "qmm_matmul_f32", "qmm_matmul_flat", "qmm_device_status", "PATH_AUTO", "PATH_MATVEC", "PATH_GEMM",
     "matmul_workspace_size", "qmm_matmul_ws", "qmm_matmul_noalloc", "matmul_noalloc_max_workspace",
     "qmm_selftest_timeout",
+    "F32", "F16", "BF16", "DTYPES", "mx4_codes_size", "mx4_scales_size", "mx4_linear_workspace_size", "qmm_mx4_quantize",
+    "qmm_mx4_dequantize", "qmm_mx4_matmul", "qmm_mx4_linear", "cache_page_size", "cache_attend_workspace_size",
+    "qmm_cache_write", "qmm_cache_read", "qmm_cache_attend",
 ]
 
 Q4_0, Q8_0, IQ4_NL, MXFP4, Q4_1, Q4_K = 0, 1, 2, 3, 4, 5
 TYPES = {"q4_0": Q4_0, "q8_0": Q8_0, "iq4_nl": IQ4_NL, "mxfp4": MXFP4, "q4_1": Q4_1, "q4_k": Q4_K}
 PATH_AUTO, PATH_MATVEC, PATH_GEMM = 0, 1, 2
+F32, F16, BF16 = 0, 1, 2
+DTYPES = {"f32": F32, "f16": F16, "bf16": BF16}
 _STATUS = {0: "QMM_OK", 1: "QMM_ERR_INVALID_ARG", 2: "QMM_ERR_UNSUPPORTED", 3: "QMM_ERR_MISALIGNED",
            4: "QMM_ERR_CUDA", 5: "QMM_ERR_TIMEOUT", 6: "QMM_ERR_RANGE", 7: "QMM_ERR_BOUNDS"}
 
@@ -93,7 +98,23 @@ def lib():
         L.qmm_matmul_f32_workspace_size.argtypes = [i64, i64]
         L.qmm_matmul_f32_workspace_size.restype = sz
         L.qmm_matmul_f32_ws.argtypes = [i32, vp, i64, i64, vp, i64, i64, vp, i64, vp, sz, vp]
-        for fn in ("qmm_quantize_weight", "qmm_repack", "qmm_unpack", "qmm_quantize_act", "qmm_matmul",
+        for fn in ("qmm_mx4_codes_size", "qmm_mx4_scales_size", "qmm_mx4_linear_workspace_size"):
+            getattr(L, fn).argtypes = [i64, i64]
+            getattr(L, fn).restype = sz
+        L.qmm_mx4_quantize.argtypes = [i32, vp, i64, i64, i64, vp, vp, vp]
+        L.qmm_mx4_dequantize.argtypes = [vp, vp, i64, i64, i32, vp, i64, vp]
+        L.qmm_mx4_matmul.argtypes = [vp, vp, i64, i64, vp, vp, i64, i32, vp, i64, vp]
+        L.qmm_mx4_linear.argtypes = [vp, vp, i64, i64, i32, vp, i64, i64, i32, vp, i64, vp, sz, vp]
+        L.qmm_cache_page_size.argtypes = [i32, i64, i64, i64]
+        L.qmm_cache_page_size.restype = sz
+        L.qmm_cache_write.argtypes = [i32, i32, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, i64, i64, vp]
+        L.qmm_cache_read.argtypes = [i32, vp, vp, i64, i64, i64, i64, vp, i64, vp, i64, i64, i32, vp, vp, i64, i64, vp]
+        L.qmm_cache_attend_workspace_size.argtypes = [i64] * 6
+        L.qmm_cache_attend_workspace_size.restype = sz
+        L.qmm_cache_attend.argtypes = [i32, vp, vp, i64, i64, i64, i64, vp, i64, vp, vp, i64, i32, vp, i64, i64, i64, vp,
+                                       ctypes.c_float, i64, i64, vp, i64, vp, vp, sz, vp]
+        for fn in ("qmm_mx4_quantize", "qmm_mx4_dequantize", "qmm_mx4_matmul", "qmm_mx4_linear", "qmm_cache_write",
+                   "qmm_cache_read", "qmm_cache_attend", "qmm_quantize_weight", "qmm_repack", "qmm_unpack", "qmm_quantize_act", "qmm_matmul",
                    "qmm_matmul_path", "qmm_device_status", "qmm_matmul_ws", "qmm_matmul_noalloc", "qmm_matmul_f32",
                    "qmm_matmul_flat", "qmm_selftest_timeout", "qmm_matmul_f32_ws"):
             getattr(L, fn).restype = i32
@@ -103,6 +124,10 @@ def lib():
 
 def _t(type_) -> int:
     return TYPES[type_] if isinstance(type_, str) else int(type_)
+
+
+def _dt(dtype) -> int:
+    return DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
 
 
 def _ptr(x) -> int | None:
@@ -246,3 +271,74 @@ def qmm_selftest_timeout(unit: int, limit_ns: int, flags, stream=None) -> None:
     """Test hook: one CTA whose bounded waits run out on purpose (unit 0: decode kernels' helper,
     1: the GEMM's); afterwards qmm_device_status() reports the timeout (see include/qmm.h)."""
     _check("qmm_selftest_timeout", lib().qmm_selftest_timeout(int(unit), int(limit_ns), _ptr(flags), _stream(stream)))
+
+
+def mx4_codes_size(R: int, K: int) -> int:
+    return int(lib().qmm_mx4_codes_size(R, K))
+
+
+def mx4_scales_size(R: int, K: int) -> int:
+    return int(lib().qmm_mx4_scales_size(R, K))
+
+
+def mx4_linear_workspace_size(M: int, K: int) -> int:
+    return int(lib().qmm_mx4_linear_workspace_size(M, K))
+
+
+def qmm_mx4_quantize(dtype, x, R: int, K: int, ldx: int, codes, scales, stream=None) -> None:
+    """Rows of `dtype` ("f32", "f16", "bf16") -> MX4 operand (codes, scales)."""
+    _check("qmm_mx4_quantize", lib().qmm_mx4_quantize(_dt(dtype), _ptr(x), R, K, ldx, _ptr(codes), _ptr(scales), _stream(stream)))
+
+
+def qmm_mx4_dequantize(codes, scales, R: int, K: int, dtype, y, ldy: int, stream=None) -> None:
+    _check("qmm_mx4_dequantize",
+           lib().qmm_mx4_dequantize(_ptr(codes), _ptr(scales), R, K, _dt(dtype), _ptr(y), ldy, _stream(stream)))
+
+
+def qmm_mx4_matmul(w_codes, w_scales, K: int, N: int, a_codes, a_scales, M: int, dtype, y, ldy: int, stream=None) -> None:
+    """y[M, N] (of `dtype`) = A @ W^T over MX4 operands."""
+    _check("qmm_mx4_matmul", lib().qmm_mx4_matmul(_ptr(w_codes), _ptr(w_scales), K, N, _ptr(a_codes), _ptr(a_scales), M,
+                                                  _dt(dtype), _ptr(y), ldy, _stream(stream)))
+
+
+def qmm_mx4_linear(w_codes, w_scales, K: int, N: int, x_dtype, x, ldx: int, M: int, y_dtype, y, ldy: int, workspace,
+                   workspace_bytes: int, stream=None) -> None:
+    """y[M, N] = MX4(x) @ W^T: the activations are quantized into the workspace, then multiplied."""
+    _check("qmm_mx4_linear", lib().qmm_mx4_linear(_ptr(w_codes), _ptr(w_scales), K, N, _dt(x_dtype), _ptr(x), ldx, M,
+                                                  _dt(y_dtype), _ptr(y), ldy, _ptr(workspace), int(workspace_bytes),
+                                                  _stream(stream)))
+
+
+def cache_page_size(type_, H: int, D: int, P: int) -> int:
+    return int(lib().qmm_cache_page_size(_t(type_), H, D, P))
+
+
+def cache_attend_workspace_size(n_seq: int, max_new: int, H: int, Hq: int, D: int, max_len: int) -> int:
+    return int(lib().qmm_cache_attend_workspace_size(n_seq, max_new, H, Hq, D, max_len))
+
+
+def qmm_cache_write(type_, dtype, k, v, ldk: int, ldv: int, T: int, H: int, D: int, slots, k_cache, v_cache, n_pages: int,
+                    P: int, stream=None) -> None:
+    """Keys and values of T tokens, quantized into their slots (page * P + place) of the paged cache."""
+    _check("qmm_cache_write", lib().qmm_cache_write(_t(type_), _dt(dtype), _ptr(k), _ptr(v), ldk, ldv, T, H, D, _ptr(slots),
+                                                    _ptr(k_cache), _ptr(v_cache), n_pages, P, _stream(stream)))
+
+
+def qmm_cache_read(type_, k_cache, v_cache, n_pages: int, P: int, H: int, D: int, pages, ld_pages: int, starts, n_seq: int,
+                   T: int, dtype, k, v, ldk: int, ldv: int, stream=None) -> None:
+    """The cached values of n_seq sequences as dense rows [T][H][D] of `dtype` (k or v may be None)."""
+    _check("qmm_cache_read", lib().qmm_cache_read(_t(type_), _ptr(k_cache), _ptr(v_cache), n_pages, P, H, D, _ptr(pages),
+                                                  ld_pages, _ptr(starts), n_seq, T, _dt(dtype), _ptr(k), _ptr(v), ldk, ldv,
+                                                  _stream(stream)))
+
+
+def qmm_cache_attend(type_, k_cache, v_cache, n_pages: int, P: int, H: int, D: int, pages, ld_pages: int, q_starts, kv_lens,
+                     n_seq: int, dtype, q, ldq: int, T: int, Hq: int, tree, scale: float, max_new: int, max_len: int, out,
+                     ldo: int, lse, workspace, workspace_bytes: int, stream=None) -> None:
+    """Attention of each sequence's new tokens (one token, a tree of drafted ones, or a piece of a prompt) over
+    its cached tokens; tree, lse and workspace may be None."""
+    _check("qmm_cache_attend",
+           lib().qmm_cache_attend(_t(type_), _ptr(k_cache), _ptr(v_cache), n_pages, P, H, D, _ptr(pages), ld_pages,
+                                  _ptr(q_starts), _ptr(kv_lens), n_seq, _dt(dtype), _ptr(q), ldq, T, Hq, _ptr(tree),
+                                  float(scale), max_new, max_len, _ptr(out), ldo, _ptr(lse), _ptr(workspace),
+                                  int(workspace_bytes), _stream(stream)))

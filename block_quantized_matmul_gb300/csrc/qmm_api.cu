@@ -7,6 +7,9 @@
 // parameters.
 #include "qmm_internal.cuh"
 
+#include "cache.cuh"
+#include "mx4.cuh"
+
 using namespace qmm;
 
 namespace {
@@ -252,6 +255,163 @@ qmm_status qmm_matmul_noalloc(qmm_type t, const void *w_tiled, int64_t K, int64_
     return from_cuda(launch_prefill_ws(t, w, K, N, a_q, a_d, M, y, ldy, scratch, cs(stream)));
 }
 
+// ---- microscaled 4-bit operands ----
+
+static bool valid_dtype(qmm_dtype t) { return t == QMM_F32 || t == QMM_F16 || t == QMM_BF16; }
+static uintptr_t dtype_align(qmm_dtype t) { return t == QMM_F32 ? 4 : 2; }
+static bool valid_rk(int64_t R, int64_t K) { return R > 0 && K > 0 && (K % 32) == 0 && R <= kMaxDim && K <= kMaxDim; }
+
+size_t qmm_mx4_codes_size(int64_t R, int64_t K) { return valid_rk(R, K) ? mx4_codes_bytes(R, K) : 0; }
+size_t qmm_mx4_scales_size(int64_t R, int64_t K) { return valid_rk(R, K) ? mx4_scales_bytes(R, K) : 0; }
+
+// The checks of a conversion between rows of type dt and an operand, in either direction.
+static qmm_status check_mx4_rows(qmm_dtype dt, const void *x, int64_t R, int64_t K, int64_t ldx, const void *codes,
+                                 const void *scales) {
+    if (!valid_dtype(dt)) return QMM_ERR_UNSUPPORTED;
+    if (!valid_rk(R, K) || ldx < K || ldx > kMaxDim || !x || !codes || !scales) return QMM_ERR_INVALID_ARG;
+    if (!aligned(x, dtype_align(dt)) || !aligned(codes, 16) || !aligned(scales, 16)) return QMM_ERR_MISALIGNED;
+    return QMM_OK;
+}
+
+qmm_status qmm_mx4_quantize(qmm_dtype dt, const void *x, int64_t R, int64_t K, int64_t ldx, void *codes, void *scales,
+                            qmm_stream_t stream) {
+    const qmm_status st = check_mx4_rows(dt, x, R, K, ldx, codes, scales);
+    if (st != QMM_OK) return st;
+    return from_cuda(launch_mx4_quantize(dt, x, R, K, ldx, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), cs(stream)));
+}
+
+qmm_status qmm_mx4_dequantize(const void *codes, const void *scales, int64_t R, int64_t K, qmm_dtype dt, void *y, int64_t ldy,
+                              qmm_stream_t stream) {
+    const qmm_status st = check_mx4_rows(dt, y, R, K, ldy, codes, scales);
+    if (st != QMM_OK) return st;
+    return from_cuda(launch_mx4_dequantize(static_cast<const uint8_t *>(codes), static_cast<const uint8_t *>(scales), R, K, dt, y,
+                                           ldy, cs(stream)));
+}
+
+// The checks of a product but for its activations.
+static qmm_status check_mx4_product(const void *wc, const void *ws, int64_t K, int64_t N, int64_t M, qmm_dtype dt, const void *y,
+                                    int64_t ldy) {
+    if (!valid_dtype(dt)) return QMM_ERR_UNSUPPORTED;
+    if (!valid_rk(M, K) || !valid_rk(N, K) || K > kMaxMatmulK || ldy < N || ldy > kMaxDim || !wc || !ws || !y)
+        return QMM_ERR_INVALID_ARG;
+    if (!aligned(wc, 16) || !aligned(ws, 16) || !aligned(y, dtype_align(dt))) return QMM_ERR_MISALIGNED;
+    return QMM_OK;
+}
+
+qmm_status qmm_mx4_matmul(const void *w_codes, const void *w_scales, int64_t K, int64_t N, const void *a_codes,
+                          const void *a_scales, int64_t M, qmm_dtype dt, void *y, int64_t ldy, qmm_stream_t stream) {
+    const qmm_status st = check_mx4_product(w_codes, w_scales, K, N, M, dt, y, ldy);
+    if (st != QMM_OK) return st;
+    if (!a_codes || !a_scales) return QMM_ERR_INVALID_ARG;
+    if (!aligned(a_codes, 16) || !aligned(a_scales, 16)) return QMM_ERR_MISALIGNED;
+    return from_cuda(launch_mx4_matmul(static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales), K, N,
+                                       static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales), M, dt, y, ldy,
+                                       cs(stream)));
+}
+
+size_t qmm_mx4_linear_workspace_size(int64_t M, int64_t K) {
+    return valid_rk(M, K) && K <= kMaxMatmulK ? round256(mx4_codes_bytes(M, K)) + mx4_scales_bytes(M, K) : 0;
+}
+
+qmm_status qmm_mx4_linear(const void *w_codes, const void *w_scales, int64_t K, int64_t N, qmm_dtype xdt, const void *x, int64_t ldx,
+                          int64_t M, qmm_dtype ydt, void *y, int64_t ldy, void *workspace, size_t workspace_bytes,
+                          qmm_stream_t stream) {
+    qmm_status st = check_mx4_product(w_codes, w_scales, K, N, M, ydt, y, ldy);
+    if (st != QMM_OK) return st;
+    if (!workspace || workspace_bytes < qmm_mx4_linear_workspace_size(M, K)) return QMM_ERR_INVALID_ARG;
+    if (!aligned(workspace, 256)) return QMM_ERR_MISALIGNED;
+    uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + round256(mx4_codes_bytes(M, K));
+    st = check_mx4_rows(xdt, x, M, K, ldx, codes, scales);
+    if (st != QMM_OK) return st;
+    const cudaError_t e = launch_mx4_quantize(xdt, x, M, K, ldx, codes, scales, cs(stream));
+    if (e != cudaSuccess) return from_cuda(e);
+    return from_cuda(launch_mx4_matmul(static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales), K, N, codes,
+                                       scales, M, ydt, y, ldy, cs(stream)));
+}
+
+// ---- block-quantized key/value cache ----
+
+static bool valid_cache_sizes(int64_t H, int64_t D, int64_t P) {
+    return H > 0 && H <= 65536 && D >= 32 && D <= 256 && (D % 32) == 0 && P >= 16 && P <= 256 && (P & (P - 1)) == 0;
+}
+
+size_t qmm_cache_page_size(qmm_type t, int64_t H, int64_t D, int64_t P) {
+    if ((t != QMM_Q8_0 && t != QMM_Q4_0) || !valid_cache_sizes(H, D, P)) return 0;
+    return (size_t)H * (size_t)P * (size_t)cache_token_bytes(t, (int)D);
+}
+
+static qmm_status check_cache(qmm_type t, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t P, int64_t H,
+                              int64_t D) {
+    if (t != QMM_Q8_0 && t != QMM_Q4_0) return QMM_ERR_UNSUPPORTED;
+    if (!valid_cache_sizes(H, D, P) || n_pages <= 0 || n_pages > kMaxDim || !k_cache || !v_cache) return QMM_ERR_INVALID_ARG;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return QMM_ERR_MISALIGNED;
+    return QMM_OK;
+}
+static bool valid_table(const int32_t *pages, int64_t ld_pages, const int32_t *starts, int64_t n_seq) {
+    return pages && starts && ld_pages > 0 && ld_pages <= kMaxDim && n_seq > 0 && n_seq <= kMaxDim;
+}
+
+qmm_status qmm_cache_write(qmm_type t, qmm_dtype dt, const void *k, const void *v, int64_t ldk, int64_t ldv, int64_t T, int64_t H,
+                           int64_t D, const int64_t *slots, void *k_cache, void *v_cache, int64_t n_pages, int64_t P,
+                           qmm_stream_t stream) {
+    if (!valid_dtype(dt)) return QMM_ERR_UNSUPPORTED;
+    const qmm_status st = check_cache(t, k_cache, v_cache, n_pages, P, H, D);
+    if (st != QMM_OK) return st;
+    if (T < 0 || T > kMaxDim || ldk < H * D || ldv < H * D || ldk > kMaxDim || ldv > kMaxDim) return QMM_ERR_INVALID_ARG;
+    if (T == 0) return QMM_OK;
+    if (!k || !v || !slots) return QMM_ERR_INVALID_ARG;
+    if (!aligned(k, dtype_align(dt)) || !aligned(v, dtype_align(dt)) || !aligned(slots, 8)) return QMM_ERR_MISALIGNED;
+    return from_cuda(launch_cache_write(t, dt, k, v, ldk, ldv, T, (int)H, (int)D, slots, static_cast<uint8_t *>(k_cache),
+                                        static_cast<uint8_t *>(v_cache), n_pages, (int)P, cs(stream)));
+}
+
+qmm_status qmm_cache_read(qmm_type t, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t P, int64_t H, int64_t D,
+                          const int32_t *pages, int64_t ld_pages, const int32_t *starts, int64_t n_seq, int64_t T, qmm_dtype dt,
+                          void *k, void *v, int64_t ldk, int64_t ldv, qmm_stream_t stream) {
+    if (!valid_dtype(dt)) return QMM_ERR_UNSUPPORTED;
+    const qmm_status st = check_cache(t, k_cache, v_cache, n_pages, P, H, D);
+    if (st != QMM_OK) return st;
+    if (T < 0 || T > kMaxDim || (k && ldk < H * D) || (v && ldv < H * D) || ldk > kMaxDim || ldv > kMaxDim)
+        return QMM_ERR_INVALID_ARG;
+    if (!valid_table(pages, ld_pages, starts, n_seq)) return QMM_ERR_INVALID_ARG;
+    if (!aligned(pages, 4) || !aligned(starts, 4) || !aligned(k, dtype_align(dt)) || !aligned(v, dtype_align(dt)))
+        return QMM_ERR_MISALIGNED;
+    if (T == 0 || (!k && !v)) return QMM_OK;
+    return from_cuda(launch_cache_read(t, static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), n_pages,
+                                       (int)P, (int)H, (int)D, pages, ld_pages, starts, n_seq, T, dt, k, v, ldk, ldv, cs(stream)));
+}
+
+static bool valid_heads(int64_t H, int64_t Hq) { return Hq > 0 && Hq <= 65536 && Hq % H == 0 && Hq / H <= 64; }
+
+size_t qmm_cache_attend_workspace_size(int64_t n_seq, int64_t max_new, int64_t H, int64_t Hq, int64_t D, int64_t max_len) {
+    if (n_seq <= 0 || n_seq > kMaxDim || max_new <= 0 || max_new > kMaxDim || max_len < 0 || max_len > kMaxDim ||
+        !valid_cache_sizes(H, D, 16) || !valid_heads(H, Hq))
+        return 0;
+    return attend_workspace_bytes(n_seq, max_new, (int)H, (int)Hq, (int)D, max_len);
+}
+
+qmm_status qmm_cache_attend(qmm_type t, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t P, int64_t H, int64_t D,
+                            const int32_t *pages, int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens, int64_t n_seq,
+                            qmm_dtype dt, const void *q, int64_t ldq, int64_t T, int64_t Hq, const uint64_t *tree, float scale,
+                            int64_t max_new, int64_t max_len, void *out, int64_t ldo, float *lse, void *workspace,
+                            size_t workspace_bytes, qmm_stream_t stream) {
+    if (dt != QMM_F16 && dt != QMM_BF16) return QMM_ERR_UNSUPPORTED;
+    const qmm_status st = check_cache(t, k_cache, v_cache, n_pages, P, H, D);
+    if (st != QMM_OK) return st;
+    if (!valid_table(pages, ld_pages, q_starts, n_seq) || !kv_lens || !valid_heads(H, Hq) || T < 0 || T > kMaxDim ||
+        ldq < Hq * D || ldo < Hq * D || ldq > kMaxDim || ldo > kMaxDim || max_len < 0 || max_len > kMaxDim)
+        return QMM_ERR_INVALID_ARG;
+    if (T == 0) return QMM_OK;
+    if (!q || !out || max_new <= 0 || max_new > kMaxDim) return QMM_ERR_INVALID_ARG;
+    if (!aligned(pages, 4) || !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(tree, 8) || !aligned(lse, 4) ||
+        !aligned(q, 16) || !aligned(out, 16) || (ldq % 8) != 0 || (ldo % 8) != 0 || !aligned(workspace, 256))
+        return QMM_ERR_MISALIGNED;
+    return from_cuda(launch_cache_attend(t, static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), n_pages,
+                                         (int)P, (int)H, (int)D, pages, ld_pages, q_starts, kv_lens, n_seq, dt, q, ldq, T, (int)Hq,
+                                         tree, scale, max_new, max_len, out, ldo, lse, workspace, workspace ? workspace_bytes : 0,
+                                         cs(stream)));
+}
+
 size_t qmm_matmul_noalloc_max_workspace(void) { return kNoAllocScratchBytes; }
 
 qmm_status qmm_selftest_timeout(int unit, uint64_t limit_ns, int *flags_dev, qmm_stream_t stream) {
@@ -269,14 +429,19 @@ qmm_status qmm_device_status(qmm_stream_t stream) {
     if (e == cudaSuccess) e = read_and_clear_matvec_status(&w, cs(stream));
     if (e == cudaSuccess) e = read_and_clear_fold_status(&f, cs(stream));
     // the bounds-check words (always 0 unless the library was built with QMM_DEBUG)
-    unsigned d[5] = {0, 0, 0, 0, 0};
+    unsigned d[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};
     if (e == cudaSuccess) e = read_dcheck_matvec(&d[0], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_gemm(&d[1], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_fold(&d[2], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_quant(&d[3], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_repack(&d[4], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_mx4(&d[5], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_mx4_gemm(&d[6], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_cache(&d[7], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_attend(&d[8], cs(stream));
     if (e != cudaSuccess) return QMM_ERR_CUDA;
-    if (d[0] | d[1] | d[2] | d[3] | d[4]) return QMM_ERR_BOUNDS;
+    for (unsigned line : d)
+        if (line) return QMM_ERR_BOUNDS;
     if (v | w | (f & 1u)) return QMM_ERR_TIMEOUT;
     return (f & 2u) ? QMM_ERR_RANGE : QMM_OK;
 }

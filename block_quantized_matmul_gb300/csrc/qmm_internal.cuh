@@ -211,6 +211,47 @@ cudaError_t read_dcheck_fold(unsigned *out, cudaStream_t s);
 cudaError_t read_dcheck_quant(unsigned *out, cudaStream_t s);
 cudaError_t read_dcheck_repack(unsigned *out, cudaStream_t s);
 
+// Microscaled 4-bit operands (mx4.cu, mx4_gemm.cu) and the block-quantized cache (cache.cu, attend.cu).
+cudaError_t launch_mx4_quantize(qmm_dtype t, const void *x, int64_t R, int64_t K, int64_t ldx, uint8_t *codes, uint8_t *scales,
+                                cudaStream_t s);
+cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, qmm_dtype t, void *y,
+                                  int64_t ldy, cudaStream_t s);
+cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
+                              int64_t M, qmm_dtype t, void *y, int64_t ldy, cudaStream_t s);
+cudaError_t launch_cache_write(qmm_type type, qmm_dtype t, const void *k, const void *v, int64_t ldk, int64_t ldv, int64_t T,
+                               int H, int D, const int64_t *slots, uint8_t *k_cache, uint8_t *v_cache, int64_t n_pages, int P,
+                               cudaStream_t s);
+cudaError_t launch_cache_read(qmm_type type, const uint8_t *k_cache, const uint8_t *v_cache, int64_t n_pages, int P, int H, int D,
+                              const int32_t *pages, int64_t ld_pages, const int32_t *starts, int64_t n_seq, int64_t T, qmm_dtype t,
+                              void *k, void *v, int64_t ldk, int64_t ldv, cudaStream_t s);
+size_t attend_workspace_bytes(int64_t n_seq, int64_t max_new, int H, int Hq, int D, int64_t max_len);
+cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uint8_t *v_cache, int64_t n_pages, int P, int H, int D,
+                                const int32_t *pages, int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens,
+                                int64_t n_seq, qmm_dtype t, const void *q, int64_t ldq, int64_t T, int Hq, const uint64_t *tree,
+                                float scale, int64_t max_new, int64_t max_len, void *out, int64_t ldo, float *lse, void *ws,
+                                size_t ws_bytes, cudaStream_t s);
+cudaError_t read_dcheck_mx4(unsigned *out, cudaStream_t s);
+cudaError_t read_dcheck_mx4_gemm(unsigned *out, cudaStream_t s);
+cudaError_t read_dcheck_cache(unsigned *out, cudaStream_t s);
+cudaError_t read_dcheck_attend(unsigned *out, cudaStream_t s);
+
+// Launches kern as a programmatic dependent of the grid before it on the stream (which the kernel waits
+// for with griddepcontrol.wait before it touches what that grid may write or still read).
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t s, const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Fixed device scratch used by qmm_matmul_noalloc (bytes, per device).
 constexpr size_t kNoAllocScratchBytes = (size_t)16 << 20;
 cudaError_t noalloc_scratch(void **out);

@@ -74,6 +74,9 @@ typedef enum { QMM_Q4_0 = 0, QMM_Q8_0 = 1, QMM_IQ4_NL = 2, QMM_MXFP4 = 3, QMM_Q4
  * runs through qmm_matmul_ws / qmm_matmul_noalloc). */
 typedef enum { QMM_PATH_AUTO = 0, QMM_PATH_MATVEC = 1, QMM_PATH_GEMM = 2 } qmm_path;
 
+/* Element types of the floating-point rows of the MX4 and cache calls (IEEE binary32, binary16, bfloat16). */
+typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
+
 /* Human-readable name of a status code (static string, never NULL). */
 QMM_API const char *qmm_status_str(qmm_status st);
 
@@ -338,6 +341,158 @@ QMM_API qmm_status qmm_matmul_noalloc(qmm_type t, const void *w_tiled_dev, int64
 
 /* Size in bytes of the fixed scratch array qmm_matmul_noalloc uses (per device). */
 QMM_API size_t qmm_matmul_noalloc_max_workspace(void);
+
+/* ---------------------------------------------------------------------------------------------
+ * Microscaled 4-bit floating point (MX4, the OCP MXFP4 format): both operands of a product in 4 bits,
+ * multiplied by the block-scaled tensor core instructions.
+ *
+ * An MX4 operand of R rows of K elements (K % 32 == 0) is two buffers:
+ *   codes   uint8 [R][K/2]: E2M1 codes (sign, two exponent bits, one mantissa bit: 0, 0.5, 1, 1.5, 2, 3, 4, 6),
+ *           element 2i of a row in the low nibble of byte i, element 2i + 1 in the high nibble.
+ *   scales  one E8M0 byte e per 32 consecutive elements of a row, worth 2^(e - 127), 255 = NaN; in blocks of
+ *           512 bytes for 128 rows x 128 elements, block (r / 128) * ceil(K / 128) + k / 128, in which row
+ *           r, block b of 32 is byte 16 * (r % 32) + 4 * ((r % 128) / 32) + b % 4.  The bytes of blocks past
+ *           K are 0; those of rows past R may hold anything.
+ * Unlike an MXFP4 tile, whose scale is an fp16, an MX4 operand keeps the whole E8M0 range.
+ * --------------------------------------------------------------------------------------------- */
+
+/* Bytes of the two buffers: R * K/2 and ceil(R/128) * ceil(K/128) * 512; 0 if R <= 0, K <= 0 or K % 32. */
+QMM_API size_t qmm_mx4_codes_size(int64_t R, int64_t K);
+QMM_API size_t qmm_mx4_scales_size(int64_t R, int64_t K);
+
+/*
+ * qmm_mx4_quantize -- floating-point rows (activations, or a weight at load time) -> MX4 operand.
+ *   x_dev       R rows of K elements of type dt, row r at x_dev + r*ldx (elements); aligned to the element
+ *               (16-byte aligned rows take the vectorised path).
+ *   codes_dev   qmm_mx4_codes_size bytes; scales_dev qmm_mx4_scales_size bytes; both 16-byte aligned.
+ * Per block of 32: e = floor(log2 max|x|) - 2 + 127, at least 0 (0 for an all-zero block); code = the E2M1
+ * value nearest to x * 2^(127 - e), ties to the even code, magnitudes beyond 6 to 6.  A block that holds
+ * an infinity or a NaN has e = 255 and codes 0: all of it is NaN.
+ * Launch overlap: a programmatic dependent that waits for the kernel before it before it reads x.
+ * Errors: INVALID_ARG (R <= 0, K <= 0, K % 32, ldx < K, NULL), UNSUPPORTED (dt), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_mx4_quantize(qmm_dtype dt, const void *x_dev, int64_t R, int64_t K, int64_t ldx, void *codes_dev,
+                                    void *scales_dev, qmm_stream_t stream);
+
+/* qmm_mx4_dequantize -- the operand's values, rounded to dt (to nearest even), into y[r*ldy + k].
+ * Same rules for the buffers; errors as above (ldy < K). */
+QMM_API qmm_status qmm_mx4_dequantize(const void *codes_dev, const void *scales_dev, int64_t R, int64_t K, qmm_dtype dt,
+                                      void *y_dev, int64_t ldy, qmm_stream_t stream);
+
+/*
+ * qmm_mx4_matmul -- Y = A * W^T over MX4 operands of M and N rows of K:
+ *   Y[m, n] = sum_b 2^(ea[m, b] + ew[n, b] - 254) * sum_{j < 32} a[m, 32b + j] * w[n, 32b + j].
+ *   w_codes_dev, w_scales_dev  the weight (N rows); a_codes_dev, a_scales_dev  the activations (M rows),
+ *               all 16-byte aligned.
+ *   y_dev       output of type dt, y[m*ldy + n] for n < N (other columns untouched); aligned to the element.
+ * Sums are fp32 in a fixed order (results are reproducible run to run) and are rounded to dt once; the
+ * error before that rounding stays below 1e-5 * sum_k |w_k * x_k|.  K may be at most 131072.
+ * A NaN scale makes every result of its row NaN; results beyond dt's range are infinities.
+ * Launch overlap: as for qmm_matmul (the weight may be streamed before the kernel before this call has
+ * completed; a_codes, a_scales and y are touched only after it has).
+ * Errors: INVALID_ARG (sizes, ldy < N, NULL), UNSUPPORTED (dt), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_mx4_matmul(const void *w_codes_dev, const void *w_scales_dev, int64_t K, int64_t N,
+                                  const void *a_codes_dev, const void *a_scales_dev, int64_t M, qmm_dtype dt, void *y_dev,
+                                  int64_t ldy, qmm_stream_t stream);
+
+/* Bytes of workspace qmm_mx4_linear needs: M * K/2 rounded up to 256, plus qmm_mx4_scales_size(M, K). */
+QMM_API size_t qmm_mx4_linear_workspace_size(int64_t M, int64_t K);
+
+/*
+ * qmm_mx4_linear -- floating-point activation rows times an MX4 weight: qmm_mx4_quantize into the workspace,
+ * then qmm_mx4_matmul, bit for bit.
+ *   x_dev  M rows of K elements of type xdt, row m at x_dev + m*ldx; y_dev of type ydt as above.
+ *   workspace_dev  >= qmm_mx4_linear_workspace_size(M, K) bytes, 256-byte aligned, overwritten; calls that
+ *                  overlap on the GPU must use different workspaces.
+ * Errors: those of the two calls, plus INVALID_ARG (workspace missing or too small) and MISALIGNED
+ * (workspace not 256-byte aligned).
+ */
+QMM_API qmm_status qmm_mx4_linear(const void *w_codes_dev, const void *w_scales_dev, int64_t K, int64_t N, qmm_dtype xdt,
+                                  const void *x_dev, int64_t ldx, int64_t M, qmm_dtype ydt, void *y_dev, int64_t ldy,
+                                  void *workspace_dev, size_t workspace_bytes, qmm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * A paged key/value cache in Q8_0 or Q4_0 blocks.
+ *
+ * A cache (one for keys, one for values) is n_pages pages of P tokens (P a power of two, 16 to 256) of H
+ * heads of D elements (D a multiple of 32, at most 256).  Page p, head h is one chunk at byte
+ * (p * H + h) * P * (code bytes + D/32 * 2): [P][D] int8 codes (Q8_0) or [P][D/2] nibble bytes (Q4_0: byte j of a
+ * block of 32 holds element j low, element j + 16 high), then [P][D/32] fp16 scales.  A value is d * q (Q8_0) or
+ * d * (q - 8) (Q4_0).  Token number i of a sequence lies in the sequence's page i / P at place i % P; its
+ * slot is page * P + place.
+ * --------------------------------------------------------------------------------------------- */
+
+/* Bytes of one page of one cache: H * P * (code bytes of D + D/32 * 2); 0 if the type is not Q8_0 or Q4_0 or
+ * a size is invalid. */
+QMM_API size_t qmm_cache_page_size(qmm_type t, int64_t H, int64_t D, int64_t P);
+
+/*
+ * qmm_cache_write -- keys and values of T new tokens, quantized into their slots.
+ *   k_dev, v_dev   [T][H][D] elements of type dt, token i at k_dev + i*ldk (ldv for values; elements, at
+ *                  least H*D); aligned to the element (16-byte aligned rows take the vectorised path).
+ *   slots_dev      int64 [T], 8-byte aligned; a token whose slot is negative or past the pool is not written.
+ *                  Two tokens of a call must not share a slot.
+ *   k_cache_dev, v_cache_dev  n_pages * qmm_cache_page_size bytes each, 16-byte aligned.
+ * Quantized by the rules of qmm_quantize_act (Q8_0, with d = max|x| * fp32(1/127)) and qmm_quantize_weight
+ * (Q4_0), scales rounded to fp16.  A block whose scale is then not finite (an infinity or a NaN in it, or values beyond the format)
+ * is stored with a NaN scale and reads as NaN.  T = 0 does nothing.
+ * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
+ * Errors: INVALID_ARG (sizes, strides, NULL), UNSUPPORTED (t, dt), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_cache_write(qmm_type t, qmm_dtype dt, const void *k_dev, const void *v_dev, int64_t ldk, int64_t ldv,
+                                   int64_t T, int64_t H, int64_t D, const int64_t *slots_dev, void *k_cache_dev,
+                                   void *v_cache_dev, int64_t n_pages, int64_t P, qmm_stream_t stream);
+
+/*
+ * qmm_cache_read -- the values of n_seq sequences, one after the other, rounded to dt.
+ *   pages_dev   int32 [n_seq][ld_pages]: the pages of each sequence in order; 4-byte aligned.
+ *   starts_dev  int32 [n_seq + 1], ascending from 0: sequence s has starts[s + 1] - starts[s] tokens (none
+ *               is fine) and its tokens are rows starts[s].. of k and v; starts[n_seq] = T.
+ *   k_dev, v_dev  [T][H][D] elements of type dt (row strides ldk, ldv); either may be NULL.
+ * Tokens in pages that are out of the pool, or past ld_pages * P, read as 0.  T = 0 does nothing.
+ * Errors: as for qmm_cache_write.
+ */
+QMM_API qmm_status qmm_cache_read(qmm_type t, const void *k_cache_dev, const void *v_cache_dev, int64_t n_pages, int64_t P,
+                                  int64_t H, int64_t D, const int32_t *pages_dev, int64_t ld_pages,
+                                  const int32_t *starts_dev, int64_t n_seq, int64_t T, qmm_dtype dt, void *k_dev, void *v_dev,
+                                  int64_t ldk, int64_t ldv, qmm_stream_t stream);
+
+/* Bytes of workspace with which qmm_cache_attend splits long sequences over the whole GPU (see there); with
+ * less it splits them less.  0 if no split is of use, or a size is invalid. */
+QMM_API size_t qmm_cache_attend_workspace_size(int64_t n_seq, int64_t max_new, int64_t H, int64_t Hq, int64_t D, int64_t max_len);
+
+/*
+ * qmm_cache_attend -- attention of each sequence's new tokens (a decode step's one token, a tree of drafted
+ * tokens, or a piece of a prompt) over its cached tokens, the new ones included: their keys and values
+ * are written first, as the last tokens of the sequence.
+ *   out[i, hq] = sum_j p_j v[j, h] / sum_j p_j,  p_j = exp(scale * q[i, hq] . k[j, h]) over the visible j,
+ *   h = hq / (Hq / H) (Hq a multiple of H, at most 64 query heads to a key/value head).
+ *   q_starts_dev  int32 [n_seq + 1], ascending from 0: sequence s has nq = q_starts[s + 1] - q_starts[s] new
+ *                 tokens, rows q_starts[s].. of q; q_starts[n_seq] = T.
+ *   kv_lens_dev   int32 [n_seq]: its cached tokens n, the new ones included (0 is fine).
+ *   q_dev, out_dev  [T][Hq][D] of type dt (QMM_F16 or QMM_BF16), row strides ldq, ldo; 16-byte aligned with
+ *                 ldq % 8 == 0 and ldo % 8 == 0.
+ *   tree_dev      NULL: new token i sees the cached tokens before the new ones, and the new tokens 0..i.
+ *                 Otherwise uint64 [T], 8-byte aligned: bit b of a token's word says whether it sees new token b
+ *                 of its sequence (itself included); new tokens past the 64th are then seen by nobody.
+ *   max_new, max_len  no sequence has more new tokens, or more cached tokens, than these; rows past max_new are not
+ *                 computed, max_len only steers the split.
+ *   lse_dev       NULL, or fp32 [T][Hq]: ln sum_j exp(scale * q . k).
+ *   workspace_dev  NULL, or workspace_bytes of scratch, 256-byte aligned; calls that overlap on the GPU must
+ *                 use different workspaces.
+ * A row that sees nothing (no cached token, or none that its mask leaves) is 0, with lse -inf.  What a row
+ * does not see does not reach it, infinities and NaN included.  Tokens in pages that are out of the pool, or
+ * past ld_pages * P, are not seen.  Softmax statistics and sums are fp32.  T = 0 does nothing.
+ * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
+ * Errors: INVALID_ARG (sizes, strides, NULL, Hq % H), UNSUPPORTED (t, dt), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_cache_attend(qmm_type t, const void *k_cache_dev, const void *v_cache_dev, int64_t n_pages, int64_t P,
+                                    int64_t H, int64_t D, const int32_t *pages_dev, int64_t ld_pages,
+                                    const int32_t *q_starts_dev, const int32_t *kv_lens_dev, int64_t n_seq, qmm_dtype dt,
+                                    const void *q_dev, int64_t ldq, int64_t T, int64_t Hq, const uint64_t *tree_dev,
+                                    float scale, int64_t max_new, int64_t max_len, void *out_dev, int64_t ldo, float *lse_dev,
+                                    void *workspace_dev, size_t workspace_bytes, qmm_stream_t stream);
 
 /*
  * qmm_device_status -- synchronizes `stream`, then returns and clears the library's device status
