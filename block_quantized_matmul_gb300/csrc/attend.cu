@@ -1,26 +1,47 @@
 // attend.cu -- attention of a few new tokens of each sequence over the block-quantized cache (cache.cuh).
 //
 // For new token i of a sequence with n cached tokens, nq of them new, and query head hq (key/value head
-// h = hq / (Hq / H)):
+// h = hq / G, G = Hq / H):
 //   s_j = scale * sum_d q[i, hq, d] * k[j, h, d]  over the visible j,
 //   out[i, hq] = sum_j exp(s_j - max s) v[j, h] / sum_j exp(s_j - max s),   lse = max s + ln(sum);
 // j is visible when j < n - nq, or when bit j - (n - nq) of the token's tree word is set (without tree
 // words: when j - (n - nq) <= i).  A row that sees nothing is 0 with lse -inf.
 //
-// One warp a (token, query head): lanes share the head's elements, one pass over the keys with the
-// running maximum and sum.
+// The nq * G rows of a sequence and key/value head are taken 16 at a time, the height of the mma
+// instruction (m16n8k16): a decode step's few rows leave the bytes of the cache as the only cost, so each
+// code is expanded in registers, once per 16 rows, and never written back.  A CTA takes one chunk of
+// the keys; its warps take tiles of 32 keys in turn, each through its own ring of asynchronous copies
+// (no barriers), with its own running maximum and sum, and the warps' results are joined at the end.
+// Sequences longer than a chunk leave one partial result per chunk in the workspace, which a second
+// kernel joins.
+//
+// Arithmetic.  Scores: the codes are exact in fp16, the query row is scaled by a power of two into fp16's
+// range (an fp16 or bf16 query loses nothing but elements 2^-14 times smaller than the row's largest),
+// the tensor cores add the products of one block of 32 in fp32, and the block's scale multiplies that sum
+// in fp32.  Values: p in fp16, times 2^14 so that weights down to 2^-28 keep all 11 bits; v = d * q
+// rounded to fp16; sums in fp32.
+//
+// A position that a row does not see must not reach it, even if it holds infinities or NaN; 0 * NaN in
+// the second product would.  So scales past the end, and value scales that are not finite, count as 0
+// there.  Where such a scale (or a value beyond fp16) was met, a plain loop then takes the CTA's rows one
+// by one, and replaces those whose result is not finite by either way; no other cache pays for it.
 #include "cache.cuh"
 #include "elem.cuh"
+#include "pipeline.cuh"
+#include "tc_common.cuh"
 
 namespace qmm {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kRowsTile = 16;
+constexpr int kKeys = 32;                  // keys of a tile
+constexpr float kBias = 14.0f;             // p is kept times 2^14
 
 struct AttendParams {
     const uint8_t *k_cache, *v_cache;
     int64_t n_pages;
-    int P, H, D, group;
+    int P, log_p, H, group, row_tiles, splits;
+    int64_t chunk;                         // keys of a split
     const int32_t *pages;
     int64_t ld_pages;
     const int32_t *q_starts, *kv_lens;
@@ -28,9 +49,116 @@ struct AttendParams {
     const void *q;
     const uint64_t *tree;
     float scale;
+    int bf16;
     void *out;
     float *lse;
+    float *part_o, *part_ml;               // [splits][T * Hq][D], [splits][T * Hq][2]
 };
+
+// The 16- or 32-byte units of a tile are permuted so that the fragment loads of a warp meet no bank
+// twice: block b of row r (DB blocks a row) goes to place b ^ swizzle, U units spanning all banks.
+template <int DB, int U>
+__device__ __forceinline__ int swz(int r, int b) {
+    constexpr int Z = (DB % 8 == 0 && U == 8) ? 8 : (DB % 4 == 0 ? 4 : (DB % 2 == 0 ? 2 : 1));
+    return b ^ ((r / (U / Z)) & (Z - 1));
+}
+
+template <int TYPE, int DB>
+struct Tile {
+    static constexpr int kUnit = TYPE == QMM_Q8_0 ? 32 : 16;           // bytes of a block's codes
+    static constexpr int kSpan = TYPE == QMM_Q8_0 ? 4 : 8;             // units of 128 bytes
+    static constexpr int kCodes = kKeys * DB * kUnit;
+    static constexpr int kScales = kKeys * DB * 2;
+    static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales;
+    static constexpr int kBytes = kVs + kScales;
+    // eight warps, or four where a tile of eight would not fit twice
+    static constexpr int kWarps = 2 * 8 * kBytes <= 200 * 1024 ? 8 : 4;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kFit = 200 * 1024 / (kWarps * kBytes);
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kOut = kWarps * kRowsTile * DB * 32 * 4;      // the warps' results, over the ring
+    static constexpr int kQ = kRowsTile * DB * 32 * 2;                 // query fragments
+    static constexpr int kRing = kStages * kWarps * kBytes > kOut ? kStages * kWarps * kBytes : kOut;
+    static constexpr int kSmem = kRing + kQ + kWarps * kRowsTile * 8 + kRowsTile * 12 + kWarps * 8 * 4;
+    static_assert(kStages >= 2, "ring too shallow");
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return tc::h2_bits(__hmul2(tc::bits_h2(a), tc::bits_h2(b))); }
+// Ones in the halves of d that are finite.
+__device__ __forceinline__ uint32_t finite2(uint32_t d) { return __hlt2_mask(__habs2(tc::bits_h2(d)), tc::bits_h2(0x7C007C00u)); }
+// Nibbles 0 and 4 of w (Q4_0 codes) as half2, minus 8: exact.
+__device__ __forceinline__ uint32_t nib_h2(uint32_t w) {
+    uint32_t h;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(h) : "r"(w), "r"(0x000F000Fu), "r"(0x64006400u));
+    return tc::h2_bits(__hsub2(tc::bits_h2(h), __halves2half2(__float2half_rn(1032.0f), __float2half_rn(1032.0f))));
+}
+
+// Element pairs of a lane's query fragment: the pair that register r (0, 1: the mma's k = 2t.., k = 2t + 8..)
+// of k step st holds within a block, for the order in which the key codes come out of their words.
+template <int TYPE>
+__device__ __forceinline__ void frag_elems(int t, int st, int r, int &e0, int &e1) {
+    if (TYPE == QMM_Q8_0) {
+        e0 = 8 * t + 4 * st + 2 * r;
+        e1 = e0 + 1;
+    } else {
+        e0 = 16 * st + 4 * t + r;
+        e1 = e0 + 2;
+    }
+}
+
+struct Rows {                              // what a CTA works on
+    int64_t s, q0, n, first, k0, k1;
+    int h, r0, rows, used;
+    int64_t nq;
+};
+
+__device__ __forceinline__ float load_q(const AttendParams &p, int64_t at) {
+    return p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q)[at]) : __half2float(static_cast<const __half *>(p.q)[at]);
+}
+__device__ __forceinline__ void store_out(const AttendParams &p, int64_t at, float v) {
+    if (p.bf16) float_to_elem(v, static_cast<__nv_bfloat16 *>(p.out)[at]);
+    else float_to_elem(v, static_cast<__half *>(p.out)[at]);
+}
+
+// Token i of the sequence sees the new token b.
+__device__ __forceinline__ bool sees(const uint64_t *tree, int64_t tok, int i, int64_t b) {
+    return tree ? b < 64 && ((tree[tok] >> b) & 1) : b <= i;
+}
+
+// Where a row's result goes: the output when its sequence is not split, else this split's partial.
+__device__ __forceinline__ void write_row(const AttendParams &p, const Rows &w, int sp, int D, int row, int d, float o, float top, float sum) {
+    const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + r % p.group, Hq = p.H * p.group;
+    const int64_t at = (w.q0 + i) * Hq + hq;
+    if (w.used == 1) {
+        store_out(p, (w.q0 + i) * p.ldo + (int64_t)hq * D + d, sum == 0.0f ? 0.0f : o / sum);
+        if (d == 0 && p.lse) p.lse[at] = sum == 0.0f ? -INFINITY : (top + __log2f(sum) - kBias) * 0.6931471805599453f;
+    } else {
+        const int64_t part = (int64_t)sp * p.T * Hq + at;
+        p.part_o[part * D + d] = o;
+        if (d == 0) {
+            p.part_ml[2 * part] = top;
+            p.part_ml[2 * part + 1] = sum;
+        }
+    }
+}
 
 template <int TYPE>
 __device__ __forceinline__ float cache_value(const uint8_t *chunk, int P, int D, int off, int e) {
@@ -42,81 +170,557 @@ __device__ __forceinline__ float cache_value(const uint8_t *chunk, int P, int D,
     return d * (float)((int)((e % 32 < 16 ? b : b >> 4) & 15u) - 8);
 }
 
-template <int TYPE, typename T>
-__global__ void __launch_bounds__(kWarps * 32) attend_simple_kernel(const AttendParams p) {
+// The CTA's rows and keys once more, a warp a row, skipping what the row does not see; rows whose result
+// is finite, and was, keep the one they have.
+template <int TYPE, int DB>
+__device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &w, int sp, const int *row_bad) {
     const int lane = threadIdx.x & 31;
-    const int64_t tok = blockIdx.x;
-    const int Hq = p.H * p.group, nb = p.D / 32;
-    int64_t s = 0;
-    while (s + 1 < p.n_seq && p.q_starts[s + 1] <= tok) ++s;
-    const int64_t i = tok - p.q_starts[s], nq = p.q_starts[s + 1] - p.q_starts[s];
-    if (i < 0 || i >= nq) return;
-    int64_t n = p.kv_lens[s];
-    const int64_t first = n - nq;
-    if (n > p.ld_pages * p.P) n = p.ld_pages * p.P;
-    for (int hq = blockIdx.y * kWarps + (threadIdx.x >> 5); hq < Hq; hq += gridDim.y * kWarps) {
-        const int h = hq / p.group;
-        const T *qp = static_cast<const T *>(p.q) + tok * p.ldq + (int64_t)hq * p.D;
-        float q[8], o[8];
+    constexpr int D = DB * 32, kWarps = Tile<TYPE, DB>::kWarps;
+    for (int row = threadIdx.x >> 5; row < w.rows; row += kWarps) {
+        const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + r % p.group;
+        float q[DB], o[DB];
 #pragma unroll
-        for (int b = 0; b < 8; ++b) {
-            q[b] = b < nb ? elem_to_float(qp[32 * b + lane]) : 0.0f;
+        for (int b = 0; b < DB; ++b) {
+            q[b] = load_q(p, (w.q0 + i) * p.ldq + (int64_t)hq * D + 32 * b + lane);
             o[b] = 0.0f;
         }
-        float top = -INFINITY, sum = 0.0f;
-        for (int64_t j = 0; j < n; ++j) {
-            if (j >= first) {
-                const int64_t b = j - first;
-                if (p.tree ? (b >= 64 || !((p.tree[tok] >> b) & 1)) : b > i) continue;
-            }
-            const int64_t page = p.pages[s * p.ld_pages + j / p.P];
+        float top = -INFINITY, sum = 0.0f;                      // in powers of two
+        for (int64_t j = w.k0; j < w.k1; ++j) {
+            if (j >= w.first && !sees(p.tree, w.q0 + i, i, j - w.first)) continue;
+            const int64_t page = p.pages[w.s * p.ld_pages + (j >> p.log_p)];
             if (page < 0 || page >= p.n_pages) continue;
-            const int64_t at = cache_chunk(TYPE, p.H, p.D, p.P, page, h);
-            const int off = (int)(j % p.P);
+            const int64_t at = cache_chunk(TYPE, p.H, D, p.P, page, w.h);
+            const int off = (int)(j & (p.P - 1));
             float x = 0.0f;
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-                if (b < nb) x += q[b] * cache_value<TYPE>(p.k_cache + at, p.P, p.D, off, 32 * b + lane);
+            for (int b = 0; b < DB; ++b) x += q[b] * cache_value<TYPE>(p.k_cache + at, p.P, D, off, 32 * b + lane);
 #pragma unroll
-            for (int w = 16; w > 0; w >>= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
-            x *= p.scale;
-            const float m = fmaxf(top, x);
-            const float base = m == -INFINITY ? 0.0f : m;
-            const float down = __expf(top - base), e = __expf(x - base);
+            for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
+            x *= p.scale * 1.4426950408889634f;
+            const float m = fmaxf(top, x), base = m == -INFINITY ? 0.0f : m;
+            const float down = exp2f(top - base), e = exp2f(x - base + kBias);
             top = m;
             sum = sum * down + e;
 #pragma unroll
-            for (int b = 0; b < 8; ++b)
-                if (b < nb) o[b] = o[b] * down + e * cache_value<TYPE>(p.v_cache + at, p.P, p.D, off, 32 * b + lane);
+            for (int b = 0; b < DB; ++b) o[b] = o[b] * down + e * cache_value<TYPE>(p.v_cache + at, p.P, D, off, 32 * b + lane);
         }
-        T *op = static_cast<T *>(p.out) + tok * p.ldo + (int64_t)hq * p.D;
+        bool fine = sum < INFINITY && !row_bad[row];
 #pragma unroll
-        for (int b = 0; b < 8; ++b)
-            if (b < nb) float_to_elem(sum == 0.0f ? 0.0f : o[b] / sum, op[32 * b + lane]);
-        if (p.lse && lane == 0) p.lse[tok * Hq + hq] = sum == 0.0f ? -INFINITY : top + __logf(sum);
+        for (int b = 0; b < DB; ++b) fine = fine && fabsf(o[b]) < INFINITY;
+        if (__all_sync(0xffffffffu, fine)) continue;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) write_row(p, w, sp, D, row, 32 * b + lane, o[b], top, sum);
+    }
+}
+
+template <int TYPE, int DB>
+__global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(const AttendParams p) {
+    using L = Tile<TYPE, DB>;
+    constexpr int D = DB * 32, S = L::kStages, UNIT = L::kUnit, SPAN = L::kSpan, CB = DB * UNIT;
+    constexpr int kWarps = L::kWarps, kThreads = L::kThreads;
+    constexpr bool kQRegs = DB <= 4;       // the query fragments stay in registers
+    extern __shared__ __align__(128) uint8_t smem[];
+    uint32_t *q_frag = reinterpret_cast<uint32_t *>(smem + L::kRing);       // [block][step][lane][4]
+    float *w_top = reinterpret_cast<float *>(smem + L::kRing + L::kQ);       // [warp][row]
+    float *w_sum = w_top + kWarps * kRowsTile;
+    float *row_mul = w_sum + kWarps * kRowsTile;                              // score -> power of two
+    float *row_down = row_mul + kRowsTile;                                    // query -> fp16
+    int *row_bad = reinterpret_cast<int *>(row_down + kRowsTile);             // its result is not finite
+    uint32_t *masks = reinterpret_cast<uint32_t *>(row_bad + kRowsTile);      // [warp][stage]
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    int64_t at = blockIdx.x;
+    const int sp = (int)(at % p.splits);
+    at /= p.splits;
+    const int rt = (int)(at % p.row_tiles);
+    at /= p.row_tiles;
+    Rows w;
+    w.h = (int)(at % p.H);
+    w.s = at / p.H;
+    w.q0 = p.q_starts[w.s];
+    w.nq = p.q_starts[w.s + 1] - w.q0;
+    w.r0 = rt * kRowsTile;
+    w.rows = (int)min((int64_t)kRowsTile, w.nq * p.group - w.r0);
+    if (w.rows <= 0) return;
+    w.n = p.kv_lens[w.s];
+    w.first = w.n - w.nq;
+    w.n = max((int64_t)0, min(w.n, p.ld_pages << p.log_p));
+    w.used = (int)min((int64_t)p.splits, max((int64_t)1, (w.n + p.chunk - 1) / p.chunk));
+    if (sp >= w.used) return;
+    w.k0 = sp * p.chunk;
+    w.k1 = sp == p.splits - 1 ? w.n : min(w.n, w.k0 + p.chunk);
+
+    // the query rows: scaled by a power of two so that the largest element lies in [1, 2), as fragments
+    for (int row = warp; row < kRowsTile; row += kWarps) {
+        const int r = w.r0 + row;
+        const int64_t base = row < w.rows ? (w.q0 + r / p.group) * p.ldq + (int64_t)(w.h * p.group + r % p.group) * D : 0;
+        float top = 0.0f;
+        for (int b = 0; b < DB; ++b)
+            if (row < w.rows) top = fmaxf(top, fabsf(load_q(p, base + 32 * b + lane)));
+#pragma unroll
+        for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        if (lane == 0) {
+            const int e = top > 0.0f && top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
+            const float mul = p.scale * 1.4426950408889634f;
+            row_down[row] = copysignf(exp2f((float)-e), mul);
+            // a scale of 0 still has to order -inf below 0
+            row_mul[row] = fmaxf(fabsf(mul), 1e-30f) * exp2f((float)e);
+            row_bad[row] = 0;
+        }
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < DB * 2 * 32 * 4; i += kThreads) {
+        const int reg = i & 3, ln = (i >> 2) & 31, st = (i >> 7) & 1, b = i >> 8;
+        const int row = (ln >> 2) + 8 * (reg & 1);
+        int e0, e1;
+        frag_elems<TYPE>(ln & 3, st, reg >> 1, e0, e1);
+        uint32_t v = 0;
+        if (row < w.rows) {
+            const int r = w.r0 + row;
+            const int64_t base = (w.q0 + r / p.group) * p.ldq + (int64_t)(w.h * p.group + r % p.group) * D + 32 * b;
+            v = pack2(load_q(p, base + e0) * row_down[row], load_q(p, base + e1) * row_down[row], __half{});
+        }
+        q_frag[i] = v;
+    }
+    __syncthreads();
+    uint32_t qr[kQRegs ? DB : 1][2][4];
+    if constexpr (kQRegs) {
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + ((b * 2 + st) * 32 + lane) * 4);
+                qr[b][st][0] = v.x; qr[b][st][1] = v.y; qr[b][st][2] = v.z; qr[b][st][3] = v.w;
+            }
+    }
+    const float mul[2] = {row_mul[g], row_mul[g + 8]};
+    // what rows g and g + 8 see of the new tokens: a tree word, or (without) tokens up to their own
+    const int tok0 = (w.r0 + g) / p.group, tok1 = (w.r0 + g + 8) / p.group;
+    uint64_t word0 = 0, word1 = 0;
+    if (p.tree) {
+        word0 = g < w.rows ? p.tree[w.q0 + tok0] : 0;
+        word1 = g + 8 < w.rows ? p.tree[w.q0 + tok1] : 0;
+    }
+
+    // ---- the ring: tile i of this warp is keys k0 + 32 * (kWarps i + warp) .. ----
+    const uint32_t ring = pipe::smem_u32(smem) + (uint32_t)(warp * S * L::kBytes);
+    const int64_t head = (int64_t)w.h * p.P * cache_token_bytes(TYPE, D), page_bytes = (int64_t)p.H * p.P * cache_token_bytes(TYPE, D);
+    const int tiles = (int)((w.k1 - w.k0 + kKeys - 1) / kKeys);
+    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+    const int32_t *table = p.pages + w.s * p.ld_pages;
+    // lanes 0-15 know the page of the tile's first 16 keys, lanes 16-31 that of the others
+    auto page_of = [&](int i) -> int {
+        const int64_t j = w.k0 + (int64_t)(i * kWarps + warp) * kKeys + (lane & 16);
+        return i < mine && j < w.k1 ? table[j >> p.log_p] : -1;
+    };
+    auto issue = [&](int i, int page) {
+        if (i < mine) {
+            const int slot = i % S;
+            const uint32_t dst = ring + (uint32_t)(slot * L::kBytes);
+            const int64_t j = w.k0 + (int64_t)(i * kWarps + warp) * kKeys;
+            const int pg[2] = {__shfl_sync(0xffffffffu, page, 0), __shfl_sync(0xffffffffu, page, 16)};
+            const bool ok[2] = {pg[0] >= 0 && pg[0] < p.n_pages, pg[1] >= 0 && pg[1] < p.n_pages};
+            const int off = (int)(j & (p.P - 1));
+            const int64_t c0 = (int64_t)pg[0] * page_bytes + head, c1 = (int64_t)pg[1] * page_bytes + head;
+            const int off1 = (off + 16) & (p.P - 1);
+            // codes, 16 bytes a lane: kKeys * CB / 16 pieces of keys, as many of values
+#pragma unroll
+            for (int it = 0; it < kKeys * CB / 16 / 32; ++it) {
+                constexpr int PK = CB / 16;                     // pieces of a key
+                const int u = it * 32 + lane, key = u / PK, c = u % PK;
+                const bool second = key >= 16;
+                if (second ? ok[1] : ok[0]) {
+                    const int64_t src = (second ? c1 + (int64_t)(off1 + key - 16) * CB : c0 + (int64_t)(off + key) * CB) + c * 16;
+                    const int blk = c * 16 / UNIT, in = c * 16 % UNIT;
+                    const int vrow = (key & 16) | ((key & 1) << 3) | ((key & 15) >> 1);
+                    cp_async16(dst + L::kK + (key * DB + swz<DB, SPAN>(key, blk)) * UNIT + in, p.k_cache + src);
+                    cp_async16(dst + L::kV + (vrow * DB + swz<DB, SPAN>(vrow, blk)) * UNIT + in, p.v_cache + src);
+                }
+            }
+            // scales: 2 * DB pieces for 16 keys
+            if (lane < 4 * DB) {
+                const bool second = lane >= 2 * DB;
+                const int c = second ? lane - 2 * DB : lane;
+                if (second ? ok[1] : ok[0]) {
+                    const int64_t src = (second ? c1 + (int64_t)off1 * (2 * DB) : c0 + (int64_t)off * (2 * DB)) + (int64_t)p.P * CB + c * 16;
+                    cp_async16(dst + L::kKs + lane * 16, p.k_cache + src);
+                    cp_async16(dst + L::kVs + lane * 16, p.v_cache + src);
+                }
+            }
+            if (lane == 0) {
+                const int64_t left = w.k1 - j;
+                uint32_t m = left >= 32 ? 0xffffffffu : (1u << (int)left) - 1u;
+                if (!ok[0]) m &= 0xffff0000u;
+                if (!ok[1]) m &= 0x0000ffffu;
+                masks[warp * 8 + slot] = m;
+            }
+        }
+        cp_commit();
+    };
+
+    float o[4 * DB][4];
+#pragma unroll
+    for (int i = 0; i < 4 * DB; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+    uint32_t odd = 0;                                            // a value scale that is not finite
+
+    int page = page_of(0);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        const int next = page_of(i + 1);
+        issue(i, page);
+        page = next;
+    }
+    for (int i = 0; i < mine; ++i) {
+        cp_wait<S - 2>();
+        __syncwarp();
+        {
+            const int next = page_of(i + S);
+            issue(i + S - 1, page);
+            page = next;
+        }
+        const uint8_t *st = smem + warp * S * L::kBytes + (i % S) * L::kBytes;
+        const uint32_t in = masks[warp * 8 + i % S];
+        const int64_t j0 = w.k0 + (int64_t)(i * kWarps + warp) * kKeys;
+
+        // ---- scores: sc[nt] holds keys 8 nt + 2t, + 1 of rows g (0, 1) and g + 8 (2, 3) ----
+        float sc[4][4];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+        const __half *ks = reinterpret_cast<const __half *>(st + L::kKs);
+#pragma unroll
+        for (int b = 0; b < DB; ++b) {
+            uint32_t a[2][4];
+            if constexpr (kQRegs) {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    a[0][r] = qr[b][0][r];
+                    a[1][r] = qr[b][1][r];
+                }
+            } else {
+#pragma unroll
+                for (int s2 = 0; s2 < 2; ++s2) {
+                    const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + ((b * 2 + s2) * 32 + lane) * 4);
+                    a[s2][0] = v.x; a[s2][1] = v.y; a[s2][2] = v.z; a[s2][3] = v.w;
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt) {
+                const int key = 8 * nt + g;
+                const uint8_t *kp = st + L::kK + (key * DB + swz<DB, SPAN>(key, b)) * UNIT;
+                uint32_t f[4];
+                if constexpr (TYPE == QMM_Q8_0) {
+                    const uint2 c = *reinterpret_cast<const uint2 *>(kp + 8 * t);
+                    tc::i8x4_to_h2x2(c.x, f[0], f[1]);
+                    tc::i8x4_to_h2x2(c.y, f[2], f[3]);
+                } else {
+                    const uint32_t c = *reinterpret_cast<const uint32_t *>(kp + 4 * t);
+                    f[0] = nib_h2(c);
+                    f[1] = nib_h2(c >> 8);
+                    f[2] = nib_h2(c >> 4);
+                    f[3] = nib_h2(c >> 12);
+                }
+                float acc[4] = {0.f, 0.f, 0.f, 0.f};
+                mma16816(acc, a[0], f[0], f[1]);
+                mma16816(acc, a[1], f[2], f[3]);
+                const float d0 = __half2float(ks[(8 * nt + 2 * t) * DB + b]), d1 = __half2float(ks[(8 * nt + 2 * t + 1) * DB + b]);
+                sc[nt][0] += d0 * acc[0];
+                sc[nt][1] += d1 * acc[1];
+                sc[nt][2] += d0 * acc[2];
+                sc[nt][3] += d1 * acc[3];
+            }
+        }
+        // ---- what is not seen ----
+        if (in != 0xffffffffu || j0 + kKeys > w.first) {
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int key = 8 * nt + 2 * t + c;
+                    const int64_t nb = j0 + key - w.first;       // place among the new tokens
+                    const bool have = (in >> key) & 1;
+                    bool s0 = have, s1 = have;
+                    if (nb >= 0) {
+                        s0 = have && (p.tree ? nb < 64 && ((word0 >> nb) & 1) : nb <= tok0);
+                        s1 = have && (p.tree ? nb < 64 && ((word1 >> nb) & 1) : nb <= tok1);
+                    }
+                    if (!s0) sc[nt][c] = -INFINITY;
+                    if (!s1) sc[nt][2 + c] = -INFINITY;
+                }
+        }
+        // ---- running maximum and sum; p to fp16 ----
+        float base[2];
+        bool moved = false;
+        float down[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            float m = fmaxf(fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1])),
+                            fmaxf(fmaxf(sc[2][2 * r], sc[2][2 * r + 1]), fmaxf(sc[3][2 * r], sc[3][2 * r + 1])));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            m = fmaxf(m * mul[r], top[r]);
+            base[r] = m == -INFINITY ? 0.0f : m;
+            down[r] = ex2(top[r] - base[r]);
+            moved |= m != top[r];
+            top[r] = m;
+        }
+        if (__any_sync(0xffffffffu, moved)) {
+            sum[0] *= down[0];
+            sum[1] *= down[1];
+#pragma unroll
+            for (int n = 0; n < 4 * DB; ++n) {
+                o[n][0] *= down[0];
+                o[n][1] *= down[0];
+                o[n][2] *= down[1];
+                o[n][3] *= down[1];
+            }
+        }
+        uint32_t pf[4][2];
+#pragma unroll
+        for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const float p0 = ex2(fmaf(sc[nt][2 * r], mul[r], kBias - base[r])), p1 = ex2(fmaf(sc[nt][2 * r + 1], mul[r], kBias - base[r]));
+                sum[r] += p0 + p1;
+                pf[nt][r] = pack2(p0, p1, __half{});
+            }
+        // ---- values: 16 keys a step; a lane's keys are 2t, 2t + 1, 2t + 8, 2t + 9 ----
+        const __half *vs = reinterpret_cast<const __half *>(st + L::kVs);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const uint32_t a[4] = {pf[2 * j][0], pf[2 * j][1], pf[2 * j + 1][0], pf[2 * j + 1][1]};
+            const uint32_t have = in >> (16 * j + 2 * t);
+            const uint32_t m01 = ((have & 1) ? 0xffffu : 0u) | ((have & 2) ? 0xffff0000u : 0u);
+            const uint32_t m89 = ((have & 256) ? 0xffffu : 0u) | ((have & 512) ? 0xffff0000u : 0u);
+            const int k0 = 16 * j + 2 * t;
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                uint32_t d01 = m01 & ((uint32_t)__half_as_ushort(vs[k0 * DB + b]) | ((uint32_t)__half_as_ushort(vs[(k0 + 1) * DB + b]) << 16));
+                uint32_t d89 = m89 & ((uint32_t)__half_as_ushort(vs[(k0 + 8) * DB + b]) | ((uint32_t)__half_as_ushort(vs[(k0 + 9) * DB + b]) << 16));
+                const uint32_t f01 = finite2(d01), f89 = finite2(d89);
+                odd |= ~(f01 & f89);
+                d01 &= f01;
+                d89 &= f89;
+                const uint8_t *vp = st + L::kV;
+                const int r0 = 16 * j + t;                       // rows of keys 2t, 2t + 8, 2t + 1, 2t + 9: t, t + 4, t + 8, t + 12
+                auto row = [&](int r) { return vp + (r * DB + swz<DB, SPAN>(r, b)) * UNIT; };
+                uint32_t x[4], y[4];                             // n tile e: keys 2t, 2t + 1 and 2t + 8, 2t + 9
+                if constexpr (TYPE == QMM_Q8_0) {
+                    const uint32_t k0w = *reinterpret_cast<const uint32_t *>(row(r0) + 4 * g), k8w = *reinterpret_cast<const uint32_t *>(row(r0 + 4) + 4 * g);
+                    const uint32_t k1w = *reinterpret_cast<const uint32_t *>(row(r0 + 8) + 4 * g), k9w = *reinterpret_cast<const uint32_t *>(row(r0 + 12) + 4 * g);
+                    tc::i8x4_to_h2x2(__byte_perm(k0w, k1w, 0x5140), x[0], x[1]);
+                    tc::i8x4_to_h2x2(__byte_perm(k0w, k1w, 0x7362), x[2], x[3]);
+                    tc::i8x4_to_h2x2(__byte_perm(k8w, k9w, 0x5140), y[0], y[1]);
+                    tc::i8x4_to_h2x2(__byte_perm(k8w, k9w, 0x7362), y[2], y[3]);
+                } else {
+                    const uint32_t c01 = (uint32_t)*reinterpret_cast<const uint16_t *>(row(r0) + 2 * g) |
+                                         ((uint32_t)*reinterpret_cast<const uint16_t *>(row(r0 + 8) + 2 * g) << 16);
+                    const uint32_t c89 = (uint32_t)*reinterpret_cast<const uint16_t *>(row(r0 + 4) + 2 * g) |
+                                         ((uint32_t)*reinterpret_cast<const uint16_t *>(row(r0 + 12) + 2 * g) << 16);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[e] = nib_h2(c01 >> (4 * e));
+                        y[e] = nib_h2(c89 >> (4 * e));
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) mma16816(o[4 * b + e], a, hmul2(x[e], d01), hmul2(y[e], d89));
+            }
+        }
+        __syncwarp();
+    }
+    cp_wait<0>();
+
+    // ---- the warps' results, joined ----
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
+        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
+    }
+    __syncthreads();                                             // the ring is free
+    float *res = reinterpret_cast<float *>(smem) + warp * kRowsTile * D;
+    if (t == 0) {
+        w_top[warp * kRowsTile + g] = top[0];
+        w_top[warp * kRowsTile + g + 8] = top[1];
+        w_sum[warp * kRowsTile + g] = sum[0];
+        w_sum[warp * kRowsTile + g + 8] = sum[1];
+    }
+#pragma unroll
+    for (int b = 0; b < DB; ++b)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int row = g + 8 * (c >> 1), n = 2 * t + (c & 1);
+                // n tile e of block b, column n: the element whose codes were fed to it
+                const int d = TYPE == QMM_Q8_0 ? 4 * n + e : 2 * n + (e >> 1) + 16 * (e & 1);
+                if (row < w.rows) res[row * D + 32 * b + d] = o[4 * b + e][c];
+            }
+    __syncthreads();
+    bool bad = odd != 0;
+    for (int i = threadIdx.x; i < w.rows * D; i += kThreads) {
+        const int row = i / D, d = i % D;
+        float m = -INFINITY;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) m = fmaxf(m, w_top[x * kRowsTile + row]);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float v = 0.0f, l = 0.0f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+            const float f = ex2(w_top[x * kRowsTile + row] - base);
+            l += f * w_sum[x * kRowsTile + row];
+            v += f * reinterpret_cast<const float *>(smem)[(x * kRowsTile + row) * D + d];
+        }
+        if (!(fabsf(v) < INFINITY) || !(l < INFINITY)) {
+            bad = true;
+            row_bad[row] = 1;
+        }
+        write_row(p, w, sp, D, row, d, v, m, l);
+    }
+    if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB>(p, w, sp, row_bad);
+}
+
+// Joins the partial results of the sequences that were split: one warp a row.
+template <int DB>
+__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) {
+    constexpr int D = DB * 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, Hq = p.H * p.group;
+    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
+    if (at >= p.T * Hq) return;
+    const int64_t tok = at / Hq;
+    const int hq = (int)(at - tok * Hq);
+    int64_t lo = 0, hi = p.n_seq - 1;
+    while (lo < hi) {
+        const int64_t mid = (lo + hi + 1) >> 1;
+        if (p.q_starts[mid] <= tok) lo = mid; else hi = mid - 1;
+    }
+    // rows past row_tiles were not computed
+    if ((tok - p.q_starts[lo]) * p.group + hq % p.group >= (int64_t)p.row_tiles * kRowsTile) return;
+    const int64_t n = max((int64_t)0, min((int64_t)p.kv_lens[lo], p.ld_pages << p.log_p));
+    const int used = (int)min((int64_t)p.splits, (n + p.chunk - 1) / p.chunk);
+    if (used <= 1) return;
+    const int64_t stride = p.T * Hq;
+    float m = -INFINITY;
+    for (int s = lane; s < used; s += 32) m = fmaxf(m, p.part_ml[2 * (s * stride + at)]);
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+    const float base = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f, o[DB];
+#pragma unroll
+    for (int b = 0; b < DB; ++b) o[b] = 0.0f;
+    for (int s = 0; s < used; ++s) {
+        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * stride + at));
+        if (ml.y == 0.0f) continue;                              // nothing seen there
+        const float f = exp2f(ml.x - base);
+        l += f * ml.y;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) o[b] += f * p.part_o[(s * stride + at) * D + 32 * b + lane];
+    }
+#pragma unroll
+    for (int b = 0; b < DB; ++b) store_out(p, tok * p.ldo + (int64_t)hq * D + 32 * b + lane, l == 0.0f ? 0.0f : o[b] / l);
+    if (lane == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l) - kBias) * 0.6931471805599453f;
+}
+
+constexpr int64_t kMinChunk = 8 * kKeys;           // one tile a warp
+constexpr int kMaxSplits = 256;
+
+// Splits of the longest sequence: until there are several CTAs an SM (ragged lengths even out), but no
+// chunk below two tiles a warp.
+int wanted_splits(int64_t units, int64_t max_len) {
+    const int64_t most = (max_len + 2 * kMinChunk - 1) / (2 * kMinChunk);
+    int64_t want = (152 * 4 + units - 1) / units;
+    want = want < most ? want : most;
+    want = want < kMaxSplits ? want : kMaxSplits;
+    return (int)(want < 1 ? 1 : want);
+}
+int64_t row_tiles_of(int64_t max_new, int group) { return (max_new * group + kRowsTile - 1) / kRowsTile; }
+size_t split_bytes(int64_t rows, int D) { return round256((size_t)rows * (size_t)(D + 2) * 4); }
+
+template <int TYPE, int DB>
+cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
+    using L = Tile<TYPE, DB>;
+    static_assert(L::kSmem <= 227 * 1024, "shared memory plan too large");
+    auto kern = attend_kernel<TYPE, DB>;
+    static int attr_done[4] = {0, 0, 0, 0};
+    cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3((unsigned)ctas), L::kThreads, L::kSmem, s, p);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const int64_t rows = p.T * p.H * p.group;
+    return launch_pdl(attend_join_kernel<DB>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, p);
+}
+
+template <int TYPE>
+cudaError_t launch_blocks(const AttendParams &p, int DB, int64_t ctas, cudaStream_t s) {
+    switch (DB) {
+        case 1: return launch_typed<TYPE, 1>(p, ctas, s);
+        case 2: return launch_typed<TYPE, 2>(p, ctas, s);
+        case 3: return launch_typed<TYPE, 3>(p, ctas, s);
+        case 4: return launch_typed<TYPE, 4>(p, ctas, s);
+        case 5: return launch_typed<TYPE, 5>(p, ctas, s);
+        case 6: return launch_typed<TYPE, 6>(p, ctas, s);
+        case 7: return launch_typed<TYPE, 7>(p, ctas, s);
+        default: return launch_typed<TYPE, 8>(p, ctas, s);
     }
 }
 
 }  // namespace
 
-size_t attend_workspace_bytes(int64_t, int64_t, int, int, int, int64_t) { return 0; }
+size_t attend_workspace_bytes(int64_t n_seq, int64_t max_new, int H, int Hq, int D, int64_t max_len) {
+    const int splits = wanted_splits(n_seq * H * row_tiles_of(max_new, Hq / H), max_len);
+    return splits == 1 ? 0 : (size_t)splits * split_bytes(n_seq * max_new * Hq, D);
+}
 
 cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uint8_t *v_cache, int64_t n_pages, int P, int H, int D,
                                 const int32_t *pages, int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens,
                                 int64_t n_seq, qmm_dtype t, const void *q, int64_t ldq, int64_t T, int Hq, const uint64_t *tree,
                                 float scale, int64_t max_new, int64_t max_len, void *out, int64_t ldo, float *lse, void *ws,
                                 size_t ws_bytes, cudaStream_t s) {
-    const AttendParams p{k_cache, v_cache, n_pages, P, H, D, Hq / H, pages, ld_pages, q_starts, kv_lens, n_seq, T, ldq, ldo, q, tree,
-                         scale, out, lse};
-    const dim3 grid((unsigned)T, (unsigned)((Hq + kWarps - 1) / kWarps));
-    if (type == QMM_Q8_0) {
-        if (t == QMM_F16) attend_simple_kernel<QMM_Q8_0, __half><<<grid, kWarps * 32, 0, s>>>(p);
-        else attend_simple_kernel<QMM_Q8_0, __nv_bfloat16><<<grid, kWarps * 32, 0, s>>>(p);
+    AttendParams p = {};
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.n_pages = n_pages;
+    p.P = P;
+    while ((1 << p.log_p) < P) ++p.log_p;
+    p.H = H;
+    p.group = Hq / H;
+    const int64_t row_tiles = row_tiles_of(max_new < T ? max_new : T, p.group);   // no sequence has more than T
+    const int64_t units = n_seq * H * row_tiles;
+    if (units > 0x7fffffff) return cudaErrorInvalidValue;
+    p.row_tiles = (int)row_tiles;
+    p.pages = pages;
+    p.ld_pages = ld_pages;
+    p.q_starts = q_starts;
+    p.kv_lens = kv_lens;
+    p.n_seq = n_seq;
+    p.T = T;
+    p.ldq = ldq;
+    p.ldo = ldo;
+    p.q = q;
+    p.tree = tree;
+    p.scale = scale;
+    p.bf16 = t == QMM_BF16;
+    p.out = out;
+    p.lse = lse;
+    const size_t per_split = split_bytes(T * Hq, D);
+    p.splits = wanted_splits(units, max_len);
+    if ((size_t)p.splits * per_split > ws_bytes) p.splits = (int)(ws_bytes / per_split);
+    if (p.splits < 2) {
+        p.splits = 1;
+        p.chunk = (int64_t)1 << 40;
     } else {
-        if (t == QMM_F16) attend_simple_kernel<QMM_Q4_0, __half><<<grid, kWarps * 32, 0, s>>>(p);
-        else attend_simple_kernel<QMM_Q4_0, __nv_bfloat16><<<grid, kWarps * 32, 0, s>>>(p);
+        p.chunk = ((max_len + p.splits - 1) / p.splits + kMinChunk - 1) / kMinChunk * kMinChunk;
+        p.part_o = static_cast<float *>(ws);
+        p.part_ml = p.part_o + (size_t)p.splits * (size_t)T * (size_t)Hq * (size_t)D;
     }
-    return cudaGetLastError();
+    const int64_t ctas = units * p.splits;
+    if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
+    return type == QMM_Q8_0 ? launch_blocks<QMM_Q8_0>(p, D / 32, ctas, s) : launch_blocks<QMM_Q4_0>(p, D / 32, ctas, s);
 }
 
 QMM_DCHECK_READER(read_dcheck_attend)

@@ -1,57 +1,363 @@
-// mx4_gemm.cu -- the product of two microscaled 4-bit operands (mx4.cuh).
+// mx4_gemm.cu -- the product of two microscaled 4-bit operands (mx4.cuh) on the block-scaled tensor cores
+// (tcgen05.mma, kind::mxf4: E2M1 x E2M1 with one E8M0 scale per 32 of either operand, fp32 sums).
 //
 //   Y[m, n] = sum_b 2^(ea[m, b] + ew[n, b] - 254) * sum_{j < 32} a[m, 32b + j] * w[n, 32b + j]
 //
-// One thread an output; the lanes of a warp take consecutive n.
+// One kernel for every number of tokens: the weight rows are the instruction's 128 rows (the lanes of
+// tensor memory), the tokens its columns, TN = 16 to 256 of them.  So one token costs no more than the
+// weight's bytes, and a lane's results of one token are consecutive in y.
+//
+// A stage of the pipeline is 256 of K: 128 weight rows x 128 bytes and TN token rows x 128 bytes by
+// tensor copies into the 128-byte-swizzled layout, and the scales of both, which are stored as the
+// instruction wants them (512 bytes for 128 rows x 128 K), by plain bulk copies.  tcgen05.cp moves the
+// scales on into tensor memory; the same thread issues the copies and the products, so they stay in order.
+// Rows past an operand's end and K past its end arrive as zero codes; the scales there are 0 (K) or
+// belong to rows whose results are not stored.
+//
+// Few tokens: the weight's row tiles alone do not fill the GPU, so the CTAs of a cluster share a tile and
+// take K in turn; each adds up the parts of its share of the tokens, in the order of the ranks, through
+// distributed shared memory.
+//
+// Warps: 0 copies, 1 products (and tensor memory), 2-5 results.
+// Every wait is bounded; on expiry the kernel records QMM_ERR_TIMEOUT, lets what is in flight land,
+// frees tensor memory and returns.
+#include <cuda.h>
+
+#include "pipeline.cuh"
 #include "qmm_internal.cuh"
 
 #include "elem.cuh"
 #include "mx4.cuh"
+#include "tc_common.cuh"
 
 namespace qmm {
 namespace {
 
+__device__ unsigned g_mx4_status = 0;      // bit 0: a bounded wait gave up
+
+using namespace pipe;
+using namespace tc;
+
+constexpr int kRows = 128;                 // weight rows per tile
+constexpr int kThreads = 192;
+constexpr int kEpilogue = 128;
+constexpr int kMaxSplit = 8;
+
+struct Mx4Params {
+    const uint8_t *ws, *as;                // scales of the weight and the activations
+    void *y;
+    int64_t N, M, ldy;
+    int n128;                              // K / 128, rounded up: scale blocks of a row of blocks
+    int nk;                                // stages: K / 256, rounded up
+    int last_steps;                        // K = 64 products of the last stage (1 to 4)
+    int m_blocks;                          // row blocks of the activations' scales
+    int split;                             // CTAs of a cluster, which share a tile's K
+    int early_weights;                     // the kernel before this one writes no weight
+    int dtype;
+};
+
+__device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return wait_bounded_on(bar, parity, abort, &g_mx4_status, kWaitLimitNs);
+}
+__device__ __forceinline__ bool wait_warp(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, wait_bounded(bar, parity, abort));
+}
+
+// Shared-memory descriptor of 32 lanes x 16 bytes of scales, unswizzled: 8-row groups 128 bytes apart.
+__device__ __forceinline__ uint64_t smem_desc_scales(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 32) | ((uint64_t)1 << 46);
+}
+// 512 bytes of scales -> four columns of tensor memory, the 32 lanes repeated in each lane quadrant.
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                         uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// Instruction descriptor: E2M1 A and B, E8M0 scales, 128 x n; `half` picks the two scales of a K = 64
+// product out of the four bytes of a column.
+__device__ __forceinline__ constexpr uint32_t idesc_mxf4(int n, int half) {
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | (1u << 23) | ((uint32_t)(kRows >> 4) << 24) |
+           ((uint32_t)(2 * half) << 29) | ((uint32_t)(2 * half) << 4);
+}
+
+template <int TN>
+struct Plan {
+    static constexpr int kTokBlocks = (TN + 127) / 128;                  // 128-row blocks of token scales
+    static constexpr int kW = 0;
+    static constexpr int kA = kW + kRows * 128;
+    static constexpr int kWS = kA + (TN * 128 + 1023) / 1024 * 1024;
+    static constexpr int kAS = kWS + 2 * kMx4ScaleBlock;
+    static constexpr int kStageBytes = kAS + kTokBlocks * 2 * kMx4ScaleBlock;
+    static constexpr int kStages = TN >= 256 ? 4 : (TN >= 128 ? 6 : 5);
+    // tensor memory: the sums, then per stage the scales of two K = 128 halves (weight 4 columns, tokens 4
+    // columns per block)
+    static constexpr int kSums = TN < 32 ? 32 : TN;
+    static constexpr int kHalfCols = 4 + 4 * kTokBlocks;
+    static constexpr int kColsUsed = kSums + kStages * 2 * kHalfCols;
+    static constexpr int kCols = kColsUsed <= 128 ? 128 : (kColsUsed <= 256 ? 256 : 512);
+    // parts of the other CTAs of a cluster: [rank][token of this CTA's share][row]
+    static constexpr int kParts = TN <= 32 ? TN * kRows * 4 : 0;
+    static constexpr int kPartsAt = kStages * kStageBytes;
+    static constexpr int kBars = kPartsAt + kParts;
+    static constexpr size_t kSmem = 1024 + kBars + (2 * kStages + 2) * 8 + 16;
+    static_assert(kColsUsed <= 512 && kSmem <= 227 * 1024, "does not fit");
+};
+
+// Stores results v[0..n) of tokens m0.. for weight row `row`, those that exist.
 template <typename T>
-__global__ void __launch_bounds__(256) mx4_matmul_kernel(const uint8_t *__restrict__ wc, const uint8_t *__restrict__ ws, int64_t K,
-                                                         int64_t N, const uint8_t *__restrict__ ac,
-                                                         const uint8_t *__restrict__ as, int64_t M, T *__restrict__ y,
-                                                         int64_t ldy) {
-    const int64_t n128 = (K + 127) / 128;
-    const int64_t n = (int64_t)blockIdx.x * 32 + (threadIdx.x & 31);
-    for (int64_t m = (int64_t)blockIdx.y * 8 + (threadIdx.x >> 5); m < M; m += (int64_t)gridDim.y * 8) {
-        if (n >= N) break;
-        float acc = 0.0f;
-        for (int64_t b = 0; b < K / 32; ++b) {
-            const uint4 a4 = *reinterpret_cast<const uint4 *>(ac + m * (K / 2) + b * 16);
-            const uint4 w4 = *reinterpret_cast<const uint4 *>(wc + n * (K / 2) + b * 16);
-            const uint32_t aw[4] = {a4.x, a4.y, a4.z, a4.w}, ww[4] = {w4.x, w4.y, w4.z, w4.w};
-            float sum = 0.0f;                                  // exact: multiples of 1/4 below 32 * 36
+__device__ __forceinline__ void store_tokens(T *y, int64_t ldy, int64_t m0, int64_t M, int64_t row, const uint32_t *v, int n) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                float av[8], wv[8];
-                mx4_values8(aw[c], av);
-                mx4_values8(ww[c], wv);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) sum += av[j] * wv[j];
-            }
-            const int ea = as[mx4_scale_word(m, b >> 2, n128) + (b & 3)], ew = ws[mx4_scale_word(n, b >> 2, n128) + (b & 3)];
-            acc += ea == 255 || ew == 255 ? NAN : ldexpf(sum, ea + ew - 254);   // one exponent: neither factor overflows alone
+    for (int c = 0; c < n; ++c)
+        if (m0 + c < M) float_to_elem(__uint_as_float(v[c]), y[(m0 + c) * ldy + row]);
+}
+
+template <int TN>
+__global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, const __grid_constant__ CUtensorMap w_map,
+                                                            const __grid_constant__ CUtensorMap a_map) {
+    using L = Plan<TN>;
+    constexpr int S = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars), *empty = full + S, *done = empty + S, *parts_in = done + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(parts_in + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = p.split > 1 ? (int)(blockIdx.x % (unsigned)p.split) : 0;
+    const int64_t tile = blockIdx.x / (unsigned)p.split;
+    const int64_t n0 = tile * kRows, m0 = (int64_t)blockIdx.y * TN;
+    const int k0 = (int)((int64_t)p.nk * rank / p.split), k1 = (int)((int64_t)p.nk * (rank + 1) / p.split);
+    const int tok_blocks = min(L::kTokBlocks, p.m_blocks - (int)(m0 / 128));
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
         }
-        float_to_elem(acc, y[m * ldy + n]);
+        mbar_init(smem_u32(done), 1);
+        mbar_init(smem_u32(parts_in), (uint32_t)(kEpilogue * p.split));
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(L::kCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    __syncwarp();
+    tc_fence_before();
+    if (p.split > 1) {
+        // the peers' barriers are in place before anything arrives on them
+        asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    } else {
+        __syncthreads();
+    }
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto blocks = [&](int k) { return min(2, p.n128 - 2 * k); };
+            auto weights = [&](int k, int s) {                 // announces the whole stage
+                const uint32_t st = smem_u32(smem + s * L::kStageBytes), bar = smem_u32(&full[s]);
+                const uint32_t sb = (uint32_t)blocks(k) * kMx4ScaleBlock;
+                mbar_arrive_expect_tx(bar, (uint32_t)(kRows * 128 + TN * 128) + sb * (uint32_t)(1 + tok_blocks));
+                tma_load_2d(st + L::kW, &w_map, k * 128, (int)n0, bar);
+                bulk_g2s(st + L::kWS, p.ws + (tile * p.n128 + 2 * k) * (int64_t)kMx4ScaleBlock, sb, bar);
+            };
+            auto tokens = [&](int k, int s) {
+                const uint32_t st = smem_u32(smem + s * L::kStageBytes), bar = smem_u32(&full[s]);
+                const uint32_t sb = (uint32_t)blocks(k) * kMx4ScaleBlock;
+                tma_load_2d(st + L::kA, &a_map, k * 128, (int)m0, bar);
+                for (int b = 0; b < tok_blocks; ++b)
+                    bulk_g2s(st + L::kAS + b * 2 * kMx4ScaleBlock,
+                             p.as + ((m0 / 128 + b) * p.n128 + 2 * k) * (int64_t)kMx4ScaleBlock, sb, bar);
+            };
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&w_map)) : "memory");
+            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a_map)) : "memory");
+            const int head = min(S, k1 - k0);
+            if (!p.early_weights) asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (int i = 0; i < head; ++i) weights(k0 + i, i);
+            if (p.early_weights) asm volatile("griddepcontrol.wait;" ::: "memory");
+            for (int i = 0; i < head; ++i) tokens(k0 + i, i);
+            int issued = head;
+            for (int i = head; i < k1 - k0; ++i) {
+                const int s = i % S;
+                if (!wait_bounded(smem_u32(&empty[s]), (uint32_t)((i / S - 1) & 1), abort)) break;
+                weights(k0 + i, s);
+                tokens(k0 + i, s);
+                issued = i + 1;
+            }
+            for (int i = issued > S ? issued - S : 0; i < issued; ++i) wait_drain(smem_u32(&full[i % S]), (uint32_t)((i / S) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0) {
+            for (int i = 0; i < k1 - k0; ++i) {
+                const int s = i % S, k = k0 + i;
+                if (!wait_bounded(smem_u32(&full[s]), (uint32_t)((i / S) & 1), abort)) break;
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + s * L::kStageBytes);
+                const uint32_t cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
+                const int steps = k == p.nk - 1 ? p.last_steps : 4;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * h >= steps) break;
+                    const uint32_t c = cols + (uint32_t)(h * L::kHalfCols);
+                    copy_scales(c, smem_desc_scales(st + L::kWS + h * kMx4ScaleBlock));
+#pragma unroll
+                    for (int b = 0; b < L::kTokBlocks; ++b)
+                        copy_scales(c + 4 + 4 * b, smem_desc_scales(st + L::kAS + (2 * b + h) * kMx4ScaleBlock));
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q >= steps) break;
+                    const uint32_t c = cols + (uint32_t)((q >> 1) * L::kHalfCols);
+                    mma_mxf4(tmem, smem_desc_sw128(st + L::kW + 32 * q), smem_desc_sw128(st + L::kA + 32 * q), idesc_mxf4(TN, q & 1), c,
+                             c + 4, i > 0 || q > 0 ? 1u : 0u);
+                }
+                mma_commit(smem_u32(&empty[s]));
+            }
+            mma_commit(smem_u32(done));
+            wait_drain(smem_u32(done), 0u);
+        }
+        __syncwarp();
+    } else {
+        const int qd = warp & 3, row = 32 * qd + lane;
+        const int64_t n = n0 + row;
+        bool ok = wait_warp(smem_u32(done), 0u, abort) && !*abort;
+        tc_fence_after();
+        asm volatile("griddepcontrol.wait;" ::: "memory");     // y may still be read by an earlier kernel
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
+        constexpr int kChunk = 16;
+        if (p.split == 1) {
+#pragma unroll 1
+            for (int c0 = 0; c0 < TN && ok; c0 += kChunk) {
+                if (m0 + c0 >= p.M) break;
+                uint32_t v[16];
+                tmem_ld16(t_lane + c0, v);
+                tmem_wait_ld(v);
+                if (n < p.N) {
+                    if (p.dtype == QMM_F32) store_tokens(static_cast<float *>(p.y), p.ldy, m0 + c0, p.M, n, v, kChunk);
+                    else if (p.dtype == QMM_F16) store_tokens(static_cast<__half *>(p.y), p.ldy, m0 + c0, p.M, n, v, kChunk);
+                    else store_tokens(static_cast<__nv_bfloat16 *>(p.y), p.ldy, m0 + c0, p.M, n, v, kChunk);
+                }
+            }
+        } else if constexpr (L::kParts > 0) {
+            // token c goes to the CTA of rank c / share, into its slot [this rank][c % share][row]
+            const int share = TN / p.split;
+            float *parts = reinterpret_cast<float *>(smem + L::kPartsAt);
+#pragma unroll 1
+            for (int c0 = 0; c0 < TN && ok; c0 += kChunk) {
+                uint32_t v[16];
+                tmem_ld16(t_lane + c0, v);
+                tmem_wait_ld(v);
+#pragma unroll
+                for (int c = 0; c < kChunk; ++c) {
+                    if (m0 + c0 + c >= p.M) break;
+                    const int to = (c0 + c) / share, at = (rank * share + (c0 + c) % share) * kRows + row;
+                    asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_addr(smem_u32(parts + at), (uint32_t)to)), "r"(v[c])
+                                 : "memory");
+                }
+            }
+            for (int to = 0; to < p.split; ++to) mbar_arrive_peer(peer_addr(smem_u32(parts_in), (uint32_t)to));
+            // nobody leaves before its peers have written here
+            const bool in = wait_cluster_bounded(smem_u32(parts_in), 0u, abort, &g_mx4_status, kWaitLimitNs);
+            if (!in) wait_drain(smem_u32(parts_in), 0u);
+            ok = ok && in;
+            for (int c = 0; c < share && ok; ++c) {
+                const int64_t m = m0 + rank * share + c;
+                if (m >= p.M || n >= p.N) break;
+                float sum = 0.0f;
+                for (int r = 0; r < p.split; ++r) sum += parts[(r * share + c) * kRows + row];
+                if (p.dtype == QMM_F32) static_cast<float *>(p.y)[m * p.ldy + n] = sum;
+                else if (p.dtype == QMM_F16) float_to_elem(sum, static_cast<__half *>(p.y)[m * p.ldy + n]);
+                else float_to_elem(sum, static_cast<__nv_bfloat16 *>(p.y)[m * p.ldy + n]);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
+    }
+}
+
+template <int TN>
+cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *ac, cudaStream_t s) {
+    using L = Plan<TN>;
+    auto kern = mx4_gemm_kernel<TN>;
+    static int attr_done[4] = {0, 0, 0, 0};
+    cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    const int64_t tiles = (p.N + kRows - 1) / kRows, toks = (p.M + TN - 1) / TN;
+    if (toks > 65535) return cudaErrorInvalidValue;
+    // K is shared until there are about three CTAs an SM, each with two stages at least
+    p.split = 1;
+    if (L::kParts > 0)
+        while (p.split < kMaxSplit && 2 * p.split <= TN && tiles * p.split < 304 && p.nk >= 4 * p.split) p.split *= 2;
+    alignas(64) CUtensorMap wm, am;
+    e = make_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, wc, (uint64_t)(K / 2), (uint64_t)p.N, (uint64_t)(K / 2), 128, kRows,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    e = make_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, ac, (uint64_t)(K / 2), (uint64_t)p.M, (uint64_t)(K / 2), 128, TN,
+                    CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(tiles * p.split), (unsigned)toks, 1);
+    cfg.blockDim = dim3(kThreads, 1, 1);
+    cfg.dynamicSmemBytes = L::kSmem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)p.split;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = p.split > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kern, p, wm, am);
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
-                              int64_t M, qmm_dtype t, void *y, int64_t ldy, cudaStream_t s) {
-    return with_dtype(t, [&](auto z) {
-        using T = decltype(z);
-        const int64_t gm = (M + 7) / 8;
-        const dim3 grid((unsigned)((N + 31) / 32), (unsigned)(gm > 65535 ? 65535 : gm));
-        mx4_matmul_kernel<T><<<grid, 256, 0, s>>>(wc, ws, K, N, ac, as, M, static_cast<T *>(y), ldy);
-        return cudaGetLastError();
-    });
+                              int64_t M, qmm_dtype t, void *y, int64_t ldy, int early_weights, cudaStream_t s) {
+    Mx4Params p = {};
+    p.ws = ws;
+    p.as = as;
+    p.y = y;
+    p.N = N;
+    p.M = M;
+    p.ldy = ldy;
+    p.n128 = (int)((K + 127) / 128);
+    p.nk = (int)((K + 255) / 256);
+    p.last_steps = (int)((K - (int64_t)(p.nk - 1) * 256 + 63) / 64);
+    p.m_blocks = (int)((M + 127) / 128);
+    p.early_weights = early_weights;
+    p.dtype = (int)t;
+    if (M <= 16) return launch_tn<16>(p, wc, K, ac, s);
+    if (M <= 32) return launch_tn<32>(p, wc, K, ac, s);
+    if (M <= 64) return launch_tn<64>(p, wc, K, ac, s);
+    if (M <= 128) return launch_tn<128>(p, wc, K, ac, s);
+    return launch_tn<256>(p, wc, K, ac, s);
+}
+
+cudaError_t read_and_clear_mx4_status(unsigned *out, cudaStream_t s) {
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_mx4_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbolAsync(g_mx4_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(s);
 }
 
 QMM_DCHECK_READER(read_dcheck_mx4_gemm)

@@ -306,7 +306,7 @@ qmm_status qmm_mx4_matmul(const void *w_codes, const void *w_scales, int64_t K, 
     if (!aligned(a_codes, 16) || !aligned(a_scales, 16)) return QMM_ERR_MISALIGNED;
     return from_cuda(launch_mx4_matmul(static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales), K, N,
                                        static_cast<const uint8_t *>(a_codes), static_cast<const uint8_t *>(a_scales), M, dt, y, ldy,
-                                       cs(stream)));
+                                       0, cs(stream)));
 }
 
 size_t qmm_mx4_linear_workspace_size(int64_t M, int64_t K) {
@@ -325,8 +325,9 @@ qmm_status qmm_mx4_linear(const void *w_codes, const void *w_scales, int64_t K, 
     if (st != QMM_OK) return st;
     const cudaError_t e = launch_mx4_quantize(xdt, x, M, K, ldx, codes, scales, cs(stream));
     if (e != cudaSuccess) return from_cuda(e);
+    // the grid before the product is the quantization, which waited for everything before it and writes no weight
     return from_cuda(launch_mx4_matmul(static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales), K, N, codes,
-                                       scales, M, ydt, y, ldy, cs(stream)));
+                                       scales, M, ydt, y, ldy, 1, cs(stream)));
 }
 
 // ---- block-quantized key/value cache ----
@@ -424,10 +425,11 @@ qmm_status qmm_selftest_timeout(int unit, uint64_t limit_ns, int *flags_dev, qmm
 }
 
 qmm_status qmm_device_status(qmm_stream_t stream) {
-    unsigned v = 0, w = 0, f = 0;
+    unsigned v = 0, w = 0, f = 0, m = 0;
     cudaError_t e = read_and_clear_device_status(&v, cs(stream));
     if (e == cudaSuccess) e = read_and_clear_matvec_status(&w, cs(stream));
     if (e == cudaSuccess) e = read_and_clear_fold_status(&f, cs(stream));
+    if (e == cudaSuccess) e = read_and_clear_mx4_status(&m, cs(stream));
     // the bounds-check words (always 0 unless the library was built with QMM_DEBUG)
     unsigned d[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};
     if (e == cudaSuccess) e = read_dcheck_matvec(&d[0], cs(stream));
@@ -442,7 +444,7 @@ qmm_status qmm_device_status(qmm_stream_t stream) {
     if (e != cudaSuccess) return QMM_ERR_CUDA;
     for (unsigned line : d)
         if (line) return QMM_ERR_BOUNDS;
-    if (v | w | (f & 1u)) return QMM_ERR_TIMEOUT;
+    if (v | w | (f & 1u) | m) return QMM_ERR_TIMEOUT;
     return (f & 2u) ? QMM_ERR_RANGE : QMM_OK;
 }
 

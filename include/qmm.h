@@ -388,8 +388,7 @@ QMM_API qmm_status qmm_mx4_dequantize(const void *codes_dev, const void *scales_
  * Sums are fp32 in a fixed order (results are reproducible run to run) and are rounded to dt once; the
  * error before that rounding stays below 1e-5 * sum_k |w_k * x_k|.  K may be at most 131072.
  * A NaN scale makes every result of its row NaN; results beyond dt's range are infinities.
- * Launch overlap: as for qmm_matmul (the weight may be streamed before the kernel before this call has
- * completed; a_codes, a_scales and y are touched only after it has).
+ * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
  * Errors: INVALID_ARG (sizes, ldy < N, NULL), UNSUPPORTED (dt), MISALIGNED, CUDA.
  */
 QMM_API qmm_status qmm_mx4_matmul(const void *w_codes_dev, const void *w_scales_dev, int64_t K, int64_t N,
@@ -401,7 +400,8 @@ QMM_API size_t qmm_mx4_linear_workspace_size(int64_t M, int64_t K);
 
 /*
  * qmm_mx4_linear -- floating-point activation rows times an MX4 weight: qmm_mx4_quantize into the workspace,
- * then qmm_mx4_matmul, bit for bit.
+ * then qmm_mx4_matmul, bit for bit.  The product starts streaming the weight while the activations are
+ * quantized; both wait for whatever came before the call.
  *   x_dev  M rows of K elements of type xdt, row m at x_dev + m*ldx; y_dev of type ydt as above.
  *   workspace_dev  >= qmm_mx4_linear_workspace_size(M, K) bytes, 256-byte aligned, overwritten; calls that
  *                  overlap on the GPU must use different workspaces.
