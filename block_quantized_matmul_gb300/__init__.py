@@ -150,11 +150,20 @@ def _ptr_located(x) -> int | None:
     return x.data_ptr()
 
 
+def _current_stream() -> int:
+    """The current stream of the current device as a raw address.  torch's raw query takes a tenth of a
+    microsecond where torch.cuda.current_stream() takes three, half of a small call's host time."""
+    import torch
+
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is None or not torch.cuda.is_initialized():
+        return torch.cuda.current_stream().cuda_stream
+    return raw(torch.cuda.current_device())
+
+
 def _stream(stream) -> int | None:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

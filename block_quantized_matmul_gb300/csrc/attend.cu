@@ -583,15 +583,19 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
     if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB>(p, w, sp, row_bad);
 }
 
-// Joins the partial results of the sequences that were split: one warp a row.
-template <int DB>
-__global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) {
+// Joins the partial results of the sequences that were split.  WPR warps take a row, each the splits of
+// its number modulo WPR: one warp for a few splits, a CTA's eight where there are many.
+constexpr int kJoinWarps = 8;
+template <int DB, int WPR>
+__global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendParams p) {
     constexpr int D = DB * 32;
+    __shared__ float s_o[WPR > 1 ? WPR : 1][WPR > 1 ? D : 1];
+    __shared__ float s_l[WPR > 1 ? WPR : 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int lane = threadIdx.x & 31, Hq = p.H * p.group;
-    const int64_t at = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (at >= p.T * Hq) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR, Hq = p.H * p.group;
+    const int64_t stride = p.T * Hq, at = (int64_t)blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
+    if (at >= stride) return;                                    // with WPR = 8 for the whole CTA
     const int64_t tok = at / Hq;
     const int hq = (int)(at - tok * Hq);
     int64_t lo = 0, hi = p.n_seq - 1;
@@ -604,7 +608,6 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) 
     const int64_t n = max((int64_t)0, min((int64_t)p.kv_lens[lo], p.ld_pages << p.log_p));
     const int used = (int)min((int64_t)p.splits, (n + p.chunk - 1) / p.chunk);
     if (used <= 1) return;
-    const int64_t stride = p.T * Hq;
     float m = -INFINITY;
     for (int s = lane; s < used; s += 32) m = fmaxf(m, p.part_ml[2 * (s * stride + at)]);
 #pragma unroll
@@ -613,17 +616,37 @@ __global__ void __launch_bounds__(128) attend_join_kernel(const AttendParams p) 
     float l = 0.0f, o[DB];
 #pragma unroll
     for (int b = 0; b < DB; ++b) o[b] = 0.0f;
-    for (int s = 0; s < used; ++s) {
+#pragma unroll 4
+    for (int s = part; s < used; s += WPR) {
         const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * stride + at));
-        if (ml.y == 0.0f) continue;                              // nothing seen there
-        const float f = exp2f(ml.x - base);
-        l += f * ml.y;
+        const bool some = ml.y != 0.0f;                          // else nothing was seen there
+        const float f = some ? exp2f(ml.x - base) : 0.0f;
+        if (some) l += f * ml.y;
 #pragma unroll
-        for (int b = 0; b < DB; ++b) o[b] += f * p.part_o[(s * stride + at) * D + 32 * b + lane];
+        for (int b = 0; b < DB; ++b) {
+            const float v = p.part_o[(s * stride + at) * D + 32 * b + lane];
+            if (some) o[b] += f * v;
+        }
     }
+    if constexpr (WPR > 1) {
 #pragma unroll
-    for (int b = 0; b < DB; ++b) store_out(p, tok * p.ldo + (int64_t)hq * D + 32 * b + lane, l == 0.0f ? 0.0f : o[b] / l);
-    if (lane == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l) - kBias) * 0.6931471805599453f;
+        for (int b = 0; b < DB; ++b) s_o[part][32 * b + lane] = o[b];
+        if (lane == 0) s_l[part] = l;
+        __syncthreads();
+        l = 0.0f;
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) l += s_l[w];
+        for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
+            float v = 0.0f;
+#pragma unroll
+            for (int w = 0; w < WPR; ++w) v += s_o[w][d];
+            store_out(p, tok * p.ldo + (int64_t)hq * D + d, l == 0.0f ? 0.0f : v / l);
+        }
+    } else {
+#pragma unroll
+        for (int b = 0; b < DB; ++b) store_out(p, tok * p.ldo + (int64_t)hq * D + 32 * b + lane, l == 0.0f ? 0.0f : o[b] / l);
+    }
+    if (lane == 0 && part == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l) - kBias) * 0.6931471805599453f;
 }
 
 constexpr int64_t kMinChunk = 8 * kKeys;           // one tile a warp
@@ -652,7 +675,8 @@ cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
     e = launch_pdl(kern, dim3((unsigned)ctas), L::kThreads, L::kSmem, s, p);
     if (e != cudaSuccess || p.splits == 1) return e;
     const int64_t rows = p.T * p.H * p.group;
-    return launch_pdl(attend_join_kernel<DB>, dim3((unsigned)((rows + 3) / 4)), 128, 0, s, p);
+    if (p.splits > kJoinWarps) return launch_pdl(attend_join_kernel<DB, kJoinWarps>, dim3((unsigned)rows), kJoinWarps * 32, 0, s, p);
+    return launch_pdl(attend_join_kernel<DB, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, p);
 }
 
 template <int TYPE>

@@ -68,6 +68,17 @@ __device__ __forceinline__ void store8(T *p, const float (&v)[8]) {
 
 inline size_t dtype_bytes(qmm_dtype t) { return t == QMM_F32 ? 4 : 2; }
 
+// n / d for n < 2^31 by a multiplication and a shift (the round-up method: with s = ceil(log2 d) and
+// m = floor(2^32 (2^s - d) / d) + 1, n / d = (high word of m n + n) >> s).
+struct FastDiv {
+    uint32_t d, mul, shift;
+    explicit FastDiv(uint32_t div) : d(div), mul(0), shift(0) {
+        while (((uint64_t)1 << shift) < d) ++shift;
+        mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << shift) - d)) / d + 1);
+    }
+    __device__ __forceinline__ uint32_t operator()(uint32_t n) const { return (__umulhi(mul, n) + n) >> shift; }
+};
+
 // Calls f with a value of the element type (its value does not matter).
 template <typename F>
 inline cudaError_t with_dtype(qmm_dtype t, F f) {

@@ -1,9 +1,10 @@
 // mx4.cu -- rows of floating-point values to microscaled 4-bit operands (mx4.cuh) and back.
 //
-// Both directions move each element once and do a few operations on it, so they are bound by memory.
-// A warp takes 256 consecutive elements of a row, 8 to a lane: 16- or 32-byte loads, 4-byte code
-// words; the four lanes of a block find its largest magnitude with two shuffles, and the scale bytes
-// of four blocks leave as one word.
+// Both directions move each element once and do a few operations on it.  A warp takes segments of 256
+// consecutive elements of a row, 8 to a lane: 16- or 32-byte loads and 4-byte code words; the four
+// lanes of a block find its largest magnitude with two shuffles, and the scale bytes of four blocks
+// leave as one word.  A warp loads kBatch segments before it works on the first, so that enough
+// bytes are on their way to hide memory's latency.
 #include "qmm_internal.cuh"
 
 #include "elem.cuh"
@@ -13,69 +14,114 @@ namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;
 
+// `trigger`: the next kernel on the stream may start early (it waits for this one before it reads the
+// operand; see launch_mx4_quantize).
 template <bool VEC, typename T>
-__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T *__restrict__ x, int64_t R, int64_t K, int64_t ldx,
-                                                                uint8_t *__restrict__ codes, uint8_t *__restrict__ scales) {
+__global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T *__restrict__ x, uint32_t items, const FastDiv nseg, int64_t K,
+                                                                int64_t ldx, uint8_t *__restrict__ codes,
+                                                                uint8_t *__restrict__ scales, int64_t r0, int trigger) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t nseg = (K + 255) / 256, n128 = (K + 127) / 128;
+    if (trigger) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t n128 = (K + 127) / 128;
     const int lane = threadIdx.x & 31;
-    for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < R * nseg;
-         i += (int64_t)gridDim.x * (kThreads / 32)) {
-        const int64_t r = i / nseg, seg = i - r * nseg, k = seg * 256 + lane * 8;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (k < K && QMM_DCHECK(r < R && k + 8 <= K)) load8<VEC>(x + r * ldx + k, v);
-        uint32_t top = 0;
+    const uint32_t warps = gridDim.x * kWarps;
+    for (uint32_t base = blockIdx.x * kWarps + (threadIdx.x >> 5); base < items; base += warps * kBatch) {
+        float v[kBatch][8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const uint32_t e = mx4_block_scale(top);
-        if (k < K) *reinterpret_cast<uint32_t *>(codes + (r * K + k) / 2) = mx4_codes8(v, e);
-        // the scales of four blocks (16 lanes) as one word; blocks past K hold 0
-        uint32_t word = e << (8 * ((lane >> 2) & 3));
-        word |= __shfl_xor_sync(0xffffffffu, word, 4);
-        word |= __shfl_xor_sync(0xffffffffu, word, 8);
-        const int64_t k128 = seg * 2 + (lane >> 4);
-        if ((lane & 15) == 0 && k128 < n128) *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(r, k128, n128)) = word;
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t i = base + u * warps, row = nseg(i);
+            const int64_t k = (int64_t)(i - row * nseg.d) * 256 + lane * 8;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
+            if (i < items && k < K && QMM_DCHECK(k + 8 <= K)) load8<VEC>(x + (r0 + row) * ldx + k, v[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t i = base + u * warps, row = nseg(i);
+            if (i >= items) break;
+            const int64_t r = r0 + row, seg = i - row * nseg.d, k = seg * 256 + lane * 8;
+            uint32_t top = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[u][j]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const uint32_t e = mx4_block_scale(top);
+            if (k < K) *reinterpret_cast<uint32_t *>(codes + (r * K + k) / 2) = mx4_codes8(v[u], e);
+            // the scales of four blocks (16 lanes) as one word; blocks past K hold 0
+            uint32_t word = e << (8 * ((lane >> 2) & 3));
+            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+            word |= __shfl_xor_sync(0xffffffffu, word, 8);
+            const int64_t k128 = seg * 2 + (lane >> 4);
+            if ((lane & 15) == 0 && k128 < n128) *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(r, k128, n128)) = word;
+        }
     }
 }
 
 template <bool VEC, typename T>
 __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t *__restrict__ codes,
-                                                                  const uint8_t *__restrict__ scales, int64_t R, int64_t K,
-                                                                  T *__restrict__ y, int64_t ldy) {
-    const int64_t nseg = (K + 255) / 256, n128 = (K + 127) / 128;
+                                                                  const uint8_t *__restrict__ scales, uint32_t items,
+                                                                  const FastDiv nseg, int64_t K, T *__restrict__ y, int64_t ldy,
+                                                                  int64_t r0) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t n128 = (K + 127) / 128;
     const int lane = threadIdx.x & 31;
-    for (int64_t i = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); i < R * nseg;
-         i += (int64_t)gridDim.x * (kThreads / 32)) {
-        const int64_t r = i / nseg, seg = i - r * nseg, k = seg * 256 + lane * 8;
-        if (k >= K || !QMM_DCHECK(r < R && k + 8 <= K)) continue;
-        const uint32_t w = *reinterpret_cast<const uint32_t *>(codes + (r * K + k) / 2);
-        const float s = mx4_scale(scales[mx4_scale_word(r, k >> 7, n128) + ((k >> 5) & 3)]);
-        float v[8];
-        mx4_values8(w, v);
+    const uint32_t warps = gridDim.x * kWarps;
+    for (uint32_t base = blockIdx.x * kWarps + (threadIdx.x >> 5); base < items; base += warps * kBatch) {
+        uint32_t w[kBatch], e[kBatch];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] *= s;
-        store8<VEC>(y + r * ldy + k, v);
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t i = base + u * warps, row = nseg(i);
+            const int64_t r = r0 + row, k = (int64_t)(i - row * nseg.d) * 256 + lane * 8;
+            w[u] = e[u] = 0;
+            if (i < items && k < K && QMM_DCHECK(k + 8 <= K)) {
+                w[u] = *reinterpret_cast<const uint32_t *>(codes + (r * K + k) / 2);
+                e[u] = scales[mx4_scale_word(r, k >> 7, n128) + ((k >> 5) & 3)];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) {
+            const uint32_t i = base + u * warps, row = nseg(i);
+            const int64_t k = (int64_t)(i - row * nseg.d) * 256 + lane * 8;
+            if (i >= items || k >= K) continue;
+            const float s = mx4_scale(e[u]);
+            float v[8];
+            mx4_values8(w[u], v);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= s;
+            store8<VEC>(y + (r0 + row) * ldy + k, v);
+        }
     }
 }
 
-unsigned grid_rows(int64_t R, int64_t K) {
-    const int64_t warps = R * ((K + 255) / 256), g = (warps + kThreads / 32 - 1) / (kThreads / 32);
-    return (unsigned)(g > 152 * 8 ? 152 * 8 : g);
+// Calls f(first row, rows, segments, grid) for pieces of fewer than 2^31 segments (one piece, but for
+// operands beyond 2^39 elements).
+template <typename F>
+cudaError_t for_rows(int64_t R, int64_t K, F f) {
+    const int64_t nseg = (K + 255) / 256, most = 0x3fffffff / nseg;
+    for (int64_t r = 0; r < R; r += most) {
+        const int64_t rows = R - r < most ? R - r : most, items = rows * nseg;
+        const int64_t g = (items + kWarps - 1) / kWarps;
+        const cudaError_t e = f(r, (uint32_t)items, FastDiv((uint32_t)nseg), dim3((unsigned)(g > 152 * 6 ? 152 * 6 : g)));
+        if (e != cudaSuccess) return e;
+    }
+    return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_mx4_quantize(qmm_dtype t, const void *x, int64_t R, int64_t K, int64_t ldx, uint8_t *codes, uint8_t *scales,
-                                cudaStream_t s) {
+                                int trigger, cudaStream_t s) {
     return with_dtype(t, [&](auto z) {
         using T = decltype(z);
         const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx * sizeof(T)) % 16 == 0;
         auto kern = vec ? mx4_quantize_kernel<true, T> : mx4_quantize_kernel<false, T>;
-        return launch_pdl(kern, dim3(grid_rows(R, K)), kThreads, 0, s, static_cast<const T *>(x), R, K, ldx, codes, scales);
+        return for_rows(R, K, [&](int64_t r, uint32_t items, FastDiv nseg, dim3 grid) {
+            return launch_pdl(kern, grid, kThreads, 0, s, static_cast<const T *>(x), items, nseg, K, ldx, codes, scales, r, trigger);
+        });
     });
 }
 
@@ -85,8 +131,9 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
         using T = decltype(z);
         const bool vec = (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && (ldy * sizeof(T)) % 16 == 0;
         auto kern = vec ? mx4_dequantize_kernel<true, T> : mx4_dequantize_kernel<false, T>;
-        kern<<<grid_rows(R, K), kThreads, 0, s>>>(codes, scales, R, K, static_cast<T *>(y), ldy);
-        return cudaGetLastError();
+        return for_rows(R, K, [&](int64_t r, uint32_t items, FastDiv nseg, dim3 grid) {
+            return launch_pdl(kern, grid, kThreads, 0, s, codes, scales, items, nseg, K, static_cast<T *>(y), ldy, r);
+        });
     });
 }
 

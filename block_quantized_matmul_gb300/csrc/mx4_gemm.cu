@@ -94,7 +94,7 @@ struct Plan {
     static constexpr int kWS = kA + (TN * 128 + 1023) / 1024 * 1024;
     static constexpr int kAS = kWS + 2 * kMx4ScaleBlock;
     static constexpr int kStageBytes = kAS + kTokBlocks * 2 * kMx4ScaleBlock;
-    static constexpr int kStages = TN >= 256 ? 4 : (TN >= 128 ? 6 : 5);
+    static constexpr int kStages = TN >= 64 ? 3 : 5;                     // two CTAs an SM up to 64 tokens
     // tensor memory: the sums, then per stage the scales of two K = 128 halves (weight 4 columns, tokens 4
     // columns per block)
     static constexpr int kSums = TN < 32 ? 32 : TN;
@@ -102,7 +102,7 @@ struct Plan {
     static constexpr int kColsUsed = kSums + kStages * 2 * kHalfCols;
     static constexpr int kCols = kColsUsed <= 128 ? 128 : (kColsUsed <= 256 ? 256 : 512);
     // parts of the other CTAs of a cluster: [rank][token of this CTA's share][row]
-    static constexpr int kParts = TN <= 32 ? TN * kRows * 4 : 0;
+    static constexpr int kParts = TN * kRows * 4;
     static constexpr int kPartsAt = kStages * kStageBytes;
     static constexpr int kBars = kPartsAt + kParts;
     static constexpr size_t kSmem = 1024 + kBars + (2 * kStages + 2) * 8 + 16;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, c
                     else store_tokens(static_cast<__nv_bfloat16 *>(p.y), p.ldy, m0 + c0, p.M, n, v, kChunk);
                 }
             }
-        } else if constexpr (L::kParts > 0) {
+        } else {
             // token c goes to the CTA of rank c / share, into its slot [this rank][c % share][row]
             const int share = TN / p.split;
             float *parts = reinterpret_cast<float *>(smem + L::kPartsAt);
@@ -301,8 +301,7 @@ cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *
     if (toks > 65535) return cudaErrorInvalidValue;
     // K is shared until there are about three CTAs an SM, each with two stages at least
     p.split = 1;
-    if (L::kParts > 0)
-        while (p.split < kMaxSplit && 2 * p.split <= TN && tiles * p.split < 304 && p.nk >= 4 * p.split) p.split *= 2;
+    while (p.split < kMaxSplit && 2 * p.split <= TN && tiles * toks * p.split < 304 && p.nk >= 4 * p.split) p.split *= 2;
     alignas(64) CUtensorMap wm, am;
     e = make_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, wc, (uint64_t)(K / 2), (uint64_t)p.N, (uint64_t)(K / 2), 128, kRows,
                     CU_TENSOR_MAP_SWIZZLE_128B);
@@ -327,6 +326,281 @@ cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *
     return cudaLaunchKernelEx(&cfg, kern, p, wm, am);
 }
 
+// ---------------------------------------------------------------------------------------------
+// Many tokens: pairs of CTAs (cta_group::2) share a tile of 256 weight rows x 256 tokens.  Each CTA holds
+// 128 of the weight rows and 128 of the tokens, and the pair's instruction reads both halves of the
+// tokens, so that a byte brought into shared memory takes part in twice the products of a single CTA's
+// tile.  The pairs stay on their SMs and take tiles in turn (tokens fastest, so that the pairs of a moment
+// share weight rows).  The eight result warps of a CTA read a finished tile into registers, 128 sums a
+// thread, which frees the accumulator for the next tile before the first result is stored.
+// ---------------------------------------------------------------------------------------------
+constexpr int kPairTok = 256;              // tokens of a pair's tile
+struct Pair {
+    static constexpr int kStages = 5;
+    static constexpr int kW = 0;
+    static constexpr int kA = kRows * 128;
+    static constexpr int kWS = kA + kPairTok / 2 * 128;
+    static constexpr int kAS = kWS + 2 * kMx4ScaleBlock;
+    static constexpr int kStageBytes = kAS + 4 * kMx4ScaleBlock;         // both CTAs hold the scales of all tokens
+    static constexpr int kSums = kPairTok;
+    static constexpr int kHalfCols = 12;                                 // weight 4, tokens 8
+    static constexpr int kBars = kStages * kStageBytes;
+    static constexpr size_t kSmem = 1024 + kBars + (2 * kStages + 2) * 8 + 16;
+    static constexpr int kThreads = 64 + 256;
+    static_assert(kSums + kStages * 2 * kHalfCols <= 512 && kSmem <= 227 * 1024, "does not fit");
+};
+
+__device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+        : "memory");
+}
+__device__ __forceinline__ void copy_scales_pair(uint32_t taddr, uint64_t desc) {
+    asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t sa, uint32_t sb,
+                                              uint32_t accumulate) {
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %6, 0;\n"
+        " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
+        : "memory");
+}
+// An arrival on the barrier at this offset in both CTAs, once the products issued so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+        "h"((uint16_t)3)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+        "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+// Completes the loads of r and keeps their uses behind it.
+__device__ __forceinline__ void tmem_wait32(uint32_t *r) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]),
+                   "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]),
+                   "+r"(r[25]), "+r"(r[26]), "+r"(r[27])
+                 :
+                 : "memory");
+    asm volatile("" : "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+struct PairParams {
+    void *y;
+    int64_t N, M, ldy;
+    int n128, nk, last_steps;
+    int m_tiles, tiles;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(Pair::kThreads, 1)
+mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap a_map,
+                const __grid_constant__ CUtensorMap ws_map, const __grid_constant__ CUtensorMap as_map) {
+    using L = Pair;
+    constexpr int S = L::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + L::kBars), *empty = full + S, *acc_full = empty + S, *acc_empty = acc_full + 1;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(acc_empty + 1);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)cluster_rank();
+    const int pairs = (int)gridDim.x / 2, pair = (int)blockIdx.x / 2;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&empty[s]), 1);
+        }
+        mbar_init(smem_u32(acc_full), 1);
+        mbar_init(smem_u32(acc_empty), 16);
+        *abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+
+    if (warp == 0) {
+        if (lane == 0) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            int it = 0;
+            bool ok = true;
+            for (int tile = pair; tile < p.tiles && ok; tile += pairs) {
+                const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+                const int row0 = nt * 2 * kRows + rank * kRows, tok0 = mt * kPairTok;
+                for (int k = 0; k < p.nk; ++k, ++it) {
+                    const int s = it % S;
+                    if (!wait_bounded(smem_u32(&empty[s]), (uint32_t)(((it / S) & 1) ^ 1), abort)) { ok = false; break; }
+                    const uint32_t st = smem_u32(smem + s * L::kStageBytes);
+                    const uint32_t bar = peer_addr(smem_u32(&full[s]), 0u);        // the leader's, for both CTAs' copies
+                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * L::kStageBytes);
+                    tma_load_2d_pair(st + L::kW, &w_map, k * 128, row0, bar);
+                    tma_load_2d_pair(st + L::kA, &a_map, k * 128, tok0 + rank * (kPairTok / 2), bar);
+                    tma_load_2d_pair(st + L::kWS, &ws_map, 0, (nt * 2 + rank) * p.n128 + 2 * k, bar);
+                    tma_load_2d_pair(st + L::kAS, &as_map, 0, (mt * 2) * p.n128 + 2 * k, bar);
+                    tma_load_2d_pair(st + L::kAS + 2 * kMx4ScaleBlock, &as_map, 0, (mt * 2 + 1) * p.n128 + 2 * k, bar);
+                }
+            }
+            // every stage has been read, and the arrivals that say so have reached this CTA
+            for (int i = it > S ? it - S : 0; i < it; ++i) wait_drain(smem_u32(&empty[i % S]), (uint32_t)((i / S) & 1));
+        }
+        __syncwarp();
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            int it = 0, done = 0;
+            bool ok = true;
+            constexpr uint32_t id0 = idesc_mxf4(kPairTok, 0) + ((uint32_t)(kRows >> 4) << 24);      // 256 rows
+            constexpr uint32_t id1 = idesc_mxf4(kPairTok, 1) + ((uint32_t)(kRows >> 4) << 24);
+            // The products of a stage are issued after the scale copies of the next one, which they hide.
+            auto products = [&](int i, int k) {
+                const int s = i % S, steps = k == p.nk - 1 ? p.last_steps : 4;
+                const uint32_t st = smem_u32(smem + s * L::kStageBytes), cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q >= steps) break;
+                    const uint32_t c = cols + (uint32_t)((q >> 1) * L::kHalfCols);
+                    mma_mxf4_pair(tmem, smem_desc_sw128(st + L::kW + 32 * q), smem_desc_sw128(st + L::kA + 32 * q), (q & 1) ? id1 : id0,
+                                  c, c + 4, k > 0 || q > 0 ? 1u : 0u);
+                }
+                mma_commit_pair(smem_u32(&empty[s]));
+            };
+            for (int tile = pair; tile < p.tiles && ok; tile += pairs, ++done) {
+                for (int k = 0; k < p.nk; ++k, ++it) {
+                    const int s = it % S;
+                    if (!wait_bounded(smem_u32(&full[s]), (uint32_t)((it / S) & 1), abort)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + s * L::kStageBytes), cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t c = cols + (uint32_t)(h * L::kHalfCols);
+                        copy_scales_pair(c, smem_desc_scales(st + L::kWS + h * kMx4ScaleBlock));
+                        copy_scales_pair(c + 4, smem_desc_scales(st + L::kAS + h * kMx4ScaleBlock));
+                        copy_scales_pair(c + 8, smem_desc_scales(st + L::kAS + (2 + h) * kMx4ScaleBlock));
+                    }
+                    if (k > 0) products(it - 1, k - 1);
+                    else if (!wait_cluster_bounded(smem_u32(acc_empty), (uint32_t)((done & 1) ^ 1), abort, &g_mx4_status, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    } else {
+                        tc_fence_after();
+                    }
+                }
+                if (ok) {
+                    products(it - 1, p.nk - 1);
+                    mma_commit_pair(smem_u32(acc_full));
+                }
+            }
+            if (!ok) {
+                // lets the products in flight finish and both CTAs go on to their end
+                mma_commit_pair(smem_u32(acc_full));
+                for (int s = 0; s < S; ++s) mma_commit_pair(smem_u32(&empty[s]));
+            }
+        }
+        __syncwarp();
+    } else {
+        const int qd = warp & 3, half = (warp - 2) >> 2, row = 32 * qd + lane;
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16) + (uint32_t)(half * (kPairTok / 2));
+        const uint32_t free_bar = peer_addr(smem_u32(acc_empty), 0u);
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        int done = 0;
+        for (int tile = pair; tile < p.tiles; tile += pairs, ++done) {
+            if (!wait_warp(smem_u32(acc_full), (uint32_t)(done & 1), abort)) break;
+            tc_fence_after();
+            uint32_t v[128];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32(t_lane + 32 * c, v + 32 * c);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_wait32(v + 32 * c);
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_peer(free_bar);
+            const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+            const int64_t n = (int64_t)nt * 2 * kRows + rank * kRows + row, m0 = (int64_t)mt * kPairTok + half * (kPairTok / 2);
+            const int have = (int)min((int64_t)(kPairTok / 2), p.M - m0);
+            if (n < p.N) {
+                T *y = static_cast<T *>(p.y) + m0 * p.ldy + n;
+#pragma unroll
+                for (int c = 0; c < kPairTok / 2; ++c) {
+                    if (c < have) float_to_elem(__uint_as_float(v[c]), *y);
+                    y += p.ldy;
+                }
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+}
+
+cudaError_t launch_pairs(const Mx4Params &q, const uint8_t *wc, int64_t K, const uint8_t *ac, cudaStream_t s) {
+    PairParams p = {q.y, q.N, q.M, q.ldy, q.n128, q.nk, q.last_steps, 0, 0};
+    const int64_t mt = (p.M + kPairTok - 1) / kPairTok, nt = (p.N + 2 * kRows - 1) / (2 * kRows);
+    if (mt * nt > 0x3fffffff) return cudaErrorInvalidValue;
+    p.m_tiles = (int)mt;
+    p.tiles = (int)(mt * nt);
+    alignas(64) CUtensorMap wm, am, wsm, asm_;
+    cudaError_t e = make_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, wc, (uint64_t)(K / 2), (uint64_t)p.N, (uint64_t)(K / 2), 128, kRows,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e == cudaSuccess)
+        e = make_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, ac, (uint64_t)(K / 2), (uint64_t)p.M, (uint64_t)(K / 2), 128, kPairTok / 2,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+    // the scales as rows of 512 bytes, two a copy
+    if (e == cudaSuccess)
+        e = make_map_2d(&wsm, CU_TENSOR_MAP_DATA_TYPE_UINT32, q.ws, 128, (uint64_t)((p.N + 127) / 128) * (uint64_t)p.n128, 512, 128, 2,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e == cudaSuccess)
+        e = make_map_2d(&asm_, CU_TENSOR_MAP_DATA_TYPE_UINT32, q.as, 128, (uint64_t)((p.M + 127) / 128) * (uint64_t)p.n128, 512, 128, 2,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+    if (e != cudaSuccess) return e;
+    auto go = [&](auto kern, int (&attr_done)[4]) {
+        cudaError_t err = ensure_smem_limit(kern, Pair::kSmem, attr_done);
+        if (err != cudaSuccess) return err;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3((unsigned)(2 * (p.tiles < 76 ? p.tiles : 76)), 1, 1);
+        cfg.blockDim = dim3(Pair::kThreads, 1, 1);
+        cfg.dynamicSmemBytes = Pair::kSmem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = 2;
+        attr[1].val.clusterDim.y = 1;
+        attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        return cudaLaunchKernelEx(&cfg, kern, p, wm, am, wsm, asm_);
+    };
+    static int done_f32[4] = {0, 0, 0, 0}, done_f16[4] = {0, 0, 0, 0}, done_bf16[4] = {0, 0, 0, 0};
+    if (q.dtype == QMM_F32) return go(mx4_pair_kernel<float>, done_f32);
+    if (q.dtype == QMM_F16) return go(mx4_pair_kernel<__half>, done_f16);
+    return go(mx4_pair_kernel<__nv_bfloat16>, done_bf16);
+}
+
 }  // namespace
 
 cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
@@ -348,7 +622,7 @@ cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, i
     if (M <= 32) return launch_tn<32>(p, wc, K, ac, s);
     if (M <= 64) return launch_tn<64>(p, wc, K, ac, s);
     if (M <= 128) return launch_tn<128>(p, wc, K, ac, s);
-    return launch_tn<256>(p, wc, K, ac, s);
+    return launch_pairs(p, wc, K, ac, s);
 }
 
 cudaError_t read_and_clear_mx4_status(unsigned *out, cudaStream_t s) {

@@ -277,7 +277,8 @@ qmm_status qmm_mx4_quantize(qmm_dtype dt, const void *x, int64_t R, int64_t K, i
                             qmm_stream_t stream) {
     const qmm_status st = check_mx4_rows(dt, x, R, K, ldx, codes, scales);
     if (st != QMM_OK) return st;
-    return from_cuda(launch_mx4_quantize(dt, x, R, K, ldx, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales), cs(stream)));
+    return from_cuda(launch_mx4_quantize(dt, x, R, K, ldx, static_cast<uint8_t *>(codes), static_cast<uint8_t *>(scales),
+                                         0, cs(stream)));
 }
 
 qmm_status qmm_mx4_dequantize(const void *codes, const void *scales, int64_t R, int64_t K, qmm_dtype dt, void *y, int64_t ldy,
@@ -323,7 +324,7 @@ qmm_status qmm_mx4_linear(const void *w_codes, const void *w_scales, int64_t K, 
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + round256(mx4_codes_bytes(M, K));
     st = check_mx4_rows(xdt, x, M, K, ldx, codes, scales);
     if (st != QMM_OK) return st;
-    const cudaError_t e = launch_mx4_quantize(xdt, x, M, K, ldx, codes, scales, cs(stream));
+    const cudaError_t e = launch_mx4_quantize(xdt, x, M, K, ldx, codes, scales, 1, cs(stream));
     if (e != cudaSuccess) return from_cuda(e);
     // the grid before the product is the quantization, which waited for everything before it and writes no weight
     return from_cuda(launch_mx4_matmul(static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales), K, N, codes,

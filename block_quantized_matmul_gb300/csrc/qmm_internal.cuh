@@ -212,8 +212,9 @@ cudaError_t read_dcheck_quant(unsigned *out, cudaStream_t s);
 cudaError_t read_dcheck_repack(unsigned *out, cudaStream_t s);
 
 // Microscaled 4-bit operands (mx4.cu, mx4_gemm.cu) and the block-quantized cache (cache.cu, attend.cu).
+// trigger: the kernel after it may start early; only for a product that reads no weight written here.
 cudaError_t launch_mx4_quantize(qmm_dtype t, const void *x, int64_t R, int64_t K, int64_t ldx, uint8_t *codes, uint8_t *scales,
-                                cudaStream_t s);
+                                int trigger, cudaStream_t s);
 cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, int64_t R, int64_t K, qmm_dtype t, void *y,
                                   int64_t ldy, cudaStream_t s);
 cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
