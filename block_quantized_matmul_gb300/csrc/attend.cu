@@ -33,14 +33,14 @@
 namespace qmm {
 namespace {
 
-constexpr int kRowsTile = 16;
+constexpr int kMmaRows = 16;
 constexpr int kKeys = 32;                  // keys of a tile
 constexpr float kBias = 14.0f;             // p is kept times 2^14
 
 struct AttendParams {
     const uint8_t *k_cache, *v_cache;
     int64_t n_pages;
-    int P, log_p, H, group, row_tiles, splits;
+    int P, log_p, H, group, tile_rows, row_tiles, splits;
     int64_t chunk;                         // keys of a split
     const int32_t *pages;
     int64_t ld_pages;
@@ -63,8 +63,9 @@ __device__ __forceinline__ int swz(int r, int b) {
     return b ^ ((r / (U / Z)) & (Z - 1));
 }
 
-template <int TYPE, int DB>
+template <int TYPE, int DB, int MT>
 struct Tile {
+    static constexpr int kRowsTile = kMmaRows * MT;
     static constexpr int kUnit = TYPE == QMM_Q8_0 ? 32 : 16;           // bytes of a block's codes
     static constexpr int kSpan = TYPE == QMM_Q8_0 ? 4 : 8;             // units of 128 bytes
     static constexpr int kCodes = kKeys * DB * kUnit;
@@ -92,9 +93,15 @@ __device__ __forceinline__ void cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// The first product of a sum.
+__device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+                 : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -172,10 +179,10 @@ __device__ __forceinline__ float cache_value(const uint8_t *chunk, int P, int D,
 
 // The CTA's rows and keys once more, a warp a row, skipping what the row does not see; rows whose result
 // is finite, and was, keep the one they have.
-template <int TYPE, int DB>
+template <int TYPE, int DB, int MT>
 __device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &w, int sp, const int *row_bad) {
     const int lane = threadIdx.x & 31;
-    constexpr int D = DB * 32, kWarps = Tile<TYPE, DB>::kWarps;
+    constexpr int D = DB * 32, kWarps = Tile<TYPE, DB, MT>::kWarps;
     for (int row = threadIdx.x >> 5; row < w.rows; row += kWarps) {
         const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + r % p.group;
         float q[DB], o[DB];
@@ -213,14 +220,46 @@ __device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &
     }
 }
 
-template <int TYPE, int DB>
-__global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(const AttendParams p) {
-    using L = Tile<TYPE, DB>;
+// The scales of two neighbouring keys, DB each, as DB words: half i is block i of the first key, half
+// DB + i block i of the second.
+template <int DB>
+__device__ __forceinline__ void load_scales(const uint8_t *p, uint32_t (&w)[DB]) {
+    if constexpr (DB % 4 == 0) {
+#pragma unroll
+        for (int i = 0; i < DB / 4; ++i) {
+            const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+            w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+        }
+    } else if constexpr (DB % 2 == 0) {
+#pragma unroll
+        for (int i = 0; i < DB / 2; ++i) {
+            const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
+            w[2 * i] = v.x; w[2 * i + 1] = v.y;
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < DB; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+    }
+}
+template <int DB>
+__device__ __forceinline__ float scale_of(const uint32_t (&w)[DB], int i) {
+    const __half2 h = tc::bits_h2(w[i >> 1]);
+    return i & 1 ? __high2float(h) : __low2float(h);
+}
+// The scales of block b of both keys as a half2.
+template <int DB>
+__device__ __forceinline__ uint32_t scale_pair(const uint32_t (&w)[DB], int b) {
+    return __byte_perm(w[b >> 1], w[(DB + b) >> 1], (b & 1 ? 0x32 : 0x10) | ((DB + b) & 1 ? 0x7600 : 0x5400));
+}
+
+template <int TYPE, int DB, int MT>
+__global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
+    using L = Tile<TYPE, DB, MT>;
     constexpr int D = DB * 32, S = L::kStages, UNIT = L::kUnit, SPAN = L::kSpan, CB = DB * UNIT;
-    constexpr int kWarps = L::kWarps, kThreads = L::kThreads;
-    constexpr bool kQRegs = DB <= 4;       // the query fragments stay in registers
+    constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kRowsTile = L::kRowsTile;
+    constexpr bool kQRegs = DB <= 4 && MT == 1;                                // the query fragments stay in registers
     extern __shared__ __align__(128) uint8_t smem[];
-    uint32_t *q_frag = reinterpret_cast<uint32_t *>(smem + L::kRing);       // [block][step][lane][4]
+    uint32_t *q_frag = reinterpret_cast<uint32_t *>(smem + L::kRing);       // [row tile][block][step][lane][4]
     float *w_top = reinterpret_cast<float *>(smem + L::kRing + L::kQ);       // [warp][row]
     float *w_sum = w_top + kWarps * kRowsTile;
     float *row_mul = w_sum + kWarps * kRowsTile;                              // score -> power of two
@@ -232,20 +271,20 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    int64_t at = blockIdx.x;
-    const int sp = (int)(at % p.splits);
-    at /= p.splits;
-    const int rt = (int)(at % p.row_tiles);
-    at /= p.row_tiles;
+    uint32_t at = blockIdx.x;
+    const int sp = (int)(at % (uint32_t)p.splits);
+    at /= (uint32_t)p.splits;
+    const int rt = (int)(at % (uint32_t)p.row_tiles);
+    at /= (uint32_t)p.row_tiles;
     Rows w;
-    w.h = (int)(at % p.H);
-    w.s = at / p.H;
+    w.h = (int)(at % (uint32_t)p.H);
+    w.s = at / (uint32_t)p.H;
     w.q0 = p.q_starts[w.s];
     w.nq = p.q_starts[w.s + 1] - w.q0;
+    w.n = p.kv_lens[w.s];
     w.r0 = rt * kRowsTile;
     w.rows = (int)min((int64_t)kRowsTile, w.nq * p.group - w.r0);
     if (w.rows <= 0) return;
-    w.n = p.kv_lens[w.s];
     w.first = w.n - w.nq;
     w.n = max((int64_t)0, min(w.n, p.ld_pages << p.log_p));
     w.used = (int)min((int64_t)p.splits, max((int64_t)1, (w.n + p.chunk - 1) / p.chunk));
@@ -253,11 +292,74 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
     w.k0 = sp * p.chunk;
     w.k1 = sp == p.splits - 1 ? w.n : min(w.n, w.k0 + p.chunk);
 
-    // the query rows: scaled by a power of two so that the largest element lies in [1, 2), as fragments
+    // ---- the ring: tile i of this warp is keys k0 + 32 * (kWarps i + warp) .. ----
+    const uint32_t ring = pipe::smem_u32(smem) + (uint32_t)(warp * S * L::kBytes);
+    const int64_t head = (int64_t)w.h * p.P * (CB + 2 * DB), page_bytes = (int64_t)p.H * p.P * (CB + 2 * DB);
+    const int tiles = (int)((w.k1 - w.k0 + kKeys - 1) / kKeys);
+    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
+    const int32_t *table = p.pages + w.s * p.ld_pages;
+    // lanes 0-15 know the page of the tile's first 16 keys, lanes 16-31 that of the others
+    auto page_of = [&](int i) -> int {
+        const int64_t j = w.k0 + (int64_t)(i * kWarps + warp) * kKeys + (lane & 16);
+        return i < mine && j < w.k1 ? table[j >> p.log_p] : -1;
+    };
+    auto issue = [&](int i, int page) {
+        if (i < mine) {
+            const int slot = i % S;
+            const uint32_t dst = ring + (uint32_t)(slot * L::kBytes);
+            const int64_t j = w.k0 + (int64_t)(i * kWarps + warp) * kKeys;
+            const int pg0 = __shfl_sync(0xffffffffu, page, 0), pg1 = __shfl_sync(0xffffffffu, page, 16);
+            const bool ok0 = pg0 >= 0 && pg0 < p.n_pages, ok1 = pg1 >= 0 && pg1 < p.n_pages;
+            const int off0 = (int)j & (p.P - 1), off1 = (off0 + 16) & (p.P - 1);
+            // where the 16 keys' codes and scales start, each contiguous
+            const int64_t c0 = (int64_t)pg0 * page_bytes + head, c1 = (int64_t)pg1 * page_bytes + head;
+            const int64_t a0 = c0 + off0 * CB + lane * 16, a1 = c1 + off1 * CB + lane * 16 - 16 * CB;
+            constexpr int PK = CB / 16, ITS = kKeys * PK / 32;     // pieces of 16 bytes: of a key, for a lane
+#pragma unroll
+            for (int it = 0; it < ITS; ++it) {
+                const int u = it * 32 + lane, key = u / PK, c = u % PK;
+                const bool second = PK % 2 == 0 ? it >= ITS / 2 : key >= 16;
+                if (second ? ok1 : ok0) {
+                    const int64_t src = (second ? a1 : a0) + it * 512;
+                    const int blk = c * 16 / UNIT, in = c * 16 % UNIT;
+                    const int vrow = (key & 16) | ((key & 1) << 3) | ((key & 15) >> 1);
+                    cp_async16(dst + L::kK + (key * DB + swz<DB, SPAN>(key, blk)) * UNIT + in, p.k_cache + src);
+                    cp_async16(dst + L::kV + (vrow * DB + swz<DB, SPAN>(vrow, blk)) * UNIT + in, p.v_cache + src);
+                }
+            }
+            // scales: 2 * DB pieces for 16 keys
+            if (lane < 4 * DB) {
+                const bool second = lane >= 2 * DB;
+                if (second ? ok1 : ok0) {
+                    const int64_t src = (second ? c1 + off1 * (2 * DB) - 32 * DB : c0 + off0 * (2 * DB)) + p.P * CB + lane * 16;
+                    cp_async16(dst + L::kKs + lane * 16, p.k_cache + src);
+                    cp_async16(dst + L::kVs + lane * 16, p.v_cache + src);
+                }
+            }
+            if (lane == 0) {
+                const int64_t left = w.k1 - j;
+                uint32_t m = left >= 32 ? 0xffffffffu : (1u << (int)left) - 1u;
+                if (!ok0) m &= 0xffff0000u;
+                if (!ok1) m &= 0x0000ffffu;
+                masks[warp * 8 + slot] = m;
+            }
+        }
+        cp_commit();
+    };
+    int page = page_of(0);
+#pragma unroll
+    for (int i = 0; i < S - 1; ++i) {
+        const int next = page_of(i + 1);
+        issue(i, page);
+        page = next;
+    }
+
+    // ---- the query rows: scaled by a power of two so that the largest element lies in [1, 2), as fragments ----
     for (int row = warp; row < kRowsTile; row += kWarps) {
         const int r = w.r0 + row;
         const int64_t base = row < w.rows ? (w.q0 + r / p.group) * p.ldq + (int64_t)(w.h * p.group + r % p.group) * D : 0;
         float top = 0.0f;
+#pragma unroll
         for (int b = 0; b < DB; ++b)
             if (row < w.rows) top = fmaxf(top, fabsf(load_q(p, base + 32 * b + lane)));
 #pragma unroll
@@ -272,9 +374,9 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < DB * 2 * 32 * 4; i += kThreads) {
-        const int reg = i & 3, ln = (i >> 2) & 31, st = (i >> 7) & 1, b = i >> 8;
-        const int row = (ln >> 2) + 8 * (reg & 1);
+    for (int i = threadIdx.x; i < MT * DB * 2 * 32 * 4; i += kThreads) {
+        const int reg = i & 3, ln = (i >> 2) & 31, st = (i >> 7) & 1, b = (i >> 8) % DB, mt = (i >> 8) / DB;
+        const int row = mt * 16 + (ln >> 2) + 8 * (reg & 1);
         int e0, e1;
         frag_elems<TYPE>(ln & 3, st, reg >> 1, e0, e1);
         uint32_t v = 0;
@@ -286,94 +388,29 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
         q_frag[i] = v;
     }
     __syncthreads();
+    auto load_frag = [&](uint32_t (&a)[4], int mt, int b, int st) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + (((mt * DB + b) * 2 + st) * 32 + lane) * 4);
+        a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+    };
     uint32_t qr[kQRegs ? DB : 1][2][4];
     if constexpr (kQRegs) {
 #pragma unroll
         for (int b = 0; b < DB; ++b)
 #pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + ((b * 2 + st) * 32 + lane) * 4);
-                qr[b][st][0] = v.x; qr[b][st][1] = v.y; qr[b][st][2] = v.z; qr[b][st][3] = v.w;
-            }
-    }
-    const float mul[2] = {row_mul[g], row_mul[g + 8]};
-    // what rows g and g + 8 see of the new tokens: a tree word, or (without) tokens up to their own
-    const int tok0 = (w.r0 + g) / p.group, tok1 = (w.r0 + g + 8) / p.group;
-    uint64_t word0 = 0, word1 = 0;
-    if (p.tree) {
-        word0 = g < w.rows ? p.tree[w.q0 + tok0] : 0;
-        word1 = g + 8 < w.rows ? p.tree[w.q0 + tok1] : 0;
+            for (int st = 0; st < 2; ++st) load_frag(qr[b][st], 0, b, st);
     }
 
-    // ---- the ring: tile i of this warp is keys k0 + 32 * (kWarps i + warp) .. ----
-    const uint32_t ring = pipe::smem_u32(smem) + (uint32_t)(warp * S * L::kBytes);
-    const int64_t head = (int64_t)w.h * p.P * cache_token_bytes(TYPE, D), page_bytes = (int64_t)p.H * p.P * cache_token_bytes(TYPE, D);
-    const int tiles = (int)((w.k1 - w.k0 + kKeys - 1) / kKeys);
-    const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-    const int32_t *table = p.pages + w.s * p.ld_pages;
-    // lanes 0-15 know the page of the tile's first 16 keys, lanes 16-31 that of the others
-    auto page_of = [&](int i) -> int {
-        const int64_t j = w.k0 + (int64_t)(i * kWarps + warp) * kKeys + (lane & 16);
-        return i < mine && j < w.k1 ? table[j >> p.log_p] : -1;
-    };
-    auto issue = [&](int i, int page) {
-        if (i < mine) {
-            const int slot = i % S;
-            const uint32_t dst = ring + (uint32_t)(slot * L::kBytes);
-            const int64_t j = w.k0 + (int64_t)(i * kWarps + warp) * kKeys;
-            const int pg[2] = {__shfl_sync(0xffffffffu, page, 0), __shfl_sync(0xffffffffu, page, 16)};
-            const bool ok[2] = {pg[0] >= 0 && pg[0] < p.n_pages, pg[1] >= 0 && pg[1] < p.n_pages};
-            const int off = (int)(j & (p.P - 1));
-            const int64_t c0 = (int64_t)pg[0] * page_bytes + head, c1 = (int64_t)pg[1] * page_bytes + head;
-            const int off1 = (off + 16) & (p.P - 1);
-            // codes, 16 bytes a lane: kKeys * CB / 16 pieces of keys, as many of values
+    float o[MT][4 * DB][4];
+    float top[MT][2], sum[MT][2];
 #pragma unroll
-            for (int it = 0; it < kKeys * CB / 16 / 32; ++it) {
-                constexpr int PK = CB / 16;                     // pieces of a key
-                const int u = it * 32 + lane, key = u / PK, c = u % PK;
-                const bool second = key >= 16;
-                if (second ? ok[1] : ok[0]) {
-                    const int64_t src = (second ? c1 + (int64_t)(off1 + key - 16) * CB : c0 + (int64_t)(off + key) * CB) + c * 16;
-                    const int blk = c * 16 / UNIT, in = c * 16 % UNIT;
-                    const int vrow = (key & 16) | ((key & 1) << 3) | ((key & 15) >> 1);
-                    cp_async16(dst + L::kK + (key * DB + swz<DB, SPAN>(key, blk)) * UNIT + in, p.k_cache + src);
-                    cp_async16(dst + L::kV + (vrow * DB + swz<DB, SPAN>(vrow, blk)) * UNIT + in, p.v_cache + src);
-                }
-            }
-            // scales: 2 * DB pieces for 16 keys
-            if (lane < 4 * DB) {
-                const bool second = lane >= 2 * DB;
-                const int c = second ? lane - 2 * DB : lane;
-                if (second ? ok[1] : ok[0]) {
-                    const int64_t src = (second ? c1 + (int64_t)off1 * (2 * DB) : c0 + (int64_t)off * (2 * DB)) + (int64_t)p.P * CB + c * 16;
-                    cp_async16(dst + L::kKs + lane * 16, p.k_cache + src);
-                    cp_async16(dst + L::kVs + lane * 16, p.v_cache + src);
-                }
-            }
-            if (lane == 0) {
-                const int64_t left = w.k1 - j;
-                uint32_t m = left >= 32 ? 0xffffffffu : (1u << (int)left) - 1u;
-                if (!ok[0]) m &= 0xffff0000u;
-                if (!ok[1]) m &= 0x0000ffffu;
-                masks[warp * 8 + slot] = m;
-            }
-        }
-        cp_commit();
-    };
-
-    float o[4 * DB][4];
+    for (int mt = 0; mt < MT; ++mt) {
+        top[mt][0] = top[mt][1] = -INFINITY;
+        sum[mt][0] = sum[mt][1] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4 * DB; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
-    float top[2] = {-INFINITY, -INFINITY}, sum[2] = {0.0f, 0.0f};
+        for (int i = 0; i < 4 * DB; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
+    }
     uint32_t odd = 0;                                            // a value scale that is not finite
 
-    int page = page_of(0);
-#pragma unroll
-    for (int i = 0; i < S - 1; ++i) {
-        const int next = page_of(i + 1);
-        issue(i, page);
-        page = next;
-    }
     for (int i = 0; i < mine; ++i) {
         cp_wait<S - 2>();
         __syncwarp();
@@ -385,28 +422,27 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
         const uint8_t *st = smem + warp * S * L::kBytes + (i % S) * L::kBytes;
         const uint32_t in = masks[warp * 8 + i % S];
         const int64_t j0 = w.k0 + (int64_t)(i * kWarps + warp) * kKeys;
+        const bool masked = in != 0xffffffffu || j0 + kKeys > w.first;
 
-        // ---- scores: sc[nt] holds keys 8 nt + 2t, + 1 of rows g (0, 1) and g + 8 (2, 3) ----
-        float sc[4][4];
+        // ---- scores: sc[mt][nt] holds keys 8 nt + 2t, + 1 of rows g (0, 1) and g + 8 (2, 3) ----
+        float sc[MT][4][4];
+        uint32_t kw[4][DB];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
-        const __half *ks = reinterpret_cast<const __half *>(st + L::kKs);
+        for (int nt = 0; nt < 4; ++nt) load_scales<DB>(st + L::kKs + (8 * nt + 2 * t) * DB * 2, kw[nt]);
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
-            uint32_t a[2][4];
-            if constexpr (kQRegs) {
+            uint32_t a[MT][2][4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    a[0][r] = qr[b][0][r];
-                    a[1][r] = qr[b][1][r];
-                }
-            } else {
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
                 for (int s2 = 0; s2 < 2; ++s2) {
-                    const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + ((b * 2 + s2) * 32 + lane) * 4);
-                    a[s2][0] = v.x; a[s2][1] = v.y; a[s2][2] = v.z; a[s2][3] = v.w;
+                    if constexpr (kQRegs) {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) a[mt][s2][r] = qr[b][s2][r];
+                    } else {
+                        load_frag(a[mt][s2], mt, b, s2);
+                    }
                 }
-            }
 #pragma unroll
             for (int nt = 0; nt < 4; ++nt) {
                 const int key = 8 * nt + g;
@@ -423,87 +459,111 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
                     f[2] = nib_h2(c >> 4);
                     f[3] = nib_h2(c >> 12);
                 }
-                float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                mma16816(acc, a[0], f[0], f[1]);
-                mma16816(acc, a[1], f[2], f[3]);
-                const float d0 = __half2float(ks[(8 * nt + 2 * t) * DB + b]), d1 = __half2float(ks[(8 * nt + 2 * t + 1) * DB + b]);
-                sc[nt][0] += d0 * acc[0];
-                sc[nt][1] += d1 * acc[1];
-                sc[nt][2] += d0 * acc[2];
-                sc[nt][3] += d1 * acc[3];
+                const float d0 = scale_of<DB>(kw[nt], b), d1 = scale_of<DB>(kw[nt], DB + b);
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    float acc[4];
+                    mma16816_first(acc, a[mt][0], f[0], f[1]);
+                    mma16816(acc, a[mt][1], f[2], f[3]);
+                    if (b == 0) {
+                        sc[mt][nt][0] = d0 * acc[0];
+                        sc[mt][nt][1] = d1 * acc[1];
+                        sc[mt][nt][2] = d0 * acc[2];
+                        sc[mt][nt][3] = d1 * acc[3];
+                    } else {
+                        sc[mt][nt][0] += d0 * acc[0];
+                        sc[mt][nt][1] += d1 * acc[1];
+                        sc[mt][nt][2] += d0 * acc[2];
+                        sc[mt][nt][3] += d1 * acc[3];
+                    }
+                }
             }
         }
         // ---- what is not seen ----
-        if (in != 0xffffffffu || j0 + kKeys > w.first) {
+        if (masked) {
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
+            for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    const int key = 8 * nt + 2 * t + c;
-                    const int64_t nb = j0 + key - w.first;       // place among the new tokens
-                    const bool have = (in >> key) & 1;
-                    bool s0 = have, s1 = have;
-                    if (nb >= 0) {
-                        s0 = have && (p.tree ? nb < 64 && ((word0 >> nb) & 1) : nb <= tok0);
-                        s1 = have && (p.tree ? nb < 64 && ((word1 >> nb) & 1) : nb <= tok1);
-                    }
-                    if (!s0) sc[nt][c] = -INFINITY;
-                    if (!s1) sc[nt][2 + c] = -INFINITY;
+                for (int r = 0; r < 2; ++r) {
+                    const int row = mt * 16 + g + 8 * r, tok = (w.r0 + row) / p.group;
+                    const uint64_t word = p.tree && row < w.rows ? p.tree[w.q0 + tok] : 0;
+#pragma unroll
+                    for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            const int key = 8 * nt + 2 * t + c;
+                            const int64_t nb = j0 + key - w.first;      // place among the new tokens
+                            bool seen = (in >> key) & 1;
+                            if (nb >= 0) seen = seen && (p.tree ? nb < 64 && ((word >> nb) & 1) : nb <= tok);
+                            if (!seen) sc[mt][nt][2 * r + c] = -INFINITY;
+                        }
                 }
         }
         // ---- running maximum and sum; p to fp16 ----
-        float base[2];
-        bool moved = false;
-        float down[2];
+        uint32_t pf[MT][4][2];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            float m = fmaxf(fmaxf(fmaxf(sc[0][2 * r], sc[0][2 * r + 1]), fmaxf(sc[1][2 * r], sc[1][2 * r + 1])),
-                            fmaxf(fmaxf(sc[2][2 * r], sc[2][2 * r + 1]), fmaxf(sc[3][2 * r], sc[3][2 * r + 1])));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-            m = fmaxf(m * mul[r], top[r]);
-            base[r] = m == -INFINITY ? 0.0f : m;
-            down[r] = ex2(top[r] - base[r]);
-            moved |= m != top[r];
-            top[r] = m;
-        }
-        if (__any_sync(0xffffffffu, moved)) {
-            sum[0] *= down[0];
-            sum[1] *= down[1];
-#pragma unroll
-            for (int n = 0; n < 4 * DB; ++n) {
-                o[n][0] *= down[0];
-                o[n][1] *= down[0];
-                o[n][2] *= down[1];
-                o[n][3] *= down[1];
-            }
-        }
-        uint32_t pf[4][2];
-#pragma unroll
-        for (int nt = 0; nt < 4; ++nt)
+        for (int mt = 0; mt < MT; ++mt) {
+            float base[2], down[2], mul[2];
+            bool moved = false;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                const float p0 = ex2(fmaf(sc[nt][2 * r], mul[r], kBias - base[r])), p1 = ex2(fmaf(sc[nt][2 * r + 1], mul[r], kBias - base[r]));
-                sum[r] += p0 + p1;
-                pf[nt][r] = pack2(p0, p1, __half{});
+                mul[r] = row_mul[mt * 16 + g + 8 * r];
+                const float (&x)[4][4] = sc[mt];
+                float m = fmaxf(fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1])),
+                                fmaxf(fmaxf(x[2][2 * r], x[2][2 * r + 1]), fmaxf(x[3][2 * r], x[3][2 * r + 1])));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+                m = fmaxf(m * mul[r], top[mt][r]);
+                base[r] = m == -INFINITY ? 0.0f : m;
+                down[r] = ex2(top[mt][r] - base[r]);
+                moved |= m != top[mt][r];
+                top[mt][r] = m;
+                base[r] = kBias - base[r];
             }
+            if (__any_sync(0xffffffffu, moved)) {
+                sum[mt][0] *= down[0];
+                sum[mt][1] *= down[1];
+#pragma unroll
+                for (int n = 0; n < 4 * DB; ++n) {
+                    o[mt][n][0] *= down[0];
+                    o[mt][n][1] *= down[0];
+                    o[mt][n][2] *= down[1];
+                    o[mt][n][3] *= down[1];
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < 4; ++nt)
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    const float p0 = ex2(fmaf(sc[mt][nt][2 * r], mul[r], base[r])), p1 = ex2(fmaf(sc[mt][nt][2 * r + 1], mul[r], base[r]));
+                    sum[mt][r] += p0 + p1;
+                    pf[mt][nt][r] = pack2(p0, p1, __half{});
+                }
+        }
         // ---- values: 16 keys a step; a lane's keys are 2t, 2t + 1, 2t + 8, 2t + 9 ----
-        const __half *vs = reinterpret_cast<const __half *>(st + L::kVs);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-            const uint32_t a[4] = {pf[2 * j][0], pf[2 * j][1], pf[2 * j + 1][0], pf[2 * j + 1][1]};
-            const uint32_t have = in >> (16 * j + 2 * t);
-            const uint32_t m01 = ((have & 1) ? 0xffffu : 0u) | ((have & 2) ? 0xffff0000u : 0u);
-            const uint32_t m89 = ((have & 256) ? 0xffffu : 0u) | ((have & 512) ? 0xffff0000u : 0u);
-            const int k0 = 16 * j + 2 * t;
+            uint32_t w01[DB], w89[DB];
+            load_scales<DB>(st + L::kVs + (16 * j + 2 * t) * DB * 2, w01);
+            load_scales<DB>(st + L::kVs + (16 * j + 2 * t + 8) * DB * 2, w89);
+            if (masked) {
+                const uint32_t have = in >> (16 * j + 2 * t);
+#pragma unroll
+                for (int i2 = 0; i2 < DB; ++i2) {
+                    // half 2 i2 and 2 i2 + 1: of the first key below DB, of the second from there
+                    constexpr uint32_t kLo = 0xFFFFu, kHi = 0xFFFF0000u;
+                    const int lo = 2 * i2 >= DB, hi = 2 * i2 + 1 >= DB;
+                    w01[i2] &= ((have >> lo) & 1 ? kLo : 0u) | ((have >> hi) & 1 ? kHi : 0u);
+                    w89[i2] &= ((have >> (8 + lo)) & 1 ? kLo : 0u) | ((have >> (8 + hi)) & 1 ? kHi : 0u);
+                    const uint32_t f01 = finite2(w01[i2]), f89 = finite2(w89[i2]);
+                    odd |= ~(f01 & f89);
+                    w01[i2] &= f01;
+                    w89[i2] &= f89;
+                }
+            }
 #pragma unroll
             for (int b = 0; b < DB; ++b) {
-                uint32_t d01 = m01 & ((uint32_t)__half_as_ushort(vs[k0 * DB + b]) | ((uint32_t)__half_as_ushort(vs[(k0 + 1) * DB + b]) << 16));
-                uint32_t d89 = m89 & ((uint32_t)__half_as_ushort(vs[(k0 + 8) * DB + b]) | ((uint32_t)__half_as_ushort(vs[(k0 + 9) * DB + b]) << 16));
-                const uint32_t f01 = finite2(d01), f89 = finite2(d89);
-                odd |= ~(f01 & f89);
-                d01 &= f01;
-                d89 &= f89;
+                const uint32_t d01 = scale_pair<DB>(w01, b), d89 = scale_pair<DB>(w89, b);
                 const uint8_t *vp = st + L::kV;
                 const int r0 = 16 * j + t;                       // rows of keys 2t, 2t + 8, 2t + 1, 2t + 9: t, t + 4, t + 8, t + 12
                 auto row = [&](int r) { return vp + (r * DB + swz<DB, SPAN>(r, b)) * UNIT; };
@@ -527,7 +587,14 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
                     }
                 }
 #pragma unroll
-                for (int e = 0; e < 4; ++e) mma16816(o[4 * b + e], a, hmul2(x[e], d01), hmul2(y[e], d89));
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t v01 = hmul2(x[e], d01), v89 = hmul2(y[e], d89);
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt) {
+                        const uint32_t a[4] = {pf[mt][2 * j][0], pf[mt][2 * j][1], pf[mt][2 * j + 1][0], pf[mt][2 * j + 1][1]};
+                        mma16816(o[mt][4 * b + e], a, v01, v89);
+                    }
+                }
             }
         }
         __syncwarp();
@@ -535,30 +602,31 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
     cp_wait<0>();
 
     // ---- the warps' results, joined ----
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 1);
-        sum[r] += __shfl_xor_sync(0xffffffffu, sum[r], 2);
-    }
     __syncthreads();                                             // the ring is free
     float *res = reinterpret_cast<float *>(smem) + warp * kRowsTile * D;
-    if (t == 0) {
-        w_top[warp * kRowsTile + g] = top[0];
-        w_top[warp * kRowsTile + g + 8] = top[1];
-        w_sum[warp * kRowsTile + g] = sum[0];
-        w_sum[warp * kRowsTile + g + 8] = sum[1];
-    }
 #pragma unroll
-    for (int b = 0; b < DB; ++b)
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int row = g + 8 * (c >> 1), n = 2 * t + (c & 1);
-                // n tile e of block b, column n: the element whose codes were fed to it
-                const int d = TYPE == QMM_Q8_0 ? 4 * n + e : 2 * n + (e >> 1) + 16 * (e & 1);
-                if (row < w.rows) res[row * D + 32 * b + d] = o[4 * b + e][c];
+        for (int r = 0; r < 2; ++r) {
+            sum[mt][r] += __shfl_xor_sync(0xffffffffu, sum[mt][r], 1);
+            sum[mt][r] += __shfl_xor_sync(0xffffffffu, sum[mt][r], 2);
+            if (t == 0) {
+                w_top[warp * kRowsTile + mt * 16 + g + 8 * r] = top[mt][r];
+                w_sum[warp * kRowsTile + mt * 16 + g + 8 * r] = sum[mt][r];
             }
+        }
+#pragma unroll
+        for (int b = 0; b < DB; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int row = mt * 16 + g + 8 * (c >> 1), n = 2 * t + (c & 1);
+                    // n tile e of block b, column n: the element whose codes were fed to it
+                    const int d = TYPE == QMM_Q8_0 ? 4 * n + e : 2 * n + (e >> 1) + 16 * (e & 1);
+                    if (row < w.rows) res[row * D + 32 * b + d] = o[mt][4 * b + e][c];
+                }
+    }
     __syncthreads();
     bool bad = odd != 0;
     for (int i = threadIdx.x; i < w.rows * D; i += kThreads) {
@@ -580,7 +648,7 @@ __global__ void __launch_bounds__(Tile<TYPE, DB>::kThreads, 1) attend_kernel(con
         }
         write_row(p, w, sp, D, row, d, v, m, l);
     }
-    if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB>(p, w, sp, row_bad);
+    if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB, MT>(p, w, sp, row_bad);
 }
 
 // Joins the partial results of the sequences that were split.  WPR warps take a row, each the splits of
@@ -604,7 +672,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
         if (p.q_starts[mid] <= tok) lo = mid; else hi = mid - 1;
     }
     // rows past row_tiles were not computed
-    if ((tok - p.q_starts[lo]) * p.group + hq % p.group >= (int64_t)p.row_tiles * kRowsTile) return;
+    if ((tok - p.q_starts[lo]) * p.group + hq % p.group >= (int64_t)p.row_tiles * p.tile_rows) return;
     const int64_t n = max((int64_t)0, min((int64_t)p.kv_lens[lo], p.ld_pages << p.log_p));
     const int used = (int)min((int64_t)p.splits, (n + p.chunk - 1) / p.chunk);
     if (used <= 1) return;
@@ -654,6 +722,9 @@ constexpr int kMaxSplits = 256;
 
 // Splits of the longest sequence: until there are several CTAs an SM (ragged lengths even out), but no
 // chunk below two tiles a warp.
+// Rows of a CTA: 32, where a sequence has more than 16 and the sums of 32 fit in registers, so that the
+// codes are expanded half as often.
+int tile_rows_of(int64_t max_new, int group, int D) { return max_new * group > kMmaRows && D <= 128 ? 2 * kMmaRows : kMmaRows; }
 int wanted_splits(int64_t units, int64_t max_len) {
     const int64_t most = (max_len + 2 * kMinChunk - 1) / (2 * kMinChunk);
     int64_t want = (152 * 4 + units - 1) / units;
@@ -661,14 +732,17 @@ int wanted_splits(int64_t units, int64_t max_len) {
     want = want < kMaxSplits ? want : kMaxSplits;
     return (int)(want < 1 ? 1 : want);
 }
-int64_t row_tiles_of(int64_t max_new, int group) { return (max_new * group + kRowsTile - 1) / kRowsTile; }
+int64_t row_tiles_of(int64_t max_new, int group, int D) {
+    const int rows = tile_rows_of(max_new, group, D);
+    return (max_new * group + rows - 1) / rows;
+}
 size_t split_bytes(int64_t rows, int D) { return round256((size_t)rows * (size_t)(D + 2) * 4); }
 
-template <int TYPE, int DB>
+template <int TYPE, int DB, int MT>
 cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
-    using L = Tile<TYPE, DB>;
+    using L = Tile<TYPE, DB, MT>;
     static_assert(L::kSmem <= 227 * 1024, "shared memory plan too large");
-    auto kern = attend_kernel<TYPE, DB>;
+    auto kern = attend_kernel<TYPE, DB, MT>;
     static int attr_done[4] = {0, 0, 0, 0};
     cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
     if (e != cudaSuccess) return e;
@@ -681,22 +755,23 @@ cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
 
 template <int TYPE>
 cudaError_t launch_blocks(const AttendParams &p, int DB, int64_t ctas, cudaStream_t s) {
+    const bool two = p.tile_rows > kMmaRows;
     switch (DB) {
-        case 1: return launch_typed<TYPE, 1>(p, ctas, s);
-        case 2: return launch_typed<TYPE, 2>(p, ctas, s);
-        case 3: return launch_typed<TYPE, 3>(p, ctas, s);
-        case 4: return launch_typed<TYPE, 4>(p, ctas, s);
-        case 5: return launch_typed<TYPE, 5>(p, ctas, s);
-        case 6: return launch_typed<TYPE, 6>(p, ctas, s);
-        case 7: return launch_typed<TYPE, 7>(p, ctas, s);
-        default: return launch_typed<TYPE, 8>(p, ctas, s);
+        case 1: return two ? launch_typed<TYPE, 1, 2>(p, ctas, s) : launch_typed<TYPE, 1, 1>(p, ctas, s);
+        case 2: return two ? launch_typed<TYPE, 2, 2>(p, ctas, s) : launch_typed<TYPE, 2, 1>(p, ctas, s);
+        case 3: return two ? launch_typed<TYPE, 3, 2>(p, ctas, s) : launch_typed<TYPE, 3, 1>(p, ctas, s);
+        case 4: return two ? launch_typed<TYPE, 4, 2>(p, ctas, s) : launch_typed<TYPE, 4, 1>(p, ctas, s);
+        case 5: return launch_typed<TYPE, 5, 1>(p, ctas, s);
+        case 6: return launch_typed<TYPE, 6, 1>(p, ctas, s);
+        case 7: return launch_typed<TYPE, 7, 1>(p, ctas, s);
+        default: return launch_typed<TYPE, 8, 1>(p, ctas, s);
     }
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int64_t n_seq, int64_t max_new, int H, int Hq, int D, int64_t max_len) {
-    const int splits = wanted_splits(n_seq * H * row_tiles_of(max_new, Hq / H), max_len);
+    const int splits = wanted_splits(n_seq * H * row_tiles_of(max_new, Hq / H, D), max_len);
     return splits == 1 ? 0 : (size_t)splits * split_bytes(n_seq * max_new * Hq, D);
 }
 
@@ -713,7 +788,9 @@ cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uin
     while ((1 << p.log_p) < P) ++p.log_p;
     p.H = H;
     p.group = Hq / H;
-    const int64_t row_tiles = row_tiles_of(max_new < T ? max_new : T, p.group);   // no sequence has more than T
+    if (max_new > T) max_new = T;                                    // no sequence has more
+    p.tile_rows = tile_rows_of(max_new, p.group, D);
+    const int64_t row_tiles = row_tiles_of(max_new, p.group, D);
     const int64_t units = n_seq * H * row_tiles;
     if (units > 0x7fffffff) return cudaErrorInvalidValue;
     p.row_tiles = (int)row_tiles;

@@ -24,12 +24,11 @@ __device__ __forceinline__ uint32_t trunc_bits(float v) { return __float_as_uint
 
 // Codes of a lane's 8 elements and the block's scale; the four lanes of a block (and so, for the
 // shuffles, the warp) call it together.  Q8_0: 8 int8 codes in w[0..1].  Q4_0: element i in nibble i of w[0].
-template <int TYPE>
-__device__ __forceinline__ uint16_t quantize8(const float (&v)[8], uint32_t (&w)[2]) {
-    // the largest magnitude, as bits: infinities and NaN come out on top
-    uint32_t bits = 0;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) bits = max(bits, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+template <int TYPE, typename T>
+__device__ __forceinline__ uint16_t quantize8(const Raw8<T> &raw, uint32_t (&w)[2]) {
+    float v[8];
+    raw.values(v);
+    uint32_t bits = raw.top_bits();
     bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
     bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
     float d;
@@ -56,7 +55,7 @@ __device__ __forceinline__ uint16_t quantize8(const float (&v)[8], uint32_t (&w)
     const uint16_t half = __half_as_ushort(__float2half_rn(d));
     w[0] = w[1] = 0;
     if (bits >= 0x7F800000u || (half & 0x7C00u) == 0x7C00u) return 0x7E00u;
-    const float id = inv_or_zero(d);
+    const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
     if (!(fabsf(id) < INFINITY)) {
         // 1 / d overflows: element by element, with the products' infinities and NaN
 #pragma unroll
@@ -109,8 +108,8 @@ struct Place {
     int off, P;
     __device__ __forceinline__ Place(int64_t slot_page, int h, int H, int off_, int log_p)
         : chunk(((slot_page * H + h) << log_p) * kToken), off(off_), P(1 << log_p) {}
-    __device__ __forceinline__ int64_t codes(int block) const { return chunk + off * kCodes + block * (kCodes / DB); }
-    __device__ __forceinline__ int64_t scale(int block) const { return chunk + P * kCodes + (off * DB + block) * 2; }
+    __device__ __forceinline__ int64_t codes(int block, int in) const { return chunk + (off * kCodes + block * (kCodes / DB) + in); }
+    __device__ __forceinline__ int64_t scale(int block) const { return chunk + (P * kCodes + (off * DB + block) * 2); }
 };
 
 // A thread takes pieces of 8 elements; blockIdx.y: 0 keys, 1 values.
@@ -125,17 +124,16 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     // items is a multiple of 4 and so is every warp's first index: the four lanes of a block are all in
     // range or all out of it, and all 32 lanes stay in the loop for the shuffles
     for (uint32_t base = blockIdx.x * kThreads + (threadIdx.x & ~31u); base < p.items; base += step * kBatch) {
-        float v[kBatch][8];
+        Raw8<T> raw[kBatch];
         int64_t slot[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const uint32_t i = base + u * step + (threadIdx.x & 31u), tok = p.per_tok(i);
             slot[u] = -1;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
+            raw[u].zero();
             if (i < p.items) {
                 slot[u] = p.slots[tok];
-                load8<VEC>(src + tok * p.ld[which] + (int64_t)(i - tok * p.per_tok.d) * 8, v[u]);
+                raw[u].template load<VEC>(src + tok * p.ld[which] + (int64_t)(i - tok * p.per_tok.d) * 8);
             }
         }
 #pragma unroll
@@ -143,7 +141,7 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
             if (base + u * step >= p.items) break;
             const uint32_t i = base + u * step + (threadIdx.x & 31u), in_tok = i - p.per_tok(i) * p.per_tok.d;
             uint32_t w[2];
-            const uint16_t d = quantize8<TYPE>(v[u], w);
+            const uint16_t d = quantize8<TYPE>(raw[u], w);
             uint32_t other = 0;
             if constexpr (TYPE == QMM_Q4_0) other = __shfl_xor_sync(0xffffffffu, w[0], 2);
             if (slot[u] < 0 || slot[u] >= p.n_slots) continue;
@@ -151,13 +149,13 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
             if (!QMM_DCHECK(h < p.H)) continue;
             const Place<TYPE, DB> at(slot[u] >> p.log_p, h, p.H, (int)(slot[u] & ((1 << p.log_p) - 1)), p.log_p);
             if constexpr (TYPE == QMM_Q8_0) {
-                *reinterpret_cast<uint2 *>(cache + at.codes(c >> 2) + 8 * (c & 3)) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2 *>(cache + at.codes(c >> 2, 8 * (c & 3))) = make_uint2(w[0], w[1]);
             } else {
                 // lanes 0, 1 hold elements 0..15 of the block, lanes 2, 3 elements 16..31; bytes 8 (lane & 1)
                 // .. + 7 pair them: the lower lane writes the first four, the upper lane the others
                 const bool upper = (c & 2) != 0;
                 const uint32_t lo = upper ? other >> 16 : w[0], hi = upper ? w[0] >> 16 : other;
-                *reinterpret_cast<uint32_t *>(cache + at.codes(c >> 2) + (c & 1) * 8 + (upper ? 4 : 0)) =
+                *reinterpret_cast<uint32_t *>(cache + at.codes(c >> 2, (c & 1) * 8 + (upper ? 4 : 0))) =
                     spread4(lo & 0xFFFFu) | (spread4(hi & 0xFFFFu) << 4);
             }
             if ((c & 3) == 0) *reinterpret_cast<uint16_t *>(cache + at.scale(c >> 2)) = d;
@@ -230,7 +228,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
                     const int h = (int)(in_tok / (4 * DB)), c = (int)(in_tok % (4 * DB));
                     const Place<TYPE, DB> at(s_page[tok], h, p.H, s_off[tok], p.log_p);
                     d[u] = *reinterpret_cast<const uint16_t *>(cache + at.scale(c >> 2));
-                    w[u] = *reinterpret_cast<const uint2 *>(cache + at.codes(c >> 2) + 8 * (TYPE == QMM_Q8_0 ? c & 3 : c & 1));
+                    w[u] = *reinterpret_cast<const uint2 *>(cache + at.codes(c >> 2, 8 * (TYPE == QMM_Q8_0 ? c & 3 : c & 1)));
                 }
             }
 #pragma unroll

@@ -29,27 +29,62 @@ __device__ __forceinline__ float2 unpack2(uint32_t w, __nv_bfloat16) {
     return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&w));
 }
 
-// 8 consecutive elements at p as fp32; VEC: p is 16-byte aligned.
-template <bool VEC, typename T>
-__device__ __forceinline__ void load8(const T *p, float (&v)[8]) {
-    if constexpr (!VEC) {
+// 8 consecutive elements as they lie in memory.
+template <typename T>
+struct Raw8 {
+    uint32_t w[2 * sizeof(T)];
+
+    __device__ __forceinline__ void zero() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = elem_to_float(p[i]);
-    } else if constexpr (sizeof(T) == 4) {
-        const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    } else {
-        const uint4 w = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        for (int i = 0; i < 2 * (int)sizeof(T); ++i) w[i] = 0u;
+    }
+    // VEC: p is 16-byte aligned.
+    template <bool VEC>
+    __device__ __forceinline__ void load(const T *p) {
+        if constexpr (VEC) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = unpack2(u[i], T{});
-            v[2 * i] = f.x;
-            v[2 * i + 1] = f.y;
+            for (int i = 0; i < (int)sizeof(T) / 2; ++i) {
+                const uint4 v = reinterpret_cast<const uint4 *>(p)[i];
+                w[4 * i] = v.x; w[4 * i + 1] = v.y; w[4 * i + 2] = v.z; w[4 * i + 3] = v.w;
+            }
+        } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        } else {
+            const uint16_t *q = reinterpret_cast<const uint16_t *>(p);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = (uint32_t)q[2 * i] | ((uint32_t)q[2 * i + 1] << 16);
         }
     }
-}
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+        if constexpr (sizeof(T) == 4) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(w[i]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack2(w[i], T{});
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    }
+    // The largest magnitude as the bits of an fp32; infinities and NaN come out on top.
+    __device__ __forceinline__ uint32_t top_bits() const {
+        if constexpr (sizeof(T) == 4) {
+            uint32_t m = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+            return m;
+        } else {
+            uint32_t m = w[0] & 0x7FFF7FFFu;
+#pragma unroll
+            for (int i = 1; i < 4; ++i) m = __vmaxu2(m, w[i] & 0x7FFF7FFFu);
+            m = max(m & 0xFFFFu, m >> 16);
+            return __float_as_uint(unpack2(m, T{}).x);
+        }
+    }
+};
 
 // 8 fp32 values rounded to T at p; VEC: p is 16-byte aligned.
 template <bool VEC, typename T>

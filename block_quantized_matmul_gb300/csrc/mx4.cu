@@ -29,27 +29,26 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T *__restr
     const int lane = threadIdx.x & 31;
     const uint32_t warps = gridDim.x * kWarps;
     for (uint32_t base = blockIdx.x * kWarps + (threadIdx.x >> 5); base < items; base += warps * kBatch) {
-        float v[kBatch][8];
+        Raw8<T> raw[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const uint32_t i = base + u * warps, row = nseg(i);
             const int64_t k = (int64_t)(i - row * nseg.d) * 256 + lane * 8;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[u][j] = 0.0f;
-            if (i < items && k < K && QMM_DCHECK(k + 8 <= K)) load8<VEC>(x + (r0 + row) * ldx + k, v[u]);
+            raw[u].zero();
+            if (i < items && k < K && QMM_DCHECK(k + 8 <= K)) raw[u].template load<VEC>(x + (r0 + row) * ldx + k);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const uint32_t i = base + u * warps, row = nseg(i);
             if (i >= items) break;
             const int64_t r = r0 + row, seg = i - row * nseg.d, k = seg * 256 + lane * 8;
-            uint32_t top = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[u][j]) & 0x7FFFFFFFu);
+            uint32_t top = raw[u].top_bits();
+            float v[8];
+            raw[u].values(v);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const uint32_t e = mx4_block_scale(top);
-            if (k < K) *reinterpret_cast<uint32_t *>(codes + (r * K + k) / 2) = mx4_codes8(v[u], e);
+            if (k < K) *reinterpret_cast<uint32_t *>(codes + (r * K + k) / 2) = mx4_codes8(v, e);
             // the scales of four blocks (16 lanes) as one word; blocks past K hold 0
             uint32_t word = e << (8 * ((lane >> 2) & 3));
             word |= __shfl_xor_sync(0xffffffffu, word, 4);

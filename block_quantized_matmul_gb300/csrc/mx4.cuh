@@ -8,7 +8,7 @@
 // lanes of 16 bytes, which tcgen05.cp copies to tensor memory as they are.
 #pragma once
 
-#include <cuda_fp4.h>
+#include <cuda_fp16.h>
 #include <stdint.h>
 
 namespace qmm {
@@ -42,22 +42,30 @@ __device__ __forceinline__ uint32_t mx4_block_scale(uint32_t abs_bits) {
 // Codes of 8 elements under scale e (element i in nibble i): E2M1 of x * 2^(127 - e), to nearest even,
 // saturating at 6.  The product is exact but for subnormal results, which round to zero anyway.
 __device__ __forceinline__ uint32_t mx4_codes8(const float (&x)[8], uint32_t e) {
-    if (e == 255u) return 0u;
     const float inv = __uint_as_float((254u - e) << 23);
-    uint32_t w = 0;
+    float v[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w |= (uint32_t)__nv_cvt_float2_to_fp4x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_E2M1, cudaRoundNearest)
-             << (8 * i);
-    return w;
+    for (int i = 0; i < 8; ++i) v[i] = x[i] * inv;
+    uint32_t w;
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        " mov.b32 %0, {b0, b1, b2, b3};\n}\n"
+        : "=r"(w)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return e == 255u ? 0u : w;
 }
 
 // Values of the 8 codes of a word, without the scale.
 __device__ __forceinline__ void mx4_values8(uint32_t w, float (&v)[8]) {
+    uint32_t h[4];
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
+        " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)((w >> (8 * i)) & 0xFFu), __NV_E2M1);
-        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
         v[2 * i] = f.x;
         v[2 * i + 1] = f.y;
     }

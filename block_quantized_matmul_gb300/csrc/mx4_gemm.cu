@@ -23,6 +23,8 @@
 // frees tensor memory and returns.
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "pipeline.cuh"
 #include "qmm_internal.cuh"
 
@@ -52,8 +54,11 @@ struct Mx4Params {
     int last_steps;                        // K = 64 products of the last stage (1 to 4)
     int m_blocks;                          // row blocks of the activations' scales
     int split;                             // CTAs of a cluster, which share a tile's K
-    int early_weights;                     // the kernel before this one writes no weight
+    int early_weights;                     // the weight may be read before the kernel before this one is done
     int dtype;
+    const void *x;                         // rows to be quantized here (fused)
+    int64_t ldx, K;
+    int x_vec;                             // they are 16-byte aligned
 };
 
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort) {
@@ -117,9 +122,12 @@ __device__ __forceinline__ void store_tokens(T *y, int64_t ldy, int64_t m0, int6
         if (m0 + c < M) float_to_elem(__uint_as_float(v[c]), y[(m0 + c) * ldy + row]);
 }
 
-template <int TN>
-__global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, const __grid_constant__ CUtensorMap w_map,
+// XT: void for operands that are quantized already, else the element type of rows that the result warps
+// quantize into each stage while its weights arrive.
+template <int TN, typename XT>
+__global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constant__ Mx4Params p, const __grid_constant__ CUtensorMap w_map,
                                                             const __grid_constant__ CUtensorMap a_map) {
+    constexpr bool kFused = !std::is_same<XT, void>::value;
     using L = Plan<TN>;
     constexpr int S = L::kStages;
     extern __shared__ uint8_t smem_raw[];
@@ -130,13 +138,13 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = p.split > 1 ? (int)(blockIdx.x % (unsigned)p.split) : 0;
     const int64_t tile = blockIdx.x / (unsigned)p.split;
-    const int64_t n0 = tile * kRows, m0 = (int64_t)blockIdx.y * TN;
+    const int64_t n0 = tile * kRows, m0 = 0;                     // one tile of tokens
     const int k0 = (int)((int64_t)p.nk * rank / p.split), k1 = (int)((int64_t)p.nk * (rank + 1) / p.split);
     const int tok_blocks = min(L::kTokBlocks, p.m_blocks - (int)(m0 / 128));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(smem_u32(&full[s]), 1);
+            mbar_init(smem_u32(&full[s]), kFused ? 1 + kEpilogue / 32 : 1);
             mbar_init(smem_u32(&empty[s]), 1);
         }
         mbar_init(smem_u32(done), 1);
@@ -167,11 +175,13 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, c
             auto weights = [&](int k, int s) {                 // announces the whole stage
                 const uint32_t st = smem_u32(smem + s * L::kStageBytes), bar = smem_u32(&full[s]);
                 const uint32_t sb = (uint32_t)blocks(k) * kMx4ScaleBlock;
-                mbar_arrive_expect_tx(bar, (uint32_t)(kRows * 128 + TN * 128) + sb * (uint32_t)(1 + tok_blocks));
+                mbar_arrive_expect_tx(bar, kFused ? (uint32_t)(kRows * 128) + sb
+                                                  : (uint32_t)(kRows * 128 + TN * 128) + sb * (uint32_t)(1 + tok_blocks));
                 tma_load_2d(st + L::kW, &w_map, k * 128, (int)n0, bar);
                 bulk_g2s(st + L::kWS, p.ws + (tile * p.n128 + 2 * k) * (int64_t)kMx4ScaleBlock, sb, bar);
             };
             auto tokens = [&](int k, int s) {
+                if (kFused) return;
                 const uint32_t st = smem_u32(smem + s * L::kStageBytes), bar = smem_u32(&full[s]);
                 const uint32_t sb = (uint32_t)blocks(k) * kMx4ScaleBlock;
                 tma_load_2d(st + L::kA, &a_map, k * 128, (int)m0, bar);
@@ -180,7 +190,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, c
                              p.as + ((m0 / 128 + b) * p.n128 + 2 * k) * (int64_t)kMx4ScaleBlock, sb, bar);
             };
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&w_map)) : "memory");
-            asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a_map)) : "memory");
+            if (!kFused) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a_map)) : "memory");
             const int head = min(S, k1 - k0);
             if (!p.early_weights) asm volatile("griddepcontrol.wait;" ::: "memory");
             for (int i = 0; i < head; ++i) weights(k0 + i, i);
@@ -231,6 +241,52 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, c
     } else {
         const int qd = warp & 3, row = 32 * qd + lane;
         const int64_t n = n0 + row;
+        if constexpr (kFused) {
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+            // row r of a stage goes to warp r % 4, 8 elements a lane; the next stage's rows are loaded before this
+            // one's are worked on
+            constexpr int kMine = TN / 4;
+            const XT *x = static_cast<const XT *>(p.x);
+            Raw8<XT> raw[kMine];
+            auto load = [&](int k) {
+                const int64_t at = (int64_t)k * 256 + lane * 8;
+#pragma unroll
+                for (int u = 0; u < kMine; ++u) {
+                    const int64_t r = qd + 4 * u;
+                    raw[u].zero();
+                    if (r < p.M && at < p.K) {
+                        if (p.x_vec) raw[u].template load<true>(x + r * p.ldx + at);
+                        else raw[u].template load<false>(x + r * p.ldx + at);
+                    }
+                }
+            };
+            load(k0);
+            for (int i = 0; i < k1 - k0; ++i) {
+                const int s = i % S;
+                if (i >= S && !wait_warp(smem_u32(&empty[s]), (uint32_t)((i / S - 1) & 1), abort)) break;
+                uint8_t *st = smem + s * L::kStageBytes;
+#pragma unroll
+                for (int u = 0; u < kMine; ++u) {
+                    const int r = qd + 4 * u;
+                    if (r >= p.M) break;
+                    uint32_t top = raw[u].top_bits();
+                    float v[8];
+                    raw[u].values(v);
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const uint32_t e = mx4_block_scale(top);
+                    *reinterpret_cast<uint32_t *>(st + L::kA + sw128_off(r, lane >> 2) + (lane & 3) * 4) = mx4_codes8(v, e);
+                    uint32_t word = e << (8 * ((lane >> 2) & 3));
+                    word |= __shfl_xor_sync(0xffffffffu, word, 4);
+                    word |= __shfl_xor_sync(0xffffffffu, word, 8);
+                    if ((lane & 15) == 0) *reinterpret_cast<uint32_t *>(st + L::kAS + (lane >> 4) * kMx4ScaleBlock + 16 * r) = word;
+                }
+                if (i + 1 < k1 - k0) load(k0 + i + 1);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&full[s]));
+            }
+        }
         bool ok = wait_warp(smem_u32(done), 0u, abort) && !*abort;
         tc_fence_after();
         asm volatile("griddepcontrol.wait;" ::: "memory");     // y may still be read by an earlier kernel
@@ -290,27 +346,29 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const Mx4Params p, c
     }
 }
 
-template <int TN>
+template <int TN, typename XT = void>
 cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *ac, cudaStream_t s) {
     using L = Plan<TN>;
-    auto kern = mx4_gemm_kernel<TN>;
+    auto kern = mx4_gemm_kernel<TN, XT>;
     static int attr_done[4] = {0, 0, 0, 0};
     cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
     if (e != cudaSuccess) return e;
-    const int64_t tiles = (p.N + kRows - 1) / kRows, toks = (p.M + TN - 1) / TN;
-    if (toks > 65535) return cudaErrorInvalidValue;
-    // K is shared until there are about three CTAs an SM, each with two stages at least
+    const int64_t tiles = (p.N + kRows - 1) / kRows;
+    // K is shared while all CTAs are on the GPU at once, each with two stages at least
+    const int64_t slots = 152 * (int64_t)(L::kSmem <= 113 * 1024 ? 2 : 1);
     p.split = 1;
-    while (p.split < kMaxSplit && 2 * p.split <= TN && tiles * toks * p.split < 304 && p.nk >= 4 * p.split) p.split *= 2;
+    while (p.split < kMaxSplit && 2 * p.split <= TN && 2 * tiles * p.split <= slots && p.nk >= 4 * p.split) p.split *= 2;
     alignas(64) CUtensorMap wm, am;
     e = make_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, wc, (uint64_t)(K / 2), (uint64_t)p.N, (uint64_t)(K / 2), 128, kRows,
                     CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
-    e = make_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, ac, (uint64_t)(K / 2), (uint64_t)p.M, (uint64_t)(K / 2), 128, TN,
-                    CU_TENSOR_MAP_SWIZZLE_128B);
+    am = wm;                                                     // not read by a fused kernel
+    if (ac)
+        e = make_map_2d(&am, CU_TENSOR_MAP_DATA_TYPE_UINT8, ac, (uint64_t)(K / 2), (uint64_t)p.M, (uint64_t)(K / 2), 128, TN,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(tiles * p.split), (unsigned)toks, 1);
+    cfg.gridDim = dim3((unsigned)(tiles * p.split), 1, 1);
     cfg.blockDim = dim3(kThreads, 1, 1);
     cfg.dynamicSmemBytes = L::kSmem;
     cfg.stream = s;
@@ -366,6 +424,14 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, u
         " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok != 0;
 }
 // An arrival on the barrier at this offset in both CTAs, once the products issued so far are done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
@@ -471,9 +537,41 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
             bool ok = true;
             constexpr uint32_t id0 = idesc_mxf4(kPairTok, 0) + ((uint32_t)(kRows >> 4) << 24);      // 256 rows
             constexpr uint32_t id1 = idesc_mxf4(kPairTok, 1) + ((uint32_t)(kRows >> 4) << 24);
-            // The products of a stage are issued after the scale copies of the next one, which they hide.
-            auto products = [&](int i, int k) {
-                const int s = i % S, steps = k == p.nk - 1 ? p.last_steps : 4;
+            auto scales = [&](int i) {
+                const int s = i % S;
+                const uint32_t st = smem_u32(smem + s * L::kStageBytes), cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t c = cols + (uint32_t)(h * L::kHalfCols);
+                    copy_scales_pair(c, smem_desc_scales(st + L::kWS + h * kMx4ScaleBlock));
+                    copy_scales_pair(c + 4, smem_desc_scales(st + L::kAS + h * kMx4ScaleBlock));
+                    copy_scales_pair(c + 8, smem_desc_scales(st + L::kAS + (2 + h) * kMx4ScaleBlock));
+                }
+            };
+            const int mine = (p.tiles - pair + pairs - 1) / pairs, total = mine * p.nk;
+            int copied = 0, k = 0;                              // stages whose scales are on their way
+            for (; it < total; ++it) {
+                const int s = it % S;
+                if (copied <= it) {
+                    if (!wait_bounded(smem_u32(&full[s]), (uint32_t)((it / S) & 1), abort)) { ok = false; break; }
+                    tc_fence_after();
+                    scales(it);
+                    copied = it + 1;
+                }
+                // the next stage's scales go ahead of this one's products, which hide them, if it is here
+                if (it + 1 < total && mbar_test(smem_u32(&full[(it + 1) % S]), (uint32_t)(((it + 1) / S) & 1))) {
+                    tc_fence_after();
+                    scales(it + 1);
+                    copied = it + 2;
+                }
+                if (k == 0) {
+                    if (!wait_cluster_bounded(smem_u32(acc_empty), (uint32_t)((done & 1) ^ 1), abort, &g_mx4_status, kWaitLimitNs)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                }
+                const int steps = k == p.nk - 1 ? p.last_steps : 4;
                 const uint32_t st = smem_u32(smem + s * L::kStageBytes), cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -483,31 +581,10 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
                                   c, c + 4, k > 0 || q > 0 ? 1u : 0u);
                 }
                 mma_commit_pair(smem_u32(&empty[s]));
-            };
-            for (int tile = pair; tile < p.tiles && ok; tile += pairs, ++done) {
-                for (int k = 0; k < p.nk; ++k, ++it) {
-                    const int s = it % S;
-                    if (!wait_bounded(smem_u32(&full[s]), (uint32_t)((it / S) & 1), abort)) { ok = false; break; }
-                    tc_fence_after();
-                    const uint32_t st = smem_u32(smem + s * L::kStageBytes), cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint32_t c = cols + (uint32_t)(h * L::kHalfCols);
-                        copy_scales_pair(c, smem_desc_scales(st + L::kWS + h * kMx4ScaleBlock));
-                        copy_scales_pair(c + 4, smem_desc_scales(st + L::kAS + h * kMx4ScaleBlock));
-                        copy_scales_pair(c + 8, smem_desc_scales(st + L::kAS + (2 + h) * kMx4ScaleBlock));
-                    }
-                    if (k > 0) products(it - 1, k - 1);
-                    else if (!wait_cluster_bounded(smem_u32(acc_empty), (uint32_t)((done & 1) ^ 1), abort, &g_mx4_status, kWaitLimitNs)) {
-                        ok = false;
-                        break;
-                    } else {
-                        tc_fence_after();
-                    }
-                }
-                if (ok) {
-                    products(it - 1, p.nk - 1);
+                if (++k == p.nk) {
                     mma_commit_pair(smem_u32(acc_full));
+                    k = 0;
+                    ++done;
                 }
             }
             if (!ok) {
@@ -603,26 +680,42 @@ cudaError_t launch_pairs(const Mx4Params &q, const uint8_t *wc, int64_t K, const
 
 }  // namespace
 
-cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
-                              int64_t M, qmm_dtype t, void *y, int64_t ldy, int early_weights, cudaStream_t s) {
+static Mx4Params make_params(const uint8_t *ws, int64_t K, int64_t N, int64_t M, qmm_dtype t, void *y, int64_t ldy) {
     Mx4Params p = {};
     p.ws = ws;
-    p.as = as;
     p.y = y;
     p.N = N;
     p.M = M;
     p.ldy = ldy;
+    p.K = K;
     p.n128 = (int)((K + 127) / 128);
     p.nk = (int)((K + 255) / 256);
     p.last_steps = (int)((K - (int64_t)(p.nk - 1) * 256 + 63) / 64);
     p.m_blocks = (int)((M + 127) / 128);
-    p.early_weights = early_weights;
     p.dtype = (int)t;
+    return p;
+}
+
+cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
+                              int64_t M, qmm_dtype t, void *y, int64_t ldy, int early_weights, cudaStream_t s) {
+    Mx4Params p = make_params(ws, K, N, M, t, y, ldy);
+    p.as = as;
+    p.early_weights = early_weights;
     if (M <= 16) return launch_tn<16>(p, wc, K, ac, s);
     if (M <= 32) return launch_tn<32>(p, wc, K, ac, s);
     if (M <= 64) return launch_tn<64>(p, wc, K, ac, s);
     if (M <= 128) return launch_tn<128>(p, wc, K, ac, s);
     return launch_pairs(p, wc, K, ac, s);
+}
+
+cudaError_t launch_mx4_linear_few(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, qmm_dtype xt, const void *x, int64_t ldx,
+                                  int64_t M, qmm_dtype t, void *y, int64_t ldy, cudaStream_t s) {
+    Mx4Params p = make_params(ws, K, N, M, t, y, ldy);
+    p.early_weights = 1;
+    p.x = x;
+    p.ldx = ldx;
+    p.x_vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx * (int64_t)dtype_bytes(xt)) % 16 == 0;
+    return with_dtype(xt, [&](auto z) { return launch_tn<kMx4FusedTokens, decltype(z)>(p, wc, K, nullptr, s); });
 }
 
 cudaError_t read_and_clear_mx4_status(unsigned *out, cudaStream_t s) {

@@ -324,6 +324,9 @@ qmm_status qmm_mx4_linear(const void *w_codes, const void *w_scales, int64_t K, 
     uint8_t *codes = static_cast<uint8_t *>(workspace), *scales = codes + round256(mx4_codes_bytes(M, K));
     st = check_mx4_rows(xdt, x, M, K, ldx, codes, scales);
     if (st != QMM_OK) return st;
+    if (M <= kMx4FusedTokens)
+        return from_cuda(launch_mx4_linear_few(static_cast<const uint8_t *>(w_codes), static_cast<const uint8_t *>(w_scales), K, N, xdt,
+                                               x, ldx, M, ydt, y, ldy, cs(stream)));
     const cudaError_t e = launch_mx4_quantize(xdt, x, M, K, ldx, codes, scales, 1, cs(stream));
     if (e != cudaSuccess) return from_cuda(e);
     // the grid before the product is the quantization, which waited for everything before it and writes no weight

@@ -219,6 +219,10 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                   int64_t ldy, cudaStream_t s);
 cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
                               int64_t M, qmm_dtype t, void *y, int64_t ldy, int early_weights, cudaStream_t s);
+// Up to kMx4FusedTokens rows, quantized inside the product's kernel.
+constexpr int kMx4FusedTokens = 16;
+cudaError_t launch_mx4_linear_few(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, qmm_dtype xt, const void *x, int64_t ldx,
+                                  int64_t M, qmm_dtype t, void *y, int64_t ldy, cudaStream_t s);
 cudaError_t read_and_clear_mx4_status(unsigned *out, cudaStream_t s);
 cudaError_t launch_cache_write(qmm_type type, qmm_dtype t, const void *k, const void *v, int64_t ldk, int64_t ldv, int64_t T,
                                int H, int D, const int64_t *slots, uint8_t *k_cache, uint8_t *v_cache, int64_t n_pages, int P,
