@@ -52,7 +52,6 @@ struct Mx4Params {
     int n128;                              // K / 128, rounded up: scale blocks of a row of blocks
     int nk;                                // stages: K / 256, rounded up
     int last_steps;                        // K = 64 products of the last stage (1 to 4)
-    int m_blocks;                          // row blocks of the activations' scales
     int split;                             // CTAs of a cluster, which share a tile's K
     int early_weights;                     // the weight may be read before the kernel before this one is done
     int dtype;
@@ -91,19 +90,37 @@ __device__ __forceinline__ constexpr uint32_t idesc_mxf4(int n, int half) {
            ((uint32_t)(2 * half) << 29) | ((uint32_t)(2 * half) << 4);
 }
 
+// One thread of the (converged) warp, the same each time.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok));
+    return ok != 0;
+}
+// A place in the ring and the phase of its barriers, kept without divisions: the threads that issue copies
+// and products have some 500 cycles a stage.
+template <int S>
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++s == S) {
+            s = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 template <int TN>
 struct Plan {
-    static constexpr int kTokBlocks = (TN + 127) / 128;                  // 128-row blocks of token scales
     static constexpr int kW = 0;
     static constexpr int kA = kW + kRows * 128;
     static constexpr int kWS = kA + (TN * 128 + 1023) / 1024 * 1024;
     static constexpr int kAS = kWS + 2 * kMx4ScaleBlock;
-    static constexpr int kStageBytes = kAS + kTokBlocks * 2 * kMx4ScaleBlock;
+    static constexpr int kStageBytes = kAS + 2 * kMx4ScaleBlock;
     static constexpr int kStages = TN >= 64 ? 3 : 5;                     // two CTAs an SM up to 64 tokens
-    // tensor memory: the sums, then per stage the scales of two K = 128 halves (weight 4 columns, tokens 4
-    // columns per block)
+    // tensor memory: the sums, then per stage the scales of two K = 128 halves (weight 4 columns, tokens 4)
     static constexpr int kSums = TN < 32 ? 32 : TN;
-    static constexpr int kHalfCols = 4 + 4 * kTokBlocks;
+    static constexpr int kHalfCols = 8;
     static constexpr int kColsUsed = kSums + kStages * 2 * kHalfCols;
     static constexpr int kCols = kColsUsed <= 128 ? 128 : (kColsUsed <= 256 ? 256 : 512);
     // parts of the other CTAs of a cluster: [rank][token of this CTA's share][row]
@@ -140,7 +157,6 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
     const int64_t tile = blockIdx.x / (unsigned)p.split;
     const int64_t n0 = tile * kRows, m0 = 0;                     // one tile of tokens
     const int k0 = (int)((int64_t)p.nk * rank / p.split), k1 = (int)((int64_t)p.nk * (rank + 1) / p.split);
-    const int tok_blocks = min(L::kTokBlocks, p.m_blocks - (int)(m0 / 128));
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -176,7 +192,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
                 const uint32_t st = smem_u32(smem + s * L::kStageBytes), bar = smem_u32(&full[s]);
                 const uint32_t sb = (uint32_t)blocks(k) * kMx4ScaleBlock;
                 mbar_arrive_expect_tx(bar, kFused ? (uint32_t)(kRows * 128) + sb
-                                                  : (uint32_t)(kRows * 128 + TN * 128) + sb * (uint32_t)(1 + tok_blocks));
+                                                  : (uint32_t)(kRows * 128 + TN * 128) + 2 * sb);
                 tma_load_2d(st + L::kW, &w_map, k * 128, (int)n0, bar);
                 bulk_g2s(st + L::kWS, p.ws + (tile * p.n128 + 2 * k) * (int64_t)kMx4ScaleBlock, sb, bar);
             };
@@ -185,9 +201,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
                 const uint32_t st = smem_u32(smem + s * L::kStageBytes), bar = smem_u32(&full[s]);
                 const uint32_t sb = (uint32_t)blocks(k) * kMx4ScaleBlock;
                 tma_load_2d(st + L::kA, &a_map, k * 128, (int)m0, bar);
-                for (int b = 0; b < tok_blocks; ++b)
-                    bulk_g2s(st + L::kAS + b * 2 * kMx4ScaleBlock,
-                             p.as + ((m0 / 128 + b) * p.n128 + 2 * k) * (int64_t)kMx4ScaleBlock, sb, bar);
+                bulk_g2s(st + L::kAS, p.as + 2 * k * (int64_t)kMx4ScaleBlock, sb, bar);
             };
             asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&w_map)) : "memory");
             if (!kFused) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&a_map)) : "memory");
@@ -208,32 +222,36 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
-            for (int i = 0; i < k1 - k0; ++i) {
-                const int s = i % S, k = k0 + i;
-                if (!wait_bounded(smem_u32(&full[s]), (uint32_t)((i / S) & 1), abort)) break;
-                tc_fence_after();
-                const uint32_t st = smem_u32(smem + s * L::kStageBytes);
-                const uint32_t cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
-                const int steps = k == p.nk - 1 ? p.last_steps : 4;
+        const bool lead = elect_one();
+        const uint32_t st0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+        const uint64_t w_desc = smem_desc_sw128(st0 + L::kW), a_desc = smem_desc_sw128(st0 + L::kA);
+        const uint64_t ws_desc = smem_desc_scales(st0 + L::kWS), as_desc = smem_desc_scales(st0 + L::kAS);
+        constexpr int kHalf = kMx4ScaleBlock >> 4;                 // in units of a descriptor's address
+        Ring<S> r;
+        for (int k = k0; k < k1; ++k, r.next()) {
+            if (!wait_warp(full0 + 8 * r.s, r.phase, abort)) break;
+            tc_fence_after();
+            const uint64_t off = (uint64_t)(uint32_t)(r.s * (L::kStageBytes >> 4));
+            const uint32_t cols = tmem + (uint32_t)(L::kSums + r.s * 2 * L::kHalfCols);
+            const int steps = k == p.nk - 1 ? p.last_steps : 4;
+            if (lead) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if (2 * h >= steps) break;
-                    const uint32_t c = cols + (uint32_t)(h * L::kHalfCols);
-                    copy_scales(c, smem_desc_scales(st + L::kWS + h * kMx4ScaleBlock));
-#pragma unroll
-                    for (int b = 0; b < L::kTokBlocks; ++b)
-                        copy_scales(c + 4 + 4 * b, smem_desc_scales(st + L::kAS + (2 * b + h) * kMx4ScaleBlock));
+                    copy_scales(cols + h * L::kHalfCols, ws_desc + off + h * kHalf);
+                    copy_scales(cols + h * L::kHalfCols + 4, as_desc + off + h * kHalf);
                 }
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    if (q >= steps) break;
                     const uint32_t c = cols + (uint32_t)((q >> 1) * L::kHalfCols);
-                    mma_mxf4(tmem, smem_desc_sw128(st + L::kW + 32 * q), smem_desc_sw128(st + L::kA + 32 * q), idesc_mxf4(TN, q & 1), c,
-                             c + 4, i > 0 || q > 0 ? 1u : 0u);
+                    if (q < steps)
+                        mma_mxf4(tmem, w_desc + off + 2 * q, a_desc + off + 2 * q, idesc_mxf4(TN, q & 1), c, c + 4,
+                                 q > 0 ? 1u : (k > k0 ? 1u : 0u));
                 }
-                mma_commit(smem_u32(&empty[s]));
+                mma_commit(empty0 + 8 * r.s);
             }
+            __syncwarp();
+        }
+        if (lead) {
             mma_commit(smem_u32(done));
             wait_drain(smem_u32(done), 0u);
         }
@@ -388,13 +406,12 @@ cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *
 // Many tokens: pairs of CTAs (cta_group::2) share a tile of 256 weight rows x 256 tokens.  Each CTA holds
 // 128 of the weight rows and 128 of the tokens, and the pair's instruction reads both halves of the
 // tokens, so that a byte brought into shared memory takes part in twice the products of a single CTA's
-// tile.  The pairs stay on their SMs and take tiles in turn (tokens fastest, so that the pairs of a moment
-// share weight rows).  The eight result warps of a CTA read a finished tile into registers, 128 sums a
+// tile.  The pairs stay on their SMs and take tiles in turn.  The eight result warps of a CTA read a finished tile into registers, 128 sums a
 // thread, which frees the accumulator for the next tile before the first result is stored.
 // ---------------------------------------------------------------------------------------------
 constexpr int kPairTok = 256;              // tokens of a pair's tile
 struct Pair {
-    static constexpr int kStages = 5;
+    static constexpr int kStages = 6;
     static constexpr int kW = 0;
     static constexpr int kA = kRows * 128;
     static constexpr int kWS = kA + kPairTok / 2 * 128;
@@ -424,14 +441,6 @@ __device__ __forceinline__ void mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, u
         " tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n}\n" ::"r"(d_tmem),
         "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa), "r"(sb), "r"(accumulate)
         : "memory");
-}
-__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
-                 : "=r"(ok)
-                 : "r"(bar), "r"(parity)
-                 : "memory");
-    return ok != 0;
 }
 // An arrival on the barrier at this offset in both CTAs, once the products issued so far are done.
 __device__ __forceinline__ void mma_commit_pair(uint32_t bar) {
@@ -466,7 +475,14 @@ struct PairParams {
     void *y;
     int64_t N, M, ldy;
     int n128, nk, last_steps;
-    int m_tiles, tiles;
+    int m_tiles, n_tiles, tiles;
+    // Tiles run through bands of 8 weight tiles, in a band through the tokens: the 76 tiles of a moment are some
+    // 8 x 10, so that each byte of either operand is asked for by 8 or 10 pairs at about the same time.
+    __device__ __forceinline__ void place(int tile, int &mt, int &nt) const {
+        const int band = tile / (8 * m_tiles), in = tile - band * 8 * m_tiles, wide = min(8, n_tiles - 8 * band);
+        mt = in / wide;
+        nt = 8 * band + in - mt * wide;
+    }
 };
 
 template <typename T>
@@ -509,22 +525,25 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
     if (warp == 0) {
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
-            int it = 0;
+            Ring<S> r;
+            const uint32_t st0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+            const uint32_t lead0 = peer_addr(full0, 0u);                   // the leader's, for both CTAs' copies
             bool ok = true;
+            int it = 0;
             for (int tile = pair; tile < p.tiles && ok; tile += pairs) {
-                const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
-                const int row0 = nt * 2 * kRows + rank * kRows, tok0 = mt * kPairTok;
-                for (int k = 0; k < p.nk; ++k, ++it) {
-                    const int s = it % S;
-                    if (!wait_bounded(smem_u32(&empty[s]), (uint32_t)(((it / S) & 1) ^ 1), abort)) { ok = false; break; }
-                    const uint32_t st = smem_u32(smem + s * L::kStageBytes);
-                    const uint32_t bar = peer_addr(smem_u32(&full[s]), 0u);        // the leader's, for both CTAs' copies
-                    if (rank == 0) mbar_arrive_expect_tx(smem_u32(&full[s]), 2 * L::kStageBytes);
+                int mt, nt;
+                p.place(tile, mt, nt);
+                const int row0 = nt * 2 * kRows + rank * kRows, tok0 = mt * kPairTok + rank * (kPairTok / 2);
+                const int wb = (nt * 2 + rank) * p.n128, ab = mt * 2 * p.n128;
+                for (int k = 0; k < p.nk; ++k, ++it, r.next()) {
+                    if (!wait_bounded(empty0 + 8 * r.s, r.phase ^ 1u, abort)) { ok = false; break; }
+                    const uint32_t st = st0 + (uint32_t)(r.s * L::kStageBytes), bar = lead0 + 8 * r.s;
+                    if (rank == 0) mbar_arrive_expect_tx(full0 + 8 * r.s, 2 * L::kStageBytes);
                     tma_load_2d_pair(st + L::kW, &w_map, k * 128, row0, bar);
-                    tma_load_2d_pair(st + L::kA, &a_map, k * 128, tok0 + rank * (kPairTok / 2), bar);
-                    tma_load_2d_pair(st + L::kWS, &ws_map, 0, (nt * 2 + rank) * p.n128 + 2 * k, bar);
-                    tma_load_2d_pair(st + L::kAS, &as_map, 0, (mt * 2) * p.n128 + 2 * k, bar);
-                    tma_load_2d_pair(st + L::kAS + 2 * kMx4ScaleBlock, &as_map, 0, (mt * 2 + 1) * p.n128 + 2 * k, bar);
+                    tma_load_2d_pair(st + L::kA, &a_map, k * 128, tok0, bar);
+                    tma_load_2d_pair(st + L::kWS, &ws_map, 0, wb + 2 * k, bar);
+                    tma_load_2d_pair(st + L::kAS, &as_map, 0, ab + 2 * k, bar);
+                    tma_load_2d_pair(st + L::kAS + 2 * kMx4ScaleBlock, &as_map, 0, ab + p.n128 + 2 * k, bar);
                 }
             }
             // every stage has been read, and the arrivals that say so have reached this CTA
@@ -532,62 +551,53 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
-            int it = 0, done = 0;
-            bool ok = true;
+        if (rank == 0) {
+            // the warp walks the stages together, so that addresses stay in uniform registers; one thread issues
+            const bool lead = elect_one();
+            const uint32_t st0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
+            const uint64_t w_desc = smem_desc_sw128(st0 + L::kW), a_desc = smem_desc_sw128(st0 + L::kA);
+            const uint64_t ws_desc = smem_desc_scales(st0 + L::kWS), as_desc = smem_desc_scales(st0 + L::kAS);
             constexpr uint32_t id0 = idesc_mxf4(kPairTok, 0) + ((uint32_t)(kRows >> 4) << 24);      // 256 rows
             constexpr uint32_t id1 = idesc_mxf4(kPairTok, 1) + ((uint32_t)(kRows >> 4) << 24);
-            auto scales = [&](int i) {
-                const int s = i % S;
-                const uint32_t st = smem_u32(smem + s * L::kStageBytes), cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t c = cols + (uint32_t)(h * L::kHalfCols);
-                    copy_scales_pair(c, smem_desc_scales(st + L::kWS + h * kMx4ScaleBlock));
-                    copy_scales_pair(c + 4, smem_desc_scales(st + L::kAS + h * kMx4ScaleBlock));
-                    copy_scales_pair(c + 8, smem_desc_scales(st + L::kAS + (2 + h) * kMx4ScaleBlock));
-                }
-            };
-            const int mine = (p.tiles - pair + pairs - 1) / pairs, total = mine * p.nk;
-            int copied = 0, k = 0;                              // stages whose scales are on their way
-            for (; it < total; ++it) {
-                const int s = it % S;
-                if (copied <= it) {
-                    if (!wait_bounded(smem_u32(&full[s]), (uint32_t)((it / S) & 1), abort)) { ok = false; break; }
-                    tc_fence_after();
-                    scales(it);
-                    copied = it + 1;
-                }
-                // the next stage's scales go ahead of this one's products, which hide them, if it is here
-                if (it + 1 < total && mbar_test(smem_u32(&full[(it + 1) % S]), (uint32_t)(((it + 1) / S) & 1))) {
-                    tc_fence_after();
-                    scales(it + 1);
-                    copied = it + 2;
-                }
-                if (k == 0) {
-                    if (!wait_cluster_bounded(smem_u32(acc_empty), (uint32_t)((done & 1) ^ 1), abort, &g_mx4_status, kWaitLimitNs)) {
-                        ok = false;
-                        break;
+            constexpr int kHalf = kMx4ScaleBlock >> 4;             // in units of a descriptor's address
+            bool ok = true;
+            uint32_t acc_phase = 1;
+            Ring<S> r;
+            for (int tile = pair; tile < p.tiles && ok; tile += pairs) {
+                for (int k = 0; k < p.nk; ++k, r.next()) {
+                    if (!wait_warp(full0 + 8 * r.s, r.phase, abort)) { ok = false; break; }
+                    if (k == 0) {
+                        if (!__all_sync(0xffffffffu, wait_cluster_bounded(smem_u32(acc_empty), acc_phase, abort, &g_mx4_status, kWaitLimitNs))) {
+                            ok = false;
+                            break;
+                        }
+                        acc_phase ^= 1u;
                     }
                     tc_fence_after();
-                }
-                const int steps = k == p.nk - 1 ? p.last_steps : 4;
-                const uint32_t st = smem_u32(smem + s * L::kStageBytes), cols = tmem + (uint32_t)(L::kSums + s * 2 * L::kHalfCols);
+                    const uint64_t off = (uint64_t)(uint32_t)(r.s * (L::kStageBytes >> 4));
+                    const uint32_t cols = tmem + (uint32_t)(L::kSums + r.s * 2 * L::kHalfCols);
+                    const int steps = k == p.nk - 1 ? p.last_steps : 4;
+                    if (lead) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    if (q >= steps) break;
-                    const uint32_t c = cols + (uint32_t)((q >> 1) * L::kHalfCols);
-                    mma_mxf4_pair(tmem, smem_desc_sw128(st + L::kW + 32 * q), smem_desc_sw128(st + L::kA + 32 * q), (q & 1) ? id1 : id0,
-                                  c, c + 4, k > 0 || q > 0 ? 1u : 0u);
-                }
-                mma_commit_pair(smem_u32(&empty[s]));
-                if (++k == p.nk) {
-                    mma_commit_pair(smem_u32(acc_full));
-                    k = 0;
-                    ++done;
+                        for (int h = 0; h < 2; ++h) {
+                            copy_scales_pair(cols + h * L::kHalfCols, ws_desc + off + h * kHalf);
+                            copy_scales_pair(cols + h * L::kHalfCols + 4, as_desc + off + h * kHalf);
+                            copy_scales_pair(cols + h * L::kHalfCols + 8, as_desc + off + (2 + h) * kHalf);
+                        }
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const uint32_t c = cols + (uint32_t)((q >> 1) * L::kHalfCols);
+                            if (q < steps)
+                                mma_mxf4_pair(tmem, w_desc + off + 2 * q, a_desc + off + 2 * q, (q & 1) ? id1 : id0, c, c + 4,
+                                              q > 0 ? 1u : (k > 0 ? 1u : 0u));
+                        }
+                        mma_commit_pair(empty0 + 8 * r.s);
+                        if (k == p.nk - 1) mma_commit_pair(smem_u32(acc_full));
+                    }
+                    __syncwarp();
                 }
             }
-            if (!ok) {
+            if (!ok && lead) {
                 // lets the products in flight finish and both CTAs go on to their end
                 mma_commit_pair(smem_u32(acc_full));
                 for (int s = 0; s < S; ++s) mma_commit_pair(smem_u32(&empty[s]));
@@ -611,7 +621,8 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_peer(free_bar);
-            const int mt = tile % p.m_tiles, nt = tile / p.m_tiles;
+            int mt, nt;
+            p.place(tile, mt, nt);
             const int64_t n = (int64_t)nt * 2 * kRows + rank * kRows + row, m0 = (int64_t)mt * kPairTok + half * (kPairTok / 2);
             const int have = (int)min((int64_t)(kPairTok / 2), p.M - m0);
             if (n < p.N) {
@@ -634,10 +645,11 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
 }
 
 cudaError_t launch_pairs(const Mx4Params &q, const uint8_t *wc, int64_t K, const uint8_t *ac, cudaStream_t s) {
-    PairParams p = {q.y, q.N, q.M, q.ldy, q.n128, q.nk, q.last_steps, 0, 0};
+    PairParams p = {q.y, q.N, q.M, q.ldy, q.n128, q.nk, q.last_steps, 0, 0, 0};
     const int64_t mt = (p.M + kPairTok - 1) / kPairTok, nt = (p.N + 2 * kRows - 1) / (2 * kRows);
     if (mt * nt > 0x3fffffff) return cudaErrorInvalidValue;
     p.m_tiles = (int)mt;
+    p.n_tiles = (int)nt;
     p.tiles = (int)(mt * nt);
     alignas(64) CUtensorMap wm, am, wsm, asm_;
     cudaError_t e = make_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, wc, (uint64_t)(K / 2), (uint64_t)p.N, (uint64_t)(K / 2), 128, kRows,
@@ -691,7 +703,6 @@ static Mx4Params make_params(const uint8_t *ws, int64_t K, int64_t N, int64_t M,
     p.n128 = (int)((K + 127) / 128);
     p.nk = (int)((K + 255) / 256);
     p.last_steps = (int)((K - (int64_t)(p.nk - 1) * 256 + 63) / 64);
-    p.m_blocks = (int)((M + 127) / 128);
     p.dtype = (int)t;
     return p;
 }
