@@ -4,89 +4,88 @@
 // The rules are those of the library's Q8_0 activations and Q4_0 weights, but that the Q8_0 scale is
 // max|x| times the fp32 nearest to 1/127; a block is 32 elements of one head of one token.  A block whose scale is not a finite fp16 (an infinity or a NaN among its
 // elements, or values beyond the format) is stored with a NaN scale and reads back as NaN, so that
-// nothing turns into a finite value on the way.  Both kernels move each byte once and are bound by
-// memory: four lanes to a block, 8 elements to a lane.
+// nothing turns into a finite value on the way.  Both kernels move each byte once; what costs beside the
+// bytes is instructions.  A lane takes 16 elements, half a block.
 #include <type_traits>
 
 #include "cache.cuh"
 #include "elem.cuh"
+#include "tc_common.cuh"
 
 namespace qmm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBatch = 4;                   // pieces of 8 elements that a thread loads before it works on the first
+constexpr int kBatch = 2;                   // pieces of 16 elements that a thread loads before it works on the first
 constexpr float kInv127 = 1.0f / 127.0f;    // rounded once: the Q8_0 scale is a product, not a quotient
 
 // The low bits of 2^23 + v rounded towards zero are trunc(v), 0 <= v < 2^23: an addition where a
 // conversion would take a slower pipe.
 __device__ __forceinline__ uint32_t trunc_bits(float v) { return __float_as_uint(__fadd_rz(v, 8388608.0f)); }
 
-// Codes of a lane's 8 elements and the block's scale; the four lanes of a block (and so, for the
-// shuffles, the warp) call it together.  Q8_0: 8 int8 codes in w[0..1].  Q4_0: element i in nibble i of w[0].
-template <int TYPE, typename T>
-__device__ __forceinline__ uint16_t quantize8(const Raw8<T> &raw, uint32_t (&w)[2]) {
-    float v[8];
-    raw.values(v);
-    uint32_t bits = raw.top_bits();
-    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
-    bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 2));
-    float d;
-    if constexpr (TYPE == QMM_Q8_0) {
-        d = __fmul_rn(__uint_as_float(bits), kInv127);
-    } else {
-        // its sign: the block's first element of that magnitude.  First the lane's own: bit i of at.
-        const unsigned group = 0xfu << (threadIdx.x & 28u);
-        uint32_t sign = 0;
-        bool have = false;
-#pragma unroll
-        for (int i = 7; i >= 0; --i) {
-            const uint32_t x = __float_as_uint(v[i]);
-            if ((x & 0x7FFFFFFFu) == bits) {
-                sign = x & 0x80000000u;
-                have = true;
-            }
-        }
-        const unsigned holders = __ballot_sync(0xffffffffu, have) & group;
-        const int from = holders ? __ffs((int)holders) - 1 : 0;
-        sign = __shfl_sync(0xffffffffu, sign, from);
-        d = __fmul_rn(__uint_as_float(bits | sign), -0.125f);
-    }
-    const uint16_t half = __half_as_ushort(__float2half_rn(d));
-    w[0] = w[1] = 0;
-    if (bits >= 0x7F800000u || (half & 0x7C00u) == 0x7C00u) return 0x7E00u;
-    const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
-    if (!(fabsf(id) < INFINITY)) {
-        // 1 / d overflows: element by element, with the products' infinities and NaN
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if constexpr (TYPE == QMM_Q8_0) {
-                w[i >> 2] |= (uint32_t)(q8_code(v[i], id) & 0xFF) << (8 * (i & 3));
-            } else {
-                const float q = __fadd_rn(__fmul_rn(v[i], id), 8.5f);
-                w[0] |= (uint32_t)(!(q >= 0.0f) ? 0 : (q >= 15.0f ? 15 : __float2int_rz(q))) << (4 * i);
-            }
-        }
-        return half;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float q = __fmul_rn(v[i], id);
-        if constexpr (TYPE == QMM_Q8_0) {
-            // half away from zero: trunc(|q| + 1/2), the sum rounded towards zero so that it cannot reach the next integer
-            const uint32_t m = trunc_bits(__fadd_rz(fminf(fabsf(q), 127.0f), 0.5f)), neg = (uint32_t)((int32_t)__float_as_uint(q) >> 31);
-            w[i >> 2] |= (((m ^ neg) - neg) & 0xFFu) << (8 * (i & 3));
-        } else {
-            w[0] |= (trunc_bits(fminf(fmaxf(__fadd_rn(q, 8.5f), 0.0f), 15.0f)) & 15u) << (4 * i);
-        }
-    }
-    return half;
+// Four values' low bytes as one word.
+__device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// The low 16 bits' four nibbles spread to the low nibbles of four bytes.
-__device__ __forceinline__ uint32_t spread4(uint32_t x) {
-    x = (x | (x << 8)) & 0x00FF00FFu;
-    return (x | (x << 4)) & 0x0F0F0F0Fu;
+// Codes of a lane's 16 elements, a byte each (Q4_0: 0..15), and the block's scale; the two lanes of a block
+// (and so, for the shuffles, the warp) call it together.
+template <int TYPE, typename T>
+__device__ __forceinline__ uint16_t quantize16(const Raw<T, 16> &raw, uint32_t (&w)[4]) {
+    float d;
+    if constexpr (TYPE == QMM_Q8_0) {
+        uint32_t bits = raw.top_bits();
+        bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, 1));
+        d = bits >= 0x7F800000u ? INFINITY : __fmul_rn(__uint_as_float(bits), kInv127);
+    } else {
+        int pos, neg;
+        raw.top_signed(pos, neg);
+        pos = max(pos, __shfl_xor_sync(0xffffffffu, pos, 1));
+        neg = max(neg, __shfl_xor_sync(0xffffffffu, neg, 1));
+        bool minus = neg > pos;
+        if (__any_sync(0xffffffffu, neg == pos)) {
+            // both signs reach the largest magnitude: the block's first element of it counts
+            constexpr uint32_t kSign = sizeof(T) == 4 ? 0x80000000u : 0x8000u;
+            uint32_t first = 0;                                  // the lane's: 2 found, 1 its sign
+#pragma unroll
+            for (int i = 15; i >= 0; --i) {
+                const uint32_t b = raw.bits(i);
+                if ((int)(b & ~kSign) == pos) first = 2u | (b & kSign ? 1u : 0u);
+            }
+            const uint32_t other = __shfl_xor_sync(0xffffffffu, first, 1);
+            const uint32_t lower = threadIdx.x & 1 ? other : first, upper = threadIdx.x & 1 ? first : other;
+            if (neg == pos) minus = ((lower & 2u ? lower : upper) & 1u) != 0;
+        }
+        const float m = bits_to_float<T>((uint32_t)max(pos, neg));
+        // infinities and NaN have no scale
+        d = m < INFINITY ? __fmul_rn(minus ? -m : m, -0.125f) : INFINITY;
+    }
+    const uint16_t half = __half_as_ushort(__float2half_rn(d));
+    w[0] = w[1] = w[2] = w[3] = 0;
+    if ((half & 0x7C00u) == 0x7C00u) {
+        if (TYPE == QMM_Q4_0) w[0] = w[1] = w[2] = w[3] = 0u;
+        return 0x7E00u;
+    }
+    const float id = d != 0.0f ? __frcp_rn(d) : 0.0f;
+    const bool slow = !(fabsf(id) < INFINITY);                  // 1 / d overflows: products may be infinities and NaN
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        uint32_t q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float x = __fmul_rn(raw.value(4 * c + i), id);
+            if constexpr (TYPE == QMM_Q8_0) {
+                // half away from zero: trunc(|x| + 1/2), the sum rounded towards zero so that it cannot reach the next integer
+                const uint32_t m = trunc_bits(__fadd_rz(fminf(fabsf(x), 127.0f), 0.5f)), neg = (uint32_t)((int32_t)__float_as_uint(x) >> 31);
+                q[i] = (m ^ neg) - neg;
+            } else {
+                q[i] = trunc_bits(fminf(fmaxf(__fadd_rn(x, 8.5f), 0.0f), 15.0f));
+            }
+            if (slow && isnan(x)) q[i] = 0;
+        }
+        w[c] = bytes4(q[0], q[1], q[2], q[3]);
+    }
+    return half;
 }
 
 struct WriteParams {
@@ -95,8 +94,8 @@ struct WriteParams {
     int64_t ld[2];
     const int64_t *slots;
     int64_t n_slots;
-    uint32_t items;                         // tokens * H * D / 8
-    FastDiv per_tok;                        // H * D / 8
+    uint32_t items;                         // tokens * H * D / 16
+    FastDiv per_tok;                        // H * D / 16
     int H, log_p;
 };
 
@@ -112,7 +111,7 @@ struct Place {
     __device__ __forceinline__ int64_t scale(int block) const { return chunk + (P * kCodes + (off * DB + block) * 2); }
 };
 
-// A thread takes pieces of 8 elements; blockIdx.y: 0 keys, 1 values.
+// A thread takes pieces of 16 elements; blockIdx.y: 0 keys, 1 values.
 template <int TYPE, int DB, bool VEC, typename T>
 __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_constant__ WriteParams p) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -121,44 +120,45 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
     const T *src = static_cast<const T *>(p.src[which]);
     uint8_t *cache = p.cache[which];
     const uint32_t step = gridDim.x * kThreads;
-    // items is a multiple of 4 and so is every warp's first index: the four lanes of a block are all in
-    // range or all out of it, and all 32 lanes stay in the loop for the shuffles
+    // items is even and so is every warp's first index: the two lanes of a block are both in range or both
+    // out of it, and all 32 lanes stay in the loop for the shuffles
     for (uint32_t base = blockIdx.x * kThreads + (threadIdx.x & ~31u); base < p.items; base += step * kBatch) {
-        Raw8<T> raw[kBatch];
+        Raw<T, 16> raw[kBatch];
         int64_t slot[kBatch];
+        uint32_t in_tok[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
             const uint32_t i = base + u * step + (threadIdx.x & 31u), tok = p.per_tok(i);
+            in_tok[u] = i - tok * p.per_tok.d;
             slot[u] = -1;
             raw[u].zero();
             if (i < p.items) {
                 slot[u] = p.slots[tok];
-                raw[u].template load<VEC>(src + tok * p.ld[which] + (int64_t)(i - tok * p.per_tok.d) * 8);
+                raw[u].template load<VEC>(src + tok * p.ld[which] + (int64_t)in_tok[u] * 16);
             }
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            if (base + u * step >= p.items) break;
-            const uint32_t i = base + u * step + (threadIdx.x & 31u), in_tok = i - p.per_tok(i) * p.per_tok.d;
-            uint32_t w[2];
-            const uint16_t d = quantize8<TYPE>(raw[u], w);
-            uint32_t other = 0;
-            if constexpr (TYPE == QMM_Q4_0) other = __shfl_xor_sync(0xffffffffu, w[0], 2);
-            if (slot[u] < 0 || slot[u] >= p.n_slots) continue;
-            const int h = (int)(in_tok / (4 * DB)), c = (int)(in_tok % (4 * DB));      // elements 8c .. 8c + 7 of the head
-            if (!QMM_DCHECK(h < p.H)) continue;
-            const Place<TYPE, DB> at(slot[u] >> p.log_p, h, p.H, (int)(slot[u] & ((1 << p.log_p) - 1)), p.log_p);
-            if constexpr (TYPE == QMM_Q8_0) {
-                *reinterpret_cast<uint2 *>(cache + at.codes(c >> 2, 8 * (c & 3))) = make_uint2(w[0], w[1]);
-            } else {
-                // lanes 0, 1 hold elements 0..15 of the block, lanes 2, 3 elements 16..31; bytes 8 (lane & 1)
-                // .. + 7 pair them: the lower lane writes the first four, the upper lane the others
-                const bool upper = (c & 2) != 0;
-                const uint32_t lo = upper ? other >> 16 : w[0], hi = upper ? w[0] >> 16 : other;
-                *reinterpret_cast<uint32_t *>(cache + at.codes(c >> 2, (c & 1) * 8 + (upper ? 4 : 0))) =
-                    spread4(lo & 0xFFFFu) | (spread4(hi & 0xFFFFu) << 4);
+            uint32_t w[4];
+            const uint16_t d = quantize16<TYPE>(raw[u], w);
+            uint32_t o0 = 0, o1 = 0;
+            const bool upper = threadIdx.x & 1;                  // elements 16..31 of the block
+            if constexpr (TYPE == QMM_Q4_0) {
+                // byte j pairs elements j and j + 16: the lower lane writes bytes 0..7, the upper lane 8..15
+                o0 = __shfl_xor_sync(0xffffffffu, upper ? w[0] : w[2], 1);
+                o1 = __shfl_xor_sync(0xffffffffu, upper ? w[1] : w[3], 1);
             }
-            if ((c & 3) == 0) *reinterpret_cast<uint16_t *>(cache + at.scale(c >> 2)) = d;
+            if (slot[u] < 0 || slot[u] >= p.n_slots) continue;
+            const int h = (int)(in_tok[u] / (2 * DB)), c = (int)(in_tok[u] % (2 * DB));      // elements 16c .. 16c + 15 of the head
+            if (!QMM_DCHECK(h < p.H)) continue;
+            const Place<TYPE, DB> at(slot[u] >> p.log_p, h, p.H, (int)slot[u] & ((1 << p.log_p) - 1), p.log_p);
+            if constexpr (TYPE == QMM_Q8_0) {
+                *reinterpret_cast<uint4 *>(cache + at.codes(c >> 1, 16 * (c & 1))) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                *reinterpret_cast<uint2 *>(cache + at.codes(c >> 1, 8 * (c & 1))) =
+                    upper ? make_uint2(o0 | (w[2] << 4), o1 | (w[3] << 4)) : make_uint2(w[0] | (o0 << 4), w[1] | (o1 << 4));
+            }
+            if (!upper) *reinterpret_cast<uint16_t *>(cache + at.scale(c >> 1)) = d;
         }
     }
 }
@@ -171,7 +171,7 @@ struct ReadParams {
     int64_t ld_pages, n_pages;
     const int32_t *starts;
     int64_t n_seq, T;
-    FastDiv per_tok;                        // H * D / 8
+    FastDiv per_tok;                        // H * D / 16
     int H, log_p;
 };
 constexpr int kReadTokens = 32;             // tokens a CTA looks up at a time
@@ -186,7 +186,47 @@ __device__ __forceinline__ int64_t find_seq(const int32_t *starts, int64_t n_seq
     return lo;
 }
 
-// A CTA takes 32 tokens: one warp finds their pages, then a thread takes pieces of 8 elements;
+// Codes times scale, rounded to T: exact in fp32 (8 by 11 bits), so one rounding either way.  q: two
+// half2 words of four codes.
+template <typename T>
+__device__ __forceinline__ void scale4(uint32_t q01, uint32_t q23, uint32_t d2, uint32_t *w) {
+    if constexpr (std::is_same<T, __half>::value) {
+        w[0] = tc::h2_bits(__hmul2(tc::bits_h2(q01), tc::bits_h2(d2)));
+        w[1] = tc::h2_bits(__hmul2(tc::bits_h2(q23), tc::bits_h2(d2)));
+    } else {
+        const float d = __low2float(tc::bits_h2(d2));
+        const float2 a = __half22float2(tc::bits_h2(q01)), b = __half22float2(tc::bits_h2(q23));
+        if constexpr (sizeof(T) == 4) {
+            w[0] = __float_as_uint(a.x * d);
+            w[1] = __float_as_uint(a.y * d);
+            w[2] = __float_as_uint(b.x * d);
+            w[3] = __float_as_uint(b.y * d);
+        } else {
+            w[0] = pack2(a.x * d, a.y * d, T{});
+            w[1] = pack2(b.x * d, b.y * d, T{});
+        }
+    }
+}
+
+// Words of N elements of T at p.
+template <bool VEC, int N, typename T>
+__device__ __forceinline__ void store_words(T *p, const uint32_t *w) {
+    constexpr int kWords = N * (int)sizeof(T) / 4;
+    if constexpr (VEC && kWords == 4) {
+        *reinterpret_cast<uint4 *>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else if constexpr (VEC) {
+#pragma unroll
+        for (int i = 0; i < kWords / 8; ++i) st32(reinterpret_cast<uint32_t *>(p) + 8 * i, w + 8 * i);
+    } else if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) reinterpret_cast<uint32_t *>(p)[i] = w[i];
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) reinterpret_cast<uint16_t *>(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    }
+}
+
+// A CTA takes 32 tokens: one warp finds their pages, then a thread takes pieces of 16 elements;
 // blockIdx.y: 0 keys, 1 values.  A token that no valid page holds reads as 0.
 template <int TYPE, int DB, bool VEC, typename T>
 __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_constant__ ReadParams p) {
@@ -216,39 +256,57 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
         __syncthreads();
         const uint32_t items = (uint32_t)min((int64_t)kReadTokens, p.T - t0) * p.per_tok.d;
         for (uint32_t base = threadIdx.x; base < items; base += kThreads * kBatch) {
-            uint2 w[kBatch];
+            // Q8_0: 16 codes in a row.  Q4_0: 8 bytes, elements 8v .. 8v + 7 of a block in the low nibbles and
+            // 16 + 8v .. in the high ones, v = the piece's place in its block
+            uint4 w[kBatch];
             uint16_t d[kBatch];
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const uint32_t i = base + u * kThreads, tok = p.per_tok(i), in_tok = i - tok * p.per_tok.d;
-                // codes and scale of a zero (Q4_0: 8 is 0)
-                w[u] = TYPE == QMM_Q8_0 ? make_uint2(0u, 0u) : make_uint2(0x88888888u, 0x88888888u);
-                d[u] = 0;
+                w[u] = make_uint4(0u, 0u, 0u, 0u);
+                d[u] = 0;                                        // any code times 0
                 if (i < items && s_page[tok] >= 0) {
-                    const int h = (int)(in_tok / (4 * DB)), c = (int)(in_tok % (4 * DB));
+                    const int h = (int)(in_tok / (2 * DB)), c = (int)(in_tok % (2 * DB));
                     const Place<TYPE, DB> at(s_page[tok], h, p.H, s_off[tok], p.log_p);
-                    d[u] = *reinterpret_cast<const uint16_t *>(cache + at.scale(c >> 2));
-                    w[u] = *reinterpret_cast<const uint2 *>(cache + at.codes(c >> 2, 8 * (TYPE == QMM_Q8_0 ? c & 3 : c & 1)));
+                    d[u] = *reinterpret_cast<const uint16_t *>(cache + at.scale(c >> 1));
+                    if constexpr (TYPE == QMM_Q8_0) {
+                        w[u] = *reinterpret_cast<const uint4 *>(cache + at.codes(c >> 1, 16 * (c & 1)));
+                    } else {
+                        const uint2 v = *reinterpret_cast<const uint2 *>(cache + at.codes(c >> 1, 8 * (c & 1)));
+                        w[u].x = v.x;
+                        w[u].y = v.y;
+                    }
                 }
             }
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const uint32_t i = base + u * kThreads, tok = p.per_tok(i), in_tok = i - tok * p.per_tok.d;
                 if (i >= items) break;
-                const float s = __half2float(__ushort_as_half(d[u]));
-                float v[8];
+                const uint32_t d2 = d[u] * 0x00010001u;
+                constexpr int kW4 = sizeof(T);                   // words of four elements
+                uint32_t v[4 * kW4];
+                const uint32_t x[4] = {w[u].x, w[u].y, w[u].z, w[u].w};
+                T *out = dst + (t0 + tok) * p.ld[which] + (int64_t)(in_tok >> 1) * 32;
+                if constexpr (TYPE == QMM_Q8_0) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    const uint32_t x = j < 4 ? w[u].x : w[u].y;
-                    // 2^23 + 128 + q (or + q) is exact, and so is the difference
-                    if constexpr (TYPE == QMM_Q8_0) {
-                        v[j] = s * (__uint_as_float(__byte_perm(x ^ 0x80808080u, 0x4B000000u, 0x7440 | (j & 3))) - 8388736.0f);
-                    } else {
-                        const uint32_t q = (x >> (8 * (j & 3) + ((in_tok & 2) ? 4 : 0))) & 15u;
-                        v[j] = s * (__uint_as_float(q | 0x4B000000u) - 8388616.0f);
+                    for (int c = 0; c < 4; ++c) {
+                        uint32_t q01, q23;
+                        tc::i8x4_to_h2x2(x[c], q01, q23);
+                        scale4<T>(q01, q23, d2, v + c * kW4);
                     }
+                    store_words<VEC, 16>(out + 16 * (in_tok & 1), v);
+                } else {
+                    const __half2 eight = __halves2half2(__float2half_rn(1032.0f), __float2half_rn(1032.0f));
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {               // low nibbles of x[0], x[1], then high ones
+                        const uint32_t n = (c < 2 ? x[c & 1] : x[c & 1] >> 4) & 0x0F0F0F0Fu;
+                        const uint32_t q01 = tc::h2_bits(__hsub2(tc::bits_h2(__byte_perm(n, 0x64646464u, 0x4140u)), eight));
+                        const uint32_t q23 = tc::h2_bits(__hsub2(tc::bits_h2(__byte_perm(n, 0x64646464u, 0x4342u)), eight));
+                        scale4<T>(q01, q23, d2, v + c * kW4);
+                    }
+                    store_words<VEC, 8>(out + 8 * (in_tok & 1), v);
+                    store_words<VEC, 8>(out + 16 + 8 * (in_tok & 1), v + 2 * kW4);
                 }
-                store8<VEC>(dst + (t0 + tok) * p.ld[which] + (int64_t)in_tok * 8, v);
             }
         }
     }
@@ -258,7 +316,6 @@ unsigned grid_for(int64_t work, int64_t per_cta) {
     const int64_t g = (work + per_cta - 1) / per_cta;
     return (unsigned)(g > 152 * 8 ? 152 * 8 : (g < 1 ? 1 : g));
 }
-bool vec_ok(const void *p, int64_t ld, size_t es) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (ld * es) % 16 == 0; }
 
 }  // namespace
 
@@ -327,8 +384,8 @@ cudaError_t launch_cache_write(qmm_type type, qmm_dtype t, const void *k, const 
                                int H, int D, const int64_t *slots, uint8_t *k_cache, uint8_t *v_cache, int64_t n_pages, int P,
                                cudaStream_t s) {
     const size_t es = dtype_bytes(t);
-    const bool vec = vec_ok(k, ldk, es) && vec_ok(v, ldv, es);
-    const WriteParams p{{k, v}, {k_cache, v_cache}, {ldk, ldv}, slots, n_pages * P, 0, FastDiv((uint32_t)(H * (D / 8))), H, log2_of(P)};
+    const bool vec = rows_aligned(k, ldk, es) && rows_aligned(v, ldv, es);
+    const WriteParams p{{k, v}, {k_cache, v_cache}, {ldk, ldv}, slots, n_pages * P, 0, FastDiv((uint32_t)(H * (D / 16))), H, log2_of(P)};
     return type == QMM_Q8_0 ? write_typed<QMM_Q8_0>(t, D / 32, vec, p, T, k, v, s) : write_typed<QMM_Q4_0>(t, D / 32, vec, p, T, k, v, s);
 }
 
@@ -336,8 +393,8 @@ cudaError_t launch_cache_read(qmm_type type, const uint8_t *k_cache, const uint8
                               const int32_t *pages, int64_t ld_pages, const int32_t *starts, int64_t n_seq, int64_t T, qmm_dtype t,
                               void *k, void *v, int64_t ldk, int64_t ldv, cudaStream_t s) {
     const size_t es = dtype_bytes(t);
-    const bool vec = (!k || vec_ok(k, ldk, es)) && (!v || vec_ok(v, ldv, es));
-    const ReadParams p{{k_cache, v_cache}, {k, v}, {ldk, ldv}, pages, ld_pages, n_pages, starts, n_seq, T, FastDiv((uint32_t)(H * (D / 8))), H, log2_of(P)};
+    const bool vec = (!k || rows_aligned(k, ldk, es)) && (!v || rows_aligned(v, ldv, es));
+    const ReadParams p{{k_cache, v_cache}, {k, v}, {ldk, ldv}, pages, ld_pages, n_pages, starts, n_seq, T, FastDiv((uint32_t)(H * (D / 16))), H, log2_of(P)};
     return type == QMM_Q8_0 ? read_typed<QMM_Q8_0>(t, D / 32, vec, p, s) : read_typed<QMM_Q4_0>(t, D / 32, vec, p, s);
 }
 

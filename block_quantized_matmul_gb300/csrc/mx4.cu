@@ -1,10 +1,11 @@
 // mx4.cu -- rows of floating-point values to microscaled 4-bit operands (mx4.cuh) and back.
 //
-// Both directions move each element once and do a few operations on it.  A warp takes segments of 256
-// consecutive elements of a row, 8 to a lane: 16- or 32-byte loads and 4-byte code words; the four
-// lanes of a block find its largest magnitude with two shuffles, and the scale bytes of four blocks
-// leave as one word.  A warp loads kBatch segments before it works on the first, so that enough
-// bytes are on their way to hide memory's latency.
+// Both directions move each element once and do a few operations on it; what costs beside the bytes is
+// instructions.  A lane takes 16 consecutive elements, half a block (a warp: 512 of a row): with 8, the
+// addresses, shuffles and scale bytes of a lane's piece weigh twice as much (8192 x 14336 bf16: 77 us).
+// Loads and stores are 32 bytes; two lanes of a block agree on its largest magnitude, and the scale
+// bytes of four blocks leave as one word.  A warp loads kBatch pieces before it works on the first,
+// so that enough bytes are on their way to hide memory's latency.
 #include "qmm_internal.cuh"
 
 #include "elem.cuh"
@@ -15,7 +16,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;
+constexpr int kBatch = 2;
+constexpr int kSeg = 512;                   // elements of a warp's piece
 
 // `trigger`: the next kernel on the stream may start early (it waits for this one before it reads the
 // operand; see launch_mx4_quantize).
@@ -29,32 +31,30 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T *__restr
     const int lane = threadIdx.x & 31;
     const uint32_t warps = gridDim.x * kWarps;
     for (uint32_t base = blockIdx.x * kWarps + (threadIdx.x >> 5); base < items; base += warps * kBatch) {
-        Raw8<T> raw[kBatch];
+        Raw<T, 16> raw[kBatch];
+        int64_t row[kBatch], col[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const uint32_t i = base + u * warps, row = nseg(i);
-            const int64_t k = (int64_t)(i - row * nseg.d) * 256 + lane * 8;
+            const uint32_t i = base + u * warps, r = nseg(i);
+            row[u] = r0 + r;
+            col[u] = i < items ? (int64_t)(i - r * nseg.d) * kSeg + lane * 16 : K;
             raw[u].zero();
-            if (i < items && k < K && QMM_DCHECK(k + 8 <= K)) raw[u].template load<VEC>(x + (r0 + row) * ldx + k);
+            if (col[u] < K && QMM_DCHECK(col[u] + 16 <= K)) raw[u].template load<VEC>(x + row[u] * ldx + col[u]);
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const uint32_t i = base + u * warps, row = nseg(i);
-            if (i >= items) break;
-            const int64_t r = r0 + row, seg = i - row * nseg.d, k = seg * 256 + lane * 8;
             uint32_t top = raw[u].top_bits();
-            float v[8];
-            raw[u].values(v);
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const uint32_t e = mx4_block_scale(top);
-            if (k < K) *reinterpret_cast<uint32_t *>(codes + (r * K + k) / 2) = mx4_codes8(v, e);
-            // the scales of four blocks (16 lanes) as one word; blocks past K hold 0
-            uint32_t word = e << (8 * ((lane >> 2) & 3));
+            float v[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) v[j] = raw[u].value(j);
+            if (col[u] < K) *reinterpret_cast<uint2 *>(codes + (row[u] * K + col[u]) / 2) = make_uint2(mx4_codes8(v, e), mx4_codes8(v + 8, e));
+            // the scales of four blocks (8 lanes) as one word; blocks past K hold 0
+            uint32_t word = e << (4 * (lane & 6));
+            word |= __shfl_xor_sync(0xffffffffu, word, 2);
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
-            word |= __shfl_xor_sync(0xffffffffu, word, 8);
-            const int64_t k128 = seg * 2 + (lane >> 4);
-            if ((lane & 15) == 0 && k128 < n128) *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(r, k128, n128)) = word;
+            if ((lane & 7) == 0 && col[u] < K) *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(row[u], col[u] >> 7, n128)) = word;
         }
     }
 }
@@ -70,28 +70,31 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t 
     const int lane = threadIdx.x & 31;
     const uint32_t warps = gridDim.x * kWarps;
     for (uint32_t base = blockIdx.x * kWarps + (threadIdx.x >> 5); base < items; base += warps * kBatch) {
-        uint32_t w[kBatch], e[kBatch];
+        uint2 w[kBatch];
+        uint32_t e[kBatch];
+        int64_t row[kBatch], col[kBatch];
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const uint32_t i = base + u * warps, row = nseg(i);
-            const int64_t r = r0 + row, k = (int64_t)(i - row * nseg.d) * 256 + lane * 8;
-            w[u] = e[u] = 0;
-            if (i < items && k < K && QMM_DCHECK(k + 8 <= K)) {
-                w[u] = *reinterpret_cast<const uint32_t *>(codes + (r * K + k) / 2);
-                e[u] = scales[mx4_scale_word(r, k >> 7, n128) + ((k >> 5) & 3)];
+            const uint32_t i = base + u * warps, r = nseg(i);
+            row[u] = r0 + r;
+            col[u] = i < items ? (int64_t)(i - r * nseg.d) * kSeg + lane * 16 : K;
+            w[u] = make_uint2(0u, 0u);
+            e[u] = 0;
+            if (col[u] < K && QMM_DCHECK(col[u] + 16 <= K)) {
+                w[u] = *reinterpret_cast<const uint2 *>(codes + (row[u] * K + col[u]) / 2);
+                e[u] = scales[mx4_scale_word(row[u], col[u] >> 7, n128) + ((lane >> 1) & 3)];
             }
         }
 #pragma unroll
         for (int u = 0; u < kBatch; ++u) {
-            const uint32_t i = base + u * warps, row = nseg(i);
-            const int64_t k = (int64_t)(i - row * nseg.d) * 256 + lane * 8;
-            if (i >= items || k >= K) continue;
+            if (col[u] >= K) continue;
             const float s = mx4_scale(e[u]);
-            float v[8];
-            mx4_values8(w[u], v);
+            float v[16];
+            mx4_values8(w[u].x, v);
+            mx4_values8(w[u].y, v + 8);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= s;
-            store8<VEC>(y + (r0 + row) * ldy + k, v);
+            for (int j = 0; j < 16; ++j) v[j] *= s;
+            store_values<VEC, 16>(y + row[u] * ldy + col[u], v);
         }
     }
 }
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(kThreads) mx4_dequantize_kernel(const uint8_t 
 // operands beyond 2^39 elements).
 template <typename F>
 cudaError_t for_rows(int64_t R, int64_t K, F f) {
-    const int64_t nseg = (K + 255) / 256, most = 0x3fffffff / nseg;
+    const int64_t nseg = (K + kSeg - 1) / kSeg, most = 0x3fffffff / nseg;
     for (int64_t r = 0; r < R; r += most) {
         const int64_t rows = R - r < most ? R - r : most, items = rows * nseg;
         const int64_t g = (items + kWarps - 1) / kWarps;
@@ -116,7 +119,7 @@ cudaError_t launch_mx4_quantize(qmm_dtype t, const void *x, int64_t R, int64_t K
                                 int trigger, cudaStream_t s) {
     return with_dtype(t, [&](auto z) {
         using T = decltype(z);
-        const bool vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx * sizeof(T)) % 16 == 0;
+        const bool vec = rows_aligned(x, ldx, sizeof(T));
         auto kern = vec ? mx4_quantize_kernel<true, T> : mx4_quantize_kernel<false, T>;
         return for_rows(R, K, [&](int64_t r, uint32_t items, FastDiv nseg, dim3 grid) {
             return launch_pdl(kern, grid, kThreads, 0, s, static_cast<const T *>(x), items, nseg, K, ldx, codes, scales, r, trigger);
@@ -128,7 +131,7 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                   int64_t ldy, cudaStream_t s) {
     return with_dtype(t, [&](auto z) {
         using T = decltype(z);
-        const bool vec = (reinterpret_cast<uintptr_t>(y) & 15u) == 0 && (ldy * sizeof(T)) % 16 == 0;
+        const bool vec = rows_aligned(y, ldy, sizeof(T));
         auto kern = vec ? mx4_dequantize_kernel<true, T> : mx4_dequantize_kernel<false, T>;
         return for_rows(R, K, [&](int64_t r, uint32_t items, FastDiv nseg, dim3 grid) {
             return launch_pdl(kern, grid, kThreads, 0, s, codes, scales, items, nseg, K, static_cast<T *>(y), ldy, r);

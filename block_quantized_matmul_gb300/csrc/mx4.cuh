@@ -41,7 +41,7 @@ __device__ __forceinline__ uint32_t mx4_block_scale(uint32_t abs_bits) {
 
 // Codes of 8 elements under scale e (element i in nibble i): E2M1 of x * 2^(127 - e), to nearest even,
 // saturating at 6.  The product is exact but for subnormal results, which round to zero anyway.
-__device__ __forceinline__ uint32_t mx4_codes8(const float (&x)[8], uint32_t e) {
+__device__ __forceinline__ uint32_t mx4_codes8(const float *x, uint32_t e) {
     const float inv = __uint_as_float((254u - e) << 23);
     float v[8];
 #pragma unroll
@@ -57,7 +57,7 @@ __device__ __forceinline__ uint32_t mx4_codes8(const float (&x)[8], uint32_t e) 
 }
 
 // Values of the 8 codes of a word, without the scale.
-__device__ __forceinline__ void mx4_values8(uint32_t w, float (&v)[8]) {
+__device__ __forceinline__ void mx4_values8(uint32_t w, float *v) {
     uint32_t h[4];
     asm("{\n .reg .b8 b0, b1, b2, b3;\n mov.b32 {b0, b1, b2, b3}, %4;\n"
         " cvt.rn.f16x2.e2m1x2 %0, b0;\n cvt.rn.f16x2.e2m1x2 %1, b1;\n cvt.rn.f16x2.e2m1x2 %2, b2;\n cvt.rn.f16x2.e2m1x2 %3, b3;\n}\n"

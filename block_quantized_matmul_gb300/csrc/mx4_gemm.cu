@@ -57,7 +57,7 @@ struct Mx4Params {
     int dtype;
     const void *x;                         // rows to be quantized here (fused)
     int64_t ldx, K;
-    int x_vec;                             // they are 16-byte aligned
+    int x_vec;                             // they are 32-byte aligned
 };
 
 __device__ __forceinline__ bool wait_bounded(uint32_t bar, uint32_t parity, volatile int *abort) {
@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
             // one's are worked on
             constexpr int kMine = TN / 4;
             const XT *x = static_cast<const XT *>(p.x);
-            Raw8<XT> raw[kMine];
+            Raw<XT, 8> raw[kMine];
             auto load = [&](int k) {
                 const int64_t at = (int64_t)k * 256 + lane * 8;
 #pragma unroll
@@ -289,7 +289,8 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
                     if (r >= p.M) break;
                     uint32_t top = raw[u].top_bits();
                     float v[8];
-                    raw[u].values(v);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[j] = raw[u].value(j);
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
                     const uint32_t e = mx4_block_scale(top);
@@ -725,7 +726,7 @@ cudaError_t launch_mx4_linear_few(const uint8_t *wc, const uint8_t *ws, int64_t 
     p.early_weights = 1;
     p.x = x;
     p.ldx = ldx;
-    p.x_vec = (reinterpret_cast<uintptr_t>(x) & 15u) == 0 && (ldx * (int64_t)dtype_bytes(xt)) % 16 == 0;
+    p.x_vec = rows_aligned(x, ldx, dtype_bytes(xt));
     return with_dtype(xt, [&](auto z) { return launch_tn<kMx4FusedTokens, decltype(z)>(p, wc, K, nullptr, s); });
 }
 

@@ -363,7 +363,7 @@ QMM_API size_t qmm_mx4_scales_size(int64_t R, int64_t K);
 /*
  * qmm_mx4_quantize -- floating-point rows (activations, or a weight at load time) -> MX4 operand.
  *   x_dev       R rows of K elements of type dt, row r at x_dev + r*ldx (elements); aligned to the element
- *               (16-byte aligned rows take the vectorised path).
+ *               (32-byte aligned rows take the vectorised path).
  *   codes_dev   qmm_mx4_codes_size bytes; scales_dev qmm_mx4_scales_size bytes; both 16-byte aligned.
  * Per block of 32: e = floor(log2 max|x|) - 2 + 127, at least 0 (0 for an all-zero block); code = the E2M1
  * value nearest to x * 2^(127 - e), ties to the even code, magnitudes beyond 6 to 6.  A block that holds
@@ -433,7 +433,7 @@ QMM_API size_t qmm_cache_page_size(qmm_type t, int64_t H, int64_t D, int64_t P);
 /*
  * qmm_cache_write -- keys and values of T new tokens, quantized into their slots.
  *   k_dev, v_dev   [T][H][D] elements of type dt, token i at k_dev + i*ldk (ldv for values; elements, at
- *                  least H*D); aligned to the element (16-byte aligned rows take the vectorised path).
+ *                  least H*D); aligned to the element (32-byte aligned rows take the vectorised path).
  *   slots_dev      int64 [T], 8-byte aligned; a token whose slot is negative or past the pool is not written.
  *                  Two tokens of a call must not share a slot.
  *   k_cache_dev, v_cache_dev  n_pages * qmm_cache_page_size bytes each, 16-byte aligned.
