@@ -7,13 +7,15 @@
 // j is visible when j < n - nq, or when bit j - (n - nq) of the token's tree word is set (without tree
 // words: when j - (n - nq) <= i).  A row that sees nothing is 0 with lse -inf.
 //
-// The nq * G rows of a sequence and key/value head are taken 16 at a time, the height of the mma
-// instruction (m16n8k16): a decode step's few rows leave the bytes of the cache as the only cost, so each
-// code is expanded in registers, once per 16 rows, and never written back.  A CTA takes one chunk of
-// the keys; its warps take tiles of 32 keys in turn, each through its own ring of asynchronous copies
-// (no barriers), with its own running maximum and sum, and the warps' results are joined at the end.
-// Sequences longer than a chunk leave one partial result per chunk in the workspace, which a second
-// kernel joins.
+// Both products are taken with the cache as the left factor: S^T = K Q^T and O^T = V^T P^T, so that the mma
+// instruction's 16 rows (m16n8k16) are keys or elements of the head, and its 8 columns are the nq * G rows
+// of a sequence and key/value head, 8 * NT of them to a CTA.  A decode step's few rows then cost half
+// the products, sums and registers of the other way round, where 16 rows are the least.  The codes are
+// expanded in registers, once for all rows of the CTA, and never written back; movmatrix turns p from the
+// first product's result into the second one's operand.  A CTA takes one chunk of the keys; its warps take
+// tiles of 32 keys in turn, each through its own ring of asynchronous copies (no barriers), with its own
+// running maximum and sum, and the warps' results are joined at the end.  Sequences longer than a chunk
+// leave one partial result per chunk in the workspace, which a second kernel joins.
 //
 // Arithmetic.  Scores: the codes are exact in fp16, the query row is scaled by a power of two into fp16's
 // range (an fp16 or bf16 query loses nothing but elements 2^-14 times smaller than the row's largest),
@@ -33,7 +35,7 @@
 namespace qmm {
 namespace {
 
-constexpr int kMmaRows = 16;
+constexpr int kMmaRows = 8;                // columns of an mma
 constexpr int kKeys = 32;                  // keys of a tile
 constexpr float kBias = 14.0f;             // p is kept times 2^14
 
@@ -63,20 +65,21 @@ __device__ __forceinline__ int swz(int r, int b) {
     return b ^ ((r / (U / Z)) & (Z - 1));
 }
 
-template <int TYPE, int DB, int MT>
+template <int TYPE, int DB, int NT>
 struct Tile {
-    static constexpr int kRowsTile = kMmaRows * MT;
+    static constexpr int kRowsTile = kMmaRows * NT;
     static constexpr int kUnit = TYPE == QMM_Q8_0 ? 32 : 16;           // bytes of a block's codes
     static constexpr int kSpan = TYPE == QMM_Q8_0 ? 4 : 8;             // units of 128 bytes
     static constexpr int kCodes = kKeys * DB * kUnit;
     static constexpr int kScales = kKeys * DB * 2;
     static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales;
     static constexpr int kBytes = kVs + kScales;
-    // eight warps, or four where a tile of eight would not fit twice
-    static constexpr int kWarps = 2 * 8 * kBytes <= 200 * 1024 ? 8 : 4;
+    // as many warps as registers (12: 170 a thread) and a ring of two tiles each allow
+    static constexpr int kRoom = 208 * 1024;
+    static constexpr int kWarps = NT == 1 && 2 * 12 * kBytes <= kRoom ? 12 : (2 * 8 * kBytes <= kRoom ? 8 : 4);
     static constexpr int kThreads = kWarps * 32;
-    static constexpr int kFit = 200 * 1024 / (kWarps * kBytes);
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static constexpr int kFit = kRoom / (kWarps * kBytes);
+    static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kOut = kWarps * kRowsTile * DB * 32 * 4;      // the warps' results, over the ring
     static constexpr int kQ = kRowsTile * DB * 32 * 2;                 // query fragments
     static constexpr int kRing = kStages * kWarps * kBytes > kOut ? kStages * kWarps * kBytes : kOut;
@@ -106,6 +109,12 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// An 8 x 8 matrix of 16-bit values, two of a row to a lane, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return tc::h2_bits(__hmul2(tc::bits_h2(a), tc::bits_h2(b))); }
@@ -179,10 +188,10 @@ __device__ __forceinline__ float cache_value(const uint8_t *chunk, int P, int D,
 
 // The CTA's rows and keys once more, a warp a row, skipping what the row does not see; rows whose result
 // is finite, and was, keep the one they have.
-template <int TYPE, int DB, int MT>
+template <int TYPE, int DB, int NT>
 __device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &w, int sp, const int *row_bad) {
     const int lane = threadIdx.x & 31;
-    constexpr int D = DB * 32, kWarps = Tile<TYPE, DB, MT>::kWarps;
+    constexpr int D = DB * 32, kWarps = Tile<TYPE, DB, NT>::kWarps;
     for (int row = threadIdx.x >> 5; row < w.rows; row += kWarps) {
         const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + r % p.group;
         float q[DB], o[DB];
@@ -241,10 +250,30 @@ __device__ __forceinline__ void load_scales(const uint8_t *p, uint32_t (&w)[DB])
         for (int i = 0; i < DB; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
     }
 }
+// The scales of one key as fp32.
 template <int DB>
-__device__ __forceinline__ float scale_of(const uint32_t (&w)[DB], int i) {
-    const __half2 h = tc::bits_h2(w[i >> 1]);
-    return i & 1 ? __high2float(h) : __low2float(h);
+__device__ __forceinline__ void load_key_scales(const uint8_t *p, float (&d)[DB]) {
+    if constexpr (DB % 2 == 0) {
+        uint32_t w[DB / 2];
+        if constexpr (DB % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < DB / 4; ++i) {
+                const uint2 v = reinterpret_cast<const uint2 *>(p)[i];
+                w[2 * i] = v.x; w[2 * i + 1] = v.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < DB / 2; ++i) w[i] = reinterpret_cast<const uint32_t *>(p)[i];
+        }
+#pragma unroll
+        for (int i = 0; i < DB / 2; ++i) {
+            d[2 * i] = __low2float(tc::bits_h2(w[i]));
+            d[2 * i + 1] = __high2float(tc::bits_h2(w[i]));
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < DB; ++i) d[i] = __half2float(reinterpret_cast<const __half *>(p)[i]);
+    }
 }
 // The scales of block b of both keys as a half2.
 template <int DB>
@@ -252,14 +281,14 @@ __device__ __forceinline__ uint32_t scale_pair(const uint32_t (&w)[DB], int b) {
     return __byte_perm(w[b >> 1], w[(DB + b) >> 1], (b & 1 ? 0x32 : 0x10) | ((DB + b) & 1 ? 0x7600 : 0x5400));
 }
 
-template <int TYPE, int DB, int MT>
-__global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
-    using L = Tile<TYPE, DB, MT>;
+template <int TYPE, int DB, int NT>
+__global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
+    using L = Tile<TYPE, DB, NT>;
     constexpr int D = DB * 32, S = L::kStages, UNIT = L::kUnit, SPAN = L::kSpan, CB = DB * UNIT;
     constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kRowsTile = L::kRowsTile;
-    constexpr bool kQRegs = DB <= 4 && MT == 1;                                // the query fragments stay in registers
+    constexpr bool kQRegs = NT == 1;                                           // the query fragments stay in registers
     extern __shared__ __align__(128) uint8_t smem[];
-    uint32_t *q_frag = reinterpret_cast<uint32_t *>(smem + L::kRing);       // [row tile][block][step][lane][4]
+    uint32_t *q_frag = reinterpret_cast<uint32_t *>(smem + L::kRing);       // [row tile][block][lane][step][2]
     float *w_top = reinterpret_cast<float *>(smem + L::kRing + L::kQ);       // [warp][row]
     float *w_sum = w_top + kWarps * kRowsTile;
     float *row_mul = w_sum + kWarps * kRowsTile;                              // score -> power of two
@@ -374,11 +403,11 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel
         }
     }
     __syncthreads();
-    for (int i = threadIdx.x; i < MT * DB * 2 * 32 * 4; i += kThreads) {
-        const int reg = i & 3, ln = (i >> 2) & 31, st = (i >> 7) & 1, b = (i >> 8) % DB, mt = (i >> 8) / DB;
-        const int row = mt * 16 + (ln >> 2) + 8 * (reg & 1);
+    for (int i = threadIdx.x; i < NT * DB * 32 * 4; i += kThreads) {
+        const int reg = i & 1, st = (i >> 1) & 1, ln = (i >> 2) & 31, b = (i >> 7) % DB, nt = (i >> 7) / DB;
+        const int row = nt * 8 + (ln >> 2);
         int e0, e1;
-        frag_elems<TYPE>(ln & 3, st, reg >> 1, e0, e1);
+        frag_elems<TYPE>(ln & 3, st, reg, e0, e1);
         uint32_t v = 0;
         if (row < w.rows) {
             const int r = w.r0 + row;
@@ -388,26 +417,26 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel
         q_frag[i] = v;
     }
     __syncthreads();
-    auto load_frag = [&](uint32_t (&a)[4], int mt, int b, int st) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + (((mt * DB + b) * 2 + st) * 32 + lane) * 4);
-        a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+    auto load_frag = [&](uint32_t (&q)[4], int nt, int b) {
+        const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + ((nt * DB + b) * 32 + lane) * 4);
+        q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
     };
-    uint32_t qr[kQRegs ? DB : 1][2][4];
+    uint32_t qr[kQRegs ? DB : 1][4];
     if constexpr (kQRegs) {
 #pragma unroll
-        for (int b = 0; b < DB; ++b)
-#pragma unroll
-            for (int st = 0; st < 2; ++st) load_frag(qr[b][st], 0, b, st);
+        for (int b = 0; b < DB; ++b) load_frag(qr[b], 0, b);
     }
 
-    float o[MT][4 * DB][4];
-    float top[MT][2], sum[MT][2];
+    // a lane's rows are 8 nt + 2t and + 1; O^T tile (b, x) holds elements e = 2x (lane g) and 2x + 1 (g + 8) of
+    // the four that a lane's code word has of block b
+    float o[NT][2 * DB][4];
+    float top[NT][2], sum[NT][2];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-        top[mt][0] = top[mt][1] = -INFINITY;
-        sum[mt][0] = sum[mt][1] = 0.0f;
+    for (int nt = 0; nt < NT; ++nt) {
+        top[nt][0] = top[nt][1] = -INFINITY;
+        sum[nt][0] = sum[nt][1] = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4 * DB; ++i) o[mt][i][0] = o[mt][i][1] = o[mt][i][2] = o[mt][i][3] = 0.0f;
+        for (int i = 0; i < 2 * DB; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.0f;
     }
     uint32_t odd = 0;                                            // a value scale that is not finite
 
@@ -424,121 +453,110 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel
         const int64_t j0 = w.k0 + (int64_t)(i * kWarps + warp) * kKeys;
         const bool masked = in != 0xffffffffu || j0 + kKeys > w.first;
 
-        // ---- scores: sc[mt][nt] holds keys 8 nt + 2t, + 1 of rows g (0, 1) and g + 8 (2, 3) ----
-        float sc[MT][4][4];
-        uint32_t kw[4][DB];
+        // ---- scores: sc[nt][mt] holds keys 16 mt + g (0, 1) and 16 mt + g + 8 (2, 3) of rows 2t, 2t + 1 ----
+        float sc[NT][2][4];
 #pragma unroll
-        for (int nt = 0; nt < 4; ++nt) load_scales<DB>(st + L::kKs + (8 * nt + 2 * t) * DB * 2, kw[nt]);
+        for (int mt = 0; mt < 2; ++mt) {
+            float d0[DB], d1[DB];
+            load_key_scales<DB>(st + L::kKs + (16 * mt + g) * DB * 2, d0);
+            load_key_scales<DB>(st + L::kKs + (16 * mt + g + 8) * DB * 2, d1);
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
-            uint32_t a[MT][2][4];
+            for (int b = 0; b < DB; ++b) {
+                uint32_t f[4], h[4];                             // codes of keys g and g + 8
+                auto codes = [&](int key, uint32_t (&x)[4]) {
+                    const uint8_t *kp = st + L::kK + (key * DB + swz<DB, SPAN>(key, b)) * UNIT;
+                    if constexpr (TYPE == QMM_Q8_0) {
+                        const uint2 c = *reinterpret_cast<const uint2 *>(kp + 8 * t);
+                        tc::i8x4_to_h2x2(c.x, x[0], x[1]);
+                        tc::i8x4_to_h2x2(c.y, x[2], x[3]);
+                    } else {
+                        const uint32_t c = *reinterpret_cast<const uint32_t *>(kp + 4 * t);
+                        x[0] = nib_h2(c);
+                        x[1] = nib_h2(c >> 8);
+                        x[2] = nib_h2(c >> 4);
+                        x[3] = nib_h2(c >> 12);
+                    }
+                };
+                codes(16 * mt + g, f);
+                codes(16 * mt + g + 8, h);
+                const uint32_t a0[4] = {f[0], h[0], f[1], h[1]}, a1[4] = {f[2], h[2], f[3], h[3]};
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                for (int s2 = 0; s2 < 2; ++s2) {
+                for (int nt = 0; nt < NT; ++nt) {
+                    uint32_t q[4];
                     if constexpr (kQRegs) {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) a[mt][s2][r] = qr[b][s2][r];
+                        for (int r = 0; r < 4; ++r) q[r] = qr[b][r];
                     } else {
-                        load_frag(a[mt][s2], mt, b, s2);
+                        load_frag(q, nt, b);
                     }
-                }
-#pragma unroll
-            for (int nt = 0; nt < 4; ++nt) {
-                const int key = 8 * nt + g;
-                const uint8_t *kp = st + L::kK + (key * DB + swz<DB, SPAN>(key, b)) * UNIT;
-                uint32_t f[4];
-                if constexpr (TYPE == QMM_Q8_0) {
-                    const uint2 c = *reinterpret_cast<const uint2 *>(kp + 8 * t);
-                    tc::i8x4_to_h2x2(c.x, f[0], f[1]);
-                    tc::i8x4_to_h2x2(c.y, f[2], f[3]);
-                } else {
-                    const uint32_t c = *reinterpret_cast<const uint32_t *>(kp + 4 * t);
-                    f[0] = nib_h2(c);
-                    f[1] = nib_h2(c >> 8);
-                    f[2] = nib_h2(c >> 4);
-                    f[3] = nib_h2(c >> 12);
-                }
-                const float d0 = scale_of<DB>(kw[nt], b), d1 = scale_of<DB>(kw[nt], DB + b);
-#pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
                     float acc[4];
-                    mma16816_first(acc, a[mt][0], f[0], f[1]);
-                    mma16816(acc, a[mt][1], f[2], f[3]);
-                    if (b == 0) {
-                        sc[mt][nt][0] = d0 * acc[0];
-                        sc[mt][nt][1] = d1 * acc[1];
-                        sc[mt][nt][2] = d0 * acc[2];
-                        sc[mt][nt][3] = d1 * acc[3];
-                    } else {
-                        sc[mt][nt][0] += d0 * acc[0];
-                        sc[mt][nt][1] += d1 * acc[1];
-                        sc[mt][nt][2] += d0 * acc[2];
-                        sc[mt][nt][3] += d1 * acc[3];
-                    }
+                    mma16816_first(acc, a0, q[0], q[1]);
+                    mma16816(acc, a1, q[2], q[3]);
+                    float (&x)[4] = sc[nt][mt];
+                    x[0] = b == 0 ? d0[b] * acc[0] : fmaf(d0[b], acc[0], x[0]);
+                    x[1] = b == 0 ? d0[b] * acc[1] : fmaf(d0[b], acc[1], x[1]);
+                    x[2] = b == 0 ? d1[b] * acc[2] : fmaf(d1[b], acc[2], x[2]);
+                    x[3] = b == 0 ? d1[b] * acc[3] : fmaf(d1[b], acc[3], x[3]);
                 }
             }
         }
         // ---- what is not seen ----
         if (masked) {
 #pragma unroll
-            for (int mt = 0; mt < MT; ++mt)
+            for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const int row = mt * 16 + g + 8 * r, tok = (w.r0 + row) / p.group;
+                for (int c = 0; c < 2; ++c) {
+                    const int row = nt * 8 + 2 * t + c, tok = (w.r0 + row) / p.group;
                     const uint64_t word = p.tree && row < w.rows ? p.tree[w.q0 + tok] : 0;
 #pragma unroll
-                    for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            const int key = 8 * nt + 2 * t + c;
-                            const int64_t nb = j0 + key - w.first;      // place among the new tokens
-                            bool seen = (in >> key) & 1;
-                            if (nb >= 0) seen = seen && (p.tree ? nb < 64 && ((word >> nb) & 1) : nb <= tok);
-                            if (!seen) sc[mt][nt][2 * r + c] = -INFINITY;
-                        }
+                    for (int x = 0; x < 4; ++x) {
+                        const int key = 8 * x + g;
+                        const int64_t nb = j0 + key - w.first;      // place among the new tokens
+                        bool seen = (in >> key) & 1;
+                        if (nb >= 0) seen = seen && (p.tree ? nb < 64 && ((word >> nb) & 1) : nb <= tok);
+                        if (!seen) sc[nt][x >> 1][2 * (x & 1) + c] = -INFINITY;
+                    }
                 }
         }
-        // ---- running maximum and sum; p to fp16 ----
-        uint32_t pf[MT][4][2];
+        // ---- running maximum and sum; p to fp16 and transposed: pt[nt][x] holds keys 8x + 2t, + 1 of row g ----
+        uint32_t pt[NT][4];
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) {
+        for (int nt = 0; nt < NT; ++nt) {
             float base[2], down[2], mul[2];
             bool moved = false;
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                mul[r] = row_mul[mt * 16 + g + 8 * r];
-                const float (&x)[4][4] = sc[mt];
-                float m = fmaxf(fmaxf(fmaxf(x[0][2 * r], x[0][2 * r + 1]), fmaxf(x[1][2 * r], x[1][2 * r + 1])),
-                                fmaxf(fmaxf(x[2][2 * r], x[2][2 * r + 1]), fmaxf(x[3][2 * r], x[3][2 * r + 1])));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                m = fmaxf(m * mul[r], top[mt][r]);
-                base[r] = m == -INFINITY ? 0.0f : m;
-                down[r] = ex2(top[mt][r] - base[r]);
-                moved |= m != top[mt][r];
-                top[mt][r] = m;
-                base[r] = kBias - base[r];
+            for (int c = 0; c < 2; ++c) {
+                mul[c] = row_mul[nt * 8 + 2 * t + c];
+                float m = fmaxf(fmaxf(sc[nt][0][c], sc[nt][0][2 + c]), fmaxf(sc[nt][1][c], sc[nt][1][2 + c]));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+                m = fmaxf(m * mul[c], top[nt][c]);
+                base[c] = m == -INFINITY ? 0.0f : m;
+                down[c] = ex2(top[nt][c] - base[c]);
+                moved |= m != top[nt][c];
+                top[nt][c] = m;
+                base[c] = kBias - base[c];
             }
             if (__any_sync(0xffffffffu, moved)) {
-                sum[mt][0] *= down[0];
-                sum[mt][1] *= down[1];
+                sum[nt][0] *= down[0];
+                sum[nt][1] *= down[1];
 #pragma unroll
-                for (int n = 0; n < 4 * DB; ++n) {
-                    o[mt][n][0] *= down[0];
-                    o[mt][n][1] *= down[0];
-                    o[mt][n][2] *= down[1];
-                    o[mt][n][3] *= down[1];
+                for (int n = 0; n < 2 * DB; ++n) {
+                    o[nt][n][0] *= down[0];
+                    o[nt][n][1] *= down[1];
+                    o[nt][n][2] *= down[0];
+                    o[nt][n][3] *= down[1];
                 }
             }
 #pragma unroll
-            for (int nt = 0; nt < 4; ++nt)
-#pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    const float p0 = ex2(fmaf(sc[mt][nt][2 * r], mul[r], base[r])), p1 = ex2(fmaf(sc[mt][nt][2 * r + 1], mul[r], base[r]));
-                    sum[mt][r] += p0 + p1;
-                    pf[mt][nt][r] = pack2(p0, p1, __half{});
-                }
+            for (int x = 0; x < 4; ++x) {
+                const float p0 = ex2(fmaf(sc[nt][x >> 1][2 * (x & 1)], mul[0], base[0]));
+                const float p1 = ex2(fmaf(sc[nt][x >> 1][2 * (x & 1) + 1], mul[1], base[1]));
+                sum[nt][0] += p0;
+                sum[nt][1] += p1;
+                pt[nt][x] = transpose8x8(pack2(p0, p1, __half{}));
+            }
         }
         // ---- values: 16 keys a step; a lane's keys are 2t, 2t + 1, 2t + 8, 2t + 9 ----
 #pragma unroll
@@ -567,7 +585,7 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel
                 const uint8_t *vp = st + L::kV;
                 const int r0 = 16 * j + t;                       // rows of keys 2t, 2t + 8, 2t + 1, 2t + 9: t, t + 4, t + 8, t + 12
                 auto row = [&](int r) { return vp + (r * DB + swz<DB, SPAN>(r, b)) * UNIT; };
-                uint32_t x[4], y[4];                             // n tile e: keys 2t, 2t + 1 and 2t + 8, 2t + 9
+                uint32_t x[4], y[4];                             // element e: keys 2t, 2t + 1 and 2t + 8, 2t + 9
                 if constexpr (TYPE == QMM_Q8_0) {
                     const uint32_t k0w = *reinterpret_cast<const uint32_t *>(row(r0) + 4 * g), k8w = *reinterpret_cast<const uint32_t *>(row(r0 + 4) + 4 * g);
                     const uint32_t k1w = *reinterpret_cast<const uint32_t *>(row(r0 + 8) + 4 * g), k9w = *reinterpret_cast<const uint32_t *>(row(r0 + 12) + 4 * g);
@@ -588,12 +606,14 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint32_t v01 = hmul2(x[e], d01), v89 = hmul2(y[e], d89);
+                    x[e] = hmul2(x[e], d01);
+                    y[e] = hmul2(y[e], d89);
+                }
 #pragma unroll
-                    for (int mt = 0; mt < MT; ++mt) {
-                        const uint32_t a[4] = {pf[mt][2 * j][0], pf[mt][2 * j][1], pf[mt][2 * j + 1][0], pf[mt][2 * j + 1][1]};
-                        mma16816(o[mt][4 * b + e], a, v01, v89);
-                    }
+                for (int z = 0; z < 2; ++z) {
+                    const uint32_t a[4] = {x[2 * z], x[2 * z + 1], y[2 * z], y[2 * z + 1]};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt) mma16816(o[nt][2 * b + z], a, pt[nt][2 * j], pt[nt][2 * j + 1]);
                 }
             }
         }
@@ -605,26 +625,27 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel
     __syncthreads();                                             // the ring is free
     float *res = reinterpret_cast<float *>(smem) + warp * kRowsTile * D;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+    for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            sum[mt][r] += __shfl_xor_sync(0xffffffffu, sum[mt][r], 1);
-            sum[mt][r] += __shfl_xor_sync(0xffffffffu, sum[mt][r], 2);
-            if (t == 0) {
-                w_top[warp * kRowsTile + mt * 16 + g + 8 * r] = top[mt][r];
-                w_sum[warp * kRowsTile + mt * 16 + g + 8 * r] = sum[mt][r];
+        for (int c = 0; c < 2; ++c) {
+            sum[nt][c] += __shfl_xor_sync(0xffffffffu, sum[nt][c], 4);
+            sum[nt][c] += __shfl_xor_sync(0xffffffffu, sum[nt][c], 8);
+            sum[nt][c] += __shfl_xor_sync(0xffffffffu, sum[nt][c], 16);
+            if (g == 0) {
+                w_top[warp * kRowsTile + nt * 8 + 2 * t + c] = top[nt][c];
+                w_sum[warp * kRowsTile + nt * 8 + 2 * t + c] = sum[nt][c];
             }
         }
 #pragma unroll
         for (int b = 0; b < DB; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int z = 0; z < 2; ++z)
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
-                    const int row = mt * 16 + g + 8 * (c >> 1), n = 2 * t + (c & 1);
-                    // n tile e of block b, column n: the element whose codes were fed to it
-                    const int d = TYPE == QMM_Q8_0 ? 4 * n + e : 2 * n + (e >> 1) + 16 * (e & 1);
-                    if (row < w.rows) res[row * D + 32 * b + d] = o[mt][4 * b + e][c];
+                    const int row = nt * 8 + 2 * t + (c & 1), e = 2 * z + (c >> 1);
+                    // the element whose codes were fed to slot e of lane g
+                    const int d = TYPE == QMM_Q8_0 ? 4 * g + e : 2 * g + (e >> 1) + 16 * (e & 1);
+                    if (row < w.rows) res[row * D + 32 * b + d] = o[nt][2 * b + z][c];
                 }
     }
     __syncthreads();
@@ -648,7 +669,7 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, MT>::kThreads, 1) attend_kernel
         }
         write_row(p, w, sp, D, row, d, v, m, l);
     }
-    if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB, MT>(p, w, sp, row_bad);
+    if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB, NT>(p, w, sp, row_bad);
 }
 
 // Joins the partial results of the sequences that were split.  WPR warps take a row, each the splits of
@@ -722,9 +743,12 @@ constexpr int kMaxSplits = 256;
 
 // Splits of the longest sequence: until there are several CTAs an SM (ragged lengths even out), but no
 // chunk below two tiles a warp.
-// Rows of a CTA: 32, where a sequence has more than 16 and the sums of 32 fit in registers, so that the
-// codes are expanded half as often.
-int tile_rows_of(int64_t max_new, int group, int D) { return max_new * group > kMmaRows && D <= 128 ? 2 * kMmaRows : kMmaRows; }
+// Rows of a CTA: the more, the less often the codes are expanded; up to what the sums leave of the registers
+// (32 of 128 elements, 16 of more).
+int tile_rows_of(int64_t max_new, int group, int D) {
+    const int64_t rows = max_new * group;
+    return rows <= kMmaRows ? kMmaRows : (rows <= 2 * kMmaRows || D > 128 ? 2 * kMmaRows : 4 * kMmaRows);
+}
 int wanted_splits(int64_t units, int64_t max_len) {
     const int64_t most = (max_len + 2 * kMinChunk - 1) / (2 * kMinChunk);
     int64_t want = (152 * 4 + units - 1) / units;
@@ -738,11 +762,11 @@ int64_t row_tiles_of(int64_t max_new, int group, int D) {
 }
 size_t split_bytes(int64_t rows, int D) { return round256((size_t)rows * (size_t)(D + 2) * 4); }
 
-template <int TYPE, int DB, int MT>
+template <int TYPE, int DB, int NT>
 cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
-    using L = Tile<TYPE, DB, MT>;
+    using L = Tile<TYPE, DB, NT>;
     static_assert(L::kSmem <= 227 * 1024, "shared memory plan too large");
-    auto kern = attend_kernel<TYPE, DB, MT>;
+    auto kern = attend_kernel<TYPE, DB, NT>;
     static int attr_done[4] = {0, 0, 0, 0};
     cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
     if (e != cudaSuccess) return e;
@@ -753,18 +777,26 @@ cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
     return launch_pdl(attend_join_kernel<DB, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, p);
 }
 
+template <int TYPE, int DB>
+cudaError_t launch_rows(const AttendParams &p, int64_t ctas, cudaStream_t s) {
+    if (p.tile_rows == kMmaRows) return launch_typed<TYPE, DB, 1>(p, ctas, s);
+    if constexpr (DB <= 4) {
+        if (p.tile_rows == 4 * kMmaRows) return launch_typed<TYPE, DB, 4>(p, ctas, s);
+    }
+    return launch_typed<TYPE, DB, 2>(p, ctas, s);
+}
+
 template <int TYPE>
 cudaError_t launch_blocks(const AttendParams &p, int DB, int64_t ctas, cudaStream_t s) {
-    const bool two = p.tile_rows > kMmaRows;
     switch (DB) {
-        case 1: return two ? launch_typed<TYPE, 1, 2>(p, ctas, s) : launch_typed<TYPE, 1, 1>(p, ctas, s);
-        case 2: return two ? launch_typed<TYPE, 2, 2>(p, ctas, s) : launch_typed<TYPE, 2, 1>(p, ctas, s);
-        case 3: return two ? launch_typed<TYPE, 3, 2>(p, ctas, s) : launch_typed<TYPE, 3, 1>(p, ctas, s);
-        case 4: return two ? launch_typed<TYPE, 4, 2>(p, ctas, s) : launch_typed<TYPE, 4, 1>(p, ctas, s);
-        case 5: return launch_typed<TYPE, 5, 1>(p, ctas, s);
-        case 6: return launch_typed<TYPE, 6, 1>(p, ctas, s);
-        case 7: return launch_typed<TYPE, 7, 1>(p, ctas, s);
-        default: return launch_typed<TYPE, 8, 1>(p, ctas, s);
+        case 1: return launch_rows<TYPE, 1>(p, ctas, s);
+        case 2: return launch_rows<TYPE, 2>(p, ctas, s);
+        case 3: return launch_rows<TYPE, 3>(p, ctas, s);
+        case 4: return launch_rows<TYPE, 4>(p, ctas, s);
+        case 5: return launch_rows<TYPE, 5>(p, ctas, s);
+        case 6: return launch_rows<TYPE, 6>(p, ctas, s);
+        case 7: return launch_rows<TYPE, 7>(p, ctas, s);
+        default: return launch_rows<TYPE, 8>(p, ctas, s);
     }
 }
 
