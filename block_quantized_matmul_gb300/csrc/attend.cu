@@ -74,16 +74,19 @@ struct Tile {
     static constexpr int kScales = kKeys * DB * 2;
     static constexpr int kK = 0, kV = kCodes, kKs = 2 * kCodes, kVs = kKs + kScales;
     static constexpr int kBytes = kVs + kScales;
-    // as many warps as registers (12: 170 a thread) and a ring of two tiles each allow
-    static constexpr int kRoom = 208 * 1024;
-    static constexpr int kWarps = NT == 1 && 2 * 12 * kBytes <= kRoom ? 12 : (2 * 8 * kBytes <= kRoom ? 8 : 4);
+    // Two CTAs share an SM, so that one's start and end, mostly latency, pass under the other's tiles: half the
+    // shared memory each, and up to 6 warps (170 registers a thread) or 4 (255) with a ring of two tiles at least.
+    static constexpr int kRoom = 104 * 1024;
+    static constexpr int kWarps = NT == 1 && 2 * 6 * kBytes <= kRoom ? 6 : (2 * 4 * kBytes <= kRoom ? 4 : 3);
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kFit = kRoom / (kWarps * kBytes);
     static constexpr int kStages = kFit > 4 ? 4 : kFit;
     static constexpr int kOut = kWarps * kRowsTile * DB * 32 * 4;      // the warps' results, over the ring
-    static constexpr int kQ = kRowsTile * DB * 32 * 2;                 // query fragments
+    // query rows in fp16: neighbouring rows 64 bytes apart, modulo the banks' 128
+    static constexpr int kQPitch = DB * 64 + (DB % 2 == 0 ? 64 : 0);
+    static constexpr int kQ = kRowsTile * kQPitch;
     static constexpr int kRing = kStages * kWarps * kBytes > kOut ? kStages * kWarps * kBytes : kOut;
-    static constexpr int kSmem = kRing + kQ + kWarps * kRowsTile * 8 + kRowsTile * 12 + kWarps * 8 * 4;
+    static constexpr int kSmem = kRing + kQ + kWarps * kRowsTile * 8 + kRowsTile * 8 + kWarps * 4 * 4;
     static_assert(kStages >= 2, "ring too shallow");
 };
 
@@ -127,17 +130,13 @@ __device__ __forceinline__ uint32_t nib_h2(uint32_t w) {
     return tc::h2_bits(__hsub2(tc::bits_h2(h), __halves2half2(__float2half_rn(1032.0f), __float2half_rn(1032.0f))));
 }
 
-// Element pairs of a lane's query fragment: the pair that register r (0, 1: the mma's k = 2t.., k = 2t + 8..)
-// of k step st holds within a block, for the order in which the key codes come out of their words.
+// Place of element e of a block in a query row: the eight elements of lane t's fragments (two k steps of
+// two registers of two) lie together, in the order in which the key codes come out of their words.
 template <int TYPE>
-__device__ __forceinline__ void frag_elems(int t, int st, int r, int &e0, int &e1) {
-    if (TYPE == QMM_Q8_0) {
-        e0 = 8 * t + 4 * st + 2 * r;
-        e1 = e0 + 1;
-    } else {
-        e0 = 16 * st + 4 * t + r;
-        e1 = e0 + 2;
-    }
+__device__ __forceinline__ int query_place(int e) {
+    if (TYPE == QMM_Q8_0) return e;
+    const int k = e & 3;                       // elements 4t, 4t + 2, 4t + 1, 4t + 3, then 16 + those
+    return ((e & 12) << 1) | ((e & 16) >> 2) | (k == 1 ? 2 : (k == 2 ? 1 : k));
 }
 
 struct Rows {                              // what a CTA works on
@@ -282,18 +281,17 @@ __device__ __forceinline__ uint32_t scale_pair(const uint32_t (&w)[DB], int b) {
 }
 
 template <int TYPE, int DB, int NT>
-__global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 1) attend_kernel(const __grid_constant__ AttendParams p) {
+__global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel(const __grid_constant__ AttendParams p) {
     using L = Tile<TYPE, DB, NT>;
     constexpr int D = DB * 32, S = L::kStages, UNIT = L::kUnit, SPAN = L::kSpan, CB = DB * UNIT;
     constexpr int kWarps = L::kWarps, kThreads = L::kThreads, kRowsTile = L::kRowsTile;
     constexpr bool kQRegs = NT == 1;                                           // the query fragments stay in registers
     extern __shared__ __align__(128) uint8_t smem[];
-    uint32_t *q_frag = reinterpret_cast<uint32_t *>(smem + L::kRing);       // [row tile][block][lane][step][2]
-    float *w_top = reinterpret_cast<float *>(smem + L::kRing + L::kQ);       // [warp][row]
+    uint8_t *q_rows = smem + L::kRing;
+    float *w_top = reinterpret_cast<float *>(q_rows + L::kQ);                // [warp][row]
     float *w_sum = w_top + kWarps * kRowsTile;
     float *row_mul = w_sum + kWarps * kRowsTile;                              // score -> power of two
-    float *row_down = row_mul + kRowsTile;                                    // query -> fp16
-    int *row_bad = reinterpret_cast<int *>(row_down + kRowsTile);             // its result is not finite
+    int *row_bad = reinterpret_cast<int *>(row_mul + kRowsTile);              // its result is not finite
     uint32_t *masks = reinterpret_cast<uint32_t *>(row_bad + kRowsTile);      // [warp][stage]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
@@ -370,7 +368,7 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 1) attend_kernel
                 uint32_t m = left >= 32 ? 0xffffffffu : (1u << (int)left) - 1u;
                 if (!ok0) m &= 0xffff0000u;
                 if (!ok1) m &= 0x0000ffffu;
-                masks[warp * 8 + slot] = m;
+                masks[warp * 4 + slot] = m;
             }
         }
         cp_commit();
@@ -383,42 +381,39 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 1) attend_kernel
         page = next;
     }
 
-    // ---- the query rows: scaled by a power of two so that the largest element lies in [1, 2), as fragments ----
-    for (int row = warp; row < kRowsTile; row += kWarps) {
-        const int r = w.r0 + row;
-        const int64_t base = row < w.rows ? (w.q0 + r / p.group) * p.ldq + (int64_t)(w.h * p.group + r % p.group) * D : 0;
+    // ---- the query rows: scaled by a power of two so that the largest element lies in [1, 2) ----
+    constexpr int kMine = (kRowsTile + kWarps - 1) / kWarps;
+    float qv[kMine][DB];
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+        const int row = warp + u * kWarps, r = w.r0 + row;
+        const int64_t base = row < w.rows ? (w.q0 + r / p.group) * p.ldq + (int64_t)(w.h * p.group + r % p.group) * D + lane : 0;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) qv[u][b] = row < w.rows ? load_q(p, base + 32 * b) : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+        const int row = warp + u * kWarps;
+        if (row >= kRowsTile) break;
         float top = 0.0f;
 #pragma unroll
-        for (int b = 0; b < DB; ++b)
-            if (row < w.rows) top = fmaxf(top, fabsf(load_q(p, base + 32 * b + lane)));
+        for (int b = 0; b < DB; ++b) top = fmaxf(top, fabsf(qv[u][b]));
 #pragma unroll
         for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        const int e = top > 0.0f && top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
+        const float mul = p.scale * 1.4426950408889634f, down = copysignf(exp2f((float)-e), mul);
         if (lane == 0) {
-            const int e = top > 0.0f && top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
-            const float mul = p.scale * 1.4426950408889634f;
-            row_down[row] = copysignf(exp2f((float)-e), mul);
             // a scale of 0 still has to order -inf below 0
             row_mul[row] = fmaxf(fabsf(mul), 1e-30f) * exp2f((float)e);
             row_bad[row] = 0;
         }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < NT * DB * 32 * 4; i += kThreads) {
-        const int reg = i & 1, st = (i >> 1) & 1, ln = (i >> 2) & 31, b = (i >> 7) % DB, nt = (i >> 7) / DB;
-        const int row = nt * 8 + (ln >> 2);
-        int e0, e1;
-        frag_elems<TYPE>(ln & 3, st, reg, e0, e1);
-        uint32_t v = 0;
-        if (row < w.rows) {
-            const int r = w.r0 + row;
-            const int64_t base = (w.q0 + r / p.group) * p.ldq + (int64_t)(w.h * p.group + r % p.group) * D + 32 * b;
-            v = pack2(load_q(p, base + e0) * row_down[row], load_q(p, base + e1) * row_down[row], __half{});
-        }
-        q_frag[i] = v;
+        __half *out = reinterpret_cast<__half *>(q_rows + row * L::kQPitch) + query_place<TYPE>(lane);
+#pragma unroll
+        for (int b = 0; b < DB; ++b) out[32 * b] = __float2half_rn(qv[u][b] * down);
     }
     __syncthreads();
     auto load_frag = [&](uint32_t (&q)[4], int nt, int b) {
-        const uint4 v = *reinterpret_cast<const uint4 *>(q_frag + ((nt * DB + b) * 32 + lane) * 4);
+        const uint4 v = *reinterpret_cast<const uint4 *>(q_rows + (nt * 8 + g) * L::kQPitch + b * 64 + t * 16);
         q[0] = v.x; q[1] = v.y; q[2] = v.z; q[3] = v.w;
     };
     uint32_t qr[kQRegs ? DB : 1][4];
@@ -449,7 +444,7 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 1) attend_kernel
             page = next;
         }
         const uint8_t *st = smem + warp * S * L::kBytes + (i % S) * L::kBytes;
-        const uint32_t in = masks[warp * 8 + i % S];
+        const uint32_t in = masks[warp * 4 + i % S];
         const int64_t j0 = w.k0 + (int64_t)(i * kWarps + warp) * kKeys;
         const bool masked = in != 0xffffffffu || j0 + kKeys > w.first;
 
@@ -741,8 +736,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
 constexpr int64_t kMinChunk = 8 * kKeys;           // one tile a warp
 constexpr int kMaxSplits = 256;
 
-// Splits of the longest sequence: until there are several CTAs an SM (ragged lengths even out), but no
-// chunk below two tiles a warp.
+// Splits of the longest sequence: until there are some CTAs for each of the 304 places on the GPU (ragged
+// lengths even out), but no chunk below two tiles a warp.
+constexpr int64_t kWantedCtas = 912;
 // Rows of a CTA: the more, the less often the codes are expanded; up to what the sums leave of the registers
 // (32 of 128 elements, 16 of more).
 int tile_rows_of(int64_t max_new, int group, int D) {
@@ -751,7 +747,7 @@ int tile_rows_of(int64_t max_new, int group, int D) {
 }
 int wanted_splits(int64_t units, int64_t max_len) {
     const int64_t most = (max_len + 2 * kMinChunk - 1) / (2 * kMinChunk);
-    int64_t want = (152 * 4 + units - 1) / units;
+    int64_t want = (kWantedCtas + units - 1) / units;
     want = want < most ? want : most;
     want = want < kMaxSplits ? want : kMaxSplits;
     return (int)(want < 1 ? 1 : want);
