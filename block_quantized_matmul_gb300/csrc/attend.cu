@@ -139,6 +139,8 @@ __device__ __forceinline__ int query_place(int e) {
     return ((e & 12) << 1) | ((e & 16) >> 2) | (k == 1 ? 2 : (k == 2 ? 1 : k));
 }
 
+constexpr int kSorted = 128;               // sequences up to which a CTA sorts them itself
+
 struct Rows {                              // what a CTA works on
     int64_t s, q0, n, first, k0, k1;
     int h, r0, rows, used;
@@ -306,6 +308,21 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
     Rows w;
     w.h = (int)(at % (uint32_t)p.H);
     w.s = at / (uint32_t)p.H;
+    if (p.n_seq > 1 && p.n_seq <= kSorted) {
+        // the longest sequences first: what is started last is then short, and the SMs end together
+        int *lens = reinterpret_cast<int *>(smem), *found = lens + kSorted;
+        for (int i = threadIdx.x; i < (int)p.n_seq; i += kThreads) lens[i] = p.kv_lens[i];
+        __syncthreads();
+        for (int i = threadIdx.x; i < (int)p.n_seq; i += kThreads) {
+            const int n = lens[i];
+            int before = 0;
+            for (int j = 0; j < (int)p.n_seq; ++j) before += lens[j] > n || (lens[j] == n && j < i);
+            if (before == (int)w.s) *found = i;
+        }
+        __syncthreads();
+        w.s = *found;
+        __syncthreads();                                         // the ring may be written
+    }
     w.q0 = p.q_starts[w.s];
     w.nq = p.q_starts[w.s + 1] - w.q0;
     w.n = p.kv_lens[w.s];
@@ -736,9 +753,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
 constexpr int64_t kMinChunk = 8 * kKeys;           // one tile a warp
 constexpr int kMaxSplits = 256;
 
-// Splits of the longest sequence: until there are some CTAs for each of the 304 places on the GPU (ragged
-// lengths even out), but no chunk below two tiles a warp.
-constexpr int64_t kWantedCtas = 912;
+// Splits of the longest sequence: as many as give each of the GPU's 304 places (two an SM) a CTA, but no chunk
+// below two tiles a warp.  Three times as many CTAs measured slower: one token over 500001 tokens 124 us for
+// 97, 304 sequences and heads of 8192 tokens 123 us for 104.
+constexpr int64_t kWantedCtas = 304;
 // Rows of a CTA: the more, the less often the codes are expanded; up to what the sums leave of the registers
 // (32 of 128 elements, 16 of more).
 int tile_rows_of(int64_t max_new, int group, int D) {
