@@ -160,16 +160,29 @@ __device__ __forceinline__ bool sees(const uint64_t *tree, int64_t tok, int i, i
     return tree ? b < 64 && ((tree[tok] >> b) & 1) : b <= i;
 }
 
-// Where a row's result goes: the output when its sequence is not split, else this split's partial.
-__device__ __forceinline__ void write_row(const AttendParams &p, const Rows &w, int sp, int D, int row, int d, float o, float top, float sum) {
-    const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + r % p.group, Hq = p.H * p.group;
+// Where N consecutive elements of a row's result go: the output when its sequence is not split, else this
+// split's partial.
+template <int N>
+__device__ __forceinline__ void write_row(const AttendParams &p, const Rows &w, int sp, int D, int row, int d, const float (&o)[N], float top,
+                                          float sum) {
+    const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + (r - i * p.group), Hq = p.H * p.group;
     const int64_t at = (w.q0 + i) * Hq + hq;
     if (w.used == 1) {
-        store_out(p, (w.q0 + i) * p.ldo + (int64_t)hq * D + d, sum == 0.0f ? 0.0f : o / sum);
+        const int64_t to = (w.q0 + i) * p.ldo + (int64_t)hq * D + d;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        if constexpr (N == 4) {
+            const float a = o[0] * inv, b = o[1] * inv, c = o[2] * inv, e = o[3] * inv;
+            uint16_t *q = static_cast<uint16_t *>(p.out) + to;   // 8-byte aligned
+            *reinterpret_cast<uint2 *>(q) = p.bf16 ? make_uint2(pack2(a, b, __nv_bfloat16{}), pack2(c, e, __nv_bfloat16{}))
+                                                   : make_uint2(pack2(a, b, __half{}), pack2(c, e, __half{}));
+        } else {
+            store_out(p, to, o[0] * inv);
+        }
         if (d == 0 && p.lse) p.lse[at] = sum == 0.0f ? -INFINITY : (top + __log2f(sum) - kBias) * 0.6931471805599453f;
     } else {
         const int64_t part = (int64_t)sp * p.T * Hq + at;
-        p.part_o[part * D + d] = o;
+        if constexpr (N == 4) *reinterpret_cast<float4 *>(p.part_o + part * D + d) = make_float4(o[0], o[1], o[2], o[3]);
+        else p.part_o[part * D + d] = o[0];
         if (d == 0) {
             p.part_ml[2 * part] = top;
             p.part_ml[2 * part + 1] = sum;
@@ -226,7 +239,10 @@ __device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &
         for (int b = 0; b < DB; ++b) fine = fine && fabsf(o[b]) < INFINITY;
         if (__all_sync(0xffffffffu, fine)) continue;
 #pragma unroll
-        for (int b = 0; b < DB; ++b) write_row(p, w, sp, D, row, 32 * b + lane, o[b], top, sum);
+        for (int b = 0; b < DB; ++b) {
+            const float v[1] = {o[b]};
+            write_row(p, w, sp, D, row, 32 * b + lane, v, top, sum);
+        }
     }
 }
 
@@ -661,25 +677,42 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
                 }
     }
     __syncthreads();
-    bool bad = odd != 0;
-    for (int i = threadIdx.x; i < w.rows * D; i += kThreads) {
-        const int row = i / D, d = i % D;
-        float m = -INFINITY;
+    // per row: the factor of each warp's part (in place of its maximum), the maximum and the sum
+    for (int row = threadIdx.x; row < w.rows; row += kThreads) {
+        float m = -INFINITY, l = 0.0f;
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) m = fmaxf(m, w_top[x * kRowsTile + row]);
         const float base = m == -INFINITY ? 0.0f : m;
-        float v = 0.0f, l = 0.0f;
 #pragma unroll
         for (int x = 0; x < kWarps; ++x) {
             const float f = ex2(w_top[x * kRowsTile + row] - base);
             l += f * w_sum[x * kRowsTile + row];
-            v += f * reinterpret_cast<const float *>(smem)[(x * kRowsTile + row) * D + d];
+            w_top[x * kRowsTile + row] = f;
         }
-        if (!(fabsf(v) < INFINITY) || !(l < INFINITY)) {
+        row_mul[row] = m;
+        w_sum[row] = l;                                          // warp 0's, read above by this thread alone
+    }
+    __syncthreads();
+    bool bad = odd != 0;
+    for (int i = threadIdx.x; i < w.rows * (D / 4); i += kThreads) {
+        const int row = i / (D / 4), d = i % (D / 4) * 4;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x) {
+            const float f = w_top[x * kRowsTile + row];
+            const float4 u = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem) + (x * kRowsTile + row) * D + d);
+            v[0] += f * u.x;
+            v[1] += f * u.y;
+            v[2] += f * u.z;
+            v[3] += f * u.w;
+        }
+        const float l = w_sum[row];
+        // 0 times a number that is not finite is NaN, and stays it through the sum
+        if (!(v[0] * 0.0f + v[1] * 0.0f + v[2] * 0.0f + v[3] * 0.0f + l * 0.0f == 0.0f)) {
             bad = true;
             row_bad[row] = 1;
         }
-        write_row(p, w, sp, D, row, d, v, m, l);
+        write_row(p, w, sp, D, row, d, v, row_mul[row], l);
     }
     if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB, NT>(p, w, sp, row_bad);
 }
