@@ -27,35 +27,14 @@
 // the second product would.  So scales past the end, and value scales that are not finite, count as 0
 // there.  Where such a scale (or a value beyond fp16) was met, a plain loop then takes the CTA's rows one
 // by one, and replaces those whose result is not finite by either way; no other cache pays for it.
-#include "cache.cuh"
-#include "elem.cuh"
-#include "pipeline.cuh"
-#include "tc_common.cuh"
+#include "attend.cuh"
 
 namespace qmm {
 namespace {
 
 constexpr int kMmaRows = 8;                // columns of an mma
 constexpr int kKeys = 32;                  // keys of a tile
-constexpr float kBias = 14.0f;             // p is kept times 2^14
 
-struct AttendParams {
-    const uint8_t *k_cache, *v_cache;
-    int64_t n_pages;
-    int P, log_p, H, group, tile_rows, row_tiles, splits;
-    int64_t chunk;                         // keys of a split
-    const int32_t *pages;
-    int64_t ld_pages;
-    const int32_t *q_starts, *kv_lens;
-    int64_t n_seq, T, ldq, ldo;
-    const void *q;
-    const uint64_t *tree;
-    float scale;
-    int bf16;
-    void *out;
-    float *lse;
-    float *part_o, *part_ml;               // [splits][T * Hq][D], [splits][T * Hq][2]
-};
 
 // The 16- or 32-byte units of a tile are permuted so that the fragment loads of a warp meet no bank
 // twice: block b of row r (DB blocks a row) goes to place b ^ swizzle, U units spanning all banks.
@@ -109,20 +88,12 @@ __device__ __forceinline__ void mma16816_first(float (&c)[4], const uint32_t (&a
                  : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.0f));
 }
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // An 8 x 8 matrix of 16-bit values, two of a row to a lane, transposed.
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return tc::h2_bits(__hmul2(tc::bits_h2(a), tc::bits_h2(b))); }
-// Ones in the halves of d that are finite.
-__device__ __forceinline__ uint32_t finite2(uint32_t d) { return __hlt2_mask(__habs2(tc::bits_h2(d)), tc::bits_h2(0x7C007C00u)); }
 // Nibbles 0 and 4 of w (Q4_0 codes) as half2, minus 8: exact.
 __device__ __forceinline__ uint32_t nib_h2(uint32_t w) {
     uint32_t h;
@@ -137,113 +108,6 @@ __device__ __forceinline__ int query_place(int e) {
     if (TYPE == QMM_Q8_0) return e;
     const int k = e & 3;                       // elements 4t, 4t + 2, 4t + 1, 4t + 3, then 16 + those
     return ((e & 12) << 1) | ((e & 16) >> 2) | (k == 1 ? 2 : (k == 2 ? 1 : k));
-}
-
-constexpr int kSorted = 128;               // sequences up to which a CTA sorts them itself
-
-struct Rows {                              // what a CTA works on
-    int64_t s, q0, n, first, k0, k1;
-    int h, r0, rows, used;
-    int64_t nq;
-};
-
-__device__ __forceinline__ float load_q(const AttendParams &p, int64_t at) {
-    return p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q)[at]) : __half2float(static_cast<const __half *>(p.q)[at]);
-}
-__device__ __forceinline__ void store_out(const AttendParams &p, int64_t at, float v) {
-    if (p.bf16) float_to_elem(v, static_cast<__nv_bfloat16 *>(p.out)[at]);
-    else float_to_elem(v, static_cast<__half *>(p.out)[at]);
-}
-
-// Token i of the sequence sees the new token b.
-__device__ __forceinline__ bool sees(const uint64_t *tree, int64_t tok, int i, int64_t b) {
-    return tree ? b < 64 && ((tree[tok] >> b) & 1) : b <= i;
-}
-
-// Where N consecutive elements of a row's result go: the output when its sequence is not split, else this
-// split's partial.
-template <int N>
-__device__ __forceinline__ void write_row(const AttendParams &p, const Rows &w, int sp, int D, int row, int d, const float (&o)[N], float top,
-                                          float sum) {
-    const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + (r - i * p.group), Hq = p.H * p.group;
-    const int64_t at = (w.q0 + i) * Hq + hq;
-    if (w.used == 1) {
-        const int64_t to = (w.q0 + i) * p.ldo + (int64_t)hq * D + d;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        if constexpr (N == 4) {
-            const float a = o[0] * inv, b = o[1] * inv, c = o[2] * inv, e = o[3] * inv;
-            uint16_t *q = static_cast<uint16_t *>(p.out) + to;   // 8-byte aligned
-            *reinterpret_cast<uint2 *>(q) = p.bf16 ? make_uint2(pack2(a, b, __nv_bfloat16{}), pack2(c, e, __nv_bfloat16{}))
-                                                   : make_uint2(pack2(a, b, __half{}), pack2(c, e, __half{}));
-        } else {
-            store_out(p, to, o[0] * inv);
-        }
-        if (d == 0 && p.lse) p.lse[at] = sum == 0.0f ? -INFINITY : (top + __log2f(sum) - kBias) * 0.6931471805599453f;
-    } else {
-        const int64_t part = (int64_t)sp * p.T * Hq + at;
-        if constexpr (N == 4) *reinterpret_cast<float4 *>(p.part_o + part * D + d) = make_float4(o[0], o[1], o[2], o[3]);
-        else p.part_o[part * D + d] = o[0];
-        if (d == 0) {
-            p.part_ml[2 * part] = top;
-            p.part_ml[2 * part + 1] = sum;
-        }
-    }
-}
-
-template <int TYPE>
-__device__ __forceinline__ float cache_value(const uint8_t *chunk, int P, int D, int off, int e) {
-    const int cb = cache_code_bytes(TYPE, D);
-    const float d = __half2float(
-        __ushort_as_half(*reinterpret_cast<const uint16_t *>(chunk + (int64_t)P * cb + ((int64_t)off * (D / 32) + e / 32) * 2)));
-    if constexpr (TYPE == QMM_Q8_0) return d * (float)(int8_t)chunk[(int64_t)off * cb + e];
-    const uint32_t b = chunk[(int64_t)off * cb + e / 32 * 16 + e % 16];
-    return d * (float)((int)((e % 32 < 16 ? b : b >> 4) & 15u) - 8);
-}
-
-// The CTA's rows and keys once more, a warp a row, skipping what the row does not see; rows whose result
-// is finite, and was, keep the one they have.
-template <int TYPE, int DB, int NT>
-__device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &w, int sp, const int *row_bad) {
-    const int lane = threadIdx.x & 31;
-    constexpr int D = DB * 32, kWarps = Tile<TYPE, DB, NT>::kWarps;
-    for (int row = threadIdx.x >> 5; row < w.rows; row += kWarps) {
-        const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + r % p.group;
-        float q[DB], o[DB];
-#pragma unroll
-        for (int b = 0; b < DB; ++b) {
-            q[b] = load_q(p, (w.q0 + i) * p.ldq + (int64_t)hq * D + 32 * b + lane);
-            o[b] = 0.0f;
-        }
-        float top = -INFINITY, sum = 0.0f;                      // in powers of two
-        for (int64_t j = w.k0; j < w.k1; ++j) {
-            if (j >= w.first && !sees(p.tree, w.q0 + i, i, j - w.first)) continue;
-            const int64_t page = p.pages[w.s * p.ld_pages + (j >> p.log_p)];
-            if (page < 0 || page >= p.n_pages) continue;
-            const int64_t at = cache_chunk(TYPE, p.H, D, p.P, page, w.h);
-            const int off = (int)(j & (p.P - 1));
-            float x = 0.0f;
-#pragma unroll
-            for (int b = 0; b < DB; ++b) x += q[b] * cache_value<TYPE>(p.k_cache + at, p.P, D, off, 32 * b + lane);
-#pragma unroll
-            for (int m = 16; m > 0; m >>= 1) x += __shfl_xor_sync(0xffffffffu, x, m);
-            x *= p.scale * 1.4426950408889634f;
-            const float m = fmaxf(top, x), base = m == -INFINITY ? 0.0f : m;
-            const float down = exp2f(top - base), e = exp2f(x - base + kBias);
-            top = m;
-            sum = sum * down + e;
-#pragma unroll
-            for (int b = 0; b < DB; ++b) o[b] = o[b] * down + e * cache_value<TYPE>(p.v_cache + at, p.P, D, off, 32 * b + lane);
-        }
-        bool fine = sum < INFINITY && !row_bad[row];
-#pragma unroll
-        for (int b = 0; b < DB; ++b) fine = fine && fabsf(o[b]) < INFINITY;
-        if (__all_sync(0xffffffffu, fine)) continue;
-#pragma unroll
-        for (int b = 0; b < DB; ++b) {
-            const float v[1] = {o[b]};
-            write_row(p, w, sp, D, row, 32 * b + lane, v, top, sum);
-        }
-    }
 }
 
 // The scales of two neighbouring keys, DB each, as DB words: half i is block i of the first key, half
@@ -316,41 +180,8 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    uint32_t at = blockIdx.x;
-    const int sp = (int)(at % (uint32_t)p.splits);
-    at /= (uint32_t)p.splits;
-    const int rt = (int)(at % (uint32_t)p.row_tiles);
-    at /= (uint32_t)p.row_tiles;
     Rows w;
-    w.h = (int)(at % (uint32_t)p.H);
-    w.s = at / (uint32_t)p.H;
-    if (p.n_seq > 1 && p.n_seq <= kSorted) {
-        // the longest sequences first: what is started last is then short, and the SMs end together
-        int *lens = reinterpret_cast<int *>(smem), *found = lens + kSorted;
-        for (int i = threadIdx.x; i < (int)p.n_seq; i += kThreads) lens[i] = p.kv_lens[i];
-        __syncthreads();
-        for (int i = threadIdx.x; i < (int)p.n_seq; i += kThreads) {
-            const int n = lens[i];
-            int before = 0;
-            for (int j = 0; j < (int)p.n_seq; ++j) before += lens[j] > n || (lens[j] == n && j < i);
-            if (before == (int)w.s) *found = i;
-        }
-        __syncthreads();
-        w.s = *found;
-        __syncthreads();                                         // the ring may be written
-    }
-    w.q0 = p.q_starts[w.s];
-    w.nq = p.q_starts[w.s + 1] - w.q0;
-    w.n = p.kv_lens[w.s];
-    w.r0 = rt * kRowsTile;
-    w.rows = (int)min((int64_t)kRowsTile, w.nq * p.group - w.r0);
-    if (w.rows <= 0) return;
-    w.first = w.n - w.nq;
-    w.n = max((int64_t)0, min(w.n, p.ld_pages << p.log_p));
-    w.used = (int)min((int64_t)p.splits, max((int64_t)1, (w.n + p.chunk - 1) / p.chunk));
-    if (sp >= w.used) return;
-    w.k0 = sp * p.chunk;
-    w.k1 = sp == p.splits - 1 ? w.n : min(w.n, w.k0 + p.chunk);
+    if (!find_rows<kRowsTile>(p, reinterpret_cast<int *>(smem), kThreads, w)) return;
 
     // ---- the ring: tile i of this warp is keys k0 + 32 * (kWarps i + warp) .. ----
     const uint32_t ring = pipe::smem_u32(smem) + (uint32_t)(warp * S * L::kBytes);
@@ -712,9 +543,9 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
             bad = true;
             row_bad[row] = 1;
         }
-        write_row(p, w, sp, D, row, d, v, row_mul[row], l);
+        write_row(p, w, D, row, d, v, row_mul[row], l);
     }
-    if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB, NT>(p, w, sp, row_bad);
+    if (__syncthreads_or(bad)) rows_one_by_one<TYPE, DB, kWarps>(p, w, row_bad);
 }
 
 // Joins the partial results of the sequences that were split.  WPR warps take a row, each the splits of
@@ -790,15 +621,15 @@ constexpr int kMaxSplits = 256;
 // below two tiles a warp.  Three times as many CTAs measured slower: one token over 500001 tokens 124 us for
 // 97, 304 sequences and heads of 8192 tokens 123 us for 104.
 constexpr int64_t kWantedCtas = 304;
-// Rows of a CTA: the more, the less often the codes are expanded; up to what the sums leave of the registers
-// (32 of 128 elements, 16 of more).
+// Rows of a CTA: 8 or 16 on mma; where there are more, and a head is at most 128 elements, 128 on tcgen05.
 int tile_rows_of(int64_t max_new, int group, int D) {
     const int64_t rows = max_new * group;
-    return rows <= kMmaRows ? kMmaRows : (rows <= 2 * kMmaRows || D > 128 ? 2 * kMmaRows : 4 * kMmaRows);
+    return rows <= kMmaRows ? kMmaRows : (rows <= 2 * kMmaRows || D > 128 ? 2 * kMmaRows : kTcRows);
 }
-int wanted_splits(int64_t units, int64_t max_len) {
-    const int64_t most = (max_len + 2 * kMinChunk - 1) / (2 * kMinChunk);
-    int64_t want = (kWantedCtas + units - 1) / units;
+int wanted_splits(int64_t units, int64_t max_len, int tile_rows) {
+    const int64_t least = tile_rows == kTcRows ? 256 : 2 * kMinChunk, places = tile_rows == kTcRows ? 152 : kWantedCtas;
+    const int64_t most = (max_len + least - 1) / least;
+    int64_t want = tile_rows == kTcRows ? places / units : (places + units - 1) / units;
     want = want < most ? want : most;
     want = want < kMaxSplits ? want : kMaxSplits;
     return (int)(want < 1 ? 1 : want);
@@ -817,40 +648,29 @@ cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
     static int attr_done[4] = {0, 0, 0, 0};
     cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
     if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)ctas), L::kThreads, L::kSmem, s, p);
-    if (e != cudaSuccess || p.splits == 1) return e;
+    return launch_pdl(kern, dim3((unsigned)ctas), L::kThreads, L::kSmem, s, p);
+}
+
+template <int DB>
+cudaError_t launch_join(const AttendParams &p, cudaStream_t s) {
     const int64_t rows = p.T * p.H * p.group;
     if (p.splits > kJoinWarps) return launch_pdl(attend_join_kernel<DB, kJoinWarps>, dim3((unsigned)rows), kJoinWarps * 32, 0, s, p);
     return launch_pdl(attend_join_kernel<DB, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, p);
 }
 
-template <int TYPE, int DB>
-cudaError_t launch_rows(const AttendParams &p, int64_t ctas, cudaStream_t s) {
-    if (p.tile_rows == kMmaRows) return launch_typed<TYPE, DB, 1>(p, ctas, s);
-    if constexpr (DB <= 4) {
-        if (p.tile_rows == 4 * kMmaRows) return launch_typed<TYPE, DB, 4>(p, ctas, s);
-    }
-    return launch_typed<TYPE, DB, 2>(p, ctas, s);
-}
-
-template <int TYPE>
-cudaError_t launch_blocks(const AttendParams &p, int DB, int64_t ctas, cudaStream_t s) {
-    switch (DB) {
-        case 1: return launch_rows<TYPE, 1>(p, ctas, s);
-        case 2: return launch_rows<TYPE, 2>(p, ctas, s);
-        case 3: return launch_rows<TYPE, 3>(p, ctas, s);
-        case 4: return launch_rows<TYPE, 4>(p, ctas, s);
-        case 5: return launch_rows<TYPE, 5>(p, ctas, s);
-        case 6: return launch_rows<TYPE, 6>(p, ctas, s);
-        case 7: return launch_rows<TYPE, 7>(p, ctas, s);
-        default: return launch_rows<TYPE, 8>(p, ctas, s);
-    }
+template <int DB>
+cudaError_t launch_blocks(qmm_type type, const AttendParams &p, int64_t ctas, cudaStream_t s) {
+    cudaError_t e;
+    if (p.tile_rows == kTcRows) e = launch_attend_tc(type, p, DB, ctas, s);
+    else if (type == QMM_Q8_0) e = p.tile_rows == kMmaRows ? launch_typed<QMM_Q8_0, DB, 1>(p, ctas, s) : launch_typed<QMM_Q8_0, DB, 2>(p, ctas, s);
+    else e = p.tile_rows == kMmaRows ? launch_typed<QMM_Q4_0, DB, 1>(p, ctas, s) : launch_typed<QMM_Q4_0, DB, 2>(p, ctas, s);
+    return e != cudaSuccess || p.splits == 1 ? e : launch_join<DB>(p, s);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int64_t n_seq, int64_t max_new, int H, int Hq, int D, int64_t max_len) {
-    const int splits = wanted_splits(n_seq * H * row_tiles_of(max_new, Hq / H, D), max_len);
+    const int splits = wanted_splits(n_seq * H * row_tiles_of(max_new, Hq / H, D), max_len, tile_rows_of(max_new, Hq / H, D));
     return splits == 1 ? 0 : (size_t)splits * split_bytes(n_seq * max_new * Hq, D);
 }
 
@@ -888,7 +708,7 @@ cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uin
     p.out = out;
     p.lse = lse;
     const size_t per_split = split_bytes(T * Hq, D);
-    p.splits = wanted_splits(units, max_len);
+    p.splits = wanted_splits(units, max_len, p.tile_rows);
     if ((size_t)p.splits * per_split > ws_bytes) p.splits = (int)(ws_bytes / per_split);
     if (p.splits < 2) {
         p.splits = 1;
@@ -900,7 +720,16 @@ cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uin
     }
     const int64_t ctas = units * p.splits;
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
-    return type == QMM_Q8_0 ? launch_blocks<QMM_Q8_0>(p, D / 32, ctas, s) : launch_blocks<QMM_Q4_0>(p, D / 32, ctas, s);
+    switch (D / 32) {
+        case 1: return launch_blocks<1>(type, p, ctas, s);
+        case 2: return launch_blocks<2>(type, p, ctas, s);
+        case 3: return launch_blocks<3>(type, p, ctas, s);
+        case 4: return launch_blocks<4>(type, p, ctas, s);
+        case 5: return launch_blocks<5>(type, p, ctas, s);
+        case 6: return launch_blocks<6>(type, p, ctas, s);
+        case 7: return launch_blocks<7>(type, p, ctas, s);
+        default: return launch_blocks<8>(type, p, ctas, s);
+    }
 }
 
 QMM_DCHECK_READER(read_dcheck_attend)

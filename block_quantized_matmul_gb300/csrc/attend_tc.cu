@@ -1,0 +1,553 @@
+// attend_tc.cu -- attention over the block-quantized cache for more rows than a decode step has (trees of
+// drafted tokens, pieces of a prompt), on tcgen05: 128 rows (new token x query head of one key/value head)
+// to a CTA, heads of up to 128 elements.
+//
+// The formulas, masks and partial results are those of attend.cu.  With 128 rows the cost is no longer the
+// cache's bytes but expanding its codes and the exponentials, so the codes are expanded once a CTA, into
+// shared memory, and both products run on the tensor cores from there:
+//   S [128 rows x 128 keys] = Q K^T   A = Q, B = K, both K-major in shared memory, S in tensor memory;
+//   O [128 rows x D]       = P V      A = P from tensor memory, B = V^T (K-major over the keys).
+// A row is a lane of tensor memory and a thread, so that a row's maximum, sum and output need no exchange
+// between threads.  The output stays in registers: the product of each tile is read back and added there,
+// scaled by how far the maximum has moved since.
+//
+// Arithmetic.  k = d * q is split exactly into two fp16 terms, k = hi + lo with hi = fp16(k), which both take part
+// (hi alone put 1e-5 into a row's log-sum); v = d * q is rounded to fp16 (2^-12); the query row is scaled by a power
+// of two into fp16's range; p is kept in fp16 times 2^14; all sums are fp32.
+//
+// The raw codes of two tiles of keys come through a ring of asynchronous copies; a key's codes are padded to
+// an odd number of 16-byte pieces, so that a warp's 32 keys meet no bank twice.  V^T is written two keys to
+// a word: slots 2l and 2l + 1 of a chunk of 64 are keys l and l + 32, the lanes of one load, and K's rows
+// (and so the columns of S and p) are in that order too.
+//
+// Warps: 0-3 rows (softmax, output; warp 0 issues the products too), 4-7 codes, up to two tiles of keys ahead.
+// (A ninth warp for the products would leave 168 registers a thread, and the rows need some 200.)
+// Tensor memory (512 columns): S twice 128, P twice 64, O 128.
+// Every wait is bounded; on expiry the kernel records QMM_ERR_TIMEOUT, lets its products land, frees
+// tensor memory and returns.
+#include <cuda.h>
+
+#include "qmm_internal.cuh"
+
+#include "attend.cuh"
+
+namespace qmm {
+namespace {
+
+__device__ unsigned g_attend_status = 0;   // bit 0: a bounded wait gave up
+
+using namespace pipe;
+using namespace tc;
+
+constexpr int kKeysTc = 128;
+constexpr int kThreadsTc = 256;
+constexpr int kColS = 0, kColP = 256, kColO = 384;
+
+template <int TYPE, int DB>
+struct TcPlan {
+    static constexpr int D = DB * 32, CB = DB * (TYPE == QMM_Q8_0 ? 32 : 16);
+    static constexpr int NC = (DB + 1) / 2;                // chunks of 64 elements: 128-byte rows
+    static constexpr int kChunk = 128 * 128;               // 128 rows of one
+    static constexpr int kVChunk = D * 128;                // D rows of 64 keys
+    static constexpr int PK = CB / 16, kPitch = (PK | 1) * 16;     // 16-byte pieces of a key's codes, and its pitch
+    static constexpr int kQ = 0, kK = kQ + NC * kChunk, kV = kK + 2 * NC * kChunk;   // K: hi, then lo
+    static constexpr int kRaw = kV + 2 * kVChunk;          // two stages of: K codes, V codes, K scales, V scales
+    static constexpr int kRawV = 128 * kPitch, kRawKs = 2 * 128 * kPitch, kRawVs = kRawKs + 128 * DB * 2, kRawBytes = kRawVs + 128 * DB * 2;
+    static constexpr int kBad = kRaw + 2 * kRawBytes;      // rows whose result is not finite
+    static constexpr int kBars = kBad + kTcRows * 4;
+    static constexpr int kNumBars = 15;
+    static constexpr size_t kSmem = 1024 + kBars + kNumBars * 8 + 16;
+    static_assert(kSmem <= 227 * 1024, "shared memory plan too large");
+};
+
+__device__ __forceinline__ bool wait_tc(uint32_t bar, uint32_t parity, volatile int *abort) {
+    return __all_sync(0xffffffffu, wait_bounded_on(bar, parity, abort, &g_attend_status, kWaitLimitNs));
+}
+
+__device__ __forceinline__ void tmem_ld32x(uint32_t taddr, uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,"
+        "%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+    // the wait writes the registers too, so that no use of them can be scheduled before it
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]),
+                   "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+    asm volatile(""
+                 : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                   "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Four unsigned bytes (codes of up to 8 bits) as two half2 of 1024 + byte, minus `off` in both halves.
+__device__ __forceinline__ void bytes_h2(uint32_t x, uint32_t off, uint32_t &lo, uint32_t &hi) {
+    lo = h2_bits(__hsub2(bits_h2(__byte_perm(x, 0x64646464u, 0x4140u)), bits_h2(off)));
+    hi = h2_bits(__hsub2(bits_h2(__byte_perm(x, 0x64646464u, 0x4342u)), bits_h2(off)));
+}
+constexpr uint32_t kOff8 = 0x64806480u;    // 1152: int8 codes with the sign bit flipped
+constexpr uint32_t kOff4 = 0x64086408u;    // 1032: nibbles
+
+template <int TYPE, int DB>
+__global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_constant__ AttendParams p) {
+    using L = TcPlan<TYPE, DB>;
+    constexpr int D = L::D, CB = L::CB, NC = L::NC;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    int *row_bad = reinterpret_cast<int *>(smem + L::kBad);
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
+    uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 2, *v_full = bars + 3, *v_empty = bars + 4, *s_full = bars + 5,
+             *p_full = bars + 7, *o_full = bars + 9, *done = bars + 10, *raw_full = bars + 11, *raw_empty = bars + 13;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kNumBars);
+    volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    int *odd_flag = reinterpret_cast<int *>(tmem_slot + 2);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    Rows w;
+    if (!find_rows<kTcRows>(p, reinterpret_cast<int *>(smem), kThreadsTc, w)) return;
+
+    if (threadIdx.x == 0) {
+        mbar_init(smem_u32(q_full), kTcRows);
+        mbar_init(smem_u32(done), 1);
+        mbar_init(smem_u32(k_full), 128);
+        mbar_init(smem_u32(k_empty), 1);
+        mbar_init(smem_u32(v_full), 128);
+        mbar_init(smem_u32(v_empty), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(smem_u32(&s_full[s]), 1);
+            mbar_init(smem_u32(&p_full[s]), kTcRows);
+            mbar_init(smem_u32(&raw_full[s]), 128);
+            mbar_init(smem_u32(&raw_empty[s]), 128);
+        }
+        mbar_init(smem_u32(o_full), 1);
+        *abort = 0;
+        *odd_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (threadIdx.x < kTcRows) row_bad[threadIdx.x] = 0;
+    __syncwarp();
+    if (warp == 0) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int tiles = (int)((w.k1 - w.k0 + kKeysTc - 1) / kKeysTc);
+    const int32_t *table = p.pages + w.s * p.ld_pages;
+    // pages of a tile's eight groups of 16 keys, in lanes 0-7 (-1: past the keys)
+    auto pages_of = [&](int i) -> int {
+        const int64_t j = w.k0 + (int64_t)i * kKeysTc + 16 * (lane & 7);
+        const int page = i < tiles && j < w.k1 ? table[j >> p.log_p] : -1;
+        return page < p.n_pages ? page : -1;
+    };
+
+    if (warp < 4) {
+        // =============================== rows ===============================
+        const int row = threadIdx.x;                           // = lane of tensor memory
+        const uint32_t t_lane = tmem + ((uint32_t)(32 * warp) << 16);
+        const int64_t r = w.r0 + row, i_tok = r / p.group;
+        float mul = 1.0f;
+        {
+            // the query row, scaled by a power of two so that its largest element lies in [1, 2)
+            uint4 raw[4 * DB];
+            const int64_t base = (w.q0 + i_tok) * p.ldq + (w.h * p.group + (r - i_tok * p.group)) * D;
+#pragma unroll
+            for (int c = 0; c < 4 * DB; ++c)
+                raw[c] = row < w.rows ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + base + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
+            uint32_t top2 = 0;
+#pragma unroll
+            for (int c = 0; c < 4 * DB; ++c) {
+                const uint32_t x = __vmaxu2(raw[c].x & 0x7FFF7FFFu, raw[c].y & 0x7FFF7FFFu), y = __vmaxu2(raw[c].z & 0x7FFF7FFFu, raw[c].w & 0x7FFF7FFFu);
+                top2 = __vmaxu2(top2, __vmaxu2(x, y));
+            }
+            const uint32_t topb = max(top2 & 0xFFFFu, top2 >> 16);
+            const float top = p.bf16 ? bits_to_float<__nv_bfloat16>(topb) : bits_to_float<__half>(topb);
+            const int e = top > 0.0f && top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
+            const float m = p.scale * 1.4426950408889634f, down = copysignf(exp2f((float)-e), m);
+            mul = fmaxf(fabsf(m), 1e-30f) * exp2f((float)e);   // a scale of 0 still has to order -inf below 0
+#pragma unroll
+            for (int c = 0; c < 8 * NC; ++c) {
+                uint32_t h[4] = {0u, 0u, 0u, 0u};
+                if (c < 4 * DB) {
+                    const uint32_t x[4] = {raw[c < 4 * DB ? c : 0].x, raw[c < 4 * DB ? c : 0].y, raw[c < 4 * DB ? c : 0].z, raw[c < 4 * DB ? c : 0].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = p.bf16 ? unpack2(x[k], __nv_bfloat16{}) : unpack2(x[k], __half{});
+                        h[k] = pack2(f.x * down, f.y * down, __half{});
+                    }
+                }
+                *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * L::kChunk + sw128_off(row, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(q_full));
+        }
+        // ---- products, by one thread of warp 0 ----
+        bool lead = false;
+        if (warp == 0) {
+            uint32_t e;
+            asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+            lead = e != 0;
+        }
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::kQ)), k_desc = smem_desc_sw128(smem_u32(smem + L::kK)),
+                       v_desc = smem_desc_sw128(smem_u32(smem + L::kV));
+        constexpr uint32_t id_s = idesc_f16(128, kKeysTc), id_o = idesc_f16(128, D);
+        auto scores = [&](int i) -> bool {
+            const int b = i & 1;
+            if (!wait_tc(smem_u32(k_full), (uint32_t)(i & 1), abort)) return false;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+                for (int k = 0; k < 4 * DB; ++k) {              // 16 elements a step, of hi, then of lo
+                    const int term = k / (2 * DB), e = k % (2 * DB);
+                    const uint64_t at = (uint64_t)((e >> 2) * (L::kChunk >> 4) + 2 * (e & 3));
+                    mma_f16_ss(tmem + kColS + 128 * b, q_desc + at, k_desc + at + (uint64_t)(term * NC * (L::kChunk >> 4)), id_s,
+                               k > 0 ? 1u : 0u);
+                }
+                mma_commit(smem_u32(k_empty));
+                mma_commit(smem_u32(&s_full[b]));
+            }
+            __syncwarp();
+            return true;
+        };
+        // all rows have given p of tile i, and have read S of tile i and the product of tile i - 1
+        auto values = [&](int i) -> bool {
+            const int b = i & 1;
+            if (!wait_tc(smem_u32(&p_full[b]), (uint32_t)((i >> 1) & 1), abort)) return false;
+            if (!wait_tc(smem_u32(v_full), (uint32_t)(i & 1), abort)) return false;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {                   // 16 keys a step
+                    const uint64_t at = (uint64_t)((k >> 2) * (L::kVChunk >> 4) + 2 * (k & 3));
+                    mma_f16_ts(tmem + kColO, tmem + kColP + 64 * b + 8 * k, v_desc + at, id_o, k > 0 ? 1u : 0u);
+                }
+                mma_commit(smem_u32(v_empty));
+                mma_commit(smem_u32(o_full));
+            }
+            __syncwarp();
+            return true;
+        };
+        const uint64_t word = p.tree && row < w.rows ? p.tree[w.q0 + i_tok] : 0;
+        float o[D];
+#pragma unroll
+        for (int d = 0; d < D; ++d) o[d] = 0.0f;
+        float top = -INFINITY, sum = 0.0f, back = 1.0f;       // back: what the pending product's row is scaled by
+        bool ok = true;
+        // adds the product of tile i: o and it are relative to the maximum after tile i
+        auto add = [&](int i) {
+            ok = wait_tc(smem_u32(o_full), (uint32_t)(i & 1), abort);
+            if (!ok) return;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < DB; ++c) {
+                uint32_t v[32];
+                tmem_ld32x(t_lane + kColO + 32 * c, v);
+#pragma unroll
+                for (int d = 0; d < 32; ++d) o[32 * c + d] = fmaf(o[32 * c + d], back, __uint_as_float(v[d]));
+            }
+        };
+        if (warp == 0 && tiles > 0) ok = wait_tc(smem_u32(q_full), 0u, abort) && scores(0);
+        int page = pages_of(0);
+        for (int i = 0; i < tiles && ok; ++i) {
+            const int b = i & 1;
+            const int64_t j0 = w.k0 + (int64_t)i * kKeysTc;
+            const uint32_t groups = __ballot_sync(0xffffffffu, lane < 8 && page >= 0);
+            page = pages_of(i + 1);
+            // the next tile's scores are under way during this one's exponentials
+            if (warp == 0 && i + 1 < tiles && !scores(i + 1)) { ok = false; break; }
+            if (!wait_tc(smem_u32(&s_full[b]), (uint32_t)((i >> 1) & 1), abort)) { ok = false; break; }
+            tc_fence_after();
+            const bool masked = groups != 0xFFu || j0 + kKeysTc > w.k1 || j0 + kKeysTc > w.first;
+            // keys 32c .. 32c + 31 of this tile that the row sees
+            auto keys = [&](int c) -> uint32_t {
+                uint32_t m = ((groups >> (2 * c)) & 1 ? 0xFFFFu : 0u) | ((groups >> (2 * c + 1)) & 1 ? 0xFFFF0000u : 0u);
+                const int64_t left = w.k1 - (j0 + 32 * c);      // keys of the split from here on
+                m &= left >= 32 ? 0xFFFFFFFFu : (left <= 0 ? 0u : (1u << (int)left) - 1u);
+                const int64_t nb = j0 + 32 * c - w.first;       // place of the first key among the new tokens
+                if (nb > -32) {
+                    uint32_t v;                                  // the row's view of new tokens nb .. nb + 31
+                    if (p.tree) {
+                        v = nb >= 64 ? 0u : (nb >= 0 ? (uint32_t)(word >> nb) : (uint32_t)(word << -nb) | ((1u << -nb) - 1u));
+                    } else {
+                        const int64_t upto = i_tok - nb + 1;     // it sees that many of them
+                        v = upto >= 32 ? 0xFFFFFFFFu : (upto <= 0 ? 0u : (1u << (int)upto) - 1u);
+                    }
+                    m &= v;
+                }
+                return m;
+            };
+            // the same for columns 32c .. 32c + 31: column k is key 16 (c & 1) + k / 2 of the chunk, plus 32 if k is odd
+            auto seen = [&](int c) -> uint32_t {
+                uint32_t e = keys(c & 2) >> (16 * (c & 1)) & 0xFFFFu, o2 = keys((c & 2) + 1) >> (16 * (c & 1)) & 0xFFFFu;
+#pragma unroll
+                for (int z = 8; z > 0; z >>= 1) {               // spreads the 16 bits to every second place
+                    const uint32_t keep = z == 8 ? 0x00FF00FFu : (z == 4 ? 0x0F0F0F0Fu : (z == 2 ? 0x33333333u : 0x55555555u));
+                    e = (e | (e << z)) & keep;
+                    o2 = (o2 | (o2 << z)) & keep;
+                }
+                return e | (o2 << 1);
+            };
+            float m = -INFINITY;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32];
+                tmem_ld32x(t_lane + kColS + 128 * b + 32 * c, v);
+                if (masked) {
+                    const uint32_t bits = seen(c);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k)
+                        if ((bits >> k) & 1) m = fmaxf(m, __uint_as_float(v[k]));
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) m = fmaxf(m, __uint_as_float(v[k]));
+                }
+            }
+            m = fmaxf(m * mul, top);
+            const float base = m == -INFINITY ? 0.0f : m, down = ex2(top - base), shift = kBias - base;
+            top = m;
+            sum *= down;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint32_t v[32], h[16];
+                tmem_ld32x(t_lane + kColS + 128 * b + 32 * c, v);
+                const uint32_t bits = masked ? seen(c) : 0xFFFFFFFFu;
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    float p0 = ex2(fmaf(__uint_as_float(v[2 * k]), mul, shift)), p1 = ex2(fmaf(__uint_as_float(v[2 * k + 1]), mul, shift));
+                    if (masked) {
+                        p0 = (bits >> (2 * k)) & 1 ? p0 : 0.0f;
+                        p1 = (bits >> (2 * k + 1)) & 1 ? p1 : 0.0f;
+                    }
+                    sum += p0 + p1;
+                    h[k] = pack2(p0, p1, __half{});
+                }
+                tmem_st16(t_lane + kColP + 64 * b + 16 * c, h);
+            }
+            if (i > 0) add(i - 1);
+            if (!ok) break;
+            back = down;
+            tmem_wait_st();
+            tc_fence_before();
+            mbar_arrive(smem_u32(&p_full[b]));
+            if (warp == 0 && !values(i)) { ok = false; break; }
+        }
+        if (ok && tiles > 0) add(tiles - 1);
+        if (lead) {
+            // every product issued has landed before tensor memory is released
+            mma_commit(smem_u32(done));
+            wait_drain(smem_u32(done), 0u);
+        }
+        // ---- the row's result ----
+        float all = sum * 0.0f;                                 // 0 unless something is not finite
+#pragma unroll
+        for (int d = 0; d < D; ++d) all = fmaf(o[d], 0.0f, all);
+        if (row < w.rows) {
+            if (!(all == 0.0f)) {
+                row_bad[row] = 1;
+                *odd_flag = 1;
+            }
+#pragma unroll
+            for (int d = 0; d < D; d += 4) {
+                const float v[4] = {o[d], o[d + 1], o[d + 2], o[d + 3]};
+                write_row(p, w, D, row, d, v, top, sum);
+            }
+        }
+    } else if (warp < 8) {
+        // =============================== codes ===============================
+        const int tid = threadIdx.x - 128, wq = warp - 4;
+        constexpr int PK = L::PK, VP = (PK + 1) / 2;            // pieces of a key; of V for a warp: every second one of 64 keys
+        const int64_t head = (int64_t)w.h * p.P * (CB + 2 * DB), page_bytes = (int64_t)p.H * p.P * (CB + 2 * DB);
+        bool odd = false;
+        // copies the raw codes and scales of tile i; `page`: its pages, in lanes 0-7
+        auto issue = [&](int i, int page) {
+            if (i < tiles) {
+                const uint32_t st = smem_u32(smem + L::kRaw + (i & 1) * L::kRawBytes);
+                const int off0 = (int)(w.k0 + (int64_t)i * kKeysTc) & (p.P - 1);      // P may be below 128
+#pragma unroll
+                for (int it = 0; it < PK; ++it) {
+                    const int u = it * 128 + tid, key = u / PK, c = u % PK;
+                    const int pg = __shfl_sync(0xffffffffu, page, key >> 4);
+                    if (pg >= 0) {
+                        const int64_t at = (int64_t)pg * page_bytes + head + ((off0 + key) & (p.P - 1)) * CB + 16 * c;
+                        cp_async16(st + key * L::kPitch + 16 * c, p.k_cache + at);
+                        cp_async16(st + L::kRawV + key * L::kPitch + 16 * c, p.v_cache + at);
+                    }
+                }
+                // scales: 2 * DB pieces for each group of 16 keys
+                const int grp = tid / (2 * DB), c = tid % (2 * DB);
+                const int pg = __shfl_sync(0xffffffffu, page, grp & 7);
+                if (grp < 8 && pg >= 0) {
+                    const int64_t at = (int64_t)pg * page_bytes + head + p.P * CB + ((off0 + 16 * grp) & (p.P - 1)) * (2 * DB) + 16 * c;
+                    cp_async16(st + L::kRawKs + tid * 16, p.k_cache + at);
+                    cp_async16(st + L::kRawVs + tid * 16, p.v_cache + at);
+                }
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(smem_u32(&raw_full[i & 1])) : "memory");
+        };
+        auto valid = [&](int i, int key, uint32_t groups) { return (groups >> (key >> 4) & 1) && w.k0 + (int64_t)i * kKeysTc + key < w.k1; };
+        auto convert_k = [&](int i, uint32_t groups) {
+            const uint8_t *raw = smem + L::kRaw + (i & 1) * L::kRawBytes;
+            const uint16_t *ks = reinterpret_cast<const uint16_t *>(raw + L::kRawKs);
+#pragma unroll
+            for (int it = 0; it < PK; ++it) {
+                const int u = it * 128 + tid, key = u / PK, c = u % PK;
+                const uint32_t d2 = valid(i, key, groups) ? ks[key * DB + (TYPE == QMM_Q8_0 ? c >> 1 : c)] * 0x00010001u : 0u;
+                const uint4 v4 = *reinterpret_cast<const uint4 *>(raw + key * L::kPitch + 16 * c);
+                const uint32_t x[4] = {v4.x, v4.y, v4.z, v4.w};
+                const int slot = (key & 64) | ((key & 31) << 1) | ((key >> 5) & 1);
+                auto store = [&](int chunk, const uint32_t *h) {   // 8 elements
+                    uint8_t *at = smem + L::kK + (chunk >> 3) * L::kChunk + sw128_off(slot, chunk & 7);
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const __half2 v = __hmul2_rn(bits_h2(h[z]), bits_h2(d2));
+                        hi[z] = h2_bits(v);
+                        lo[z] = h2_bits(__hfma2(bits_h2(h[z]), bits_h2(d2), __hneg2(v)));     // exact
+                    }
+                    *reinterpret_cast<uint4 *>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4 *>(at + NC * L::kChunk) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                };
+                if constexpr (TYPE == QMM_Q8_0) {
+                    uint32_t h[8];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) bytes_h2(x[k] ^ 0x80808080u, kOff8, h[2 * k], h[2 * k + 1]);
+                    store(2 * c, h);
+                    store(2 * c + 1, h + 4);
+                } else {
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {               // elements 0-15 in the low nibbles, 16-31 in the high ones
+                        uint32_t h[8];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) bytes_h2((x[k] >> (4 * n)) & 0x0F0F0F0Fu, kOff4, h[2 * k], h[2 * k + 1]);
+                        store(4 * c + 2 * n, h);
+                        store(4 * c + 2 * n + 1, h + 4);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(k_full));
+        };
+        auto convert_v = [&](int i, uint32_t groups) {
+            const uint8_t *raw = smem + L::kRaw + (i & 1) * L::kRawBytes;
+            const uint16_t *vs = reinterpret_cast<const uint16_t *>(raw + L::kRawVs);
+            const int ka = 64 * (wq & 1) + lane, kb = ka + 32;     // slots 2 lane and 2 lane + 1
+            const uint32_t have = (valid(i, ka, groups) ? 0xFFFFu : 0u) | (valid(i, kb, groups) ? 0xFFFF0000u : 0u);
+            uint8_t *vt = smem + L::kV + (wq & 1) * L::kVChunk + (lane & 3) * 4;
+#pragma unroll
+            for (int it = 0; it < VP; ++it) {
+                const int c = 2 * it + (wq >> 1), blk = TYPE == QMM_Q8_0 ? c >> 1 : c;
+                if (c >= PK) break;
+                uint32_t d2 = have & ((uint32_t)vs[ka * DB + blk] | ((uint32_t)vs[kb * DB + blk] << 16));
+                const uint32_t fine = finite2(d2);
+                odd |= fine != 0xFFFFFFFFu;
+                d2 &= fine;
+                const uint4 a4 = *reinterpret_cast<const uint4 *>(raw + L::kRawV + ka * L::kPitch + 16 * c);
+                const uint4 b4 = *reinterpret_cast<const uint4 *>(raw + L::kRawV + kb * L::kPitch + 16 * c);
+                const uint32_t xa[4] = {a4.x, a4.y, a4.z, a4.w}, xb[4] = {b4.x, b4.y, b4.z, b4.w};
+                auto store4 = [&](int d0, uint32_t a, uint32_t bq, uint32_t off) {   // elements d0 .. d0 + 3 of both keys
+                    uint32_t h[4];
+                    bytes_h2(__byte_perm(a, bq, 0x5140), off, h[0], h[1]);
+                    bytes_h2(__byte_perm(a, bq, 0x7362), off, h[2], h[3]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) *reinterpret_cast<uint32_t *>(vt + sw128_off(d0 + k, lane >> 2)) = hmul2(h[k], d2);
+                };
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    if constexpr (TYPE == QMM_Q8_0) {
+                        store4(16 * c + 4 * k, xa[k] ^ 0x80808080u, xb[k] ^ 0x80808080u, kOff8);
+                    } else {
+                        store4(32 * c + 4 * k, xa[k] & 0x0F0F0F0Fu, xb[k] & 0x0F0F0F0Fu, kOff4);
+                        store4(32 * c + 16 + 4 * k, (xa[k] >> 4) & 0x0F0F0F0Fu, (xb[k] >> 4) & 0x0F0F0F0Fu, kOff4);
+                    }
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(v_full));
+        };
+        int pg0 = pages_of(0), pg1 = pages_of(1), pg2 = pages_of(2);       // of tiles i, i + 1, i + 2
+        issue(0, pg0);
+        issue(1, pg1);
+        if (tiles > 0 && wait_tc(smem_u32(&raw_full[0]), 0u, abort)) {
+            convert_k(0, __ballot_sync(0xffffffffu, lane < 8 && pg0 >= 0));
+            for (int i = 0; i < tiles; ++i) {
+                const uint32_t groups = __ballot_sync(0xffffffffu, lane < 8 && pg0 >= 0);
+                // the keys of the next tile once the scores of this one are computed, then this one's values
+                if (i + 1 < tiles) {
+                    if (!wait_tc(smem_u32(&raw_full[(i + 1) & 1]), (uint32_t)(((i + 1) >> 1) & 1), abort)) break;
+                    if (!wait_tc(smem_u32(k_empty), (uint32_t)(i & 1), abort)) break;
+                    convert_k(i + 1, __ballot_sync(0xffffffffu, lane < 8 && pg1 >= 0));
+                }
+                if (i > 0 && !wait_tc(smem_u32(v_empty), (uint32_t)((i - 1) & 1), abort)) break;
+                convert_v(i, groups);
+                mbar_arrive(smem_u32(&raw_empty[i & 1]));
+                if (i + 2 < tiles) {
+                    if (!wait_tc(smem_u32(&raw_empty[i & 1]), (uint32_t)((i >> 1) & 1), abort)) break;
+                    issue(i + 2, pg2);
+                }
+                pg0 = pg1;
+                pg1 = pg2;
+                pg2 = pages_of(i + 3);
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        if (odd) *odd_flag = 1;
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+    }
+    if (*odd_flag) rows_one_by_one<TYPE, DB, kThreadsTc / 32>(p, w, row_bad);
+}
+
+template <int TYPE, int DB>
+cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
+    auto kern = attend_tc_kernel<TYPE, DB>;
+    static int attr_done[4] = {0, 0, 0, 0};
+    const cudaError_t e = ensure_smem_limit(kern, TcPlan<TYPE, DB>::kSmem, attr_done);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)ctas), kThreadsTc, TcPlan<TYPE, DB>::kSmem, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_attend_tc(qmm_type type, const AttendParams &p, int DB, int64_t ctas, cudaStream_t s) {
+    if (type == QMM_Q8_0) {
+        switch (DB) {
+            case 1: return launch_typed<QMM_Q8_0, 1>(p, ctas, s);
+            case 2: return launch_typed<QMM_Q8_0, 2>(p, ctas, s);
+            case 3: return launch_typed<QMM_Q8_0, 3>(p, ctas, s);
+            default: return launch_typed<QMM_Q8_0, 4>(p, ctas, s);
+        }
+    }
+    switch (DB) {
+        case 1: return launch_typed<QMM_Q4_0, 1>(p, ctas, s);
+        case 2: return launch_typed<QMM_Q4_0, 2>(p, ctas, s);
+        case 3: return launch_typed<QMM_Q4_0, 3>(p, ctas, s);
+        default: return launch_typed<QMM_Q4_0, 4>(p, ctas, s);
+    }
+}
+
+cudaError_t read_and_clear_attend_status(unsigned *out, cudaStream_t s) {
+    unsigned zero = 0;
+    cudaError_t e = cudaMemcpyFromSymbolAsync(out, g_attend_status, sizeof(unsigned), 0, cudaMemcpyDeviceToHost, s);
+    if (e != cudaSuccess) return e;
+    e = cudaMemcpyToSymbolAsync(g_attend_status, &zero, sizeof(unsigned), 0, cudaMemcpyHostToDevice, s);
+    if (e != cudaSuccess) return e;
+    return cudaStreamSynchronize(s);
+}
+
+QMM_DCHECK_READER(read_dcheck_attend_tc)
+
+}  // namespace qmm

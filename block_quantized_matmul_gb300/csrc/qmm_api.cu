@@ -7,7 +7,7 @@
 // parameters.
 #include "qmm_internal.cuh"
 
-#include "cache.cuh"
+#include "attend.cuh"
 #include "mx4.cuh"
 
 using namespace qmm;
@@ -429,13 +429,14 @@ qmm_status qmm_selftest_timeout(int unit, uint64_t limit_ns, int *flags_dev, qmm
 }
 
 qmm_status qmm_device_status(qmm_stream_t stream) {
-    unsigned v = 0, w = 0, f = 0, m = 0;
+    unsigned v = 0, w = 0, f = 0, m = 0, a = 0;
     cudaError_t e = read_and_clear_device_status(&v, cs(stream));
     if (e == cudaSuccess) e = read_and_clear_matvec_status(&w, cs(stream));
     if (e == cudaSuccess) e = read_and_clear_fold_status(&f, cs(stream));
     if (e == cudaSuccess) e = read_and_clear_mx4_status(&m, cs(stream));
+    if (e == cudaSuccess) e = read_and_clear_attend_status(&a, cs(stream));
     // the bounds-check words (always 0 unless the library was built with QMM_DEBUG)
-    unsigned d[9] = {0, 0, 0, 0, 0, 0, 0, 0, 0};
+    unsigned d[10] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
     if (e == cudaSuccess) e = read_dcheck_matvec(&d[0], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_gemm(&d[1], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_fold(&d[2], cs(stream));
@@ -445,10 +446,11 @@ qmm_status qmm_device_status(qmm_stream_t stream) {
     if (e == cudaSuccess) e = read_dcheck_mx4_gemm(&d[6], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_cache(&d[7], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_attend(&d[8], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_attend_tc(&d[9], cs(stream));
     if (e != cudaSuccess) return QMM_ERR_CUDA;
     for (unsigned line : d)
         if (line) return QMM_ERR_BOUNDS;
-    if (v | w | (f & 1u) | m) return QMM_ERR_TIMEOUT;
+    if (v | w | (f & 1u) | m | a) return QMM_ERR_TIMEOUT;
     return (f & 2u) ? QMM_ERR_RANGE : QMM_OK;
 }
 
