@@ -7,22 +7,23 @@
 // shared memory, and both products run on the tensor cores from there:
 //   S [128 rows x 128 keys] = Q K^T   A = Q, B = K, both K-major in shared memory, S in tensor memory;
 //   O [128 rows x D]       = P V      A = P from tensor memory, B = V^T (K-major over the keys).
-// A row is a lane of tensor memory and a thread, so that a row's maximum, sum and output need no exchange
-// between threads.  The output stays in registers: the product of each tile is read back and added there,
-// scaled by how far the maximum has moved since.
+// A row is a lane of tensor memory and a thread, so that a row's maximum and sum need no exchange between
+// threads.  Two groups of four warps take the tiles of keys in turn, each with its own maximum, sum and output:
+// a tile's path from scores to p is mostly latency, and the groups' overlap.  The outputs stay in tensor memory.
+// p is taken relative to a reference that follows the row's maximum only when that has grown by more than
+// 2^8, so that the output is seldom rescaled; the groups' results are joined at the end.
 //
 // Arithmetic.  k = d * q is split exactly into two fp16 terms, k = hi + lo with hi = fp16(k), which both take part
 // (hi alone put 1e-5 into a row's log-sum); v = d * q is rounded to fp16 (2^-12); the query row is scaled by a power
-// of two into fp16's range; p is kept in fp16 times 2^14; all sums are fp32.
+// of two into fp16's range; p is kept in fp16 times 2^7 (at most 2^15); all sums are fp32.
 //
 // The raw codes of two tiles of keys come through a ring of asynchronous copies; a key's codes are padded to
 // an odd number of 16-byte pieces, so that a warp's 32 keys meet no bank twice.  V^T is written two keys to
 // a word: slots 2l and 2l + 1 of a chunk of 64 are keys l and l + 32, the lanes of one load, and K's rows
 // (and so the columns of S and p) are in that order too.
 //
-// Warps: 0-3 rows (softmax, output; warp 0 issues the products too), 4-7 codes, up to two tiles of keys ahead.
-// (A ninth warp for the products would leave 168 registers a thread, and the rows need some 200.)
-// Tensor memory (512 columns): S twice 128, P twice 64, O 128.
+// Warps: 0-3 and 4-7 rows, of even and odd tiles; 8-11 codes, up to two tiles ahead; 12 products.
+// Tensor memory (512 columns): S twice 128 (p overwrites the S that it came from), O twice 128.
 // Every wait is bounded; on expiry the kernel records QMM_ERR_TIMEOUT, lets its products land, frees
 // tensor memory and returns.
 #include <cuda.h>
@@ -40,8 +41,9 @@ using namespace pipe;
 using namespace tc;
 
 constexpr int kKeysTc = 128;
-constexpr int kThreadsTc = 256;
-constexpr int kColS = 0, kColP = 256, kColO = 384;
+constexpr int kThreadsTc = 416;
+constexpr int kColS = 0, kColO = 256;
+constexpr float kBiasTc = 7.0f, kSlack = 8.0f;             // p is kept times 2^7; the maximum may pass its reference by 2^8
 
 template <int TYPE, int DB>
 struct TcPlan {
@@ -54,8 +56,9 @@ struct TcPlan {
     static constexpr int kRaw = kV + 2 * kVChunk;          // two stages of: K codes, V codes, K scales, V scales
     static constexpr int kRawV = 128 * kPitch, kRawKs = 2 * 128 * kPitch, kRawVs = kRawKs + 128 * DB * 2, kRawBytes = kRawVs + 128 * DB * 2;
     static constexpr int kBad = kRaw + 2 * kRawBytes;      // rows whose result is not finite
-    static constexpr int kBars = kBad + kTcRows * 4;
-    static constexpr int kNumBars = 15;
+    static constexpr int kStats = kBad + kTcRows * 4;      // [group][row]: reference and sum
+    static constexpr int kBars = kStats + 2 * kTcRows * 8;
+    static constexpr int kNumBars = 16;
     static constexpr size_t kSmem = 1024 + kBars + kNumBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory plan too large");
 };
@@ -103,7 +106,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     int *row_bad = reinterpret_cast<int *>(smem + L::kBad);
     uint64_t *bars = reinterpret_cast<uint64_t *>(smem + L::kBars);
     uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 2, *v_full = bars + 3, *v_empty = bars + 4, *s_full = bars + 5,
-             *p_full = bars + 7, *o_full = bars + 9, *done = bars + 10, *raw_full = bars + 11, *raw_empty = bars + 13;
+             *p_full = bars + 7, *o_full = bars + 9, *raw_full = bars + 11, *raw_empty = bars + 13, *done = bars + 15;
+    float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kNumBars);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *odd_flag = reinterpret_cast<int *>(tmem_slot + 2);
@@ -124,17 +128,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&s_full[s]), 1);
             mbar_init(smem_u32(&p_full[s]), kTcRows);
+            mbar_init(smem_u32(&o_full[s]), 1);
             mbar_init(smem_u32(&raw_full[s]), 128);
             mbar_init(smem_u32(&raw_empty[s]), 128);
         }
-        mbar_init(smem_u32(o_full), 1);
         *abort = 0;
         *odd_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (threadIdx.x < kTcRows) row_bad[threadIdx.x] = 0;
     __syncwarp();
-    if (warp == 0) {
+    if (warp == 12) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -151,10 +155,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
         return page < p.n_pages ? page : -1;
     };
 
-    if (warp < 4) {
+    const int row = threadIdx.x & 127, group = threadIdx.x >> 7;   // of the row warps; row = lane of tensor memory
+    const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
+    if (warp < 8) {
         // =============================== rows ===============================
-        const int row = threadIdx.x;                           // = lane of tensor memory
-        const uint32_t t_lane = tmem + ((uint32_t)(32 * warp) << 16);
         const int64_t r = w.r0 + row, i_tok = r / p.group;
         float mul = 1.0f;
         {
@@ -175,97 +179,35 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
             const int e = top > 0.0f && top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
             const float m = p.scale * 1.4426950408889634f, down = copysignf(exp2f((float)-e), m);
             mul = fmaxf(fabsf(m), 1e-30f) * exp2f((float)e);   // a scale of 0 still has to order -inf below 0
+            if (group == 0) {
 #pragma unroll
-            for (int c = 0; c < 8 * NC; ++c) {
-                uint32_t h[4] = {0u, 0u, 0u, 0u};
-                if (c < 4 * DB) {
-                    const uint32_t x[4] = {raw[c < 4 * DB ? c : 0].x, raw[c < 4 * DB ? c : 0].y, raw[c < 4 * DB ? c : 0].z, raw[c < 4 * DB ? c : 0].w};
+                for (int c = 0; c < 8 * NC; ++c) {
+                    uint32_t h[4] = {0u, 0u, 0u, 0u};
+                    if (c < 4 * DB) {
+                        const uint32_t x[4] = {raw[c < 4 * DB ? c : 0].x, raw[c < 4 * DB ? c : 0].y, raw[c < 4 * DB ? c : 0].z, raw[c < 4 * DB ? c : 0].w};
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = p.bf16 ? unpack2(x[k], __nv_bfloat16{}) : unpack2(x[k], __half{});
-                        h[k] = pack2(f.x * down, f.y * down, __half{});
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 f = p.bf16 ? unpack2(x[k], __nv_bfloat16{}) : unpack2(x[k], __half{});
+                            h[k] = pack2(f.x * down, f.y * down, __half{});
+                        }
                     }
+                    *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * L::kChunk + sw128_off(row, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
                 }
-                *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * L::kChunk + sw128_off(row, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+                fence_proxy_async_smem();
+                mbar_arrive(smem_u32(q_full));
             }
-            fence_proxy_async_smem();
-            mbar_arrive(smem_u32(q_full));
         }
-        // ---- products, by one thread of warp 0 ----
-        bool lead = false;
-        if (warp == 0) {
-            uint32_t e;
-            asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
-            lead = e != 0;
-        }
-        const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::kQ)), k_desc = smem_desc_sw128(smem_u32(smem + L::kK)),
-                       v_desc = smem_desc_sw128(smem_u32(smem + L::kV));
-        constexpr uint32_t id_s = idesc_f16(128, kKeysTc), id_o = idesc_f16(128, D);
-        auto scores = [&](int i) -> bool {
-            const int b = i & 1;
-            if (!wait_tc(smem_u32(k_full), (uint32_t)(i & 1), abort)) return false;
-            tc_fence_after();
-            if (lead) {
-#pragma unroll
-                for (int k = 0; k < 4 * DB; ++k) {              // 16 elements a step, of hi, then of lo
-                    const int term = k / (2 * DB), e = k % (2 * DB);
-                    const uint64_t at = (uint64_t)((e >> 2) * (L::kChunk >> 4) + 2 * (e & 3));
-                    mma_f16_ss(tmem + kColS + 128 * b, q_desc + at, k_desc + at + (uint64_t)(term * NC * (L::kChunk >> 4)), id_s,
-                               k > 0 ? 1u : 0u);
-                }
-                mma_commit(smem_u32(k_empty));
-                mma_commit(smem_u32(&s_full[b]));
-            }
-            __syncwarp();
-            return true;
-        };
-        // all rows have given p of tile i, and have read S of tile i and the product of tile i - 1
-        auto values = [&](int i) -> bool {
-            const int b = i & 1;
-            if (!wait_tc(smem_u32(&p_full[b]), (uint32_t)((i >> 1) & 1), abort)) return false;
-            if (!wait_tc(smem_u32(v_full), (uint32_t)(i & 1), abort)) return false;
-            tc_fence_after();
-            if (lead) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {                   // 16 keys a step
-                    const uint64_t at = (uint64_t)((k >> 2) * (L::kVChunk >> 4) + 2 * (k & 3));
-                    mma_f16_ts(tmem + kColO, tmem + kColP + 64 * b + 8 * k, v_desc + at, id_o, k > 0 ? 1u : 0u);
-                }
-                mma_commit(smem_u32(v_empty));
-                mma_commit(smem_u32(o_full));
-            }
-            __syncwarp();
-            return true;
-        };
         const uint64_t word = p.tree && row < w.rows ? p.tree[w.q0 + i_tok] : 0;
-        float o[D];
-#pragma unroll
-        for (int d = 0; d < D; ++d) o[d] = 0.0f;
-        float top = -INFINITY, sum = 0.0f, back = 1.0f;       // back: what the pending product's row is scaled by
+        float ref = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
         bool ok = true;
-        // adds the product of tile i: o and it are relative to the maximum after tile i
-        auto add = [&](int i) {
-            ok = wait_tc(smem_u32(o_full), (uint32_t)(i & 1), abort);
-            if (!ok) return;
-            tc_fence_after();
-#pragma unroll
-            for (int c = 0; c < DB; ++c) {
-                uint32_t v[32];
-                tmem_ld32x(t_lane + kColO + 32 * c, v);
-#pragma unroll
-                for (int d = 0; d < 32; ++d) o[32 * c + d] = fmaf(o[32 * c + d], back, __uint_as_float(v[d]));
-            }
-        };
-        if (warp == 0 && tiles > 0) ok = wait_tc(smem_u32(q_full), 0u, abort) && scores(0);
-        int page = pages_of(0);
-        for (int i = 0; i < tiles && ok; ++i) {
-            const int b = i & 1;
+        int page = pages_of(group);
+        for (int i = group; i < tiles; i += 2) {
+            const uint32_t phase = (uint32_t)((i >> 1) & 1);
+            const uint32_t t_s = t_lane + kColS + 128 * group;
             const int64_t j0 = w.k0 + (int64_t)i * kKeysTc;
             const uint32_t groups = __ballot_sync(0xffffffffu, lane < 8 && page >= 0);
-            page = pages_of(i + 1);
-            // the next tile's scores are under way during this one's exponentials
-            if (warp == 0 && i + 1 < tiles && !scores(i + 1)) { ok = false; break; }
-            if (!wait_tc(smem_u32(&s_full[b]), (uint32_t)((i >> 1) & 1), abort)) { ok = false; break; }
+            page = pages_of(i + 2);
+            if (!wait_tc(smem_u32(&s_full[group]), phase, abort)) { ok = false; break; }
             tc_fence_after();
             const bool masked = groups != 0xFFu || j0 + kKeysTc > w.k1 || j0 + kKeysTc > w.first;
             // keys 32c .. 32c + 31 of this tile that the row sees
@@ -297,29 +239,46 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                 }
                 return e | (o2 << 1);
             };
-            float m = -INFINITY;
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t v[32];
-                tmem_ld32x(t_lane + kColS + 128 * b + 32 * c, v);
+                tmem_ld32x(t_s + 32 * c, v);
                 if (masked) {
                     const uint32_t bits = seen(c);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k)
-                        if ((bits >> k) & 1) m = fmaxf(m, __uint_as_float(v[k]));
+                    for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], (bits >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) m = fmaxf(m, __uint_as_float(v[k]));
+                    for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
                 }
             }
-            m = fmaxf(m * mul, top);
-            const float base = m == -INFINITY ? 0.0f : m, down = ex2(top - base), shift = kBias - base;
-            top = m;
-            sum *= down;
+            const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
+            if (__any_sync(0xffffffffu, m > ref + kSlack || (ref == -INFINITY && m > -INFINITY))) {
+                const float to = fmaxf(m, ref), down = ex2(ref - (to == -INFINITY ? 0.0f : to));
+                ref = to;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) sum[k] *= down;
+                if (i >= 2) {
+                    // the group's products so far, all done, are rescaled
+                    if (!wait_tc(smem_u32(&o_full[group]), phase ^ 1u, abort)) { ok = false; break; }
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 2 * DB; ++c) {
+                        uint32_t v[16];
+                        tmem_ld16(t_lane + kColO + 128 * group + 16 * c, v);
+                        tmem_wait_ld(v);
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(__uint_as_float(v[k]) * down);
+                        tmem_st16(t_lane + kColO + 128 * group + 16 * c, v);
+                    }
+                }
+            }
+            const float shift = kBiasTc - (ref == -INFINITY ? 0.0f : ref);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 uint32_t v[32], h[16];
-                tmem_ld32x(t_lane + kColS + 128 * b + 32 * c, v);
+                tmem_ld32x(t_s + 32 * c, v);
                 const uint32_t bits = masked ? seen(c) : 0xFFFFFFFFu;
 #pragma unroll
                 for (int k = 0; k < 16; ++k) {
@@ -328,43 +287,23 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                         p0 = (bits >> (2 * k)) & 1 ? p0 : 0.0f;
                         p1 = (bits >> (2 * k + 1)) & 1 ? p1 : 0.0f;
                     }
-                    sum += p0 + p1;
+                    sum[k & 3] += p0 + p1;
                     h[k] = pack2(p0, p1, __half{});
                 }
-                tmem_st16(t_lane + kColP + 64 * b + 16 * c, h);
+                tmem_st16(t_s + 16 * c, h);                     // over columns that have been read
             }
-            if (i > 0) add(i - 1);
-            if (!ok) break;
-            back = down;
             tmem_wait_st();
             tc_fence_before();
-            mbar_arrive(smem_u32(&p_full[b]));
-            if (warp == 0 && !values(i)) { ok = false; break; }
+            mbar_arrive(smem_u32(&p_full[group]));
         }
-        if (ok && tiles > 0) add(tiles - 1);
-        if (lead) {
-            // every product issued has landed before tensor memory is released
-            mma_commit(smem_u32(done));
-            wait_drain(smem_u32(done), 0u);
+        if (ok && tiles > group) {
+            const int last = (tiles - 1 - group) >> 1;          // the group's last tile, counted among its own
+            ok = wait_tc(smem_u32(&o_full[group]), (uint32_t)(last & 1), abort);
         }
-        // ---- the row's result ----
-        float all = sum * 0.0f;                                 // 0 unless something is not finite
-#pragma unroll
-        for (int d = 0; d < D; ++d) all = fmaf(o[d], 0.0f, all);
-        if (row < w.rows) {
-            if (!(all == 0.0f)) {
-                row_bad[row] = 1;
-                *odd_flag = 1;
-            }
-#pragma unroll
-            for (int d = 0; d < D; d += 4) {
-                const float v[4] = {o[d], o[d + 1], o[d + 2], o[d + 3]};
-                write_row(p, w, D, row, d, v, top, sum);
-            }
-        }
-    } else if (warp < 8) {
+        stats[group * kTcRows + row] = make_float2(ref, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    } else if (warp < 12) {
         // =============================== codes ===============================
-        const int tid = threadIdx.x - 128, wq = warp - 4;
+        const int tid = threadIdx.x - 256, wq = warp - 8;
         constexpr int PK = L::PK, VP = (PK + 1) / 2;            // pieces of a key; of V for a warp: every second one of 64 keys
         const int64_t head = (int64_t)w.h * p.P * (CB + 2 * DB), page_bytes = (int64_t)p.H * p.P * (CB + 2 * DB);
         bool odd = false;
@@ -501,10 +440,99 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
         if (odd) *odd_flag = 1;
+    } else {
+        // =============================== products ===============================
+        uint32_t e;
+        asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(e));
+        const bool lead = e != 0;
+        const uint64_t q_desc = smem_desc_sw128(smem_u32(smem + L::kQ)), k_desc = smem_desc_sw128(smem_u32(smem + L::kK)),
+                       v_desc = smem_desc_sw128(smem_u32(smem + L::kV));
+        constexpr uint32_t id_s = idesc_f16(128, kKeysTc), id_o = idesc_f16(128, D);
+        auto scores = [&](int i) -> bool {
+            if (!wait_tc(smem_u32(k_full), (uint32_t)(i & 1), abort)) return false;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+                for (int k = 0; k < 4 * DB; ++k) {              // 16 elements a step, of hi, then of lo
+                    const int term = k / (2 * DB), el = k % (2 * DB);
+                    const uint64_t at = (uint64_t)((el >> 2) * (L::kChunk >> 4) + 2 * (el & 3));
+                    mma_f16_ss(tmem + kColS + 128 * (i & 1), q_desc + at, k_desc + at + (uint64_t)(term * NC * (L::kChunk >> 4)), id_s,
+                               k > 0 ? 1u : 0u);
+                }
+                mma_commit(smem_u32(k_empty));
+                mma_commit(smem_u32(&s_full[i & 1]));
+            }
+            __syncwarp();
+            return true;
+        };
+        bool ok = tiles == 0 || (wait_tc(smem_u32(q_full), 0u, abort) && scores(0) && (tiles == 1 || scores(1)));
+        for (int i = 0; i < tiles && ok; ++i) {
+            const int b = i & 1;
+            if (!wait_tc(smem_u32(&p_full[b]), (uint32_t)((i >> 1) & 1), abort)) break;
+            if (!wait_tc(smem_u32(v_full), (uint32_t)(i & 1), abort)) break;
+            tc_fence_after();
+            if (lead) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {                   // 16 keys a step
+                    const uint64_t at = (uint64_t)((k >> 2) * (L::kVChunk >> 4) + 2 * (k & 3));
+                    mma_f16_ts(tmem + kColO + 128 * b, tmem + kColS + 128 * b + 8 * k, v_desc + at, id_o, i >= 2 || k > 0 ? 1u : 0u);
+                }
+                mma_commit(smem_u32(v_empty));
+                mma_commit(smem_u32(&o_full[b]));
+            }
+            __syncwarp();
+            // the next scores of this group overwrite the p that the products above read
+            if (i + 2 < tiles && (!wait_tc(smem_u32(&o_full[b]), (uint32_t)((i >> 1) & 1), abort) || !scores(i + 2))) break;
+        }
+        if (lead) {
+            // every product issued has landed before tensor memory is released
+            mma_commit(smem_u32(done));
+            wait_drain(smem_u32(done), 0u);
+        }
+        __syncwarp();
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    tc_fence_after();
+    if (warp < 8) {
+        // ---- the two groups' results, joined; a group writes its half of the elements ----
+        const float2 a = stats[row], b = stats[kTcRows + row];
+        const float m = fmaxf(a.x, b.x), base = m == -INFINITY ? 0.0f : m;
+        const float fa = ex2(a.x - base), fb = ex2(b.x - base), sum = fa * a.y + fb * b.y;
+        float all = sum * 0.0f;                                 // 0 unless something is not finite
+#pragma unroll
+        for (int c = 0; c < DB; ++c) {
+            uint32_t u[16], v[16];
+            const uint32_t at = t_lane + kColO + group * (D / 2) + 16 * c;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) u[k] = v[k] = 0u;
+            if (tiles > 0) {
+                tmem_ld16(at, u);
+                tmem_wait_ld(u);
+            }
+            if (tiles > 1) {
+                tmem_ld16(at + 128, v);
+                tmem_wait_ld(v);
+            }
+#pragma unroll
+            for (int k = 0; k < 16; k += 4) {
+                float o[4];
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    o[z] = fa * __uint_as_float(u[k + z]) + fb * __uint_as_float(v[k + z]);
+                    all = fmaf(o[z], 0.0f, all);
+                }
+                if (row < w.rows) write_row(p, w, D, row, group * (D / 2) + 16 * c + k, o, m + (kBias - kBiasTc), sum);
+            }
+        }
+        if (row < w.rows && !(all == 0.0f)) {
+            row_bad[row] = 1;
+            *odd_flag = 1;
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
