@@ -555,14 +555,14 @@ template <int DB, int WPR>
 __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const AttendParams p) {
     constexpr int D = DB * 32;
     __shared__ float s_o[WPR > 1 ? WPR : 1][WPR > 1 ? D : 1];
-    __shared__ float s_l[WPR > 1 ? WPR : 1];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    __shared__ float2 s_l[WPR > 1 ? WPR : 1];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR, Hq = p.H * p.group;
     const int64_t stride = p.T * Hq, at = (int64_t)blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
     if (at >= stride) return;                                    // with WPR = 8 for the whole CTA
     const int64_t tok = at / Hq;
     const int hq = (int)(at - tok * Hq);
+    // the lengths are no results of the kernel before this one, which has waited for whoever wrote them
     int64_t lo = 0, hi = p.n_seq - 1;
     while (lo < hi) {
         const int64_t mid = (lo + hi + 1) >> 1;
@@ -573,38 +573,61 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     const int64_t n = max((int64_t)0, min((int64_t)p.kv_lens[lo], p.ld_pages << p.log_p));
     const int used = (int)min((int64_t)p.splits, (n + p.chunk - 1) / p.chunk);
     if (used <= 1) return;
-    float m = -INFINITY;
-    for (int s = lane; s < used; s += 32) m = fmaxf(m, p.part_ml[2 * (s * stride + at)]);
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-    const float base = m == -INFINITY ? 0.0f : m;
-    float l = 0.0f, o[DB];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // four parts at a time, each under way before the first is used
+    float m = -INFINITY, l = 0.0f, o[DB];
 #pragma unroll
     for (int b = 0; b < DB; ++b) o[b] = 0.0f;
-#pragma unroll 4
-    for (int s = part; s < used; s += WPR) {
-        const float2 ml = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * stride + at));
-        const bool some = ml.y != 0.0f;                          // else nothing was seen there
-        const float f = some ? exp2f(ml.x - base) : 0.0f;
-        if (some) l += f * ml.y;
+    for (int s0 = part; s0 < used; s0 += 4 * WPR) {
+        float2 ml[4];
+        float v[4][DB];
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
-            const float v = p.part_o[(s * stride + at) * D + 32 * b + lane];
-            if (some) o[b] += f * v;
+        for (int u = 0; u < 4; ++u) {
+            const int s = s0 + u * WPR;
+            ml[u] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+            for (int b = 0; b < DB; ++b) v[u][b] = 0.0f;
+            if (s < used) {
+                ml[u] = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * stride + at));
+#pragma unroll
+                for (int b = 0; b < DB; ++b) v[u][b] = p.part_o[(s * stride + at) * D + 32 * b + lane];
+            }
+        }
+        const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m), base = top == -INFINITY ? 0.0f : top;
+        const float down = exp2f(m - base);
+        m = top;
+        l *= down;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) o[b] *= down;
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (ml[u].y == 0.0f) continue;                       // nothing was seen there
+            const float f = exp2f(ml[u].x - base);
+            l += f * ml[u].y;
+#pragma unroll
+            for (int b = 0; b < DB; ++b) o[b] += f * v[u][b];
         }
     }
     if constexpr (WPR > 1) {
 #pragma unroll
         for (int b = 0; b < DB; ++b) s_o[part][32 * b + lane] = o[b];
-        if (lane == 0) s_l[part] = l;
+        if (lane == 0) s_l[part] = make_float2(m, l);
         __syncthreads();
+        m = -INFINITY;
         l = 0.0f;
 #pragma unroll
-        for (int w = 0; w < WPR; ++w) l += s_l[w];
+        for (int w = 0; w < WPR; ++w) m = fmaxf(m, s_l[w].x);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float f[WPR];
+#pragma unroll
+        for (int w = 0; w < WPR; ++w) {
+            f[w] = s_l[w].y == 0.0f ? 0.0f : exp2f(s_l[w].x - base);
+            l += f[w] * s_l[w].y;
+        }
         for (int d = threadIdx.x; d < D; d += kJoinWarps * 32) {
             float v = 0.0f;
 #pragma unroll
-            for (int w = 0; w < WPR; ++w) v += s_o[w][d];
+            for (int w = 0; w < WPR; ++w) v += f[w] * s_o[w][d];
             store_out(p, tok * p.ldo + (int64_t)hq * D + d, l == 0.0f ? 0.0f : v / l);
         }
     } else {
@@ -621,15 +644,20 @@ constexpr int kMaxSplits = 256;
 // below two tiles a warp.  Three times as many CTAs measured slower: one token over 500001 tokens 124 us for
 // 97, 304 sequences and heads of 8192 tokens 123 us for 104.
 constexpr int64_t kWantedCtas = 304;
-// Rows of a CTA: 8 or 16 on mma; where there are more, and a head is at most 128 elements, 128 on tcgen05.
+// Rows of a CTA: 8, 16 or (of up to 128 elements) 32 on mma; where there are more, and a head has at most 128
+// elements, 128 on tcgen05.  (32 rows of 38 sequences of 8192 tokens: 287 us on mma, 351 on tcgen05; 128 rows: four
+// times 287, or 361.)
 int tile_rows_of(int64_t max_new, int group, int D) {
     const int64_t rows = max_new * group;
-    return rows <= kMmaRows ? kMmaRows : (rows <= 2 * kMmaRows || D > 128 ? 2 * kMmaRows : kTcRows);
+    if (rows <= kMmaRows) return kMmaRows;
+    if (rows <= 2 * kMmaRows || D > 128) return 2 * kMmaRows;
+    return rows <= 4 * kMmaRows ? 4 * kMmaRows : kTcRows;
 }
+// On tcgen05 (one CTA an SM) 200 for 152 places: a batch's sequences are on average shorter than its longest.
 int wanted_splits(int64_t units, int64_t max_len, int tile_rows) {
-    const int64_t least = tile_rows == kTcRows ? 256 : 2 * kMinChunk, places = tile_rows == kTcRows ? 152 : kWantedCtas;
-    const int64_t most = (max_len + least - 1) / least;
-    int64_t want = tile_rows == kTcRows ? places / units : (places + units - 1) / units;
+    const bool tc = tile_rows == kTcRows;
+    const int64_t least = tc ? 256 : 2 * kMinChunk, most = (max_len + least - 1) / least;
+    int64_t want = tc ? 200 / units : (kWantedCtas + units - 1) / units;
     want = want < most ? want : most;
     want = want < kMaxSplits ? want : kMaxSplits;
     return (int)(want < 1 ? 1 : want);
@@ -658,12 +686,20 @@ cudaError_t launch_join(const AttendParams &p, cudaStream_t s) {
     return launch_pdl(attend_join_kernel<DB, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, p);
 }
 
+template <int TYPE, int DB>
+cudaError_t launch_rows(const AttendParams &p, int64_t ctas, cudaStream_t s) {
+    if (p.tile_rows == kMmaRows) return launch_typed<TYPE, DB, 1>(p, ctas, s);
+    if constexpr (DB <= 4) {
+        if (p.tile_rows == 4 * kMmaRows) return launch_typed<TYPE, DB, 4>(p, ctas, s);
+    }
+    return launch_typed<TYPE, DB, 2>(p, ctas, s);
+}
+
 template <int DB>
 cudaError_t launch_blocks(qmm_type type, const AttendParams &p, int64_t ctas, cudaStream_t s) {
     cudaError_t e;
     if (p.tile_rows == kTcRows) e = launch_attend_tc(type, p, DB, ctas, s);
-    else if (type == QMM_Q8_0) e = p.tile_rows == kMmaRows ? launch_typed<QMM_Q8_0, DB, 1>(p, ctas, s) : launch_typed<QMM_Q8_0, DB, 2>(p, ctas, s);
-    else e = p.tile_rows == kMmaRows ? launch_typed<QMM_Q4_0, DB, 1>(p, ctas, s) : launch_typed<QMM_Q4_0, DB, 2>(p, ctas, s);
+    else e = type == QMM_Q8_0 ? launch_rows<QMM_Q8_0, DB>(p, ctas, s) : launch_rows<QMM_Q4_0, DB>(p, ctas, s);
     return e != cudaSuccess || p.splits == 1 ? e : launch_join<DB>(p, s);
 }
 

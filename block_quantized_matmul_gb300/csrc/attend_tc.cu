@@ -22,7 +22,8 @@
 // a word: slots 2l and 2l + 1 of a chunk of 64 are keys l and l + 32, the lanes of one load, and K's rows
 // (and so the columns of S and p) are in that order too.
 //
-// Warps: 0-3 and 4-7 rows, of even and odd tiles; 8-11 codes, up to two tiles ahead; 12 products.
+// Warps: 0-3 and 4-7 rows, of even and odd tiles; 8-15 codes, up to two tiles ahead; 16 products.  (Four warps of
+// codes took twice as long as the rows: 277 us for 38 sequences of 8192 tokens, 128 rows, against 113 without.)
 // Tensor memory (512 columns): S twice 128 (p overwrites the S that it came from), O twice 128.
 // Every wait is bounded; on expiry the kernel records QMM_ERR_TIMEOUT, lets its products land, frees
 // tensor memory and returns.
@@ -41,7 +42,8 @@ using namespace pipe;
 using namespace tc;
 
 constexpr int kKeysTc = 128;
-constexpr int kThreadsTc = 416;
+constexpr int kCodeWarps = 8, kCodeThreads = kCodeWarps * 32;
+constexpr int kThreadsTc = 256 + kCodeThreads + 32;
 constexpr int kColS = 0, kColO = 256;
 constexpr float kBiasTc = 7.0f, kSlack = 8.0f;             // p is kept times 2^7; the maximum may pass its reference by 2^8
 
@@ -94,6 +96,14 @@ __device__ __forceinline__ void bytes_h2(uint32_t x, uint32_t off, uint32_t &lo,
     lo = h2_bits(__hsub2(bits_h2(__byte_perm(x, 0x64646464u, 0x4140u)), bits_h2(off)));
     hi = h2_bits(__hsub2(bits_h2(__byte_perm(x, 0x64646464u, 0x4342u)), bits_h2(off)));
 }
+__device__ __forceinline__ void swap_halves(uint32_t (&h)[8], bool swap) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t a = swap ? h[4 + k] : h[k], b = swap ? h[k] : h[4 + k];
+        h[k] = a;
+        h[4 + k] = b;
+    }
+}
 constexpr uint32_t kOff8 = 0x64806480u;    // 1152: int8 codes with the sign bit flipped
 constexpr uint32_t kOff4 = 0x64086408u;    // 1032: nibbles
 
@@ -121,16 +131,16 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     if (threadIdx.x == 0) {
         mbar_init(smem_u32(q_full), kTcRows);
         mbar_init(smem_u32(done), 1);
-        mbar_init(smem_u32(k_full), 128);
+        mbar_init(smem_u32(k_full), kCodeThreads);
         mbar_init(smem_u32(k_empty), 1);
-        mbar_init(smem_u32(v_full), 128);
+        mbar_init(smem_u32(v_full), kCodeThreads);
         mbar_init(smem_u32(v_empty), 1);
         for (int s = 0; s < 2; ++s) {
             mbar_init(smem_u32(&s_full[s]), 1);
             mbar_init(smem_u32(&p_full[s]), kTcRows);
             mbar_init(smem_u32(&o_full[s]), 1);
-            mbar_init(smem_u32(&raw_full[s]), 128);
-            mbar_init(smem_u32(&raw_empty[s]), 128);
+            mbar_init(smem_u32(&raw_full[s]), kCodeThreads);
+            mbar_init(smem_u32(&raw_empty[s]), kCodeThreads);
         }
         *abort = 0;
         *odd_flag = 0;
@@ -138,7 +148,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     }
     if (threadIdx.x < kTcRows) row_bad[threadIdx.x] = 0;
     __syncwarp();
-    if (warp == 12) {
+    if (warp == 8 + kCodeWarps) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(512) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -301,10 +311,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
             ok = wait_tc(smem_u32(&o_full[group]), (uint32_t)(last & 1), abort);
         }
         stats[group * kTcRows + row] = make_float2(ref, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-    } else if (warp < 12) {
+    } else if (warp < 8 + kCodeWarps) {
         // =============================== codes ===============================
         const int tid = threadIdx.x - 256, wq = warp - 8;
-        constexpr int PK = L::PK, VP = (PK + 1) / 2;            // pieces of a key; of V for a warp: every second one of 64 keys
+        constexpr int PK = L::PK;                              // pieces of a key
+        constexpr int KP = (128 * PK + kCodeThreads - 1) / kCodeThreads, VW = kCodeWarps / 2, VP = (PK + VW - 1) / VW;
         const int64_t head = (int64_t)w.h * p.P * (CB + 2 * DB), page_bytes = (int64_t)p.H * p.P * (CB + 2 * DB);
         bool odd = false;
         // copies the raw codes and scales of tile i; `page`: its pages, in lanes 0-7
@@ -313,10 +324,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                 const uint32_t st = smem_u32(smem + L::kRaw + (i & 1) * L::kRawBytes);
                 const int off0 = (int)(w.k0 + (int64_t)i * kKeysTc) & (p.P - 1);      // P may be below 128
 #pragma unroll
-                for (int it = 0; it < PK; ++it) {
-                    const int u = it * 128 + tid, key = u / PK, c = u % PK;
-                    const int pg = __shfl_sync(0xffffffffu, page, key >> 4);
-                    if (pg >= 0) {
+                for (int it = 0; it < KP; ++it) {
+                    const int u = it * kCodeThreads + tid, key = u / PK, c = u % PK;
+                    const int pg = __shfl_sync(0xffffffffu, page, (key >> 4) & 7);
+                    if (pg >= 0 && key < 128) {
                         const int64_t at = (int64_t)pg * page_bytes + head + ((off0 + key) & (p.P - 1)) * CB + 16 * c;
                         cp_async16(st + key * L::kPitch + 16 * c, p.k_cache + at);
                         cp_async16(st + L::kRawV + key * L::kPitch + 16 * c, p.v_cache + at);
@@ -338,8 +349,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
             const uint8_t *raw = smem + L::kRaw + (i & 1) * L::kRawBytes;
             const uint16_t *ks = reinterpret_cast<const uint16_t *>(raw + L::kRawKs);
 #pragma unroll
-            for (int it = 0; it < PK; ++it) {
-                const int u = it * 128 + tid, key = u / PK, c = u % PK;
+            for (int it = 0; it < KP; ++it) {
+                const int u = it * kCodeThreads + tid, key = u / PK, c = u % PK;
+                if (key >= 128) break;
                 const uint32_t d2 = valid(i, key, groups) ? ks[key * DB + (TYPE == QMM_Q8_0 ? c >> 1 : c)] * 0x00010001u : 0u;
                 const uint4 v4 = *reinterpret_cast<const uint4 *>(raw + key * L::kPitch + 16 * c);
                 const uint32_t x[4] = {v4.x, v4.y, v4.z, v4.w};
@@ -360,16 +372,20 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                     uint32_t h[8];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) bytes_h2(x[k] ^ 0x80808080u, kOff8, h[2 * k], h[2 * k + 1]);
-                    store(2 * c, h);
-                    store(2 * c + 1, h + 4);
+                    // lanes of the second chunk of 64 elements take their halves the other way round: the first chunk's
+                    // lanes are in the same banks
+                    swap_halves(h, c >> 2 & 1);
+                    store(2 * c + (c >> 2 & 1), h);
+                    store(2 * c + 1 - (c >> 2 & 1), h + 4);
                 } else {
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {               // elements 0-15 in the low nibbles, 16-31 in the high ones
                         uint32_t h[8];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) bytes_h2((x[k] >> (4 * n)) & 0x0F0F0F0Fu, kOff4, h[2 * k], h[2 * k + 1]);
-                        store(4 * c + 2 * n, h);
-                        store(4 * c + 2 * n + 1, h + 4);
+                        swap_halves(h, c >> 1 & 1);
+                        store(4 * c + 2 * n + (c >> 1 & 1), h);
+                        store(4 * c + 2 * n + 1 - (c >> 1 & 1), h + 4);
                     }
                 }
             }
@@ -384,7 +400,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
             uint8_t *vt = smem + L::kV + (wq & 1) * L::kVChunk + (lane & 3) * 4;
 #pragma unroll
             for (int it = 0; it < VP; ++it) {
-                const int c = 2 * it + (wq >> 1), blk = TYPE == QMM_Q8_0 ? c >> 1 : c;
+                const int c = VW * it + (wq >> 1), blk = TYPE == QMM_Q8_0 ? c >> 1 : c;
                 if (c >= PK) break;
                 uint32_t d2 = have & ((uint32_t)vs[ka * DB + blk] | ((uint32_t)vs[kb * DB + blk] << 16));
                 const uint32_t fine = finite2(d2);
@@ -532,7 +548,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 12) {
+    if (warp == 8 + kCodeWarps) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
     }
