@@ -150,15 +150,20 @@ def _ptr_located(x) -> int | None:
     return x.data_ptr()
 
 
-def _current_stream() -> int:
-    """The current stream of the current device as a raw address.  torch's raw query takes a tenth of a
-    microsecond where torch.cuda.current_stream() takes three, half of a small call's host time."""
-    import torch
+_raw_stream = None
 
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is None or not torch.cuda.is_initialized():
-        return torch.cuda.current_stream().cuda_stream
-    return raw(torch.cuda.current_device())
+
+def _current_stream() -> int:
+    """The current stream of the current device as a raw address.  torch's raw queries take a few tenths of a
+    microsecond where torch.cuda.current_stream() takes three, half of a small call's host time."""
+    global _raw_stream
+    if _raw_stream is None:
+        import torch
+
+        torch.cuda.current_stream()                                  # initializes CUDA, or says why it cannot
+        raw, device = (getattr(torch._C, name, None) for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        _raw_stream = (lambda: raw(device())) if raw and device else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def _stream(stream) -> int | None:

@@ -4,7 +4,8 @@
 //   Y[m, n] = sum_b 2^(ea[m, b] + ew[n, b] - 254) * sum_{j < 32} a[m, 32b + j] * w[n, 32b + j]
 //
 // One kernel for every number of tokens: the weight rows are the instruction's 128 rows (the lanes of
-// tensor memory), the tokens its columns, TN = 16 to 256 of them.  So one token costs no more than the
+// tensor memory), the tokens its columns, TN = 16 or 32 of them (256 in the pairs' kernel below,
+// which is as fast from 33 tokens on for 4096 weight rows, and faster for more: 64 tokens x 14336 rows 12.1 us for 19.0).  So one token costs no more than the
 // weight's bytes, and a lane's results of one token are consecutive in y.
 //
 // A stage of the pipeline is 256 of K: 128 weight rows x 128 bytes and TN token rows x 128 bytes by
@@ -117,7 +118,7 @@ struct Plan {
     static constexpr int kWS = kA + (TN * 128 + 1023) / 1024 * 1024;
     static constexpr int kAS = kWS + 2 * kMx4ScaleBlock;
     static constexpr int kStageBytes = kAS + 2 * kMx4ScaleBlock;
-    static constexpr int kStages = TN >= 64 ? 3 : 5;                     // two CTAs an SM up to 64 tokens
+    static constexpr int kStages = TN >= 32 ? 4 : 5;                     // two CTAs an SM
     // tensor memory: the sums, then per stage the scales of two K = 128 halves (weight 4 columns, tokens 4)
     static constexpr int kSums = TN < 32 ? 32 : TN;
     static constexpr int kHalfCols = 8;
@@ -263,7 +264,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
             asm volatile("griddepcontrol.wait;" ::: "memory");
             // row r of a stage goes to warp r % 4, 8 elements a lane; the next stage's rows are loaded before this
             // one's are worked on
-            constexpr int kMine = TN / 4;
+            constexpr int kMine = kMx4FusedTokens / 4;
             const XT *x = static_cast<const XT *>(p.x);
             Raw<XT, 8> raw[kMine];
             auto load = [&](int k) {
@@ -373,10 +374,12 @@ cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *
     cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
     if (e != cudaSuccess) return e;
     const int64_t tiles = (p.N + kRows - 1) / kRows;
-    // K is shared while all CTAs are on the GPU at once, each with two stages at least
-    const int64_t slots = 152 * (int64_t)(L::kSmem <= 113 * 1024 ? 2 : 1);
+    // K is shared while all CTAs are on the GPU at once, each with four stages at least (with two, one token through
+    // 4096 x 4096 takes 6.3 us for 5.1)
+    static_assert(L::kSmem <= 113 * 1024, "two CTAs do not fit on an SM");
+    constexpr int64_t slots = 304;
     p.split = 1;
-    while (p.split < kMaxSplit && 2 * p.split <= TN && 2 * tiles * p.split <= slots && p.nk >= 4 * p.split) p.split *= 2;
+    while (p.split < kMaxSplit && 2 * p.split <= TN && 2 * tiles * p.split <= slots && p.nk >= 8 * p.split) p.split *= 2;
     alignas(64) CUtensorMap wm, am;
     e = make_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, wc, (uint64_t)(K / 2), (uint64_t)p.N, (uint64_t)(K / 2), 128, kRows,
                     CU_TENSOR_MAP_SWIZZLE_128B);
@@ -404,7 +407,7 @@ cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *
 }
 
 // ---------------------------------------------------------------------------------------------
-// Many tokens: pairs of CTAs (cta_group::2) share a tile of 256 weight rows x 256 tokens.  Each CTA holds
+// More than 32 tokens: pairs of CTAs (cta_group::2) share a tile of 256 weight rows x 256 tokens.  Each CTA holds
 // 128 of the weight rows and 128 of the tokens, and the pair's instruction reads both halves of the
 // tokens, so that a byte brought into shared memory takes part in twice the products of a single CTA's
 // tile.  The pairs stay on their SMs and take tiles in turn.  The eight result warps of a CTA read a finished tile into registers, 128 sums a
@@ -715,8 +718,6 @@ cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, i
     p.early_weights = early_weights;
     if (M <= 16) return launch_tn<16>(p, wc, K, ac, s);
     if (M <= 32) return launch_tn<32>(p, wc, K, ac, s);
-    if (M <= 64) return launch_tn<64>(p, wc, K, ac, s);
-    if (M <= 128) return launch_tn<128>(p, wc, K, ac, s);
     return launch_pairs(p, wc, K, ac, s);
 }
 
@@ -727,7 +728,7 @@ cudaError_t launch_mx4_linear_few(const uint8_t *wc, const uint8_t *ws, int64_t 
     p.x = x;
     p.ldx = ldx;
     p.x_vec = rows_aligned(x, ldx, dtype_bytes(xt));
-    return with_dtype(xt, [&](auto z) { return launch_tn<kMx4FusedTokens, decltype(z)>(p, wc, K, nullptr, s); });
+    return with_dtype(xt, [&](auto z) { return launch_tn<16, decltype(z)>(p, wc, K, nullptr, s); });
 }
 
 cudaError_t read_and_clear_mx4_status(unsigned *out, cudaStream_t s) {

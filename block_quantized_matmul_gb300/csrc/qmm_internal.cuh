@@ -219,8 +219,9 @@ cudaError_t launch_mx4_dequantize(const uint8_t *codes, const uint8_t *scales, i
                                   int64_t ldy, cudaStream_t s);
 cudaError_t launch_mx4_matmul(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, const uint8_t *ac, const uint8_t *as,
                               int64_t M, qmm_dtype t, void *y, int64_t ldy, int early_weights, cudaStream_t s);
-// Up to kMx4FusedTokens rows, quantized inside the product's kernel.
-constexpr int kMx4FusedTokens = 16;
+// Up to kMx4FusedTokens rows, quantized inside the product's kernel, by every CTA for itself (a row to a warp; with
+// 8 rows a kernel of their own is as fast, with 16 faster).
+constexpr int kMx4FusedTokens = 4;
 cudaError_t launch_mx4_linear_few(const uint8_t *wc, const uint8_t *ws, int64_t K, int64_t N, qmm_dtype xt, const void *x, int64_t ldx,
                                   int64_t M, qmm_dtype t, void *y, int64_t ldy, cudaStream_t s);
 cudaError_t read_and_clear_mx4_status(unsigned *out, cudaStream_t s);

@@ -400,7 +400,7 @@ QMM_API size_t qmm_mx4_linear_workspace_size(int64_t M, int64_t K);
 
 /*
  * qmm_mx4_linear -- floating-point activation rows times an MX4 weight: qmm_mx4_quantize into the workspace,
- * then qmm_mx4_matmul, bit for bit.  Up to 16 rows are quantized inside the product's kernel, and the
+ * then qmm_mx4_matmul, bit for bit.  Up to 4 rows are quantized inside the product's kernel, and the
  * workspace is not touched.  That kernel starts streaming the weight before the kernel before it on the
  * stream has completed (x and y are touched only after it has): so the weight must not be written by the
  * kernel launched immediately before this call if that kernel itself lets dependents start early.  A
