@@ -15,7 +15,8 @@
 //
 // Arithmetic.  k = d * q is split exactly into two fp16 terms, k = hi + lo with hi = fp16(k), which both take part
 // (hi alone put 1e-5 into a row's log-sum); v = d * q is rounded to fp16 (2^-12); the query row is scaled by a power
-// of two into fp16's range; p is kept in fp16 times 2^7 (at most 2^15); all sums are fp32.
+// of two into fp16's range; p is kept in fp16 times 2^7 (at most 2^15), for fp16 outputs in two terms (see attend.cu);
+// all sums are fp32.
 //
 // The raw codes of two tiles of keys come through a ring of asynchronous copies; a key's codes are padded to
 // an odd number of 16-byte pieces, so that a warp's 32 keys meet no bank twice.  V^T is written two keys to
@@ -165,6 +166,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
         return page < p.n_pages ? page : -1;
     };
 
+    const bool two = !p.bf16;                                       // p in two terms, where the output keeps 11 bits
     const int row = threadIdx.x & 127, group = threadIdx.x >> 7;   // of the row warps; row = lane of tensor memory
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     if (warp < 8) {
@@ -299,8 +301,18 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                     }
                     sum[k & 3] += p0 + p1;
                     h[k] = pack2(p0, p1, __half{});
+                    if (two) {
+                        const float2 hi = unpack2(h[k], __half{});
+                        v[k] = pack2(p0 - hi.x, p1 - hi.y, __half{});
+                    }
                 }
-                tmem_st16(t_s + 16 * c, h);                     // over columns that have been read
+                // over the columns that were read: 16 of hi, 16 of lo
+                tmem_st16(t_s + 32 * c, h);
+                if (two) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) h[k] = v[k];
+                    tmem_st16(t_s + 32 * c + 16, h);
+                }
             }
             tmem_wait_st();
             tc_fence_before();
@@ -491,7 +503,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {                   // 16 keys a step
                     const uint64_t at = (uint64_t)((k >> 2) * (L::kVChunk >> 4) + 2 * (k & 3));
-                    mma_f16_ts(tmem + kColO + 128 * b, tmem + kColS + 128 * b + 8 * k, v_desc + at, id_o, i >= 2 || k > 0 ? 1u : 0u);
+                    const uint32_t pa = tmem + kColS + 128 * b + 32 * (k >> 1) + 8 * (k & 1);
+                    mma_f16_ts(tmem + kColO + 128 * b, pa, v_desc + at, id_o, i >= 2 || k > 0 ? 1u : 0u);
+                    if (two) mma_f16_ts(tmem + kColO + 128 * b, pa + 16, v_desc + at, id_o, 1u);
                 }
                 mma_commit(smem_u32(v_empty));
                 mma_commit(smem_u32(&o_full[b]));
