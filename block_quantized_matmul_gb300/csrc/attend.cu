@@ -37,7 +37,6 @@ namespace {
 constexpr int kMmaRows = 8;                // columns of an mma
 constexpr int kKeys = 32;                  // keys of a tile
 
-
 // The 16- or 32-byte units of a tile are permuted so that the fragment loads of a warp meet no bank
 // twice: block b of row r (DB blocks a row) goes to place b ^ swizzle, U units spanning all banks.
 template <int DB, int U>
@@ -67,8 +66,10 @@ struct Tile {
     static constexpr int kQPitch = DB * 64 + (DB % 2 == 0 ? 64 : 0);
     static constexpr int kQ = kRowsTile * kQPitch;
     static constexpr int kRing = kStages * kWarps * kBytes > kOut ? kStages * kWarps * kBytes : kOut;
-    static constexpr int kSmem = kRing + kQ + kWarps * kRowsTile * 8 + kRowsTile * 8 + kWarps * 4 * 4;
-    static_assert(kStages >= 2, "ring too shallow");
+    static constexpr int kSmem = kRing + kQ + kRowsTile * 8 + kWarps * 4 * 4;
+    static_assert(kStages >= 2 && kStages <= 4, "ring depth");
+    static_assert(kWarps * kRowsTile * 8 <= kQ, "the warps' maxima and sums lie over the query rows");
+    static_assert(kSmem <= 113 * 1024, "two CTAs do not fit an SM");
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src) {
@@ -174,9 +175,8 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
     constexpr bool kQRegs = NT == 1;                                           // the query fragments stay in registers
     extern __shared__ __align__(128) uint8_t smem[];
     uint8_t *q_rows = smem + L::kRing;
-    float *w_top = reinterpret_cast<float *>(q_rows + L::kQ);                // [warp][row]
-    float *w_sum = w_top + kWarps * kRowsTile;
-    float *row_mul = w_sum + kWarps * kRowsTile;                              // score -> power of two
+    float *w_top = reinterpret_cast<float *>(q_rows), *w_sum = w_top + kWarps * kRowsTile;   // [warp][row], after the last tile
+    float *row_mul = reinterpret_cast<float *>(q_rows + L::kQ);               // score -> power of two
     int *row_bad = reinterpret_cast<int *>(row_mul + kRowsTile);              // its result is not finite
     uint32_t *masks = reinterpret_cast<uint32_t *>(row_bad + kRowsTile);      // [warp][stage]
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -572,21 +572,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, part = warp % WPR, Hq = p.H * p.group;
     const int64_t stride = p.T * Hq, at = (int64_t)blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
-    if (at >= stride) return;                                    // with WPR = 8 for the whole CTA
-    const int64_t tok = at / Hq;
+    const int64_t tok = (uint32_t)at / (uint32_t)Hq;
     const int hq = (int)(at - tok * Hq);
-    // the lengths are no results of the kernel before this one, which has waited for whoever wrote them
-    int64_t lo = 0, hi = p.n_seq - 1;
-    while (lo < hi) {
-        const int64_t mid = (lo + hi + 1) >> 1;
-        if (p.q_starts[mid] <= tok) lo = mid; else hi = mid - 1;
+    // The lengths are no results of the kernel before this one, which has waited for whoever wrote them.  Nobody
+    // leaves before the wait: a kernel that waits for this one has to find the one before it complete too.
+    __shared__ uint32_t s_chunk;
+    int s = -1, start = 0;                                       // the row's sequence: the last that starts at or before it
+    for (int base = 0; base < (int)p.n_seq; base += 32) {
+        const int from = base + lane < (int)p.n_seq ? __ldcg(p.q_starts + base + lane) : INT_MAX;
+        const unsigned upto = __ballot_sync(0xffffffffu, from <= tok);
+        if (upto == 0) break;
+        s = base + __popc(upto) - 1;
+        start = __shfl_sync(0xffffffffu, from, __popc(upto) - 1);
+        if (upto != 0xffffffffu) break;
     }
-    // rows past row_tiles were not computed
-    if ((tok - p.q_starts[lo]) * p.group + hq % p.group >= (int64_t)p.row_tiles * p.tile_rows) return;
-    const int64_t n = max((int64_t)0, min((int64_t)p.kv_lens[lo], p.ld_pages << p.log_p));
-    const int used = (int)min((int64_t)p.splits, (n + p.chunk - 1) / p.chunk);
-    if (used <= 1) return;
+    const int len = s >= 0 ? __ldcg(p.kv_lens + s) : 0;
+    if (warp == 0) {
+        const uint32_t chunk = chunk_of(p, len_at(p, 0));
+        if (lane == 0) s_chunk = chunk;
+    }
+    __syncthreads();
+    const int used = splits_of(cached(p, len), s_chunk);
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // (rows past row_tiles were not computed)
+    if (at >= stride || s < 0 || used <= 1 || (tok - start) * p.group + hq % p.group >= (int64_t)p.row_tiles * p.tile_rows) return;
     // four parts at a time, each under way before the first is used
     float m = -INFINITY, l = 0.0f, o[DB];
 #pragma unroll
@@ -596,14 +605,14 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
         float v[4][DB];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-            const int s = s0 + u * WPR;
+            const int sp = s0 + u * WPR;
             ml[u] = make_float2(-INFINITY, 0.0f);
 #pragma unroll
             for (int b = 0; b < DB; ++b) v[u][b] = 0.0f;
-            if (s < used) {
-                ml[u] = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (s * stride + at));
+            if (sp < used) {
+                ml[u] = *reinterpret_cast<const float2 *>(p.part_ml + 2 * (sp * stride + at));
 #pragma unroll
-                for (int b = 0; b < DB; ++b) v[u][b] = p.part_o[(s * stride + at) * D + 32 * b + lane];
+                for (int b = 0; b < DB; ++b) v[u][b] = p.part_o[(sp * stride + at) * D + 32 * b + lane];
             }
         }
         const float top = fmaxf(fmaxf(fmaxf(ml[0].x, ml[1].x), fmaxf(ml[2].x, ml[3].x)), m), base = top == -INFINITY ? 0.0f : top;
@@ -650,13 +659,6 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     if (lane == 0 && part == 0 && p.lse) p.lse[at] = l == 0.0f ? -INFINITY : (m + __log2f(l) - kBias) * 0.6931471805599453f;
 }
 
-constexpr int64_t kMinChunk = 8 * kKeys;           // one tile a warp
-constexpr int kMaxSplits = 256;
-
-// Splits of the longest sequence: as many as give each of the GPU's 304 places (two an SM) a CTA, but no chunk
-// below two tiles a warp.  Three times as many CTAs measured slower: one token over 500001 tokens 124 us for
-// 97, 304 sequences and heads of 8192 tokens 123 us for 104.
-constexpr int64_t kWantedCtas = 304;
 // Rows of a CTA: 8, 16 or (of up to 128 elements) 32 on mma; where there are more, and a head has at most 128
 // elements, 128 on tcgen05.  (32 rows of 38 sequences of 8192 tokens: 287 us on mma, 351 on tcgen05; 128 rows: four
 // times 287, or 361.)
@@ -666,25 +668,40 @@ int tile_rows_of(int64_t max_new, int group, int D) {
     if (rows <= 2 * kMmaRows || D > 128) return 2 * kMmaRows;
     return rows <= 4 * kMmaRows ? 4 * kMmaRows : kTcRows;
 }
-// On tcgen05 (one CTA an SM) 200 for 152 places: a batch's sequences are on average shorter than its longest.
-int wanted_splits(int64_t units, int64_t max_len, int tile_rows) {
-    const bool tc = tile_rows == kTcRows;
-    const int64_t least = tc ? 256 : 2 * kMinChunk, most = (max_len + least - 1) / least;
-    int64_t want = tc ? 200 / units : (kWantedCtas + units - 1) / units;
-    want = want < most ? want : most;
-    want = want < kMaxSplits ? want : kMaxSplits;
-    return (int)(want < 1 ? 1 : want);
-}
 int64_t row_tiles_of(int64_t max_new, int group, int D) {
     const int rows = tile_rows_of(max_new, group, D);
     return (max_new * group + rows - 1) / rows;
+}
+
+// How far sequences may be split.  The GPU has 304 places for the CTAs of attend_kernel (two an SM), 152 for those of
+// attend_tc_kernel: as many splits as fill them once, or also twice where whole sequences fill more than half, and none
+// where whole sequences fill them.  Three times as many CTAs as places measured slower: one token over 500001
+// tokens 124 us for 97.  A sequence that is longer than the others takes up to four times the splits of an even
+// batch.  `even`: splits of each sequence in an even batch; the others as in AttendParams.
+struct Split {
+    int splits, budget, waves, least, fixed, even;
+};
+Split split_of(int64_t n_seq, int H, int64_t row_tiles, int tile_rows, int64_t max_len) {
+    const bool tc = tile_rows == kTcRows;
+    const int64_t places = tc ? 152 : 304, per = H * row_tiles, units = n_seq * per;
+    Split s = {1, (int)n_seq, 1, tc ? 2 : 4, tc ? 2 : 6, 1};
+    if (units >= places) return s;
+    s.budget = (int)(places / per);
+    s.waves = 2 * units > places ? 2 : 1;
+    const int64_t all = (int64_t)s.budget * s.waves, even = (all + n_seq - 1) / n_seq;
+    const int64_t steps = (max_len + kStep - 1) / kStep, most = (steps + s.least - 1) / s.least;
+    int64_t want = all - n_seq + 1;
+    want = want < 4 * even ? want : 4 * even;
+    want = want < most ? want : most;
+    s.splits = (int)(want < 1 ? 1 : want);
+    s.even = (int)(even < most ? even : most);
+    return s;
 }
 size_t split_bytes(int64_t rows, int D) { return round256((size_t)rows * (size_t)(D + 2) * 4); }
 
 template <int TYPE, int DB, int NT, bool TWO = true>
 cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
     using L = Tile<TYPE, DB, NT>;
-    static_assert(L::kSmem <= 227 * 1024, "shared memory plan too large");
     auto kern = attend_kernel<TYPE, DB, NT, TWO>;
     static int attr_done[4] = {0, 0, 0, 0};
     cudaError_t e = ensure_smem_limit(kern, L::kSmem, attr_done);
@@ -693,9 +710,9 @@ cudaError_t launch_typed(const AttendParams &p, int64_t ctas, cudaStream_t s) {
 }
 
 template <int DB>
-cudaError_t launch_join(const AttendParams &p, cudaStream_t s) {
+cudaError_t launch_join(const AttendParams &p, int even, cudaStream_t s) {
     const int64_t rows = p.T * p.H * p.group;
-    if (p.splits > kJoinWarps) return launch_pdl(attend_join_kernel<DB, kJoinWarps>, dim3((unsigned)rows), kJoinWarps * 32, 0, s, p);
+    if (even > kJoinWarps) return launch_pdl(attend_join_kernel<DB, kJoinWarps>, dim3((unsigned)rows), kJoinWarps * 32, 0, s, p);
     return launch_pdl(attend_join_kernel<DB, 1>, dim3((unsigned)((rows + kJoinWarps - 1) / kJoinWarps)), kJoinWarps * 32, 0, s, p);
 }
 
@@ -709,17 +726,17 @@ cudaError_t launch_rows(const AttendParams &p, int64_t ctas, cudaStream_t s) {
 }
 
 template <int DB>
-cudaError_t launch_blocks(qmm_type type, const AttendParams &p, int64_t ctas, cudaStream_t s) {
+cudaError_t launch_blocks(qmm_type type, const AttendParams &p, int64_t ctas, int even, cudaStream_t s) {
     cudaError_t e;
     if (p.tile_rows == kTcRows) e = launch_attend_tc(type, p, DB, ctas, s);
     else e = type == QMM_Q8_0 ? launch_rows<QMM_Q8_0, DB>(p, ctas, s) : launch_rows<QMM_Q4_0, DB>(p, ctas, s);
-    return e != cudaSuccess || p.splits == 1 ? e : launch_join<DB>(p, s);
+    return e != cudaSuccess || p.splits == 1 ? e : launch_join<DB>(p, even, s);
 }
 
 }  // namespace
 
 size_t attend_workspace_bytes(int64_t n_seq, int64_t max_new, int H, int Hq, int D, int64_t max_len) {
-    const int splits = wanted_splits(n_seq * H * row_tiles_of(max_new, Hq / H, D), max_len, tile_rows_of(max_new, Hq / H, D));
+    const int splits = split_of(n_seq, H, row_tiles_of(max_new, Hq / H, D), tile_rows_of(max_new, Hq / H, D), max_len).splits;
     return splits == 1 ? 0 : (size_t)splits * split_bytes(n_seq * max_new * Hq, D);
 }
 
@@ -757,27 +774,31 @@ cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uin
     p.out = out;
     p.lse = lse;
     const size_t per_split = split_bytes(T * Hq, D);
-    p.splits = wanted_splits(units, max_len, p.tile_rows);
+    const Split split = split_of(n_seq, H, row_tiles, p.tile_rows, max_len);
+    p.splits = split.splits;
+    p.budget = split.budget;
+    p.waves = split.waves;
+    p.least = split.least;
+    p.fixed = split.fixed;
     if ((size_t)p.splits * per_split > ws_bytes) p.splits = (int)(ws_bytes / per_split);
     if (p.splits < 2) {
         p.splits = 1;
-        p.chunk = (int64_t)1 << 40;
     } else {
-        p.chunk = ((max_len + p.splits - 1) / p.splits + kMinChunk - 1) / kMinChunk * kMinChunk;
         p.part_o = static_cast<float *>(ws);
         p.part_ml = p.part_o + (size_t)p.splits * (size_t)T * (size_t)Hq * (size_t)D;
     }
-    const int64_t ctas = units * p.splits;
+    const int64_t ctas = p.splits > 1 ? (int64_t)p.budget * p.waves * H * row_tiles : units;
+    if (p.splits > 1 && T * Hq > 0x7fffffff) return cudaErrorInvalidValue;       // rows of the join
     if (ctas > 0x7fffffff) return cudaErrorInvalidValue;
     switch (D / 32) {
-        case 1: return launch_blocks<1>(type, p, ctas, s);
-        case 2: return launch_blocks<2>(type, p, ctas, s);
-        case 3: return launch_blocks<3>(type, p, ctas, s);
-        case 4: return launch_blocks<4>(type, p, ctas, s);
-        case 5: return launch_blocks<5>(type, p, ctas, s);
-        case 6: return launch_blocks<6>(type, p, ctas, s);
-        case 7: return launch_blocks<7>(type, p, ctas, s);
-        default: return launch_blocks<8>(type, p, ctas, s);
+        case 1: return launch_blocks<1>(type, p, ctas, split.even, s);
+        case 2: return launch_blocks<2>(type, p, ctas, split.even, s);
+        case 3: return launch_blocks<3>(type, p, ctas, split.even, s);
+        case 4: return launch_blocks<4>(type, p, ctas, split.even, s);
+        case 5: return launch_blocks<5>(type, p, ctas, split.even, s);
+        case 6: return launch_blocks<6>(type, p, ctas, split.even, s);
+        case 7: return launch_blocks<7>(type, p, ctas, split.even, s);
+        default: return launch_blocks<8>(type, p, ctas, split.even, s);
     }
 }
 

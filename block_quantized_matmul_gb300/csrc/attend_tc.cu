@@ -60,7 +60,8 @@ struct TcPlan {
     static constexpr int kRawV = 128 * kPitch, kRawKs = 2 * 128 * kPitch, kRawVs = kRawKs + 128 * DB * 2, kRawBytes = kRawVs + 128 * DB * 2;
     static constexpr int kBad = kRaw + 2 * kRawBytes;      // rows whose result is not finite
     static constexpr int kStats = kBad + kTcRows * 4;      // [group][row]: reference and sum
-    static constexpr int kBars = kStats + 2 * kTcRows * 8;
+    static constexpr int kMul = kStats + 2 * kTcRows * 8;  // score -> power of two
+    static constexpr int kBars = kMul + kTcRows * 4;
     static constexpr int kNumBars = 16;
     static constexpr size_t kSmem = 1024 + kBars + kNumBars * 8 + 16;
     static_assert(kSmem <= 227 * 1024, "shared memory plan too large");
@@ -119,6 +120,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     uint64_t *q_full = bars, *k_full = bars + 1, *k_empty = bars + 2, *v_full = bars + 3, *v_empty = bars + 4, *s_full = bars + 5,
              *p_full = bars + 7, *o_full = bars + 9, *raw_full = bars + 11, *raw_empty = bars + 13, *done = bars + 15;
     float2 *stats = reinterpret_cast<float2 *>(smem + L::kStats);
+    float *muls = reinterpret_cast<float *>(smem + L::kMul);
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(bars + L::kNumBars);
     volatile int *abort = reinterpret_cast<volatile int *>(tmem_slot + 1);
     int *odd_flag = reinterpret_cast<int *>(tmem_slot + 2);
@@ -130,7 +132,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     if (!find_rows<kTcRows>(p, reinterpret_cast<int *>(smem), kThreadsTc, w)) return;
 
     if (threadIdx.x == 0) {
-        mbar_init(smem_u32(q_full), kTcRows);
+        mbar_init(smem_u32(q_full), 2 * kTcRows);
         mbar_init(smem_u32(done), 1);
         mbar_init(smem_u32(k_full), kCodeThreads);
         mbar_init(smem_u32(k_empty), 1);
@@ -171,44 +173,43 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     const uint32_t t_lane = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
     if (warp < 8) {
         // =============================== rows ===============================
-        const int64_t r = w.r0 + row, i_tok = r / p.group;
-        float mul = 1.0f;
+        const int r = w.r0 + row, i_tok = r / p.group;
         {
-            // the query row, scaled by a power of two so that its largest element lies in [1, 2)
-            uint4 raw[4 * DB];
-            const int64_t base = (w.q0 + i_tok) * p.ldq + (w.h * p.group + (r - i_tok * p.group)) * D;
+            // the query rows, scaled by a power of two so that the largest element lies in [1, 2): sixteen lanes a row, two
+            // rows of a warp's sixteen at a time
+            const int c = lane & 15;                            // eight elements of the row
+            uint4 raw[8];
 #pragma unroll
-            for (int c = 0; c < 4 * DB; ++c)
-                raw[c] = row < w.rows ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + base + 8 * c) : make_uint4(0u, 0u, 0u, 0u);
-            uint32_t top2 = 0;
-#pragma unroll
-            for (int c = 0; c < 4 * DB; ++c) {
-                const uint32_t x = __vmaxu2(raw[c].x & 0x7FFF7FFFu, raw[c].y & 0x7FFF7FFFu), y = __vmaxu2(raw[c].z & 0x7FFF7FFFu, raw[c].w & 0x7FFF7FFFu);
-                top2 = __vmaxu2(top2, __vmaxu2(x, y));
+            for (int u = 0; u < 8; ++u) {
+                const int x = 16 * warp + 2 * u + (lane >> 4), rx = w.r0 + x, tok = rx / p.group;
+                const int64_t at = (w.q0 + tok) * p.ldq + (int64_t)(w.h * p.group + (rx - tok * p.group)) * D + 8 * c;
+                raw[u] = x < w.rows && c < 4 * DB ? *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p.q) + at) : make_uint4(0u, 0u, 0u, 0u);
             }
-            const uint32_t topb = max(top2 & 0xFFFFu, top2 >> 16);
-            const float top = p.bf16 ? bits_to_float<__nv_bfloat16>(topb) : bits_to_float<__half>(topb);
-            const int e = top > 0.0f && top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
-            const float m = p.scale * 1.4426950408889634f, down = copysignf(exp2f((float)-e), m);
-            mul = fmaxf(fabsf(m), 1e-30f) * exp2f((float)e);   // a scale of 0 still has to order -inf below 0
-            if (group == 0) {
 #pragma unroll
-                for (int c = 0; c < 8 * NC; ++c) {
-                    uint32_t h[4] = {0u, 0u, 0u, 0u};
-                    if (c < 4 * DB) {
-                        const uint32_t x[4] = {raw[c < 4 * DB ? c : 0].x, raw[c < 4 * DB ? c : 0].y, raw[c < 4 * DB ? c : 0].z, raw[c < 4 * DB ? c : 0].w};
+            for (int u = 0; u < 8; ++u) {
+                const int x = 16 * warp + 2 * u + (lane >> 4);
+                uint32_t top2 = __vmaxu2(__vmaxu2(raw[u].x & 0x7FFF7FFFu, raw[u].y & 0x7FFF7FFFu), __vmaxu2(raw[u].z & 0x7FFF7FFFu, raw[u].w & 0x7FFF7FFFu));
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 f = p.bf16 ? unpack2(x[k], __nv_bfloat16{}) : unpack2(x[k], __half{});
-                            h[k] = pack2(f.x * down, f.y * down, __half{});
-                        }
-                    }
-                    *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * L::kChunk + sw128_off(row, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
+                for (int z = 8; z > 0; z >>= 1) top2 = __vmaxu2(top2, __shfl_xor_sync(0xffffffffu, top2, z));
+                const uint32_t topb = max(top2 & 0xFFFFu, top2 >> 16);
+                const float top = p.bf16 ? bits_to_float<__nv_bfloat16>(topb) : bits_to_float<__half>(topb);
+                const int e = top > 0.0f && top < INFINITY ? max((int)(__float_as_uint(top) >> 23) - 127, -120) : 0;
+                const float m = p.scale * 1.4426950408889634f, down = copysignf(exp2f((float)-e), m);
+                if (c == 0) muls[x] = fmaxf(fabsf(m), 1e-30f) * exp2f((float)e);   // a scale of 0 still has to order -inf below 0
+                const uint32_t in[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                uint32_t h[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const float2 f = p.bf16 ? unpack2(in[k], __nv_bfloat16{}) : unpack2(in[k], __half{});
+                    h[k] = pack2(f.x * down, f.y * down, __half{});
                 }
-                fence_proxy_async_smem();
-                mbar_arrive(smem_u32(q_full));
+                if (c < 8 * NC) *reinterpret_cast<uint4 *>(smem + L::kQ + (c >> 3) * L::kChunk + sw128_off(x, c & 7)) = make_uint4(h[0], h[1], h[2], h[3]);
             }
+            fence_proxy_async_smem();
+            mbar_arrive(smem_u32(q_full));
         }
+        asm volatile("bar.sync 1, 256;" ::: "memory");
+        const float mul = muls[row];
         const uint64_t word = p.tree && row < w.rows ? p.tree[w.q0 + i_tok] : 0;
         float ref = -INFINITY, sum[4] = {0.f, 0.f, 0.f, 0.f};
         bool ok = true;
@@ -252,18 +253,17 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                 return e | (o2 << 1);
             };
             float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t v[32];
                 tmem_ld32x(t_s + 32 * c, v);
                 if (masked) {
                     const uint32_t bits = seen(c);
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], (bits >> k) & 1 ? __uint_as_float(v[k]) : -INFINITY);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
+                    for (int k = 0; k < 32; ++k) v[k] = (bits >> k) & 1 ? v[k] : 0xFF800000u;
                 }
+#pragma unroll
+                for (int k = 0; k < 32; ++k) mx[k & 3] = fmaxf(mx[k & 3], __uint_as_float(v[k]));
             }
             const float m = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * mul;
             if (__any_sync(0xffffffffu, m > ref + kSlack || (ref == -INFINITY && m > -INFINITY))) {
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                     // the group's products so far, all done, are rescaled
                     if (!wait_tc(smem_u32(&o_full[group]), phase ^ 1u, abort)) { ok = false; break; }
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < 2 * DB; ++c) {
                         uint32_t v[16];
                         tmem_ld16(t_lane + kColO + 128 * group + 16 * c, v);
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                 }
             }
             const float shift = kBiasTc - (ref == -INFINITY ? 0.0f : ref);
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < 4; ++c) {
                 uint32_t v[32], h[16];
                 tmem_ld32x(t_s + 32 * c, v);
@@ -545,10 +545,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                 tmem_wait_ld(v);
             }
 #pragma unroll
-            for (int k = 0; k < 16; k += 4) {
-                float o[4];
+            for (int k = 0; k < 16; k += 8) {
+                float o[8];
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
+                for (int z = 0; z < 8; ++z) {
                     o[z] = fa * __uint_as_float(u[k + z]) + fb * __uint_as_float(v[k + z]);
                     all = fmaf(o[z], 0.0f, all);
                 }
