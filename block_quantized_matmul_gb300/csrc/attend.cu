@@ -165,8 +165,11 @@ __device__ __forceinline__ uint32_t scale_pair(const uint32_t (&w)[DB], int b) {
     return __byte_perm(w[b >> 1], w[(DB + b) >> 1], (b & 1 ? 0x32 : 0x10) | ((DB + b) & 1 ? 0x7600 : 0x5400));
 }
 
-// TWO: the kernel can take p in two terms, and does for fp16 outputs.  (Without it 32 rows keep their registers:
-// 286 us against 390 for 38 sequences of 8192 tokens, bf16.)
+// What bounds it: for up to 8 rows of Q8_0 the cache's bytes (38 sequences of 8192 tokens, 8 heads of 128: 106 us, 6.4 TB/s);
+// for Q4_0 (97 us, 3.7 TB/s) and for more rows the instructions that expand the codes and take the exponentials (16
+// rows 132 us, 32 rows 198); for short sequences the chain of copy, products, softmax and join (777 tokens: 8.4 us).
+// TWO: the kernel can take p in two terms, and does for fp16 outputs (32 rows: 256 us).  Without it 32 rows keep
+// their registers.
 template <int TYPE, int DB, int NT, bool TWO>
 __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel(const __grid_constant__ AttendParams p) {
     using L = Tile<TYPE, DB, NT>;
@@ -660,8 +663,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
 }
 
 // Rows of a CTA: 8, 16 or (of up to 128 elements) 32 on mma; where there are more, and a head has at most 128
-// elements, 128 on tcgen05.  (32 rows of 38 sequences of 8192 tokens: 287 us on mma, 351 on tcgen05; 128 rows: four
-// times 287, or 361.)
+// elements, 128 on tcgen05.  (38 sequences of 8192 tokens, 8 heads of 128, bf16 / fp16: 32 rows 198 / 256 us on mma, 33 to
+// 128 rows 336 / 354 on tcgen05, where two tiles of 32 would take twice 198 / 256.  Heads of 64: 33 to 64 rows 292 / 297
+// on tcgen05, 232 / 307 as two tiles on mma; trees of 60 rows over 200 to 4096 tokens of Q4_0, 31 and 37.)
 int tile_rows_of(int64_t max_new, int group, int D) {
     const int64_t rows = max_new * group;
     if (rows <= kMmaRows) return kMmaRows;
@@ -679,17 +683,17 @@ int64_t row_tiles_of(int64_t max_new, int group, int D) {
 // tokens 124 us for 97.  A sequence that is longer than the others takes up to four times the splits of an even
 // batch.  `even`: splits of each sequence in an even batch; the others as in AttendParams.
 struct Split {
-    int splits, budget, waves, least, fixed, even;
+    int splits, budget, waves, fixed, even;
 };
 Split split_of(int64_t n_seq, int H, int64_t row_tiles, int tile_rows, int64_t max_len) {
     const bool tc = tile_rows == kTcRows;
     const int64_t places = tc ? 152 : 304, per = H * row_tiles, units = n_seq * per;
-    Split s = {1, (int)n_seq, 1, tc ? 2 : 4, tc ? 2 : 6, 1};
+    Split s = {1, (int)n_seq, 1, tc ? 2 : 6, 1};
     if (units >= places) return s;
     s.budget = (int)(places / per);
     s.waves = 2 * units > places ? 2 : 1;
     const int64_t all = (int64_t)s.budget * s.waves, even = (all + n_seq - 1) / n_seq;
-    const int64_t steps = (max_len + kStep - 1) / kStep, most = (steps + s.least - 1) / s.least;
+    const int64_t most = (max_len + kStep - 1) / kStep;
     int64_t want = all - n_seq + 1;
     want = want < 4 * even ? want : 4 * even;
     want = want < most ? want : most;
@@ -778,7 +782,6 @@ cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uin
     p.splits = split.splits;
     p.budget = split.budget;
     p.waves = split.waves;
-    p.least = split.least;
     p.fixed = split.fixed;
     if ((size_t)p.splits * per_split > ws_bytes) p.splits = (int)(ws_bytes / per_split);
     if (p.splits < 2) {
