@@ -39,7 +39,9 @@ __device__ __forceinline__ float ex2(float x) {
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) { return tc::h2_bits(__hmul2(tc::bits_h2(a), tc::bits_h2(b))); }
 // Ones in the halves of d that are finite.
 __device__ __forceinline__ uint32_t finite2(uint32_t d) { return __hlt2_mask(__habs2(tc::bits_h2(d)), tc::bits_h2(0x7C007C00u)); }
+
 constexpr int kSorted = 128;               // sequences up to which a CTA sorts them itself
+
 // Splits are multiples of it, and may be as short: 777 tokens of 8 heads take 8.4 us with one step at least, 8.7 with two,
 // 10.1 with four (a tile of 32 keys takes a warp longer than the join takes for another part).
 constexpr int kStep = 128;

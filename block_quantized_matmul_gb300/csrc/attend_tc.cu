@@ -26,6 +26,13 @@
 // Warps: 0-3 and 4-7 rows, of even and odd tiles; 8-15 codes, up to two tiles ahead; 16 products.  (Four warps of
 // codes took twice as long as the rows: 277 us for 38 sequences of 8192 tokens, 128 rows, against 113 without.)
 // Tensor memory (512 columns): S twice 128 (p overwrites the S that it came from), O twice 128.
+//
+// What bounds it: a tile's chain (scores, two passes over them, p, values) at two tiles under way, and the instructions of
+// the exponentials and of the expansion.  38 sequences of 8192 tokens, 4 heads, 128 rows of bf16: 171 us, 478
+// TFLOP/s (2.7 us a tile of 128 keys); trees of 32 tokens x 4 over 8 sequences of 200 to 4096 tokens of Q4_0,
+// fp16: 42 us, of which 7 pass before the first scores, 4 in the writing of partial results and 6 in the join.
+// The passes over the scores are loops: unrolled, the code of the three roles does not stay in the instruction
+// cache (51 us for the trees, 437 for 38 sequences, 8 heads, fp16, against 42 and 354).
 // Every wait is bounded; on expiry the kernel records QMM_ERR_TIMEOUT, lets its products land, frees
 // tensor memory and returns.
 #include <cuda.h>

@@ -472,7 +472,8 @@ QMM_API size_t qmm_cache_attend_workspace_size(int64_t n_seq, int64_t max_new, i
  *   out[i, hq] = sum_j p_j v[j, h] / sum_j p_j,  p_j = exp(scale * q[i, hq] . k[j, h]) over the visible j,
  *   h = hq / (Hq / H) (Hq a multiple of H, at most 64 query heads to a key/value head).
  *   q_starts_dev  int32 [n_seq + 1], ascending from 0: sequence s has nq = q_starts[s + 1] - q_starts[s] new
- *                 tokens, rows q_starts[s].. of q; q_starts[n_seq] = T.
+ *                 tokens, rows q_starts[s].. of q; q_starts[n_seq] = T.  A sequence
+ *                 whose rows do not lie in q is skipped.
  *   kv_lens_dev   int32 [n_seq]: its cached tokens n, the new ones included (0 is fine).
  *   q_dev, out_dev  [T][Hq][D] of type dt (QMM_F16 or QMM_BF16), row strides ldq, ldo; 16-byte aligned with
  *                 ldq % 8 == 0 and ldo % 8 == 0.
@@ -480,7 +481,7 @@ QMM_API size_t qmm_cache_attend_workspace_size(int64_t n_seq, int64_t max_new, i
  *                 Otherwise uint64 [T], 8-byte aligned: bit b of a token's word says whether it sees new token b
  *                 of its sequence (itself included); new tokens past the 64th are then seen by nobody.
  *   max_new, max_len  no sequence has more new tokens, or more cached tokens, than these; rows past max_new are not
- *                 computed, max_len only steers the split.
+ *                 computed, max_len only bounds the splits (how long they are is decided on the GPU, from kv_lens).
  *   lse_dev       NULL, or fp32 [T][Hq]: ln sum_j exp(scale * q . k).
  *   workspace_dev  NULL, or workspace_bytes of scratch, 256-byte aligned; calls that overlap on the GPU must
  *                 use different workspaces.
