@@ -67,11 +67,13 @@ __device__ __forceinline__ uint32_t fewest_steps(const AttendParams &p, uint32_t
     uint32_t hi = max(lo, most);                                 // one split a sequence: not more than the budget
     for (int round = 0; round < 2 && lo < hi; ++round) {
         const uint32_t c = lo + (uint32_t)((uint64_t)(hi - lo) * lane / 31);
-        const uint32_t inv = 0xFFFFFFFFu / c + 1;                // t / c by a multiplication, at times one too many for t * c >= 2^32
+        // t / c, rounded up, by a multiplication (at times one too many for t * c >= 2^32; for c = 1, where 2^32 / c does not
+        // fit, (t + 1) (2^32 - 1) / 2^32 = t)
+        const uint32_t inv = 0xFFFFFFFFu / c + (c > 1), up = max(c - 1, 1u);
         uint32_t used = 0;
         for (int base = 0; base < n; base += 32) {
             const uint32_t t = base == 0 ? mine : steps_at(p, base);
-            for (int l = 0; l < min(32, n - base); ++l) used += max(1u, __umulhi(__shfl_sync(0xffffffffu, t, l) + c - 1, inv));
+            for (int l = 0; l < min(32, n - base); ++l) used += max(1u, __umulhi(__shfl_sync(0xffffffffu, t, l) + up, inv));
         }
         const int first = __ffs(__ballot_sync(0xffffffffu, used <= budget)) - 1;     // more keys, fewer splits: lane 31's fit
         hi = __shfl_sync(0xffffffffu, c, first);
