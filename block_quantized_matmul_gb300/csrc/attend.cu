@@ -589,7 +589,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
         start = __shfl_sync(0xffffffffu, from, __popc(upto) - 1);
         if (upto != 0xffffffffu) break;
     }
-    const int len = s >= 0 ? __ldcg(p.kv_lens + s) : 0;
+    const int len = s >= 0 ? __ldcg(p.kv_lens + s) : 0, end = s >= 0 ? __ldcg(p.q_starts + s + 1) : 0;
     if (warp == 0) {
         const uint32_t chunk = chunk_of(p, len_at(p, 0));
         if (lane == 0) s_chunk = chunk;
@@ -597,8 +597,9 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     __syncthreads();
     const int used = splits_of(cached(p, len), s_chunk);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // (rows past row_tiles were not computed)
-    if (at >= stride || s < 0 || used <= 1 || (tok - start) * p.group + hq % p.group >= (int64_t)p.row_tiles * p.tile_rows) return;
+    // rows of no sequence, and of those that do not lie in q, were not computed, nor were rows past row_tiles
+    if (at >= stride || s < 0 || start < 0 || tok >= end || end > p.T) return;
+    if (used <= 1 || (tok - start) * p.group + hq % p.group >= (int64_t)p.row_tiles * p.tile_rows) return;
     // four parts at a time, each under way before the first is used
     float m = -INFINITY, l = 0.0f, o[DB];
 #pragma unroll

@@ -473,7 +473,8 @@ QMM_API size_t qmm_cache_attend_workspace_size(int64_t n_seq, int64_t max_new, i
  *   h = hq / (Hq / H) (Hq a multiple of H, at most 64 query heads to a key/value head).
  *   q_starts_dev  int32 [n_seq + 1], ascending from 0: sequence s has nq = q_starts[s + 1] - q_starts[s] new
  *                 tokens, rows q_starts[s].. of q; q_starts[n_seq] = T.  A sequence
- *                 whose rows do not lie in q is skipped.
+ *                 whose rows do not all lie in q is skipped: its rows, as any that belong to no sequence, keep what
+ *                 out and lse hold.
  *   kv_lens_dev   int32 [n_seq]: its cached tokens n, the new ones included (0 is fine).
  *   q_dev, out_dev  [T][Hq][D] of type dt (QMM_F16 or QMM_BF16), row strides ldq, ldo; 16-byte aligned with
  *                 ldq % 8 == 0 and ldo % 8 == 0.
