@@ -134,7 +134,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     Rows w;
     if (!find_rows<kTcRows>(p, reinterpret_cast<int *>(smem), kThreadsTc, w)) return;
 
@@ -166,6 +165,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    // Not before the allocation: a kernel that allocates before it waits for this one, as the products do, could else
+    // hold columns of this SM's tensor memory while it waits, and the allocation would wait for them.
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int tiles = (int)((w.k1 - w.k0 + kKeysTc - 1) / kKeysTc);
     const int32_t *table = p.pages + w.s * p.ld_pages;
     // pages of a tile's eight groups of 16 keys, in lanes 0-7 (-1: past the keys)

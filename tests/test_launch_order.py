@@ -1,0 +1,43 @@
+"""The order of launch-overlap instructions in the kernels' sources, on the host: what a GPU test could only show by
+hanging, or by a race that it may not meet."""
+import glob
+import os
+import re
+
+import pytest
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "block_quantized_matmul_gb300", "csrc")
+START, WAIT, ALLOC = "griddepcontrol.launch_dependents", "griddepcontrol.wait", "tcgen05.alloc"
+
+
+def kernels():
+    """{name: body without comments} of every __global__ function of the library."""
+    found = {}
+    for path in sorted(glob.glob(os.path.join(CSRC, "*.cu"))):
+        with open(path) as f:
+            text = re.sub(r"//[^\n]*", "", f.read())
+        for m in re.finditer(r"__global__", text):
+            name = re.search(r"(\w+_kernel)\s*\(", text[m.end():])
+            at = text.index("{", m.end() + name.end())
+            depth, end = 1, at + 1
+            while depth:
+                depth += {"{": 1, "}": -1}.get(text[end], 0)
+                end += 1
+            found[f"{os.path.basename(path)}:{name.group(1)}"] = text[at:end]
+    return found
+
+
+KERNELS = kernels()
+
+
+def test_kernels_are_found():
+    assert len(KERNELS) >= 20 and "attend_tc.cu:attend_tc_kernel" in KERNELS and "mx4_gemm.cu:mx4_pair_kernel" in KERNELS
+
+
+@pytest.mark.parametrize("name", [n for n, body in KERNELS.items() if ALLOC in body and START in body])
+def test_tensor_memory_is_allocated_before_dependents_start(name):
+    """A dependent that allocates tensor memory and then waits for this kernel must not be able to take the columns that
+    a CTA of this kernel still has to allocate: neither could go on."""
+    body = KERNELS[name]
+    assert body.index(ALLOC) < body.index(START)
+    assert "__syncthreads" in body[body.index(ALLOC):body.index(START)] or "barrier.cluster.wait" in body[body.index(ALLOC):body.index(START)]
