@@ -58,6 +58,12 @@ __global__ void __launch_bounds__(kThreads) mx4_quantize_kernel(const T *__restr
             if ((lane & 7) == 0 && col[u] < K) *reinterpret_cast<uint32_t *>(scales + mx4_scale_word(row[u], col[u] >> 7, n128)) = word;
         }
     }
+    if (!trigger) {
+        // The product for few tokens streams its weight before it waits for the kernel before it, so an operand must be
+        // visible device-wide, to bulk copies too, by the time this grid's blocks have exited.
+        __threadfence();
+        asm volatile("fence.proxy.async.global;" ::: "memory");
+    }
 }
 
 template <bool VEC, typename T>

@@ -403,8 +403,9 @@ QMM_API size_t qmm_mx4_linear_workspace_size(int64_t M, int64_t K);
  * then qmm_mx4_matmul, bit for bit.  Up to 4 rows are quantized inside the product's kernel, and the
  * workspace is not touched.  That kernel starts streaming the weight before the kernel before it on the
  * stream has completed (x and y are touched only after it has): so the weight must not be written by the
- * kernel launched immediately before this call if that kernel itself lets dependents start early.  A
- * weight from qmm_mx4_quantize, from a copy, or from any earlier kernel is fine.
+ * kernel launched immediately before this call if that kernel itself lets dependents start early, or
+ * exits without a device-wide fence behind its stores.  A weight from qmm_mx4_quantize (which makes its
+ * stores visible before it exits), from a copy, or from any earlier kernel is fine.
  *   x_dev  M rows of K elements of type xdt, row m at x_dev + m*ldx; y_dev of type ydt as above.
  *   workspace_dev  >= qmm_mx4_linear_workspace_size(M, K) bytes, 256-byte aligned, overwritten; calls that
  *                  overlap on the GPU must use different workspaces.

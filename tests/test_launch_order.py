@@ -41,3 +41,11 @@ def test_tensor_memory_is_allocated_before_dependents_start(name):
     body = KERNELS[name]
     assert body.index(ALLOC) < body.index(START)
     assert "__syncthreads" in body[body.index(ALLOC):body.index(START)] or "barrier.cluster.wait" in body[body.index(ALLOC):body.index(START)]
+
+
+@pytest.mark.parametrize("name", ["repack.cu:repack_kernel", "repack.cu:repack_q4k_kernel", "mx4.cu:mx4_quantize_kernel"])
+def test_weights_are_visible_when_their_kernel_exits(name):
+    """Kernels that stream a weight before they wait rely on it: a fence behind the last store."""
+    body = KERNELS[name]
+    last_store = max(m.start() for m in re.finditer(r"[^=!<>]=[^=]", body))
+    assert "__threadfence()" in body[last_store:]
