@@ -185,7 +185,6 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
     }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         if (lane == 0) {
@@ -211,6 +210,9 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
             if (!p.early_weights) asm volatile("griddepcontrol.wait;" ::: "memory");
             for (int i = 0; i < head; ++i) weights(k0 + i, i);
             if (p.early_weights) asm volatile("griddepcontrol.wait;" ::: "memory");
+            // Only now: the next kernel may read its weight before it waits, which is sound as long as everything before
+            // this kernel is complete (and tensor memory has to be allocated before).
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
             for (int i = 0; i < head; ++i) tokens(k0 + i, i);
             int issued = head;
             for (int i = head; i < k1 - k0; ++i) {
@@ -525,11 +527,11 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;" ::: "memory");
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         if (lane == 0) {
             asm volatile("griddepcontrol.wait;" ::: "memory");
+            asm volatile("griddepcontrol.launch_dependents;" ::: "memory");      // only now: as in the kernel for few tokens
             Ring<S> r;
             const uint32_t st0 = smem_u32(smem), full0 = smem_u32(full), empty0 = smem_u32(empty);
             const uint32_t lead0 = peer_addr(full0, 0u);                   // the leader's, for both CTAs' copies

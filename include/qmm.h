@@ -181,9 +181,11 @@ QMM_API qmm_status qmm_quantize_act(const float *x_dev, int64_t M, int64_t K, in
  * It may start while the kernel before it on the stream is finishing, and it starts streaming the
  * weight tiles at once; it waits for that kernel to complete before it reads a_q, a_d or y.  So
  * the tiles must not be written by the kernel launched immediately before this call if that
- * kernel itself lets dependents start early.  Tiles from qmm_repack (which makes its stores
- * visible before it exits), from a copy, or from any earlier kernel are fine.  qmm_quantize_act
- * is launched the same way and waits before it reads x.
+ * kernel itself lets dependents start early, or exits without a device-wide fence behind its stores.
+ * Tiles from qmm_repack (which makes its stores visible before it exits), from a copy, or from any
+ * earlier kernel are fine; a decode kernel lets its dependents start before it has waited itself, so
+ * where only decode kernels lie between, the rule holds for the kernel before them.
+ * qmm_quantize_act is launched the same way and waits before it reads x.
  * Errors: INVALID_ARG (sizes, ldy < N, NULL), UNSUPPORTED, MISALIGNED, CUDA.
  */
 QMM_API qmm_status qmm_matmul(qmm_type t, const void *w_tiled_dev, int64_t K, int64_t N, const int8_t *a_q_dev,
@@ -405,7 +407,10 @@ QMM_API size_t qmm_mx4_linear_workspace_size(int64_t M, int64_t K);
  * stream has completed (x and y are touched only after it has): so the weight must not be written by the
  * kernel launched immediately before this call if that kernel itself lets dependents start early, or
  * exits without a device-wide fence behind its stores.  A weight from qmm_mx4_quantize (which makes its
- * stores visible before it exits), from a copy, or from any earlier kernel is fine.
+ * stores visible before it exits), from a copy, or from any earlier kernel is fine.  (The decode kernels of
+ * qmm_matmul, qmm_matmul_f32, qmm_matmul_f32_ws and qmm_matmul_flat let dependents start before they have
+ * waited themselves: where they alone lie between, the rule holds for the kernel before them.  All other
+ * kernels of the library wait first.)
  *   x_dev  M rows of K elements of type xdt, row m at x_dev + m*ldx; y_dev of type ydt as above.
  *   workspace_dev  >= qmm_mx4_linear_workspace_size(M, K) bytes, 256-byte aligned, overwritten; calls that
  *                  overlap on the GPU must use different workspaces.

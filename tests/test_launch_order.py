@@ -49,3 +49,15 @@ def test_weights_are_visible_when_their_kernel_exits(name):
     body = KERNELS[name]
     last_store = max(m.start() for m in re.finditer(r"[^=!<>]=[^=]", body))
     assert "__threadfence()" in body[last_store:]
+
+
+@pytest.mark.parametrize("name", [n for n, body in KERNELS.items() if START in body and n.startswith(("mx4", "cache", "attend."))
+                                  or n.startswith("attend_tc")])
+def test_dependents_start_after_the_wait(name):
+    """A kernel that reads its weight before it waits relies on the one before it: that has seen everything before itself
+    complete when it lets others start.  The join starts them sooner, behind an attention that has waited."""
+    body = KERNELS[name]
+    if name == "attend.cu:attend_join_kernel":
+        assert all(KERNELS[n].index(WAIT) < KERNELS[n].index(START) for n in ("attend.cu:attend_kernel", "attend_tc.cu:attend_tc_kernel"))
+    else:
+        assert body.index(WAIT) < body.index(START)
