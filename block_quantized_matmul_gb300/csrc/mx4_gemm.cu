@@ -20,6 +20,8 @@
 // take K in turn; each adds up the parts of its share of the tokens, in the order of the ranks, through
 // distributed shared memory.
 //
+// Long K: after each 16384 of K the sums go on in another accumulator (kDrain), and the result warps add them up in fp32.
+//
 // Warps: 0 copies, 1 products (and tensor memory), 2-5 results.
 // Every wait is bounded; on expiry the kernel records QMM_ERR_TIMEOUT, lets what is in flight land,
 // frees tensor memory and returns.
@@ -46,6 +48,10 @@ constexpr int kRows = 128;                 // weight rows per tile
 constexpr int kThreads = 192;
 constexpr int kEpilogue = 128;
 constexpr int kMaxSplit = 8;               // CTAs of a cluster
+// Stages (16384 of K) after which sums go on in a fresh accumulator.  The tensor cores round every addition to a sum towards
+// zero, so the error grows with the products added to one: with data of one sign 5.7e-6 of the sum at K = 16384, 1.2e-5 at
+// 32768 and 4.5e-5 at 131072 in a single accumulator, and the stated bound is 1e-5.
+constexpr int kDrain = 64;
 
 struct Mx4Params {
     const uint8_t *ws, *as;                // scales of the weight and the activations
@@ -55,6 +61,7 @@ struct Mx4Params {
     int nk;                                // stages: K / 256, rounded up
     int last_steps;                        // K = 64 products of the last stage (1 to 4)
     int split;                             // CTAs of a cluster, which share a tile's K
+    int sums, cols;                        // accumulators of a CTA; columns of tensor memory
     int early_weights;                     // the weight may be read before the kernel before this one is done
     int dtype;
     const void *x;                         // rows to be quantized here (fused)
@@ -120,17 +127,23 @@ struct Plan {
     static constexpr int kAS = kWS + 2 * kMx4ScaleBlock;
     static constexpr int kStageBytes = kAS + 2 * kMx4ScaleBlock;
     static constexpr int kStages = TN >= 32 ? 4 : 5;                     // two CTAs an SM
-    // tensor memory: the sums, then per stage the scales of two K = 128 halves (weight 4 columns, tokens 4)
-    static constexpr int kSums = TN < 32 ? 32 : TN;
+    // tensor memory: an accumulator of 32 columns for each kDrain stages, then per stage the scales of two K = 128 halves
+    // (weight 4 columns, tokens 4)
+    static constexpr int kSums = 32;
     static constexpr int kHalfCols = 8;
-    static constexpr int kColsUsed = kSums + kStages * 2 * kHalfCols;
-    static constexpr int kCols = kColsUsed <= 128 ? 128 : (kColsUsed <= 256 ? 256 : 512);
+    static constexpr int cols(int sums) {
+        const int used = sums * kSums + kStages * 2 * kHalfCols;
+        return used <= 128 ? 128 : (used <= 256 ? 256 : 512);
+    }
+    static constexpr int kMostSums = (int)(kMaxMatmulK / 256 / kDrain);
     // parts of the other CTAs of a cluster: [rank][token of this CTA's share][row]
     static constexpr int kParts = TN * kRows * 4;
     static constexpr int kPartsAt = kStages * kStageBytes;
     static constexpr int kBars = kPartsAt + kParts;
     static constexpr size_t kSmem = 1024 + kBars + (2 * kStages + 2) * 8 + 16;
-    static_assert(kColsUsed <= 512 && kSmem <= 227 * 1024, "does not fit");
+    static_assert(TN <= kSums && kMostSums * kSums + kStages * 2 * kHalfCols <= 512 && kSmem <= 227 * 1024, "does not fit");
+    // the CTAs of a cluster wait for one another and may share an SM, so that two have to fit its tensor memory
+    static_assert(cols(kMostSums / 2) <= 256, "does not fit");
 };
 
 // Stores results v[0..n) of tokens m0.. for weight row `row`, those that exist.
@@ -171,7 +184,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 1) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(L::kCols)
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_slot)), "r"(p.cols)
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
@@ -236,7 +249,9 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
             if (!wait_warp(full0 + 8 * r.s, r.phase, abort)) break;
             tc_fence_after();
             const uint64_t off = (uint64_t)(uint32_t)(r.s * (L::kStageBytes >> 4));
-            const uint32_t cols = tmem + (uint32_t)(L::kSums + r.s * 2 * L::kHalfCols);
+            const uint32_t cols = tmem + (uint32_t)(p.sums * L::kSums + r.s * 2 * L::kHalfCols);
+            const int in_sum = (k - k0) % kDrain;
+            const uint32_t sum = tmem + (uint32_t)((k - k0) / kDrain * L::kSums);
             const int steps = k == p.nk - 1 ? p.last_steps : 4;
             if (lead) {
 #pragma unroll
@@ -248,8 +263,8 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
                 for (int q = 0; q < 4; ++q) {
                     const uint32_t c = cols + (uint32_t)((q >> 1) * L::kHalfCols);
                     if (q < steps)
-                        mma_mxf4(tmem, w_desc + off + 2 * q, a_desc + off + 2 * q, idesc_mxf4(TN, q & 1), c, c + 4,
-                                 q > 0 ? 1u : (k > k0 ? 1u : 0u));
+                        mma_mxf4(sum, w_desc + off + 2 * q, a_desc + off + 2 * q, idesc_mxf4(TN, q & 1), c, c + 4,
+                                 q > 0 ? 1u : (in_sum > 0 ? 1u : 0u));
                 }
                 mma_commit(empty0 + 8 * r.s);
             }
@@ -315,13 +330,25 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
         asm volatile("griddepcontrol.wait;" ::: "memory");     // y may still be read by an earlier kernel
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
         constexpr int kChunk = 16;
+        const int sums = (k1 - k0 + kDrain - 1) / kDrain;
+        // results of tokens c0 .. c0 + 15: the accumulators added up
+        auto load_sums = [&](int c0, uint32_t (&v)[16]) {
+            tmem_ld16(t_lane + c0, v);
+            tmem_wait_ld(v);
+            for (int r = 1; r < sums; ++r) {
+                uint32_t u[16];
+                tmem_ld16(t_lane + r * L::kSums + c0, u);
+                tmem_wait_ld(u);
+#pragma unroll
+                for (int c = 0; c < 16; ++c) v[c] = __float_as_uint(__uint_as_float(v[c]) + __uint_as_float(u[c]));
+            }
+        };
         if (p.split == 1) {
 #pragma unroll 1
             for (int c0 = 0; c0 < TN && ok; c0 += kChunk) {
                 if (m0 + c0 >= p.M) break;
                 uint32_t v[16];
-                tmem_ld16(t_lane + c0, v);
-                tmem_wait_ld(v);
+                load_sums(c0, v);
                 if (n < p.N) {
                     if (p.dtype == QMM_F32) store_tokens(static_cast<float *>(p.y), p.ldy, m0 + c0, p.M, n, v, kChunk);
                     else if (p.dtype == QMM_F16) store_tokens(static_cast<__half *>(p.y), p.ldy, m0 + c0, p.M, n, v, kChunk);
@@ -335,8 +362,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
 #pragma unroll 1
             for (int c0 = 0; c0 < TN && ok; c0 += kChunk) {
                 uint32_t v[16];
-                tmem_ld16(t_lane + c0, v);
-                tmem_wait_ld(v);
+                load_sums(c0, v);
 #pragma unroll
                 for (int c = 0; c < kChunk; ++c) {
                     if (m0 + c0 + c >= p.M) break;
@@ -365,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
     __syncthreads();
     if (warp == 1) {
         tc_fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(L::kCols) : "memory");
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(p.cols) : "memory");
     }
 }
 
@@ -383,6 +409,8 @@ cudaError_t launch_tn(Mx4Params p, const uint8_t *wc, int64_t K, const uint8_t *
     constexpr int64_t slots = 304;
     p.split = 1;
     while (p.split < kMaxSplit && 2 * p.split <= TN && 2 * tiles * p.split <= slots && p.nk >= 8 * p.split) p.split *= 2;
+    p.sums = ((p.nk + p.split - 1) / p.split + kDrain - 1) / kDrain;
+    p.cols = L::cols(p.sums);
     alignas(64) CUtensorMap wm, am;
     e = make_map_2d(&wm, CU_TENSOR_MAP_DATA_TYPE_UINT8, wc, (uint64_t)(K / 2), (uint64_t)p.N, (uint64_t)(K / 2), 128, kRows,
                     CU_TENSOR_MAP_SWIZZLE_128B);
@@ -466,6 +494,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t *r) {
           "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+// Eight columns, loaded by the time it returns.
+__device__ __forceinline__ void tmem_ld8_wait(uint32_t taddr, uint32_t (&r)[8]) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
 // Completes the loads of r and keeps their uses behind it.
 __device__ __forceinline__ void tmem_wait32(uint32_t *r) {
     asm volatile("tcgen05.wait::ld.sync.aligned;"
@@ -492,7 +528,8 @@ struct PairParams {
     }
 };
 
-template <typename T>
+// LONG: more than kDrain stages.  The accumulator then starts anew after each kDrain, and the result warps add up.
+template <typename T, bool LONG>
 __global__ void __launch_bounds__(Pair::kThreads, 1)
 mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, const __grid_constant__ CUtensorMap a_map,
                 const __grid_constant__ CUtensorMap ws_map, const __grid_constant__ CUtensorMap as_map) {
@@ -573,7 +610,8 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
             for (int tile = pair; tile < p.tiles && ok; tile += pairs) {
                 for (int k = 0; k < p.nk; ++k, r.next()) {
                     if (!wait_warp(full0 + 8 * r.s, r.phase, abort)) { ok = false; break; }
-                    if (k == 0) {
+                    const int in_sum = LONG ? k % kDrain : k;
+                    if (in_sum == 0) {
                         if (!__all_sync(0xffffffffu, wait_cluster_bounded(smem_u32(acc_empty), acc_phase, abort, &g_mx4_status, kWaitLimitNs))) {
                             ok = false;
                             break;
@@ -596,10 +634,10 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
                             const uint32_t c = cols + (uint32_t)((q >> 1) * L::kHalfCols);
                             if (q < steps)
                                 mma_mxf4_pair(tmem, w_desc + off + 2 * q, a_desc + off + 2 * q, (q & 1) ? id1 : id0, c, c + 4,
-                                              q > 0 ? 1u : (k > 0 ? 1u : 0u));
+                                              q > 0 ? 1u : (in_sum > 0 ? 1u : 0u));
                         }
                         mma_commit_pair(empty0 + 8 * r.s);
-                        if (k == p.nk - 1) mma_commit_pair(smem_u32(acc_full));
+                        if (k == p.nk - 1 || (LONG && in_sum == kDrain - 1)) mma_commit_pair(smem_u32(acc_full));
                     }
                     __syncwarp();
                 }
@@ -628,6 +666,26 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive_peer(free_bar);
+            if constexpr (LONG) {
+                bool ok = true;
+                for (int k = kDrain; k < p.nk; k += kDrain) {
+                    ++done;
+                    ok = wait_warp(smem_u32(acc_full), (uint32_t)(done & 1), abort);
+                    if (!ok) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int c = 0; c < 16; ++c) {
+                        uint32_t u[8];
+                        tmem_ld8_wait(t_lane + 8 * c, u);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[8 * c + i] = __float_as_uint(__uint_as_float(v[8 * c + i]) + __uint_as_float(u[i]));
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_peer(free_bar);
+                }
+                if (!ok) break;
+            }
             int mt, nt;
             p.place(tile, mt, nt);
             const int64_t n = (int64_t)nt * 2 * kRows + rank * kRows + row, m0 = (int64_t)mt * kPairTok + half * (kPairTok / 2);
@@ -691,10 +749,11 @@ cudaError_t launch_pairs(const Mx4Params &q, const uint8_t *wc, int64_t K, const
         cfg.numAttrs = 2;
         return cudaLaunchKernelEx(&cfg, kern, p, wm, am, wsm, asm_);
     };
-    static int done_f32[4] = {0, 0, 0, 0}, done_f16[4] = {0, 0, 0, 0}, done_bf16[4] = {0, 0, 0, 0};
-    if (q.dtype == QMM_F32) return go(mx4_pair_kernel<float>, done_f32);
-    if (q.dtype == QMM_F16) return go(mx4_pair_kernel<__half>, done_f16);
-    return go(mx4_pair_kernel<__nv_bfloat16>, done_bf16);
+    static int done[6][4] = {};
+    const bool lng = p.nk > kDrain;
+    if (q.dtype == QMM_F32) return lng ? go(mx4_pair_kernel<float, true>, done[0]) : go(mx4_pair_kernel<float, false>, done[1]);
+    if (q.dtype == QMM_F16) return lng ? go(mx4_pair_kernel<__half, true>, done[2]) : go(mx4_pair_kernel<__half, false>, done[3]);
+    return lng ? go(mx4_pair_kernel<__nv_bfloat16, true>, done[4]) : go(mx4_pair_kernel<__nv_bfloat16, false>, done[5]);
 }
 
 }  // namespace
