@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
         const uint64_t w_desc = smem_desc_sw128(st0 + L::kW), a_desc = smem_desc_sw128(st0 + L::kA);
         const uint64_t ws_desc = smem_desc_scales(st0 + L::kWS), as_desc = smem_desc_scales(st0 + L::kAS);
         constexpr int kHalf = kMx4ScaleBlock >> 4;                 // in units of a descriptor's address
+        asm volatile("griddepcontrol.wait;" ::: "memory");     // here too: however long the kernel before takes, no bounded wait sees it
         Ring<S> r;
         for (int k = k0; k < k1; ++k, r.next()) {
             if (!wait_warp(full0 + 8 * r.s, r.phase, abort)) break;
@@ -278,8 +279,8 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
     } else {
         const int qd = warp & 3, row = 32 * qd + lane;
         const int64_t n = n0 + row;
+        asm volatile("griddepcontrol.wait;" ::: "memory");     // y may still be read by an earlier kernel, x written
         if constexpr (kFused) {
-            asm volatile("griddepcontrol.wait;" ::: "memory");
             // row r of a stage goes to warp r % 4, 8 elements a lane; the next stage's rows are loaded before this
             // one's are worked on
             constexpr int kMine = kMx4FusedTokens / 4;
@@ -327,7 +328,6 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
         }
         bool ok = wait_warp(smem_u32(done), 0u, abort) && !*abort;
         tc_fence_after();
-        asm volatile("griddepcontrol.wait;" ::: "memory");     // y may still be read by an earlier kernel
         const uint32_t t_lane = tmem + ((uint32_t)(32 * qd) << 16);
         constexpr int kChunk = 16;
         const int sums = (k1 - k0 + kDrain - 1) / kDrain;
@@ -604,6 +604,7 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
             constexpr uint32_t id0 = idesc_mxf4(kPairTok, 0) + ((uint32_t)(kRows >> 4) << 24);      // 256 rows
             constexpr uint32_t id1 = idesc_mxf4(kPairTok, 1) + ((uint32_t)(kRows >> 4) << 24);
             constexpr int kHalf = kMx4ScaleBlock >> 4;             // in units of a descriptor's address
+            asm volatile("griddepcontrol.wait;" ::: "memory");     // before the first bounded wait
             bool ok = true;
             uint32_t acc_phase = 1;
             Ring<S> r;

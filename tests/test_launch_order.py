@@ -61,3 +61,15 @@ def test_dependents_start_after_the_wait(name):
         assert all(KERNELS[n].index(WAIT) < KERNELS[n].index(START) for n in ("attend.cu:attend_kernel", "attend_tc.cu:attend_tc_kernel"))
     else:
         assert body.index(WAIT) < body.index(START)
+
+
+@pytest.mark.parametrize("name", ["mx4_gemm.cu:mx4_gemm_kernel", "mx4_gemm.cu:mx4_pair_kernel"])
+def test_bounded_waits_start_after_the_wait(name):
+    """A wait with a limit must not have the kernel before in it, which may take any time: each warp's part waits for that
+    kernel (without a limit) before its first bounded wait."""
+    body = KERNELS[name]
+    roles = re.split(r"if \(warp == 0\) \{|\} else if \(warp == 1\) \{\s*\n|\n    \} else \{", body[body.rindex("uint32_t tmem = *tmem_slot"):])[1:4]
+    assert len(roles) == 3
+    for part in roles:
+        first = re.search(r"wait_(bounded|warp|cluster_bounded)\(", part)
+        assert first and WAIT in part[:first.start()]
