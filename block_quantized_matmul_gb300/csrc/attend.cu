@@ -199,7 +199,7 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
     // lanes 0-15 know the page of the tile's first 16 keys, lanes 16-31 that of the others
     auto page_of = [&](int i) -> int {
         const int64_t j = w.k0 + (int64_t)(i * kWarps + warp) * kKeys + (lane & 16);
-        return i < mine && j < w.k1 ? table[j >> p.log_p] : -1;
+        return i < mine && j < w.k1 && QMM_DCHECK((j >> p.log_p) < p.ld_pages) ? table[j >> p.log_p] : -1;
     };
     auto issue = [&](int i, int page) {
         if (i < mine) {
@@ -217,8 +217,8 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
             for (int it = 0; it < ITS; ++it) {
                 const int u = it * 32 + lane, key = u / PK, c = u % PK;
                 const bool second = PK % 2 == 0 ? it >= ITS / 2 : key >= 16;
-                if (second ? ok1 : ok0) {
-                    const int64_t src = (second ? a1 : a0) + it * 512;
+                const int64_t src = (second ? a1 : a0) + it * 512;
+                if ((second ? ok1 : ok0) && QMM_DCHECK(src >= 0 && src + 16 <= p.n_pages * page_bytes)) {
                     const int blk = c * 16 / UNIT, in = c * 16 % UNIT;
                     const int vrow = (key & 16) | ((key & 1) << 3) | ((key & 15) >> 1);
                     cp_async16(dst + L::kK + (key * DB + swz<DB, SPAN>(key, blk)) * UNIT + in, p.k_cache + src);
@@ -228,8 +228,8 @@ __global__ void __launch_bounds__(Tile<TYPE, DB, NT>::kThreads, 2) attend_kernel
             // scales: 2 * DB pieces for 16 keys
             if (lane < 4 * DB) {
                 const bool second = lane >= 2 * DB;
-                if (second ? ok1 : ok0) {
-                    const int64_t src = (second ? c1 + off1 * (2 * DB) - 32 * DB : c0 + off0 * (2 * DB)) + p.P * CB + lane * 16;
+                const int64_t src = (second ? c1 + off1 * (2 * DB) - 32 * DB : c0 + off0 * (2 * DB)) + p.P * CB + lane * 16;
+                if ((second ? ok1 : ok0) && QMM_DCHECK(src >= 0 && src + 16 <= p.n_pages * page_bytes)) {
                     cp_async16(dst + L::kKs + lane * 16, p.k_cache + src);
                     cp_async16(dst + L::kVs + lane * 16, p.v_cache + src);
                 }
@@ -600,6 +600,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     // rows of no sequence, and of those that do not lie in q, were not computed, nor were rows past row_tiles
     if (at >= stride || s < 0 || start < 0 || tok >= end || end > p.T) return;
     if (used <= 1 || (tok - start) * p.group + hq % p.group >= (int64_t)p.row_tiles * p.tile_rows) return;
+    if (!QMM_DCHECK(used <= p.splits && tok < p.T)) return;
     // four parts at a time, each under way before the first is used
     float m = -INFINITY, l = 0.0f, o[DB];
 #pragma unroll

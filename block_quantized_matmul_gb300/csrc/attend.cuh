@@ -163,6 +163,8 @@ __device__ __forceinline__ bool find_rows(const AttendParams &p, int *scratch, i
         const bool rest = s < 0;
         if (rest) s = j;
         if (s >= (int)p.n_seq) return false;
+        // every split has a CTA: the whole ones before this rest, and a rest of each sequence
+        if (rest) (void)QMM_DCHECK(((int)w.s - j + (int)p.n_seq) * p.H * p.row_tiles <= (int)gridDim.x);
         if (s < 32) {
             len = __shfl_sync(0xffffffffu, lens, s);
             q0 = __shfl_sync(0xffffffffu, from, s);
@@ -228,6 +230,7 @@ __device__ __forceinline__ void write_row(const AttendParams &p, const Rows &w, 
                                           float sum) {
     const int r = w.r0 + row, i = r / p.group, hq = w.h * p.group + (r - i * p.group), Hq = p.H * p.group;
     const int64_t at = (w.q0 + i) * Hq + hq;
+    if (!QMM_DCHECK(row < w.rows && w.q0 + i < p.T && hq < Hq && d + N <= D && w.sp < w.used && (w.used == 1 || w.used <= p.splits))) return;
     if (w.used == 1) {
         const int64_t to = (w.q0 + i) * p.ldo + (int64_t)hq * D + d;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
@@ -287,6 +290,7 @@ __device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &
         float top = -INFINITY, sum = 0.0f;                      // in powers of two
         for (int64_t j = w.k0; j < w.k1; ++j) {
             if (j >= w.first && !sees(p.tree, w.q0 + i, i, j - w.first)) continue;
+            if (!QMM_DCHECK((j >> p.log_p) < p.ld_pages && w.s < p.n_seq)) continue;
             const int64_t page = p.pages[w.s * p.ld_pages + (j >> p.log_p)];
             if (page < 0 || page >= p.n_pages) continue;
             const int64_t at = cache_chunk(TYPE, p.H, D, p.P, page, w.h);

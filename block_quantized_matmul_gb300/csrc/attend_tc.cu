@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
     // pages of a tile's eight groups of 16 keys, in lanes 0-7 (-1: past the keys)
     auto pages_of = [&](int i) -> int {
         const int64_t j = w.k0 + (int64_t)i * kKeysTc + 16 * (lane & 7);
-        const int page = i < tiles && j < w.k1 ? table[j >> p.log_p] : -1;
+        const int page = i < tiles && j < w.k1 && QMM_DCHECK((j >> p.log_p) < p.ld_pages) ? table[j >> p.log_p] : -1;
         return page < p.n_pages ? page : -1;
     };
 
@@ -348,8 +348,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                 for (int it = 0; it < KP; ++it) {
                     const int u = it * kCodeThreads + tid, key = u / PK, c = u % PK;
                     const int pg = __shfl_sync(0xffffffffu, page, (key >> 4) & 7);
-                    if (pg >= 0 && key < 128) {
-                        const int64_t at = (int64_t)pg * page_bytes + head + ((off0 + key) & (p.P - 1)) * CB + 16 * c;
+                    const int64_t at = (int64_t)pg * page_bytes + head + ((off0 + key) & (p.P - 1)) * CB + 16 * c;
+                    if (pg >= 0 && key < 128 && QMM_DCHECK(at + 16 <= p.n_pages * page_bytes)) {
                         cp_async16(st + key * L::kPitch + 16 * c, p.k_cache + at);
                         cp_async16(st + L::kRawV + key * L::kPitch + 16 * c, p.v_cache + at);
                     }
@@ -357,8 +357,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1) attend_tc_kernel(const __grid_c
                 // scales: 2 * DB pieces for each group of 16 keys
                 const int grp = tid / (2 * DB), c = tid % (2 * DB);
                 const int pg = __shfl_sync(0xffffffffu, page, grp & 7);
-                if (grp < 8 && pg >= 0) {
-                    const int64_t at = (int64_t)pg * page_bytes + head + p.P * CB + ((off0 + 16 * grp) & (p.P - 1)) * (2 * DB) + 16 * c;
+                const int64_t at = (int64_t)pg * page_bytes + head + p.P * CB + ((off0 + 16 * grp) & (p.P - 1)) * (2 * DB) + 16 * c;
+                if (grp < 8 && pg >= 0 && QMM_DCHECK(at + 16 <= p.n_pages * page_bytes)) {
                     cp_async16(st + L::kRawKs + tid * 16, p.k_cache + at);
                     cp_async16(st + L::kRawVs + tid * 16, p.v_cache + at);
                 }

@@ -111,6 +111,10 @@ struct Place {
         : chunk(((slot_page * H + h) << log_p) * kToken), off(off_), P(1 << log_p) {}
     __device__ __forceinline__ int64_t codes(int block, int in) const { return chunk + (off * kCodes + block * (kCodes / DB) + in); }
     __device__ __forceinline__ int64_t scale(int block) const { return chunk + (P * kCodes + (off * DB + block) * 2); }
+    // A block's codes and scale lie in a cache of so many pages (for checks).
+    __device__ __forceinline__ bool inside(int64_t pages, int H, int block) const {
+        return off >= 0 && off < P && block >= 0 && block < DB && chunk >= 0 && chunk + (int64_t)P * kToken <= pages * H * P * kToken;
+    }
 };
 
 // A thread takes pieces of 16 elements; blockIdx.y: 0 keys, 1 values.
@@ -152,8 +156,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const __grid_cons
             }
             if (slot[u] < 0 || slot[u] >= p.n_slots) continue;
             const int h = (int)(in_tok[u] / (2 * DB)), c = (int)(in_tok[u] % (2 * DB));      // elements 16c .. 16c + 15 of the head
-            if (!QMM_DCHECK(h < p.H)) continue;
             const Place<TYPE, DB> at(slot[u] >> p.log_p, h, p.H, (int)slot[u] & ((1 << p.log_p) - 1), p.log_p);
+            if (!QMM_DCHECK(h < p.H && at.inside(p.n_slots >> p.log_p, p.H, c >> 1))) continue;
             if constexpr (TYPE == QMM_Q8_0) {
                 *reinterpret_cast<uint4 *>(cache + at.codes(c >> 1, 16 * (c & 1))) = make_uint4(w[0], w[1], w[2], w[3]);
             } else {
@@ -248,7 +252,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
             int off = 0;
             if (tok < p.T) {
                 const int64_t s = find_seq(p.starts, p.n_seq, tok), pos = tok - p.starts[s], pi = pos >> p.log_p;
-                if (pos >= 0 && pi < p.ld_pages) page = p.pages[s * p.ld_pages + pi];
+                if (pos >= 0 && pi < p.ld_pages && QMM_DCHECK(s < p.n_seq)) page = p.pages[s * p.ld_pages + pi];
                 if (page >= p.n_pages) page = -1;
                 off = (int)(pos & ((1 << p.log_p) - 1));
             }
@@ -270,6 +274,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
                 if (i < items && s_page[tok] >= 0) {
                     const int h = (int)(in_tok / (2 * DB)), c = (int)(in_tok % (2 * DB));
                     const Place<TYPE, DB> at(s_page[tok], h, p.H, s_off[tok], p.log_p);
+                    if (!QMM_DCHECK(h < p.H && at.inside(p.n_pages, p.H, c >> 1))) continue;
                     d[u] = *reinterpret_cast<const uint16_t *>(cache + at.scale(c >> 1));
                     if constexpr (TYPE == QMM_Q8_0) {
                         w[u] = *reinterpret_cast<const uint4 *>(cache + at.codes(c >> 1, 16 * (c & 1)));
@@ -283,7 +288,7 @@ __global__ void __launch_bounds__(kThreads) cache_read_kernel(const __grid_const
 #pragma unroll
             for (int u = 0; u < kBatch; ++u) {
                 const uint32_t i = base + u * kThreads, tok = p.per_tok(i), in_tok = i - tok * p.per_tok.d;
-                if (i >= items) break;
+                if (i >= items || !QMM_DCHECK(t0 + tok < p.T)) break;
                 const uint32_t d2 = d[u] * 0x00010001u;
                 constexpr int kW4 = sizeof(T);                   // words of four elements
                 uint32_t v[4 * kW4];

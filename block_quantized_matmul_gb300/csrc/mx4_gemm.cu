@@ -151,7 +151,7 @@ template <typename T>
 __device__ __forceinline__ void store_tokens(T *y, int64_t ldy, int64_t m0, int64_t M, int64_t row, const uint32_t *v, int n) {
 #pragma unroll
     for (int c = 0; c < n; ++c)
-        if (m0 + c < M) float_to_elem(__uint_as_float(v[c]), y[(m0 + c) * ldy + row]);
+        if (m0 + c < M && QMM_DCHECK(row < ldy)) float_to_elem(__uint_as_float(v[c]), y[(m0 + c) * ldy + row]);
 }
 
 // XT: void for operands that are quantized already, else the element type of rows that the result warps
@@ -205,6 +205,8 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
             auto weights = [&](int k, int s) {                 // announces the whole stage
                 const uint32_t st = smem_u32(smem + s * L::kStageBytes), bar = smem_u32(&full[s]);
                 const uint32_t sb = (uint32_t)blocks(k) * kMx4ScaleBlock;
+                // (the stage's wait then runs out)
+                if (!QMM_DCHECK(s < S && k < p.nk && blocks(k) > 0 && 2 * k + blocks(k) <= p.n128 && n0 < p.N)) return;
                 mbar_arrive_expect_tx(bar, kFused ? (uint32_t)(kRows * 128) + sb
                                                   : (uint32_t)(kRows * 128 + TN * 128) + 2 * sb);
                 tma_load_2d(st + L::kW, &w_map, k * 128, (int)n0, bar);
@@ -367,6 +369,7 @@ __global__ void __launch_bounds__(kThreads) mx4_gemm_kernel(const __grid_constan
                 for (int c = 0; c < kChunk; ++c) {
                     if (m0 + c0 + c >= p.M) break;
                     const int to = (c0 + c) / share, at = (rank * share + (c0 + c) % share) * kRows + row;
+                    if (!QMM_DCHECK(to < p.split && at < TN * kRows)) break;
                     asm volatile("st.shared::cluster.b32 [%0], %1;" ::"r"(peer_addr(smem_u32(parts + at), (uint32_t)to)), "r"(v[c])
                                  : "memory");
                 }
@@ -691,7 +694,7 @@ mx4_pair_kernel(const PairParams p, const __grid_constant__ CUtensorMap w_map, c
             p.place(tile, mt, nt);
             const int64_t n = (int64_t)nt * 2 * kRows + rank * kRows + row, m0 = (int64_t)mt * kPairTok + half * (kPairTok / 2);
             const int have = (int)min((int64_t)(kPairTok / 2), p.M - m0);
-            if (n < p.N) {
+            if (n < p.N && QMM_DCHECK(mt >= 0 && mt < p.m_tiles && nt >= 0 && nt < p.n_tiles && n < p.ldy)) {
                 T *y = static_cast<T *>(p.y) + m0 * p.ldy + n;
 #pragma unroll
                 for (int c = 0; c < kPairTok / 2; ++c) {
