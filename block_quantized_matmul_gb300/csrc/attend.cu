@@ -580,16 +580,22 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     // The lengths are no results of the kernel before this one, which has waited for whoever wrote them.  Nobody
     // leaves before the wait: a kernel that waits for this one has to find the one before it complete too.
     __shared__ uint32_t s_chunk;
-    int s = -1, start = 0;                                       // the row's sequence: the last that starts at or before it
-    for (int base = 0; base < (int)p.n_seq; base += 32) {
-        const int from = base + lane < (int)p.n_seq ? __ldcg(p.q_starts + base + lane) : INT_MAX;
+    int s = -1, start = 0, end = 0;                              // the row's sequence: the last that starts at or before it
+    for (int base = 0; base <= (int)p.n_seq; base += 32) {
+        const int from = base + lane <= (int)p.n_seq ? __ldcg(p.q_starts + base + lane) : INT_MAX;
         const unsigned upto = __ballot_sync(0xffffffffu, from <= tok);
-        if (upto == 0) break;
-        s = base + __popc(upto) - 1;
-        start = __shfl_sync(0xffffffffu, from, __popc(upto) - 1);
-        if (upto != 0xffffffffu) break;
+        const int n = __popc(upto);
+        if (n > 0) {
+            s = base + n - 1;
+            start = __shfl_sync(0xffffffffu, from, n - 1);
+        }
+        if (n < 32) {
+            end = __shfl_sync(0xffffffffu, from, n);             // where the next one starts
+            break;
+        }
     }
-    const int len = s >= 0 ? __ldcg(p.kv_lens + s) : 0, end = s >= 0 ? __ldcg(p.q_starts + s + 1) : 0;
+    const bool mine = s >= 0 && s < (int)p.n_seq;                // s = n_seq: behind the last
+    const int len = mine ? __ldcg(p.kv_lens + s) : 0;
     if (warp == 0) {
         const uint32_t chunk = chunk_of(p, len_at(p, 0));
         if (lane == 0) s_chunk = chunk;
@@ -598,7 +604,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) attend_join_kernel(const Atte
     const int used = splits_of(cached(p, len), s_chunk);
     asm volatile("griddepcontrol.wait;" ::: "memory");
     // rows of no sequence, and of those that do not lie in q, were not computed, nor were rows past row_tiles
-    if (at >= stride || s < 0 || start < 0 || tok >= end || end > p.T) return;
+    if (at >= stride || !mine || start < 0 || end > p.T) return;
     if (used <= 1 || (tok - start) * p.group + hq % p.group >= (int64_t)p.row_tiles * p.tile_rows) return;
     if (!QMM_DCHECK(used <= p.splits && tok < p.T)) return;
     // four parts at a time, each under way before the first is used
