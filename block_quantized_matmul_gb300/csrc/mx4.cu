@@ -3,7 +3,7 @@
 // Both directions move each element once and do a few operations on it; what costs beside the bytes is
 // instructions.  A lane takes 16 consecutive elements, half a block (a warp: 512 of a row): with 8, the
 // addresses, shuffles and scale bytes of a lane's piece weigh twice as much (8192 x 14336 bf16: 77 us, with 16 about
-// 50).  Bound by memory: 14336 x 4096 fp32 to MX4 and back, 532 MB, 89 us, 6.0 TB/s.
+// 50).  Bound by memory: 14336 x 4096 fp32 to MX4 and back, 532 MB, 90 us, 5.9 TB/s.
 // Loads and stores are 32 bytes; two lanes of a block agree on its largest magnitude, and the scale
 // bytes of four blocks leave as one word.  A warp loads kBatch pieces before it works on the first,
 // so that enough bytes are on their way to hide memory's latency.
