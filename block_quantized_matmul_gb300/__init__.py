@@ -36,7 +36,9 @@ __all__ = [
     "qmm_selftest_timeout",
     "F32", "F16", "BF16", "DTYPES", "mx4_codes_size", "mx4_scales_size", "mx4_linear_workspace_size", "qmm_mx4_quantize",
     "qmm_mx4_dequantize", "qmm_mx4_matmul", "qmm_mx4_linear", "cache_page_size", "cache_attend_workspace_size",
-    "qmm_cache_write", "qmm_cache_read", "qmm_cache_attend",
+    "qmm_cache_write", "qmm_cache_read", "qmm_cache_attend", "qmm_cache_plan", "cache_bounds_size", "qmm_cache_bounds",
+    "cache_select_workspace_size", "qmm_cache_select", "cache_attend_chosen_workspace_size", "qmm_cache_attend_chosen",
+    "qmm_norm", "qmm_norm_q8", "qmm_norm_mx4", "qmm_sample",
 ]
 
 Q4_0, Q8_0, IQ4_NL, MXFP4, Q4_1, Q4_K = 0, 1, 2, 3, 4, 5
@@ -113,7 +115,23 @@ def lib():
         L.qmm_cache_attend_workspace_size.restype = sz
         L.qmm_cache_attend.argtypes = [i32, vp, vp, i64, i64, i64, i64, vp, i64, vp, vp, i64, i32, vp, i64, i64, i64, vp,
                                        ctypes.c_float, i64, i64, vp, i64, vp, vp, sz, vp]
-        for fn in ("qmm_mx4_quantize", "qmm_mx4_dequantize", "qmm_mx4_matmul", "qmm_mx4_linear", "qmm_cache_write",
+        L.qmm_cache_plan.argtypes = [vp, vp, i64, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp]
+        L.qmm_cache_bounds_size.argtypes = [i64, i64]
+        L.qmm_cache_select_workspace_size.argtypes = [i64] * 4
+        L.qmm_cache_attend_chosen_workspace_size.argtypes = [i64] * 6
+        for fn in ("qmm_cache_bounds_size", "qmm_cache_select_workspace_size", "qmm_cache_attend_chosen_workspace_size"):
+            getattr(L, fn).restype = sz
+        L.qmm_cache_bounds.argtypes = [i32, vp, i64, i64, i64, i64, vp, i64, vp, vp, i64, i64, i64, vp, vp]
+        L.qmm_cache_select.argtypes = [vp, i64, i64, i64, i64, vp, i64, vp, vp, i64, i32, vp, i64, i64, i64, vp, i64, i64, i64, i64,
+                                       i64, vp, vp, sz, vp]
+        L.qmm_cache_attend_chosen.argtypes = [i32, vp, vp, i64, i64, i64, i64, vp, i64, vp, vp, i64, i32, vp, i64, i64, i64, vp,
+                                              ctypes.c_float, vp, i64, vp, i64, vp, vp, sz, vp]
+        norm = [i32, vp, i64, i32, vp, i64, i64, i64, vp, vp, i64, ctypes.c_float, vp, ctypes.c_float, vp, i64]
+        L.qmm_norm.argtypes = norm + [i32, vp, i64, vp]
+        L.qmm_norm_q8.argtypes = L.qmm_norm_mx4.argtypes = norm + [vp, vp, vp]
+        L.qmm_sample.argtypes = [i32, vp, i64, i64, i64, vp, vp, vp, vp, vp, vp, vp, vp]
+        for fn in ("qmm_cache_plan", "qmm_cache_bounds", "qmm_cache_select", "qmm_cache_attend_chosen", "qmm_norm", "qmm_norm_q8",
+                   "qmm_norm_mx4", "qmm_sample", "qmm_mx4_quantize", "qmm_mx4_dequantize", "qmm_mx4_matmul", "qmm_mx4_linear", "qmm_cache_write",
                    "qmm_cache_read", "qmm_cache_attend", "qmm_quantize_weight", "qmm_repack", "qmm_unpack", "qmm_quantize_act", "qmm_matmul",
                    "qmm_matmul_path", "qmm_device_status", "qmm_matmul_ws", "qmm_matmul_noalloc", "qmm_matmul_f32",
                    "qmm_matmul_flat", "qmm_selftest_timeout", "qmm_matmul_f32_ws"):
@@ -356,3 +374,82 @@ def qmm_cache_attend(type_, k_cache, v_cache, n_pages: int, P: int, H: int, D: i
                                   _ptr(q_starts), _ptr(kv_lens), n_seq, _dt(dtype), _ptr(q), ldq, T, Hq, _ptr(tree),
                                   float(scale), max_new, max_len, _ptr(out), ldo, _ptr(lse), _ptr(workspace),
                                   int(workspace_bytes), _stream(stream)))
+
+
+def qmm_cache_plan(lens, news, n_seq: int, P: int, pages, ld_pages: int, ring, n_ring: int, ring_at, T: int, q_starts, kv_lens, slots,
+                   positions, next_lens, next_at, stream=None) -> None:
+    """Page tables, slots and row starts of a step from the requests' lengths and new tokens; positions, next_lens and
+    next_at may be None, next_lens may be lens and next_at may be ring_at."""
+    _check("qmm_cache_plan", lib().qmm_cache_plan(_ptr(lens), _ptr(news), n_seq, P, _ptr(pages), ld_pages, _ptr(ring), n_ring,
+                                                  _ptr(ring_at), T, _ptr(q_starts), _ptr(kv_lens), _ptr(slots), _ptr(positions),
+                                                  _ptr(next_lens), _ptr(next_at), _stream(stream)))
+
+
+def cache_bounds_size(H: int, D: int) -> int:
+    return int(lib().qmm_cache_bounds_size(H, D))
+
+
+def qmm_cache_bounds(type_, k_cache, n_pages: int, P: int, H: int, D: int, pages, ld_pages: int, q_starts, kv_lens, n_seq: int, T: int,
+                     max_new: int, bounds, stream=None) -> None:
+    """The range of the keys of the pages that hold a step's new tokens (after qmm_cache_write)."""
+    _check("qmm_cache_bounds", lib().qmm_cache_bounds(_t(type_), _ptr(k_cache), n_pages, P, H, D, _ptr(pages), ld_pages, _ptr(q_starts),
+                                                      _ptr(kv_lens), n_seq, T, max_new, _ptr(bounds), _stream(stream)))
+
+
+def cache_select_workspace_size(T: int, H: int, P: int, max_len: int) -> int:
+    return int(lib().qmm_cache_select_workspace_size(T, H, P, max_len))
+
+
+def qmm_cache_select(bounds, n_pages: int, P: int, H: int, D: int, pages, ld_pages: int, q_starts, kv_lens, n_seq: int, dtype, q, ldq: int,
+                     T: int, Hq: int, tree, max_new: int, max_len: int, sinks: int, recent: int, budget: int, chosen, workspace,
+                     workspace_bytes: int, stream=None) -> None:
+    """The numbers of the `budget` pages that each new token and key/value head attends over: chosen [T][H][budget]."""
+    _check("qmm_cache_select",
+           lib().qmm_cache_select(_ptr(bounds), n_pages, P, H, D, _ptr(pages), ld_pages, _ptr(q_starts), _ptr(kv_lens), n_seq, _dt(dtype),
+                                  _ptr(q), ldq, T, Hq, _ptr(tree), max_new, max_len, sinks, recent, budget, _ptr(chosen),
+                                  _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def cache_attend_chosen_workspace_size(T: int, H: int, Hq: int, D: int, P: int, budget: int) -> int:
+    return int(lib().qmm_cache_attend_chosen_workspace_size(T, H, Hq, D, P, budget))
+
+
+def qmm_cache_attend_chosen(type_, k_cache, v_cache, n_pages: int, P: int, H: int, D: int, pages, ld_pages: int, q_starts, kv_lens,
+                            n_seq: int, dtype, q, ldq: int, T: int, Hq: int, tree, scale: float, chosen, budget: int, out, ldo: int, lse,
+                            workspace, workspace_bytes: int, stream=None) -> None:
+    """Attention of each new token over the tokens of its chosen pages; tree, lse and workspace may be None."""
+    _check("qmm_cache_attend_chosen",
+           lib().qmm_cache_attend_chosen(_t(type_), _ptr(k_cache), _ptr(v_cache), n_pages, P, H, D, _ptr(pages), ld_pages, _ptr(q_starts),
+                                         _ptr(kv_lens), n_seq, _dt(dtype), _ptr(q), ldq, T, Hq, _ptr(tree), float(scale), _ptr(chosen),
+                                         budget, _ptr(out), ldo, _ptr(lse), _ptr(workspace), int(workspace_bytes), _stream(stream)))
+
+
+def qmm_norm(x_dtype, x, ldx: int, h_dtype, h, ldh: int, R: int, N: int, w_post, gate, ldg: int, scale: float, w_pre, eps: float, h_out,
+             ldho: int, y_dtype, y, ldy: int, stream=None) -> None:
+    """h_out = h + scale * gate * (rms(x) * w_post), y = rms(h_out) * w_pre; x, w_post, gate and w_pre may be None, and
+    without x h_out may be None."""
+    _check("qmm_norm", lib().qmm_norm(_dt(x_dtype), _ptr(x), ldx, _dt(h_dtype), _ptr(h), ldh, R, N, _ptr(w_post), _ptr(gate), ldg,
+                                      float(scale), _ptr(w_pre), float(eps), _ptr(h_out), ldho, _dt(y_dtype), _ptr(y), ldy,
+                                      _stream(stream)))
+
+
+def qmm_norm_q8(x_dtype, x, ldx: int, h_dtype, h, ldh: int, R: int, N: int, w_post, gate, ldg: int, scale: float, w_pre, eps: float, h_out,
+                ldho: int, a_q, a_d, stream=None) -> None:
+    """qmm_norm with y as the Q8_0 operand (a_q, a_d) of qmm_matmul."""
+    _check("qmm_norm_q8", lib().qmm_norm_q8(_dt(x_dtype), _ptr(x), ldx, _dt(h_dtype), _ptr(h), ldh, R, N, _ptr(w_post), _ptr(gate), ldg,
+                                            float(scale), _ptr(w_pre), float(eps), _ptr(h_out), ldho, _ptr(a_q), _ptr(a_d),
+                                            _stream(stream)))
+
+
+def qmm_norm_mx4(x_dtype, x, ldx: int, h_dtype, h, ldh: int, R: int, N: int, w_post, gate, ldg: int, scale: float, w_pre, eps: float, h_out,
+                 ldho: int, codes, scales, stream=None) -> None:
+    """qmm_norm with y as the MX4 operand (codes, scales) of qmm_mx4_matmul."""
+    _check("qmm_norm_mx4", lib().qmm_norm_mx4(_dt(x_dtype), _ptr(x), ldx, _dt(h_dtype), _ptr(h), ldh, R, N, _ptr(w_post), _ptr(gate),
+                                              ldg, float(scale), _ptr(w_pre), float(eps), _ptr(h_out), ldho, _ptr(codes), _ptr(scales),
+                                              _stream(stream)))
+
+
+def qmm_sample(dtype, logits, ld: int, R: int, V: int, temperature, top_k, top_p, min_p, u, tokens, logp, stream=None) -> None:
+    """One token of each row of logits, from random numbers u; temperature, top_k, top_p, min_p and logp may be None."""
+    _check("qmm_sample", lib().qmm_sample(_dt(dtype), _ptr(logits), ld, R, V, _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p),
+                                          _ptr(u), _ptr(tokens), _ptr(logp), _stream(stream)))

@@ -29,6 +29,9 @@ struct AttendParams {
     void *out;
     float *lse;
     float *part_o, *part_ml;               // [splits][T * Hq][D], [splits][T * Hq][2]
+    const int32_t *chosen;                 // [T][H][list_len]: the pages chosen for each token and head (attend_chosen.cu)
+    int list_len;
+    uint32_t chunk;                        // keys of such a list in a split
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -110,7 +113,27 @@ __device__ __forceinline__ int splits_of(int64_t n, uint32_t chunk) { return (in
 struct Rows {                              // what a CTA works on
     int64_t s, q0, nq, n, first, k0, k1;
     int h, r0, rows, sp, used;
+    // of a list of chosen pages: the list, and the places that its token sees: all below `upto`, but with tree words of those
+    // from `first` on the ones whose bit is set
+    const int32_t *list;
+    int64_t upto;
+    uint64_t word;
+    bool tree;
 };
+
+// Which of the places at .. at + 15 the token of a list sees, as bits.
+__device__ __forceinline__ uint32_t seen16(const Rows &w, int64_t at) {
+    if (at < 0 || at >= w.upto) return 0u;
+    uint32_t m = w.upto - at >= 16 ? 0xffffu : (1u << (int)(w.upto - at)) - 1u;
+    if (w.tree && at + 16 > w.first) {
+        // bit k: place at + k is new token b + k of the sequence
+        const int64_t b = at - w.first;
+        if (b >= 64) m = 0u;
+        else if (b >= 0) m &= (uint32_t)(w.word >> b);
+        else m &= (uint32_t)(w.word << -b) | ((1u << (int)-b) - 1u);
+    }
+    return m;
+}
 
 // The CTA's rows and keys, from its index: row tiles fastest, then heads, then sequences (longest first) or, where
 // they are split, all whole splits and then the rest of each sequence.  False: it has none.  `scratch`: kSorted + 1 ints of shared
@@ -275,7 +298,7 @@ __device__ __forceinline__ float cache_value(const uint8_t *chunk, int P, int D,
 
 // The CTA's rows and keys once more, a warp a row, skipping what the row does not see; rows whose result
 // is finite, and was, keep the one they have.
-template <int TYPE, int DB, int WARPS>
+template <int TYPE, int DB, int WARPS, bool CHOSEN = false>
 __device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &w, const int *row_bad) {
     const int lane = threadIdx.x & 31;
     constexpr int D = DB * 32;
@@ -289,9 +312,16 @@ __device__ __noinline__ void rows_one_by_one(const AttendParams &p, const Rows &
         }
         float top = -INFINITY, sum = 0.0f;                      // in powers of two
         for (int64_t j = w.k0; j < w.k1; ++j) {
-            if (j >= w.first && !sees(p.tree, w.q0 + i, i, j - w.first)) continue;
-            if (!QMM_DCHECK((j >> p.log_p) < p.ld_pages && w.s < p.n_seq)) continue;
-            const int64_t page = p.pages[w.s * p.ld_pages + (j >> p.log_p)];
+            int64_t number = j >> p.log_p;
+            if constexpr (CHOSEN) {
+                if (!QMM_DCHECK(number < p.list_len)) continue;
+                number = w.list[number];
+                if (!((seen16(w, (number << p.log_p) + (j & (p.P - 16))) >> (j & 15)) & 1)) continue;
+            } else {
+                if (j >= w.first && !sees(p.tree, w.q0 + i, i, j - w.first)) continue;
+            }
+            if (!QMM_DCHECK(number < p.ld_pages && w.s < p.n_seq)) continue;
+            const int64_t page = p.pages[w.s * p.ld_pages + number];
             if (page < 0 || page >= p.n_pages) continue;
             const int64_t at = cache_chunk(TYPE, p.H, D, p.P, page, w.h);
             const int off = (int)(j & (p.P - 1));

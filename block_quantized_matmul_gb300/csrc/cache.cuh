@@ -19,4 +19,21 @@ __host__ __device__ __forceinline__ int64_t cache_chunk(int type, int H, int D, 
     return (page * H + h) * ((int64_t)P * cache_token_bytes(type, D));
 }
 
+// The last i of 0 .. n with starts[i] <= row (starts ascending), -1 if there is none.  By one warp, 32 probes at a time.
+__device__ __forceinline__ int64_t last_start(const int32_t *starts, int64_t n, int64_t row) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, left = n + 1;
+    while (true) {
+        const int64_t step = (left + 31) / 32, at = lane * step;
+        const int upto = __popc(__ballot_sync(0xffffffffu, at < left && starts[lo + at] <= row));
+        if (upto == 0) return -1;                                      // (the first probe of later rounds is <= row)
+        lo += (upto - 1) * step;
+        if (step == 1) return lo;
+        left = min(step, left - (upto - 1) * step);
+    }
+}
+
+// Bytes of the bounds of a page's head: [2][D] int8 codes, [D/32] fp16 scales, zeros up to 16 bytes.
+__host__ __device__ __forceinline__ int cache_bound_bytes(int D) { return (2 * D + D / 32 * 2 + 15) / 16 * 16; }
+
 }  // namespace qmm

@@ -1,0 +1,176 @@
+// cache_plan.cu -- the plan of a step over the paged cache: from each request's cached length and new tokens the
+// pages it is given, the first row of each sequence, and the slot of every row.
+//
+// For sequence s with n cached tokens, m new ones and held(n) = ceil(n / P):
+//   need = held(n + m) - held(n),   line = sum of need up to and including s (of those that fit their rows of the table),
+//   it is run when it fits, and need = 0 or line <= free.
+// Sums of need never fall, so once one waits for want of pages all later ones that need a page wait too: the pages of
+// those that run are the ring's entries first + line - need ...
+//
+// One cluster of CTAs does it all: each CTA runs the same scan over the sequences (a tile of as many as it has threads at a
+// time) and takes every C-th part of the rows that fall into them, so that no sum has to travel between CTAs; the cluster's
+// barrier, between the last read of a tile of lengths and the first write of its results, lets the new
+// lengths replace the old.  What bounds it is latency: the loads of the lengths, three scans in one, a row's search
+// for its sequence (8 or 10 steps in shared memory), and a load of the page.
+#include <climits>
+
+#include "qmm_internal.cuh"
+
+namespace qmm {
+namespace {
+
+struct PlanParams {
+    const int32_t *lens, *news;
+    int64_t n_seq, ld_pages, n_ring, T;
+    int log_p;
+    int32_t *pages, *ring;
+    const int64_t *ring_at;
+    int32_t *q_starts, *kv_lens;
+    int64_t *slots;
+    int32_t *positions, *next_lens;
+    int64_t *next_at;
+};
+
+struct Sums {
+    int64_t rows, need, back;               // new tokens, pages wanted, pages given back
+};
+__device__ __forceinline__ Sums operator+(const Sums &a, const Sums &b) { return {a.rows + b.rows, a.need + b.need, a.back + b.back}; }
+
+// Inclusive sums over the first `width` lanes of a warp.
+__device__ __forceinline__ Sums warp_sums(Sums x, int width) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        if (m >= width) break;
+        const Sums y = {__shfl_up_sync(0xffffffffu, x.rows, m), __shfl_up_sync(0xffffffffu, x.need, m), __shfl_up_sync(0xffffffffu, x.back, m)};
+        if (lane >= m) x = x + y;
+    }
+    return x;
+}
+
+// Place number `at` of a ring of n, for at >= 0.
+__device__ __forceinline__ int64_t around(int64_t at, int64_t n) { return at < n ? at : at % n; }
+
+constexpr int kWaits = -1, kDone = -2;      // in place of the pages that a sequence holds
+
+template <int THREADS>
+__global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p) {
+    constexpr int kWarps = THREADS / 32;
+    __shared__ Sums part[kWarps];
+    __shared__ int64_t s_start[THREADS], s_base[THREADS];             // first row; first new page, or first page given back, in the ring
+    __shared__ int s_len[THREADS], s_held[THREADS];
+    __shared__ unsigned long long s_taken;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ctas = (int)gridDim.x, cta = (int)blockIdx.x;
+    if (threadIdx.x == 0) s_taken = 0;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int P = 1 << p.log_p;
+    const int64_t first = p.ring_at[0], last = p.ring_at[1], free = last - first, room = min(p.ld_pages << p.log_p, (int64_t)INT_MAX);
+    const int64_t front = ((first % p.n_ring) + p.n_ring) % p.n_ring, behind = ((last % p.n_ring) + p.n_ring) % p.n_ring;
+    Sums done = {0, 0, 0};
+    for (int64_t base = 0; base < p.n_seq; base += THREADS) {
+        const int64_t s = base + threadIdx.x;
+        const bool have = s < p.n_seq;
+        const int64_t len = have ? max((int64_t)0, min((int64_t)p.lens[s], room)) : 0, news = have ? p.news[s] : 0;
+        const int64_t held = (len + P - 1) >> p.log_p, rows = max(news, (int64_t)0);
+        bool run = news >= 0 && len + rows <= room;
+        const Sums v = {rows, run ? ((len + rows + P - 1) >> p.log_p) - held : 0, news < 0 ? held : 0};
+        // ---- sums of all before: over the warp, over the warps, over the tiles ----
+        Sums x = warp_sums(v, 32);
+        if (lane == 31) part[warp] = x;
+        __syncthreads();
+        if (warp == 0) {
+            const Sums w = warp_sums(lane < kWarps ? part[lane] : Sums{0, 0, 0}, kWarps);
+            if (lane < kWarps) part[lane] = w;
+        }
+        __syncthreads();
+        const Sums all = part[kWarps - 1], before = warp ? part[warp - 1] : Sums{0, 0, 0};
+        x = {done.rows + before.rows + x.rows - v.rows, done.need + before.need + x.need - v.need, done.back + before.back + x.back - v.back};
+        run = run && x.rows + rows <= p.T && (v.need == 0 || x.need + v.need <= free);
+        const unsigned takes = __ballot_sync(0xffffffffu, run && v.need > 0);
+        if (takes && lane == 31 - __clz(takes)) atomicMax(&s_taken, (unsigned long long)(x.need + v.need));
+        s_start[threadIdx.x] = x.rows;
+        s_len[threadIdx.x] = (int)len;
+        s_held[threadIdx.x] = news < 0 ? kDone : (run ? (int)held : kWaits);
+        s_base[threadIdx.x] = news < 0 ? around(behind + x.back, p.n_ring) : around(front + x.need, p.n_ring);
+        __syncthreads();
+        // everybody has read the tile's lengths and, before the first results, the ring's counters
+        if (ctas > 1) {
+            asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+        }
+        if (have && cta == (int)((base / THREADS) % ctas)) {
+            p.q_starts[s] = (int32_t)min(x.rows, (int64_t)INT_MAX);
+            p.kv_lens[s] = run ? (int32_t)(len + rows) : 0;
+            if (p.next_lens) p.next_lens[s] = news < 0 ? 0 : (int32_t)(run ? len + rows : len);
+        }
+        // ---- pages that go back: a warp a sequence ----
+        for (int i = warp * ctas + cta; i < THREADS; i += kWarps * ctas) {
+            if (s_held[i] != kDone) continue;
+            const int n = (s_len[i] + P - 1) >> p.log_p;
+            for (int k = lane; k < n; k += 32) {
+                const int64_t to = around(s_base[i] + k, p.n_ring);
+                if (QMM_DCHECK(to >= 0 && to < p.n_ring && k < p.ld_pages && base + i < p.n_seq)) p.ring[to] = p.pages[(base + i) * p.ld_pages + k];
+            }
+        }
+        // ---- the rows that fall into this tile ----
+        const int64_t r1 = min(done.rows + all.rows, p.T);
+        for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < r1; r += (int64_t)ctas * THREADS) {
+            int lo = 0, hi = THREADS;                                  // the last sequence that starts at or before the row
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (s_start[mid] <= r) lo = mid;
+                else hi = mid;
+            }
+            int64_t slot = -1;
+            int pos = -1;
+            if (s_held[lo] >= 0) {
+                pos = s_len[lo] + (int)(r - s_start[lo]);
+                const int number = pos >> p.log_p, k = number - s_held[lo], place = pos & (P - 1);
+                int64_t page = -1;
+                if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) {
+                    int32_t *entry = p.pages + (base + lo) * p.ld_pages + number;
+                    if (k >= 0) {
+                        page = p.ring[around(s_base[lo] + k, p.n_ring)];
+                        if (place == 0) *entry = (int32_t)page;
+                    } else {
+                        page = *entry;
+                    }
+                }
+                slot = page * P + place;
+            }
+            p.slots[r] = slot;
+            if (p.positions) p.positions[r] = pos;
+        }
+        done = done + all;
+        __syncthreads();                                              // the tile's arrays are free again
+    }
+    for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < p.T; r += (int64_t)ctas * THREADS) {
+        p.slots[r] = -1;
+        if (p.positions) p.positions[r] = -1;
+    }
+    if (cta == 0 && threadIdx.x == 0) {
+        p.q_starts[p.n_seq] = (int32_t)min(done.rows, (int64_t)INT_MAX);
+        if (p.next_at) {
+            p.next_at[0] = first + (int64_t)s_taken;
+            p.next_at[1] = last + done.back;
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_plan(const int32_t *lens, const int32_t *news, int64_t n_seq, int P, int32_t *pages, int64_t ld_pages,
+                              int32_t *ring, int64_t n_ring, const int64_t *ring_at, int64_t T, int32_t *q_starts, int32_t *kv_lens,
+                              int64_t *slots, int32_t *positions, int32_t *next_lens, int64_t *next_at, cudaStream_t s) {
+    PlanParams p = {lens, news, n_seq, ld_pages, n_ring, T, 0, pages, ring, ring_at, q_starts, kv_lens, slots, positions, next_lens, next_at};
+    while ((1 << p.log_p) < P) ++p.log_p;
+    if (n_seq <= 256 && T <= 1024) return launch_pdl(cache_plan_kernel<256>, dim3(1), 256, 0, s, p);
+    unsigned ctas = 1;
+    while (ctas < 8 && (int64_t)ctas * 2048 < T) ctas *= 2;
+    return launch_pdl_cluster(cache_plan_kernel<1024>, dim3(ctas), ctas, 1024, 0, s, p);
+}
+
+QMM_DCHECK_READER(read_dcheck_cache_plan)
+
+}  // namespace qmm

@@ -1,0 +1,422 @@
+// cache_select.cu -- which pages of the block-quantized cache (cache.cuh) a new token attends over.
+//
+// Bounds.  For a page, a head and an element e: lo = min_j k[j, e], hi = max_j k[j, e] over the page's tokens, in codes of 8
+// bits with one scale a block of 32 for both, rounded outwards: d = up16(max(|lo|, |hi|) / 127), floor(lo / d), ceil(hi / d).
+// Minima and maxima do not depend on an order, so a page's bounds are a function of its keys alone.
+//
+// Score.  sum_e q_e k_e <= sum_e (q_e > 0 ? q_e hi_e : q_e lo_e) for every key of the page.  The query row is quantized by the
+// activations' rule, so the sum over a block of 32 is a whole number S below 2^20, exact in any order, and
+//   score = sum_b (dq_b d_b) S_b  takes three fp32 roundings a block in the order of the blocks: every way of computing it
+// gives the same bits, and so the same choice of pages.
+#include <climits>
+
+#include "cache.cuh"
+#include "elem.cuh"
+#include "tc_common.cuh"
+
+namespace qmm {
+namespace {
+
+// ---------------------------------------------------------------------------------------------
+// Bounds
+// ---------------------------------------------------------------------------------------------
+struct BoundsParams {
+    const uint8_t *k_cache;
+    int64_t n_pages, ld_pages, n_seq, T, max_new;
+    int H, log_p, per_seq;                  // pages of a sequence that may hold new tokens
+    const int32_t *pages, *q_starts, *kv_lens;
+    uint8_t *bounds;
+};
+
+__device__ __forceinline__ uint32_t pack4(const int (&q)[4]) {
+    return (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 | (uint32_t)q[3] << 24;
+}
+
+constexpr int kBoundWarps = 4;
+
+// A warp takes a page of a head.  Lanes: PK pieces of 16 bytes of codes make a token (Q8_0: half a block each,
+// Q4_0: a block), 32 / PK tokens at a time; what the lanes of a piece have found is joined at the end.
+template <int TYPE, int DB>
+__global__ void __launch_bounds__(kBoundWarps * 32) cache_bounds_kernel(const BoundsParams p) {
+    constexpr int CB = DB * (TYPE == QMM_Q8_0 ? 32 : 16), PK = CB / 16, TOK = 32 / PK, E = TYPE == QMM_Q8_0 ? 16 : 32, D = DB * 32;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int lane = threadIdx.x & 31, P = 1 << p.log_p;
+    int64_t unit = (int64_t)blockIdx.x * kBoundWarps + (threadIdx.x >> 5);
+    const int h = (int)(unit % p.H);
+    unit /= p.H;
+    const int64_t s = unit / p.per_seq;
+    if (s >= p.n_seq) return;
+    const int64_t q0 = p.q_starts[s], q1 = p.q_starts[s + 1], n = max((int64_t)0, min((int64_t)p.kv_lens[s], p.ld_pages << p.log_p));
+    if (q0 < 0 || q1 > p.T || q1 <= q0 || n == 0) return;
+    const int64_t from = max((int64_t)0, (int64_t)p.kv_lens[s] - min(q1 - q0, p.max_new)) >> p.log_p, number = from + unit % p.per_seq;
+    if (number > (n - 1) >> p.log_p || !QMM_DCHECK(number < p.ld_pages)) return;
+    const int64_t page = p.pages[s * p.ld_pages + number];
+    if (page < 0 || page >= p.n_pages) return;
+    const int have = (int)min((int64_t)P, n - (number << p.log_p));
+    const uint8_t *chunk = p.k_cache + cache_chunk(TYPE, p.H, D, P, page, h);
+    const uint16_t *scales = reinterpret_cast<const uint16_t *>(chunk + (int64_t)P * CB);
+    const int piece = lane % PK, block = TYPE == QMM_Q8_0 ? piece / 2 : piece;
+    float lo[E], hi[E];
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+        lo[i] = INFINITY;
+        hi[i] = -INFINITY;
+    }
+    for (int j = lane / PK; lane < TOK * PK && j < have; j += TOK) {
+        const uint4 c = *reinterpret_cast<const uint4 *>(chunk + (int64_t)j * CB + piece * 16);
+        const float d = __half2float(__ushort_as_half(scales[j * DB + block]));
+        odd |= !(fabsf(d) < INFINITY);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if constexpr (TYPE == QMM_Q8_0) {
+                    const float v = d * (float)(int8_t)(w[i] >> (8 * k));
+                    lo[4 * i + k] = fminf(lo[4 * i + k], v);
+                    hi[4 * i + k] = fmaxf(hi[4 * i + k], v);
+                } else {
+                    const float v = d * (float)((int)((w[i] >> (8 * k)) & 15u) - 8), u = d * (float)((int)((w[i] >> (8 * k + 4)) & 15u) - 8);
+                    lo[4 * i + k] = fminf(lo[4 * i + k], v);
+                    hi[4 * i + k] = fmaxf(hi[4 * i + k], v);
+                    lo[16 + 4 * i + k] = fminf(lo[16 + 4 * i + k], u);
+                    hi[16 + 4 * i + k] = fmaxf(hi[16 + 4 * i + k], u);
+                }
+            }
+    }
+    // ---- the lanes of a piece ----
+    for (int m = 1; m < TOK; ++m) {
+        const int src = (lane + m * PK) & 31;
+        const bool other = lane < PK;
+        odd |= __shfl_sync(0xffffffffu, (int)odd, src) && other;
+#pragma unroll
+        for (int i = 0; i < E; ++i) {
+            const float a = __shfl_sync(0xffffffffu, lo[i], src), b = __shfl_sync(0xffffffffu, hi[i], src);
+            if (other) {
+                lo[i] = fminf(lo[i], a);
+                hi[i] = fmaxf(hi[i], b);
+            }
+        }
+    }
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+    if constexpr (TYPE == QMM_Q8_0) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        odd |= __shfl_xor_sync(0xffffffffu, (int)odd, 1) != 0;
+    }
+    if (lane >= PK) return;
+    const __half half = odd ? __ushort_as_half(0x7E00u) : __float2half_ru(__fdiv_rn(top, 127.0f));
+    const float d = odd ? 0.0f : __half2float(half);
+    uint8_t *out = p.bounds + (page * p.H + h) * cache_bound_bytes(D);
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+        uint32_t w[E / 4];
+#pragma unroll
+        for (int i = 0; i < E / 4; ++i) {
+            int q[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const float v = d > 0.0f ? __fdiv_rn(x ? hi[4 * i + k] : lo[4 * i + k], d) : 0.0f;
+                q[k] = (int)fminf(fmaxf(x ? ceilf(v) : floorf(v), -127.0f), 127.0f);
+            }
+            w[i] = pack4(q);
+        }
+#pragma unroll
+        for (int i = 0; i < E / 16; ++i)
+            *reinterpret_cast<uint4 *>(out + x * D + piece * E + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    }
+    if (TYPE == QMM_Q4_0 || (piece & 1) == 0) reinterpret_cast<__half *>(out + 2 * D)[block] = half;
+    if (lane == 0)
+        for (int i = D + DB; i < cache_bound_bytes(D) / 2; ++i) reinterpret_cast<uint16_t *>(out)[i] = 0;
+}
+
+// ---------------------------------------------------------------------------------------------
+// Scores
+// ---------------------------------------------------------------------------------------------
+struct Token {                              // a new token, and the pages in question for it
+    int64_t s, seen;                        // its sequence; number of pages (0: none)
+    int64_t old;                            // the first of the last ones that are always chosen
+};
+
+// The token of a row of q; false: the row is no sequence's, or past max_new.  By a whole warp.
+__device__ __forceinline__ bool find_token(const SelectParams &p, int64_t row, Token &t) {
+    t.s = last_start(p.q_starts, p.n_seq, row);
+    if (t.s < 0 || t.s >= p.n_seq) return false;
+    const int64_t q0 = p.q_starts[t.s], q1 = p.q_starts[t.s + 1], len = p.kv_lens[t.s], nq = q1 - q0, i = row - q0;
+    if (q0 < 0 || q1 > p.T || i >= p.max_new) return false;
+    const int64_t n = min(len, p.ld_pages << p.log_p), first = len - nq;
+    // the last place that the token sees, and the place from which the last pages are counted
+    const int64_t end = p.tree ? n - 1 : min(first + i, n - 1), from = p.tree ? first : first + i;
+    t.seen = end < 0 || (len + ((int64_t)1 << p.log_p) - 1) >> p.log_p > p.most ? 0 : (end >> p.log_p) + 1;
+    t.old = (from < 0 ? 0 : from >> p.log_p) - (p.recent - 1);
+    return true;
+}
+
+constexpr int kScoreThreads = 128, kTokTile = 8;
+
+// A thread takes a page, whose codes stay in its registers, for up to kTokTile tokens (neighbouring rows of q; rows of another
+// sequence load their own page) and all query rows of a head, whose codes (positive and negative ones apart) it reads from
+// shared memory, the same for all threads.
+template <int DB>
+__global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const SelectParams p) {
+    constexpr int D = DB * 32, BB = (2 * D + 2 * DB + 15) / 16 * 16;
+    extern __shared__ __align__(16) uint8_t smem[];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int h = (int)(blockIdx.y % (unsigned)p.H);
+    const int64_t row0 = (int64_t)blockIdx.x * p.tok_tile, page0 = (int64_t)(blockIdx.y / (unsigned)p.H) * kScoreThreads;
+    const int toks = (int)min((int64_t)p.tok_tile, p.T - row0);
+    Token tok[kTokTile];
+    bool any = false;
+#pragma unroll
+    for (int k = 0; k < kTokTile; ++k) {
+        tok[k].seen = 0;
+        // where all pages are chosen, nobody asks for scores
+        if (k < toks && find_token(p, row0 + k, tok[k]) && tok[k].seen > p.budget) any |= tok[k].seen > page0;
+        else tok[k].seen = 0;
+    }
+    if (!any) return;
+    // ---- the tile's query rows, a warp a row ----
+    const int lane = threadIdx.x & 31, rows = toks * p.group;
+    uint8_t *codes = smem;                                             // [row][2][D]: negative, positive
+    float *dq = reinterpret_cast<float *>(smem + p.tok_tile * p.group * 2 * D);   // [row][DB]
+    for (int r = threadIdx.x >> 5; r < rows; r += kScoreThreads / 32) {
+        const int64_t src = (row0 + r / p.group) * p.ldq + (int64_t)(h * p.group + r % p.group) * D + lane;
+#pragma unroll
+        for (int b = 0; b < DB; ++b) {
+            const float x = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q)[src + 32 * b])
+                                   : __half2float(static_cast<const __half *>(p.q)[src + 32 * b]);
+            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7FFFFFFFu);
+            const bool fine = top < 0x7F800000u;
+            const float d = fine ? q8_scale(__uint_as_float(top)) : 0.0f;
+            const int a = fine ? q8_code(x, inv_or_zero(d)) : 0;
+            codes[r * 2 * D + 32 * b + lane] = (uint8_t)(int8_t)min(a, 0);
+            codes[r * 2 * D + D + 32 * b + lane] = (uint8_t)max(a, 0);
+            if (lane == 0) dq[r * DB + b] = fine ? d : NAN;
+        }
+    }
+    __syncthreads();
+    const int64_t number = page0 + threadIdx.x;
+    uint4 c[DB * 4];                                                   // lowest: 2 a block, then highest
+    float d[DB];
+    int64_t loaded = -1;
+    bool there = false;
+#pragma unroll
+    for (int k = 0; k < kTokTile; ++k) {
+        if (number >= tok[k].seen || !QMM_DCHECK(number < p.ld_pages && number < p.most)) continue;
+        if (tok[k].s != loaded) {
+            loaded = tok[k].s;
+            const int64_t page = p.pages[loaded * p.ld_pages + number];
+            there = page >= 0 && page < p.n_pages;
+            if (there) {
+                const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (page * p.H + h) * BB);
+#pragma unroll
+                for (int i = 0; i < DB * 4; ++i) c[i] = src[i];
+                const __half *ds = reinterpret_cast<const __half *>(src + DB * 4);
+#pragma unroll
+                for (int b = 0; b < DB; ++b) d[b] = __half2float(ds[b]);
+            }
+        }
+        float best = -INFINITY;
+        for (int g = 0; g < p.group && there; ++g) {
+            const int r = k * p.group + g;
+            const uint4 *a = reinterpret_cast<const uint4 *>(codes + r * 2 * D);
+            float score = 0.0f;
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                int x = 0, y = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const uint4 m = a[2 * b + i], q = a[DB * 2 + 2 * b + i], lo = c[2 * b + i], hi = c[DB * 2 + 2 * b + i];
+                    x = __dp4a((int)m.x, (int)lo.x, x);
+                    x = __dp4a((int)m.y, (int)lo.y, x);
+                    x = __dp4a((int)m.z, (int)lo.z, x);
+                    x = __dp4a((int)m.w, (int)lo.w, x);
+                    y = __dp4a((int)q.x, (int)hi.x, y);
+                    y = __dp4a((int)q.y, (int)hi.y, y);
+                    y = __dp4a((int)q.z, (int)hi.z, y);
+                    y = __dp4a((int)q.w, (int)hi.w, y);
+                }
+                score = __fadd_rn(score, __fmul_rn(__fmul_rn(dq[r * DB + b], d[b]), (float)(x + y)));
+            }
+            best = isnan(score) ? INFINITY : fmaxf(best, score);
+        }
+        p.scores[((row0 + k) * p.H + h) * p.most + number] = best;
+    }
+}
+
+// ---------------------------------------------------------------------------------------------
+// The choice
+// ---------------------------------------------------------------------------------------------
+constexpr int kChooseThreads = 256;
+
+// fp32 as an unsigned number of the same order (-0 does not occur: sums that begin at +0 do not end there).
+__device__ __forceinline__ uint32_t ordered(float v) {
+    const uint32_t b = __float_as_uint(v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
+// Sums of v over the threads before this one, and over all.
+__device__ __forceinline__ uint32_t sums_before(uint32_t v, uint32_t *part, uint32_t &all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t x = v;
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, m);
+        if (lane >= m) x += y;
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    uint32_t before = 0;
+    all = 0;
+#pragma unroll
+    for (int w = 0; w < kChooseThreads / 32; ++w) {
+        const uint32_t y = part[w];
+        if (w < warp) before += y;
+        all += y;
+    }
+    __syncthreads();
+    return before + x - v;
+}
+
+// A CTA takes a token and head: the rank-th largest score by four histograms of 8 bits each, then the pages above it, and
+// as many of those at it as are still wanted, the earliest first, in the order of their numbers.
+__global__ void __launch_bounds__(kChooseThreads) cache_choose_kernel(const SelectParams p) {
+    __shared__ uint32_t hist[256], part[kChooseThreads / 32], s_prefix, s_rank;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t row = blockIdx.x / (unsigned)p.H;
+    const int h = (int)(blockIdx.x % (unsigned)p.H);
+    Token t;
+    if (!find_token(p, row, t)) return;
+    int32_t *out = p.chosen + (row * p.H + h) * p.budget;
+    const int seen = (int)t.seen, budget = (int)p.budget;
+    if (seen <= budget) {
+        for (int i = threadIdx.x; i < budget; i += kChooseThreads) out[i] = i < seen ? i : -1;
+        return;
+    }
+    const int front = (int)min(p.sinks, t.seen), back = max(front, (int)max((int64_t)0, min(t.old, t.seen)));   // always chosen: below front, from back on
+    const int always = front + seen - back;
+    uint32_t rank = (uint32_t)max(0, budget - always);                 // of the pages front .. back - 1
+    const float *scores = p.scores + (row * p.H + h) * p.most;
+    uint32_t prefix = 0, mask = 0;
+    if (rank > 0) {
+        for (int shift = 24; shift >= 0; shift -= 8) {
+            hist[threadIdx.x] = 0;
+            __syncthreads();
+            for (int i = front + threadIdx.x; i < back; i += kChooseThreads) {
+                const uint32_t key = ordered(scores[i]);
+                if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+            }
+            __syncthreads();
+            // thread i has the bin 255 - i, so that sums before it are of larger keys
+            uint32_t all;
+            const uint32_t mine = hist[255 - threadIdx.x], before = sums_before(mine, part, all);
+            if (before < rank && before + mine >= rank) {
+                s_prefix = prefix | (uint32_t)(255 - threadIdx.x) << shift;
+                s_rank = rank - before;
+            }
+            __syncthreads();
+            prefix = s_prefix;
+            rank = s_rank;
+            mask |= 255u << shift;
+        }
+    }
+    // ---- the chosen pages, ascending ----
+    const bool some = budget > always;
+    int at = 0;
+    uint32_t ties = 0;                                                 // pages at the border so far
+    for (int base = 0; base < seen; base += kChooseThreads) {
+        const int i = base + threadIdx.x;
+        bool above = false, tie = false;
+        if (i < seen) {
+            if (i < front || i >= back) {
+                above = true;
+            } else if (some) {
+                const uint32_t key = ordered(scores[i]);
+                above = key > prefix;
+                tie = key == prefix;
+            }
+        }
+        uint32_t all, n_ties;
+        const uint32_t tie_at = ties + sums_before(tie ? 1u : 0u, part, n_ties);
+        const bool in = above || (tie && tie_at < rank);
+        const uint32_t place = sums_before(in ? 1u : 0u, part, all);
+        if (in && at + (int)place < budget) out[at + place] = i;
+        at += (int)all;
+        ties += n_ties;
+    }
+    for (int i = min(at, budget) + threadIdx.x; i < budget; i += kChooseThreads) out[i] = -1;
+}
+
+template <int DB>
+cudaError_t launch_score(const SelectParams &p, cudaStream_t s) {
+    const size_t smem = (size_t)p.tok_tile * p.group * (2 * DB * 32 + DB * 4);    // up to 64 rows: 35 KB
+    const int64_t x = (p.T + p.tok_tile - 1) / p.tok_tile, y = (p.most + kScoreThreads - 1) / kScoreThreads * p.H;
+    if (x > 0x7fffffff || y > 65535) return cudaErrorInvalidValue;
+    return launch_pdl(cache_score_kernel<DB>, dim3((unsigned)x, (unsigned)y), kScoreThreads, smem, s, p);
+}
+
+template <int TYPE, int DB>
+cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s) {
+    const int64_t units = p.n_seq * p.per_seq * p.H, grid = (units + kBoundWarps - 1) / kBoundWarps;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    return launch_pdl(cache_bounds_kernel<TYPE, DB>, dim3((unsigned)grid), kBoundWarps * 32, 0, s, p);
+}
+
+template <int TYPE>
+cudaError_t launch_bounds_d(const BoundsParams &p, int D, cudaStream_t s) {
+    switch (D / 32) {
+        case 1: return launch_bounds<TYPE, 1>(p, s);
+        case 2: return launch_bounds<TYPE, 2>(p, s);
+        case 3: return launch_bounds<TYPE, 3>(p, s);
+        case 4: return launch_bounds<TYPE, 4>(p, s);
+        case 5: return launch_bounds<TYPE, 5>(p, s);
+        case 6: return launch_bounds<TYPE, 6>(p, s);
+        case 7: return launch_bounds<TYPE, 7>(p, s);
+        default: return launch_bounds<TYPE, 8>(p, s);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_cache_bounds(qmm_type type, const uint8_t *k_cache, int64_t n_pages, int P, int H, int D, const int32_t *pages,
+                                int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens, int64_t n_seq, int64_t T,
+                                int64_t max_new, uint8_t *bounds, cudaStream_t s) {
+    BoundsParams p = {k_cache, n_pages, ld_pages, n_seq, T, max_new < T ? max_new : T, H, 0, 0, pages, q_starts, kv_lens, bounds};
+    while ((1 << p.log_p) < P) ++p.log_p;
+    const int64_t per_seq = (p.max_new + P - 2) / P + 1;               // max_new neighbours lie in so many pages at most
+    if (per_seq > 0x7fffffff) return cudaErrorInvalidValue;
+    p.per_seq = (int)per_seq;
+    return type == QMM_Q8_0 ? launch_bounds_d<QMM_Q8_0>(p, D, s) : launch_bounds_d<QMM_Q4_0>(p, D, s);
+}
+
+cudaError_t launch_cache_select(const SelectParams &from, int D, cudaStream_t s) {
+    SelectParams p = from;
+    if (p.T * p.H > 0x7fffffff) return cudaErrorInvalidValue;
+    // rows of one sequence share a page's codes; a single token's CTA is done the sooner without company
+    p.tok_tile = p.max_new == 1 ? 1 : kTokTile;
+    while (p.tok_tile > 1 && p.tok_tile * p.group > 64) p.tok_tile /= 2;
+    cudaError_t e = cudaSuccess;
+    if (p.most > p.budget) {
+        switch (D / 32) {
+            case 1: e = launch_score<1>(p, s); break;
+            case 2: e = launch_score<2>(p, s); break;
+            case 3: e = launch_score<3>(p, s); break;
+            case 4: e = launch_score<4>(p, s); break;
+            case 5: e = launch_score<5>(p, s); break;
+            case 6: e = launch_score<6>(p, s); break;
+            case 7: e = launch_score<7>(p, s); break;
+            default: e = launch_score<8>(p, s); break;
+        }
+    }
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_choose_kernel, dim3((unsigned)(p.T * p.H)), kChooseThreads, 0, s, p);
+}
+
+QMM_DCHECK_READER(read_dcheck_cache_select)
+
+}  // namespace qmm

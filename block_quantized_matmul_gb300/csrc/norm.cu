@@ -1,0 +1,242 @@
+// norm.cu -- the norm behind a block, its gate and residual, and the norm before the next block, in one pass:
+//   b = w_post ? x / sqrt(mean(x^2) + eps) * w_post : x,   h' = round(h + scale * gate * b),
+//   y = h' / sqrt(mean(h'^2) + eps) * w_pre,
+// with y as rows, as Q8_0 blocks or as MX4 blocks.
+//
+// A row stays in registers from its load to its last store, so x, h and gate are read once and h' and y written
+// once; each thread holds C pieces of 8 consecutive elements, so that four neighbouring threads hold a block of 32.  Rows of up
+// to 1024 elements take a warp each, longer ones a CTA.  Element types are parameters of the launch, not of
+// the kernel: the branches are uniform, and the kernel is bound by memory.
+#include "qmm_internal.cuh"
+
+#include "elem.cuh"
+#include "mx4.cuh"
+
+namespace qmm {
+namespace {
+
+// Elements at .. at + 7 of a row of n; VEC: aligned, and all there.
+template <bool VEC>
+__device__ __forceinline__ void load8(float (&v)[8], const void *row, int type, int at, int n) {
+    if constexpr (VEC) {
+        if (type == QMM_F32) {
+            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + at);
+            const float4 a = q[0], b = q[1];
+            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        } else {
+            const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + at);
+            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = type == QMM_F16 ? unpack2(w[i], __half{}) : unpack2(w[i], __nv_bfloat16{});
+                v[2 * i] = f.x;
+                v[2 * i + 1] = f.y;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            v[i] = 0.0f;
+            if (at + i >= n) continue;
+            if (type == QMM_F32) v[i] = static_cast<const float *>(row)[at + i];
+            else if (type == QMM_F16) v[i] = __half2float(static_cast<const __half *>(row)[at + i]);
+            else v[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[at + i]);
+        }
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(const float (&v)[8], void *row, int type, int at, int n) {
+    if constexpr (VEC) {
+        if (type == QMM_F32) {
+            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(row) + at);
+            q[0] = make_float4(v[0], v[1], v[2], v[3]);
+            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+        } else {
+            uint32_t w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = type == QMM_F16 ? pack2(v[2 * i], v[2 * i + 1], __half{}) : pack2(v[2 * i], v[2 * i + 1], __nv_bfloat16{});
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            if (at + i >= n) continue;
+            if (type == QMM_F32) static_cast<float *>(row)[at + i] = v[i];
+            else if (type == QMM_F16) static_cast<__half *>(row)[at + i] = __float2half_rn(v[i]);
+            else static_cast<__nv_bfloat16 *>(row)[at + i] = __float2bfloat16_rn(v[i]);
+        }
+    }
+}
+
+__device__ __forceinline__ float rounded(float v, int type) {
+    return type == QMM_F32 ? v : (type == QMM_F16 ? __half2float(__float2half_rn(v)) : __bfloat162float(__float2bfloat16_rn(v)));
+}
+__device__ __forceinline__ const void *row_of(const void *p, int type, int64_t at) {
+    return static_cast<const uint8_t *>(p) + at * (type == QMM_F32 ? 4 : 2);
+}
+
+// The sum over the threads of a row.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float v, float *part) {
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+    if constexpr (TPR > 32) {
+        constexpr int kWarps = TPR / 32;
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) part[threadIdx.x >> 5] = v;
+        __syncthreads();
+        v = lane < kWarps ? part[lane] : 0.0f;
+#pragma unroll
+        for (int m = kWarps / 2; m > 0; m >>= 1) v += __shfl_xor_sync(0xffffffffu, v, m);
+        v = __shfl_sync(0xffffffffu, v, 0);
+    }
+    return v;
+}
+
+// TPR threads take a row, C pieces of 8 elements each.
+template <int TPR, int C, bool VEC>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormParams p) {
+    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+    static_assert(TPR == 32 || kRows == 1, "a row is a warp's or a CTA's");
+    __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int t = threadIdx.x % TPR;
+    const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
+    if (row >= p.R) return;                                            // (a whole warp)
+    const int n = p.N;
+    const float inv_n = 1.0f / (float)n;
+    float h[C][8];
+    const void *hr = row_of(p.h, p.hdt, row * p.ldh);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * TPR + t) * 8;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
+        if (at < n) load8<VEC>(h[c], hr, p.hdt, at, n);
+    }
+    if (p.x) {
+        // a thread of 1024 has no registers to keep 32 elements of x beside those of h: it loads them again
+        constexpr bool kKeep = C < 4 || TPR == 32;
+        float x[kKeep ? C : 1][8], sum = 0.0f;
+        const void *xr = row_of(p.x, p.xdt, row * p.ldx), *gr = p.gate ? row_of(p.gate, p.xdt, row * p.ldg) : nullptr;
+        auto load_x = [&](float (&v)[8], int at) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+            if (at < n) load8<VEC>(v, xr, p.xdt, at, n);
+        };
+        if constexpr (kKeep) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) load_x(x[c], (c * TPR + t) * 8);
+        }
+        float r = 1.0f;
+        if (p.w_post) {
+#pragma unroll
+            for (int c = 0; c < C; ++c) {
+                if constexpr (!kKeep) load_x(x[0], (c * TPR + t) * 8);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) sum += x[kKeep ? c : 0][i] * x[kKeep ? c : 0][i];
+            }
+            r = 1.0f / sqrtf(row_sum<TPR>(sum, part[0]) * inv_n + p.eps);
+        }
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = (c * TPR + t) * 8;
+            if (at >= n) continue;
+            float g[8], w[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) g[i] = w[i] = 1.0f;
+            if constexpr (!kKeep) load_x(x[0], at);
+            if (p.w_post) load8<VEC>(w, p.w_post, QMM_F32, at, n);
+            if (gr) load8<VEC>(g, gr, p.xdt, at, n);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[c][i] = rounded(h[c][i] + p.scale * (x[kKeep ? c : 0][i] * r * w[i] * g[i]), p.hdt);
+        }
+    }
+    if (p.h_out) {
+        void *out = const_cast<void *>(row_of(p.h_out, p.hdt, row * p.ldho));
+#pragma unroll
+        for (int c = 0; c < C; ++c) {
+            const int at = (c * TPR + t) * 8;
+            if (at < n && QMM_DCHECK(!VEC || at + 8 <= n)) store8<VEC>(h[c], out, p.hdt, at, n);
+        }
+    }
+    float sum = 0.0f;
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) sum += (c * TPR + t) * 8 + i < n ? h[c][i] * h[c][i] : 0.0f;
+    const float r = 1.0f / sqrtf(row_sum<TPR>(sum, part[1]) * inv_n + p.eps);
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * TPR + t) * 8;
+        const bool in = at < n;
+        float w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = 1.0f;
+        if (p.w_pre && in) load8<VEC>(w, p.w_pre, QMM_F32, at, n);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = in ? __fmul_rn(__fmul_rn(h[c][i], r), w[i]) : 0.0f;
+        if (p.form == kNormRows) {
+            if (in) store8<VEC>(w, const_cast<void *>(row_of(p.y, p.ydt, row * p.ldy)), p.ydt, at, n);
+            continue;
+        }
+        // the largest magnitude of the block of 32 that four threads hold
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(w[i]) & 0x7FFFFFFFu);
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        if (p.form == kNormQ8) {
+            const float d = q8_scale(__uint_as_float(top)), id = inv_or_zero(d);
+            uint32_t b[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) b[i >> 2] |= ((uint32_t)q8_code(w[i], id) & 255u) << (8 * (i & 3));
+            if (in) {
+                *reinterpret_cast<uint2 *>(static_cast<int8_t *>(p.y) + row * n + at) = make_uint2(b[0], b[1]);
+                if ((t & 3) == 0) reinterpret_cast<__half *>(p.scales)[row * (n / 32) + at / 32] = __float2half_rn(d);
+            }
+        } else {
+            const uint32_t e = mx4_block_scale(top);
+            // the scales of four blocks (16 threads) as one word; blocks past n hold 0
+            uint32_t word = in ? e << (2 * (t & 12)) : 0u;
+            word |= __shfl_xor_sync(0xffffffffu, word, 4);
+            word |= __shfl_xor_sync(0xffffffffu, word, 8);
+            if (in) {
+                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.y) + (row * n + at) / 2) = mx4_codes8(w, e);
+                if ((t & 15) == 0) *reinterpret_cast<uint32_t *>(p.scales + mx4_scale_word(row, at >> 7, (n + 127) / 128)) = word;
+            }
+        }
+    }
+}
+
+template <int TPR, int C>
+cudaError_t launch_rows(const NormParams &p, bool vec, cudaStream_t s) {
+    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+    const int64_t grid = (p.R + kRows - 1) / kRows;
+    if (grid > 0x7fffffff) return cudaErrorInvalidValue;
+    return launch_pdl(vec ? norm_kernel<TPR, C, true> : norm_kernel<TPR, C, false>, dim3((unsigned)grid), TPR < 256 ? 256 : TPR, 0, s, p);
+}
+
+}  // namespace
+
+cudaError_t launch_norm(const NormParams &p, cudaStream_t s) {
+    auto fits = [&](const void *q, int type, int64_t ld) { return !q || rows_aligned(q, ld, type == QMM_F32 ? 4 : 2); };
+    const bool vec = p.N % 8 == 0 && fits(p.x, p.xdt, p.ldx) && fits(p.h, p.hdt, p.ldh) && fits(p.gate, p.xdt, p.ldg) &&
+                     fits(p.h_out, p.hdt, p.ldho) && fits(p.w_post, QMM_F32, 0) && fits(p.w_pre, QMM_F32, 0) &&
+                     (p.form != kNormRows || fits(p.y, p.ydt, p.ldy));
+    if (p.N <= 256) return launch_rows<32, 1>(p, vec, s);
+    if (p.N <= 512) return launch_rows<32, 2>(p, vec, s);
+    if (p.N <= 1024) return launch_rows<32, 4>(p, vec, s);
+    if (p.N <= 2048) return launch_rows<256, 1>(p, vec, s);
+    if (p.N <= 4096) return launch_rows<512, 1>(p, vec, s);
+    if (p.N <= 8192) return launch_rows<1024, 1>(p, vec, s);
+    if (p.N <= 16384) return launch_rows<1024, 2>(p, vec, s);
+    return launch_rows<1024, 4>(p, vec, s);
+}
+
+QMM_DCHECK_READER(read_dcheck_norm)
+
+}  // namespace qmm

@@ -8,6 +8,7 @@
 #include "qmm_internal.cuh"
 
 #include "attend.cuh"
+#include "cache.cuh"
 #include "mx4.cuh"
 
 using namespace qmm;
@@ -417,6 +418,211 @@ qmm_status qmm_cache_attend(qmm_type t, const void *k_cache, const void *v_cache
                                          cs(stream)));
 }
 
+// ---- the plan of a step ----
+
+static bool valid_page(int64_t P) { return P >= 16 && P <= 256 && (P & (P - 1)) == 0; }
+
+qmm_status qmm_cache_plan(const int32_t *lens, const int32_t *news, int64_t n_seq, int64_t P, int32_t *pages, int64_t ld_pages,
+                          int32_t *ring, int64_t n_ring, const int64_t *ring_at, int64_t T, int32_t *q_starts, int32_t *kv_lens,
+                          int64_t *slots, int32_t *positions, int32_t *next_lens, int64_t *next_at, qmm_stream_t stream) {
+    if (n_seq <= 0 || n_seq > kMaxDim || !valid_page(P) || ld_pages <= 0 || ld_pages > kMaxDim / P || n_ring <= 0 || n_ring > kMaxDim ||
+        T < 0 || T > kMaxDim)
+        return QMM_ERR_INVALID_ARG;
+    if (!lens || !news || !pages || !ring || !ring_at || !q_starts || !kv_lens || (T > 0 && !slots)) return QMM_ERR_INVALID_ARG;
+    if (!aligned(lens, 4) || !aligned(news, 4) || !aligned(pages, 4) || !aligned(ring, 4) || !aligned(ring_at, 8) ||
+        !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(slots, 8) || !aligned(positions, 4) || !aligned(next_lens, 4) ||
+        !aligned(next_at, 8))
+        return QMM_ERR_MISALIGNED;
+    return from_cuda(launch_cache_plan(lens, news, n_seq, (int)P, pages, ld_pages, ring, n_ring, ring_at, T, q_starts, kv_lens, slots,
+                                       positions, next_lens, next_at, cs(stream)));
+}
+
+// ---- sparse attention ----
+
+size_t qmm_cache_bounds_size(int64_t H, int64_t D) { return valid_cache_sizes(H, D, 16) ? (size_t)H * (size_t)cache_bound_bytes((int)D) : 0; }
+
+qmm_status qmm_cache_bounds(qmm_type t, const void *k_cache, int64_t n_pages, int64_t P, int64_t H, int64_t D, const int32_t *pages,
+                            int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens, int64_t n_seq, int64_t T,
+                            int64_t max_new, void *bounds, qmm_stream_t stream) {
+    const qmm_status st = check_cache(t, k_cache, k_cache, n_pages, P, H, D);
+    if (st != QMM_OK) return st;
+    if (!valid_table(pages, ld_pages, q_starts, n_seq) || !kv_lens || T < 0 || T > kMaxDim) return QMM_ERR_INVALID_ARG;
+    if (T == 0) return QMM_OK;
+    if (!bounds || max_new <= 0 || max_new > kMaxDim) return QMM_ERR_INVALID_ARG;
+    if (!aligned(pages, 4) || !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(bounds, 16)) return QMM_ERR_MISALIGNED;
+    return from_cuda(launch_cache_bounds(t, static_cast<const uint8_t *>(k_cache), n_pages, (int)P, (int)H, (int)D, pages, ld_pages,
+                                         q_starts, kv_lens, n_seq, T, max_new, static_cast<uint8_t *>(bounds), cs(stream)));
+}
+
+size_t qmm_cache_select_workspace_size(int64_t T, int64_t H, int64_t P, int64_t max_len) {
+    if (T <= 0 || T > kMaxDim || H <= 0 || H > 65536 || !valid_page(P) || max_len < 0 || max_len > kMaxDim) return 0;
+    return round256((size_t)T * (size_t)H * (size_t)((max_len + P - 1) / P) * 4);
+}
+
+qmm_status qmm_cache_select(const void *bounds, int64_t n_pages, int64_t P, int64_t H, int64_t D, const int32_t *pages, int64_t ld_pages,
+                            const int32_t *q_starts, const int32_t *kv_lens, int64_t n_seq, qmm_dtype dt, const void *q, int64_t ldq,
+                            int64_t T, int64_t Hq, const uint64_t *tree, int64_t max_new, int64_t max_len, int64_t sinks,
+                            int64_t recent, int64_t budget, int32_t *chosen, void *workspace, size_t workspace_bytes,
+                            qmm_stream_t stream) {
+    if (dt != QMM_F16 && dt != QMM_BF16) return QMM_ERR_UNSUPPORTED;
+    if (!valid_cache_sizes(H, D, P) || n_pages <= 0 || n_pages > kMaxDim || !valid_table(pages, ld_pages, q_starts, n_seq) || !kv_lens ||
+        !valid_heads(H, Hq) || T < 0 || T > kMaxDim || ldq < Hq * D || ldq > kMaxDim || max_len < 0 || max_len > kMaxDim || recent < 1 ||
+        recent > 65536 || sinks < 0 || sinks > 65536 || budget > 65536)
+        return QMM_ERR_INVALID_ARG;
+    if (T == 0) return QMM_OK;
+    if (!bounds || !q || !chosen || max_new <= 0 || max_new > kMaxDim || (tree && max_new > 64)) return QMM_ERR_INVALID_ARG;
+    if (budget < sinks + recent + (tree ? (max_new - 1 + P - 1) / P : 0)) return QMM_ERR_INVALID_ARG;
+    const size_t need = qmm_cache_select_workspace_size(T, H, P, max_len);
+    if (workspace_bytes < need || (need && !workspace)) return QMM_ERR_INVALID_ARG;
+    if (!aligned(bounds, 16) || !aligned(pages, 4) || !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(q, 16) ||
+        (ldq % 8) != 0 || !aligned(tree, 8) || !aligned(chosen, 4) || !aligned(workspace, 256))
+        return QMM_ERR_MISALIGNED;
+    SelectParams p = {};
+    p.bounds = static_cast<const uint8_t *>(bounds);
+    p.n_pages = n_pages;
+    p.ld_pages = ld_pages;
+    p.n_seq = n_seq;
+    p.ldq = ldq;
+    p.T = T;
+    p.most = (max_len + P - 1) / P;
+    while ((1 << p.log_p) < P) ++p.log_p;
+    p.H = (int)H;
+    p.group = (int)(Hq / H);
+    p.bf16 = dt == QMM_BF16;
+    p.tree = tree != nullptr;
+    p.sinks = sinks;
+    p.recent = recent;
+    p.budget = budget;
+    p.pages = pages;
+    p.q_starts = q_starts;
+    p.kv_lens = kv_lens;
+    p.q = q;
+    p.max_new = max_new < T ? max_new : T;
+    p.scores = static_cast<float *>(workspace);
+    p.chosen = chosen;
+    return from_cuda(launch_cache_select(p, (int)D, cs(stream)));
+}
+
+size_t qmm_cache_attend_chosen_workspace_size(int64_t T, int64_t H, int64_t Hq, int64_t D, int64_t P, int64_t budget) {
+    if (T <= 0 || T > kMaxDim || !valid_cache_sizes(H, D, P) || !valid_heads(H, Hq) || budget <= 0 || budget > 65536) return 0;
+    return attend_chosen_workspace_bytes(T, (int)H, (int)Hq, (int)D, (int)P, budget);
+}
+
+qmm_status qmm_cache_attend_chosen(qmm_type t, const void *k_cache, const void *v_cache, int64_t n_pages, int64_t P, int64_t H, int64_t D,
+                                   const int32_t *pages, int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens,
+                                   int64_t n_seq, qmm_dtype dt, const void *q, int64_t ldq, int64_t T, int64_t Hq, const uint64_t *tree,
+                                   float scale, const int32_t *chosen, int64_t budget, void *out, int64_t ldo, float *lse,
+                                   void *workspace, size_t workspace_bytes, qmm_stream_t stream) {
+    if (dt != QMM_F16 && dt != QMM_BF16) return QMM_ERR_UNSUPPORTED;
+    const qmm_status st = check_cache(t, k_cache, v_cache, n_pages, P, H, D);
+    if (st != QMM_OK) return st;
+    if (!valid_table(pages, ld_pages, q_starts, n_seq) || !kv_lens || !valid_heads(H, Hq) || T < 0 || T > kMaxDim || ldq < Hq * D ||
+        ldo < Hq * D || ldq > kMaxDim || ldo > kMaxDim || budget <= 0 || budget > 65536)
+        return QMM_ERR_INVALID_ARG;
+    if (T == 0) return QMM_OK;
+    if (!q || !out || !chosen) return QMM_ERR_INVALID_ARG;
+    if (!aligned(pages, 4) || !aligned(q_starts, 4) || !aligned(kv_lens, 4) || !aligned(tree, 8) || !aligned(lse, 4) || !aligned(q, 16) ||
+        !aligned(out, 16) || !aligned(chosen, 4) || (ldq % 8) != 0 || (ldo % 8) != 0 || !aligned(workspace, 256))
+        return QMM_ERR_MISALIGNED;
+    return from_cuda(launch_cache_attend_chosen(t, static_cast<const uint8_t *>(k_cache), static_cast<const uint8_t *>(v_cache), n_pages,
+                                                (int)P, (int)H, (int)D, pages, ld_pages, q_starts, kv_lens, n_seq, dt, q, ldq, T, (int)Hq,
+                                                tree, scale, chosen, budget, out, ldo, lse, workspace, workspace ? workspace_bytes : 0,
+                                                cs(stream)));
+}
+
+// ---- norms and sampling ----
+
+// The checks of the norm calls but for what they write; fills p.
+static qmm_status check_norm(NormParams &p, qmm_dtype xdt, const void *x, int64_t ldx, qmm_dtype hdt, const void *h, int64_t ldh, int64_t R,
+                             int64_t N, const float *w_post, const void *gate, int64_t ldg, float scale, const float *w_pre, float eps,
+                             void *h_out, int64_t ldho) {
+    if (!valid_dtype(xdt) || !valid_dtype(hdt)) return QMM_ERR_UNSUPPORTED;
+    if (R < 0 || R > kMaxDim || N <= 0 || N > kMaxNormN || ldh < N || ldh > kMaxDim || (x && (ldx < N || ldx > kMaxDim)) ||
+        (gate && ((ldg != 0 && ldg < N) || ldg > kMaxDim)) || (h_out && (ldho < N || ldho > kMaxDim)))
+        return QMM_ERR_INVALID_ARG;
+    if (R > 0 && (!h || (x && !h_out))) return QMM_ERR_INVALID_ARG;
+    if (!aligned(x, dtype_align(xdt)) || !aligned(gate, dtype_align(xdt)) || !aligned(h, dtype_align(hdt)) ||
+        !aligned(h_out, dtype_align(hdt)) || !aligned(w_post, 4) || !aligned(w_pre, 4))
+        return QMM_ERR_MISALIGNED;
+    p.x = x;
+    p.h = h;
+    p.gate = x ? gate : nullptr;
+    p.h_out = h_out;
+    p.w_post = x ? w_post : nullptr;
+    p.w_pre = w_pre;
+    p.ldx = ldx;
+    p.ldh = ldh;
+    p.ldg = ldg;
+    p.ldho = ldho;
+    p.R = R;
+    p.N = (int)N;
+    p.xdt = xdt;
+    p.hdt = hdt;
+    p.scale = scale;
+    p.eps = eps;
+    return QMM_OK;
+}
+
+qmm_status qmm_norm(qmm_dtype xdt, const void *x, int64_t ldx, qmm_dtype hdt, const void *h, int64_t ldh, int64_t R, int64_t N,
+                    const float *w_post, const void *gate, int64_t ldg, float scale, const float *w_pre, float eps, void *h_out,
+                    int64_t ldho, qmm_dtype ydt, void *y, int64_t ldy, qmm_stream_t stream) {
+    if (!valid_dtype(ydt)) return QMM_ERR_UNSUPPORTED;
+    NormParams p = {};
+    const qmm_status st = check_norm(p, xdt, x, ldx, hdt, h, ldh, R, N, w_post, gate, ldg, scale, w_pre, eps, h_out, ldho);
+    if (st != QMM_OK) return st;
+    if (ldy < N || ldy > kMaxDim || (R > 0 && !y)) return QMM_ERR_INVALID_ARG;
+    if (!aligned(y, dtype_align(ydt))) return QMM_ERR_MISALIGNED;
+    if (R == 0) return QMM_OK;
+    p.y = y;
+    p.ldy = ldy;
+    p.ydt = ydt;
+    p.form = kNormRows;
+    return from_cuda(launch_norm(p, cs(stream)));
+}
+
+qmm_status qmm_norm_q8(qmm_dtype xdt, const void *x, int64_t ldx, qmm_dtype hdt, const void *h, int64_t ldh, int64_t R, int64_t N,
+                       const float *w_post, const void *gate, int64_t ldg, float scale, const float *w_pre, float eps, void *h_out,
+                       int64_t ldho, int8_t *a_q, uint16_t *a_d, qmm_stream_t stream) {
+    NormParams p = {};
+    const qmm_status st = check_norm(p, xdt, x, ldx, hdt, h, ldh, R, N, w_post, gate, ldg, scale, w_pre, eps, h_out, ldho);
+    if (st != QMM_OK) return st;
+    if (N % 32 != 0 || (R > 0 && (!a_q || !a_d))) return QMM_ERR_INVALID_ARG;
+    if (!aligned(a_q, 16) || !aligned(a_d, 4)) return QMM_ERR_MISALIGNED;
+    if (R == 0) return QMM_OK;
+    p.y = a_q;
+    p.scales = reinterpret_cast<uint8_t *>(a_d);
+    p.form = kNormQ8;
+    return from_cuda(launch_norm(p, cs(stream)));
+}
+
+qmm_status qmm_norm_mx4(qmm_dtype xdt, const void *x, int64_t ldx, qmm_dtype hdt, const void *h, int64_t ldh, int64_t R, int64_t N,
+                        const float *w_post, const void *gate, int64_t ldg, float scale, const float *w_pre, float eps, void *h_out,
+                        int64_t ldho, void *codes, void *scales, qmm_stream_t stream) {
+    NormParams p = {};
+    const qmm_status st = check_norm(p, xdt, x, ldx, hdt, h, ldh, R, N, w_post, gate, ldg, scale, w_pre, eps, h_out, ldho);
+    if (st != QMM_OK) return st;
+    if (N % 32 != 0 || (R > 0 && (!codes || !scales))) return QMM_ERR_INVALID_ARG;
+    if (!aligned(codes, 16) || !aligned(scales, 16)) return QMM_ERR_MISALIGNED;
+    if (R == 0) return QMM_OK;
+    p.y = codes;
+    p.scales = static_cast<uint8_t *>(scales);
+    p.form = kNormMx4;
+    return from_cuda(launch_norm(p, cs(stream)));
+}
+
+qmm_status qmm_sample(qmm_dtype dt, const void *logits, int64_t ld, int64_t R, int64_t V, const float *temperature, const int32_t *top_k,
+                      const float *top_p, const float *min_p, const float *u, int32_t *tokens, float *logp, qmm_stream_t stream) {
+    if (!valid_dtype(dt)) return QMM_ERR_UNSUPPORTED;
+    if (R < 0 || R > kMaxDim || V <= 0 || V > kMaxVocab || ld < V || ld > kMaxDim) return QMM_ERR_INVALID_ARG;
+    if (R == 0) return QMM_OK;
+    if (!logits || !u || !tokens) return QMM_ERR_INVALID_ARG;
+    if (!aligned(logits, dtype_align(dt)) || !aligned(temperature, 4) || !aligned(top_k, 4) || !aligned(top_p, 4) || !aligned(min_p, 4) ||
+        !aligned(u, 4) || !aligned(tokens, 4) || !aligned(logp, 4))
+        return QMM_ERR_MISALIGNED;
+    SampleParams p = {logits, ld, R, (int)V, temperature, top_p, min_p, u, top_k, tokens, logp};
+    return from_cuda(launch_sample(dt, p, cs(stream)));
+}
+
 size_t qmm_matmul_noalloc_max_workspace(void) { return kNoAllocScratchBytes; }
 
 qmm_status qmm_selftest_timeout(int unit, uint64_t limit_ns, int *flags_dev, qmm_stream_t stream) {
@@ -436,7 +642,7 @@ qmm_status qmm_device_status(qmm_stream_t stream) {
     if (e == cudaSuccess) e = read_and_clear_mx4_status(&m, cs(stream));
     if (e == cudaSuccess) e = read_and_clear_attend_status(&a, cs(stream));
     // the bounds-check words (always 0 unless the library was built with QMM_DEBUG)
-    unsigned d[10] = {0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+    unsigned d[15] = {};
     if (e == cudaSuccess) e = read_dcheck_matvec(&d[0], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_gemm(&d[1], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_fold(&d[2], cs(stream));
@@ -447,6 +653,11 @@ qmm_status qmm_device_status(qmm_stream_t stream) {
     if (e == cudaSuccess) e = read_dcheck_cache(&d[7], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_attend(&d[8], cs(stream));
     if (e == cudaSuccess) e = read_dcheck_attend_tc(&d[9], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_cache_plan(&d[10], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_cache_select(&d[11], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_attend_chosen(&d[12], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_norm(&d[13], cs(stream));
+    if (e == cudaSuccess) e = read_dcheck_sample(&d[14], cs(stream));
     if (e != cudaSuccess) return QMM_ERR_CUDA;
     for (unsigned line : d)
         if (line) return QMM_ERR_BOUNDS;

@@ -237,6 +237,60 @@ cudaError_t launch_cache_attend(qmm_type type, const uint8_t *k_cache, const uin
                                 int64_t n_seq, qmm_dtype t, const void *q, int64_t ldq, int64_t T, int Hq, const uint64_t *tree,
                                 float scale, int64_t max_new, int64_t max_len, void *out, int64_t ldo, float *lse, void *ws,
                                 size_t ws_bytes, cudaStream_t s);
+// The plan of a step (cache_plan.cu), sparse attention (cache_select.cu, attend_chosen.cu), norms (norm.cu) and sampling
+// (sample.cu).
+cudaError_t launch_cache_plan(const int32_t *lens, const int32_t *news, int64_t n_seq, int P, int32_t *pages, int64_t ld_pages,
+                              int32_t *ring, int64_t n_ring, const int64_t *ring_at, int64_t T, int32_t *q_starts, int32_t *kv_lens,
+                              int64_t *slots, int32_t *positions, int32_t *next_lens, int64_t *next_at, cudaStream_t s);
+cudaError_t launch_cache_bounds(qmm_type type, const uint8_t *k_cache, int64_t n_pages, int P, int H, int D, const int32_t *pages,
+                                int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens, int64_t n_seq, int64_t T,
+                                int64_t max_new, uint8_t *bounds, cudaStream_t s);
+struct SelectParams {
+    const uint8_t *bounds;
+    int64_t n_pages, ld_pages, n_seq, ldq, T, most;   // most: pages of a sequence at most, the row length of `scores`
+    int log_p, H, group, bf16, tree, tok_tile;        // tok_tile: rows of q of a CTA of the scores
+    int64_t sinks, recent, budget;
+    const int32_t *pages, *q_starts, *kv_lens;
+    const void *q;
+    int64_t max_new;
+    float *scores;                          // [T][H][most]
+    int32_t *chosen;
+};
+cudaError_t launch_cache_select(const SelectParams &p, int D, cudaStream_t s);
+size_t attend_chosen_workspace_bytes(int64_t T, int H, int Hq, int D, int P, int64_t budget);
+cudaError_t launch_cache_attend_chosen(qmm_type type, const uint8_t *k_cache, const uint8_t *v_cache, int64_t n_pages, int P, int H, int D,
+                                       const int32_t *pages, int64_t ld_pages, const int32_t *q_starts, const int32_t *kv_lens,
+                                       int64_t n_seq, qmm_dtype t, const void *q, int64_t ldq, int64_t T, int Hq, const uint64_t *tree,
+                                       float scale, const int32_t *chosen, int64_t budget, void *out, int64_t ldo, float *lse, void *ws,
+                                       size_t ws_bytes, cudaStream_t s);
+enum NormForm { kNormRows = 0, kNormQ8 = 1, kNormMx4 = 2 };
+struct NormParams {
+    const void *x, *h, *gate;
+    void *h_out, *y;                        // y: rows, int8 codes or E2M1 codes
+    uint8_t *scales;                        // fp16 block scales, or E8M0 scales
+    const float *w_post, *w_pre;
+    int64_t ldx, ldh, ldg, ldho, ldy, R;
+    int N, xdt, hdt, ydt, form;
+    float scale, eps;
+};
+cudaError_t launch_norm(const NormParams &p, cudaStream_t s);
+constexpr int64_t kMaxNormN = 32768;
+struct SampleParams {
+    const void *logits;
+    int64_t ld, R;
+    int V;
+    const float *temperature, *top_p, *min_p, *u;
+    const int32_t *top_k;
+    int32_t *tokens;
+    float *logp;
+};
+cudaError_t launch_sample(qmm_dtype t, const SampleParams &p, cudaStream_t s);
+constexpr int64_t kMaxVocab = (int64_t)1 << 20;
+cudaError_t read_dcheck_cache_plan(unsigned *out, cudaStream_t s);
+cudaError_t read_dcheck_cache_select(unsigned *out, cudaStream_t s);
+cudaError_t read_dcheck_attend_chosen(unsigned *out, cudaStream_t s);
+cudaError_t read_dcheck_norm(unsigned *out, cudaStream_t s);
+cudaError_t read_dcheck_sample(unsigned *out, cudaStream_t s);
 cudaError_t read_dcheck_mx4(unsigned *out, cudaStream_t s);
 cudaError_t read_dcheck_mx4_gemm(unsigned *out, cudaStream_t s);
 cudaError_t read_dcheck_cache(unsigned *out, cudaStream_t s);
@@ -256,6 +310,27 @@ inline cudaError_t launch_pdl(void (*kern)(P...), dim3 grid, unsigned threads, s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+// The same in clusters of `cluster` CTAs.
+template <typename... P, typename... A>
+inline cudaError_t launch_pdl_cluster(void (*kern)(P...), dim3 grid, unsigned cluster, unsigned threads, size_t smem, cudaStream_t s,
+                                      const A &...args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kern, args...);
 }
 

@@ -74,7 +74,7 @@ typedef enum { QMM_Q4_0 = 0, QMM_Q8_0 = 1, QMM_IQ4_NL = 2, QMM_MXFP4 = 3, QMM_Q4
  * runs through qmm_matmul_ws / qmm_matmul_noalloc). */
 typedef enum { QMM_PATH_AUTO = 0, QMM_PATH_MATVEC = 1, QMM_PATH_GEMM = 2 } qmm_path;
 
-/* Element types of the floating-point rows of the MX4 and cache calls (IEEE binary32, binary16, bfloat16). */
+/* Element types of the floating-point rows of the MX4, cache, norm and sampling calls (IEEE binary32, binary16, bfloat16). */
 typedef enum { QMM_F32 = 0, QMM_F16 = 1, QMM_BF16 = 2 } qmm_dtype;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -505,6 +505,190 @@ QMM_API qmm_status qmm_cache_attend(qmm_type t, const void *k_cache_dev, const v
                                     const void *q_dev, int64_t ldq, int64_t T, int64_t Hq, const uint64_t *tree_dev,
                                     float scale, int64_t max_new, int64_t max_len, void *out_dev, int64_t ldo, float *lse_dev,
                                     void *workspace_dev, size_t workspace_bytes, qmm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The plan of a step over the paged cache: page tables, slots and row starts, made on the GPU.
+ * --------------------------------------------------------------------------------------------- */
+
+/*
+ * qmm_cache_plan -- from the requests' cached lengths and new tokens of a step, what the cache calls take.
+ *   lens_dev      int32 [n_seq]: tokens cached before the step (values outside 0 .. ld_pages * P count as the nearest of the two).
+ *   news_dev      int32 [n_seq]: new tokens of the step; 0: none; negative: the request is done, its pages are free again.
+ *   pages_dev     int32 [n_seq][ld_pages]: the pages of each sequence in order; the entries of pages that a sequence is
+ *                 given in this call are written, all others stay.
+ *   ring_dev, n_ring  int32 [n_ring]: the free pages.  ring_at_dev int64 [2]: entries ring_at[0] .. ring_at[1] - 1
+ *                 (modulo n_ring) are free.  Pages are taken from the front, and those of finished requests are put behind
+ *                 the end (to be taken by the next call at the earliest).  n_ring is at least the number of pages that are
+ *                 free or go back in the call; the counters only grow.
+ *   T             rows of the step (of q, k, v and of slots and positions); 0 is fine.
+ * A sequence with new tokens takes rows q_starts[s] .. of the step, in order.  It needs ceil((len + new) / P) - ceil(len / P)
+ * pages, and waits (is not run in this step) when those would not fit its row of pages_dev, when its rows would pass
+ * T, or when it needs pages and those of all sequences up to and including it, the waiting ones for want
+ * of pages included, are more than are free.  A sequence that needs no page never waits for want of them.
+ * Outputs:
+ *   q_starts_dev  int32 [n_seq + 1]: the first row of each sequence, and all rows (sums beyond INT32_MAX count as that).
+ *   kv_lens_dev   int32 [n_seq]: len + new; 0 for a sequence that waits (its rows of qmm_cache_attend are then 0) or is done.
+ *   slots_dev     int64 [T]: page * P + place of each row's token; -1 (not written by qmm_cache_write) for rows of
+ *                 sequences that wait, and for rows behind the last sequence.
+ *   positions_dev NULL, or int32 [T]: place of each row's token in its sequence; -1 where its slot is.
+ *   next_lens_dev NULL, or int32 [n_seq]: tokens cached after the step (unchanged for a sequence that waits, 0 for one that is done).
+ *   next_at_dev   NULL, or int64 [2]: the ring's counters after the step.
+ * next_lens_dev may be lens_dev and next_at_dev may be ring_at_dev (a captured graph then carries the state from replay to
+ * replay); no other two buffers may overlap.  Without that the call reads only what it does not write, and can be repeated.
+ * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
+ * Errors: INVALID_ARG (n_seq <= 0, ld_pages <= 0, T < 0, n_ring <= 0, P, NULL), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_cache_plan(const int32_t *lens_dev, const int32_t *news_dev, int64_t n_seq, int64_t P, int32_t *pages_dev,
+                                  int64_t ld_pages, int32_t *ring_dev, int64_t n_ring, const int64_t *ring_at_dev, int64_t T,
+                                  int32_t *q_starts_dev, int32_t *kv_lens_dev, int64_t *slots_dev, int32_t *positions_dev,
+                                  int32_t *next_lens_dev, int64_t *next_at_dev, qmm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Sparse attention over the paged cache: each new token and key/value head attends over the pages that a cheap
+ * score chooses for it.
+ *
+ * The bounds of a page are, for each head and element, the lowest and the highest value among the page's keys, in codes of
+ * 8 bits: for each page and head [2][D] int8 (lowest, then highest), then [D/32] fp16 scales, one for both codes of a block of
+ * 32, then zeros up to a multiple of 16 bytes.  With top the largest magnitude among the 64 values of a block, its scale d
+ * is top/127 rounded up to fp16, lowest = floor(value/d), highest = ceil(value/d), within [-127, 127] (0 where d is 0; IEEE
+ * fp32 divisions).  A block in which a key has a scale that is not finite has a NaN scale and codes 0.
+ *
+ * score(i, h, page) = max over the query heads of h of sum_b fp32(dq_b * d_b) * S_b, block after block in fp32,
+ *   S_b = sum over the block of a * (a > 0 ? highest : lowest)  (a whole number),
+ * a and dq the query row's codes by the rule of qmm_quantize_act and the scale they stem from (not rounded to fp16; a block that
+ * holds an infinity or a NaN has a NaN scale).  It is not less than any q . k of the page, but for the roundings of q and of the
+ * divisions.  A NaN score counts as +inf.
+ * --------------------------------------------------------------------------------------------- */
+
+/* Bytes of one page's bounds: H * round_up(2 D + D/32 * 2, 16); 0 if a size is invalid. */
+QMM_API size_t qmm_cache_bounds_size(int64_t H, int64_t D);
+
+/*
+ * qmm_cache_bounds -- the bounds of the pages that hold the step's new tokens, from the keys as they are cached: call it
+ * after qmm_cache_write, with the same step's arguments.
+ *   k_cache_dev, pages_dev, q_starts_dev, kv_lens_dev, T, max_new  as for qmm_cache_attend.  All keys of those pages up to kv_lens
+ *                are read, the older ones too.  Pages out of the pool, past ld_pages, or of new tokens past max_new (the
+ *                last max_new tokens of a sequence count) are left as they are.
+ *   bounds_dev   n_pages * qmm_cache_bounds_size(H, D) bytes, 16-byte aligned.
+ * T = 0 does nothing.  Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
+ * Errors: INVALID_ARG (sizes, NULL), UNSUPPORTED (t), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_cache_bounds(qmm_type t, const void *k_cache_dev, int64_t n_pages, int64_t P, int64_t H, int64_t D,
+                                    const int32_t *pages_dev, int64_t ld_pages, const int32_t *q_starts_dev,
+                                    const int32_t *kv_lens_dev, int64_t n_seq, int64_t T, int64_t max_new, void *bounds_dev,
+                                    qmm_stream_t stream);
+
+/* Bytes of workspace qmm_cache_select needs: 4 * T * H * ceil(max_len / P), rounded up to 256 (0 if a size is invalid). */
+QMM_API size_t qmm_cache_select_workspace_size(int64_t T, int64_t H, int64_t P, int64_t max_len);
+
+/*
+ * qmm_cache_select -- for each new token and key/value head the pages it attends over.
+ *   bounds_dev   as written by qmm_cache_bounds for every page that holds tokens; 16-byte aligned.
+ *   pages_dev, q_starts_dev, kv_lens_dev, q_dev, ldq, T, Hq, max_new  as for qmm_cache_attend.
+ *   tree_dev     NULL or not, as it will be for qmm_cache_attend_chosen (the words are not read).
+ *   max_len      no sequence has more cached tokens than this; the rows of one that has get no page.
+ *   chosen_dev   int32 [T][H][budget]: the numbers (0 is the sequence's first page) of the chosen pages, ascending, then -1.
+ * The pages in question are those up to the token's own (with tree words: up to the sequence's last).  Always chosen are the first `sinks` of
+ * them and the last `recent` ones, the token's own included (with tree words: those with new tokens, and recent - 1 before them);
+ * then those of the highest scores, the earlier page on ties, until there are `budget` in all.  (If more than `budget` pages are
+ * always chosen, the first of them are.)
+ * Rows of no sequence, of sequences whose rows do not all lie in q, and past max_new, are left as they are.
+ * T = 0 does nothing.  Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
+ * Errors: INVALID_ARG (sizes, strides, NULL, Hq % H, recent < 1, sinks < 0, budget < sinks + recent (+ ceil((max_new - 1) / P) with
+ * tree words), budget > 65536, tree words with max_new > 64, workspace too small), UNSUPPORTED (dt), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_cache_select(const void *bounds_dev, int64_t n_pages, int64_t P, int64_t H, int64_t D,
+                                    const int32_t *pages_dev, int64_t ld_pages, const int32_t *q_starts_dev,
+                                    const int32_t *kv_lens_dev, int64_t n_seq, qmm_dtype dt, const void *q_dev, int64_t ldq,
+                                    int64_t T, int64_t Hq, const uint64_t *tree_dev, int64_t max_new, int64_t max_len,
+                                    int64_t sinks, int64_t recent, int64_t budget, int32_t *chosen_dev, void *workspace_dev,
+                                    size_t workspace_bytes, qmm_stream_t stream);
+
+/* Bytes of workspace with which qmm_cache_attend_chosen spreads few rows over the whole GPU; with less it spreads them less.
+ * 0 if that is of no use, or a size is invalid. */
+QMM_API size_t qmm_cache_attend_chosen_workspace_size(int64_t T, int64_t H, int64_t Hq, int64_t D, int64_t P, int64_t budget);
+
+/*
+ * qmm_cache_attend_chosen -- qmm_cache_attend, each row over the tokens of its chosen pages only.
+ *   chosen_dev, budget  as written by qmm_cache_select, or any int32 [T][H][budget]: a list ends at its first negative entry; pages
+ *                past the sequence's end hold nothing that a row sees, and a page that is listed twice counts twice.  A
+ *                list of -1 alone gives a row that sees nothing.
+ *   the rest     as for qmm_cache_attend (rows of all T tokens of sequences are computed; there is no max_new).
+ * Errors: those of qmm_cache_attend, plus INVALID_ARG (budget <= 0 or > 65536, chosen NULL) and MISALIGNED (chosen, 4 bytes).
+ */
+QMM_API qmm_status qmm_cache_attend_chosen(qmm_type t, const void *k_cache_dev, const void *v_cache_dev, int64_t n_pages, int64_t P,
+                                           int64_t H, int64_t D, const int32_t *pages_dev, int64_t ld_pages,
+                                           const int32_t *q_starts_dev, const int32_t *kv_lens_dev, int64_t n_seq, qmm_dtype dt,
+                                           const void *q_dev, int64_t ldq, int64_t T, int64_t Hq, const uint64_t *tree_dev,
+                                           float scale, const int32_t *chosen_dev, int64_t budget, void *out_dev, int64_t ldo,
+                                           float *lse_dev, void *workspace_dev, size_t workspace_bytes, qmm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The norms around a block, with its gate and residual.
+ * --------------------------------------------------------------------------------------------- */
+
+/*
+ * qmm_norm -- from a block's output x and the residual stream h, the next stream and the next block's input:
+ *   b = w_post ? rms(x) * w_post : x,   h' = h + scale * gate * b   (rounded to hdt),   y = rms(h') * w_pre,
+ *   rms(v) = v / sqrt(mean(v^2) + eps),
+ * row by row, in fp32 but for the roundings of h' and y.
+ *   x_dev      NULL (h' = h then, and h_out may be NULL), or R rows of N elements of type xdt, row r at x_dev + r*ldx.
+ *   h_dev      R rows of type hdt (row stride ldh).
+ *   w_post_dev, w_pre_dev  NULL, or fp32 [N].  NULL for w_post: no norm behind the block.  NULL for w_pre: all ones.
+ *   gate_dev   NULL (ones), or elements of type xdt: R rows of stride ldg, or one row for all with ldg = 0.
+ *   h_out_dev  R rows of type hdt (row stride ldho); may be h_dev with ldho = ldh.
+ *   y_dev      R rows of type ydt (row stride ldy).
+ * N is at most 32768; R = 0 does nothing.  Pointers are aligned to their elements (fp32 weights to 4 bytes); rows that are aligned to 32
+ * bytes, with weights aligned to 32 bytes and N % 8 == 0, take the vectorised path.  y may not overlap x, h or gate; h_out may not
+ * overlap x or gate.
+ * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
+ * Errors: INVALID_ARG (sizes, strides, NULL), UNSUPPORTED (types), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_norm(qmm_dtype xdt, const void *x_dev, int64_t ldx, qmm_dtype hdt, const void *h_dev, int64_t ldh, int64_t R,
+                            int64_t N, const float *w_post_dev, const void *gate_dev, int64_t ldg, float scale,
+                            const float *w_pre_dev, float eps, void *h_out_dev, int64_t ldho, qmm_dtype ydt, void *y_dev,
+                            int64_t ldy, qmm_stream_t stream);
+
+/* qmm_norm_q8 -- qmm_norm followed by qmm_quantize_act on y as fp32, bit for bit: a_q_dev int8 [R][N] (16-byte aligned) and
+ * a_d_dev fp16 [R][N/32] (4-byte aligned).  N % 32 == 0; the rest as for qmm_norm. */
+QMM_API qmm_status qmm_norm_q8(qmm_dtype xdt, const void *x_dev, int64_t ldx, qmm_dtype hdt, const void *h_dev, int64_t ldh, int64_t R,
+                               int64_t N, const float *w_post_dev, const void *gate_dev, int64_t ldg, float scale,
+                               const float *w_pre_dev, float eps, void *h_out_dev, int64_t ldho, int8_t *a_q_dev, uint16_t *a_d_dev,
+                               qmm_stream_t stream);
+
+/* qmm_norm_mx4 -- qmm_norm followed by qmm_mx4_quantize on y as fp32, bit for bit: the activation operand of qmm_mx4_matmul (R rows of
+ * N; both buffers 16-byte aligned).  N % 32 == 0; the rest as for qmm_norm. */
+QMM_API qmm_status qmm_norm_mx4(qmm_dtype xdt, const void *x_dev, int64_t ldx, qmm_dtype hdt, const void *h_dev, int64_t ldh, int64_t R,
+                                int64_t N, const float *w_post_dev, const void *gate_dev, int64_t ldg, float scale,
+                                const float *w_pre_dev, float eps, void *h_out_dev, int64_t ldho, void *codes_dev, void *scales_dev,
+                                qmm_stream_t stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Tokens from logits.
+ * --------------------------------------------------------------------------------------------- */
+
+/*
+ * qmm_sample -- one token of each row of logits, from given random numbers.
+ *   logits_dev   R rows of V elements of type dt, row r at logits_dev + r*ld; aligned to the element.  NaN counts as -inf.
+ *   temperature_dev, top_p_dev, min_p_dev  fp32 [R]; top_k_dev int32 [R]; each may be NULL (1, off, off, off).
+ *   u_dev        fp32 [R]: random numbers in [0, 1) (others count as the nearest of those, NaN as 0).
+ *   tokens_dev   int32 [R]; logp_dev NULL, or fp32 [R].
+ * With z a row, m its maximum and w_i = exp((z_i - m) / temperature), ranked by z (the earlier index first on ties), are kept
+ *   the top_k first (all where top_k <= 0),
+ *   of those the ones before which the others sum to less than top_p of the sum of the top_k first (all where top_p >= 1 or NaN), and
+ *   of those the ones with w_i >= min_p (all where min_p <= 0 or NaN);
+ * the first in rank is always kept.  The token is the first index at which the sum of the kept w up to and including it exceeds u
+ * times the sum of all kept; logp is ln of its share.  temperature <= 0 (or NaN): the first in rank, logp 0.  A row
+ * in which every logit is -inf or NaN gives token -1 and logp -inf.  An infinite maximum leaves the +inf ones, equally likely.
+ * w is held in fixed point, 2^-43 of the largest, within 2^-41, and sums are exact from there: the result does not depend on
+ * the order of summation, and differs from the formula's only where u or top_p lies within about V * 2^-43 of a border.
+ * V is at most 2^20; R = 0 does nothing.
+ * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
+ * Errors: INVALID_ARG (R < 0, V <= 0, V > 2^20, ld < V, NULL), UNSUPPORTED (dt), MISALIGNED, CUDA.
+ */
+QMM_API qmm_status qmm_sample(qmm_dtype dt, const void *logits_dev, int64_t ld, int64_t R, int64_t V, const float *temperature_dev,
+                              const int32_t *top_k_dev, const float *top_p_dev, const float *min_p_dev, const float *u_dev,
+                              int32_t *tokens_dev, float *logp_dev, qmm_stream_t stream);
 
 /*
  * qmm_device_status -- synchronizes `stream`, then returns and clears the library's device status
