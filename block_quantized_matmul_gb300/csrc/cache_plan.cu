@@ -12,9 +12,11 @@
 // barrier, between the last read of a tile of lengths and the first write of its results, lets the new
 // lengths replace the old.  What bounds it is latency: the loads of the lengths, three scans in one, a row's search
 // for its sequence (8 or 10 steps in shared memory), and a load of the page.
+// Eight CTAs are few for the rows of many prompts (412000 rows: 75 us).  Those the cluster leaves to a second kernel over the whole
+// GPU, and takes the new pages instead, one in P rows: what the rows need stands in the outputs and the tables then.
 #include <climits>
 
-#include "qmm_internal.cuh"
+#include "cache.cuh"
 
 namespace qmm {
 namespace {
@@ -53,12 +55,14 @@ __device__ __forceinline__ int64_t around(int64_t at, int64_t n) { return at < n
 
 constexpr int kWaits = -1, kDone = -2;      // in place of the pages that a sequence holds
 
-template <int THREADS>
+// ROWS: the rows too; otherwise the new pages, and cache_plan_rows_kernel takes the rows.
+template <int THREADS, bool ROWS>
 __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p) {
     constexpr int kWarps = THREADS / 32;
     __shared__ Sums part[kWarps];
     __shared__ int64_t s_start[THREADS], s_base[THREADS];             // first row; first new page, or first page given back, in the ring
     __shared__ int s_len[THREADS], s_held[THREADS];
+    __shared__ int64_t s_line[ROWS ? 1 : THREADS];                     // pages wanted by the sequences before
     __shared__ unsigned long long s_taken;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ctas = (int)gridDim.x, cta = (int)blockIdx.x;
     if (threadIdx.x == 0) s_taken = 0;
@@ -90,6 +94,7 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
         const unsigned takes = __ballot_sync(0xffffffffu, run && v.need > 0);
         if (takes && lane == 31 - __clz(takes)) atomicMax(&s_taken, (unsigned long long)(x.need + v.need));
         s_start[threadIdx.x] = x.rows;
+        if constexpr (!ROWS) s_line[threadIdx.x] = x.need;
         s_len[threadIdx.x] = (int)len;
         s_held[threadIdx.x] = news < 0 ? kDone : (run ? (int)held : kWaits);
         s_base[threadIdx.x] = news < 0 ? around(behind + x.back, p.n_ring) : around(front + x.need, p.n_ring);
@@ -113,41 +118,58 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
                 if (QMM_DCHECK(to >= 0 && to < p.n_ring && k < p.ld_pages && base + i < p.n_seq)) p.ring[to] = p.pages[(base + i) * p.ld_pages + k];
             }
         }
-        // ---- the rows that fall into this tile ----
-        const int64_t r1 = min(done.rows + all.rows, p.T);
-        for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < r1; r += (int64_t)ctas * THREADS) {
-            int lo = 0, hi = THREADS;                                  // the last sequence that starts at or before the row
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (s_start[mid] <= r) lo = mid;
-                else hi = mid;
-            }
-            int64_t slot = -1;
-            int pos = -1;
-            if (s_held[lo] >= 0) {
-                pos = s_len[lo] + (int)(r - s_start[lo]);
-                const int number = pos >> p.log_p, k = number - s_held[lo], place = pos & (P - 1);
-                int64_t page = -1;
-                if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) {
-                    int32_t *entry = p.pages + (base + lo) * p.ld_pages + number;
-                    if (k >= 0) {
-                        page = p.ring[around(s_base[lo] + k, p.n_ring)];
-                        if (place == 0) *entry = (int32_t)page;
-                    } else {
-                        page = *entry;
-                    }
+        if constexpr (ROWS) {
+            // ---- the rows that fall into this tile ----
+            const int64_t r1 = min(done.rows + all.rows, p.T);
+            for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < r1; r += (int64_t)ctas * THREADS) {
+                int lo = 0, hi = THREADS;                                  // the last sequence that starts at or before the row
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_start[mid] <= r) lo = mid;
+                    else hi = mid;
                 }
-                slot = page * P + place;
+                int64_t slot = -1;
+                int pos = -1;
+                if (s_held[lo] >= 0) {
+                    pos = s_len[lo] + (int)(r - s_start[lo]);
+                    const int number = pos >> p.log_p, k = number - s_held[lo], place = pos & (P - 1);
+                    int64_t page = -1;
+                    if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) {
+                        int32_t *entry = p.pages + (base + lo) * p.ld_pages + number;
+                        if (k >= 0) {
+                            page = p.ring[around(s_base[lo] + k, p.n_ring)];
+                            if (place == 0) *entry = (int32_t)page;
+                        } else {
+                            page = *entry;
+                        }
+                    }
+                    slot = page * P + place;
+                }
+                p.slots[r] = slot;
+                if (p.positions) p.positions[r] = pos;
             }
-            p.slots[r] = slot;
-            if (p.positions) p.positions[r] = pos;
+        } else {
+            // ---- the new pages of this tile ----
+            for (int64_t at = done.need + (int64_t)cta * THREADS + threadIdx.x; at < done.need + all.need; at += (int64_t)ctas * THREADS) {
+                int lo = 0, hi = THREADS;                              // the last sequence whose pages start at or before it
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (s_line[mid] <= at) lo = mid;
+                    else hi = mid;
+                }
+                if (s_held[lo] < 0) continue;
+                const int64_t number = s_held[lo] + (at - s_line[lo]);
+                if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) p.pages[(base + lo) * p.ld_pages + number] = p.ring[around(front + at, p.n_ring)];
+            }
         }
         done = done + all;
         __syncthreads();                                              // the tile's arrays are free again
     }
-    for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < p.T; r += (int64_t)ctas * THREADS) {
-        p.slots[r] = -1;
-        if (p.positions) p.positions[r] = -1;
+    if constexpr (ROWS) {
+        for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < p.T; r += (int64_t)ctas * THREADS) {
+            p.slots[r] = -1;
+            if (p.positions) p.positions[r] = -1;
+        }
     }
     if (cta == 0 && threadIdx.x == 0) {
         p.q_starts[p.n_seq] = (int32_t)min(done.rows, (int64_t)INT_MAX);
@@ -158,6 +180,35 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
     }
 }
 
+// The rows' slots and positions from what the first kernel has written, kRowsOfCta neighbouring rows to a CTA.
+constexpr int kRowThreads = 256, kRowsOfCta = 8 * kRowThreads;
+__global__ void __launch_bounds__(kRowThreads) cache_plan_rows_kernel(const PlanParams p) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int64_t r0 = (int64_t)blockIdx.x * kRowsOfCta, r1 = min(p.T, r0 + kRowsOfCta);
+    const int64_t s0 = max((int64_t)0, last_start(p.q_starts, p.n_seq, r0)), s1 = last_start(p.q_starts, p.n_seq, r1 - 1);
+    for (int64_t r = r0 + threadIdx.x; r < r1; r += kRowThreads) {
+        int64_t lo = s0, hi = s1 + 1;
+        while (hi - lo > 1) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (p.q_starts[mid] <= r) lo = mid;
+            else hi = mid;
+        }
+        int64_t slot = -1;
+        int pos = -1;
+        if (lo < p.n_seq) {
+            const int from = p.q_starts[lo], to = p.q_starts[lo + 1], len = p.kv_lens[lo];
+            if (len > 0) {                                             // (0: the sequence waits)
+                pos = len - (to - from) + (int)(r - from);
+                const int number = pos >> p.log_p;
+                if (QMM_DCHECK(pos >= 0 && number < p.ld_pages)) slot = (int64_t)p.pages[lo * p.ld_pages + number] << p.log_p | (pos & ((1 << p.log_p) - 1));
+            }
+        }
+        p.slots[r] = slot;
+        if (p.positions) p.positions[r] = pos;
+    }
+}
+
 }  // namespace
 
 cudaError_t launch_cache_plan(const int32_t *lens, const int32_t *news, int64_t n_seq, int P, int32_t *pages, int64_t ld_pages,
@@ -165,10 +216,15 @@ cudaError_t launch_cache_plan(const int32_t *lens, const int32_t *news, int64_t 
                               int64_t *slots, int32_t *positions, int32_t *next_lens, int64_t *next_at, cudaStream_t s) {
     PlanParams p = {lens, news, n_seq, ld_pages, n_ring, T, 0, pages, ring, ring_at, q_starts, kv_lens, slots, positions, next_lens, next_at};
     while ((1 << p.log_p) < P) ++p.log_p;
-    if (n_seq <= 256 && T <= 1024) return launch_pdl(cache_plan_kernel<256>, dim3(1), 256, 0, s, p);
-    unsigned ctas = 1;
-    while (ctas < 8 && (int64_t)ctas * 2048 < T) ctas *= 2;
-    return launch_pdl_cluster(cache_plan_kernel<1024>, dim3(ctas), ctas, 1024, 0, s, p);
+    if (n_seq <= 256 && T <= 1024) return launch_pdl(cache_plan_kernel<256, true>, dim3(1), 256, 0, s, p);
+    if (T <= 8192) {
+        unsigned ctas = 1;
+        while (ctas < 8 && (int64_t)ctas * 1024 < T) ctas *= 2;
+        return launch_pdl_cluster(cache_plan_kernel<1024, true>, dim3(ctas), ctas, 1024, 0, s, p);
+    }
+    const cudaError_t e = launch_pdl_cluster(cache_plan_kernel<1024, false>, dim3(8), 8, 1024, 0, s, p);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(cache_plan_rows_kernel, dim3((unsigned)((T + kRowsOfCta - 1) / kRowsOfCta)), kRowThreads, 0, s, p);
 }
 
 QMM_DCHECK_READER(read_dcheck_cache_plan)

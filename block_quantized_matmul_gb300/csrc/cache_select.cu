@@ -28,17 +28,28 @@ struct BoundsParams {
     uint8_t *bounds;
 };
 
-__device__ __forceinline__ uint32_t pack4(const int (&q)[4]) {
-    return (uint32_t)(q[0] & 255) | (uint32_t)(q[1] & 255) << 8 | (uint32_t)(q[2] & 255) << 16 | (uint32_t)q[3] << 24;
+__device__ __forceinline__ uint32_t pack4(int a, int b, int c, int d) {
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8 | (uint32_t)(c & 255) << 16 | (uint32_t)d << 24;
 }
 
 constexpr int kBoundWarps = 4;
 
+// Bytes of w as fp32, the sign bits flipped (0 .. 255: 128 + the value): the low bits of 2^23 + v, no conversion.
+__device__ __forceinline__ float byte_float(uint32_t w, int k) { return __fsub_rn(__uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 | k)), 8388736.0f); }
+// Nibble k of w as fp32, minus 8.
+__device__ __forceinline__ float nibble_float(uint32_t w, int k) {
+    return __fsub_rn(__uint_as_float(((w >> (4 * k)) & 15u) | 0x4B000000u), 8388616.0f);
+}
+
 // A warp takes a page of a head.  Lanes: PK pieces of 16 bytes of codes make a token (Q8_0: half a block each,
-// Q4_0: a block), 32 / PK tokens at a time; what the lanes of a piece have found is joined at the end.
+// Q4_0: a block), TOK = 32 / PK tokens at a time.  In the end the TOK lanes of a piece share its E elements out: half after half
+// is exchanged for a partner's, until each has E / TOK of them over all tokens, to quantize and store.  (Where PK is no power of two
+// the first PK lanes take all of them.)  Bound by the instructions of the expansion: four to five for an element.
 template <int TYPE, int DB>
 __global__ void __launch_bounds__(kBoundWarps * 32) cache_bounds_kernel(const BoundsParams p) {
     constexpr int CB = DB * (TYPE == QMM_Q8_0 ? 32 : 16), PK = CB / 16, TOK = 32 / PK, E = TYPE == QMM_Q8_0 ? 16 : 32, D = DB * 32;
+    constexpr bool kShare = (PK & (PK - 1)) == 0;
+    constexpr int N = kShare ? E / TOK : E;                            // elements of a lane in the end
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int lane = threadIdx.x & 31, P = 1 << p.log_p;
@@ -56,7 +67,7 @@ __global__ void __launch_bounds__(kBoundWarps * 32) cache_bounds_kernel(const Bo
     const int have = (int)min((int64_t)P, n - (number << p.log_p));
     const uint8_t *chunk = p.k_cache + cache_chunk(TYPE, p.H, D, P, page, h);
     const uint16_t *scales = reinterpret_cast<const uint16_t *>(chunk + (int64_t)P * CB);
-    const int piece = lane % PK, block = TYPE == QMM_Q8_0 ? piece / 2 : piece;
+    const int piece = lane % PK, turn = min(lane / PK, TOK - 1), block = TYPE == QMM_Q8_0 ? piece / 2 : piece;
     float lo[E], hi[E];
     bool odd = false;
 #pragma unroll
@@ -64,71 +75,97 @@ __global__ void __launch_bounds__(kBoundWarps * 32) cache_bounds_kernel(const Bo
         lo[i] = INFINITY;
         hi[i] = -INFINITY;
     }
-    for (int j = lane / PK; lane < TOK * PK && j < have; j += TOK) {
-        const uint4 c = *reinterpret_cast<const uint4 *>(chunk + (int64_t)j * CB + piece * 16);
-        const float d = __half2float(__ushort_as_half(scales[j * DB + block]));
-        odd |= !(fabsf(d) < INFINITY);
-        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
+    // tokens past the last stand for the last once more; two at a time
+    for (int j = turn; j < have; j += 2 * TOK) {
+        const int j2 = min(j + TOK, have - 1);
+        const uint4 c = *reinterpret_cast<const uint4 *>(chunk + (int64_t)j * CB + piece * 16), c2 = *reinterpret_cast<const uint4 *>(chunk + (int64_t)j2 * CB + piece * 16);
+        const float d = __half2float(__ushort_as_half(scales[j * DB + block])), d2 = __half2float(__ushort_as_half(scales[j2 * DB + block]));
+        odd |= !(fabsf(d) < INFINITY) || !(fabsf(d2) < INFINITY);
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w}, w2[4] = {c2.x, c2.y, c2.z, c2.w};
+        auto take = [&](int e, float v, float u) {
+            lo[e] = fminf(fminf(lo[e], v), u);
+            hi[e] = fmaxf(fmaxf(hi[e], v), u);
+        };
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (TYPE == QMM_Q8_0) {
+                const uint32_t x = w[i] ^ 0x80808080u, x2 = w2[i] ^ 0x80808080u;
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                if constexpr (TYPE == QMM_Q8_0) {
-                    const float v = d * (float)(int8_t)(w[i] >> (8 * k));
-                    lo[4 * i + k] = fminf(lo[4 * i + k], v);
-                    hi[4 * i + k] = fmaxf(hi[4 * i + k], v);
-                } else {
-                    const float v = d * (float)((int)((w[i] >> (8 * k)) & 15u) - 8), u = d * (float)((int)((w[i] >> (8 * k + 4)) & 15u) - 8);
-                    lo[4 * i + k] = fminf(lo[4 * i + k], v);
-                    hi[4 * i + k] = fmaxf(hi[4 * i + k], v);
-                    lo[16 + 4 * i + k] = fminf(lo[16 + 4 * i + k], u);
-                    hi[16 + 4 * i + k] = fmaxf(hi[16 + 4 * i + k], u);
+                for (int k = 0; k < 4; ++k) take(4 * i + k, d * byte_float(x, k), d2 * byte_float(x2, k));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) take(4 * i + k / 2 + 16 * (k & 1), d * nibble_float(w[i], k), d2 * nibble_float(w2[i], k));
+            }
+        }
+    }
+    // (a lane whose first token is past the last has found nothing; the others of its piece have)
+    float top = 0.0f;
+    if constexpr (kShare) {
+#pragma unroll
+        for (int m = TOK / 2, count = E / 2; m > 0; m /= 2, count /= 2) {
+            const bool upper = (turn & m) != 0;
+#pragma unroll
+            for (int i = 0; i < E / 2; ++i) {
+                if (i >= count) break;
+                const float a = __shfl_xor_sync(0xffffffffu, upper ? lo[i] : lo[i + count], m * PK);
+                const float b = __shfl_xor_sync(0xffffffffu, upper ? hi[i] : hi[i + count], m * PK);
+                lo[i] = fminf(upper ? lo[i + count] : lo[i], a);
+                hi[i] = fmaxf(upper ? hi[i + count] : hi[i], b);
+            }
+        }
+    } else {
+        for (int m = 1; m < TOK; ++m) {
+            const int src = (lane + m * PK) & 31;
+            const bool other = lane < PK;
+#pragma unroll
+            for (int i = 0; i < E; ++i) {
+                const float a = __shfl_sync(0xffffffffu, lo[i], src), b = __shfl_sync(0xffffffffu, hi[i], src);
+                if (other) {
+                    lo[i] = fminf(lo[i], a);
+                    hi[i] = fmaxf(hi[i], b);
                 }
             }
-    }
-    // ---- the lanes of a piece ----
-    for (int m = 1; m < TOK; ++m) {
-        const int src = (lane + m * PK) & 31;
-        const bool other = lane < PK;
-        odd |= __shfl_sync(0xffffffffu, (int)odd, src) && other;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const float a = __shfl_sync(0xffffffffu, lo[i], src), b = __shfl_sync(0xffffffffu, hi[i], src);
-            if (other) {
-                lo[i] = fminf(lo[i], a);
-                hi[i] = fmaxf(hi[i], b);
-            }
         }
     }
-    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < E; ++i) top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
-    if constexpr (TYPE == QMM_Q8_0) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        odd |= __shfl_xor_sync(0xffffffffu, (int)odd, 1) != 0;
+    for (int i = 0; i < N; ++i) top = fmaxf(top, fmaxf(fabsf(lo[i]), fabsf(hi[i])));
+    // over the lanes of a block: its pieces, and the turns of each
+    uint32_t worst = odd ? 0x7FC00000u : __float_as_uint(top);         // a scale that is not finite comes out on top
+    if constexpr (kShare) {
+#pragma unroll
+        for (int m = PK; m < 32; m *= 2) worst = max(worst, __shfl_xor_sync(0xffffffffu, worst, m));
+    } else {
+        uint32_t all = worst;
+        for (int m = 1; m < TOK; ++m) {
+            const uint32_t x = __shfl_sync(0xffffffffu, worst, (lane + m * PK) & 31);
+            if (x > 0x7F800000u) all = max(all, x);                    // (the others' tops are not joined yet)
+        }
+        worst = all;
     }
-    if (lane >= PK) return;
-    const __half half = odd ? __ushort_as_half(0x7E00u) : __float2half_ru(__fdiv_rn(top, 127.0f));
-    const float d = odd ? 0.0f : __half2float(half);
+    if constexpr (TYPE == QMM_Q8_0) worst = max(worst, __shfl_xor_sync(0xffffffffu, worst, 1));
+    if (!kShare && lane >= PK) return;
+    const bool bad = worst >= 0x7F800000u;
+    const __half half = bad ? __ushort_as_half(0x7E00u) : __float2half_ru(__fdiv_rn(__uint_as_float(worst), 127.0f));
+    const float d = bad ? 0.0f : __half2float(half);
     uint8_t *out = p.bounds + (page * p.H + h) * cache_bound_bytes(D);
+    const int e0 = piece * E + (kShare ? turn * N : 0);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
-        uint32_t w[E / 4];
+        int q[N < 4 ? 4 : N] = {};
 #pragma unroll
-        for (int i = 0; i < E / 4; ++i) {
-            int q[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const float v = d > 0.0f ? __fdiv_rn(x ? hi[4 * i + k] : lo[4 * i + k], d) : 0.0f;
-                q[k] = (int)fminf(fmaxf(x ? ceilf(v) : floorf(v), -127.0f), 127.0f);
-            }
-            w[i] = pack4(q);
+        for (int i = 0; i < N; ++i) {
+            const float v = d > 0.0f ? __fdiv_rn(x ? hi[i] : lo[i], d) : 0.0f;
+            q[i] = (int)fminf(fmaxf(x ? ceilf(v) : floorf(v), -127.0f), 127.0f);
         }
+        uint8_t *to = out + x * D + e0;
+        if constexpr (N == 1) *to = (uint8_t)q[0];
+        else if constexpr (N == 2) *reinterpret_cast<uint16_t *>(to) = (uint16_t)(pack4(q[0], q[1], 0, 0));
+        else {
 #pragma unroll
-        for (int i = 0; i < E / 16; ++i)
-            *reinterpret_cast<uint4 *>(out + x * D + piece * E + 16 * i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            for (int i = 0; i < N / 4; ++i) reinterpret_cast<uint32_t *>(to)[i] = pack4(q[4 * i], q[4 * i + 1], q[4 * i + 2], q[4 * i + 3]);
+        }
     }
-    if (TYPE == QMM_Q4_0 || (piece & 1) == 0) reinterpret_cast<__half *>(out + 2 * D)[block] = half;
+    if ((!kShare || turn == 0) && (TYPE == QMM_Q4_0 || (piece & 1) == 0)) reinterpret_cast<__half *>(out + 2 * D)[block] = half;
     if (lane == 0)
         for (int i = D + DB; i < cache_bound_bytes(D) / 2; ++i) reinterpret_cast<uint16_t *>(out)[i] = 0;
 }
@@ -259,97 +296,169 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 
-// Sums of v over the threads before this one, and over all.
-__device__ __forceinline__ uint32_t sums_before(uint32_t v, uint32_t *part, uint32_t &all) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t x = v;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const uint32_t y = __shfl_up_sync(0xffffffffu, x, m);
-        if (lane >= m) x += y;
-    }
-    if (lane == 31) part[warp] = x;
-    __syncthreads();
-    uint32_t before = 0;
-    all = 0;
-#pragma unroll
-    for (int w = 0; w < kChooseThreads / 32; ++w) {
-        const uint32_t y = part[w];
-        if (w < warp) before += y;
-        all += y;
-    }
-    __syncthreads();
-    return before + x - v;
-}
+constexpr int kChooseWarps = kChooseThreads / 32, kHeld = 16, kFew = 64;
 
-// A CTA takes a token and head: the rank-th largest score by four histograms of 8 bits each, then the pages above it, and
-// as many of those at it as are still wanted, the earliest first, in the order of their numbers.
+// A CTA takes a token and head.  The border, the rank-th largest score, is found in histograms of 256 bins over the range
+// of the scores that are still in question, until a bin holds a few, which are ranked against each other; then come the pages above it, and
+// as many of those at it as are still wanted, the earliest first, in the order of their numbers.  A warp has a run of neighbouring
+// pages: up to kHeld * 32 of them (HELD) stay in registers.
+template <bool HELD>
 __global__ void __launch_bounds__(kChooseThreads) cache_choose_kernel(const SelectParams p) {
-    __shared__ uint32_t hist[256], part[kChooseThreads / 32], s_prefix, s_rank;
+    __shared__ uint32_t hist[256], few[kFew], part[2][kChooseWarps], s_lo, s_rank, s_count, s_border, s_ties;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int64_t row = blockIdx.x / (unsigned)p.H;
-    const int h = (int)(blockIdx.x % (unsigned)p.H);
+    const int h = (int)(blockIdx.x % (unsigned)p.H), tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Token t;
     if (!find_token(p, row, t)) return;
     int32_t *out = p.chosen + (row * p.H + h) * p.budget;
     const int seen = (int)t.seen, budget = (int)p.budget;
     if (seen <= budget) {
-        for (int i = threadIdx.x; i < budget; i += kChooseThreads) out[i] = i < seen ? i : -1;
+        for (int i = tid; i < budget; i += kChooseThreads) out[i] = i < seen ? i : -1;
         return;
     }
     const int front = (int)min(p.sinks, t.seen), back = max(front, (int)max((int64_t)0, min(t.old, t.seen)));   // always chosen: below front, from back on
-    const int always = front + seen - back;
-    uint32_t rank = (uint32_t)max(0, budget - always);                 // of the pages front .. back - 1
+    uint32_t rank = (uint32_t)max(0, budget - (front + seen - back));  // of the pages front .. back - 1
     const float *scores = p.scores + (row * p.H + h) * p.most;
-    uint32_t prefix = 0, mask = 0;
+    const int run = (seen + kChooseThreads - 1) / kChooseThreads * 32, begin = warp * run, end = min(seen, begin + run);
+    // keys of the pages in question; 0 is no score's
+    uint32_t held[HELD ? kHeld : 1];
+    auto load = [&](int i) { return i >= front && i < back && i < end ? ordered(scores[i]) : 0u; };
+    auto each = [&](auto f) {
+        if constexpr (HELD) {
+#pragma unroll
+            for (int u = 0; u < kHeld; ++u)
+                if (begin + 32 * u < end) f(begin + 32 * u + lane, held[u]);
+        } else {
+            for (int i = begin + lane; i - lane < end; i += 32) f(i, load(i));
+        }
+    };
+    if constexpr (HELD) {
+#pragma unroll
+        for (int u = 0; u < kHeld; ++u) held[u] = load(begin + 32 * u + lane);
+    }
+    uint32_t border = 0xFFFFFFFFu, ties = 0;                           // keys above it are chosen, and so many of those at it
     if (rank > 0) {
-        for (int shift = 24; shift >= 0; shift -= 8) {
-            hist[threadIdx.x] = 0;
+        uint32_t lo = 0xFFFFFFFFu, hi = 0;
+        each([&](int, uint32_t key) {
+            if (key) {
+                lo = min(lo, key);
+                hi = max(hi, key);
+            }
+        });
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        if (lane == 0) {
+            part[0][warp] = lo;
+            part[1][warp] = hi;
+        }
+        __syncthreads();
+        lo = __reduce_min_sync(0xffffffffu, part[0][lane % kChooseWarps]);
+        hi = __reduce_max_sync(0xffffffffu, part[1][lane % kChooseWarps]);
+        while (true) {
+            // bins of 2^shift keys, 256 of which hold lo .. hi
+            const int shift = max(0, 24 - __clz(hi - lo));
+            hist[tid] = 0;
+            if (tid == 0) s_count = 0;
             __syncthreads();
-            for (int i = front + threadIdx.x; i < back; i += kChooseThreads) {
-                const uint32_t key = ordered(scores[i]);
-                if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+            each([&](int, uint32_t key) {
+                if (key >= lo && key <= hi) atomicAdd(&hist[(key - lo) >> shift], 1u);
+            });
+            __syncthreads();
+            if (warp == 0) {
+                // eight bins to a lane, from the top
+                uint32_t bin[8], sum = 0;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) sum += bin[k] = hist[255 - 8 * lane - k];
+                uint32_t before = sum;
+#pragma unroll
+                for (int m = 1; m < 32; m <<= 1) {
+                    const uint32_t y = __shfl_up_sync(0xffffffffu, before, m);
+                    if (lane >= m) before += y;
+                }
+                before -= sum;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    if (before < rank && before + bin[k] >= rank) {
+                        s_lo = lo + ((uint32_t)(255 - 8 * lane - k) << shift);
+                        s_rank = rank - before;
+                        s_border = bin[k];
+                    }
+                    before += bin[k];
+                }
             }
             __syncthreads();
-            // thread i has the bin 255 - i, so that sums before it are of larger keys
-            uint32_t all;
-            const uint32_t mine = hist[255 - threadIdx.x], before = sums_before(mine, part, all);
-            if (before < rank && before + mine >= rank) {
-                s_prefix = prefix | (uint32_t)(255 - threadIdx.x) << shift;
-                s_rank = rank - before;
-            }
-            __syncthreads();
-            prefix = s_prefix;
+            const uint32_t count = s_border;
+            lo = s_lo;
+            if (hi - lo >= 1u << shift) hi = lo + ((1u << shift) - 1);
             rank = s_rank;
-            mask |= 255u << shift;
+            if (shift == 0) {
+                border = lo;
+                ties = rank;
+                break;
+            }
+            if (count > kFew) {
+                __syncthreads();                                       // before hist is cleared
+                continue;
+            }
+            each([&](int, uint32_t key) {
+                if (key >= lo && key <= hi) few[atomicAdd(&s_count, 1u)] = key;
+            });
+            __syncthreads();
+            if (tid < (int)count) {
+                const uint32_t key = few[tid];
+                uint32_t above = 0, equal = 0;
+                for (int k = 0; k < (int)count; ++k) {
+                    above += few[k] > key;
+                    equal += few[k] == key;
+                }
+                if (above < rank && above + equal >= rank) {
+                    s_border = key;
+                    s_ties = rank - above;
+                }
+            }
+            __syncthreads();
+            border = s_border;
+            ties = s_ties;
+            break;
         }
     }
     // ---- the chosen pages, ascending ----
-    const bool some = budget > always;
-    int at = 0;
-    uint32_t ties = 0;                                                 // pages at the border so far
-    for (int base = 0; base < seen; base += kChooseThreads) {
-        const int i = base + threadIdx.x;
-        bool above = false, tie = false;
-        if (i < seen) {
-            if (i < front || i >= back) {
-                above = true;
-            } else if (some) {
-                const uint32_t key = ordered(scores[i]);
-                above = key > prefix;
-                tie = key == prefix;
-            }
-        }
-        uint32_t all, n_ties;
-        const uint32_t tie_at = ties + sums_before(tie ? 1u : 0u, part, n_ties);
-        const bool in = above || (tie && tie_at < rank);
-        const uint32_t place = sums_before(in ? 1u : 0u, part, all);
-        if (in && at + (int)place < budget) out[at + place] = i;
-        at += (int)all;
-        ties += n_ties;
+    uint32_t n_in = 0, n_ties = 0;
+    auto state = [&](int i, uint32_t key, bool &in, bool &tie) {
+        tie = key != 0 && key == border;
+        in = i < end && (i < front || i >= back || key > border);      // (a key of the pages in question is below 0xFFFFFFFF, but NaN's: +inf's)
+    };
+    each([&](int i, uint32_t key) {
+        bool in, tie;
+        state(i, key, in, tie);
+        n_in += __popc(__ballot_sync(0xffffffffu, in));
+        n_ties += __popc(__ballot_sync(0xffffffffu, tie));
+    });
+    __syncthreads();                                                   // part is read above
+    if (lane == 0) {
+        part[0][warp] = n_in;
+        part[1][warp] = n_ties;
     }
-    for (int i = min(at, budget) + threadIdx.x; i < budget; i += kChooseThreads) out[i] = -1;
+    __syncthreads();
+    uint32_t at = 0, tied = 0;                                         // chosen, and at the border, in the runs before
+    for (int w = 0; w < warp; ++w) {
+        const uint32_t more = part[1][w];
+        at += part[0][w] + min(more, ties - min(ties, tied));
+        tied += more;
+    }
+    each([&](int i, uint32_t key) {
+        bool in, tie;
+        state(i, key, in, tie);
+        const unsigned tie_mask = __ballot_sync(0xffffffffu, tie), below = (1u << lane) - 1;
+        if (tie && tied + __popc(tie_mask & below) < ties) in = true;
+        tied += __popc(tie_mask);
+        const unsigned mask = __ballot_sync(0xffffffffu, in);
+        const uint32_t to = at + __popc(mask & below);
+        if (in && to < (uint32_t)budget) out[to] = i;
+        at += __popc(mask);
+    });
+    // (as many as the budget are chosen: more pages are seen than that)
 }
 
 template <int DB>
@@ -414,7 +523,8 @@ cudaError_t launch_cache_select(const SelectParams &from, int D, cudaStream_t s)
         }
     }
     if (e != cudaSuccess) return e;
-    return launch_pdl(cache_choose_kernel, dim3((unsigned)(p.T * p.H)), kChooseThreads, 0, s, p);
+    return launch_pdl(p.most <= kHeld * kChooseThreads ? cache_choose_kernel<true> : cache_choose_kernel<false>, dim3((unsigned)(p.T * p.H)),
+                      kChooseThreads, 0, s, p);
 }
 
 QMM_DCHECK_READER(read_dcheck_cache_select)

@@ -15,64 +15,92 @@
 namespace qmm {
 namespace {
 
-// Elements at .. at + 7 of a row of n; VEC: aligned, and all there.
+// Eight elements of a row as they lie in memory (16 bits: the first four words), converted once they are needed.
+struct Raw8 {
+    uint32_t w[8];
+};
+
+// Elements at .. at + 7 of a row of n (those past its end as 0); VEC: 32-byte aligned rows, and all there.
 template <bool VEC>
-__device__ __forceinline__ void load8(float (&v)[8], const void *row, int type, int at, int n) {
+__device__ __forceinline__ void load8(Raw8 &r, const void *row, int type, int at, int n) {
     if constexpr (VEC) {
         if (type == QMM_F32) {
-            const float4 *q = reinterpret_cast<const float4 *>(static_cast<const float *>(row) + at);
-            const float4 a = q[0], b = q[1];
-            v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-            v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+            const uint4 *q = reinterpret_cast<const uint4 *>(static_cast<const float *>(row) + at);
+            const uint4 a = q[0], b = q[1];
+            r = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
         } else {
             const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(row) + at);
-            const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = type == QMM_F16 ? unpack2(w[i], __half{}) : unpack2(w[i], __nv_bfloat16{});
-                v[2 * i] = f.x;
-                v[2 * i + 1] = f.y;
-            }
+            r.w[0] = a.x; r.w[1] = a.y; r.w[2] = a.z; r.w[3] = a.w;
         }
+    } else if (type == QMM_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = at + i < n ? static_cast<const uint32_t *>(row)[at + i] : 0u;
+    } else {
+        uint32_t e[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) e[i] = at + i < n ? static_cast<const uint16_t *>(row)[at + i] : 0u;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = e[2 * i] | e[2 * i + 1] << 16;
+    }
+}
+
+// The branches on the type are taken for eight elements at a time: selects in their place, element by element, cost three
+// times the instructions of everything else.
+__device__ __forceinline__ void values8(float (&v)[8], const Raw8 &r, int type) {
+    if (type == QMM_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(r.w[i] << 16);
+            v[2 * i + 1] = __uint_as_float(r.w[i] & 0xFFFF0000u);
+        }
+    } else if (type == QMM_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r.w[i]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            v[i] = 0.0f;
-            if (at + i >= n) continue;
-            if (type == QMM_F32) v[i] = static_cast<const float *>(row)[at + i];
-            else if (type == QMM_F16) v[i] = __half2float(static_cast<const __half *>(row)[at + i]);
-            else v[i] = __bfloat162float(static_cast<const __nv_bfloat16 *>(row)[at + i]);
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = unpack2(r.w[i], __half{});
+            v[2 * i] = f.x;
+            v[2 * i + 1] = f.y;
         }
+    }
+}
+
+// v rounded to the type, as it will lie in memory.
+__device__ __forceinline__ void round8(Raw8 &r, const float (&v)[8], int type) {
+    if (type == QMM_BF16) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = pack2(v[2 * i], v[2 * i + 1], __nv_bfloat16{});
+    } else if (type == QMM_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r.w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) r.w[i] = pack2(v[2 * i], v[2 * i + 1], __half{});
     }
 }
 
 template <bool VEC>
-__device__ __forceinline__ void store8(const float (&v)[8], void *row, int type, int at, int n) {
+__device__ __forceinline__ void store8(const Raw8 &r, void *row, int type, int at, int n) {
     if constexpr (VEC) {
         if (type == QMM_F32) {
-            float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(row) + at);
-            q[0] = make_float4(v[0], v[1], v[2], v[3]);
-            q[1] = make_float4(v[4], v[5], v[6], v[7]);
+            uint4 *q = reinterpret_cast<uint4 *>(static_cast<float *>(row) + at);
+            q[0] = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
+            q[1] = make_uint4(r.w[4], r.w[5], r.w[6], r.w[7]);
         } else {
-            uint32_t w[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = type == QMM_F16 ? pack2(v[2 * i], v[2 * i + 1], __half{}) : pack2(v[2 * i], v[2 * i + 1], __nv_bfloat16{});
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + at) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(row) + at) = make_uint4(r.w[0], r.w[1], r.w[2], r.w[3]);
         }
+    } else if (type == QMM_F32) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (at + i < n) static_cast<uint32_t *>(row)[at + i] = r.w[i];
     } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            if (at + i >= n) continue;
-            if (type == QMM_F32) static_cast<float *>(row)[at + i] = v[i];
-            else if (type == QMM_F16) static_cast<__half *>(row)[at + i] = __float2half_rn(v[i]);
-            else static_cast<__nv_bfloat16 *>(row)[at + i] = __float2bfloat16_rn(v[i]);
-        }
+        for (int i = 0; i < 8; ++i)
+            if (at + i < n) static_cast<uint16_t *>(row)[at + i] = (uint16_t)(r.w[i >> 1] >> (16 * (i & 1)));
     }
 }
 
-__device__ __forceinline__ float rounded(float v, int type) {
-    return type == QMM_F32 ? v : (type == QMM_F16 ? __half2float(__float2half_rn(v)) : __bfloat162float(__float2bfloat16_rn(v)));
-}
 __device__ __forceinline__ const void *row_of(const void *p, int type, int64_t at) {
     return static_cast<const uint8_t *>(p) + at * (type == QMM_F32 ? 4 : 2);
 }
@@ -103,97 +131,125 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
     __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int t = threadIdx.x % TPR;
+    const int t = threadIdx.x % TPR, n = p.N;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (row >= p.R) return;                                            // (a whole warp)
-    const int n = p.N;
     const float inv_n = 1.0f / (float)n;
+    const void *hr = row_of(p.h, p.hdt, row * p.ldh), *xr = p.x ? row_of(p.x, p.xdt, row * p.ldx) : nullptr;
+    const void *gr = p.gate ? row_of(p.gate, p.xdt, row * p.ldg) : nullptr;
+    // of x the pieces are kept as they lie in memory; a thread of 1024 has no registers for four of them, and loads them again
+    constexpr bool kKeep = C < 4 || TPR == 32;
+    Raw8 rx[kKeep ? C : 1];
     float h[C][8];
-    const void *hr = row_of(p.h, p.hdt, row * p.ldh);
+    if (kKeep && xr) {
+#pragma unroll
+        for (int c = 0; c < C; ++c)
+            if ((c * TPR + t) * 8 < n) load8<VEC>(rx[c], xr, p.xdt, (c * TPR + t) * 8, n);
+    }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int at = (c * TPR + t) * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
-        if (at < n) load8<VEC>(h[c], hr, p.hdt, at, n);
+        if (at >= n) continue;
+        Raw8 r;
+        load8<VEC>(r, hr, p.hdt, at, n);
+        values8(h[c], r, p.hdt);
     }
-    if (p.x) {
-        // a thread of 1024 has no registers to keep 32 elements of x beside those of h: it loads them again
-        constexpr bool kKeep = C < 4 || TPR == 32;
-        float x[kKeep ? C : 1][8], sum = 0.0f;
-        const void *xr = row_of(p.x, p.xdt, row * p.ldx), *gr = p.gate ? row_of(p.gate, p.xdt, row * p.ldg) : nullptr;
-        auto load_x = [&](float (&v)[8], int at) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-            if (at < n) load8<VEC>(v, xr, p.xdt, at, n);
-        };
-        if constexpr (kKeep) {
-#pragma unroll
-            for (int c = 0; c < C; ++c) load_x(x[c], (c * TPR + t) * 8);
-        }
+    if (xr) {
         float r = 1.0f;
         if (p.w_post) {
+            float sum = 0.0f;
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                if constexpr (!kKeep) load_x(x[0], (c * TPR + t) * 8);
+                const int at = (c * TPR + t) * 8;
+                if (at >= n) continue;
+                float x[8];
+                if constexpr (!kKeep) load8<VEC>(rx[0], xr, p.xdt, at, n);
+                values8(x, rx[kKeep ? c : 0], p.xdt);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) sum += x[kKeep ? c : 0][i] * x[kKeep ? c : 0][i];
+                for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
             }
             r = 1.0f / sqrtf(row_sum<TPR>(sum, part[0]) * inv_n + p.eps);
         }
+        r *= p.scale;
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const int at = (c * TPR + t) * 8;
             if (at >= n) continue;
-            float g[8], w[8];
+            float x[8], w[8];
+            Raw8 raw;
+            if constexpr (!kKeep) load8<VEC>(rx[0], xr, p.xdt, at, n);
+            values8(x, rx[kKeep ? c : 0], p.xdt);
+            if (p.w_post) {
+                load8<VEC>(raw, p.w_post, QMM_F32, at, n);
+                values8(w, raw, QMM_F32);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) g[i] = w[i] = 1.0f;
-            if constexpr (!kKeep) load_x(x[0], at);
-            if (p.w_post) load8<VEC>(w, p.w_post, QMM_F32, at, n);
-            if (gr) load8<VEC>(g, gr, p.xdt, at, n);
+                for (int i = 0; i < 8; ++i) x[i] *= w[i];
+            }
+            if (gr) {
+                load8<VEC>(raw, gr, p.xdt, at, n);
+                values8(w, raw, p.xdt);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[c][i] = rounded(h[c][i] + p.scale * (x[kKeep ? c : 0][i] * r * w[i] * g[i]), p.hdt);
+                for (int i = 0; i < 8; ++i) x[i] *= w[i];
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[c][i] += x[i] * r;
         }
     }
-    if (p.h_out) {
-        void *out = const_cast<void *>(row_of(p.h_out, p.hdt, row * p.ldho));
-#pragma unroll
-        for (int c = 0; c < C; ++c) {
-            const int at = (c * TPR + t) * 8;
-            if (at < n && QMM_DCHECK(!VEC || at + 8 <= n)) store8<VEC>(h[c], out, p.hdt, at, n);
-        }
-    }
+    // ---- h' rounded and stored; its sum of squares ----
     float sum = 0.0f;
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int c = 0; c < C; ++c) {
+        const int at = (c * TPR + t) * 8;
+        if (at >= n) continue;
+        if (p.h_out) {
+            Raw8 r;
+            round8(r, h[c], p.hdt);
+            if (QMM_DCHECK(!VEC || at + 8 <= n)) store8<VEC>(r, const_cast<void *>(row_of(p.h_out, p.hdt, row * p.ldho)), p.hdt, at, n);
+            if (p.hdt != QMM_F32) values8(h[c], r, p.hdt);
+        }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) sum += (c * TPR + t) * 8 + i < n ? h[c][i] * h[c][i] : 0.0f;
+        for (int i = 0; i < 8; ++i) sum += VEC || at + i < n ? h[c][i] * h[c][i] : 0.0f;
+    }
     const float r = 1.0f / sqrtf(row_sum<TPR>(sum, part[1]) * inv_n + p.eps);
+    // ---- y ----
 #pragma unroll
     for (int c = 0; c < C; ++c) {
         const int at = (c * TPR + t) * 8;
         const bool in = at < n;
-        float w[8];
+        float y[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = 1.0f;
-        if (p.w_pre && in) load8<VEC>(w, p.w_pre, QMM_F32, at, n);
+        for (int i = 0; i < 8; ++i) y[i] = 0.0f;
+        if (in) {
+            float w[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) w[i] = in ? __fmul_rn(__fmul_rn(h[c][i], r), w[i]) : 0.0f;
+            for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(h[c][i], r);
+            if (p.w_pre) {
+                Raw8 raw;
+                load8<VEC>(raw, p.w_pre, QMM_F32, at, n);
+                values8(w, raw, QMM_F32);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = __fmul_rn(y[i], w[i]);
+            }
+        }
         if (p.form == kNormRows) {
-            if (in) store8<VEC>(w, const_cast<void *>(row_of(p.y, p.ydt, row * p.ldy)), p.ydt, at, n);
+            Raw8 o;
+            round8(o, y, p.ydt);
+            if (in) store8<VEC>(o, const_cast<void *>(row_of(p.y, p.ydt, row * p.ldy)), p.ydt, at, n);
             continue;
         }
         // the largest magnitude of the block of 32 that four threads hold
         uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(w[i]) & 0x7FFFFFFFu);
+        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         if (p.form == kNormQ8) {
             const float d = q8_scale(__uint_as_float(top)), id = inv_or_zero(d);
             uint32_t b[2] = {0, 0};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) b[i >> 2] |= ((uint32_t)q8_code(w[i], id) & 255u) << (8 * (i & 3));
+            for (int i = 0; i < 8; ++i) b[i >> 2] |= ((uint32_t)q8_code(y[i], id) & 255u) << (8 * (i & 3));
             if (in) {
                 *reinterpret_cast<uint2 *>(static_cast<int8_t *>(p.y) + row * n + at) = make_uint2(b[0], b[1]);
                 if ((t & 3) == 0) reinterpret_cast<__half *>(p.scales)[row * (n / 32) + at / 32] = __float2half_rn(d);
@@ -205,7 +261,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
             word |= __shfl_xor_sync(0xffffffffu, word, 4);
             word |= __shfl_xor_sync(0xffffffffu, word, 8);
             if (in) {
-                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.y) + (row * n + at) / 2) = mx4_codes8(w, e);
+                *reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(p.y) + (row * n + at) / 2) = mx4_codes8(y, e);
                 if ((t & 15) == 0) *reinterpret_cast<uint32_t *>(p.scales + mx4_scale_word(row, at >> 7, (n + 127) / 128)) = word;
             }
         }

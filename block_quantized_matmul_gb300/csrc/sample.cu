@@ -3,18 +3,20 @@
 //   those the ones before which the others sum to less than top_p of the whole, of those the ones with w >= min_p; the token
 //   is the first index at which the running sum of the kept w exceeds u times their sum.
 //
-// Every cut is a prefix of the order of z, so what is kept is "z above a border, and the t first of those at it".  The
-// border is found digit by digit of z as an ordered 32-bit number (11, 11 and 10 bits): a histogram of counts for top_k, of
-// sums of w for top_p.
+// Every cut is a prefix of one order, that of (z descending, index ascending), so what is kept is all up to a border element.
+// The border is found by a histogram of 2048 bins over the distance from the maximum, of counts for top_k and of
+// sums of w for top_p; the elements of the border's bin are then gathered in one CTA and sorted.  Where the first
+// top_k elements and the rest of their bin fit there, that CTA does all that is left with them alone.  Where a bin holds too
+// much (logits of few values, or of a scale far from the temperature's), the border is found digit by digit instead.
 //
 // Borders of sums have to fall where the formula's do, to within an error far below one token's share: fp32 sums over 10^5 tokens
-// would not do, and fp64 is too slow on this GPU for every logit.  So w is a whole number, 2^43 for the largest, computed in
-// pairs of fp32 and 64-bit integers (`weight`, within 2^-42), and all sums are sums of integers: exact, and
-// the same in any order, so histograms may be filled by atomics.
+// would not do, and fp64 is too slow on this GPU for every logit.  So w is a whole number, 2^43 for the largest (`weight`), and
+// all sums are sums of integers: exact, and the same in any order, so histograms may be filled by atomics.
 //
 // A cluster of up to 8 CTAs takes a row, each CTA a slice of it that stays in shared memory from the first pass on.  What the
-// CTAs find is exchanged through distributed shared memory: each adds up all histograms for itself, so a digit costs one cluster
-// barrier.
+// CTAs find is exchanged through distributed shared memory: each adds up all histograms for itself.
+#include <climits>
+
 #include "qmm_internal.cuh"
 
 #include "elem.cuh"
@@ -22,46 +24,59 @@
 namespace qmm {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 2048, kMaxCluster = 8;
+constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 4 * kThreads, kMaxCluster = 8;
+constexpr int kCand = 2 * kThreads;         // elements that one CTA sorts
 constexpr int kOne = 43;                    // w of the largest logit is 2^kOne
+constexpr int kPowers = 2048;
 
-// 2^(j / 1024) times 2^kOne, from the square roots of 2: ten factors at most, each within 2^-52.
+// 2^(j / kPowers) times 2^kOne, from the square roots of 2: eleven factors at most, each within 2^-52.
 struct Powers {
-    uint64_t v[1024];
+    uint64_t v[kPowers];
 };
 constexpr Powers make_powers() {
-    double root[10] = {};
+    double root[11] = {};
     double x = 2.0;
-    for (int i = 0; i < 10; ++i) {
+    for (int i = 0; i < 11; ++i) {
         double r = 1.0 + (x - 1.0) / 2;     // Newton's iteration for the square root of x, 1 < x <= 2
         for (int k = 0; k < 6; ++k) r = 0.5 * (r + x / r);
         root[i] = x = r;
     }
     Powers p = {};
-    for (int j = 0; j < 1024; ++j) {
+    for (int j = 0; j < kPowers; ++j) {
         double v = 1.0;
-        for (int i = 0; i < 10; ++i)
-            if (j & (512 >> i)) v *= root[i];
+        for (int i = 0; i < 11; ++i)
+            if (j & (kPowers / 2 >> i)) v *= root[i];
         p.v[j] = (uint64_t)(v * (double)((uint64_t)1 << kOne) + 0.5);
     }
     return p;
 }
 __device__ const Powers g_powers = make_powers();
 
-struct alignas(16) Shared {
-    uint64_t powers[1024];
-    uint32_t lo[2][kBins], hi[2][kBins];    // a histogram of counts (lo), or of sums in two words, of this CTA's slice
-    uint64_t seg_sum[kWarps];               // of each warp's segment: sum of w above the border, and how many are at it
-    uint32_t seg_ties[kWarps];
-    uint64_t part[kWarps];
-    float top, ch, cl;                      // the slice's maximum; log2(e) / temperature in two terms
+// What the CTAs of a row share about it.
+struct Row {
+    float top, scale;                       // largest logit; bins of a histogram for a unit of distance from it
+    float ch, cl;                           // c = log2(e) / temperature in two terms
+    float y0, gh, gl;                       // top * c; what is left of it above y0's multiple n0 of 1 / kPowers, in two terms
+    int n0;
+    int wide;                               // too far apart for `weight`'s short way
     uint64_t least;                         // w that min_p asks for
+};
+
+struct alignas(16) Shared {
+    uint32_t powers[kPowers];               // g_powers in units of 2^-30
+    uint32_t lo[kBins], hi[kBins];          // a histogram of this CTA's slice: counts (lo), or sums in two words
+    uint64_t cand[kCand];                   // of the row's first CTA: gathered elements, ~ordered(z) << 32 | index
+    uint32_t n_cand;
+    uint64_t seg_sum[kWarps];               // sum of the kept w of each warp's segment
+    uint64_t part[kWarps];
+    float top, bottom;                      // the slice's largest, and smallest finite, logit
+    int first;
+    Row row;
     // what one thread finds for all
-    uint32_t prefix;
-    uint64_t left, all;
+    int bin;
+    uint64_t left, upto, border;
     int seg;
     uint64_t target;
-    uint64_t quota;
 };
 
 __device__ __forceinline__ void cluster_sync() {
@@ -89,33 +104,64 @@ __device__ __forceinline__ uint4 remote_u128(const void *p, int rank) {
     asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(remote(p, rank)) : "memory");
     return v;
 }
+__device__ __forceinline__ uint32_t remote_add(const void *p, int rank, uint32_t v) {
+    uint32_t old;
+    asm volatile("atom.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(remote(p, rank)), "r"(v) : "memory");
+    return old;
+}
+__device__ __forceinline__ void remote_store(const void *p, int rank, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(remote(p, rank)), "l"(v) : "memory");
+}
 
 __device__ __forceinline__ uint32_t ordered(float v) {
     const uint32_t b = __float_as_uint(v);
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+// An element's place in the order: the smaller the earlier.
+__device__ __forceinline__ uint64_t place_of(float z, int index) { return (uint64_t)~ordered(z) << 32 | (uint32_t)index; }
+__device__ __forceinline__ float logit_of(uint64_t place) { return unordered(~(uint32_t)(place >> 32)); }
 
-// w of logit z under the maximum m: 2^kOne * 2^y, y = (z - m) * (ch + cl), to the nearest whole number but for 2^-42 of itself.
-// z - m and the product are pairs of fp32 (46 bits or more); y = n / 1024 + g, |g| <= 1/2048, and 2^g - 1 = t + t^2/2 + t^3/6
-// with t = g ln 2 in two terms (the next term is below 2^-50), as a whole number of 2^-42.
-__device__ __forceinline__ uint64_t weight(float z, float m, float ch, float cl, const uint64_t *powers) {
-    if (z == m) return (uint64_t)1 << kOne;
-    const float hi = __fsub_rn(z, m), b = __fsub_rn(hi, z), lo = __fadd_rn(__fsub_rn(z, __fsub_rn(hi, b)), __fsub_rn(-m, b));
+// w of a logit whose distance from the largest is small, or whatever it is: z - top and its product with c as pairs of fp32.
+__device__ __noinline__ uint64_t weight_long(float z, float top, float ch, float cl) {
+    if (z == top) return (uint64_t)1 << kOne;
+    const float hi = __fsub_rn(z, top), b = __fsub_rn(hi, z), lo = __fadd_rn(__fsub_rn(z, __fsub_rn(hi, b)), __fsub_rn(-top, b));
     const float yh = __fmul_rn(hi, ch), yl = __fadd_rn(__fmaf_rn(hi, ch, -yh), __fmaf_rn(hi, cl, __fmul_rn(lo, ch)));
     if (!(yh > -(float)(kOne + 1))) return 0;                          // (and for z = -inf)
-    const float magic = 12582912.0f, r = __fmaf_rn(yh, 1024.0f, magic);
-    const int n = __float_as_int(r) - __float_as_int(magic);
-    const float g = __fmaf_rn(__fsub_rn(r, magic), -1.0f / 1024.0f, yh);
+    const float magic = 12582912.0f, k = __fmaf_rn(yh, (float)kPowers, magic);
+    const int n = __float_as_int(k) - __float_as_int(magic);
+    const float g = __fmaf_rn(__fsub_rn(k, magic), -1.0f / kPowers, yh);
     const float ln2h = 0.693147182464599609375f, ln2l = -1.9046542943909386e-9f;      // ln 2 and what fp32 leaves of it
     const float th = __fmul_rn(g, ln2h), tl = __fadd_rn(__fmaf_rn(g, ln2h, -th), __fmaf_rn(g, ln2l, __fmul_rn(yl, ln2h)));
     const float t = __fadd_rn(th, tl), small = __fmaf_rn(__fmul_rn(t, t), __fmaf_rn(t, 1.0f / 6.0f, 0.5f), tl);
     const float unit = 4398046511104.0f;                               // 2^42
     const int p = __float2int_rn(__fmul_rn(th, unit)) + __float2int_rn(__fmul_rn(small, unit));
-    const uint64_t base = powers[n & 1023];
+    const uint64_t base = g_powers.v[n & (kPowers - 1)];
     const uint64_t w = base + (uint64_t)(((int64_t)p * (int64_t)(int32_t)(base >> 13)) >> 29);
-    const int down = -(n >> 10);                                       // 0 .. kOne + 1
+    const int down = -(n >> 11);                                       // 0 .. kOne + 1
     return down <= 0 ? w : (w + ((uint64_t)1 << (down - 1))) >> down;
+}
+
+// w of logit z: 2^kOne * 2^y, y = (z - top) * c, to the nearest whole number but for 2^-34 of itself.
+// Below 2^-14 of the largest (all but 2^14 logits at most, and mostly a few) 30 bits hold what of w counts: y = z c - top c =
+// n / kPowers + f with |f| <= 1 / kPowers, where the multiple of 1 / kPowers and the rest are taken apart for z c (a
+// product in two terms) and for top c (once a row); 2^f - 1 = t + t^2/2 + t^3/6, t = f ln 2 (the next term is 2^-50),
+// is multiplied on as a whole number of 2^-32.  Half the instructions of the long way, which takes the rest.
+__device__ __forceinline__ uint64_t weight(const Row &r, float z, const uint32_t *powers) {
+    const float yh = __fmul_rn(z, r.ch), y = __fsub_rn(yh, r.y0);
+    if (r.wide || !(y < -14.25f)) return weight_long(z, r.top, r.ch, r.cl);
+    if (!(y > -(float)(kOne + 1) - 0.25f)) return 0;
+    const float yl = __fmaf_rn(z, r.cl, __fmaf_rn(z, r.ch, -yh));
+    const float magic = 12582912.0f, k = __fmaf_rn(yh, (float)kPowers, magic);
+    const float g = __fmaf_rn(__fsub_rn(k, magic), -1.0f / kPowers, yh);
+    const float t = __fmul_rn(__fadd_rn(__fsub_rn(g, r.gh), __fsub_rn(yl, r.gl)), 0.693147182464599609375f);
+    const float p = __fmaf_rn(__fmul_rn(t, t), __fmaf_rn(t, 1.0f / 6.0f, 0.5f), t);
+    const int q = __float_as_int(__fmaf_rn(p, 4294967296.0f, magic)) - __float_as_int(magic);
+    const int n = __float_as_int(k) - __float_as_int(magic) - r.n0;
+    const uint32_t base = powers[n & (kPowers - 1)], w = base + (uint32_t)__mulhi((int)base, q);
+    uint32_t a;
+    asm("shr.u32 %0, %1, %2;" : "=r"(a) : "r"(w), "r"(-(n >> 11) - 14));      // (by 32 and more: 0)
+    return (a >> 1) + (a & 1);
 }
 
 // ceil or floor of f * x for 0 <= f <= 1.
@@ -148,45 +194,76 @@ __device__ __forceinline__ uint64_t sums_before(uint64_t v, uint64_t *part, uint
     }
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    uint64_t before = 0;
-    all = 0;
+    uint64_t s = lane < kWarps ? part[lane] : 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        const uint64_t y = part[w];
-        if (w < warp) before += y;
-        all += y;
+    for (int m = 1; m < kWarps; m <<= 1) {
+        const uint64_t y = __shfl_up_sync(0xffffffffu, s, m);
+        if (lane >= m) s += y;
     }
+    all = __shfl_sync(0xffffffffu, s, kWarps - 1);
+    const uint64_t before = __shfl_sync(0xffffffffu, s, warp ? warp - 1 : 0);
     __syncthreads();
-    return before + x - v;
+    return (warp ? before : 0) + x - v;
+}
+
+// a[0 .. n) ascending, by the whole CTA; n <= kCand, room for the next power of two.
+__device__ __forceinline__ void sort(uint64_t *a, int n) {
+    int n2 = 2;
+    while (n2 < n) n2 *= 2;
+    for (int i = n + (int)threadIdx.x; i < n2; i += kThreads) a[i] = ~(uint64_t)0;
+    __syncthreads();
+    for (int size = 2; size <= n2; size *= 2)
+        for (int half = size / 2; half > 0; half /= 2) {
+            const int i = (int)threadIdx.x / half * 2 * half + (int)threadIdx.x % half, j = i + half;
+            if (j < n2) {
+                const uint64_t x = a[i], y = a[j];
+                if ((x > y) == ((i & size) == 0)) {
+                    a[i] = y;
+                    a[j] = x;
+                }
+            }
+            __syncthreads();
+        }
 }
 
 // STAGED: the slice lies in shared memory after the first pass, otherwise it is read again each time.
 template <typename T, bool STAGED>
-__global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, int ctas, int per, int vec) {
-    constexpr int kLevels = sizeof(T) == 4 ? 3 : 2;                    // 16-bit logits as fp32 end within 22 bits
-    constexpr uint32_t kKey = sizeof(T) == 4 ? 0xFFFFFFFFu : 0xFFFFFC00u;
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int ctas, int per, int vec) {
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     T *stage = reinterpret_cast<T *>(smem + sizeof(Shared));
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, rank = (int)(blockIdx.x % (unsigned)ctas);
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)(blockIdx.x % (unsigned)ctas);
     const int64_t row = blockIdx.x / (unsigned)ctas;
-    for (int i = threadIdx.x; i < 1024; i += kThreads) sh.powers[i] = g_powers.v[i];
-    for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[0][i] = sh.lo[1][i] = sh.hi[0][i] = sh.hi[1][i] = 0;
+    for (int i = tid; i < kPowers; i += kThreads) sh.powers[i] = (uint32_t)(g_powers.v[i] >> (kOne - 30));
+    if (tid == 0) {
+        sh.n_cand = 0;
+        sh.seg = -1;
+    }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    auto barrier = [&] {
+        if (ctas > 1) cluster_sync();
+        else __syncthreads();
+    };
     const int from = min(rank * per, p.V), n = min(per, p.V - from);
     const T *src = static_cast<const T *>(p.logits) + row * p.ld + from;
     // NaN counts as -inf, -0 as 0
-    auto clean = [](float v) { return isnan(v) ? -INFINITY : v + 0.0f; };
-    auto logit = [&](int i) { return clean(elem_to_float(STAGED ? stage[i] : src[i])); };
+    auto logit = [&](int i) {
+        const float v = elem_to_float(STAGED ? stage[i] : src[i]);
+        return isnan(v) ? -INFINITY : v + 0.0f;
+    };
 
-    // ---- the first pass: the slice to shared memory, its maximum ----
-    float top = -INFINITY;
+    // ---- the first pass: the slice to shared memory, its largest and smallest finite logit ----
+    float top = -INFINITY, bottom = INFINITY;
+    auto look = [&](float v) {                                         // (fmaxf and fminf pass over NaN)
+        top = fmaxf(top, v);
+        bottom = fminf(bottom, v == -INFINITY ? INFINITY : v);
+    };
     constexpr int kVec = 16 / (int)sizeof(T), kAhead = 4;
     int done = 0;
     if (vec) {
         const int pieces = n / kVec;
-        for (int i = threadIdx.x; i < pieces; i += kThreads * kAhead) {
+        for (int i = tid; i < pieces; i += kThreads * kAhead) {
             uint4 v[kAhead];
 #pragma unroll
             for (int u = 0; u < kAhead; ++u)
@@ -197,244 +274,345 @@ __global__ void __launch_bounds__(kThreads) sample_kernel(const SampleParams p, 
                 if constexpr (STAGED) reinterpret_cast<uint4 *>(stage)[i + u * kThreads] = v[u];
                 const T *e = reinterpret_cast<const T *>(&v[u]);
 #pragma unroll
-                for (int k = 0; k < kVec; ++k) top = fmaxf(top, elem_to_float(e[k]));      // (fmaxf passes over NaN)
+                for (int k = 0; k < kVec; ++k) look(elem_to_float(e[k]));
             }
         }
         done = pieces * kVec;
     }
-    for (int i = done + threadIdx.x; i < n; i += kThreads) {
+    for (int i = done + tid; i < n; i += kThreads) {
         const T v = src[i];
         if constexpr (STAGED) stage[i] = v;
-        top = fmaxf(top, elem_to_float(v));
+        look(elem_to_float(v));
     }
 #pragma unroll
-    for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-    if (lane == 0) sh.part[warp] = __float_as_uint(top);
+    for (int m = 16; m > 0; m >>= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+        bottom = fminf(bottom, __shfl_xor_sync(0xffffffffu, bottom, m));
+    }
+    if (lane == 0) sh.part[warp] = (uint64_t)__float_as_uint(top) << 32 | __float_as_uint(bottom);
     const float temperature = p.temperature ? p.temperature[row] : 1.0f, top_p = p.top_p ? p.top_p[row] : 1.0f, min_p = p.min_p ? p.min_p[row] : 0.0f;
     const int top_k = p.top_k ? p.top_k[row] : 0;
-    if (threadIdx.x == 0) {
-        const double c = 1.4426950408889634074 / (double)temperature;
-        sh.ch = (float)c;
-        sh.cl = fabsf(sh.ch) < INFINITY ? (float)(c - (double)sh.ch) : 0.0f;
-        sh.least = min_p > 0.0f && min_p <= 1.0f ? (uint64_t)ceil((double)min_p * (double)((uint64_t)1 << kOne)) : 0;
-    }
+    const float u = p.u[row];
     __syncthreads();
     if (warp == 0) {
-        top = lane < kWarps ? __uint_as_float((uint32_t)sh.part[lane]) : -INFINITY;
+        const uint64_t both = sh.part[lane % kWarps];
+        top = __uint_as_float((uint32_t)(both >> 32));
+        bottom = __uint_as_float((uint32_t)both);
 #pragma unroll
-        for (int m = 16; m > 0; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        if (lane == 0) sh.top = top;
+        for (int m = kWarps / 2; m > 0; m >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+            bottom = fminf(bottom, __shfl_xor_sync(0xffffffffu, bottom, m));
+        }
+        if (lane == 0) {
+            sh.top = top;
+            sh.bottom = bottom;
+        }
+    }
+    barrier();
+    if (warp == 0) {
+        top = lane < ctas ? __uint_as_float(remote_u32(&sh.top, lane)) : -INFINITY;
+        bottom = lane < ctas ? __uint_as_float(remote_u32(&sh.bottom, lane)) : INFINITY;
+#pragma unroll
+        for (int m = kMaxCluster / 2; m > 0; m >>= 1) {
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+            bottom = fminf(bottom, __shfl_xor_sync(0xffffffffu, bottom, m));
+        }
+        if (lane == 0) {
+            Row &r = sh.row;
+            const double c = 1.4426950408889634074 / (double)temperature, y0 = (double)(top + 0.0f) * c;
+            r.top = top + 0.0f;
+            r.scale = (float)(kBins - 1) / fminf(__fsub_rn(top, bottom), 64.0f * fmaxf(1.0f, temperature));   // (bottom = inf: 0 or less)
+            r.ch = (float)c;
+            r.cl = fabsf(r.ch) < INFINITY ? (float)(c - (double)r.ch) : 0.0f;
+            r.y0 = (float)y0;
+            r.wide = !(fabs(y0) < 900.0);
+            const double n0 = r.wide ? 0.0 : rint(y0 * kPowers), g = y0 - n0 / kPowers;
+            r.n0 = (int)n0;
+            r.gh = (float)g;
+            r.gl = (float)(g - (double)r.gh);
+            r.least = min_p > 0.0f && min_p <= 1.0f ? (uint64_t)ceil((double)min_p * (double)((uint64_t)1 << kOne)) : 0;
+        }
     }
     __syncthreads();
-    if (ctas > 1) cluster_sync();
-    top = -INFINITY;
-    for (int c = 0; c < ctas; ++c) top = fmaxf(top, __uint_as_float(remote_u32(&sh.top, c)));
-    const float m = top + 0.0f, ch = sh.ch, cl = sh.cl;
-    const bool nothing = m == -INFINITY;
-    const uint64_t least = nothing ? ~(uint64_t)0 : sh.least;            // (nothing is kept of nothing)
+    const Row r = sh.row;
+    auto write = [&](int index, float z, uint64_t total) {
+        if (!QMM_DCHECK(index >= 0 && index < p.V)) return;
+        p.tokens[row] = index;
+        if (!p.logp) return;
+        const double y = z == r.top ? 0.0 : ((double)z - (double)r.top) / (double)temperature;
+        p.logp[row] = (float)(y - log((double)total * (1.0 / (double)((uint64_t)1 << kOne))));
+    };
 
-    // ---- what is kept: keys above `border`, and the first `quota` of those at it ----
-    uint32_t border = 0;                                               // no logit's key but -inf's, whose w is 0, is as low
-    uint64_t quota = 0;
-    const bool first_only = !(temperature > 0.0f) || top_k == 1 || min_p > 1.0f || top_p <= 0.0f;
-    int round = 0;                                                     // histograms so far: they use two buffers in turn
-    // Adds up the CTAs' histograms and finds the bin in which the sum from above reaches `want`; sh.prefix: the
-    // bin, sh.left: what is wanted of it.  want(all) gives the sum that is wanted.
-    auto find_bin = [&](bool sums, auto want) {
-        const int buf = round & 1;
-        ++round;
+    if (r.top == -INFINITY || !(temperature > 0.0f) || top_k == 1 || min_p > 1.0f || top_p <= 0.0f) {
+        // ---- the first in rank alone, or nothing ----
+        int first = INT_MAX;
+        for (int i = tid; i < n; i += kThreads)
+            if (logit(i) == r.top) first = min(first, from + i);
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (tid == 0) sh.first = INT_MAX;
         __syncthreads();
-        if (ctas > 1) cluster_sync();
-        uint64_t bin[4] = {0, 0, 0, 0};                                // 4 i .. 4 i + 3 from the top
-        const int at = kBins - 4 - 4 * (int)threadIdx.x;
-        for (int c = 0; c < ctas; ++c) {
-            const uint4 lo = remote_u128(&sh.lo[buf][at], c);
-            bin[3] += lo.x; bin[2] += lo.y; bin[1] += lo.z; bin[0] += lo.w;
-            if (sums) {
-                const uint4 hi = remote_u128(&sh.hi[buf][at], c);
-                bin[3] += (uint64_t)hi.x << 32; bin[2] += (uint64_t)hi.y << 32; bin[1] += (uint64_t)hi.z << 32; bin[0] += (uint64_t)hi.w << 32;
+        if (lane == 0) atomicMin(&sh.first, first);
+        __syncthreads();
+        barrier();
+        if (rank == 0 && warp == 0) {
+            first = lane < ctas ? (int)remote_u32(&sh.first, lane) : INT_MAX;
+            first = __reduce_min_sync(0xffffffffu, first);
+            if (lane == 0) {
+                p.tokens[row] = r.top == -INFINITY ? -1 : first;
+                if (p.logp) p.logp[row] = r.top == -INFINITY ? -INFINITY : 0.0f;
             }
         }
-        // the buffer of the round before is read by nobody any more: zeros for the next round
-        for (int i = threadIdx.x; i < kBins; i += kThreads) sh.lo[buf ^ 1][i] = sh.hi[buf ^ 1][i] = 0;
-        uint64_t all;
-        uint64_t before = sums_before(bin[0] + bin[1] + bin[2] + bin[3], sh.part, all);
+        barrier();                                                     // nobody leaves while its memory is read
+        return;
+    }
+
+    // ---- what is kept: places up to `border` ----
+    uint64_t border = ~(uint64_t)0;
+    auto kept = [&](float z, int i) { return place_of(z, from + i) <= border; };
+    auto clear = [&] {
+        for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
+        __syncthreads();
+    };
+    auto add = [&](int bin, uint64_t w) {
+        const uint32_t x = (uint32_t)w, old = atomicAdd(&sh.lo[bin], x), up = (uint32_t)(w >> 32) + (old + x < x ? 1u : 0u);
+        if (up) atomicAdd(&sh.hi[bin], up);
+    };
+    // Adds up the CTAs' histograms and finds the bin in which the sum from bin 0 on reaches want(sum of all): sh.bin, what is
+    // wanted of it sh.left, and the sum up to its end sh.upto.
+    auto find_bin = [&](bool sums, auto want) {
+        __syncthreads();
+        barrier();
+        uint64_t bin[4] = {0, 0, 0, 0};
+        for (int c = 0; c < ctas; ++c) {
+            const uint4 lo = remote_u128(&sh.lo[4 * tid], c);
+            bin[0] += lo.x; bin[1] += lo.y; bin[2] += lo.z; bin[3] += lo.w;
+            if (sums) {
+                const uint4 hi = remote_u128(&sh.hi[4 * tid], c);
+                bin[0] += (uint64_t)hi.x << 32; bin[1] += (uint64_t)hi.y << 32; bin[2] += (uint64_t)hi.z << 32; bin[3] += (uint64_t)hi.w << 32;
+            }
+        }
+        uint64_t all, before = sums_before(bin[0] + bin[1] + bin[2] + bin[3], sh.part, all);
         const uint64_t w = want(all);
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             if (before < w && before + bin[k] >= w) {
-                sh.prefix = (uint32_t)(kBins - 1 - 4 * (int)threadIdx.x - k);
+                sh.bin = 4 * tid + k;
                 sh.left = w - before;
+                sh.upto = before + bin[k];
             }
             before += bin[k];
         }
         __syncthreads();
     };
-    constexpr int kShift[3] = {21, 10, 0};
-    if (first_only) {
-        border = ordered(m) & kKey;
-        quota = 1;
-    } else if (!nothing) {
-        if (top_k > 0 && top_k < p.V) {
-            uint64_t left = (uint64_t)top_k;
-            uint32_t prefix = 0, mask = 0;
-#pragma unroll
-            for (int level = 0; level < kLevels; ++level) {
-                uint32_t *hist = sh.lo[round & 1];
-                const int shift = kShift[level], bits = level == 2 ? 10 : 11;
-                for (int i = threadIdx.x; i < n; i += kThreads) {
-                    const uint32_t key = ordered(logit(i));
-                    if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & ((1u << bits) - 1)], 1u);
-                }
-                find_bin(false, [&](uint64_t) { return left; });
-                prefix |= sh.prefix << shift;
-                mask |= ((1u << bits) - 1) << shift;
-                left = sh.left;
+    // The bin of a logit by its distance from the largest: subtraction and product are monotonic, so bins follow the order.
+    auto bin_of = [&](float z) { return min(kBins - 1, __float2int_rz(__fmul_rn(__fsub_rn(r.top, z), r.scale))); };   // (NaN gives bin 0: inf - inf)
+    // The kept elements of bins first .. last to the first CTA (at most kCand of them; all are counted).
+    auto gather = [&](int first, int last) {
+        for (int base = 0; base < n; base += kThreads) {
+            const int i = base + tid;
+            float z = 0.0f;
+            bool in = false;
+            if (i < n) {
+                z = logit(i);
+                const int b = bin_of(z);
+                in = b >= first && b <= last && kept(z, i);
             }
-            border = prefix;
-            quota = left;
+            const unsigned who = __ballot_sync(0xffffffffu, in);
+            if (who == 0) continue;
+            uint32_t at = 0;
+            if (lane == 0) at = remote_add(&sh.n_cand, 0, (uint32_t)__popc(who));
+            at = __shfl_sync(0xffffffffu, at, 0) + (uint32_t)__popc(who & ((1u << lane) - 1));
+            if (in && at < kCand) remote_store(&sh.cand[at], 0, place_of(z, from + i));
         }
-        if (top_p < 1.0f) {
-            // the ones at the border of top_k count as one element of their common w
-            const uint32_t kth = border;
-            const uint64_t kth_quota = quota;
-            const float kth_z = unordered(kKey != 0xFFFFFFFFu && !(kth & 0x80000000u) ? kth | ~kKey : kth);
-            uint64_t left = 0;
-            uint32_t prefix = 0, mask = 0;
+        __syncthreads();
+        barrier();
+    };
+    // The border among the gathered: the left-th of them, or the one at which the sum of w reaches `left`.
+    auto border_of_gathered = [&](bool sums, uint64_t left) {
+        if (rank == 0) {
+            const int m = (int)sh.n_cand;
+            sort(sh.cand, m);
+            if (sums) {
+                uint64_t w[2], all;
 #pragma unroll
-            for (int level = 0; level < kLevels; ++level) {
-                uint32_t *lo = sh.lo[round & 1], *hi = sh.hi[round & 1];
-                const int shift = kShift[level], bits = level == 2 ? 10 : 11;
-                auto add = [&](uint32_t key, uint64_t w) {
-                    const uint32_t bin = (key >> shift) & ((1u << bits) - 1), x = (uint32_t)w, old = atomicAdd(&lo[bin], x);
-                    const uint32_t up = (uint32_t)(w >> 32) + (old + x < x ? 1u : 0u);
-                    if (up) atomicAdd(&hi[bin], up);
-                };
-                for (int i = threadIdx.x; i < n; i += kThreads) {
-                    const float z = logit(i);
-                    const uint32_t key = ordered(z);
-                    if ((key & mask) != prefix || (key & kKey) <= kth) continue;
-                    const uint64_t w = weight(z, m, ch, cl, sh.powers);
-                    if (w) add(key, w);
+                for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < m ? weight(r, logit_of(sh.cand[2 * tid + k]), sh.powers) : 0;
+                uint64_t before = sums_before(w[0] + w[1], sh.part, all);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    if (before < left && before + w[k] >= left) sh.border = sh.cand[2 * tid + k];
+                    before += w[k];
                 }
-                if (rank == 0 && threadIdx.x == 0 && kth_quota && (kth & mask) == prefix) {
-                    const uint64_t w = kth_quota * weight(kth_z, m, ch, cl, sh.powers);
-                    if (w) add(kth, w);
-                }
-                if (level == 0) {
-                    find_bin(true, [&](uint64_t all) {
-                        const uint64_t w = times(top_p, all, true);
-                        return w ? w : (uint64_t)1;
-                    });
-                } else {
-                    find_bin(true, [&](uint64_t) { return left; });
-                }
-                prefix |= sh.prefix << shift;
-                mask |= ((1u << bits) - 1) << shift;
-                left = sh.left;
+            } else if (tid == 0) {
+                sh.border = sh.cand[(int)left - 1];
             }
-            border = prefix;
-            const float z = unordered(kKey != 0xFFFFFFFFu && !(prefix & 0x80000000u) ? prefix | ~kKey : prefix);
-            const uint64_t w = weight(z, m, ch, cl, sh.powers);
-            quota = w ? (left + w - 1) / w : 1;
+            if (tid == 0) sh.n_cand = 0;
+            __syncthreads();
+        }
+        barrier();
+        border = remote_u64(&sh.border, 0);
+    };
+    // The border by the digits of the places, 11, 11 and 10 bits of the logit and twice 10 of the index: whatever the logits.
+    auto border_by_digits = [&](bool sums, uint64_t left) {
+        constexpr int kShift[5] = {53, 42, 32, 10, 0}, kBits[5] = {11, 11, 10, 10, 10};
+        uint64_t prefix = 0, mask = 0;
+        const uint64_t old = border;
+        for (int digit = 0; digit < 5; ++digit) {
+            const uint32_t low = (1u << kBits[digit]) - 1;
+            clear();
+            for (int i = tid; i < n; i += kThreads) {
+                const float z = logit(i);
+                const uint64_t place = place_of(z, from + i);
+                if ((place & mask) != prefix || place > old) continue;
+                const int bin = (int)((place >> kShift[digit]) & low);
+                if (!sums) {
+                    atomicAdd(&sh.lo[bin], 1u);
+                } else {
+                    const uint64_t w = weight(r, z, sh.powers);
+                    if (w) add(bin, w);
+                }
+            }
+            find_bin(sums, [&](uint64_t) { return left; });
+            prefix |= (uint64_t)(uint32_t)sh.bin << kShift[digit];
+            mask |= (uint64_t)low << kShift[digit];
+            left = sh.left;
+            if (sums && digit == 2) {
+                // the logit is found: of its equals so many are kept
+                const uint64_t w = weight(r, logit_of(prefix), sh.powers);
+                left = w ? (left + w - 1) / w : 1;
+                sums = false;
+            }
+            barrier();                                                 // before the histograms are cleared
+        }
+        border = prefix;
+    };
+
+    if (top_k > 0 && top_k < p.V) {
+        clear();
+        for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.lo[bin_of(logit(i))], 1u);
+        find_bin(false, [&](uint64_t) { return (uint64_t)top_k; });
+        const int bin = sh.bin;
+        const uint64_t left = sh.left, upto = sh.upto;
+        if (upto <= kCand) {
+            // ---- the first CTA alone: cuts in the order of the logits, then the token in the order of the indexes ----
+            gather(0, bin);
+            if (rank != 0) return;
+            uint64_t *ws = reinterpret_cast<uint64_t *>(sh.lo), *order = reinterpret_cast<uint64_t *>(sh.hi);
+            sort(sh.cand, (int)upto);
+            uint64_t w[2], all, total;
+#pragma unroll
+            for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < top_k && 2 * tid + k < (int)upto ? weight(r, logit_of(sh.cand[2 * tid + k]), sh.powers) : 0;
+            uint64_t before = sums_before(w[0] + w[1], sh.part, all);
+            const uint64_t want = top_p < 1.0f ? max((uint64_t)1, times(top_p, all, true)) : ~(uint64_t)0;
+            int mine = 0;                                              // kept of this thread's two
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int i = 2 * tid + k;
+                if (i < top_k && i < (int)upto && before < want && (i == 0 || w[k] >= r.least)) {
+                    ws[i] = w[k];
+                    order[i] = (uint64_t)(uint32_t)sh.cand[i] << 32 | (uint32_t)i;
+                    ++mine;
+                }
+                before += w[k];
+            }
+            const int m = __syncthreads_count(mine >= 1) + __syncthreads_count(mine >= 2);
+            sort(order, m);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < m ? ws[(uint32_t)order[2 * tid + k]] : 0;
+            before = sums_before(w[0] + w[1], sh.part, total);
+            const uint64_t target = u >= 1.0f ? total - 1 : (u > 0.0f ? times(u, total, false) : 0);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (before <= target && target < before + w[k]) {
+                    const uint64_t place = sh.cand[(uint32_t)order[2 * tid + k]];
+                    write((int)(uint32_t)place, logit_of(place), total);
+                }
+                before += w[k];
+            }
+            return;
+        }
+        // (the elements of the bin: what lies in it, of the counts up to its end)
+        gather(bin, bin);
+        if (remote_u32(&sh.n_cand, 0) <= kCand) {
+            barrier();                                                 // the count is read before it is cleared
+            border_of_gathered(false, left);
+        } else {
+            barrier();
+            if (rank == 0 && tid == 0) sh.n_cand = 0;
+            border_by_digits(false, (uint64_t)top_k);
+        }
+    }
+    if (top_p < 1.0f) {
+        clear();
+        for (int i = tid; i < n; i += kThreads) {
+            const float z = logit(i);
+            if (!kept(z, i)) continue;
+            const uint64_t w = weight(r, z, sh.powers);
+            if (w) add(bin_of(z), w);
+        }
+        uint64_t want = 0;
+        find_bin(true, [&](uint64_t all) { return want = max((uint64_t)1, times(top_p, all, true)); });
+        const int bin = sh.bin;
+        const uint64_t left = sh.left;
+        gather(bin, bin);
+        if (remote_u32(&sh.n_cand, 0) <= kCand) {
+            barrier();
+            border_of_gathered(true, left);
+        } else {
+            barrier();
+            border_by_digits(true, want);
         }
     }
 
     // ---- sums of the warps' segments, in the order of the indexes ----
-    const float border_z = border == 0 ? -INFINITY : unordered(kKey != 0xFFFFFFFFu && !(border & 0x80000000u) ? border | ~kKey : border);
-    uint64_t at_border = border == 0 ? 0 : weight(border_z, m, ch, cl, sh.powers);
-    if (at_border < least) at_border = 0;
     const int seg_len = (per + kWarps * 32 - 1) / (kWarps * 32) * 32;
+    auto weight_of = [&](int i) -> uint64_t {
+        const float z = logit(i);
+        if (!kept(z, i)) return 0;
+        const uint64_t w = weight(r, z, sh.powers);
+        return w >= r.least ? w : 0;
+    };
     {
         uint64_t sum = 0;
-        uint32_t ties = 0;
         const int end = min(n, (warp + 1) * seg_len);
-        for (int i = warp * seg_len + lane; i < end; i += 32) {
-            const float z = logit(i);
-            const uint32_t key = ordered(z) & kKey;
-            if (key > border) {
-                const uint64_t w = weight(z, m, ch, cl, sh.powers);
-                if (w >= least) sum += w;
-            }
-            ties += key == border;
+        if (border == ~(uint64_t)0 && r.least == 0) {
+#pragma unroll 2
+            for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight(r, logit(i), sh.powers);
+        } else {
+            for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight_of(i);
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        ties = __reduce_add_sync(0xffffffffu, ties);
-        if (lane == 0) {
-            sh.seg_sum[warp] = sum;
-            sh.seg_ties[warp] = ties;
-        }
+        if (lane == 0) sh.seg_sum[warp] = sum;
     }
-    if (threadIdx.x == 0) sh.seg = -1;
     __syncthreads();
-    if (ctas > 1) cluster_sync();
+    barrier();
     uint64_t total;
     {
         // thread j has segment j % kWarps of CTA j / kWarps
-        const int j = threadIdx.x;
-        uint64_t sum = 0, ties = 0, all;
-        if (j < ctas * kWarps) {
-            sum = remote_u64(&sh.seg_sum[j % kWarps], j / kWarps);
-            ties = remote_u32(&sh.seg_ties[j % kWarps], j / kWarps);
-        }
-        const uint64_t ties_before = sums_before(ties, sh.part, all);
-        const uint64_t mine = quota > ties_before ? min(ties, quota - ties_before) : 0;
-        sum += mine * at_border;
+        const uint64_t sum = tid < ctas * kWarps ? remote_u64(&sh.seg_sum[tid % kWarps], tid / kWarps) : 0;
         const uint64_t before = sums_before(sum, sh.part, total);
         // u beyond [0, 1) counts as its nearest end, NaN as 0
-        const float u = p.u[row];
         const uint64_t target = u >= 1.0f ? total - 1 : (u > 0.0f ? times(u, total, false) : 0);
         if (before <= target && target < before + sum) {
-            sh.seg = j;
+            sh.seg = tid;
             sh.target = target - before;
-            sh.quota = mine;
         }
     }
-    if (ctas > 1) cluster_sync();                                      // nobody reads another CTA's memory from here on
-    else __syncthreads();
+    barrier();                                                         // nobody reads another CTA's memory from here on
     const int seg = sh.seg;
-    if (seg < 0) {
-        // nothing to choose from: every logit is -inf or NaN
-        if (rank == 0 && threadIdx.x == 0) {
-            p.tokens[row] = -1;
-            if (p.logp) p.logp[row] = -INFINITY;
-        }
-        return;
-    }
-    if (seg / kWarps != rank) return;
+    if (seg < 0 || seg / kWarps != rank) return;
 
     // ---- the token: this CTA's threads share the segment ----
     const int begin = (seg % kWarps) * seg_len, end = min(n, begin + seg_len), each = (seg_len + kThreads - 1) / kThreads;
-    const int i0 = min(end, begin + (int)threadIdx.x * each), i1 = min(end, i0 + each);
-    uint64_t all, ties = 0, sum = 0;
-    for (int i = i0; i < i1; ++i) ties += (ordered(logit(i)) & kKey) == border;
-    uint64_t tie = sums_before(ties, sh.part, all);
-    const uint64_t mine = sh.quota > tie ? sh.quota - tie : 0;         // of this thread's, so many at the border are kept
-    uint64_t kept = 0;
-    auto weight_of = [&](int i) -> uint64_t {
-        const float z = logit(i);
-        const uint32_t key = ordered(z) & kKey;
-        if (key > border) {
-            const uint64_t w = weight(z, m, ch, cl, sh.powers);
-            return w >= least ? w : 0;
-        }
-        return key == border && kept++ < mine ? at_border : 0;
-    };
+    const int i0 = min(end, begin + tid * each), i1 = min(end, i0 + each);
+    uint64_t all, sum = 0;
     for (int i = i0; i < i1; ++i) sum += weight_of(i);
     uint64_t before = sums_before(sum, sh.part, all);
     if (before <= sh.target && sh.target < before + sum) {
-        kept = 0;
         for (int i = i0; i < i1; ++i) {
             before += weight_of(i);
             if (sh.target < before) {
-                if (!QMM_DCHECK(from + i < p.V)) break;
-                p.tokens[row] = from + i;
-                if (p.logp) {
-                    const float z = logit(i);
-                    const double y = z == m || first_only ? 0.0 : ((double)z - (double)m) / (double)temperature;
-                    p.logp[row] = (float)(y - log((double)total * (1.0 / (double)((uint64_t)1 << kOne))));
-                }
+                write(from + i, logit(i), total);
                 break;
             }
         }
