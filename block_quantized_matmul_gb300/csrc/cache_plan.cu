@@ -53,16 +53,16 @@ __device__ __forceinline__ Sums warp_sums(Sums x, int width) {
 // Place number `at` of a ring of n, for at >= 0.
 __device__ __forceinline__ int64_t around(int64_t at, int64_t n) { return at < n ? at : at % n; }
 
-constexpr int kWaits = -1, kDone = -2;      // in place of the pages that a sequence holds
+constexpr int kWaits = -1;                  // in place of the pages that a sequence holds (and for one that is done)
 
 // ROWS: the rows too; otherwise the new pages, and cache_plan_rows_kernel takes the rows.
 template <int THREADS, bool ROWS>
 __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p) {
     constexpr int kWarps = THREADS / 32;
     __shared__ Sums part[kWarps];
-    __shared__ int64_t s_start[THREADS], s_base[THREADS];             // first row; first new page, or first page given back, in the ring
+    __shared__ int64_t s_start[THREADS], s_base[THREADS];             // first row; first new page in the ring
     __shared__ int s_len[THREADS], s_held[THREADS];
-    __shared__ int64_t s_line[ROWS ? 1 : THREADS];                     // pages wanted by the sequences before
+    __shared__ int64_t s_line[ROWS ? 1 : THREADS], s_back[THREADS];   // pages wanted, and pages given back, by the sequences before
     __shared__ unsigned long long s_taken;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ctas = (int)gridDim.x, cta = (int)blockIdx.x;
     if (threadIdx.x == 0) s_taken = 0;
@@ -95,9 +95,10 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
         if (takes && lane == 31 - __clz(takes)) atomicMax(&s_taken, (unsigned long long)(x.need + v.need));
         s_start[threadIdx.x] = x.rows;
         if constexpr (!ROWS) s_line[threadIdx.x] = x.need;
+        s_back[threadIdx.x] = x.back;
         s_len[threadIdx.x] = (int)len;
-        s_held[threadIdx.x] = news < 0 ? kDone : (run ? (int)held : kWaits);
-        s_base[threadIdx.x] = news < 0 ? around(behind + x.back, p.n_ring) : around(front + x.need, p.n_ring);
+        s_held[threadIdx.x] = run ? (int)held : kWaits;
+        s_base[threadIdx.x] = around(front + x.need, p.n_ring);
         __syncthreads();
         // everybody has read the tile's lengths and, before the first results, the ring's counters
         if (ctas > 1) {
@@ -109,25 +110,39 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
             p.kv_lens[s] = run ? (int32_t)(len + rows) : 0;
             if (p.next_lens) p.next_lens[s] = news < 0 ? 0 : (int32_t)(run ? len + rows : len);
         }
-        // ---- pages that go back: a warp a sequence ----
-        for (int i = warp * ctas + cta; i < THREADS; i += kWarps * ctas) {
-            if (s_held[i] != kDone) continue;
-            const int n = (s_len[i] + P - 1) >> p.log_p;
-            for (int k = lane; k < n; k += 32) {
-                const int64_t to = around(s_base[i] + k, p.n_ring);
-                if (QMM_DCHECK(to >= 0 && to < p.n_ring && k < p.ld_pages && base + i < p.n_seq)) p.ring[to] = p.pages[(base + i) * p.ld_pages + k];
+        // the last sequence of the tile for which `first` is not above `at`
+        auto find = [](const int64_t *first, int64_t at) {
+            int lo = 0, hi = THREADS;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (first[mid] <= at) lo = mid;
+                else hi = mid;
+            }
+            return lo;
+        };
+        // ---- pages that go back, four of them under way at a time ----
+        for (int64_t at = done.back + (int64_t)cta * THREADS + threadIdx.x; at < done.back + all.back; at += (int64_t)ctas * THREADS * 4) {
+            int32_t page[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t i = at + (int64_t)u * ctas * THREADS;
+                page[u] = 0;
+                if (i >= done.back + all.back) continue;
+                const int lo = find(s_back, i);
+                const int64_t k = i - s_back[lo];
+                if (QMM_DCHECK(k < p.ld_pages && base + lo < p.n_seq)) page[u] = p.pages[(base + lo) * p.ld_pages + k];
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const int64_t i = at + (int64_t)u * ctas * THREADS, to = around(behind + i, p.n_ring);
+                if (i < done.back + all.back && QMM_DCHECK(to >= 0 && to < p.n_ring)) p.ring[to] = page[u];
             }
         }
         if constexpr (ROWS) {
             // ---- the rows that fall into this tile ----
             const int64_t r1 = min(done.rows + all.rows, p.T);
             for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < r1; r += (int64_t)ctas * THREADS) {
-                int lo = 0, hi = THREADS;                                  // the last sequence that starts at or before the row
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_start[mid] <= r) lo = mid;
-                    else hi = mid;
-                }
+                const int lo = find(s_start, r);
                 int64_t slot = -1;
                 int pos = -1;
                 if (s_held[lo] >= 0) {
@@ -151,12 +166,7 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
         } else {
             // ---- the new pages of this tile ----
             for (int64_t at = done.need + (int64_t)cta * THREADS + threadIdx.x; at < done.need + all.need; at += (int64_t)ctas * THREADS) {
-                int lo = 0, hi = THREADS;                              // the last sequence whose pages start at or before it
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (s_line[mid] <= at) lo = mid;
-                    else hi = mid;
-                }
+                const int lo = find(s_line, at);
                 if (s_held[lo] < 0) continue;
                 const int64_t number = s_held[lo] + (at - s_line[lo]);
                 if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) p.pages[(base + lo) * p.ld_pages + number] = p.ring[around(front + at, p.n_ring)];

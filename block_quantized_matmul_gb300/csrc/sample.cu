@@ -58,7 +58,7 @@ struct Row {
     float ch, cl;                           // c = log2(e) / temperature in two terms
     float y0, gh, gl;                       // top * c; what is left of it above y0's multiple n0 of 1 / kPowers, in two terms
     int n0;
-    int wide;                               // too far apart for `weight`'s short way
+    int wide;                               // too far apart for `weight`
     uint64_t least;                         // w that min_p asks for
 };
 
@@ -122,8 +122,15 @@ __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(
 __device__ __forceinline__ uint64_t place_of(float z, int index) { return (uint64_t)~ordered(z) << 32 | (uint32_t)index; }
 __device__ __forceinline__ float logit_of(uint64_t place) { return unordered(~(uint32_t)(place >> 32)); }
 
-// w of a logit whose distance from the largest is small, or whatever it is: z - top and its product with c as pairs of fp32.
-__device__ __noinline__ uint64_t weight_long(float z, float top, float ch, float cl) {
+// w = base * (1 + p) 2^-down for base of 2^kOne .. 2^(kOne + 1), |p| < 2^-11.
+__device__ __forceinline__ uint64_t scaled(uint64_t base, int p_2_42, int down) {
+    const uint64_t w = base + (uint64_t)(((int64_t)p_2_42 * (int64_t)(int32_t)(base >> 13)) >> 29);
+    return down <= 0 ? w : (w + ((uint64_t)1 << (down - 1))) >> down;
+}
+
+// w of a logit in a row whose logits or temperature are so far from 1 that `weight`'s steps would not hold: z - top and its
+// product with c as pairs of fp32, within 2^-40.
+__device__ __noinline__ uint64_t weight_wide(float z, float top, float ch, float cl) {
     if (z == top) return (uint64_t)1 << kOne;
     const float hi = __fsub_rn(z, top), b = __fsub_rn(hi, z), lo = __fadd_rn(__fsub_rn(z, __fsub_rn(hi, b)), __fsub_rn(-top, b));
     const float yh = __fmul_rn(hi, ch), yl = __fadd_rn(__fmaf_rn(hi, ch, -yh), __fmaf_rn(hi, cl, __fmul_rn(lo, ch)));
@@ -135,32 +142,31 @@ __device__ __noinline__ uint64_t weight_long(float z, float top, float ch, float
     const float th = __fmul_rn(g, ln2h), tl = __fadd_rn(__fmaf_rn(g, ln2h, -th), __fmaf_rn(g, ln2l, __fmul_rn(yl, ln2h)));
     const float t = __fadd_rn(th, tl), small = __fmaf_rn(__fmul_rn(t, t), __fmaf_rn(t, 1.0f / 6.0f, 0.5f), tl);
     const float unit = 4398046511104.0f;                               // 2^42
-    const int p = __float2int_rn(__fmul_rn(th, unit)) + __float2int_rn(__fmul_rn(small, unit));
-    const uint64_t base = g_powers.v[n & (kPowers - 1)];
-    const uint64_t w = base + (uint64_t)(((int64_t)p * (int64_t)(int32_t)(base >> 13)) >> 29);
-    const int down = -(n >> 11);                                       // 0 .. kOne + 1
-    return down <= 0 ? w : (w + ((uint64_t)1 << (down - 1))) >> down;
+    return scaled(g_powers.v[n & (kPowers - 1)], __float2int_rn(__fmul_rn(th, unit)) + __float2int_rn(__fmul_rn(small, unit)), -(n >> 11));
 }
 
-// w of logit z: 2^kOne * 2^y, y = (z - top) * c, to the nearest whole number but for 2^-34 of itself.
-// Below 2^-14 of the largest (all but 2^14 logits at most, and mostly a few) 30 bits hold what of w counts: y = z c - top c =
-// n / kPowers + f with |f| <= 1 / kPowers, where the multiple of 1 / kPowers and the rest are taken apart for z c (a
-// product in two terms) and for top c (once a row); 2^f - 1 = t + t^2/2 + t^3/6, t = f ln 2 (the next term is 2^-50),
-// is multiplied on as a whole number of 2^-32.  Half the instructions of the long way, which takes the rest.
+// w of logit z: 2^kOne * 2^y, y = (z - top) * c, to the nearest whole number but for 2^-34 of itself; 0 for NaN.
+// y = z c - top c = n / kPowers + f with |f| <= 1 / kPowers, where the multiple of 1 / kPowers and the rest are taken apart
+// for z c (a product in two terms) and for top c (once a row); 2^f - 1 = t + t^2/2 + t^3/6, t = f ln 2 (the next term
+// is 2^-50).  Below 2^-14 of the largest (all but 2^14 logits at most, and mostly a few) 30 bits hold what of w counts.
 __device__ __forceinline__ uint64_t weight(const Row &r, float z, const uint32_t *powers) {
+    if (r.wide) return weight_wide(z, r.top, r.ch, r.cl);
     const float yh = __fmul_rn(z, r.ch), y = __fsub_rn(yh, r.y0);
-    if (r.wide || !(y < -14.25f)) return weight_long(z, r.top, r.ch, r.cl);
     if (!(y > -(float)(kOne + 1) - 0.25f)) return 0;
     const float yl = __fmaf_rn(z, r.cl, __fmaf_rn(z, r.ch, -yh));
     const float magic = 12582912.0f, k = __fmaf_rn(yh, (float)kPowers, magic);
     const float g = __fmaf_rn(__fsub_rn(k, magic), -1.0f / kPowers, yh);
     const float t = __fmul_rn(__fadd_rn(__fsub_rn(g, r.gh), __fsub_rn(yl, r.gl)), 0.693147182464599609375f);
     const float p = __fmaf_rn(__fmul_rn(t, t), __fmaf_rn(t, 1.0f / 6.0f, 0.5f), t);
+    const int n = __float_as_int(k) - __float_as_int(magic) - r.n0, down = -(n >> 11);
+    if (down < 14) {
+        if (z == r.top) return (uint64_t)1 << kOne;
+        return scaled(g_powers.v[n & (kPowers - 1)], __float2int_rn(__fmul_rn(p, 4398046511104.0f)), down);
+    }
     const int q = __float_as_int(__fmaf_rn(p, 4294967296.0f, magic)) - __float_as_int(magic);
-    const int n = __float_as_int(k) - __float_as_int(magic) - r.n0;
     const uint32_t base = powers[n & (kPowers - 1)], w = base + (uint32_t)__mulhi((int)base, q);
     uint32_t a;
-    asm("shr.u32 %0, %1, %2;" : "=r"(a) : "r"(w), "r"(-(n >> 11) - 14));      // (by 32 and more: 0)
+    asm("shr.u32 %0, %1, %2;" : "=r"(a) : "r"(w), "r"(down - 14));     // (by 32 and more: 0)
     return (a >> 1) + (a & 1);
 }
 
@@ -575,8 +581,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         uint64_t sum = 0;
         const int end = min(n, (warp + 1) * seg_len);
         if (border == ~(uint64_t)0 && r.least == 0) {
-#pragma unroll 2
-            for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight(r, logit(i), sh.powers);
+#pragma unroll 4
+            for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight(r, elem_to_float(STAGED ? stage[i] : src[i]), sh.powers);
         } else {
             for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight_of(i);
         }
