@@ -7,16 +7,15 @@
 // Sums of need never fall, so once one waits for want of pages all later ones that need a page wait too: the pages of
 // those that run are the ring's entries first + line - need ...
 //
-// One cluster of CTAs does it all: each CTA runs the same scan over the sequences (a tile of as many as it has threads at a
-// time) and takes every C-th part of the rows that fall into them, so that no sum has to travel between CTAs; the cluster's
-// barrier, between the last read of a tile of lengths and the first write of its results, lets the new
-// lengths replace the old.  What bounds it is latency: the loads of the lengths, three scans in one, a row's search
-// for its sequence (8 or 10 steps in shared memory), and a load of the page.
-// Eight CTAs are few for the rows of many prompts (412000 rows: 75 us).  Those the cluster leaves to a second kernel over the whole
-// GPU, and takes the new pages instead, one in P rows: what the rows need stands in the outputs and the tables then.
+// Every CTA runs the same scan over the sequences (a tile of as many as it has threads at a time) and takes its share of the
+// rows, the new pages and the pages given back that fall into it, so that no sum has to travel between CTAs.  A few
+// CTAs do for a decode step; with 152 the rows of many prompts (412000 rows of 2048 sequences) take 11 us, with a cluster
+// of eight they took 29.  Where the new lengths or counters replace the old ones, which other CTAs may still read, a
+// second kernel writes them.  What bounds it is latency: the loads of the lengths, three scans in one, a row's
+// search for its sequence (8 or 10 steps in shared memory), and a load of the page.
 #include <climits>
 
-#include "cache.cuh"
+#include "qmm_internal.cuh"
 
 namespace qmm {
 namespace {
@@ -31,6 +30,7 @@ struct PlanParams {
     int64_t *slots;
     int32_t *positions, *next_lens;
     int64_t *next_at;
+    int later;                              // next_lens and next_at are cache_plan_next_kernel's
 };
 
 struct Sums {
@@ -55,14 +55,13 @@ __device__ __forceinline__ int64_t around(int64_t at, int64_t n) { return at < n
 
 constexpr int kWaits = -1;                  // in place of the pages that a sequence holds (and for one that is done)
 
-// ROWS: the rows too; otherwise the new pages, and cache_plan_rows_kernel takes the rows.
-template <int THREADS, bool ROWS>
+template <int THREADS>
 __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p) {
     constexpr int kWarps = THREADS / 32;
     __shared__ Sums part[kWarps];
     __shared__ int64_t s_start[THREADS], s_base[THREADS];             // first row; first new page in the ring
     __shared__ int s_len[THREADS], s_held[THREADS];
-    __shared__ int64_t s_line[ROWS ? 1 : THREADS], s_back[THREADS];   // pages wanted, and pages given back, by the sequences before
+    __shared__ int64_t s_back[THREADS];                               // pages given back by the sequences before
     __shared__ unsigned long long s_taken;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, ctas = (int)gridDim.x, cta = (int)blockIdx.x;
     if (threadIdx.x == 0) s_taken = 0;
@@ -94,21 +93,15 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
         const unsigned takes = __ballot_sync(0xffffffffu, run && v.need > 0);
         if (takes && lane == 31 - __clz(takes)) atomicMax(&s_taken, (unsigned long long)(x.need + v.need));
         s_start[threadIdx.x] = x.rows;
-        if constexpr (!ROWS) s_line[threadIdx.x] = x.need;
         s_back[threadIdx.x] = x.back;
         s_len[threadIdx.x] = (int)len;
         s_held[threadIdx.x] = run ? (int)held : kWaits;
         s_base[threadIdx.x] = around(front + x.need, p.n_ring);
         __syncthreads();
-        // everybody has read the tile's lengths and, before the first results, the ring's counters
-        if (ctas > 1) {
-            asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
-            asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-        }
         if (have && cta == (int)((base / THREADS) % ctas)) {
             p.q_starts[s] = (int32_t)min(x.rows, (int64_t)INT_MAX);
             p.kv_lens[s] = run ? (int32_t)(len + rows) : 0;
-            if (p.next_lens) p.next_lens[s] = news < 0 ? 0 : (int32_t)(run ? len + rows : len);
+            if (p.next_lens && !p.later) p.next_lens[s] = news < 0 ? 0 : (int32_t)(run ? len + rows : len);
         }
         // the last sequence of the tile for which `first` is not above `at`
         auto find = [](const int64_t *first, int64_t at) {
@@ -138,84 +131,78 @@ __global__ void __launch_bounds__(THREADS) cache_plan_kernel(const PlanParams p)
                 if (i < done.back + all.back && QMM_DCHECK(to >= 0 && to < p.n_ring)) p.ring[to] = page[u];
             }
         }
-        if constexpr (ROWS) {
-            // ---- the rows that fall into this tile ----
-            const int64_t r1 = min(done.rows + all.rows, p.T);
-            for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < r1; r += (int64_t)ctas * THREADS) {
-                const int lo = find(s_start, r);
-                int64_t slot = -1;
-                int pos = -1;
-                if (s_held[lo] >= 0) {
-                    pos = s_len[lo] + (int)(r - s_start[lo]);
-                    const int number = pos >> p.log_p, k = number - s_held[lo], place = pos & (P - 1);
-                    int64_t page = -1;
-                    if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) {
-                        int32_t *entry = p.pages + (base + lo) * p.ld_pages + number;
-                        if (k >= 0) {
-                            page = p.ring[around(s_base[lo] + k, p.n_ring)];
-                            if (place == 0) *entry = (int32_t)page;
-                        } else {
-                            page = *entry;
-                        }
+        // ---- the rows that fall into this tile ----
+        const int64_t r1 = min(done.rows + all.rows, p.T);
+        for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < r1; r += (int64_t)ctas * THREADS) {
+            const int lo = find(s_start, r);
+            int64_t slot = -1;
+            int pos = -1;
+            if (s_held[lo] >= 0) {
+                pos = s_len[lo] + (int)(r - s_start[lo]);
+                const int number = pos >> p.log_p, k = number - s_held[lo], place = pos & (P - 1);
+                int64_t page = -1;
+                if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) {
+                    int32_t *entry = p.pages + (base + lo) * p.ld_pages + number;
+                    if (k >= 0) {
+                        page = p.ring[around(s_base[lo] + k, p.n_ring)];
+                        if (place == 0) *entry = (int32_t)page;
+                    } else {
+                        page = *entry;
                     }
-                    slot = page * P + place;
                 }
-                p.slots[r] = slot;
-                if (p.positions) p.positions[r] = pos;
+                slot = page * P + place;
             }
-        } else {
-            // ---- the new pages of this tile ----
-            for (int64_t at = done.need + (int64_t)cta * THREADS + threadIdx.x; at < done.need + all.need; at += (int64_t)ctas * THREADS) {
-                const int lo = find(s_line, at);
-                if (s_held[lo] < 0) continue;
-                const int64_t number = s_held[lo] + (at - s_line[lo]);
-                if (QMM_DCHECK(number < p.ld_pages && base + lo < p.n_seq)) p.pages[(base + lo) * p.ld_pages + number] = p.ring[around(front + at, p.n_ring)];
-            }
+            p.slots[r] = slot;
+            if (p.positions) p.positions[r] = pos;
         }
         done = done + all;
         __syncthreads();                                              // the tile's arrays are free again
     }
-    if constexpr (ROWS) {
-        for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < p.T; r += (int64_t)ctas * THREADS) {
-            p.slots[r] = -1;
-            if (p.positions) p.positions[r] = -1;
-        }
+    for (int64_t r = done.rows + (int64_t)cta * THREADS + threadIdx.x; r < p.T; r += (int64_t)ctas * THREADS) {
+        p.slots[r] = -1;
+        if (p.positions) p.positions[r] = -1;
     }
     if (cta == 0 && threadIdx.x == 0) {
         p.q_starts[p.n_seq] = (int32_t)min(done.rows, (int64_t)INT_MAX);
-        if (p.next_at) {
+        if (p.next_at && !p.later) {
             p.next_at[0] = first + (int64_t)s_taken;
             p.next_at[1] = last + done.back;
         }
     }
 }
 
-// The rows' slots and positions from what the first kernel has written, kRowsOfCta neighbouring rows to a CTA.
-constexpr int kRowThreads = 256, kRowsOfCta = 8 * kRowThreads;
-__global__ void __launch_bounds__(kRowThreads) cache_plan_rows_kernel(const PlanParams p) {
+// The lengths and the ring's counters after the step, from those before it and from kv_lens, by one CTA.
+__global__ void __launch_bounds__(1024) cache_plan_next_kernel(const PlanParams p) {
+    __shared__ unsigned long long s_taken, s_back;
+    if (threadIdx.x == 0) s_taken = s_back = 0;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int64_t r0 = (int64_t)blockIdx.x * kRowsOfCta, r1 = min(p.T, r0 + kRowsOfCta);
-    const int64_t s0 = max((int64_t)0, last_start(p.q_starts, p.n_seq, r0)), s1 = last_start(p.q_starts, p.n_seq, r1 - 1);
-    for (int64_t r = r0 + threadIdx.x; r < r1; r += kRowThreads) {
-        int64_t lo = s0, hi = s1 + 1;
-        while (hi - lo > 1) {
-            const int64_t mid = (lo + hi) >> 1;
-            if (p.q_starts[mid] <= r) lo = mid;
-            else hi = mid;
-        }
-        int64_t slot = -1;
-        int pos = -1;
-        if (lo < p.n_seq) {
-            const int from = p.q_starts[lo], to = p.q_starts[lo + 1], len = p.kv_lens[lo];
-            if (len > 0) {                                             // (0: the sequence waits)
-                pos = len - (to - from) + (int)(r - from);
-                const int number = pos >> p.log_p;
-                if (QMM_DCHECK(pos >= 0 && number < p.ld_pages)) slot = (int64_t)p.pages[lo * p.ld_pages + number] << p.log_p | (pos & ((1 << p.log_p) - 1));
-            }
-        }
-        p.slots[r] = slot;
-        if (p.positions) p.positions[r] = pos;
+    const int P = 1 << p.log_p;
+    const int64_t room = min(p.ld_pages << p.log_p, (int64_t)INT_MAX);
+    unsigned long long taken = 0, back = 0;
+    for (int64_t s = threadIdx.x; s < p.n_seq; s += 1024) {
+        const int64_t len = max((int64_t)0, min((int64_t)p.lens[s], room)), held = (len + P - 1) >> p.log_p, after = p.kv_lens[s];
+        const int news = p.news[s];
+        const bool runs = news > 0 && after > 0;
+        if (runs) taken += ((after + P - 1) >> p.log_p) - held;
+        if (news < 0) back += held;
+        if (p.next_lens) p.next_lens[s] = news < 0 ? 0 : (int32_t)(runs ? after : len);
+    }
+#pragma unroll
+    for (int m = 16; m > 0; m >>= 1) {
+        taken += __shfl_xor_sync(0xffffffffu, taken, m);
+        back += __shfl_xor_sync(0xffffffffu, back, m);
+    }
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) {
+        atomicAdd(&s_taken, taken);
+        atomicAdd(&s_back, back);
+    }
+    __syncthreads();
+    if (threadIdx.x == 0 && p.next_at && QMM_DCHECK(p.n_ring > 0)) {
+        const int64_t first = p.ring_at[0], last = p.ring_at[1];
+        p.next_at[0] = first + (int64_t)s_taken;
+        p.next_at[1] = last + (int64_t)s_back;
     }
 }
 
@@ -224,17 +211,15 @@ __global__ void __launch_bounds__(kRowThreads) cache_plan_rows_kernel(const Plan
 cudaError_t launch_cache_plan(const int32_t *lens, const int32_t *news, int64_t n_seq, int P, int32_t *pages, int64_t ld_pages,
                               int32_t *ring, int64_t n_ring, const int64_t *ring_at, int64_t T, int32_t *q_starts, int32_t *kv_lens,
                               int64_t *slots, int32_t *positions, int32_t *next_lens, int64_t *next_at, cudaStream_t s) {
-    PlanParams p = {lens, news, n_seq, ld_pages, n_ring, T, 0, pages, ring, ring_at, q_starts, kv_lens, slots, positions, next_lens, next_at};
+    PlanParams p = {lens, news, n_seq, ld_pages, n_ring, T, 0, pages, ring, ring_at, q_starts, kv_lens, slots, positions, next_lens, next_at, 0};
     while ((1 << p.log_p) < P) ++p.log_p;
-    if (n_seq <= 256 && T <= 1024) return launch_pdl(cache_plan_kernel<256, true>, dim3(1), 256, 0, s, p);
-    if (T <= 8192) {
-        unsigned ctas = 1;
-        while (ctas < 8 && (int64_t)ctas * 1024 < T) ctas *= 2;
-        return launch_pdl_cluster(cache_plan_kernel<1024, true>, dim3(ctas), ctas, 1024, 0, s, p);
-    }
-    const cudaError_t e = launch_pdl_cluster(cache_plan_kernel<1024, false>, dim3(8), 8, 1024, 0, s, p);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(cache_plan_rows_kernel, dim3((unsigned)((T + kRowsOfCta - 1) / kRowsOfCta)), kRowThreads, 0, s, p);
+    if (n_seq <= 256 && T <= 1024) return launch_pdl(cache_plan_kernel<256>, dim3(1), 256, 0, s, p);
+    // two rows a thread; a sequence that is done may give back many pages
+    const int64_t want = (T + 16 * n_seq + 2047) / 2048;
+    const unsigned ctas = (unsigned)(want < 152 ? want : 152);
+    p.later = ctas > 1 && (next_lens == lens || next_at == ring_at);
+    const cudaError_t e = launch_pdl(cache_plan_kernel<1024>, dim3(ctas), 1024, 0, s, p);
+    return e != cudaSuccess || !p.later ? e : launch_pdl(cache_plan_next_kernel, dim3(1), 1024, 0, s, p);
 }
 
 QMM_DCHECK_READER(read_dcheck_cache_plan)

@@ -12,7 +12,6 @@
 
 #include "cache.cuh"
 #include "elem.cuh"
-#include "tc_common.cuh"
 
 namespace qmm {
 namespace {
@@ -173,21 +172,34 @@ __global__ void __launch_bounds__(kBoundWarps * 32) cache_bounds_kernel(const Bo
 // ---------------------------------------------------------------------------------------------
 // Scores
 // ---------------------------------------------------------------------------------------------
+struct Sequence {
+    int64_t s, q0, q1, len;                 // number, rows of q q0 .. q1 - 1 (none: it is not computed), cached tokens
+};
+// The sequence of a row of q.  By a whole warp.
+__device__ __forceinline__ Sequence find_sequence(const SelectParams &p, int64_t row) {
+    Sequence q = {last_start(p.q_starts, p.n_seq, row), 0, 0, 0};
+    if (q.s < 0 || q.s >= p.n_seq) return q;
+    const int64_t q0 = p.q_starts[q.s], q1 = p.q_starts[q.s + 1];
+    q.len = p.kv_lens[q.s];
+    if (q0 < 0 || q1 > p.T) return q;
+    q.q0 = q0;
+    q.q1 = q1;
+    return q;
+}
+
 struct Token {                              // a new token, and the pages in question for it
     int64_t s, seen;                        // its sequence; number of pages (0: none)
     int64_t old;                            // the first of the last ones that are always chosen
 };
-
-// The token of a row of q; false: the row is no sequence's, or past max_new.  By a whole warp.
-__device__ __forceinline__ bool find_token(const SelectParams &p, int64_t row, Token &t) {
-    t.s = last_start(p.q_starts, p.n_seq, row);
-    if (t.s < 0 || t.s >= p.n_seq) return false;
-    const int64_t q0 = p.q_starts[t.s], q1 = p.q_starts[t.s + 1], len = p.kv_lens[t.s], nq = q1 - q0, i = row - q0;
-    if (q0 < 0 || q1 > p.T || i >= p.max_new) return false;
-    const int64_t n = min(len, p.ld_pages << p.log_p), first = len - nq;
+// The token of a row of q of its sequence; false: the row is past max_new, or not computed.
+__device__ __forceinline__ bool find_token(const SelectParams &p, const Sequence &q, int64_t row, Token &t) {
+    const int64_t i = row - q.q0;
+    if (row >= q.q1 || i >= p.max_new) return false;
+    const int64_t n = min(q.len, p.ld_pages << p.log_p), first = q.len - (q.q1 - q.q0);
     // the last place that the token sees, and the place from which the last pages are counted
     const int64_t end = p.tree ? n - 1 : min(first + i, n - 1), from = p.tree ? first : first + i;
-    t.seen = end < 0 || (len + ((int64_t)1 << p.log_p) - 1) >> p.log_p > p.most ? 0 : (end >> p.log_p) + 1;
+    t.s = q.s;
+    t.seen = end < 0 || (q.len + ((int64_t)1 << p.log_p) - 1) >> p.log_p > p.most ? 0 : (end >> p.log_p) + 1;
     t.old = (from < 0 ? 0 : from >> p.log_p) - (p.recent - 1);
     return true;
 }
@@ -204,18 +216,21 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int h = (int)(blockIdx.y % (unsigned)p.H);
-    const int64_t row0 = (int64_t)blockIdx.x * p.tok_tile, page0 = (int64_t)(blockIdx.y / (unsigned)p.H) * kScoreThreads;
+    const int64_t row0 = (int64_t)blockIdx.x * p.tok_tile, cta0 = (int64_t)(blockIdx.y / (unsigned)p.H) * kScoreThreads;
+    const int64_t stride = (int64_t)(gridDim.y / (unsigned)p.H) * kScoreThreads;
     const int toks = (int)min((int64_t)p.tok_tile, p.T - row0);
     Token tok[kTokTile];
-    bool any = false;
+    int64_t all = 0;                                                   // pages that any token of the tile asks about
+    Sequence of = find_sequence(p, row0);
 #pragma unroll
     for (int k = 0; k < kTokTile; ++k) {
-        tok[k].seen = 0;
+        tok[k] = {-1, 0, 0};
+        if (k < toks && k > 0 && row0 + k >= of.q1) of = find_sequence(p, row0 + k);
         // where all pages are chosen, nobody asks for scores
-        if (k < toks && find_token(p, row0 + k, tok[k]) && tok[k].seen > p.budget) any |= tok[k].seen > page0;
+        if (k < toks && find_token(p, of, row0 + k, tok[k]) && tok[k].seen > p.budget) all = max(all, tok[k].seen);
         else tok[k].seen = 0;
     }
-    if (!any) return;
+    if (all <= cta0) return;
     // ---- the tile's query rows, a warp a row ----
     const int lane = threadIdx.x & 31, rows = toks * p.group;
     uint8_t *codes = smem;                                             // [row][2][D]: negative, positive
@@ -236,52 +251,53 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
         }
     }
     __syncthreads();
-    const int64_t number = page0 + threadIdx.x;
-    uint4 c[DB * 4];                                                   // lowest: 2 a block, then highest
-    float d[DB];
-    int64_t loaded = -1;
-    bool there = false;
+    for (int64_t number = cta0 + threadIdx.x; number < all; number += stride) {
+        uint4 c[DB * 4];                                                   // lowest: 2 a block, then highest
+        float d[DB];
+        int64_t loaded = -1;
+        bool there = false;
 #pragma unroll
-    for (int k = 0; k < kTokTile; ++k) {
-        if (number >= tok[k].seen || !QMM_DCHECK(number < p.ld_pages && number < p.most)) continue;
-        if (tok[k].s != loaded) {
-            loaded = tok[k].s;
-            const int64_t page = p.pages[loaded * p.ld_pages + number];
-            there = page >= 0 && page < p.n_pages;
-            if (there) {
-                const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (page * p.H + h) * BB);
+        for (int k = 0; k < kTokTile; ++k) {
+            if (number >= tok[k].seen || !QMM_DCHECK(number < p.ld_pages && number < p.most)) continue;
+            if (tok[k].s != loaded) {
+                loaded = tok[k].s;
+                const int64_t page = p.pages[loaded * p.ld_pages + number];
+                there = page >= 0 && page < p.n_pages;
+                if (there) {
+                    const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (page * p.H + h) * BB);
 #pragma unroll
-                for (int i = 0; i < DB * 4; ++i) c[i] = src[i];
-                const __half *ds = reinterpret_cast<const __half *>(src + DB * 4);
+                    for (int i = 0; i < DB * 4; ++i) c[i] = src[i];
+                    const __half *ds = reinterpret_cast<const __half *>(src + DB * 4);
 #pragma unroll
-                for (int b = 0; b < DB; ++b) d[b] = __half2float(ds[b]);
-            }
-        }
-        float best = -INFINITY;
-        for (int g = 0; g < p.group && there; ++g) {
-            const int r = k * p.group + g;
-            const uint4 *a = reinterpret_cast<const uint4 *>(codes + r * 2 * D);
-            float score = 0.0f;
-#pragma unroll
-            for (int b = 0; b < DB; ++b) {
-                int x = 0, y = 0;
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const uint4 m = a[2 * b + i], q = a[DB * 2 + 2 * b + i], lo = c[2 * b + i], hi = c[DB * 2 + 2 * b + i];
-                    x = __dp4a((int)m.x, (int)lo.x, x);
-                    x = __dp4a((int)m.y, (int)lo.y, x);
-                    x = __dp4a((int)m.z, (int)lo.z, x);
-                    x = __dp4a((int)m.w, (int)lo.w, x);
-                    y = __dp4a((int)q.x, (int)hi.x, y);
-                    y = __dp4a((int)q.y, (int)hi.y, y);
-                    y = __dp4a((int)q.z, (int)hi.z, y);
-                    y = __dp4a((int)q.w, (int)hi.w, y);
+                    for (int b = 0; b < DB; ++b) d[b] = __half2float(ds[b]);
                 }
-                score = __fadd_rn(score, __fmul_rn(__fmul_rn(dq[r * DB + b], d[b]), (float)(x + y)));
             }
-            best = isnan(score) ? INFINITY : fmaxf(best, score);
+            float best = -INFINITY;
+            for (int g = 0; g < p.group && there; ++g) {
+                const int r = k * p.group + g;
+                const uint4 *a = reinterpret_cast<const uint4 *>(codes + r * 2 * D);
+                float score = 0.0f;
+#pragma unroll
+                for (int b = 0; b < DB; ++b) {
+                    int x = 0, y = 0;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint4 m = a[2 * b + i], q = a[DB * 2 + 2 * b + i], lo = c[2 * b + i], hi = c[DB * 2 + 2 * b + i];
+                        x = __dp4a((int)m.x, (int)lo.x, x);
+                        x = __dp4a((int)m.y, (int)lo.y, x);
+                        x = __dp4a((int)m.z, (int)lo.z, x);
+                        x = __dp4a((int)m.w, (int)lo.w, x);
+                        y = __dp4a((int)q.x, (int)hi.x, y);
+                        y = __dp4a((int)q.y, (int)hi.y, y);
+                        y = __dp4a((int)q.z, (int)hi.z, y);
+                        y = __dp4a((int)q.w, (int)hi.w, y);
+                    }
+                    score = __fadd_rn(score, __fmul_rn(__fmul_rn(dq[r * DB + b], d[b]), (float)(x + y)));
+                }
+                best = isnan(score) ? INFINITY : fmaxf(best, score);
+            }
+            p.scores[((row0 + k) * p.H + h) * p.most + number] = best;
         }
-        p.scores[((row0 + k) * p.H + h) * p.most + number] = best;
     }
 }
 
@@ -310,7 +326,7 @@ __global__ void __launch_bounds__(kChooseThreads) cache_choose_kernel(const Sele
     const int64_t row = blockIdx.x / (unsigned)p.H;
     const int h = (int)(blockIdx.x % (unsigned)p.H), tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Token t;
-    if (!find_token(p, row, t)) return;
+    if (!find_token(p, find_sequence(p, row), row, t)) return;
     int32_t *out = p.chosen + (row * p.H + h) * p.budget;
     const int seen = (int)t.seen, budget = (int)p.budget;
     if (seen <= budget) {
@@ -464,9 +480,12 @@ __global__ void __launch_bounds__(kChooseThreads) cache_choose_kernel(const Sele
 template <int DB>
 cudaError_t launch_score(const SelectParams &p, cudaStream_t s) {
     const size_t smem = (size_t)p.tok_tile * p.group * (2 * DB * 32 + DB * 4);    // up to 64 rows: 35 KB
-    const int64_t x = (p.T + p.tok_tile - 1) / p.tok_tile, y = (p.most + kScoreThreads - 1) / kScoreThreads * p.H;
-    if (x > 0x7fffffff || y > 65535) return cudaErrorInvalidValue;
-    return launch_pdl(cache_score_kernel<DB>, dim3((unsigned)x, (unsigned)y), kScoreThreads, smem, s, p);
+    // each CTA prepares the tile's query rows for itself, so it takes as many pages as leave the GPU four CTAs an SM
+    const int64_t x = (p.T + p.tok_tile - 1) / p.tok_tile, chunks = (p.most + kScoreThreads - 1) / kScoreThreads;
+    int64_t split = (4 * 152 + x * p.H - 1) / (x * p.H);
+    split = split < chunks ? split : chunks;
+    if (x > 0x7fffffff || split * p.H > 65535) return cudaErrorInvalidValue;
+    return launch_pdl(cache_score_kernel<DB>, dim3((unsigned)x, (unsigned)(split * p.H)), kScoreThreads, smem, s, p);
 }
 
 template <int TYPE, int DB>

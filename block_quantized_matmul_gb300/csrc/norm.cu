@@ -3,10 +3,10 @@
 //   y = h' / sqrt(mean(h'^2) + eps) * w_pre,
 // with y as rows, as Q8_0 blocks or as MX4 blocks.
 //
-// A row stays in registers from its load to its last store, so x, h and gate are read once and h' and y written
-// once; each thread holds C pieces of 8 consecutive elements, so that four neighbouring threads hold a block of 32.  Rows of up
-// to 1024 elements take a warp each, longer ones a CTA.  Element types are parameters of the launch, not of
-// the kernel: the branches are uniform, and the kernel is bound by memory.
+// x, h and gate are read once and h' and y written once: a row stays on the SM from its load to its last store.  Each thread
+// holds C pieces of 8 consecutive elements, so that four neighbouring threads hold a block of 32.  Rows of up to 1024 elements take
+// a warp each, longer ones a CTA; what a thread does once a row (sums, roots, addresses) is about 150 instructions, so it
+// takes 16 elements where rows are many.
 #include "qmm_internal.cuh"
 
 #include "elem.cuh"
@@ -130,20 +130,23 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
     return v;
 }
 
-// TPR threads take a row, C pieces of 8 elements each.
-template <int TPR, int C, bool VEC>
+// TPR threads take a row, C pieces of 8 elements each.  TYPES: of x, h and y, where the compiler knows them (9 x + 3 h + y), or -1.
+// (8192 rows of 4096, both norms and a gate, bf16: 46 us, 5.8 TB/s; with the types as parameters of the launch 65, for branches
+// and unused registers.  A ring of asynchronous copies under CTAs that go on from row to row: 52.)
+template <int TPR, int C, bool VEC, int TYPES>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormParams p) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
     static_assert(TPR == 32 || kRows == 1, "a row is a warp's or a CTA's");
     __shared__ float part[2][TPR > 32 ? TPR / 32 : 1];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int xdt = TYPES < 0 ? p.xdt : TYPES / 9, hdt = TYPES < 0 ? p.hdt : TYPES / 3 % 3, ydt = TYPES < 0 ? p.ydt : TYPES % 3;
     const int t = threadIdx.x % TPR, n = p.N;
+    const float inv_n = 1.0f / (float)n;
     const int64_t row = (int64_t)blockIdx.x * kRows + threadIdx.x / TPR;
     if (row >= p.R) return;                                            // (a whole warp)
-    const float inv_n = 1.0f / (float)n;
-    const void *hr = row_of(p.h, p.hdt, row * p.ldh), *xr = p.x ? row_of(p.x, p.xdt, row * p.ldx) : nullptr;
-    const void *gr = p.gate ? row_of(p.gate, p.xdt, row * p.ldg) : nullptr;
+    const void *hr = row_of(p.h, hdt, row * p.ldh), *xr = p.x ? row_of(p.x, xdt, row * p.ldx) : nullptr;
+    const void *gr = p.gate ? row_of(p.gate, xdt, row * p.ldg) : nullptr;
     // of x the pieces are kept as they lie in memory; a thread of 1024 has no registers for four of them, and loads them again
     constexpr bool kKeep = C < 4 || TPR == 32;
     Raw8 rx[kKeep ? C : 1];
@@ -151,7 +154,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
     if (kKeep && xr) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
-            if ((c * TPR + t) * 8 < n) load8<VEC>(rx[c], xr, p.xdt, (c * TPR + t) * 8, n);
+            if ((c * TPR + t) * 8 < n) load8<VEC>(rx[c], xr, xdt, (c * TPR + t) * 8, n);
     }
 #pragma unroll
     for (int c = 0; c < C; ++c) {
@@ -160,8 +163,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
         for (int i = 0; i < 8; ++i) h[c][i] = 0.0f;
         if (at >= n) continue;
         Raw8 r;
-        load8<VEC>(r, hr, p.hdt, at, n);
-        values8(h[c], r, p.hdt);
+        load8<VEC>(r, hr, hdt, at, n);
+        values8(h[c], r, hdt);
     }
     if (xr) {
         float r = 1.0f;
@@ -172,8 +175,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
                 const int at = (c * TPR + t) * 8;
                 if (at >= n) continue;
                 float x[8];
-                if constexpr (!kKeep) load8<VEC>(rx[0], xr, p.xdt, at, n);
-                values8(x, rx[kKeep ? c : 0], p.xdt);
+                if constexpr (!kKeep) load8<VEC>(rx[0], xr, xdt, at, n);
+                values8(x, rx[kKeep ? c : 0], xdt);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum += x[i] * x[i];
             }
@@ -186,8 +189,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
             if (at >= n) continue;
             float x[8], w[8];
             Raw8 raw;
-            if constexpr (!kKeep) load8<VEC>(rx[0], xr, p.xdt, at, n);
-            values8(x, rx[kKeep ? c : 0], p.xdt);
+            if constexpr (!kKeep) load8<VEC>(rx[0], xr, xdt, at, n);
+            values8(x, rx[kKeep ? c : 0], xdt);
             if (p.w_post) {
                 load8<VEC>(raw, p.w_post, QMM_F32, at, n);
                 values8(w, raw, QMM_F32);
@@ -195,8 +198,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
                 for (int i = 0; i < 8; ++i) x[i] *= w[i];
             }
             if (gr) {
-                load8<VEC>(raw, gr, p.xdt, at, n);
-                values8(w, raw, p.xdt);
+                load8<VEC>(raw, gr, xdt, at, n);
+                values8(w, raw, xdt);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] *= w[i];
             }
@@ -212,9 +215,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
         if (at >= n) continue;
         if (p.h_out) {
             Raw8 r;
-            round8(r, h[c], p.hdt);
-            if (QMM_DCHECK(!VEC || at + 8 <= n)) store8<VEC>(r, const_cast<void *>(row_of(p.h_out, p.hdt, row * p.ldho)), p.hdt, at, n);
-            if (p.hdt != QMM_F32) values8(h[c], r, p.hdt);
+            round8(r, h[c], hdt);
+            if (QMM_DCHECK(!VEC || at + 8 <= n)) store8<VEC>(r, const_cast<void *>(row_of(p.h_out, hdt, row * p.ldho)), hdt, at, n);
+            if (hdt != QMM_F32) values8(h[c], r, hdt);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) sum += VEC || at + i < n ? h[c][i] * h[c][i] : 0.0f;
@@ -242,8 +245,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
         }
         if (p.form == kNormRows) {
             Raw8 o;
-            round8(o, y, p.ydt);
-            if (in) store8<VEC>(o, const_cast<void *>(row_of(p.y, p.ydt, row * p.ldy)), p.ydt, at, n);
+            round8(o, y, ydt);
+            if (in) store8<VEC>(o, const_cast<void *>(row_of(p.y, ydt, row * p.ldy)), ydt, at, n);
             continue;
         }
         // the largest magnitude of the block of 32 that four threads hold
@@ -275,12 +278,23 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
     }
 }
 
-template <int TPR, int C>
-cudaError_t launch_rows(const NormParams &p, bool vec, cudaStream_t s) {
-    constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
+template <int TPR, int C, int TYPES>
+cudaError_t launch_typed(const NormParams &p, bool vec, cudaStream_t s) {
+    constexpr int kRows = TPR < 256 ? 256 / TPR : 1, kThreads = TPR < 256 ? 256 : TPR;
     const int64_t grid = (p.R + kRows - 1) / kRows;
     if (grid > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_pdl(vec ? norm_kernel<TPR, C, true> : norm_kernel<TPR, C, false>, dim3((unsigned)grid), TPR < 256 ? 256 : TPR, 0, s, p);
+    return launch_pdl(vec ? norm_kernel<TPR, C, true, TYPES> : norm_kernel<TPR, C, false, -1>, dim3((unsigned)grid), kThreads, 0, s, p);
+}
+template <int TPR, int C>
+cudaError_t launch_rows(const NormParams &p, bool vec, cudaStream_t s) {
+    // many rows of bf16, with a residual stream of either kind; few rows are bound by latency
+    constexpr int kBf16 = QMM_BF16 * 13, kBf16Stream32 = QMM_BF16 * 9 + QMM_F32 * 3 + QMM_BF16;
+    if (vec && p.R > 152) {
+        const bool y16 = p.form != kNormRows || p.ydt == QMM_BF16, x16 = !p.x || p.xdt == QMM_BF16;
+        if (x16 && y16 && p.hdt == QMM_BF16) return launch_typed<TPR, C, kBf16>(p, vec, s);
+        if (x16 && y16 && p.hdt == QMM_F32) return launch_typed<TPR, C, kBf16Stream32>(p, vec, s);
+    }
+    return launch_typed<TPR, C, -1>(p, vec, s);
 }
 
 }  // namespace

@@ -72,6 +72,7 @@ struct alignas(16) Shared {
     float top, bottom;                      // the slice's largest, and smallest finite, logit
     int first;
     Row row;
+    double c;
     // what one thread finds for all
     int bin;
     uint64_t left, upto, border;
@@ -300,6 +301,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const int top_k = p.top_k ? p.top_k[row] : 0;
     const float u = p.u[row];
     __syncthreads();
+    if (tid == kThreads - 1) {
+        // what of the row's constants needs no maximum
+        const double c = 1.4426950408889634074 / (double)temperature;
+        sh.c = c;
+        sh.row.ch = (float)c;
+        sh.row.cl = fabsf((float)c) < INFINITY ? (float)(c - (double)(float)c) : 0.0f;
+        sh.row.least = min_p > 0.0f && min_p <= 1.0f ? (uint64_t)ceil((double)min_p * (double)((uint64_t)1 << kOne)) : 0;
+    }
     if (warp == 0) {
         const uint64_t both = sh.part[lane % kWarps];
         top = __uint_as_float((uint32_t)(both >> 32));
@@ -325,18 +334,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         if (lane == 0) {
             Row &r = sh.row;
-            const double c = 1.4426950408889634074 / (double)temperature, y0 = (double)(top + 0.0f) * c;
+            const double y0 = (double)(top + 0.0f) * sh.c;
             r.top = top + 0.0f;
             r.scale = (float)(kBins - 1) / fminf(__fsub_rn(top, bottom), 64.0f * fmaxf(1.0f, temperature));   // (bottom = inf: 0 or less)
-            r.ch = (float)c;
-            r.cl = fabsf(r.ch) < INFINITY ? (float)(c - (double)r.ch) : 0.0f;
             r.y0 = (float)y0;
             r.wide = !(fabs(y0) < 900.0);
             const double n0 = r.wide ? 0.0 : rint(y0 * kPowers), g = y0 - n0 / kPowers;
             r.n0 = (int)n0;
             r.gh = (float)g;
             r.gl = (float)(g - (double)r.gh);
-            r.least = min_p > 0.0f && min_p <= 1.0f ? (uint64_t)ceil((double)min_p * (double)((uint64_t)1 << kOne)) : 0;
         }
     }
     __syncthreads();
