@@ -24,8 +24,9 @@
 namespace qmm {
 namespace {
 
-constexpr int kThreads = 512, kWarps = kThreads / 32, kBins = 4 * kThreads, kMaxCluster = 8;
-constexpr int kCand = 2 * kThreads;         // elements that one CTA sorts
+constexpr int kBins = 2048, kSums = 512, kMaxCluster = 8;     // bins of a slice's histogram, and sums of four of them that the CTAs exchange
+constexpr int kCand = 1024;                 // elements that one CTA sorts
+constexpr int kMaxWarps = 32;
 constexpr int kOne = 43;                    // w of the largest logit is 2^kOne
 constexpr int kPowers = 2048;
 
@@ -63,19 +64,21 @@ struct Row {
 };
 
 struct alignas(16) Shared {
-    uint32_t powers[kPowers];               // g_powers in units of 2^-30
-    uint32_t lo[kBins], hi[kBins];          // a histogram of this CTA's slice: counts (lo), or sums in two words
+    uint32_t powers[kPowers];               // g_powers in units of 2^-30,
+    uint16_t more[kPowers];                 // and the 13 bits below
+    uint32_t lo[kBins], hi[kBins];          // the histogram of this CTA's slice: counts (lo), or sums in two words
     uint64_t cand[kCand];                   // of the row's first CTA: gathered elements, ~ordered(z) << 32 | index
-    uint32_t n_cand;
-    uint64_t seg_sum[kWarps];               // sum of the kept w of each warp's segment
-    uint64_t part[kWarps];
+    uint64_t list[kCand];                   // this CTA's part of them
+    uint32_t n_cand, n_list, list_at;
+    uint64_t sums[kSums];                   // the histogram, four bins to a sum
+    uint64_t seg_sum[kMaxWarps];            // sum of the kept w of each warp's segment
+    uint64_t part[kMaxWarps];
     float top, bottom;                      // the slice's largest, and smallest finite, logit
     int first;
     Row row;
-    double c;
     // what one thread finds for all
     int bin;
-    uint64_t left, upto, border;
+    uint64_t left, upto, border;            // border: a place
     int seg;
     uint64_t target;
 };
@@ -119,8 +122,8 @@ __device__ __forceinline__ uint32_t ordered(float v) {
     return b & 0x80000000u ? ~b : b | 0x80000000u;
 }
 __device__ __forceinline__ float unordered(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
-// An element's place in the order: the smaller the earlier.
-__device__ __forceinline__ uint64_t place_of(float z, int index) { return (uint64_t)~ordered(z) << 32 | (uint32_t)index; }
+// An element's place in the order: the smaller the earlier.  (-0 is 0.)
+__device__ __forceinline__ uint64_t place_of(float z, int index) { return (uint64_t)~ordered(z + 0.0f) << 32 | (uint32_t)index; }
 __device__ __forceinline__ float logit_of(uint64_t place) { return unordered(~(uint32_t)(place >> 32)); }
 
 // w = base * (1 + p) 2^-down for base of 2^kOne .. 2^(kOne + 1), |p| < 2^-11.
@@ -150,7 +153,7 @@ __device__ __noinline__ uint64_t weight_wide(float z, float top, float ch, float
 // y = z c - top c = n / kPowers + f with |f| <= 1 / kPowers, where the multiple of 1 / kPowers and the rest are taken apart
 // for z c (a product in two terms) and for top c (once a row); 2^f - 1 = t + t^2/2 + t^3/6, t = f ln 2 (the next term
 // is 2^-50).  Below 2^-14 of the largest (all but 2^14 logits at most, and mostly a few) 30 bits hold what of w counts.
-__device__ __forceinline__ uint64_t weight(const Row &r, float z, const uint32_t *powers) {
+__device__ __forceinline__ uint64_t weight(const Row &r, float z, const Shared &sh) {
     if (r.wide) return weight_wide(z, r.top, r.ch, r.cl);
     const float yh = __fmul_rn(z, r.ch), y = __fsub_rn(yh, r.y0);
     if (!(y > -(float)(kOne + 1) - 0.25f)) return 0;
@@ -159,17 +162,20 @@ __device__ __forceinline__ uint64_t weight(const Row &r, float z, const uint32_t
     const float g = __fmaf_rn(__fsub_rn(k, magic), -1.0f / kPowers, yh);
     const float t = __fmul_rn(__fadd_rn(__fsub_rn(g, r.gh), __fsub_rn(yl, r.gl)), 0.693147182464599609375f);
     const float p = __fmaf_rn(__fmul_rn(t, t), __fmaf_rn(t, 1.0f / 6.0f, 0.5f), t);
-    const int n = __float_as_int(k) - __float_as_int(magic) - r.n0, down = -(n >> 11);
+    const int n = __float_as_int(k) - __float_as_int(magic) - r.n0, down = -(n >> 11), j = n & (kPowers - 1);
+    const uint32_t base = sh.powers[j];
     if (down < 14) {
         if (z == r.top) return (uint64_t)1 << kOne;
-        return scaled(g_powers.v[n & (kPowers - 1)], __float2int_rn(__fmul_rn(p, 4398046511104.0f)), down);
+        return scaled((uint64_t)base << (kOne - 30) | sh.more[j], __float2int_rn(__fmul_rn(p, 4398046511104.0f)), down);
     }
     const int q = __float_as_int(__fmaf_rn(p, 4294967296.0f, magic)) - __float_as_int(magic);
-    const uint32_t base = powers[n & (kPowers - 1)], w = base + (uint32_t)__mulhi((int)base, q);
+    const uint32_t w = base + (uint32_t)__mulhi((int)base, q);
     uint32_t a;
     asm("shr.u32 %0, %1, %2;" : "=r"(a) : "r"(w), "r"(down - 14));     // (by 32 and more: 0)
     return (a >> 1) + (a & 1);
 }
+// The same where time does not matter: the code of all phases has to come to the SMs too.
+__device__ __noinline__ uint64_t weight_of_few(const Shared &sh, float z) { return weight(sh.row, z, sh); }
 
 // ceil or floor of f * x for 0 <= f <= 1.
 __device__ __forceinline__ uint64_t times(float f, uint64_t x, bool up) {
@@ -190,8 +196,30 @@ __device__ __forceinline__ uint64_t times(float f, uint64_t x, bool up) {
     return q + (up && rest ? 1 : 0);
 }
 
+// (z - top) / temperature - ln(total / 2^kOne), rounded once but for 2^-30 of itself: the quotient and the logarithm as pairs
+// of fp32.  ln(total / 2^kOne) = ln 2 * (e + j / kPowers) + ln(1 + x), x = total / (2^e g_powers[j]) - 1.
+__device__ __noinline__ float log_share(float z, float top, float temperature, uint64_t total) {
+    float y = 0.0f, y1 = 0.0f;
+    if (z != top) {
+        const float d = __fsub_rn(z, top), b = __fsub_rn(d, z), low = __fadd_rn(__fsub_rn(z, __fsub_rn(d, b)), __fsub_rn(-top, b));
+        y = __fdiv_rn(d, temperature);
+        if (fabsf(y) < INFINITY && fabsf(d) < INFINITY && fabsf(y) > 1e-30f) y1 = __fdiv_rn(__fadd_rn(__fmaf_rn(-y, temperature, d), low), temperature);
+    }
+    const int e = 63 - __clzll((long long)total) - kOne;               // total >= 2^kOne
+    const uint64_t m = total >> e;
+    const int j = min(kPowers - 1, max(0, (int)(__log2f((float)m * (1.0f / 8796093022208.0f)) * kPowers)));
+    const uint64_t base = g_powers.v[j];
+    const float x = __fdiv_rn((float)(int64_t)(m - base), (float)base);
+    const float ln2h = 0.693147182464599609375f, ln2l = -1.9046542943909386e-9f;
+    const float k = (float)e + (float)j * (1.0f / kPowers), l = __fmul_rn(k, ln2h);
+    const float l1 = __fadd_rn(__fmaf_rn(k, ln2l, __fmaf_rn(k, ln2h, -l)), __fmaf_rn(__fmul_rn(x, x), __fmaf_rn(x, 1.0f / 3.0f, -0.5f), x));
+    const float s = __fsub_rn(y, l), back = __fsub_rn(s, y);
+    return __fadd_rn(s, __fadd_rn(__fadd_rn(__fsub_rn(y, __fsub_rn(s, back)), __fsub_rn(-l, back)), __fsub_rn(y1, l1)));
+}
+
 // Sums of v over the threads before this one; `all`: over all of them.
-__device__ __forceinline__ uint64_t sums_before(uint64_t v, uint64_t *part, uint64_t &all) {
+template <int WARPS>
+__device__ __noinline__ uint64_t sums_before(uint64_t v, uint64_t *part, uint64_t &all) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t x = v;
 #pragma unroll
@@ -201,49 +229,62 @@ __device__ __forceinline__ uint64_t sums_before(uint64_t v, uint64_t *part, uint
     }
     if (lane == 31) part[warp] = x;
     __syncthreads();
-    uint64_t s = lane < kWarps ? part[lane] : 0;
+    uint64_t s = lane < WARPS ? part[lane] : 0;
 #pragma unroll
-    for (int m = 1; m < kWarps; m <<= 1) {
+    for (int m = 1; m < WARPS; m <<= 1) {
         const uint64_t y = __shfl_up_sync(0xffffffffu, s, m);
         if (lane >= m) s += y;
     }
-    all = __shfl_sync(0xffffffffu, s, kWarps - 1);
+    all = __shfl_sync(0xffffffffu, s, WARPS - 1);
     const uint64_t before = __shfl_sync(0xffffffffu, s, warp ? warp - 1 : 0);
     __syncthreads();
     return (warp ? before : 0) + x - v;
 }
 
-// a[0 .. n) ascending, by the whole CTA; n <= kCand, room for the next power of two.
-__device__ __forceinline__ void sort(uint64_t *a, int n) {
+// a[0 .. n) ascending, by the whole CTA (up to 64 elements by its first warp); n <= kCand, room for the next power of two.
+__device__ __noinline__ void sort(uint64_t *a, int n) {
     int n2 = 2;
     while (n2 < n) n2 *= 2;
-    for (int i = n + (int)threadIdx.x; i < n2; i += kThreads) a[i] = ~(uint64_t)0;
+    for (int i = n + (int)threadIdx.x; i < n2; i += (int)blockDim.x) a[i] = ~(uint64_t)0;
     __syncthreads();
-    for (int size = 2; size <= n2; size *= 2)
-        for (int half = size / 2; half > 0; half /= 2) {
-            const int i = (int)threadIdx.x / half * 2 * half + (int)threadIdx.x % half, j = i + half;
-            if (j < n2) {
-                const uint64_t x = a[i], y = a[j];
-                if ((x > y) == ((i & size) == 0)) {
-                    a[i] = y;
-                    a[j] = x;
+    const int t = (int)threadIdx.x;
+    if (n2 > 64 || t < 32) {
+#pragma unroll 1
+        for (int size = 2; size <= n2; size *= 2)
+#pragma unroll 1
+            for (int half = size / 2; half > 0; half /= 2) {
+                const int i = 2 * t - (t & (half - 1)), j = i + half;
+                if (j < n2) {
+                    const uint64_t x = a[i], y = a[j];
+                    if ((x > y) == ((i & size) == 0)) {
+                        a[i] = y;
+                        a[j] = x;
+                    }
                 }
+                if (n2 > 64) __syncthreads();
+                else __syncwarp();
             }
-            __syncthreads();
-        }
+    }
+    __syncthreads();
 }
 
 // STAGED: the slice lies in shared memory after the first pass, otherwise it is read again each time.
-template <typename T, bool STAGED>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams p, int ctas, int per, int vec) {
+template <typename T, bool STAGED, int THREADS>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const SampleParams p, int ctas, int per, int vec) {
+    constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+    constexpr bool kClean = STAGED && sizeof(T) == 4;                   // fp32: NaN is taken out as the slice is staged
     extern __shared__ __align__(16) uint8_t smem[];
     Shared &sh = *reinterpret_cast<Shared *>(smem);
     T *stage = reinterpret_cast<T *>(smem + sizeof(Shared));
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5, rank = (int)(blockIdx.x % (unsigned)ctas);
     const int64_t row = blockIdx.x / (unsigned)ctas;
-    for (int i = tid; i < kPowers; i += kThreads) sh.powers[i] = (uint32_t)(g_powers.v[i] >> (kOne - 30));
+    for (int i = tid; i < kPowers; i += kThreads) {
+        const uint64_t v = g_powers.v[i];
+        sh.powers[i] = (uint32_t)(v >> (kOne - 30));
+        sh.more[i] = (uint16_t)(v & ((1u << (kOne - 30)) - 1));
+    }
     if (tid == 0) {
-        sh.n_cand = 0;
+        sh.n_cand = sh.n_list = 0;
         sh.seg = -1;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -254,10 +295,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     };
     const int from = min(rank * per, p.V), n = min(per, p.V - from);
     const T *src = static_cast<const T *>(p.logits) + row * p.ld + from;
-    // NaN counts as -inf, -0 as 0
+    // NaN counts as -inf
     auto logit = [&](int i) {
         const float v = elem_to_float(STAGED ? stage[i] : src[i]);
-        return isnan(v) ? -INFINITY : v + 0.0f;
+        return kClean || !isnan(v) ? v : -INFINITY;
     };
 
     // ---- the first pass: the slice to shared memory, its largest and smallest finite logit ----
@@ -278,6 +319,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
 #pragma unroll
             for (int u = 0; u < kAhead; ++u) {
                 if (i + u * kThreads >= pieces) continue;
+                if constexpr (kClean) {
+                    float *e = reinterpret_cast<float *>(&v[u]);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) e[k] = isnan(e[k]) ? -INFINITY : e[k];
+                }
                 if constexpr (STAGED) reinterpret_cast<uint4 *>(stage)[i + u * kThreads] = v[u];
                 const T *e = reinterpret_cast<const T *>(&v[u]);
 #pragma unroll
@@ -287,7 +333,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         done = pieces * kVec;
     }
     for (int i = done + tid; i < n; i += kThreads) {
-        const T v = src[i];
+        T v = src[i];
+        if constexpr (kClean) v = isnan(v) ? -INFINITY : v;
         if constexpr (STAGED) stage[i] = v;
         look(elem_to_float(v));
     }
@@ -301,14 +348,6 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const int top_k = p.top_k ? p.top_k[row] : 0;
     const float u = p.u[row];
     __syncthreads();
-    if (tid == kThreads - 1) {
-        // what of the row's constants needs no maximum
-        const double c = 1.4426950408889634074 / (double)temperature;
-        sh.c = c;
-        sh.row.ch = (float)c;
-        sh.row.cl = fabsf((float)c) < INFINITY ? (float)(c - (double)(float)c) : 0.0f;
-        sh.row.least = min_p > 0.0f && min_p <= 1.0f ? (uint64_t)ceil((double)min_p * (double)((uint64_t)1 << kOne)) : 0;
-    }
     if (warp == 0) {
         const uint64_t both = sh.part[lane % kWarps];
         top = __uint_as_float((uint32_t)(both >> 32));
@@ -334,15 +373,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         }
         if (lane == 0) {
             Row &r = sh.row;
-            const double y0 = (double)(top + 0.0f) * sh.c;
+            // (pairs of fp32: a chain of fp64 operations takes microseconds on this GPU)
+            const float log2e_h = 1.44269502162933349609375f, log2e_l = 1.92596299112661746e-8f;      // log2(e) and what fp32 leaves of it
             r.top = top + 0.0f;
             r.scale = (float)(kBins - 1) / fminf(__fsub_rn(top, bottom), 64.0f * fmaxf(1.0f, temperature));   // (bottom = inf: 0 or less)
-            r.y0 = (float)y0;
-            r.wide = !(fabs(y0) < 900.0);
-            const double n0 = r.wide ? 0.0 : rint(y0 * kPowers), g = y0 - n0 / kPowers;
+            r.ch = __fdiv_rn(log2e_h, temperature);
+            r.cl = r.ch < INFINITY ? __fdiv_rn(__fadd_rn(__fmaf_rn(-r.ch, temperature, log2e_h), log2e_l), temperature) : 0.0f;
+            r.y0 = __fmul_rn(r.top, r.ch);
+            r.wide = !(fabsf(r.y0) < 900.0f) || r.ch < 1e-30f;         // (below that the remainder of the division is lost)
+            const float n0 = r.wide ? 0.0f : rintf(r.y0 * kPowers), y1 = __fmaf_rn(r.top, r.cl, __fmaf_rn(r.top, r.ch, -r.y0));
+            const float g = __fmaf_rn(n0, -1.0f / kPowers, r.y0);
             r.n0 = (int)n0;
-            r.gh = (float)g;
-            r.gl = (float)(g - (double)r.gh);
+            r.gh = __fadd_rn(g, y1);
+            const float back = __fsub_rn(r.gh, g);
+            r.gl = __fadd_rn(__fsub_rn(g, __fsub_rn(r.gh, back)), __fsub_rn(y1, back));
+            r.least = min_p > 0.0f && min_p <= 1.0f ? times(min_p, (uint64_t)1 << kOne, true) : 0;
         }
     }
     __syncthreads();
@@ -351,8 +396,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         if (!QMM_DCHECK(index >= 0 && index < p.V)) return;
         p.tokens[row] = index;
         if (!p.logp) return;
-        const double y = z == r.top ? 0.0 : ((double)z - (double)r.top) / (double)temperature;
-        p.logp[row] = (float)(y - log((double)total * (1.0 / (double)((uint64_t)1 << kOne))));
+        p.logp[row] = log_share(z, r.top, temperature, total);
     };
 
     if (r.top == -INFINITY || !(temperature > 0.0f) || top_k == 1 || min_p > 1.0f || top_p <= 0.0f) {
@@ -378,9 +422,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         return;
     }
 
-    // ---- what is kept: places up to `border` ----
-    uint64_t border = ~(uint64_t)0;
-    auto kept = [&](float z, int i) { return place_of(z, from + i) <= border; };
+    // ---- what is kept: places up to that of index border_i at logit border_z ----
+    float border_z = -INFINITY;
+    int border_i = INT_MAX;
+    auto kept = [&](float z, int i) { return z > border_z || (z == border_z && from + i <= border_i); };
+    auto set_border = [&](uint64_t place) {
+        border_z = logit_of(place);
+        border_i = (int)(uint32_t)place;
+    };
     auto clear = [&] {
         for (int i = tid; i < kBins; i += kThreads) sh.lo[i] = sh.hi[i] = 0;
         __syncthreads();
@@ -389,30 +438,70 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
         const uint32_t x = (uint32_t)w, old = atomicAdd(&sh.lo[bin], x), up = (uint32_t)(w >> 32) + (old + x < x ? 1u : 0u);
         if (up) atomicAdd(&sh.hi[bin], up);
     };
-    // Adds up the CTAs' histograms and finds the bin in which the sum from bin 0 on reaches want(sum of all): sh.bin, what is
-    // wanted of it sh.left, and the sum up to its end sh.upto.
-    auto find_bin = [&](bool sums, auto want) {
-        __syncthreads();
-        barrier();
-        uint64_t bin[4] = {0, 0, 0, 0};
-        for (int c = 0; c < ctas; ++c) {
-            const uint4 lo = remote_u128(&sh.lo[4 * tid], c);
-            bin[0] += lo.x; bin[1] += lo.y; bin[2] += lo.z; bin[3] += lo.w;
-            if (sums) {
-                const uint4 hi = remote_u128(&sh.hi[4 * tid], c);
-                bin[0] += (uint64_t)hi.x << 32; bin[1] += (uint64_t)hi.y << 32; bin[2] += (uint64_t)hi.z << 32; bin[3] += (uint64_t)hi.w << 32;
+    // Of the four bins that find_bins has found the one in question, as sh.bin, sh.left and sh.upto.  (The CTAs exchange sums of
+    // four bins, for all bins a CTA would read 64 KB of the others' memory: 3 us.)
+    auto find_bin_of_four = [&](bool sums) {
+        if (warp == 0) {
+            uint64_t s[4] = {0, 0, 0, 0};
+            if (lane < ctas) {
+                const uint4 lo = remote_u128(&sh.lo[sh.bin], lane);
+                s[0] = lo.x; s[1] = lo.y; s[2] = lo.z; s[3] = lo.w;
+                if (sums) {
+                    const uint4 hi = remote_u128(&sh.hi[sh.bin], lane);
+                    s[0] += (uint64_t)hi.x << 32; s[1] += (uint64_t)hi.y << 32; s[2] += (uint64_t)hi.z << 32; s[3] += (uint64_t)hi.w << 32;
+                }
+            }
+            uint64_t all = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+#pragma unroll
+                for (int m = 1; m < kMaxCluster; m <<= 1) s[k] += __shfl_xor_sync(0xffffffffu, s[k], m);
+                all += s[k];
+            }
+            if (lane == 0) {
+                uint64_t before = 0, left = sh.left, upto = sh.upto - all;
+                int bin = 0;
+                uint64_t in = s[0];
+#pragma unroll
+                for (int k = 1; k < 4; ++k) {
+                    if (bin == k - 1 && before + in < left) {
+                        before += in;
+                        in = s[k];
+                        bin = k;
+                    }
+                }
+                sh.bin += bin;
+                sh.left = left - before;
+                sh.upto = upto + before + in;
             }
         }
-        uint64_t all, before = sums_before(bin[0] + bin[1] + bin[2] + bin[3], sh.part, all);
-        const uint64_t w = want(all);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            if (before < w && before + bin[k] >= w) {
-                sh.bin = 4 * tid + k;
-                sh.left = w - before;
-                sh.upto = before + bin[k];
+        __syncthreads();
+    };
+    // Adds up the CTAs' histograms and finds the four bins in which the sum from bin 0 on reaches want(sum of all): sh.bin (the
+    // first of them), what is wanted of them sh.left, and the sum up to their end sh.upto.
+    auto find_bins = [&](bool sums, auto want) {
+        __syncthreads();
+        if (tid < kSums) {
+            uint64_t s = 0;
+            const uint4 lo = *reinterpret_cast<const uint4 *>(&sh.lo[4 * tid]);
+            s = (uint64_t)lo.x + lo.y + lo.z + lo.w;
+            if (sums) {
+                const uint4 hi = *reinterpret_cast<const uint4 *>(&sh.hi[4 * tid]);
+                s += ((uint64_t)hi.x + hi.y + hi.z + hi.w) << 32;
             }
-            before += bin[k];
+            sh.sums[tid] = s;
+        }
+        __syncthreads();
+        barrier();
+        uint64_t s = 0;
+        if (tid < kSums)
+            for (int c = 0; c < ctas; ++c) s += remote_u64(&sh.sums[tid], c);
+        uint64_t all;
+        const uint64_t before = sums_before<kWarps>(s, sh.part, all), w = want(all);
+        if (before < w && before + s >= w) {
+            sh.bin = 4 * tid;
+            sh.left = w - before;
+            sh.upto = before + s;
         }
         __syncthreads();
     };
@@ -420,22 +509,21 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     auto bin_of = [&](float z) { return min(kBins - 1, __float2int_rz(__fmul_rn(__fsub_rn(r.top, z), r.scale))); };   // (NaN gives bin 0: inf - inf)
     // The kept elements of bins first .. last to the first CTA (at most kCand of them; all are counted).
     auto gather = [&](int first, int last) {
-        for (int base = 0; base < n; base += kThreads) {
-            const int i = base + tid;
-            float z = 0.0f;
-            bool in = false;
-            if (i < n) {
-                z = logit(i);
-                const int b = bin_of(z);
-                in = b >= first && b <= last && kept(z, i);
-            }
-            const unsigned who = __ballot_sync(0xffffffffu, in);
-            if (who == 0) continue;
-            uint32_t at = 0;
-            if (lane == 0) at = remote_add(&sh.n_cand, 0, (uint32_t)__popc(who));
-            at = __shfl_sync(0xffffffffu, at, 0) + (uint32_t)__popc(who & ((1u << lane) - 1));
-            if (in && at < kCand) remote_store(&sh.cand[at], 0, place_of(z, from + i));
+#pragma unroll 4
+        for (int i = tid; i < n; i += kThreads) {
+            const float z = logit(i);
+            const int b = bin_of(z);
+            if (b < first || b > last || !kept(z, i)) continue;        // (they are few)
+            const uint32_t at = atomicAdd(&sh.n_list, 1u);
+            if (at < kCand) sh.list[at] = place_of(z, from + i);
         }
+        __syncthreads();
+        const uint32_t count = sh.n_list;
+        if (tid == 0 && count) sh.list_at = remote_add(&sh.n_cand, 0, count);
+        __syncthreads();
+        for (uint32_t k = tid; k < min(count, (uint32_t)kCand); k += kThreads)
+            if (sh.list_at + k < kCand) remote_store(&sh.cand[sh.list_at + k], 0, sh.list[k]);
+        if (tid == 0) sh.n_list = 0;
         __syncthreads();
         barrier();
     };
@@ -447,8 +535,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             if (sums) {
                 uint64_t w[2], all;
 #pragma unroll
-                for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < m ? weight(r, logit_of(sh.cand[2 * tid + k]), sh.powers) : 0;
-                uint64_t before = sums_before(w[0] + w[1], sh.part, all);
+                for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < m ? weight_of_few(sh, logit_of(sh.cand[2 * tid + k])) : 0;
+                uint64_t before = sums_before<kWarps>(w[0] + w[1], sh.part, all);
 #pragma unroll
                 for (int k = 0; k < 2; ++k) {
                     if (before < left && before + w[k] >= left) sh.border = sh.cand[2 * tid + k];
@@ -461,59 +549,78 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             __syncthreads();
         }
         barrier();
-        border = remote_u64(&sh.border, 0);
+        set_border(remote_u64(&sh.border, 0));
     };
-    // The border by the digits of the places, 11, 11 and 10 bits of the logit and twice 10 of the index: whatever the logits.
+    // The border by the digits of the places, 9 bits at a time, 32 of the logit and 20 of the index: whatever the logits.
     auto border_by_digits = [&](bool sums, uint64_t left) {
-        constexpr int kShift[5] = {53, 42, 32, 10, 0}, kBits[5] = {11, 11, 10, 10, 10};
-        uint64_t prefix = 0, mask = 0;
-        const uint64_t old = border;
-        for (int digit = 0; digit < 5; ++digit) {
-            const uint32_t low = (1u << kBits[digit]) - 1;
+        uint64_t prefix = 0;
+#pragma unroll 1
+        for (int digit = 0; digit < 7; ++digit) {
+            const int shift = digit < 4 ? 32 + (digit < 3 ? 23 - 9 * digit : 0) : (digit == 4 ? 11 : (digit == 5 ? 2 : 0));
+            const int bits = digit == 3 ? 5 : (digit == 6 ? 2 : 9);
             clear();
             for (int i = tid; i < n; i += kThreads) {
                 const float z = logit(i);
                 const uint64_t place = place_of(z, from + i);
-                if ((place & mask) != prefix || place > old) continue;
-                const int bin = (int)((place >> kShift[digit]) & low);
+                if (place >> shift >> bits != prefix || !kept(z, i)) continue;
+                const int bin = 4 * (int)((place >> shift) & ((1u << bits) - 1));
                 if (!sums) {
                     atomicAdd(&sh.lo[bin], 1u);
                 } else {
-                    const uint64_t w = weight(r, z, sh.powers);
+                    const uint64_t w = weight_of_few(sh, z);
                     if (w) add(bin, w);
                 }
             }
-            find_bin(sums, [&](uint64_t) { return left; });
-            prefix |= (uint64_t)(uint32_t)sh.bin << kShift[digit];
-            mask |= (uint64_t)low << kShift[digit];
+            find_bins(sums, [&](uint64_t) { return left; });
+            prefix = prefix << bits | (uint32_t)(sh.bin / 4);
             left = sh.left;
-            if (sums && digit == 2) {
-                // the logit is found: of its equals so many are kept
-                const uint64_t w = weight(r, logit_of(prefix), sh.powers);
-                left = w ? (left + w - 1) / w : 1;
-                sums = false;
+            if (digit == 3) {
+                prefix <<= 12;                                         // (an index has 20 bits)
+                if (sums) {
+                    // the logit is found: of its equals so many are kept
+                    const uint64_t w = weight_of_few(sh, unordered(~(uint32_t)(prefix >> 12)));
+                    left = w ? (left + w - 1) / w : 1;
+                    sums = false;
+                }
             }
             barrier();                                                 // before the histograms are cleared
         }
-        border = prefix;
+        set_border(prefix);
     };
 
-    if (top_k > 0 && top_k < p.V) {
+    // ---- the cuts, of counts and of sums ----
+#pragma unroll 1
+    for (int cut = 0; cut < 2; ++cut) {
+        const bool sums = cut == 1;
+        if (sums ? !(top_p < 1.0f) : !(top_k > 0 && top_k < p.V)) continue;
         clear();
-        for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.lo[bin_of(logit(i))], 1u);
-        find_bin(false, [&](uint64_t) { return (uint64_t)top_k; });
+        if (!sums) {
+#pragma unroll 4
+            for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.lo[bin_of(logit(i))], 1u);
+        } else {
+#pragma unroll 2
+            for (int i = tid; i < n; i += kThreads) {
+                const float z = logit(i);
+                const uint64_t w = kept(z, i) ? weight(r, z, sh) : 0;
+                if (w) add(bin_of(z), w);
+            }
+        }
+        uint64_t want = 0;
+        find_bins(sums, [&](uint64_t all) { return want = sums ? max((uint64_t)1, times(top_p, all, true)) : (uint64_t)top_k; });
+        find_bin_of_four(sums);
         const int bin = sh.bin;
         const uint64_t left = sh.left, upto = sh.upto;
-        if (upto <= kCand) {
+        const bool alone = !sums && upto <= kCand;
+        gather(alone ? 0 : bin, bin);
+        if (alone) {
             // ---- the first CTA alone: cuts in the order of the logits, then the token in the order of the indexes ----
-            gather(0, bin);
             if (rank != 0) return;
             uint64_t *ws = reinterpret_cast<uint64_t *>(sh.lo), *order = reinterpret_cast<uint64_t *>(sh.hi);
             sort(sh.cand, (int)upto);
             uint64_t w[2], all, total;
 #pragma unroll
-            for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < top_k && 2 * tid + k < (int)upto ? weight(r, logit_of(sh.cand[2 * tid + k]), sh.powers) : 0;
-            uint64_t before = sums_before(w[0] + w[1], sh.part, all);
+            for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < top_k && 2 * tid + k < (int)upto ? weight_of_few(sh, logit_of(sh.cand[2 * tid + k])) : 0;
+            uint64_t before = sums_before<kWarps>(w[0] + w[1], sh.part, all);
             const uint64_t want = top_p < 1.0f ? max((uint64_t)1, times(top_p, all, true)) : ~(uint64_t)0;
             int mine = 0;                                              // kept of this thread's two
 #pragma unroll
@@ -530,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             sort(order, m);
 #pragma unroll
             for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < m ? ws[(uint32_t)order[2 * tid + k]] : 0;
-            before = sums_before(w[0] + w[1], sh.part, total);
+            before = sums_before<kWarps>(w[0] + w[1], sh.part, total);
             const uint64_t target = u >= 1.0f ? total - 1 : (u > 0.0f ? times(u, total, false) : 0);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
@@ -542,36 +649,13 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
             }
             return;
         }
-        // (the elements of the bin: what lies in it, of the counts up to its end)
-        gather(bin, bin);
-        if (remote_u32(&sh.n_cand, 0) <= kCand) {
-            barrier();                                                 // the count is read before it is cleared
-            border_of_gathered(false, left);
+        const bool fits = remote_u32(&sh.n_cand, 0) <= kCand;
+        barrier();                                                     // the count is read before it is cleared
+        if (fits) {
+            border_of_gathered(sums, left);
         } else {
-            barrier();
             if (rank == 0 && tid == 0) sh.n_cand = 0;
-            border_by_digits(false, (uint64_t)top_k);
-        }
-    }
-    if (top_p < 1.0f) {
-        clear();
-        for (int i = tid; i < n; i += kThreads) {
-            const float z = logit(i);
-            if (!kept(z, i)) continue;
-            const uint64_t w = weight(r, z, sh.powers);
-            if (w) add(bin_of(z), w);
-        }
-        uint64_t want = 0;
-        find_bin(true, [&](uint64_t all) { return want = max((uint64_t)1, times(top_p, all, true)); });
-        const int bin = sh.bin;
-        const uint64_t left = sh.left;
-        gather(bin, bin);
-        if (remote_u32(&sh.n_cand, 0) <= kCand) {
-            barrier();
-            border_of_gathered(true, left);
-        } else {
-            barrier();
-            border_by_digits(true, want);
+            border_by_digits(sums, want);
         }
     }
 
@@ -580,17 +664,22 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     auto weight_of = [&](int i) -> uint64_t {
         const float z = logit(i);
         if (!kept(z, i)) return 0;
-        const uint64_t w = weight(r, z, sh.powers);
+        const uint64_t w = weight_of_few(sh, z);
         return w >= r.least ? w : 0;
     };
     {
         uint64_t sum = 0;
         const int end = min(n, (warp + 1) * seg_len);
-        if (border == ~(uint64_t)0 && r.least == 0) {
+        if (border_i == INT_MAX && r.least == 0) {                     // all are kept
 #pragma unroll 4
-            for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight(r, elem_to_float(STAGED ? stage[i] : src[i]), sh.powers);
+            for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight(r, logit(i), sh);
         } else {
-            for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight_of(i);
+#pragma unroll 2
+            for (int i = warp * seg_len + lane; i < end; i += 32) {
+                const float z = logit(i);
+                const uint64_t w = kept(z, i) ? weight(r, z, sh) : 0;
+                sum += w >= r.least ? w : 0;
+            }
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -602,7 +691,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     {
         // thread j has segment j % kWarps of CTA j / kWarps
         const uint64_t sum = tid < ctas * kWarps ? remote_u64(&sh.seg_sum[tid % kWarps], tid / kWarps) : 0;
-        const uint64_t before = sums_before(sum, sh.part, total);
+        const uint64_t before = sums_before<kWarps>(sum, sh.part, total);
         // u beyond [0, 1) counts as its nearest end, NaN as 0
         const uint64_t target = u >= 1.0f ? total - 1 : (u > 0.0f ? times(u, total, false) : 0);
         if (before <= target && target < before + sum) {
@@ -619,7 +708,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     const int i0 = min(end, begin + tid * each), i1 = min(end, i0 + each);
     uint64_t all, sum = 0;
     for (int i = i0; i < i1; ++i) sum += weight_of(i);
-    uint64_t before = sums_before(sum, sh.part, all);
+    uint64_t before = sums_before<kWarps>(sum, sh.part, all);
     if (before <= sh.target && sh.target < before + sum) {
         for (int i = i0; i < i1; ++i) {
             before += weight_of(i);
@@ -631,14 +720,14 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
 }
 
-template <typename T, bool STAGED>
+template <typename T, bool STAGED, int THREADS>
 cudaError_t launch(const SampleParams &p, int ctas, int per, int vec, cudaStream_t s) {
     const size_t smem = sizeof(Shared) + (STAGED ? ((size_t)per * sizeof(T) + 15) / 16 * 16 : 0);
     static int done[4] = {0, 0, 0, 0};
-    const cudaError_t e = ensure_smem_limit(sample_kernel<T, STAGED>, 227 * 1024, done);
+    const cudaError_t e = ensure_smem_limit(sample_kernel<T, STAGED, THREADS>, 227 * 1024, done);
     if (e != cudaSuccess) return e;
     if (p.R * ctas > 0x7fffffff) return cudaErrorInvalidValue;
-    return launch_pdl_cluster(sample_kernel<T, STAGED>, dim3((unsigned)(p.R * ctas)), (unsigned)ctas, kThreads, smem, s, p, ctas, per, vec);
+    return launch_pdl_cluster(sample_kernel<T, STAGED, THREADS>, dim3((unsigned)(p.R * ctas)), (unsigned)ctas, THREADS, smem, s, p, ctas, per, vec);
 }
 
 }  // namespace
@@ -646,15 +735,15 @@ cudaError_t launch(const SampleParams &p, int ctas, int per, int vec, cudaStream
 cudaError_t launch_sample(qmm_dtype t, const SampleParams &p, cudaStream_t s) {
     return with_dtype(t, [&](auto z) {
         using T = decltype(z);
-        // slices of 64 KB, two CTAs an SM; smaller ones where rows are few
-        constexpr int kSlice = 64 * 1024 / (int)sizeof(T);
+        // slices of 60 KB, two CTAs an SM; smaller ones where rows are few, and there one CTA of twice the threads
+        constexpr int kSlice = 60 * 1024 / (int)sizeof(T);
         int ctas = 1;
         while (ctas < kMaxCluster && (int64_t)ctas * kSlice < p.V) ctas *= 2;
         while (ctas < kMaxCluster && p.R * ctas * 2 <= 152 && p.V / (ctas * 2) >= 2048) ctas *= 2;
         const int per = ((p.V + ctas - 1) / ctas + 15) / 16 * 16;
         const bool vec = (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && (p.ld * (int64_t)sizeof(T)) % 16 == 0;
-        if (sizeof(Shared) + (size_t)per * sizeof(T) <= 227 * 1024) return launch<T, true>(p, ctas, per, vec, s);
-        return launch<T, false>(p, ctas, per, vec, s);
+        if (sizeof(Shared) + (size_t)per * sizeof(T) > 227 * 1024) return launch<T, false, 512>(p, ctas, per, vec, s);
+        return p.R * ctas <= 152 ? launch<T, true, 1024>(p, ctas, per, vec, s) : launch<T, true, 512>(p, ctas, per, vec, s);
     });
 }
 
