@@ -198,7 +198,7 @@ __device__ __forceinline__ uint64_t times(float f, uint64_t x, bool up) {
 
 // (z - top) / temperature - ln(total / 2^kOne), rounded once but for 2^-30 of itself: the quotient and the logarithm as pairs
 // of fp32.  ln(total / 2^kOne) = ln 2 * (e + j / kPowers) + ln(1 + x), x = total / (2^e g_powers[j]) - 1.
-__device__ __noinline__ float log_share(float z, float top, float temperature, uint64_t total) {
+__device__ __noinline__ float log_share(const Shared &sh, float z, float top, float temperature, uint64_t total) {
     float y = 0.0f, y1 = 0.0f;
     if (z != top) {
         const float d = __fsub_rn(z, top), b = __fsub_rn(d, z), low = __fadd_rn(__fsub_rn(z, __fsub_rn(d, b)), __fsub_rn(-top, b));
@@ -208,7 +208,7 @@ __device__ __noinline__ float log_share(float z, float top, float temperature, u
     const int e = 63 - __clzll((long long)total) - kOne;               // total >= 2^kOne
     const uint64_t m = total >> e;
     const int j = min(kPowers - 1, max(0, (int)(__log2f((float)m * (1.0f / 8796093022208.0f)) * kPowers)));
-    const uint64_t base = g_powers.v[j];
+    const uint64_t base = (uint64_t)sh.powers[j] << (kOne - 30) | sh.more[j];
     const float x = __fdiv_rn((float)(int64_t)(m - base), (float)base);
     const float ln2h = 0.693147182464599609375f, ln2l = -1.9046542943909386e-9f;
     const float k = (float)e + (float)j * (1.0f / kPowers), l = __fmul_rn(k, ln2h);
@@ -242,6 +242,7 @@ __device__ __noinline__ uint64_t sums_before(uint64_t v, uint64_t *part, uint64_
 }
 
 // a[0 .. n) ascending, by the whole CTA (up to 64 elements by its first warp); n <= kCand, room for the next power of two.
+// (In registers, with shuffles between the lanes of a warp: 64 elements as fast, 1024 in 512 threads slower.)
 __device__ __noinline__ void sort(uint64_t *a, int n) {
     int n2 = 2;
     while (n2 < n) n2 *= 2;
@@ -338,6 +339,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         if constexpr (STAGED) stage[i] = v;
         look(elem_to_float(v));
     }
+    const float own_top = top;
 #pragma unroll
     for (int m = 16; m > 0; m >>= 1) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
@@ -396,7 +398,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         if (!QMM_DCHECK(index >= 0 && index < p.V)) return;
         p.tokens[row] = index;
         if (!p.logp) return;
-        p.logp[row] = log_share(z, r.top, temperature, total);
+        p.logp[row] = log_share(sh, z, r.top, temperature, total);
     };
 
     if (r.top == -INFINITY || !(temperature > 0.0f) || top_k == 1 || min_p > 1.0f || top_p <= 0.0f) {
@@ -494,8 +496,13 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         __syncthreads();
         barrier();
         uint64_t s = 0;
-        if (tid < kSums)
-            for (int c = 0; c < ctas; ++c) s += remote_u64(&sh.sums[tid], c);
+        if (tid < kSums) {
+            uint64_t of[kMaxCluster];                                  // all under way before the first is added
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) of[c] = c < ctas ? remote_u64(&sh.sums[tid], c) : 0;
+#pragma unroll
+            for (int c = 0; c < kMaxCluster; ++c) s += of[c];
+        }
         uint64_t all;
         const uint64_t before = sums_before<kWarps>(s, sh.part, all), w = want(all);
         if (before < w && before + s >= w) {
@@ -593,25 +600,39 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     for (int cut = 0; cut < 2; ++cut) {
         const bool sums = cut == 1;
         if (sums ? !(top_p < 1.0f) : !(top_k > 0 && top_k < p.V)) continue;
-        clear();
-        if (!sums) {
+        // The k largest logits lie no lower than the k-th largest of the threads' maxima: where k is small a histogram of those alone,
+        // one logit a thread, leaves few candidates.  (Shared memory takes about two atomic additions a cycle.)
+        bool alone, quick = !sums && 8 * top_k <= kThreads * ctas;
+        int bin;
+        uint64_t left, upto, want;
+#pragma unroll 1
+        while (true) {
+            clear();
+            if (quick) {
+                atomicAdd(&sh.lo[bin_of(own_top)], 1u);
+            } else if (!sums) {
 #pragma unroll 4
-            for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.lo[bin_of(logit(i))], 1u);
-        } else {
+                for (int i = tid; i < n; i += kThreads) atomicAdd(&sh.lo[bin_of(logit(i))], 1u);
+            } else {
 #pragma unroll 2
-            for (int i = tid; i < n; i += kThreads) {
-                const float z = logit(i);
-                const uint64_t w = kept(z, i) ? weight(r, z, sh) : 0;
-                if (w) add(bin_of(z), w);
+                for (int i = tid; i < n; i += kThreads) {
+                    const float z = logit(i);
+                    const uint64_t w = kept(z, i) ? weight(r, z, sh) : 0;
+                    if (w) add(bin_of(z), w);
+                }
             }
+            find_bins(sums, [&](uint64_t all) { return want = sums ? max((uint64_t)1, times(top_p, all, true)) : (uint64_t)top_k; });
+            find_bin_of_four(sums);
+            bin = sh.bin;
+            left = sh.left;
+            alone = quick || (!sums && sh.upto <= kCand);
+            gather(alone ? 0 : bin, bin);
+            upto = remote_u32(&sh.n_cand, 0);
+            barrier();                                                 // the count is read before it is cleared
+            if (!quick || upto <= kCand) break;
+            if (rank == 0 && tid == 0) sh.n_cand = 0;
+            quick = false;
         }
-        uint64_t want = 0;
-        find_bins(sums, [&](uint64_t all) { return want = sums ? max((uint64_t)1, times(top_p, all, true)) : (uint64_t)top_k; });
-        find_bin_of_four(sums);
-        const int bin = sh.bin;
-        const uint64_t left = sh.left, upto = sh.upto;
-        const bool alone = !sums && upto <= kCand;
-        gather(alone ? 0 : bin, bin);
         if (alone) {
             // ---- the first CTA alone: cuts in the order of the logits, then the token in the order of the indexes ----
             if (rank != 0) return;
@@ -649,9 +670,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             }
             return;
         }
-        const bool fits = remote_u32(&sh.n_cand, 0) <= kCand;
-        barrier();                                                     // the count is read before it is cleared
-        if (fits) {
+        if (upto <= kCand) {
             border_of_gathered(sums, left);
         } else {
             if (rank == 0 && tid == 0) sh.n_cand = 0;
