@@ -12,6 +12,7 @@
 
 #include "cache.cuh"
 #include "elem.cuh"
+#include "tc_common.cuh"
 
 namespace qmm {
 namespace {
@@ -204,39 +205,75 @@ __device__ __forceinline__ bool find_token(const SelectParams &p, const Sequence
     return true;
 }
 
-constexpr int kScoreThreads = 128, kTokTile = 8;
+constexpr int kScoreWarps = 4, kScoreThreads = kScoreWarps * 32, kTokTile = 8, kScorePages = kScoreWarps * 16;
 
-// A thread takes a page, whose codes stay in its registers, for up to kTokTile tokens (neighbouring rows of q; rows of another
-// sequence load their own page) and all query rows of a head, whose codes (positive and negative ones apart) it reads from
-// shared memory, the same for all threads.
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Bytes of a query row's codes in fp16 for one sign: neighbouring rows 64 bytes apart, modulo the banks' 128.
+constexpr int score_pitch(int DB) { return DB * 64 + (DB % 2 == 0 ? 64 : 0); }
+
+// Pages are the 16 rows of an mma (m16n8k16), query rows its 8 columns; codes are exact in fp16, and so are their sums in
+// fp32 (below 2^20), so the tensor cores give the whole numbers S.  A warp takes 16 pages, whose codes stay in its registers, for
+// up to kTokTile tokens (neighbouring rows of q; rows of another sequence load their own pages).  The columns of a
+// product are the query heads of one token, 8 at a time, or of 8 / span tokens with span >= group a power of two, so
+// that the maximum over a group is one over neighbouring columns.
 template <int DB>
 __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const SelectParams p) {
-    constexpr int D = DB * 32, BB = (2 * D + 2 * DB + 15) / 16 * 16;
+    constexpr int D = DB * 32, BB = (2 * D + 2 * DB + 15) / 16 * 16, kPitch = score_pitch(DB);
     extern __shared__ __align__(16) uint8_t smem[];
+    // the tile's products: tokens s_from[i] .. s_from[i + 1] - 1 of sequence s_seq[i], which ask about s_most[i] pages at most
+    __shared__ int s_seen[kTokTile], s_from[kTokTile + 1], s_seq[kTokTile], s_most[kTokTile], s_n;
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    const int h = (int)(blockIdx.y % (unsigned)p.H);
-    const int64_t row0 = (int64_t)blockIdx.x * p.tok_tile, cta0 = (int64_t)(blockIdx.y / (unsigned)p.H) * kScoreThreads;
-    const int64_t stride = (int64_t)(gridDim.y / (unsigned)p.H) * kScoreThreads;
+    const int h = (int)(blockIdx.y % (unsigned)p.H), lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int64_t row0 = (int64_t)blockIdx.x * p.tok_tile;
+    const int cta0 = (int)(blockIdx.y / (unsigned)p.H) * kScorePages, stride = (int)(gridDim.y / (unsigned)p.H) * kScorePages;
     const int toks = (int)min((int64_t)p.tok_tile, p.T - row0);
-    Token tok[kTokTile];
-    int64_t all = 0;                                                   // pages that any token of the tile asks about
-    Sequence of = find_sequence(p, row0);
-#pragma unroll
-    for (int k = 0; k < kTokTile; ++k) {
-        tok[k] = {-1, 0, 0};
-        if (k < toks && k > 0 && row0 + k >= of.q1) of = find_sequence(p, row0 + k);
-        // where all pages are chosen, nobody asks for scores
-        if (k < toks && find_token(p, of, row0 + k, tok[k]) && tok[k].seen > p.budget) all = max(all, tok[k].seen);
-        else tok[k].seen = 0;
+    const int log_span = p.group > 4 ? 3 : (p.group > 2 ? 2 : p.group - 1), span = 1 << log_span, per = p.group > 8 ? 1 : 8 >> log_span;
+    int all = 0;                                                       // pages that any token of the tile asks about
+    {
+        Sequence of = find_sequence(p, row0);
+        int n = 0, from = 0, seq = -1, most = 0;                       // the product that is being filled
+        for (int k = 0; k < toks; ++k) {
+            if (k > 0 && row0 + k >= of.q1) of = find_sequence(p, row0 + k);
+            Token tok;
+            // where all pages are chosen, nobody asks for scores
+            int seen = 0;
+            if (find_token(p, of, row0 + k, tok) && tok.seen > p.budget) seen = (int)tok.seen;
+            if (k > 0 && (k - from == per || (int)of.s != seq)) {
+                if (threadIdx.x == 0) {
+                    s_from[n] = from;
+                    s_seq[n] = seq;
+                    s_most[n] = most;
+                }
+                ++n;
+                from = k;
+                most = 0;
+            }
+            seq = (int)of.s;
+            most = max(most, seen);
+            all = max(all, seen);
+            if (threadIdx.x == 0) s_seen[k] = seen;
+        }
+        if (threadIdx.x == 0) {
+            s_from[n] = from;
+            s_seq[n] = seq;
+            s_most[n] = most;
+            s_from[n + 1] = toks;
+            s_n = n + 1;
+        }
     }
     if (all <= cta0) return;
-    // ---- the tile's query rows, a warp a row ----
-    const int lane = threadIdx.x & 31, rows = toks * p.group;
-    uint8_t *codes = smem;                                             // [row][2][D]: negative, positive
-    float *dq = reinterpret_cast<float *>(smem + p.tok_tile * p.group * 2 * D);   // [row][DB]
-    for (int r = threadIdx.x >> 5; r < rows; r += kScoreThreads / 32) {
+    // ---- the tile's query rows, a warp a row: [row][negative, positive] codes as fp16, [row][DB] scales ----
+    const int rows = toks * p.group;
+    float *dq = reinterpret_cast<float *>(smem + p.tok_tile * p.group * 2 * kPitch);
+    for (int r = warp; r < rows; r += kScoreWarps) {
         const int64_t src = (row0 + r / p.group) * p.ldq + (int64_t)(h * p.group + r % p.group) * D + lane;
+        __half *codes = reinterpret_cast<__half *>(smem + r * 2 * kPitch);
 #pragma unroll
         for (int b = 0; b < DB; ++b) {
             const float x = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q)[src + 32 * b])
@@ -245,58 +282,92 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
             const bool fine = top < 0x7F800000u;
             const float d = fine ? q8_scale(__uint_as_float(top)) : 0.0f;
             const int a = fine ? q8_code(x, inv_or_zero(d)) : 0;
-            codes[r * 2 * D + 32 * b + lane] = (uint8_t)(int8_t)min(a, 0);
-            codes[r * 2 * D + D + 32 * b + lane] = (uint8_t)max(a, 0);
+            codes[32 * b + lane] = __int2half_rn(min(a, 0));
+            codes[kPitch / 2 + 32 * b + lane] = __int2half_rn(max(a, 0));
             if (lane == 0) dq[r * DB + b] = fine ? d : NAN;
         }
     }
     __syncthreads();
-    for (int64_t number = cta0 + threadIdx.x; number < all; number += stride) {
-        uint4 c[DB * 4];                                                   // lowest: 2 a block, then highest
-        float d[DB];
-        int64_t loaded = -1;
-        bool there = false;
+    // a lane has pages page0 + g and + 8, and of each block of codes the eight from 8 t on
+    for (int page0 = cta0 + warp * 16; page0 < all; page0 += stride) {
+        uint32_t a[DB][2][2][4];                                       // [block][lowest, highest][k step][registers]
+        float d[DB][2];
+        int loaded = -1;
+        bool there[2] = {false, false};
+        for (int i = 0; i < s_n; ++i) {
+            if (s_most[i] <= page0) continue;
+            if (s_seq[i] != loaded) {
+                loaded = s_seq[i];
 #pragma unroll
-        for (int k = 0; k < kTokTile; ++k) {
-            if (number >= tok[k].seen || !QMM_DCHECK(number < p.ld_pages && number < p.most)) continue;
-            if (tok[k].s != loaded) {
-                loaded = tok[k].s;
-                const int64_t page = p.pages[loaded * p.ld_pages + number];
-                there = page >= 0 && page < p.n_pages;
-                if (there) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(p.bounds + (page * p.H + h) * BB);
+                for (int e = 0; e < 2; ++e) {
+                    const int number = page0 + g + 8 * e;
+                    const int page = number < p.ld_pages && number < p.most ? p.pages[loaded * p.ld_pages + number] : -1;
+                    there[e] = page >= 0 && page < p.n_pages;
+                    const uint8_t *src = p.bounds + ((int64_t)(there[e] ? page : 0) * p.H + h) * BB;
 #pragma unroll
-                    for (int i = 0; i < DB * 4; ++i) c[i] = src[i];
-                    const __half *ds = reinterpret_cast<const __half *>(src + DB * 4);
+                    for (int b = 0; b < DB; ++b) {
 #pragma unroll
-                    for (int b = 0; b < DB; ++b) d[b] = __half2float(ds[b]);
+                        for (int x = 0; x < 2; ++x) {
+                            const uint2 c = *reinterpret_cast<const uint2 *>(src + x * D + 32 * b + 8 * t);
+                            tc::i8x4_to_h2x2(c.x, a[b][x][0][e], a[b][x][0][2 + e]);
+                            tc::i8x4_to_h2x2(c.y, a[b][x][1][e], a[b][x][1][2 + e]);
+                        }
+                        d[b][e] = __half2float(reinterpret_cast<const __half *>(src + 2 * D)[b]);
+                    }
                 }
             }
-            float best = -INFINITY;
-            for (int g = 0; g < p.group && there; ++g) {
-                const int r = k * p.group + g;
-                const uint4 *a = reinterpret_cast<const uint4 *>(codes + r * 2 * D);
-                float score = 0.0f;
+            const int k0 = s_from[i], k1 = s_from[i + 1];
+            float best[2][2];                                          // [page g, g + 8][column 2t, 2t + 1]
+            best[0][0] = best[0][1] = best[1][0] = best[1][1] = -INFINITY;
+            for (int turn = 0; turn < p.group; turn += 8) {
+                // the query row of a column; the tile's first in the place of those that have none
+                auto row_of = [&](int c) {
+                    const int k = k0 + (c >> log_span), q = turn + (c & (span - 1));
+                    return k < k1 && q < p.group ? k * p.group + q : -1;
+                };
+                const int r0 = row_of(2 * t), r1 = row_of(2 * t + 1);
+                const uint8_t *codes = smem + max(row_of(g), 0) * 2 * kPitch + 16 * t;
+                const float *dq0 = dq + max(r0, 0) * DB, *dq1 = dq + max(r1, 0) * DB;
+                float score[2][2] = {{0.0f, 0.0f}, {0.0f, 0.0f}};
 #pragma unroll
                 for (int b = 0; b < DB; ++b) {
-                    int x = 0, y = 0;
+                    const uint4 lo = *reinterpret_cast<const uint4 *>(codes + 64 * b), hi = *reinterpret_cast<const uint4 *>(codes + kPitch + 64 * b);
+                    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    mma16816(acc, a[b][0][0], lo.x, lo.y);
+                    mma16816(acc, a[b][0][1], lo.z, lo.w);
+                    mma16816(acc, a[b][1][0], hi.x, hi.y);
+                    mma16816(acc, a[b][1][1], hi.z, hi.w);
+                    const float d0 = dq0[b], d1 = dq1[b];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint4 m = a[2 * b + i], q = a[DB * 2 + 2 * b + i], lo = c[2 * b + i], hi = c[DB * 2 + 2 * b + i];
-                        x = __dp4a((int)m.x, (int)lo.x, x);
-                        x = __dp4a((int)m.y, (int)lo.y, x);
-                        x = __dp4a((int)m.z, (int)lo.z, x);
-                        x = __dp4a((int)m.w, (int)lo.w, x);
-                        y = __dp4a((int)q.x, (int)hi.x, y);
-                        y = __dp4a((int)q.y, (int)hi.y, y);
-                        y = __dp4a((int)q.z, (int)hi.z, y);
-                        y = __dp4a((int)q.w, (int)hi.w, y);
+                    for (int e = 0; e < 2; ++e) {
+                        score[e][0] = __fadd_rn(score[e][0], __fmul_rn(__fmul_rn(d0, d[b][e]), acc[2 * e]));
+                        score[e][1] = __fadd_rn(score[e][1], __fmul_rn(__fmul_rn(d1, d[b][e]), acc[2 * e + 1]));
                     }
-                    score = __fadd_rn(score, __fmul_rn(__fmul_rn(dq[r * DB + b], d[b]), (float)(x + y)));
                 }
-                best = isnan(score) ? INFINITY : fmaxf(best, score);
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (r0 >= 0) best[e][0] = isnan(score[e][0]) ? INFINITY : fmaxf(best[e][0], score[e][0]);
+                    if (r1 >= 0) best[e][1] = isnan(score[e][1]) ? INFINITY : fmaxf(best[e][1], score[e][1]);
+                }
             }
-            p.scores[((row0 + k) * p.H + h) * p.most + number] = best;
+            // the maximum over a token's columns: in its first one; with one column each, a lane has two tokens
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                if (log_span >= 1) best[e][0] = fmaxf(best[e][0], best[e][1]);
+                if (log_span >= 2) best[e][0] = fmaxf(best[e][0], __shfl_xor_sync(0xffffffffu, best[e][0], 1));
+                if (log_span >= 3) best[e][0] = fmaxf(best[e][0], __shfl_xor_sync(0xffffffffu, best[e][0], 2));
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int col = 2 * t + c, k = k0 + (col >> log_span);
+                if ((col & (span - 1)) != 0 || k >= k1) continue;
+                float *out = p.scores + ((row0 + k) * p.H + h) * p.most;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int number = page0 + g + 8 * e;
+                    if (number < s_seen[k] && QMM_DCHECK(number < p.most && number < p.ld_pages)) out[number] = there[e] ? best[e][c] : -INFINITY;
+                }
+            }
         }
     }
 }
@@ -479,11 +550,16 @@ __global__ void __launch_bounds__(kChooseThreads) cache_choose_kernel(const Sele
 
 template <int DB>
 cudaError_t launch_score(const SelectParams &p, cudaStream_t s) {
-    const size_t smem = (size_t)p.tok_tile * p.group * (2 * DB * 32 + DB * 4);    // up to 64 rows: 35 KB
-    // each CTA prepares the tile's query rows for itself, so it takes as many pages as leave the GPU four CTAs an SM
-    const int64_t x = (p.T + p.tok_tile - 1) / p.tok_tile, chunks = (p.most + kScoreThreads - 1) / kScoreThreads;
-    int64_t split = (4 * 152 + x * p.H - 1) / (x * p.H);
+    const size_t smem = (size_t)p.tok_tile * p.group * (2 * score_pitch(DB) + DB * 4);    // up to 64 rows: 76 KB
+    static int done[4] = {0, 0, 0, 0};
+    const cudaError_t e = ensure_smem_limit(cache_score_kernel<DB>, 64 * (2 * score_pitch(DB) + DB * 4), done);
+    if (e != cudaSuccess) return e;
+    // each CTA prepares the tile's query rows for itself, so it takes as many pages as leave the GPU about three CTAs an SM
+    const int64_t x = (p.T + p.tok_tile - 1) / p.tok_tile, chunks = (p.most + kScorePages - 1) / kScorePages;
+    int64_t split = (3 * 152 + x * p.H - 1) / (x * p.H);
     split = split < chunks ? split : chunks;
+    const int64_t turns = (chunks + split - 1) / split;
+    split = (chunks + turns - 1) / turns;
     if (x > 0x7fffffff || split * p.H > 65535) return cudaErrorInvalidValue;
     return launch_pdl(cache_score_kernel<DB>, dim3((unsigned)x, (unsigned)(split * p.H)), kScoreThreads, smem, s, p);
 }
