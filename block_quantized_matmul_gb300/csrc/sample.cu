@@ -15,6 +15,10 @@
 //
 // A cluster of up to 8 CTAs takes a row, each CTA a slice of it that stays in shared memory from the first pass on.  What the
 // CTAs find is exchanged through distributed shared memory: each adds up all histograms for itself.
+//
+// What bounds it.  Few rows: a chain of passes, barriers of the cluster (about a microsecond each) and sorts: greedy 4.5 us, plain 10.7,
+// top_k = 50 15.9, top_p = 0.95 27.3 (128256 logits).  Many rows: the instructions of `weight`, about 30 a logit and pass (256
+// rows of 128256 fp32 logits, plain: 132 us, 60 % of the issue slots, for 19.6 us of bytes), and with top_p its atomic additions.
 #include <climits>
 
 #include "qmm_internal.cuh"
@@ -287,6 +291,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
     if (tid == 0) {
         sh.n_cand = sh.n_list = 0;
         sh.seg = -1;
+        sh.bin = 0;
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -550,7 +555,7 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
                     before += w[k];
                 }
             } else if (tid == 0) {
-                sh.border = sh.cand[(int)left - 1];
+                sh.border = sh.cand[min((int)left, m) - 1];
             }
             if (tid == 0) sh.n_cand = 0;
             __syncthreads();

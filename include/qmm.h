@@ -593,6 +593,8 @@ QMM_API size_t qmm_cache_select_workspace_size(int64_t T, int64_t H, int64_t P, 
  * then those of the highest scores, the earlier page on ties, until there are `budget` in all.  (If more than `budget` pages are
  * always chosen, the first of them are.)
  * Rows of no sequence, of sequences whose rows do not all lie in q, and past max_new, are left as they are.
+ *   workspace_dev  >= qmm_cache_select_workspace_size(T, H, P, max_len) bytes, 256-byte aligned, overwritten; calls that overlap on the
+ *                GPU (replays of two captured graphs too) must use different workspaces.
  * T = 0 does nothing.  Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
  * Errors: INVALID_ARG (sizes, strides, NULL, Hq % H, recent < 1, sinks < 0, budget < sinks + recent (+ ceil((max_new - 1) / P) with
  * tree words), budget > 65536, tree words with max_new > 64, workspace too small), UNSUPPORTED (dt), MISALIGNED, CUDA.
@@ -680,8 +682,9 @@ QMM_API qmm_status qmm_norm_mx4(qmm_dtype xdt, const void *x_dev, int64_t ldx, q
  * the first in rank is always kept.  The token is the first index at which the sum of the kept w up to and including it exceeds u
  * times the sum of all kept; logp is ln of its share.  temperature <= 0 (or NaN): the first in rank, logp 0.  A row
  * in which every logit is -inf or NaN gives token -1 and logp -inf.  An infinite maximum leaves the +inf ones, equally likely.
- * w is held in fixed point, 2^-43 of the largest, within 2^-41, and sums are exact from there: the result does not depend on
- * the order of summation, and differs from the formula's only where u or top_p lies within about V * 2^-43 of a border.
+ * w is held in fixed point, to the nearest 2^-43 of the largest but for 2^-34 of itself, and sums are exact from there: the result
+ * does not depend on the order of summation, and differs from the formula's only where u, top_p or min_p lies within about
+ * 2^-33 + V * 2^-43 of a border.
  * V is at most 2^20; R = 0 does nothing.
  * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
  * Errors: INVALID_ARG (R < 0, V <= 0, V > 2^20, ld < V, NULL), UNSUPPORTED (dt), MISALIGNED, CUDA.

@@ -31,8 +31,8 @@ def text_of(name):
 @pytest.mark.parametrize("name,access", [
     ("attend_mma.cuh", "table[j >> p.log_p]"), ("attend_mma.cuh", "table[number]"), ("attend_mma.cuh", "cp_async16(dst + L::kK "),
     ("attend_mma.cuh", "cp_async16(dst + L::kKs"), ("attend.cuh", "p.pages[w.s * p.ld_pages + number]"), ("cache_plan.cu", "p.ring[to] ="),
-    ("cache_plan.cu", "p.pages + (base + lo)"), ("cache_select.cu", "p.pages[s * p.ld_pages + number]"), ("sample.cu", "p.tokens[row] = from + i"),
-    ("norm.cu", "store8<VEC>(h[c], out"),
+    ("cache_plan.cu", "p.pages + (base + lo)"), ("cache_select.cu", "p.pages[s * p.ld_pages + number]"), ("sample.cu", "p.tokens[row] = index;"),
+    ("norm.cu", "store8<VEC>(r, const_cast<void *>(row_of(p.h_out"),
 ])
 def test_accesses_by_device_data_are_checked(name, access):
     """A check stands within the thirty lines before the access, or on its line."""
