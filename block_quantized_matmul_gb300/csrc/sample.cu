@@ -16,9 +16,9 @@
 // A cluster of up to 8 CTAs takes a row, each CTA a slice of it that stays in shared memory from the first pass on.  What the
 // CTAs find is exchanged through distributed shared memory: each adds up all histograms for itself.
 //
-// What bounds it.  Few rows: a chain of passes, barriers of the cluster (about a microsecond each) and sorts: greedy 4.5 us, plain 10.7,
-// top_k = 50 15.9, top_p = 0.95 27.3 (128256 logits).  Many rows: the instructions of `weight`, about 30 a logit and pass (256
-// rows of 128256 fp32 logits, plain: 132 us, 60 % of the issue slots, for 19.6 us of bytes), and with top_p its atomic additions.
+// What bounds it.  Few rows: a chain of passes, barriers of the cluster (about a microsecond each) and sorts: greedy 4.7 us, plain 10.9,
+// top_k = 50 16.5, top_p = 0.95 26.2 (128256 logits).  Many rows: the instructions of `weight`, about 30 a logit and pass (256
+// rows of 128256 fp32 logits, plain: 130 us, 60 % of the issue slots, for 19.6 us of bytes), and with top_p its atomic additions.
 #include <climits>
 
 #include "qmm_internal.cuh"
@@ -697,13 +697,37 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
         if (border_i == INT_MAX && r.least == 0) {                     // all are kept
 #pragma unroll 4
             for (int i = warp * seg_len + lane; i < end; i += 32) sum += weight(r, logit(i), sh);
-        } else {
+        } else if (border_i == INT_MAX) {
 #pragma unroll 2
             for (int i = warp * seg_len + lane; i < end; i += 32) {
-                const float z = logit(i);
-                const uint64_t w = kept(z, i) ? weight(r, z, sh) : 0;
+                const uint64_t w = weight(r, logit(i), sh);
                 sum += w >= r.least ? w : 0;
             }
+        } else {
+            // those kept are lined up first: their weights, in any order, are then a whole warp's work (64 rows, top_p = 0.95: 89 us,
+            // with each weight where it lies 99)
+            float *line = reinterpret_cast<float *>(sh.list) + 64 * warp;
+            int waiting = 0;
+            auto take = [&](bool have) {
+                const uint64_t w = have ? weight(r, line[lane], sh) : 0;
+                sum += w >= r.least ? w : 0;
+            };
+            for (int i = warp * seg_len + lane; i - lane < end; i += 32) {
+                const float z = i < end ? logit(i) : 0.0f;
+                const bool in = i < end && kept(z, i);
+                const unsigned mask = __ballot_sync(0xffffffffu, in);
+                if (in) line[waiting + __popc(mask & ((1u << lane) - 1))] = z;
+                waiting += __popc(mask);
+                if (waiting < 32) continue;
+                __syncwarp();
+                take(true);
+                const float next = line[32 + lane];
+                __syncwarp();
+                line[lane] = next;
+                waiting -= 32;
+            }
+            __syncwarp();
+            take(lane < waiting);
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
@@ -759,10 +783,18 @@ cudaError_t launch(const SampleParams &p, int ctas, int per, int vec, cudaStream
 cudaError_t launch_sample(qmm_dtype t, const SampleParams &p, cudaStream_t s) {
     return with_dtype(t, [&](auto z) {
         using T = decltype(z);
-        // slices of 60 KB, two CTAs an SM; smaller ones where rows are few, and there one CTA of twice the threads
-        constexpr int kSlice = 60 * 1024 / (int)sizeof(T);
-        int ctas = 1;
-        while (ctas < kMaxCluster && (int64_t)ctas * kSlice < p.V) ctas *= 2;
+        // Slices of 60 KB, two CTAs an SM; smaller ones where rows are few, and there one CTA of twice the threads; the largest ones of which
+        // an SM holds two where rows are so many that their CTAs are more than two waves.  (128256 bf16 logits, clusters of 8 and of 4, us:
+        // 128 rows of mixed requests 87 and 86, of top_k = 50 63 and 43, of top_p = 0.95 168 and 141; 64 rows 53 and 63, 38 and
+        // 22, 91 and 79: in one wave the slowest request's own time counts.)
+        constexpr int kSlice = 60 * 1024 / (int)sizeof(T), kLargest = (228 * 512 - 1024 - (int)sizeof(Shared)) / 128 * 128 / (int)sizeof(T);
+        auto clusters = [&](int slice) {
+            int ctas = 1;
+            while (ctas < kMaxCluster && (int64_t)ctas * slice < p.V) ctas *= 2;
+            return ctas;
+        };
+        int ctas = clusters(kSlice);
+        if (p.R * ctas > 2 * 304) ctas = clusters(kLargest);
         while (ctas < kMaxCluster && p.R * ctas * 2 <= 152 && p.V / (ctas * 2) >= 2048) ctas *= 2;
         const int per = ((p.V + ctas - 1) / ctas + 15) / 16 * 16;
         const bool vec = (reinterpret_cast<uintptr_t>(p.logits) & 15u) == 0 && (p.ld * (int64_t)sizeof(T)) % 16 == 0;

@@ -85,6 +85,15 @@ def test_every_cut_at_once_over_many_rows(torch, dtype):
           rng.choice([1.0, 0.99, 0.5, 0.01, 0.0, -1.0, 2.0], R), rng.choice([0.0, 0.001, 0.3, 0.999, 1.0, 1.5, -1.0], R), rng.random(R))
 
 
+@pytest.mark.parametrize("V", [123000, 128256, 129500])
+def test_rows_in_few_large_slices(torch, V):
+    """So many rows of 16-bit logits that each is taken in as few and large slices as fit, where they fit."""
+    rng = np.random.default_rng(V)
+    R = 80
+    check(torch, "bf16", logits(torch, "bf16", R, V, 19), rng.choice([0.0, 0.7, 1.0, 1.3], R, p=[0.1, 0.3, 0.3, 0.3]), rng.choice([0, 1, 40, 3000], R), rng.choice([1.0, 0.95, 0.5], R),
+          rng.choice([0.0, 0.01], R), rng.random(R).astype(np.float32))
+
+
 @pytest.mark.parametrize("V", [4000, 130000])
 def test_wide_cuts_and_flat_logits(torch, V):
     """Cuts that keep many tokens, where borders lie in the bulk."""
@@ -92,6 +101,21 @@ def test_wide_cuts_and_flat_logits(torch, V):
     rng = np.random.default_rng(2)
     z = logits(torch, "f32", R, V, 5, 0.3)
     check(torch, "f32", z, [1.0, 1.3, 0.8, 1.0, 5.0, 1.0], [0, V // 2, V - 1, 0, V // 3, 0], [0.95, 0.9, 0.5, 0.999, 0.99, 1.0], [0, 0, 0, 0.3, 0.2, 0.5], rng.random(R))
+
+
+@pytest.mark.parametrize("top_p", [0.3, 0.9, 0.999])
+def test_a_border_among_logits_that_are_all_low(torch, top_p):
+    """One logit on top, and V - 1 around the level at which all together weigh as much as top_p leaves of it."""
+    V, t = 30000, 0.7
+    rng = np.random.default_rng(18)
+    level = t * np.log(V / (1 - top_p))
+    shifts = np.array([-3, -1, -0.3, -0.1, -0.03, -0.01, 0, 0.01, 0.03, 0.1, 0.3, 1, 3])
+    z = 5 - level + t * shifts[:, None] + 0.02 * rng.standard_normal((len(shifts), V))
+    z[:, 777] = 5
+    z[:, 20000:20005] = 4.9 - np.arange(5)
+    R = len(shifts)
+    check(torch, "f32", torch.from_numpy(z.astype(np.float32)).cuda(), [t] * R, None, [top_p] * R, None, rng.random(R).astype(np.float32))
+    check(torch, "f32", torch.from_numpy(z.astype(np.float32)).cuda(), [t] * R, [25000] * R, [top_p] * R, None, rng.random(R).astype(np.float32))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
