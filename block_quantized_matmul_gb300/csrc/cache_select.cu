@@ -13,7 +13,8 @@
 // each (17 us for the 22 MB of Q4_0 keys of four prompts of 3000 to 16384 tokens and 8 heads, 58 % of the issue slots; 5.2 us for
 // the pages of 64 new tokens).
 // Scores: on mma, so that a page's codes are converted once for eight query rows: 128 tokens of 8 x 4 heads of 128 over 1024
-// pages take 42 us where products of bytes on the ALUs took 62.  Choice: latency, a histogram or two and a ranking (9 us).
+// pages take 42 us (cold) where products of bytes on the ALUs took 62; with the choice 47 in a graph, 50 before query rows were loaded
+// four at a time and page numbers a turn ahead.  Choice: latency, a histogram or two and a ranking (9 us).
 #include "cache.cuh"
 #include "elem.cuh"
 #include "tc_common.cuh"
@@ -275,24 +276,38 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
     // ---- the tile's query rows, a warp a row: [row][negative, positive] codes as fp16, [row][DB] scales ----
     const int rows = toks * p.group;
     float *dq = reinterpret_cast<float *>(smem + p.tok_tile * p.group * 2 * kPitch);
-    for (int r = warp; r < rows; r += kScoreWarps) {
-        const int64_t src = (row0 + r / p.group) * p.ldq + (int64_t)(h * p.group + r % p.group) * D + lane;
-        __half *codes = reinterpret_cast<__half *>(smem + r * 2 * kPitch);
+    constexpr int kAhead = 4;                                          // rows under way at a time
+    for (int r0 = warp; r0 < rows; r0 += kScoreWarps * kAhead) {
+        uint16_t raw[kAhead][DB];
 #pragma unroll
-        for (int b = 0; b < DB; ++b) {
-            const float x = p.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16 *>(p.q)[src + 32 * b])
-                                   : __half2float(static_cast<const __half *>(p.q)[src + 32 * b]);
-            const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7FFFFFFFu);
-            const bool fine = top < 0x7F800000u;
-            const float d = fine ? q8_scale(__uint_as_float(top)) : 0.0f;
-            const int a = fine ? q8_code(x, inv_or_zero(d)) : 0;
-            codes[32 * b + lane] = __int2half_rn(min(a, 0));
-            codes[kPitch / 2 + 32 * b + lane] = __int2half_rn(max(a, 0));
-            if (lane == 0) dq[r * DB + b] = fine ? d : NAN;
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = r0 + u * kScoreWarps;
+            if (r >= rows) break;
+            const uint16_t *src = static_cast<const uint16_t *>(p.q) + (row0 + r / p.group) * p.ldq + (int64_t)(h * p.group + r % p.group) * D + lane;
+#pragma unroll
+            for (int b = 0; b < DB; ++b) raw[u][b] = src[32 * b];
+        }
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int r = r0 + u * kScoreWarps;
+            if (r >= rows) break;
+            __half *codes = reinterpret_cast<__half *>(smem + r * 2 * kPitch);
+#pragma unroll
+            for (int b = 0; b < DB; ++b) {
+                const float x = p.bf16 ? __uint_as_float((uint32_t)raw[u][b] << 16) : __half2float(__ushort_as_half(raw[u][b]));
+                const uint32_t top = __reduce_max_sync(0xffffffffu, __float_as_uint(x) & 0x7FFFFFFFu);
+                const bool fine = top < 0x7F800000u;
+                const float d = fine ? q8_scale(__uint_as_float(top)) : 0.0f;
+                const int a = fine ? q8_code(x, inv_or_zero(d)) : 0;
+                codes[32 * b + lane] = __int2half_rn(min(a, 0));
+                codes[kPitch / 2 + 32 * b + lane] = __int2half_rn(max(a, 0));
+                if (lane == 0) dq[r * DB + b] = fine ? d : NAN;
+            }
         }
     }
     __syncthreads();
     // a lane has pages page0 + g and + 8, and of each block of codes the eight from 8 t on
+    int ahead[2] = {-1, -1}, ahead_seq = -1, ahead_at = -1;            // numbers in the pool of the pages from ahead_at on, of one sequence
     for (int page0 = cta0 + warp * 16; page0 < all; page0 += stride) {
         uint32_t a[DB][2][2][4];                                       // [block][lowest, highest][k step][registers]
         float d[DB][2];
@@ -302,10 +317,10 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
             if (s_most[i] <= page0) continue;
             if (s_seq[i] != loaded) {
                 loaded = s_seq[i];
+                auto page_of = [&](int number) { return number < p.ld_pages && number < p.most ? p.pages[loaded * p.ld_pages + number] : -1; };
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const int number = page0 + g + 8 * e;
-                    const int page = number < p.ld_pages && number < p.most ? p.pages[loaded * p.ld_pages + number] : -1;
+                    const int page = loaded == ahead_seq && page0 == ahead_at ? ahead[e] : page_of(page0 + g + 8 * e);
                     there[e] = page >= 0 && page < p.n_pages;
                     const uint8_t *src = p.bounds + ((int64_t)(there[e] ? page : 0) * p.H + h) * BB;
 #pragma unroll
@@ -318,6 +333,12 @@ __global__ void __launch_bounds__(kScoreThreads) cache_score_kernel(const Select
                         }
                         d[b][e] = __half2float(reinterpret_cast<const __half *>(src + 2 * D)[b]);
                     }
+                }
+                if (ahead_seq < 0 || loaded == ahead_seq) {
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) ahead[e] = page_of(page0 + stride + g + 8 * e);
+                    ahead_seq = loaded;
+                    ahead_at = page0 + stride;
                 }
             }
             const int k0 = s_from[i], k1 = s_from[i + 1];
