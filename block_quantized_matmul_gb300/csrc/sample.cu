@@ -723,8 +723,8 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
                 take(true);
                 const float next = line[32 + lane];
                 __syncwarp();
-                line[lane] = next;
                 waiting -= 32;
+                if (lane < waiting) line[lane] = next;                 // (the places behind are other lanes' to write)
             }
             __syncwarp();
             take(lane < waiting);
