@@ -13,8 +13,8 @@
 // each (17 us for the 22 MB of Q4_0 keys of four prompts of 3000 to 16384 tokens and 8 heads, 58 % of the issue slots; 5.2 us for
 // the pages of 64 new tokens).
 // Scores: on mma, so that a page's codes are converted once for eight query rows: 128 tokens of 8 x 4 heads of 128 over 1024
-// pages take 42 us (cold) where products of bytes on the ALUs took 62; with the choice 47 in a graph, 50 before query rows were loaded
-// four at a time and page numbers a turn ahead.  Choice: latency, a histogram or two and a ranking (9 us).
+// pages take 36 us (cold; 62 with products of bytes on the ALUs, 42 before query rows were loaded four at a time and page numbers a turn
+// ahead), with the choice 47 in a graph: half of the issue slots.  Choice: latency, a histogram or two and a ranking (9 us).
 #include "cache.cuh"
 #include "elem.cuh"
 #include "tc_common.cuh"
