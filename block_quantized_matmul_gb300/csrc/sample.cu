@@ -642,24 +642,32 @@ __global__ void __launch_bounds__(THREADS, 1024 / THREADS) sample_kernel(const S
             // ---- the first CTA alone: cuts in the order of the logits, then the token in the order of the indexes ----
             if (rank != 0) return;
             uint64_t *ws = reinterpret_cast<uint64_t *>(sh.lo), *order = reinterpret_cast<uint64_t *>(sh.hi);
+            if (tid == 0) sh.first = (int)upto;
             sort(sh.cand, (int)upto);
             uint64_t w[2], all, total;
 #pragma unroll
             for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < top_k && 2 * tid + k < (int)upto ? weight_of_few(sh, logit_of(sh.cand[2 * tid + k])) : 0;
             uint64_t before = sums_before<kWarps>(w[0] + w[1], sh.part, all);
             const uint64_t want = top_p < 1.0f ? max((uint64_t)1, times(top_p, all, true)) : ~(uint64_t)0;
-            int mine = 0;                                              // kept of this thread's two
+            // kept are the elements before the first one that a cut takes: weights of neighbouring logits can lie a unit the wrong way
+            // round, so one behind it may be large enough again
+            int first = INT_MAX;
+#pragma unroll
+            for (int k = 1; k >= 0; --k) {
+                const int i = 2 * tid + k;
+                if (i >= top_k || i >= (int)upto || (k ? before + w[0] : before) >= want || (i > 0 && w[k] < r.least)) first = i;
+            }
+            first = __reduce_min_sync(0xffffffffu, first);
+            if (lane == 0 && first < INT_MAX) atomicMin(&sh.first, first);
+            __syncthreads();
+            const int m = sh.first;
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 const int i = 2 * tid + k;
-                if (i < top_k && i < (int)upto && before < want && (i == 0 || w[k] >= r.least)) {
-                    ws[i] = w[k];
-                    order[i] = (uint64_t)(uint32_t)sh.cand[i] << 32 | (uint32_t)i;
-                    ++mine;
-                }
-                before += w[k];
+                if (i >= m) continue;
+                ws[i] = w[k];
+                order[i] = (uint64_t)(uint32_t)sh.cand[i] << 32 | (uint32_t)i;
             }
-            const int m = __syncthreads_count(mine >= 1) + __syncthreads_count(mine >= 2);
             sort(order, m);
 #pragma unroll
             for (int k = 0; k < 2; ++k) w[k] = 2 * tid + k < m ? ws[(uint32_t)order[2 * tid + k]] : 0;
