@@ -249,14 +249,15 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
             if (in) store8<VEC>(o, const_cast<void *>(row_of(p.y, ydt, row * p.ldy)), ydt, at, n);
             continue;
         }
-        // the largest magnitude of the block of 32 that four threads hold
-        uint32_t top = 0;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the largest magnitude of the block of 32 that four threads hold, by the rule of the operand: Q8_0 passes over NaN in
+        // a block that holds anything else, in MX4 it comes out on top
         if (p.form == kNormQ8) {
-            const float d = q8_scale(__uint_as_float(top)), id = inv_or_zero(d);
+            float top = fabsf(y[0]);
+#pragma unroll
+            for (int i = 1; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float d = q8_scale(top), id = inv_or_zero(d);
             uint32_t b[2] = {0, 0};
 #pragma unroll
             for (int i = 0; i < 8; ++i) b[i >> 2] |= ((uint32_t)q8_code(y[i], id) & 255u) << (8 * (i & 3));
@@ -265,6 +266,11 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
                 if ((t & 3) == 0) reinterpret_cast<__half *>(p.scales)[row * (n / 32) + at / 32] = __float2half_rn(d);
             }
         } else {
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) top = max(top, __float_as_uint(y[i]) & 0x7FFFFFFFu);
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const uint32_t e = mx4_block_scale(top);
             // the scales of four blocks (16 threads) as one word; blocks past n hold 0
             uint32_t word = in ? e << (2 * (t & 12)) : 0u;
