@@ -205,6 +205,7 @@ __device__ __forceinline__ bool find_token(const SelectParams &p, const Sequence
     // the last place that the token sees, and the place from which the last pages are counted
     const int64_t end = p.tree ? n - 1 : min(first + i, n - 1), from = p.tree ? first : first + i;
     t.s = q.s;
+    // (a row of `scores` has whole pages, so a sequence that ends in the last of them has its place there)
     t.seen = end < 0 || (q.len + ((int64_t)1 << p.log_p) - 1) >> p.log_p > p.most ? 0 : (end >> p.log_p) + 1;
     t.old = (from < 0 ? 0 : from >> p.log_p) - (p.recent - 1);
     return true;

@@ -586,7 +586,8 @@ QMM_API size_t qmm_cache_select_workspace_size(int64_t T, int64_t H, int64_t P, 
  *   bounds_dev   as written by qmm_cache_bounds for every page that holds tokens; 16-byte aligned.
  *   pages_dev, q_starts_dev, kv_lens_dev, q_dev, ldq, T, Hq, max_new  as for qmm_cache_attend.
  *   tree_dev     NULL or not, as it will be for qmm_cache_attend_chosen (the words are not read).
- *   max_len      no sequence has more cached tokens than this; the rows of one that has get no page.
+ *   max_len      no sequence has more cached tokens than this.  It is taken in whole pages: the rows of a sequence with more than
+ *                ceil(max_len / P) pages get no page, up to there they get theirs.
  *   chosen_dev   int32 [T][H][budget]: the numbers (0 is the sequence's first page) of the chosen pages, ascending, then -1.
  * The pages in question are those up to the token's own (with tree words: up to the sequence's last).  Always chosen are the first `sinks` of
  * them and the last `recent` ones, the token's own included (with tree words: those with new tokens, and recent - 1 before them);
