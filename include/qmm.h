@@ -525,9 +525,12 @@ QMM_API qmm_status qmm_cache_attend(qmm_type t, const void *k_cache_dev, const v
  * pages, and waits (is not run in this step) when those would not fit its row of pages_dev, when its rows would pass
  * T, or when it needs pages and those of all sequences up to and including it, the waiting ones for want
  * of pages included, are more than are free.  A sequence that needs no page never waits for want of them.
+ * One whose first row would lie behind T waits as well, even if it has no new tokens.
  * Outputs:
  *   q_starts_dev  int32 [n_seq + 1]: the first row of each sequence, and all rows (sums beyond INT32_MAX count as that).
- *   kv_lens_dev   int32 [n_seq]: len + new; 0 for a sequence that waits (its rows of qmm_cache_attend are then 0) or is done.
+ *   kv_lens_dev   int32 [n_seq]: len + new; 0 for a sequence that waits or is done.  With length 0 the rows of qmm_cache_attend and
+ *                 qmm_cache_attend_chosen are 0, as long as all of the sequence's rows lie below T; those of a sequence whose rows
+ *                 pass T, and of all behind it, they leave as they are.
  *   slots_dev     int64 [T]: page * P + place of each row's token; -1 (not written by qmm_cache_write) for rows of
  *                 sequences that wait, and for rows behind the last sequence.
  *   positions_dev NULL, or int32 [T]: place of each row's token in its sequence; -1 where its slot is.
