@@ -153,10 +153,13 @@ __device__ __noinline__ uint64_t weight_wide(float z, float top, float ch, float
     return scaled(g_powers.v[n & (kPowers - 1)], __float2int_rn(__fmul_rn(th, unit)) + __float2int_rn(__fmul_rn(small, unit)), -(n >> 11));
 }
 
-// w of logit z: 2^kOne * 2^y, y = (z - top) * c, to the nearest whole number but for 2^-34 of itself; 0 for NaN.
+// w of logit z: 2^kOne * 2^y, y = (z - top) * c, as a whole number within 9/8 and 2^-34 of itself; 0 for NaN.
 // y = z c - top c = n / kPowers + f with |f| <= 1 / kPowers, where the multiple of 1 / kPowers and the rest are taken apart
 // for z c (a product in two terms) and for top c (once a row); 2^f - 1 = t + t^2/2 + t^3/6, t = f ln 2 (the next term
-// is 2^-50).  Below 2^-14 of the largest (all but 2^14 logits at most, and mostly a few) 30 bits hold what of w counts.
+// is 2^-50).  Down to 2^-13 of the largest it is the nearest to within 2^-34 of itself.  Below, 30 bits hold what of w counts (2^14 logits at
+// most lie higher, and mostly a few): the table's word and the product are cut to them, which takes up to one off, and the fraction p
+// is a multiple of 2^-32, an eighth.  So w comes out low there, by a quarter on average at 2^-14 and half as much with each power of
+// two below; a sum over 2^20 such logits by 2^18, of at least 2^49.
 __device__ __forceinline__ uint64_t weight(const Row &r, float z, const Shared &sh) {
     if (r.wide) return weight_wide(z, r.top, r.ch, r.cl);
     const float yh = __fmul_rn(z, r.ch), y = __fsub_rn(yh, r.y0);

@@ -686,9 +686,9 @@ QMM_API qmm_status qmm_norm_mx4(qmm_dtype xdt, const void *x_dev, int64_t ldx, q
  * the first in rank is always kept.  The token is the first index at which the sum of the kept w up to and including it exceeds u
  * times the sum of all kept; logp is ln of its share.  temperature <= 0 (or NaN): the first in rank, logp 0.  A row
  * in which every logit is -inf or NaN gives token -1 and logp -inf.  An infinite maximum leaves the +inf ones, equally likely.
- * w is held in fixed point, to the nearest 2^-43 of the largest but for 2^-34 of itself, and sums are exact from there: the result
- * does not depend on the order of summation, and differs from the formula's only where u, top_p or min_p lies within about
- * 2^-33 + V * 2^-43 of a border.
+ * w is held in fixed point, within 9/8 of 2^-43 of the largest and 2^-34 of itself, and sums are exact from there: the result does
+ * not depend on the order of summation, and differs from the formula's only where u, top_p or min_p lies within about 2^-33 + V * 2^-42
+ * of a border.
  * V is at most 2^20; R = 0 does nothing.
  * Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
  * Errors: INVALID_ARG (R < 0, V <= 0, V > 2^20, ld < V, NULL), UNSUPPORTED (dt), MISALIGNED, CUDA.

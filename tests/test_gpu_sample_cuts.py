@@ -56,3 +56,29 @@ def test_a_border_among_weights_that_lie_within_their_error(torch, top, t, top_p
             edge = np.abs(upto / upto[-1] - float(u[k])).min()
             if edge > 1e-8:
                 assert tok[i, k] == kept[int((upto <= float(u[k]) * upto[-1]).sum())], (i, k, j[0])
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_weights_keep_their_stated_distance(torch, seed):  # noqa: F811
+    """Two logits: a min_p of the lower one's weight, less (more) than 9/8 of 2^-43 and 2^-34 of itself, keeps (drops) it.  With u = 0 the
+    token is the lower one, the first index, exactly when it is kept.  min_p in fp32 is rounded away from the weight."""
+    n = 20000
+    rng = np.random.default_rng(seed)
+    t = np.exp(rng.uniform(-1.5, 1.5, n)).astype(f32)
+    top = rng.uniform(-20, 20, n).astype(f32)
+    # all powers of two down to 2^-43, 2^-14 to 2^-18 the most
+    y = np.where(rng.random(n) < 0.5, rng.uniform(0, 43, n), rng.uniform(13, 18, n))
+    z = (top - y * np.log(2) * t.astype(np.float64)).astype(f32)
+    w = np.exp((z.astype(np.float64) - top) / t) * 2.0 ** 43
+    err = 9 / 8 + 2.0 ** -34 * w * (1 + 1e-3)                   # (fp64's own exponential: 2^-50)
+    low, high = np.floor(w - err) * 2.0 ** -43, (w + err) * 2.0 ** -43
+    q0, q1 = low.astype(f32), high.astype(f32)
+    q0 = np.where(q0 > low, np.nextafter(q0, f32(0)), q0)
+    q1 = np.where(q1 <= high, np.nextafter(q1, f32(2)), q1)
+    use = (low > 0) & (q1 < 1) & (z < top)
+    assert use.sum() > n // 2
+    rows = torch.from_numpy(np.stack([z, top], 1)[use]).cuda()
+    m = len(rows)
+    for q, want in ((q0, 0), (q1, 1)):
+        tok, _ = run(torch, "f32", rows, t[use], None, None, q[use], np.zeros(m, f32))
+        assert (tok == want).all(), (want, np.flatnonzero(tok != want)[:5])
