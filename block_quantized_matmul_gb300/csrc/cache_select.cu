@@ -9,12 +9,17 @@
 //   score = sum_b (dq_b d_b) S_b  takes three fp32 roundings a block in the order of the blocks: every way of computing it
 // gives the same bits, and so the same choice of pages.
 //
-// What bounds them.  Bounds: the loads of a page's keys and, with many pages, the conversions of their codes and two comparisons for
-// each (17 us for the 22 MB of Q4_0 keys of four prompts of 3000 to 16384 tokens and 8 heads, 58 % of the issue slots; 5.2 us for
-// the pages of 64 new tokens).
+// What bounds them.  Bounds: latency, the loads of a page's keys in rounds (5.2 us for the pages of 64 new tokens); with many pages also
+// instructions, 9.6 an element with the join of the lanes and the codes of the bounds (17 us for the 22 MB of Q4_0 keys of four prompts of 3000 to 16384
+// tokens and 8 heads: 58 % of the issue slots; with 94 registers a thread four warps share a scheduler, and a third of the time in which
+// a warp does not issue is a wait for loads).  A step's grid is its sequences times the pages of the longest prompt, most of them of no use
+// where prompts and single tokens come together: 255 sequences with a token each and a prompt of 2048 take 22 us, 256 such sequences 6.7
+// (4096 to 8096 cached tokens, Q8_0, 8 heads, pages of 64).
 // Scores: on mma, so that a page's codes are converted once for eight query rows: 128 tokens of 8 x 4 heads of 128 over 1024
 // pages take 36 us (cold; 62 with products of bytes on the ALUs, 42 before query rows were loaded four at a time and page numbers a turn
-// ahead), with the choice 47 in a graph: half of the issue slots.  Choice: latency, a histogram or two and a ranking (9 us).
+// ahead), with the choice 47 in a graph: half of the issue slots.  Tokens of several sequences in a tile are scored one sequence after the
+// other: the choice takes 289 us for those 255 tokens and the prompt, and 50 for the 256 tokens, a tile each.  Choice: latency, a
+// histogram or two and a ranking (9 us).
 #include "cache.cuh"
 #include "elem.cuh"
 #include "tc_common.cuh"
@@ -49,7 +54,7 @@ __device__ __forceinline__ float nibble_float(uint32_t w, int k) {
 // A warp takes a page of a head.  Lanes: PK pieces of 16 bytes of codes make a token (Q8_0: half a block each,
 // Q4_0: a block), TOK = 32 / PK tokens at a time.  In the end the TOK lanes of a piece share its E elements out: half after half
 // is exchanged for a partner's, until each has E / TOK of them over all tokens, to quantize and store.  (Where PK is no power of two
-// the first PK lanes take all of them.)  Bound by the instructions of the expansion: four to five for an element.
+// the first PK lanes take all of them.)
 template <int TYPE, int DB>
 __global__ void __launch_bounds__(kBoundWarps * 32) cache_bounds_kernel(const BoundsParams p) {
     constexpr int CB = DB * (TYPE == QMM_Q8_0 ? 32 : 16), PK = CB / 16, TOK = 32 / PK, E = TYPE == QMM_Q8_0 ? 16 : 32, D = DB * 32;

@@ -131,8 +131,10 @@ __device__ __forceinline__ float row_sum(float v, float *part) {
 }
 
 // TPR threads take a row, C pieces of 8 elements each.  TYPES: of x, h and y, where the compiler knows them (9 x + 3 h + y), or -1.
-// (8192 rows of 4096, both norms and a gate, bf16: 46 us, 5.8 TB/s; with the types as parameters of the launch 65, for branches
-// and unused registers.  A ring of asynchronous copies under CTAs that go on from row to row: 52.)
+// 8192 rows of 4096, both norms and a gate, us (bytes at the copy rate): bf16 45 (40), with an fp32 stream 62 (60), to a Q8_0 operand 55 (36), to
+// an MX4 operand 47 (33).  With the types as parameters of the launch bf16 takes 65, for branches and unused registers; fp16 rows, which have no
+// instance of their own, 66 (40), their operands 74 (36) and 66 (33), fp32 rows 94 (80).  A ring of asynchronous copies under
+// CTAs that go on from row to row: 52.
 template <int TPR, int C, bool VEC, int TYPES>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormParams p) {
     constexpr int kRows = TPR < 256 ? 256 / TPR : 1;
@@ -148,6 +150,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) norm_kernel(const NormP
     const void *hr = row_of(p.h, hdt, row * p.ldh), *xr = p.x ? row_of(p.x, xdt, row * p.ldx) : nullptr;
     const void *gr = p.gate ? row_of(p.gate, xdt, row * p.ldg) : nullptr;
     // of x the pieces are kept as they lie in memory; a thread of 1024 has no registers for four of them, and loads them again
+    // (and with the types unknown still keeps 7 to 24 words of them in local memory: rows of more than 16384)
     constexpr bool kKeep = C < 4 || TPR == 32;
     Raw8 rx[kKeep ? C : 1];
     float h[C][8];

@@ -17,8 +17,10 @@
 // CTAs find is exchanged through distributed shared memory: each adds up all histograms for itself.
 //
 // What bounds it.  Few rows: a chain of passes, barriers of the cluster (about a microsecond each) and sorts: greedy 4.7 us, plain 10.9,
-// top_k = 50 16.5, top_p = 0.95 26.2 (128256 logits).  Many rows: the instructions of `weight`, about 30 a logit and pass (256
-// rows of 128256 fp32 logits, plain: 130 us, 60 % of the issue slots, for 19.6 us of bytes), and with top_p its atomic additions.
+// top_k = 50 16.5, top_p = 0.95 26.2 (128256 logits).  Many rows: 130 us for 256 rows of 128256 fp32 logits, plain, for 19.6 us of
+// bytes, at 84 instructions a logit (executed, of 64 such rows): 36 for staging, the table, the passes and the search, 37 for `weight` in 30 bits, and 12 on
+// average for its way in 64 bits, which half of the warps take besides (5 % of the logits lie within 2^-14 of the largest).  They fill 52 to 60 %
+// of the issue slots; barriers and loads take the rest.  With top_p its atomic additions.
 #include <climits>
 
 #include "qmm_internal.cuh"
