@@ -573,6 +573,7 @@ QMM_API size_t qmm_cache_bounds_size(int64_t H, int64_t D);
  *                are read, the older ones too.  Pages out of the pool, past ld_pages, or of new tokens past max_new (the
  *                last max_new tokens of a sequence count) are left as they are.
  *   bounds_dev   n_pages * qmm_cache_bounds_size(H, D) bytes, 16-byte aligned.
+ * n_seq * (min(max_new, T) / P + 2) * H is below 2^33 (CUDA otherwise).
  * T = 0 does nothing.  Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
  * Errors: INVALID_ARG (sizes, NULL), UNSUPPORTED (t), MISALIGNED, CUDA.
  */
@@ -599,6 +600,7 @@ QMM_API size_t qmm_cache_select_workspace_size(int64_t T, int64_t H, int64_t P, 
  * Rows of no sequence, of sequences whose rows do not all lie in q, and past max_new, are left as they are.
  *   workspace_dev  >= qmm_cache_select_workspace_size(T, H, P, max_len) bytes, 256-byte aligned, overwritten; calls that overlap on the
  *                GPU (replays of two captured graphs too) must use different workspaces.
+ * T * H is below 2^31, H below 65536 (CUDA otherwise).
  * T = 0 does nothing.  Launch overlap: a programmatic dependent that waits for the kernel before it before it touches memory.
  * Errors: INVALID_ARG (sizes, strides, NULL, Hq % H, recent < 1, sinks < 0, budget < sinks + recent (+ ceil((max_new - 1) / P) with
  * tree words), budget > 65536, tree words with max_new > 64, workspace too small), UNSUPPORTED (dt), MISALIGNED, CUDA.
@@ -620,6 +622,7 @@ QMM_API size_t qmm_cache_attend_chosen_workspace_size(int64_t T, int64_t H, int6
  *                past the sequence's end hold nothing that a row sees, and a page that is listed twice counts twice.  A
  *                list of -1 alone gives a row that sees nothing.
  *   the rest     as for qmm_cache_attend (rows of all T tokens of sequences are computed; there is no max_new).
+ * T * H is below 2^29 (CUDA where the grid would be too large).
  * Errors: those of qmm_cache_attend, plus INVALID_ARG (budget <= 0 or > 65536, chosen NULL) and MISALIGNED (chosen, 4 bytes).
  */
 QMM_API qmm_status qmm_cache_attend_chosen(qmm_type t, const void *k_cache_dev, const void *v_cache_dev, int64_t n_pages, int64_t P,
